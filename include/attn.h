@@ -82,7 +82,10 @@ typedef struct CUstream_st *cudaStream_t;
 #define ATTN_DEVERR_WAIT_TIMEOUT 0x100  /* a pipeline barrier wait ran past its time limit;
                                            low byte names the wait site */
 #define ATTN_DEVERR_BAD_SEQLENS 0x200   /* cu_seqlens not non-decreasing from 0, or its last
-                                           entry exceeds the packed length */
+                                           entry exceeds the packed length; or a sequence's key count
+                                           outside what its page table row can hold */
+#define ATTN_DEVERR_BAD_PAGE 0x300      /* a page table entry that a call needed lies outside
+                                           [0, num_pages) */
 
 /*
  * attn_fwd -- attention forward, bf16 inputs and outputs, fp32 accumulation.
@@ -330,6 +333,190 @@ int attn_rotary(const void *x, void *y, int B, int L, int H, int d, int rot_dim,
 int attn_rotary_packed(const void *x, void *y, int B, int L, int h_total, int h_rot, int d, int rot_dim,
                        float base, int interleaved, const int *cu_seqlens_or_null, int total,
                        const int *offsets_or_null, int fp16, cudaStream_t stream);
+
+/*
+ * ---- paged key/value caches ------------------------------------------------
+ *
+ * A paged cache keeps the keys and values of many sequences in pages of
+ * page_size tokens: key j of sequence b is token j % page_size of page
+ * page_table[b, j / page_size].  Pages of one sequence may lie anywhere in the
+ * pool, in any order; sequences may share pages that none of them writes.
+ * attn_cache_append writes the keys and values of new tokens,
+ * attn_fwd_paged and attn_decode_paged attend over the pages,
+ * attn_key_weights sums the attention weight that each key receives, and
+ * attn_cache_evict drops the lightest keys.
+ *
+ * attn_paged_kv describes the cache (a HOST struct; its pointers are device
+ * pointers):
+ *   k, v          first element of the key and of the value pages.  Element
+ *                 (page, token, head, feature) lies stride_page * page +
+ *                 stride_token * token + stride_head * head + feature
+ *                 elements from it; the strides are positive multiples of 8
+ *                 elements, the same for k and v, so pages of both may
+ *                 interleave in one buffer and heads may come before tokens.
+ *                 16-byte aligned.
+ *   num_pages     pages in the pool.
+ *   page_size     tokens in a page: 16, 32, 64, 128 or 256.
+ *   num_kv_heads, head_dim (64 or 128), fp16 (0 bf16, 1 fp16).
+ *   page_table    int32, row b at page_table + b * table_stride, max_pages
+ *                 entries of which the first ceil(seqlens_k[b] / page_size)
+ *                 are read; the others may hold anything.
+ *   seqlens_k     int32 (B): keys of each sequence, 0 .. max_pages * page_size.
+ * What lies in the pages past a sequence's last key is never used, whatever
+ * its value (a NaN included).
+ *
+ * The host reads neither array.  A sequence whose key count is out of range
+ * is taken as having no keys, and ATTN_DEVERR_BAD_SEQLENS is recorded; a page
+ * table entry outside [0, num_pages) records ATTN_DEVERR_BAD_PAGE, no memory
+ * outside the pool is touched, and the outputs of that sequence are
+ * unspecified.  A pair cu_seqlens[b], cu_seqlens[b + 1] that is decreasing or
+ * leaves [0, total] makes sequence b have no new tokens and records
+ * ATTN_DEVERR_BAD_SEQLENS.
+ *
+ * Each call returns ATTN_OK, ATTN_EINVAL, ATTN_EUNSUPPORTED (head_dim,
+ * page_size, a device that is not sm_103) or ATTN_ELAUNCH.  None allocates:
+ * scratch memory is the caller's (attn_paged_workspace_bytes), so calls that
+ * run at the same time, or graphs replayed at the same time, only need
+ * workspaces of their own.
+ */
+typedef struct attn_paged_kv {
+  void *k;
+  void *v;
+  const int *page_table;
+  const int *seqlens_k;
+  long long stride_page, stride_token, stride_head;
+  int table_stride, max_pages, num_pages, page_size;
+  int num_kv_heads, head_dim, fp16;
+} attn_paged_kv;
+
+/*
+ * attn_rotary_scaled -- rotary position embedding with given frequencies (for
+ * contexts longer than the trained one: position interpolation, a changed
+ * base, per-frequency blends) and its gradient.  With a = position *
+ * freqs[p] and A = amplitude, pair p (the features (p, p + rot_dim / 2), or
+ * (2p, 2p + 1) when interleaved) becomes
+ *     A (x1 cos a - x2 sin a, x1 sin a + x2 cos a);
+ * features from rot_dim on are copied.  inverse = 1 turns by -a instead: the
+ * gradient of the embedding, dx = A R(-a) dy.
+ *   x   (B, L, H, d), or packed (total, H, d) with cu_seqlens; element
+ *       (row, head, feature) at row * x_stride_token + head * x_stride_head +
+ *       feature.
+ *   y   contiguous rows of H x d; disjoint from x, or x itself (then x is
+ *       contiguous too).  In packed calls rows outside every sequence are left
+ *       as they are unless positions are given.
+ *   freqs   HOST array of rot_dim / 2 finite doubles, radians per position,
+ *       copied before the call returns; rot_dim even, 0 < rot_dim <= d, at
+ *       most 512.
+ *   Position of token i of sequence b: i + offsets[b] (device int32 (B) or
+ *       null for 0), or positions[row] (device int32, one per row, may be
+ *       negative; then offsets are not allowed and cu_seqlens not needed:
+ *       B = 1, L = rows).
+ * The angle is reduced to a fraction of a turn in 64-bit fixed point before
+ * the sine and cosine in fp32, so it is as exact at position 2^31 as near 0.
+ * Returns ATTN_OK, ATTN_EINVAL or ATTN_ELAUNCH.
+ */
+int attn_rotary_scaled(const void *x, void *y, int B, int L, int H, int d, int rot_dim, const double *freqs,
+                       float amplitude, int interleaved, int inverse, long long x_stride_token,
+                       long long x_stride_head, const int *cu_seqlens_or_null, int total,
+                       const int *offsets_or_null, const int *positions_or_null, int fp16, cudaStream_t stream);
+
+/*
+ * attn_cache_append -- writes the new tokens' keys and values into the pages,
+ * in one pass with the rotary embedding of the queries and keys.  Sequence b's
+ * new tokens are rows cu_seqlens[b] .. cu_seqlens[b + 1] - 1 of q, k and v
+ * (device int32 (B + 1), rows up to total); they are the last of its
+ * seqlens_k[b] keys, so seqlens_k counts them already.  A new token whose key
+ * index would be negative (more new tokens than keys) is not written and
+ * records ATTN_DEVERR_BAD_SEQLENS.  Two sequences must not append to the same
+ * page.
+ *   q, q_out  (total, Hq, d), or both null.  q_out = rotary of q, contiguous,
+ *             disjoint from q or q itself (then q is contiguous).
+ *   k, v      (total, Hkv, d).
+ *   *_stride_token   elements between tokens (heads of a token are
+ *             contiguous), multiples of 8: slices of one projection's output.
+ *   freqs     as attn_rotary_scaled, or null: no rotation (q must be null).
+ *   positions device int32 (total), the rotary positions; null: the key
+ *             index.  (After an eviction the two differ.)
+ * Rows outside every sequence are left alone.
+ */
+int attn_cache_append(const void *q, const void *k, const void *v, void *q_out, long long q_stride_token,
+                      long long k_stride_token, long long v_stride_token, int B, int Hq, int total,
+                      const attn_paged_kv *cache, const int *cu_seqlens, int rot_dim, const double *freqs_or_null,
+                      float amplitude, int interleaved, const int *positions_or_null, cudaStream_t stream);
+
+/* attn_paged_workspace_bytes -- scratch memory that attn_fwd_paged (decode =
+ * 0) or attn_decode_paged (decode = 1) needs on the current device for head
+ * dimension d, whatever the other sizes; a negative return code on failure. */
+long long attn_paged_workspace_bytes(int d, int decode);
+
+/*
+ * attn_fwd_paged -- attention of a chunk of new tokens over a paged cache:
+ * attn_fwd_varlen with the keys in pages.  q, o (total_q, Hq, d) contiguous,
+ * sequence b's queries cu_seqlens_q[b] .. cu_seqlens_q[b + 1] - 1; lse (Hq,
+ * total_q) fp32.  Causal aligns bottom-right: query i of Lq_b sees key j iff
+ * j <= i + seqlens_k[b] - Lq_b.  A query that sees no key gives O = 0 and
+ * lse = -inf; rows outside every sequence are left as they are.  Hq a multiple
+ * of num_kv_heads, scale finite and not negative, B <= 65535.
+ * workspace: 256-byte aligned, attn_paged_workspace_bytes(d, 0) bytes.
+ */
+int attn_fwd_paged(const void *q, void *o, float *lse, int B, int Hq, int total_q, const attn_paged_kv *cache,
+                   const int *cu_seqlens_q, int causal, float scale, void *workspace, long long workspace_bytes,
+                   cudaStream_t stream);
+
+/*
+ * attn_decode_paged -- one decoding step over a paged cache: attn_decode with
+ * the keys in pages, one query per sequence.  q, o (B, Hq, d) contiguous, lse
+ * (Hq, B) fp32; a sequence without keys gives O = 0 and lse = -inf.  Any Hq
+ * that is a multiple of num_kv_heads; B <= 65535.  workspace as above, with
+ * decode = 1.
+ */
+int attn_decode_paged(const void *q, void *o, float *lse, int B, int Hq, const attn_paged_kv *cache, float scale,
+                      void *workspace, long long workspace_bytes, cudaStream_t stream);
+
+/*
+ * attn_key_weights -- the attention weight that each cached key receives from
+ * a chunk of queries, summed over the queries and over the query heads of its
+ * key/value head:
+ *     weights[b, g, j] = decay * weights[b, g, j] + sum_h sum_i exp(scale q_ih . k_j - lse_ih)
+ * over the heads h of group g and the queries i of sequence b that see key j.
+ * q, cu_seqlens_q, causal and scale as attn_fwd_paged was given them and lse
+ * (Hq, total_q) as it returned it (or attn_decode_paged, with cu_seqlens_q =
+ * {0, 1, ..., B}); a query with lse = -inf adds nothing.  weights (B,
+ * num_kv_heads, weights_len) fp32, entries j >= seqlens_k[b] are left as they
+ * are; decay = 0 does not read what was there.  weights_len at least
+ * every seqlens_k[b] (a longer sequence is taken as bad).  cache->v is not
+ * read and may be null.
+ */
+int attn_key_weights(const void *q, const float *lse, float *weights, int weights_len, int B, int Hq, int total_q,
+                     const attn_paged_kv *cache, const int *cu_seqlens_q, int causal, float scale, float decay,
+                     cudaStream_t stream);
+
+/*
+ * attn_cache_evict -- cuts every sequence of a cache back to `budget` keys per
+ * key/value head.  For a sequence with n = seqlens_k[b] > budget keys each
+ * head keeps its last `recent` keys and, of the others, the budget - recent
+ * with the largest weights[b, g, j] (among equal weights the lower j; a NaN
+ * counts as larger than any number); a sequence with n <= budget keeps all.
+ * The kept keys stay in order: key and value rows move to key indices 0 ..
+ * m - 1, m = min(n, budget).
+ *   weights      (B, num_kv_heads, weights_len) fp32.
+ *   kept         int32 (B, num_kv_heads, budget), written: the kept indices in
+ *                ascending order, -1 from m on.
+ *   seqlens_out  int32 (B), written: m.  Not seqlens_k itself.
+ *   weights_out  fp32 (B, num_kv_heads, weights_out_len >= budget), written:
+ *                the kept keys' weights, 0 from m on; may be weights itself.
+ *   dst_page_table   null: rows move within the sequence's own pages (in
+ *                place; pages past the m-th key are free afterwards).  Else the
+ *                pages to write, row b at dst_page_table + b * dst_stride, dst_max_pages
+ *                entries (at least ceil(budget / page_size)); entry i of row b is
+ *                either page i of the sequence itself or a page that no
+ *                sequence of the call reads or writes otherwise.
+ * 0 <= recent <= budget, budget >= 1.  In place, sequences must not share
+ * pages.
+ */
+int attn_cache_evict(const float *weights, int weights_len, int *kept, int *seqlens_out, float *weights_out,
+                     int weights_out_len, int B, const attn_paged_kv *cache, const int *dst_page_table, int dst_stride,
+                     int dst_max_pages, int budget, int recent, cudaStream_t stream);
 
 /*
  * Padded batches around the varlen forward (the flash-attention

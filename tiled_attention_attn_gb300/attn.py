@@ -128,6 +128,7 @@ def lib(path: Optional[str] = None):
         L.attn_cache_stats.restype = i
         L.attn_selftest_plan_cache.argtypes = [i, i, i, ip, ip]
         L.attn_selftest_plan_cache.restype = i
+        _paged.declare(L)
         if path is None:
             _lib = L
         return L
@@ -796,3 +797,18 @@ def trace_enable(buf: Optional[torch.Tensor], events_per_stream: int = 0) -> Non
         rc = lib().attn_trace_enable(buf.data_ptr(), int(events_per_stream))
     if rc != ATTN_OK:
         raise AttnError(rc, "attn_trace_enable")
+
+
+# paged key/value caches
+from . import paged as _paged  # noqa: E402
+from .paged import (  # noqa: E402,F401
+    ATTN_DEVERR_BAD_PAGE,
+    attn_decode_paged,
+    attn_fwd_paged,
+    cache_append,
+    cache_evict,
+    key_weights,
+    rotary_freqs,
+    rotary_scaled,
+    rotary_scaled_func,
+)

@@ -1,0 +1,84 @@
+// The paged key/value cache as the kernels see it, and the host checks that
+// its entry points share.
+#pragma once
+#include <cstdint>
+
+#include "attn.h"
+#include "attn_internal.h"
+
+namespace attn {
+
+struct PagedKV {
+  uint16_t* k;
+  uint16_t* v;
+  const int* table;     // row b at table + b * table_stride
+  const int* seqlens;   // (B)
+  long long s_page, s_token, s_head;   // elements
+  int table_stride, max_pages, num_pages, page_log2, hkv;
+};
+
+constexpr int kPagedMaxB = 65535;
+
+inline bool ptr_aligned(const void* p, uintptr_t a) { return (reinterpret_cast<uintptr_t>(p) % a) == 0; }
+
+// Checks the host struct and fills `out`.  need_v: the values are used.
+inline int paged_check(const attn_paged_kv* c, int B, bool need_v, PagedKV& out) {
+  if (!c || !c->k || (need_v && !c->v) || !c->page_table || !c->seqlens_k) return ATTN_EINVAL;
+  if (!ptr_aligned(c->k, 16) || (need_v && !ptr_aligned(c->v, 16))) return ATTN_EINVAL;
+  if (B <= 0 || B > kPagedMaxB || c->num_kv_heads <= 0 || c->num_kv_heads > 65535 || c->num_pages <= 0) return ATTN_EINVAL;
+  if (c->max_pages <= 0 || c->table_stride < c->max_pages || (c->fp16 != 0 && c->fp16 != 1)) return ATTN_EINVAL;
+  for (long long s : {c->stride_page, c->stride_token, c->stride_head})
+    if (s <= 0 || s % 8 != 0 || s >= (1LL << 39)) return ATTN_EINVAL;
+  if (c->head_dim != 64 && c->head_dim != 128) return ATTN_EUNSUPPORTED;
+  int lg = 4;
+  while (lg <= 8 && (1 << lg) != c->page_size) ++lg;
+  if (lg > 8) return ATTN_EUNSUPPORTED;
+  if (static_cast<long long>(c->max_pages) << lg > (1LL << 30)) return ATTN_EINVAL;   // 32-bit key indices
+  out.k = static_cast<uint16_t*>(c->k);
+  out.v = static_cast<uint16_t*>(c->v);
+  out.table = c->page_table;
+  out.seqlens = c->seqlens_k;
+  out.s_page = c->stride_page;
+  out.s_token = c->stride_token;
+  out.s_head = c->stride_head;
+  out.table_stride = c->table_stride;
+  out.max_pages = c->max_pages;
+  out.num_pages = c->num_pages;
+  out.page_log2 = lg;
+  out.hkv = c->num_kv_heads;
+  return ATTN_OK;
+}
+
+#if defined(__CUDACC__)
+// Keys of sequence b: 0 (and the error recorded) when out of range.
+__device__ __forceinline__ int paged_len(const PagedKV& c, int b, int* err) {
+  const int n = __ldg(c.seqlens + b);
+  if (n < 0 || n > (c.max_pages << c.page_log2)) {
+    atomicCAS(err, 0, ATTN_DEVERR_BAD_SEQLENS);
+    return 0;
+  }
+  return n;
+}
+// Page i of sequence b, or -1 (and the error recorded) when it is not one.
+__device__ __forceinline__ int paged_page(const PagedKV& c, int b, int i, int* err) {
+  const int p = __ldg(c.table + static_cast<long long>(b) * c.table_stride + i);
+  if (p < 0 || p >= c.num_pages) {
+    atomicCAS(err, 0, ATTN_DEVERR_BAD_PAGE);
+    return -1;
+  }
+  return p;
+}
+// First row and count of sequence b's new tokens: none (and the error
+// recorded) when its offsets are decreasing or leave [0, total].
+__device__ __forceinline__ int chunk_len(const int* cu, int b, int total, int& row, int* err) {
+  const int a = __ldg(cu + b), e = __ldg(cu + b + 1);
+  row = a;
+  if (a < 0 || e < a || e > total) {
+    atomicCAS(err, 0, ATTN_DEVERR_BAD_SEQLENS);
+    return 0;
+  }
+  return e - a;
+}
+#endif
+
+}  // namespace attn
