@@ -18,6 +18,7 @@
 #include "attn_cache.h"
 #include "attn_internal.h"
 #include "attn_launch.h"
+#include "attn_paged_launch.h"
 #include "attn_pair_launch.h"
 #include "attn_params.h"
 #include "attn_plan.h"
@@ -814,6 +815,25 @@ int encode_map(const void* ptr, bool bf16, int d, int H, int L, int B, CUtensorM
   const cuuint64_t strides[3] = {static_cast<cuuint64_t>(d) * 2, static_cast<cuuint64_t>(H) * d * 2,
                                  static_cast<cuuint64_t>(L) * H * d * 2};
   const cuuint32_t box[4] = {64, 1, static_cast<cuuint32_t>(kBM), 1};
+  const cuuint32_t es[4] = {1, 1, 1, 1};
+  const CUresult r = g_encode(&out, bf16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 4,
+                              const_cast<void*>(ptr), dims, strides, box, es, CU_TENSOR_MAP_INTERLEAVE_NONE,
+                              CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                              CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  return r == CUDA_SUCCESS ? ATTN_OK : ATTN_EINVAL;
+}
+
+int tile_map(const void* ptr, bool bf16, int d, int H, int L, int N, long long s_h, long long s_l, long long s_n,
+             int box_h, int box_l, CUtensorMap& out) {
+  {
+    std::lock_guard<std::mutex> lock(g_mu);
+    if (!get_encode()) return ATTN_ELAUNCH;
+  }
+  const cuuint64_t dims[4] = {static_cast<cuuint64_t>(d), static_cast<cuuint64_t>(H), static_cast<cuuint64_t>(L),
+                              static_cast<cuuint64_t>(N)};
+  const cuuint64_t strides[3] = {static_cast<cuuint64_t>(s_h) * 2, static_cast<cuuint64_t>(s_l) * 2,
+                                 static_cast<cuuint64_t>(s_n) * 2};
+  const cuuint32_t box[4] = {64, static_cast<cuuint32_t>(box_h), static_cast<cuuint32_t>(box_l), 1};
   const cuuint32_t es[4] = {1, 1, 1, 1};
   const CUresult r = g_encode(&out, bf16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 4,
                               const_cast<void*>(ptr), dims, strides, box, es, CU_TENSOR_MAP_INTERLEAVE_NONE,

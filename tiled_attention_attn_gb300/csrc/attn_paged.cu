@@ -10,7 +10,7 @@
 #include <cmath>
 #include <cstdint>
 
-#include "attn_paged.h"
+#include "attn_paged_launch.h"
 
 namespace attn {
 namespace {
@@ -142,6 +142,11 @@ int run(bool decode, const void* q, void* o, float* lse, int B, int Hq, int tota
   DeviceInfo info;
   if (int rc = device_info(dev, info)) return rc;
   if (!info.supported) return ATTN_EUNSUPPORTED;
+  if (decode) {
+    if (ws_bytes < paged_decode_workspace(info.sm_count, cache->head_dim)) return ATTN_EINVAL;
+    return paged_decode(q, o, lse, B, Hq, c, cache->head_dim, cache->fp16 == 0, cache->page_size, scale, ws,
+                        info.sm_count, info.err_word, stream);
+  }
   const long long items = static_cast<long long>(total) * Hq;
   const int grid = static_cast<int>((items + kWarps - 1) / kWarps);
   const bool bf16 = cache->fp16 == 0;
@@ -170,7 +175,11 @@ extern "C" {
 long long attn_paged_workspace_bytes(int d, int decode) {
   if (d != 64 && d != 128) return ATTN_EUNSUPPORTED;
   if (decode != 0 && decode != 1) return ATTN_EINVAL;
-  return 256;
+  int dev = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess) return ATTN_ELAUNCH;
+  attn::DeviceInfo info;
+  if (int rc = attn::device_info(dev, info)) return rc;
+  return decode ? attn::paged_decode_workspace(info.sm_count, d) : 256;
 }
 
 int attn_fwd_paged(const void* q, void* o, float* lse, int B, int Hq, int total_q, const attn_paged_kv* cache,
