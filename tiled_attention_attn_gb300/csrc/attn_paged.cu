@@ -22,69 +22,10 @@ __device__ __forceinline__ float cvt(uint16_t x) {
   if constexpr (BF16) return __bfloat162float(__ushort_as_bfloat16(x));
   return __half2float(__ushort_as_half(x));
 }
-template <bool BF16>
-__device__ __forceinline__ uint16_t to16(float x) {
-  if constexpr (BF16) return __bfloat16_as_ushort(__float2bfloat16_rn(x));
-  return __half_as_ushort(__float2half_rn(x));
-}
 __device__ __forceinline__ float warp_sum(float x) {
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) x += __shfl_xor_sync(0xffffffffu, x, o);
   return x;
-}
-
-// cu == nullptr: row b of q is sequence b's only query.
-template <int D, bool BF16>
-__global__ void __launch_bounds__(kWarps * 32) paged_rows_kernel(const uint16_t* q, uint16_t* o, float* lse, PagedKV c,
-                                                                 const int* cu, int B, int Hq, int total, int causal,
-                                                                 float scale, int* err) {
-  constexpr int E = D / 32;
-  const int lane = threadIdx.x & 31;
-  const long long item = static_cast<long long>(blockIdx.x) * kWarps + (threadIdx.x >> 5);
-  if (item >= static_cast<long long>(total) * Hq) return;
-  const int row = static_cast<int>(item / Hq), h = static_cast<int>(item - static_cast<long long>(row) * Hq);
-  int b = row, first = row, n_q = 1;
-  if (cu) {
-    int lo = 0, hi = B;
-    while (hi - lo > 1) {
-      const int mid = (lo + hi) >> 1;
-      if (__ldg(cu + mid) <= row) lo = mid; else hi = mid;
-    }
-    b = lo;
-    n_q = chunk_len(cu, b, total, first, err);
-    if (row < first || row >= first + n_q) return;
-  }
-  const int len = paged_len(c, b, err);
-  const int n = causal ? min(len, row - first + 1 + len - n_q) : len;   // keys this row sees
-  const int g = h / (Hq / c.hkv);
-  float qv[E], acc[E];
-#pragma unroll
-  for (int e = 0; e < E; ++e) {
-    qv[e] = cvt<BF16>(q[item * D + lane + 32 * e]) * scale;
-    acc[e] = 0.0f;
-  }
-  float m = -INFINITY, l = 0.0f;
-  int page = -1;
-  for (int j = 0; j < n; ++j) {
-    const int slot = j & ((1 << c.page_log2) - 1);
-    if (slot == 0) page = paged_page(c, b, j >> c.page_log2, err);
-    if (page < 0) continue;
-    const long long at = page * c.s_page + slot * c.s_token + g * c.s_head;
-    float s = 0.0f;
-#pragma unroll
-    for (int e = 0; e < E; ++e) s = fmaf(qv[e], cvt<BF16>(c.k[at + lane + 32 * e]), s);
-    s = warp_sum(s);
-    const float mn = fmaxf(m, s);
-    const float r = m == -INFINITY ? 0.0f : expf(m - mn), w = mn == -INFINITY ? 0.0f : expf(s - mn);
-    m = mn;
-    l = l * r + w;
-#pragma unroll
-    for (int e = 0; e < E; ++e) acc[e] = acc[e] * r + w * cvt<BF16>(c.v[at + lane + 32 * e]);
-  }
-  const float inv = l > 0.0f ? 1.0f / l : 0.0f;
-#pragma unroll
-  for (int e = 0; e < E; ++e) o[item * D + lane + 32 * e] = to16<BF16>(acc[e] * inv);
-  if (lane == 0) lse[static_cast<long long>(h) * total + row] = l > 0.0f ? m + logf(l) : -INFINITY;
 }
 
 // One warp per (sequence, key/value head, key).
@@ -142,29 +83,14 @@ int run(bool decode, const void* q, void* o, float* lse, int B, int Hq, int tota
   DeviceInfo info;
   if (int rc = device_info(dev, info)) return rc;
   if (!info.supported) return ATTN_EUNSUPPORTED;
-  if (decode) {
-    if (ws_bytes < paged_decode_workspace(info.sm_count, cache->head_dim)) return ATTN_EINVAL;
-    return paged_decode(q, o, lse, B, Hq, c, cache->head_dim, cache->fp16 == 0, cache->page_size, scale, ws,
-                        info.sm_count, info.err_word, stream);
-  }
-  const long long items = static_cast<long long>(total) * Hq;
-  const int grid = static_cast<int>((items + kWarps - 1) / kWarps);
+  const int d = cache->head_dim;
+  if (ws_bytes < (decode ? paged_decode_workspace(info.sm_count, d) : paged_fwd_workspace(info.sm_count, d)))
+    return ATTN_EINVAL;
   const bool bf16 = cache->fp16 == 0;
-  auto* qp = static_cast<const uint16_t*>(q);
-  auto* op = static_cast<uint16_t*>(o);
-#define ATTN_RUN(D, T) \
-  paged_rows_kernel<D, T><<<grid, kWarps * 32, 0, stream>>>(qp, op, lse, c, cu, B, Hq, total, causal, scale, info.err_word)
-  if (cache->head_dim == 64) {
-    if (bf16) ATTN_RUN(64, true);
-    else ATTN_RUN(64, false);
-  } else {
-    if (bf16) ATTN_RUN(128, true);
-    else ATTN_RUN(128, false);
-  }
-#undef ATTN_RUN
-  if (cudaGetLastError() != cudaSuccess) return ATTN_ELAUNCH;
-  count_launch();
-  return ATTN_OK;
+  if (decode)
+    return paged_decode(q, o, lse, B, Hq, c, d, bf16, cache->page_size, scale, ws, info.sm_count, info.err_word, stream);
+  return paged_fwd(q, o, lse, B, Hq, total, c, d, bf16, cache->page_size, cu, causal != 0, scale, ws, info.sm_count,
+                   info.err_word, stream);
 }
 
 }  // namespace
@@ -179,7 +105,7 @@ long long attn_paged_workspace_bytes(int d, int decode) {
   if (cudaGetDevice(&dev) != cudaSuccess) return ATTN_ELAUNCH;
   attn::DeviceInfo info;
   if (int rc = attn::device_info(dev, info)) return rc;
-  return decode ? attn::paged_decode_workspace(info.sm_count, d) : 256;
+  return decode ? attn::paged_decode_workspace(info.sm_count, d) : attn::paged_fwd_workspace(info.sm_count, d);
 }
 
 int attn_fwd_paged(const void* q, void* o, float* lse, int B, int Hq, int total_q, const attn_paged_kv* cache,

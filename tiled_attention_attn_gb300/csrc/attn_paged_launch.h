@@ -17,4 +17,8 @@ long long paged_decode_workspace(int sms, int d);
 int paged_decode(const void* q, void* o, float* lse, int B, int Hq, const PagedKV& c, int d, bool bf16, int page_size,
                  float scale, void* ws, int sms, int* err, cudaStream_t stream);
 
+long long paged_fwd_workspace(int sms, int d);
+int paged_fwd(const void* q, void* o, float* lse, int B, int Hq, int total, const PagedKV& c, int d, bool bf16,
+              int page_size, const int* cu, bool causal, float scale, void* ws, int sms, int* err, cudaStream_t stream);
+
 }  // namespace attn
