@@ -444,10 +444,13 @@ int attn_cache_append(const void *q, const void *k, const void *v, void *q_out, 
                       const attn_paged_kv *cache, const int *cu_seqlens, int rot_dim, const double *freqs_or_null,
                       float amplitude, int interleaved, const int *positions_or_null, cudaStream_t stream);
 
-/* attn_paged_workspace_bytes -- scratch memory that attn_fwd_paged (decode =
- * 0) or attn_decode_paged (decode = 1) needs on the current device for head
- * dimension d, whatever the other sizes; a negative return code on failure. */
-long long attn_paged_workspace_bytes(int d, int decode);
+/* attn_paged_workspace_bytes -- scratch memory that a call needs on the
+ * current device for head dimension d, whatever the other sizes; a negative
+ * return code on failure.  call: which one. */
+#define ATTN_PAGED_CHUNK 0    /* attn_fwd_paged */
+#define ATTN_PAGED_DECODE 1   /* attn_decode_paged */
+#define ATTN_PAGED_WEIGHTS 2  /* attn_key_weights */
+long long attn_paged_workspace_bytes(int d, int call);
 
 /*
  * attn_fwd_paged -- attention of a chunk of new tokens over a paged cache:
@@ -457,7 +460,8 @@ long long attn_paged_workspace_bytes(int d, int decode);
  * j <= i + seqlens_k[b] - Lq_b.  A query that sees no key gives O = 0 and
  * lse = -inf; rows outside every sequence are left as they are.  Hq a multiple
  * of num_kv_heads, scale finite and not negative, B <= 65535.
- * workspace: 256-byte aligned, attn_paged_workspace_bytes(d, 0) bytes.
+ * workspace: 256-byte aligned, attn_paged_workspace_bytes(d,
+ * ATTN_PAGED_CHUNK) bytes.
  */
 int attn_fwd_paged(const void *q, void *o, float *lse, int B, int Hq, int total_q, const attn_paged_kv *cache,
                    const int *cu_seqlens_q, int causal, float scale, void *workspace, long long workspace_bytes,
@@ -467,8 +471,8 @@ int attn_fwd_paged(const void *q, void *o, float *lse, int B, int Hq, int total_
  * attn_decode_paged -- one decoding step over a paged cache: attn_decode with
  * the keys in pages, one query per sequence.  q, o (B, Hq, d) contiguous, lse
  * (Hq, B) fp32; a sequence without keys gives O = 0 and lse = -inf.  Any Hq
- * that is a multiple of num_kv_heads; B <= 65535.  workspace as above, with
- * decode = 1.
+ * that is a multiple of num_kv_heads; B <= 65535.  workspace as above, for
+ * ATTN_PAGED_DECODE.
  */
 int attn_decode_paged(const void *q, void *o, float *lse, int B, int Hq, const attn_paged_kv *cache, float scale,
                       void *workspace, long long workspace_bytes, cudaStream_t stream);
@@ -485,11 +489,12 @@ int attn_decode_paged(const void *q, void *o, float *lse, int B, int Hq, const a
  * num_kv_heads, weights_len) fp32, entries j >= seqlens_k[b] are left as they
  * are; decay = 0 does not read what was there.  weights_len at least
  * every seqlens_k[b] (a longer sequence is taken as bad).  cache->v is not
- * read and may be null.
+ * read and may be null.  The sums' order depends on the lengths alone: the same
+ * call gives the same bits.  workspace as above, for ATTN_PAGED_WEIGHTS.
  */
 int attn_key_weights(const void *q, const float *lse, float *weights, int weights_len, int B, int Hq, int total_q,
                      const attn_paged_kv *cache, const int *cu_seqlens_q, int causal, float scale, float decay,
-                     cudaStream_t stream);
+                     void *workspace, long long workspace_bytes, cudaStream_t stream);
 
 /*
  * attn_cache_evict -- cuts every sequence of a cache back to `budget` keys per

@@ -32,8 +32,9 @@ def decode(L, c=None, q=16, o=16, lse=16, B=2, Hq=4, scale=0.125, ws=256, n=1 <<
     return L.attn_decode_paged(q, o, lse, B, Hq, c or cache(), F(scale), ws, n, None)
 
 
-def weights(L, c=None, q=16, lse=16, w=16, n=64, B=2, Hq=4, total=8, cu=16, causal=1, scale=0.125, decay=1.0):
-    return L.attn_key_weights(q, lse, w, n, B, Hq, total, c or cache(), cu, causal, F(scale), F(decay), None)
+def weights(L, c=None, q=16, lse=16, w=16, n=64, B=2, Hq=4, total=8, cu=16, causal=1, scale=0.125, decay=1.0, ws=256,
+            m=1 << 40):
+    return L.attn_key_weights(q, lse, w, n, B, Hq, total, c or cache(), cu, causal, F(scale), F(decay), ws, m, None)
 
 
 def evict(L, c=None, w=16, n=64, kept=16, lens=32, wo=48, no=64, B=2, dst=None, ds=0, dm=0, budget=8, recent=2):
@@ -91,7 +92,8 @@ def test_decode_refusals(attn_lib, bad):
 
 
 @pytest.mark.parametrize("bad", COMMON + [dict(w=None), dict(w=2), dict(n=0), dict(cu=None), dict(total=-1),
-                                          dict(causal=-1), dict(decay=math.nan), dict(decay=math.inf)], ids=str)
+                                          dict(causal=-1), dict(decay=math.nan), dict(decay=math.inf),
+                                          dict(ws=None), dict(ws=128), dict(m=0)], ids=str)
 def test_weights_refusals(attn_lib, bad):
     assert weights(attn_lib, **bad) == attn.ATTN_EINVAL
 
@@ -134,7 +136,7 @@ def test_nothing_to_do(attn_lib):
 
 def test_workspace_query_refusals(attn_lib):
     assert attn_lib.attn_paged_workspace_bytes(96, 0) == attn.ATTN_EUNSUPPORTED
-    assert attn_lib.attn_paged_workspace_bytes(64, 2) == attn.ATTN_EINVAL
+    assert attn_lib.attn_paged_workspace_bytes(64, 3) == attn.ATTN_EINVAL
 
 
 def test_binding_refuses_host_tensors_and_wrong_types():

@@ -38,6 +38,7 @@
 #include <type_traits>
 
 #include "attn_paged.h"
+#include "attn_paged_line.cuh"
 #include "attn_paged_launch.h"
 #include "attn_params.h"
 #include "ptx.cuh"
@@ -235,20 +236,8 @@ __global__ void __launch_bounds__(kThreads, 1) decode_kernel(const __grid_consta
   const int b_lo = min(tid * strip, p.B), b_hi = min(b_lo + strip, p.B);
   long long mine = 0;
   for (int b = b_lo; b < b_hi; ++b) mine += static_cast<long long>(nh) * (steps_of<KS>(paged_len(p.c, b, p.err)) + 1);
-  long long incl = mine;
-#pragma unroll
-  for (int o = 1; o < 32; o <<= 1) {
-    const long long y = __shfl_up_sync(0xffffffffu, incl, o);
-    if (lane >= o) incl += y;
-  }
-  if (lane == 31) warp_sums[warp] = incl;
-  __syncthreads();
-  long long total = 0, before = incl - mine;
-#pragma unroll
-  for (int w = 0; w < kThreads / 32; ++w) {
-    if (w < warp) before += warp_sums[w];
-    total += warp_sums[w];
-  }
+  long long total;
+  const long long before = block_prefix<kThreads>(mine, warp_sums, total);
   // equal ranges, but of at least kMinSteps: below that the merge of more
   // pieces costs more than the steps it saves
   constexpr int kMinSteps = 4;

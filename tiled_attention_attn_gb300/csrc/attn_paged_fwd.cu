@@ -33,6 +33,7 @@
 
 #include "attn_kernel.cuh"
 #include "attn_paged.h"
+#include "attn_paged_line.cuh"
 #include "attn_paged_launch.h"
 
 namespace attn {
@@ -59,28 +60,6 @@ struct Params {
   int span;            // tokens per sub-tile
   float scale_log2;
 };
-
-// sum over i < n of floor((a i + b) / m), for a, b >= 0: the whole multiples of
-// m in a and b are summed directly; of what is left, points under a line of
-// slope a / m < 1 are counted by columns of the transposed line, as in
-// Euclid's algorithm.
-__device__ inline long long floor_sum(long long n, long long m, long long a, long long b) {
-  long long sum = 0;
-  while (n > 0) {
-    sum += n * (n - 1) / 2 * (a / m) + n * (b / m);
-    a %= m;
-    b %= m;
-    const long long top = a * n + b;   // the line's end, in m-ths
-    if (top < m) break;
-    // rows 1 .. top / m, each crossed at the column where the line reaches it
-    n = top / m;
-    b = top % m;
-    const long long t = m;
-    m = a;
-    a = t;
-  }
-  return sum;
-}
 
 // The CTA's walk over units.
 struct Walk {
@@ -233,20 +212,8 @@ __global__ void __launch_bounds__(kThreads, 1) fwd_kernel(const __grid_constant_
     line.load(w0);
     mine += line.cost(w0);
   }
-  long long incl = mine;
-#pragma unroll
-  for (int o = 1; o < 32; o <<= 1) {
-    const long long y = __shfl_up_sync(0xffffffffu, incl, o);
-    if (lane >= o) incl += y;
-  }
-  if (lane == 31) warp_sums[warp] = incl;
-  __syncthreads();
-  long long total = 0, before = incl - mine;
-#pragma unroll
-  for (int w = 0; w < kThreads / 32; ++w) {
-    if (w < warp) before += warp_sums[w];
-    total += warp_sums[w];
-  }
+  long long total;
+  const long long before = block_prefix<kThreads>(mine, warp_sums, total);
   const long long range = max((total + gridDim.x - 1) / gridDim.x, static_cast<long long>(kMinTiles));
   const long long begin = blockIdx.x * range, end = min(begin + range, total);
   if (begin >= before && begin < before + mine) {

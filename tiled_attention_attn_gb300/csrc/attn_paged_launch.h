@@ -21,4 +21,9 @@ long long paged_fwd_workspace(int sms, int d);
 int paged_fwd(const void* q, void* o, float* lse, int B, int Hq, int total, const PagedKV& c, int d, bool bf16,
               int page_size, const int* cu, bool causal, float scale, void* ws, int sms, int* err, cudaStream_t stream);
 
+long long paged_weights_workspace(int sms);
+int paged_weights(const void* q, const float* lse, float* weights, int weights_len, int B, int Hq, int total,
+                  const PagedKV& c, int d, bool bf16, int page_size, const int* cu, bool causal, float scale,
+                  float decay, void* ws, int sms, int* err, cudaStream_t stream);
+
 }  // namespace attn

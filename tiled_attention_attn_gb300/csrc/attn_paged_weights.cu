@@ -1,0 +1,594 @@
+// The attention weight that each cached key receives from a chunk of queries
+// (attn_key_weights):
+//   weights[b, g, j] = decay weights[b, g, j] + sum_h sum_i exp(scale q_ih . k_j - lse_ih)
+// The forward's lse makes every weight independent of the others, so no
+// softmax statistics are needed, only the scores again.
+//
+// S^T = K Q^T on tcgen05: the keys on the MMA's M dimension, (token, query
+// head) rows on N, so each thread owns one key, sums its columns in registers,
+// and the sum needs no exchange.  A CTA's unit is 256 keys of one key/value
+// head, two M = 128 tiles whose K stays in shared memory, against the
+// sequence's query tiles (all heads of the group), streamed through a ring: a
+// query tile serves both key tiles, which halves what the ring draws from L2.
+// Each key tile has its warpgroup and two S^T buffers in TMEM.
+//
+// NT, the columns of a query tile: 128 for chunks; 16 when a sequence has few
+// rows (one token's heads), where a 128-row box would fetch mostly other
+// sequences' queries.  The sums are fp32 in a fixed order.
+//
+// Work: the units' query tiles form a line cut into equal ranges, one per CTA;
+// a unit that reaches over a cut leaves 256 partial sums per piece, which
+// weights_merge_kernel adds in order (no atomics: the same bits every time).
+//
+// Bound: one exponential a pair (32 a clock and SM) and 2 d FLOPs for chunks;
+// K read once (HBM) for single tokens.
+#include <cuda_bf16.h>
+#include <cuda_fp16.h>
+#include <cuda_runtime.h>
+
+#include <cstdint>
+
+#include "attn_paged.h"
+#include "attn_paged_launch.h"
+#include "attn_paged_line.cuh"
+#include "attn_params.h"
+#include "ptx.cuh"
+
+namespace attn {
+namespace pwts {
+
+constexpr int kThr = 320;        // TMA warp, MMA warp, two warpgroups of four warps
+constexpr int kWTma = 0;
+constexpr int kWMma = 1;
+constexpr int kKeys = 256;       // keys per unit
+constexpr int kMinTiles = 4;     // a range's least length
+constexpr float kLog2e = 1.4426950408889634f;
+
+struct Params {
+  CUtensorMap tm_q;    // (d, Hq, total, 1), box 64 x heads x span x 1
+  CUtensorMap tm_k;    // (d, Hkv, page_size, num_pages), box 64 x 1 x min(page_size, 128) x 1
+  PagedKV c;
+  const float* lse;    // (Hq, total)
+  float* weights;      // (B, Hkv, len)
+  const int* cu;
+  int4* rec;           // per CTA: the unit whose first piece it ran (sequence, head, block, pieces)
+  float* part;         // partial sums [2 CTAs][256]
+  int* err;
+  unsigned long long timeout_ns;
+  int B, Hq, total, len, group, heads, parts, span;
+  float scale_log2, decay;
+};
+
+struct Walk {
+  int b, g, kb;
+  int q_len, k_len, row_q, n_kb;
+  long long p, begin, end;   // unit start on the line; this CTA's range
+  int n, t0, t1;             // query tiles of the unit; this CTA's part
+};
+
+// Unit kb of a sequence: keys 256 kb .. and the tokens that see them, the last
+// min(q_len, k_len - 256 kb) of the chunk (all, without the causal mask).
+template <bool CAUSAL>
+struct Line {
+  const Params& p;
+  __device__ int tokens(const Walk& w, int kb) const {
+    return CAUSAL ? min(w.q_len, w.k_len - kb * kKeys) : w.q_len;
+  }
+  __device__ int tiles(const Walk& w, int kb) const { return (tokens(w, kb) + p.span - 1) / p.span * p.parts; }
+  // cost of the units before kb of one head: query tiles, and one for K
+  __device__ long long before(const Walk& w, int kb) const {
+    if (kb <= 0) return 0;
+    const long long all = (w.q_len + p.span - 1) / p.span;
+    long long sum;
+    if (!CAUSAL) {
+      sum = all * kb;
+    } else {
+      const int off = w.k_len - w.q_len;
+      const int full = off < 0 ? 0 : min(kb, off / kKeys + 1);   // units that every token sees
+      sum = all * full;
+      if (kb > full)
+        sum += floor_sum(kb - full, p.span, kKeys, static_cast<long long>(w.k_len) - static_cast<long long>(kKeys) * (kb - 1) + p.span - 1);
+    }
+    return sum * p.parts + kb;
+  }
+  __device__ void load(Walk& w) const {
+    w.q_len = chunk_len(p.cu, w.b, p.total, w.row_q, p.err);
+    w.k_len = paged_len(p.c, w.b, p.err);
+    if (w.k_len > p.len) {
+      atomicCAS(p.err, 0, ATTN_DEVERR_BAD_SEQLENS);
+      w.k_len = 0;
+    }
+    w.n_kb = (w.k_len + kKeys - 1) / kKeys;
+  }
+  __device__ long long cost(const Walk& w) const { return before(w, w.n_kb) * p.c.hkv; }
+  __device__ void advance(Walk& w) const {
+    w.p += w.n + 1;
+    if (++w.kb == w.n_kb) {
+      w.kb = 0;
+      if (++w.g == p.c.hkv) {
+        w.g = 0;
+        while (++w.b < p.B) {
+          load(w);
+          if (w.n_kb > 0) break;
+        }
+      }
+    }
+    if (w.b < p.B) w.n = tiles(w, w.kb);
+  }
+  __device__ bool next(Walk& w, bool first) const {
+    if (!first) advance(w);
+    while (w.b < p.B && w.p < w.end) {
+      const long long lo = w.begin - w.p, hi = w.end - w.p;
+      w.t0 = lo > 0 ? static_cast<int>(min(lo, static_cast<long long>(w.n))) : 0;
+      w.t1 = static_cast<int>(min(hi, static_cast<long long>(w.n)));
+      if (w.t0 < w.t1 || (w.n == 0 && lo <= 0)) return true;
+      advance(w);
+    }
+    return false;
+  }
+  // query tile i of unit kb: its head part and first token
+  __device__ void tile(const Walk& w, int i, int& part, int& tok) const {
+    const int t = tokens(w, w.kb), per = (t + p.span - 1) / p.span;
+    part = i / per;
+    tok = w.q_len - t + (i - part * per) * p.span;
+  }
+  // whether some key of key tile x sees a token of the tile starting at tok
+  __device__ bool active(const Walk& w, int x, int tok) const {
+    const int key = w.kb * kKeys + x * 128;
+    if (key >= w.k_len) return false;
+    return !CAUSAL || min(tok + p.span, w.q_len) - 1 + (w.k_len - w.q_len) >= key;
+  }
+};
+
+template <int D, int NT>
+struct WCfg {
+  static constexpr int kChunks = D / 64;
+  static constexpr int kKTile = 128 * D * 2;              // one key tile
+  static constexpr int kKStage = 2 * kKTile;
+  static constexpr int kQStage = NT * D * 2;
+  static constexpr int kKS = NT == 128 ? (D == 128 ? 2 : 3) : (D == 128 ? 3 : 6);
+  static constexpr int kQS = NT == 128 ? (D == 128 ? 2 : 4) : 4;
+  static constexpr int kOffK = 0;
+  static constexpr int kOffQ = kOffK + kKS * kKStage;
+  static constexpr int kOffL = kOffQ + kQS * kQStage;     // lse columns, times log2 e: [warp][parity][NT]
+  static constexpr int kOffBar = kOffL + 8 * 2 * NT * 4;
+  static constexpr int kNBars = 2 * kKS + 2 * kQS + 8 + 1;
+  static constexpr int kOffMisc = kOffBar + (kNBars + 1) / 2 * 16;
+  static constexpr int kSmem = kOffMisc + 256 + 1024;
+  static constexpr uint32_t kTmemCols = 4 * NT;           // [key tile][buffer]
+  static_assert(kSmem <= 227 * 1024, "shared memory");
+};
+
+template <int D, int NT, bool BF16, bool CAUSAL>
+__global__ void __launch_bounds__(kThr, 1) weights_kernel(const __grid_constant__ Params p) {
+  using C = WCfg<D, NT>;
+  extern __shared__ __align__(1024) uint8_t smem_raw[];
+  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const uint32_t sbase = smem_u32(smem);
+  const uint32_t sK = sbase + C::kOffK, sQ = sbase + C::kOffQ;
+  const uint32_t bar0 = sbase + C::kOffBar;
+  auto b_k_full = [&](int s) { return bar0 + 8 * s; };
+  auto b_k_empty = [&](int s) { return bar0 + 8 * (C::kKS + s); };
+  const uint32_t bar1 = bar0 + 16 * C::kKS;
+  auto b_q_full = [&](int s) { return bar1 + 8 * s; };
+  auto b_q_empty = [&](int s) { return bar1 + 8 * (C::kQS + s); };
+  const uint32_t bar2 = bar1 + 16 * C::kQS;
+  auto b_s_full = [&](int x, int s) { return bar2 + 8 * (2 * x + s); };
+  auto b_s_free = [&](int x, int s) { return bar2 + 32 + 8 * (2 * x + s); };
+  const uint32_t b_drain = bar2 + 64;
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + C::kOffMisc);
+  volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + C::kOffMisc + 4);
+  volatile int* start = reinterpret_cast<volatile int*>(smem + C::kOffMisc + 8);   // b, g, kb
+  volatile long long* start_p = reinterpret_cast<volatile long long*>(smem + C::kOffMisc + 24);
+  long long* warp_sums = reinterpret_cast<long long*>(smem + C::kOffMisc + 32);
+  WaitCtl wc{p.err, abort_flag, p.timeout_ns};
+
+  if (tid == 0) {
+    *abort_flag = 0;
+    start[0] = p.B;
+    for (int s = 0; s < C::kKS; ++s) {
+      mbar_init(b_k_full(s), 1);
+      mbar_init(b_k_empty(s), 1);
+    }
+    for (int s = 0; s < C::kQS; ++s) {
+      mbar_init(b_q_full(s), 1);
+      mbar_init(b_q_empty(s), 1);
+    }
+    for (int x = 0; x < 2; ++x)
+      for (int s = 0; s < 2; ++s) {
+        mbar_init(b_s_full(x, s), 1);
+        mbar_init(b_s_free(x, s), 4);   // the four warps of the key tile
+      }
+    mbar_init(b_drain, 1);
+    fence_mbar_init();
+  }
+  if (warp == kWTma && lane == 0) {
+    tma_prefetch_desc(&p.tm_q);
+    tma_prefetch_desc(&p.tm_k);
+  }
+  if (warp == kWMma) {
+    tmem_alloc(smem_u32(tmem_slot), C::kTmemCols);
+    tmem_relinquish();
+  }
+
+  const Line<CAUSAL> line{p};
+  Walk w0;
+  const int strip = (p.B + kThr - 1) / kThr;
+  const int b_lo = min(tid * strip, p.B), b_hi = min(b_lo + strip, p.B);
+  long long mine = 0;
+  for (w0.b = b_lo; w0.b < b_hi; ++w0.b) {
+    line.load(w0);
+    mine += line.cost(w0);
+  }
+  long long total;
+  const long long before = block_prefix<kThr>(mine, warp_sums, total);
+  const long long range = max((total + gridDim.x - 1) / gridDim.x, static_cast<long long>(kMinTiles));
+  const long long begin = blockIdx.x * range, end = min(begin + range, total);
+  if (begin >= before && begin < before + mine) {
+    long long at = before;
+    for (w0.b = b_lo; w0.b < b_hi; ++w0.b) {
+      line.load(w0);
+      const long long cost = line.cost(w0);
+      if (begin < at + cost) {
+        const long long per = line.before(w0, w0.n_kb);
+        const int g = static_cast<int>((begin - at) / per);
+        at += g * per;
+        int lo = 0, hi = w0.n_kb;   // the last unit that starts at or before `begin`
+        while (hi - lo > 1) {
+          const int mid = (lo + hi) >> 1;
+          if (at + line.before(w0, mid) <= begin) lo = mid; else hi = mid;
+        }
+        start[0] = w0.b;
+        start[1] = g;
+        start[2] = lo;
+        *start_p = at + line.before(w0, lo);
+        break;
+      }
+      at += cost;
+    }
+  }
+  if (tid == 0) p.rec[blockIdx.x] = make_int4(0, 0, 0, 0);
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = *tmem_slot;
+  grid_launch_dependents();
+  w0.b = start[0];
+  w0.begin = begin;
+  w0.end = end;
+  w0.p = 0;
+  w0.g = w0.kb = w0.n = w0.n_kb = 0;
+  if (w0.b < p.B) {
+    w0.g = start[1];
+    w0.kb = start[2];
+    w0.p = *start_p;
+    line.load(w0);
+    w0.n = line.tiles(w0, w0.kb);
+  }
+
+  if (warp == kWTma) {
+    // ------------------------------------------------------------------ TMA producer
+    uint32_t k_cnt = 0, q_cnt = 0;
+    const int box = min(1 << p.c.page_log2, 128);   // tokens per box
+    const int n_pg = 128 / box;                     // boxes along a key tile
+    // this lane's box of K: key tile x, feature chunk, page
+    const int pg = lane % n_pg, ch = (lane / n_pg) % C::kChunks, x = lane / (n_pg * C::kChunks);
+    const bool has = lane < 2 * C::kChunks * n_pg;
+    const uint32_t dst0 = sK + x * C::kKTile + ch * 16384 + pg * box * 128;
+    Walk w = w0;
+    bool ok = true;
+    for (bool more = line.next(w, true); more && ok; more = line.next(w, false)) {
+      if (w.t1 <= w.t0) continue;
+      const int key = w.kb * kKeys + x * 128 + pg * box;
+      int page = -1;
+      if (has && key < w.k_len) {
+        page = paged_page(p.c, w.b, key >> p.c.page_log2, p.err);
+        if (page < 0) page = p.c.num_pages;   // no page: rows past the pool read as zeros
+      }
+      const int ks = k_cnt % C::kKS;
+      if (!mbar_wait_warp(b_k_empty(ks), ((k_cnt / C::kKS) & 1) ^ 1, wc, ATTN_DEVERR_WAIT_TIMEOUT_SITE(kSiteKEmpty))) break;
+      const uint32_t n_box = __popc(__ballot_sync(0xffffffffu, page >= 0));
+      if (lane == 0) mbar_arrive_expect_tx(b_k_full(ks), n_box * box * 128);
+      __syncwarp();
+      if (page >= 0)
+        tma_load_4d(dst0 + ks * C::kKStage, &p.tm_k, b_k_full(ks), ch * 64, w.g, key & ((1 << p.c.page_log2) - 1), page);
+      ++k_cnt;
+      for (int i = w.t0; i < w.t1; ++i) {
+        const int qs = q_cnt % C::kQS;
+        if (!mbar_wait_warp(b_q_empty(qs), ((q_cnt / C::kQS) & 1) ^ 1, wc,
+                            ATTN_DEVERR_WAIT_TIMEOUT_SITE(kSiteQEmpty))) { ok = false; break; }
+        if (lane == 0) {
+          int part, tok;
+          line.tile(w, i, part, tok);
+          mbar_arrive_expect_tx(b_q_full(qs), C::kChunks * p.heads * p.span * 128);
+#pragma unroll
+          for (int c = 0; c < C::kChunks; ++c)
+            tma_load_4d(sQ + qs * C::kQStage + c * NT * 128, &p.tm_q, b_q_full(qs), c * 64,
+                        w.g * p.group + part * p.heads, w.row_q + tok, 0);
+        }
+        ++q_cnt;
+      }
+    }
+    if (lane == 0 && *abort_flag) {
+      // let the loads already issued land before the CTA exits
+      for (int s = 0; s < C::kKS; ++s) {
+        const uint32_t n = (k_cnt + C::kKS - 1 - s) / C::kKS;
+        if (n > 0) mbar_wait(b_k_full(s), (n - 1) & 1, wc, ATTN_DEVERR_WAIT_TIMEOUT_SITE(kSiteDrain), false);
+      }
+      for (int s = 0; s < C::kQS; ++s) {
+        const uint32_t n = (q_cnt + C::kQS - 1 - s) / C::kQS;
+        if (n > 0) mbar_wait(b_q_full(s), (n - 1) & 1, wc, ATTN_DEVERR_WAIT_TIMEOUT_SITE(kSiteDrain), false);
+      }
+    }
+  } else if (warp == kWMma) {
+    // ------------------------------------------------------------------ MMA issuer
+    if (lane == 0) {
+      constexpr uint32_t kIdesc = idesc_f16_f32acc(128, NT, BF16, false);
+      const uint64_t dk0 = sdesc_sw128(sK, 16, 1024);
+      const uint64_t dq0 = sdesc_sw128(sQ, 16, 1024);
+      uint32_t k_cnt = 0, q_cnt = 0, s_cnt[2] = {0, 0};
+      bool ok = true;
+      Walk w = w0;
+      for (bool more = line.next(w, true); more && ok; more = line.next(w, false)) {
+        if (w.t1 <= w.t0) continue;
+        const int ks = k_cnt % C::kKS;
+        if (!mbar_wait(b_k_full(ks), (k_cnt / C::kKS) & 1, wc, ATTN_DEVERR_WAIT_TIMEOUT_SITE(kSiteKFull))) break;
+        ++k_cnt;
+        for (int i = w.t0; i < w.t1 && ok; ++i) {
+          const int qs = q_cnt % C::kQS;
+          if (!mbar_wait(b_q_full(qs), (q_cnt / C::kQS) & 1, wc, ATTN_DEVERR_WAIT_TIMEOUT_SITE(kSiteQFull))) {
+            ok = false;
+            break;
+          }
+          ++q_cnt;
+          int part, tok;
+          line.tile(w, i, part, tok);
+#pragma unroll
+          for (int x = 0; x < 2; ++x) {
+            if (!line.active(w, x, tok)) continue;
+            const int sb = s_cnt[x] & 1;
+            if (!mbar_wait(b_s_free(x, sb), ((s_cnt[x] >> 1) & 1) ^ 1, wc, ATTN_DEVERR_WAIT_TIMEOUT_SITE(kSiteSFree))) {
+              ok = false;
+              break;
+            }
+            ++s_cnt[x];
+            tc_fence_after();
+#pragma unroll
+            for (int kk = 0; kk < D / 16; ++kk) {
+              const uint64_t a = dk0 + ((ks * C::kKStage + x * C::kKTile + (kk >> 2) * 16384 + (kk & 3) * 32) >> 4);
+              const uint64_t b = dq0 + ((qs * C::kQStage + (kk >> 2) * NT * 128 + (kk & 3) * 32) >> 4);
+              umma_ss(tmem + (2 * x + sb) * NT, a, b, kIdesc, kk > 0 ? 1u : 0u);
+            }
+            umma_commit(b_s_full(x, sb));
+          }
+          umma_commit(b_q_empty(qs));
+        }
+        if (!ok) break;
+        umma_commit(b_k_empty(ks));
+      }
+      umma_commit(b_drain);
+      mbar_wait(b_drain, 0, wc, ATTN_DEVERR_WAIT_TIMEOUT_SITE(kSiteDrain), false);
+    }
+  } else {
+    // ------------------------------------------------------------------ one warpgroup per key tile
+    const int x = (warp - 2) >> 2;
+    const int quarter = warp & 3;
+    const int lrow = quarter * 32 + lane;   // TMEM lane: key of the tile
+    const uint32_t t_s = tmem + (static_cast<uint32_t>(quarter * 32) << 16) + 2 * x * NT;
+    // each warp keeps the tile's lse columns for itself: lane's columns are
+    // lane, lane + 32, ...
+    float* lse_s = reinterpret_cast<float*>(smem + C::kOffL) + (warp - 2) * 2 * NT;
+    constexpr int NC = (NT + 31) / 32;
+    int col_tok[NC], col_head[NC];
+#pragma unroll
+    for (int k = 0; k < NC; ++k) {
+      col_tok[k] = (lane + 32 * k) / p.heads;
+      col_head[k] = lane + 32 * k - col_tok[k] * p.heads;
+    }
+    const float2 c2 = make_float2(p.scale_log2, p.scale_log2);
+    uint32_t s_cnt = 0;
+    Walk w = w0;
+    bool ok = true;
+    for (bool more = line.next(w, true); more && ok; more = line.next(w, false)) {
+      const int key = w.kb * kKeys + x * 128 + lrow;
+      float2 sum = make_float2(0.0f, 0.0f);
+      // this lane's lse columns of query tile i; +inf where the column is no
+      // query or its query saw no key
+      auto load_lse = [&](int i, float (&l)[NC]) {
+        int part, tok;
+        line.tile(w, i, part, tok);
+        const int n_heads = min(p.heads, p.group - part * p.heads);
+        const float* base = p.lse + static_cast<long long>(w.g * p.group + part * p.heads) * p.total + w.row_q + tok;
+#pragma unroll
+        for (int k = 0; k < NC; ++k) {
+          l[k] = INFINITY;
+          if (lane + 32 * k < NT && col_tok[k] < p.span && col_head[k] < n_heads && tok + col_tok[k] < w.q_len) {
+            const float v = __ldg(base + static_cast<long long>(col_head[k]) * p.total + col_tok[k]);
+            if (v != -INFINITY) l[k] = v * kLog2e;
+          }
+        }
+      };
+      float l_next[NC];
+      if (w.t0 < w.t1) load_lse(w.t0, l_next);
+      for (int i = w.t0; i < w.t1; ++i) {
+        int part, tok;
+        line.tile(w, i, part, tok);
+        const int sb = s_cnt & 1;
+        const bool act = line.active(w, x, tok);
+        float* ls = lse_s + sb * NT;   // its last readers are two tiles back
+        if (act) {
+#pragma unroll
+          for (int k = 0; k < NC; ++k)
+            if (lane + 32 * k < NT) ls[lane + 32 * k] = l_next[k];
+        }
+        if (i + 1 < w.t1) load_lse(i + 1, l_next);
+        if (!act) continue;
+        __syncwarp();
+        if (!mbar_wait_warp(b_s_full(x, sb), (s_cnt >> 1) & 1, wc, ATTN_DEVERR_WAIT_TIMEOUT_SITE(kSiteSFull))) {
+          ok = false;
+          break;
+        }
+        ++s_cnt;
+        tc_fence_after();
+        // columns this key sees: from c_lo (causal), those that are queries
+        const int n_heads = min(p.heads, p.group - part * p.heads);
+        int c_lo = 0;
+        if (CAUSAL) c_lo = max(0, (key - (w.k_len - w.q_len) - tok)) * p.heads;
+        const bool full = (!CAUSAL || w.kb * kKeys + x * 128 + 127 - (w.k_len - w.q_len) <= tok) &&
+                          tok + p.span <= w.q_len && n_heads == p.heads && p.heads * p.span == NT;
+        constexpr int CB = NT < 32 ? NT : 32;   // columns per TMEM load
+#pragma unroll
+        for (int c0 = 0; c0 < NT; c0 += CB) {
+          uint32_t r[CB];
+          if constexpr (CB == 32) tmem_ld_32x32b_x32(t_s + sb * NT + c0, r);
+          else tmem_ld_32x32b_x16(t_s + sb * NT + c0, r);
+          tmem_wait_ld(r);
+          if (c0 + CB == NT) {
+            // the buffer is in registers: the next scores may overwrite it
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(b_s_free(x, sb));
+          }
+#pragma unroll
+          for (int k = 0; k < CB; k += 4) {
+            const float4 l4 = *reinterpret_cast<const float4*>(ls + c0 + k);
+            const float2 a = ffma2(make_float2(__uint_as_float(r[k]), __uint_as_float(r[k + 1])), c2, make_float2(-l4.x, -l4.y));
+            const float2 b = ffma2(make_float2(__uint_as_float(r[k + 2]), __uint_as_float(r[k + 3])), c2, make_float2(-l4.z, -l4.w));
+            float2 e0 = make_float2(ex2_approx(a.x), ex2_approx(a.y));
+            float2 e1 = make_float2(ex2_approx(b.x), ex2_approx(b.y));
+            if (!full) {
+              // dropped by index and by lse = +inf, whatever the score
+              if (c0 + k < c_lo || l4.x == INFINITY) e0.x = 0.0f;
+              if (c0 + k + 1 < c_lo || l4.y == INFINITY) e0.y = 0.0f;
+              if (c0 + k + 2 < c_lo || l4.z == INFINITY) e1.x = 0.0f;
+              if (c0 + k + 3 < c_lo || l4.w == INFINITY) e1.y = 0.0f;
+            }
+            sum = fadd2(sum, fadd2(e0, e1));
+          }
+        }
+      }
+      if (!ok) break;
+      const bool whole = w.t1 - w.t0 == w.n;
+      const float s = sum.x + sum.y;
+      if (whole) {
+        if (key < w.k_len) {
+          float* out = p.weights + (static_cast<long long>(w.b) * p.c.hkv + w.g) * p.len + key;
+          *out = (p.decay != 0.0f ? p.decay * *out : 0.0f) + s;
+        }
+      } else {
+        p.part[(2 * blockIdx.x + (w.t0 == 0 ? 1 : 0)) * kKeys + x * 128 + lrow] = s;
+        if (w.t0 == 0 && warp == 2 && lane == 0)
+          p.rec[blockIdx.x] = make_int4(w.b, w.g, w.kb,
+                                        static_cast<int>((w.p + w.n - 1) / range) - static_cast<int>(blockIdx.x) + 1);
+      }
+    }
+  }
+  tc_fence_before();
+  __syncthreads();
+  if (warp == kWMma) {
+    __syncwarp();
+    tc_fence_after();
+    tmem_dealloc(tmem, C::kTmemCols);
+  }
+}
+
+// Adds the pieces of the unit that block x's CTA began, in order.
+__global__ void __launch_bounds__(kKeys) weights_merge_kernel(const __grid_constant__ Params p) {
+  grid_wait_prerequisites();
+  const int c = blockIdx.x;
+  const int4 rec = __ldcg(p.rec + c);
+  if (rec.w <= 1) return;
+  const int key = rec.z * kKeys + threadIdx.x;
+  float s = __ldcg(p.part + (2 * c + 1) * kKeys + threadIdx.x);
+  for (int i = 1; i < rec.w; ++i) s += __ldcg(p.part + 2 * (c + i) * kKeys + threadIdx.x);
+  if (key >= __ldg(p.c.seqlens + rec.x)) return;
+  float* out = p.weights + (static_cast<long long>(rec.x) * p.c.hkv + rec.y) * p.len + key;
+  *out = (p.decay != 0.0f ? p.decay * *out : 0.0f) + s;
+}
+
+template <int D, int NT, bool BF16, bool CAUSAL>
+cudaError_t launch(const Params& p, int grid, cudaStream_t stream) {
+  constexpr int smem = WCfg<D, NT>::kSmem;
+  static bool attr_done[64] = {};   // per instantiation
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  if (dev < 0 || dev >= 64 || !attr_done[dev]) {
+    e = cudaFuncSetAttribute(weights_kernel<D, NT, BF16, CAUSAL>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+    if (e != cudaSuccess) return e;
+    if (dev >= 0 && dev < 64) attr_done[dev] = true;
+  }
+  weights_kernel<D, NT, BF16, CAUSAL><<<grid, kThr, smem, stream>>>(p);
+  e = cudaGetLastError();
+  if (e != cudaSuccess) return e;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(grid);
+  cfg.blockDim = dim3(kKeys);
+  cfg.stream = stream;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, weights_merge_kernel, p);
+}
+
+template <int D, int NT>
+cudaError_t pick(const Params& p, bool bf16, bool causal, int grid, cudaStream_t stream) {
+  if (bf16) return causal ? launch<D, NT, true, true>(p, grid, stream) : launch<D, NT, true, false>(p, grid, stream);
+  return causal ? launch<D, NT, false, true>(p, grid, stream) : launch<D, NT, false, false>(p, grid, stream);
+}
+
+size_t rec_bytes(int sms) { return (static_cast<size_t>(sms) * sizeof(int4) + 255) / 256 * 256; }
+
+}  // namespace pwts
+
+long long paged_weights_workspace(int sms) {
+  return static_cast<long long>(pwts::rec_bytes(sms) + static_cast<size_t>(2 * sms) * pwts::kKeys * sizeof(float));
+}
+
+int paged_weights(const void* q, const float* lse, float* weights, int weights_len, int B, int Hq, int total,
+                  const PagedKV& c, int d, bool bf16, int page_size, const int* cu, bool causal, float scale,
+                  float decay, void* ws, int sms, int* err, cudaStream_t stream) {
+  pwts::Params p;
+  p.c = c;
+  p.group = Hq / c.hkv;
+  // few rows per sequence: tiles of 16 columns
+  const bool few = static_cast<long long>(total) * p.group <= 16LL * B;
+  const int nt = few ? 16 : 128;
+  p.parts = (p.group + nt - 1) / nt;
+  p.heads = (p.group + p.parts - 1) / p.parts;
+  p.parts = (p.group + p.heads - 1) / p.heads;
+  p.span = nt / p.heads;
+  // with no rows at all nothing is loaded through the map
+  const int rows = total > 0 ? total : 1;
+  if (int rc = tile_map(q, bf16, d, Hq, rows, 1, d, static_cast<long long>(Hq) * d,
+                        static_cast<long long>(rows) * Hq * d, p.heads, p.span, p.tm_q))
+    return rc;
+  const int box = page_size < 128 ? page_size : 128;
+  if (int rc = tile_map(c.k, bf16, d, c.hkv, page_size, c.num_pages, c.s_head, c.s_token, c.s_page, 1, box, p.tm_k)) return rc;
+  char* w = static_cast<char*>(ws);
+  p.rec = reinterpret_cast<int4*>(w);
+  p.part = reinterpret_cast<float*>(w + pwts::rec_bytes(sms));
+  p.lse = lse;
+  p.weights = weights;
+  p.cu = cu;
+  p.err = err;
+  p.timeout_ns = wait_timeout_ns();
+  p.B = B;
+  p.Hq = Hq;
+  p.total = total;
+  p.len = weights_len;
+  p.scale_log2 = scale * pwts::kLog2e;
+  p.decay = decay;
+  cudaError_t e;
+  if (d == 64) e = few ? pwts::pick<64, 16>(p, bf16, causal, sms, stream) : pwts::pick<64, 128>(p, bf16, causal, sms, stream);
+  else e = few ? pwts::pick<128, 16>(p, bf16, causal, sms, stream) : pwts::pick<128, 128>(p, bf16, causal, sms, stream);
+  if (e != cudaSuccess) return ATTN_ELAUNCH;
+  count_launch();
+  count_launch();
+  return ATTN_OK;
+}
+
+}  // namespace attn

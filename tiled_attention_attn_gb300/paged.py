@@ -45,7 +45,7 @@ def declare(L) -> None:
     L.attn_cache_append.argtypes = [vp, vp, vp, vp, ll, ll, ll, i, i, i, kv, vp, i, vp, f, i, vp, vp]
     L.attn_fwd_paged.argtypes = [vp, vp, vp, i, i, i, kv, vp, i, f, vp, ll, vp]
     L.attn_decode_paged.argtypes = [vp, vp, vp, i, i, kv, f, vp, ll, vp]
-    L.attn_key_weights.argtypes = [vp, vp, vp, i, i, i, i, kv, vp, i, f, f, vp]
+    L.attn_key_weights.argtypes = [vp, vp, vp, i, i, i, i, kv, vp, i, f, f, vp, ll, vp]
     L.attn_cache_evict.argtypes = [vp, i, vp, vp, vp, i, i, kv, vp, i, i, i, i, vp]
     L.attn_paged_workspace_bytes.argtypes = [i, i]
     L.attn_paged_workspace_bytes.restype = ll
@@ -308,11 +308,14 @@ def cache_append(k: torch.Tensor, v: torch.Tensor, k_pages: torch.Tensor, v_page
 _ws_bytes: dict = {}
 
 
-def _workspace(device: torch.device, d: int, decode: bool) -> torch.Tensor:
-    key = (device.index, d, decode)
+_CHUNK, _DECODE, _WEIGHTS = 0, 1, 2   # ATTN_PAGED_*
+
+
+def _workspace(device: torch.device, d: int, call: int) -> torch.Tensor:
+    key = (device.index, d, call)
     n = _ws_bytes.get(key)
     if n is None:
-        n = _attn.lib().attn_paged_workspace_bytes(d, int(decode))
+        n = _attn.lib().attn_paged_workspace_bytes(d, call)
         if n < 0:
             raise _attn.AttnError(int(n), "attn_paged_workspace_bytes")
         _ws_bytes[key] = n
@@ -348,7 +351,7 @@ def attn_fwd_paged(q: torch.Tensor, k_pages: torch.Tensor, v_pages: torch.Tensor
         scale = 1.0 / math.sqrt(c.head_dim)
     with _on(q.device, stream) as s:
         out, lse = _outputs(q, out, lse)
-        ws = _workspace(q.device, c.head_dim, False)
+        ws = _workspace(q.device, c.head_dim, _CHUNK)
         rc = _attn.lib().attn_fwd_paged(q.data_ptr(), out.data_ptr(), lse.data_ptr(), B, q.shape[1], q.shape[0],
                                         ctypes.byref(c), cu_seqlens.data_ptr(), int(bool(causal)), float(scale),
                                         ws.data_ptr(), ws.numel(), s) if q.shape[0] else 0
@@ -371,7 +374,7 @@ def attn_decode_paged(q: torch.Tensor, k_pages: torch.Tensor, v_pages: torch.Ten
         scale = 1.0 / math.sqrt(c.head_dim)
     with _on(q.device, stream) as s:
         out, lse = _outputs(q, out, lse)
-        ws = _workspace(q.device, c.head_dim, True)
+        ws = _workspace(q.device, c.head_dim, _DECODE)
         rc = _attn.lib().attn_decode_paged(q.data_ptr(), out.data_ptr(), lse.data_ptr(), q.shape[0], q.shape[1],
                                            ctypes.byref(c), float(scale), ws.data_ptr(), ws.numel(), s)
     _check_rc(rc, "attn_decode_paged")
@@ -404,9 +407,10 @@ def key_weights(q: torch.Tensor, k_pages: torch.Tensor, lse: torch.Tensor, page_
         if weights.dim() != 3 or weights.shape[:2] != (B, c.num_kv_heads) or weights.dtype != torch.float32 or \
                 weights.device != dev or not weights.is_contiguous():
             raise ValueError("weights must be a contiguous float32 tensor (B, Hkv, n)")
+        ws = _workspace(dev, d, _WEIGHTS)
         rc = _attn.lib().attn_key_weights(q.data_ptr() or None, lse.data_ptr() or None, weights.data_ptr() or None,
                                           weights.shape[2], B, Hq, T, ctypes.byref(c), cu_seqlens.data_ptr(),
-                                          int(bool(causal)), float(scale), float(decay), s)
+                                          int(bool(causal)), float(scale), float(decay), ws.data_ptr(), ws.numel(), s)
     _check_rc(rc, "attn_key_weights")
     return weights
 
