@@ -126,18 +126,37 @@ struct Line {
     }
     return false;
   }
-  // query tile i of unit kb: its head part and first token
-  __device__ void tile(const Walk& w, int i, int& part, int& tok) const {
-    const int t = tokens(w, w.kb), per = (t + p.span - 1) / p.span;
-    part = i / per;
-    tok = w.q_len - t + (i - part * per) * p.span;
+};
+
+// The query tiles of a piece, from its first: head part and first token, and
+// which key tiles see the tile (kept as running values: the roles are single
+// threads or few warps, whose dependent integer divisions would show).
+template <bool CAUSAL>
+struct Tiles {
+  int part, tok, tok0, q_len, span;
+  int tok_min[2];   // key tile x is seen by a tile that starts at tok >= tok_min[x]
+  __device__ Tiles(const Params& p, const Walk& w, const Line<CAUSAL>& line) {
+    const int t = line.tokens(w, w.kb), per = (t + p.span - 1) / p.span;
+    span = p.span;
+    q_len = w.q_len;
+    tok0 = w.q_len - t;
+    part = per > 0 ? w.t0 / per : 0;
+    tok = tok0 + (w.t0 - part * per) * p.span;
+#pragma unroll
+    for (int x = 0; x < 2; ++x) {
+      const int key = w.kb * kKeys + x * 128;
+      // the tile's last token, tok + span - 1, sees keys up to it + k_len - q_len
+      tok_min[x] = key >= w.k_len ? 0x7fffffff : CAUSAL ? key - (w.k_len - w.q_len) - p.span + 1 : -0x7fffffff;
+    }
   }
-  // whether some key of key tile x sees a token of the tile starting at tok
-  __device__ bool active(const Walk& w, int x, int tok) const {
-    const int key = w.kb * kKeys + x * 128;
-    if (key >= w.k_len) return false;
-    return !CAUSAL || min(tok + p.span, w.q_len) - 1 + (w.k_len - w.q_len) >= key;
+  __device__ void next() {
+    tok += span;
+    if (tok >= q_len) {
+      tok = tok0;
+      ++part;
+    }
   }
+  __device__ bool active(int x) const { return tok >= (x == 0 ? tok_min[0] : tok_min[1]); }
 };
 
 template <int D, int NT>
@@ -158,6 +177,57 @@ struct WCfg {
   static constexpr uint32_t kTmemCols = 4 * NT;           // [key tile][buffer]
   static_assert(kSmem <= 227 * 1024, "shared memory");
 };
+
+// Adds exp2(s c - lse) of CB columns to sum; MASK drops those before column
+// c_lo - c0 and those whose lse is +inf, whatever their score.
+template <int CB, bool MASK>
+__device__ __forceinline__ void add_columns(const uint32_t (&r)[CB], const float* ls, float2 c2, int lim, float2 (&sum)[2]) {
+#pragma unroll
+  for (int k = 0; k < CB; k += 4) {
+    const float4 l4 = *reinterpret_cast<const float4*>(ls + k);
+    const float2 a = ffma2(make_float2(__uint_as_float(r[k]), __uint_as_float(r[k + 1])), c2, make_float2(-l4.x, -l4.y));
+    const float2 b = ffma2(make_float2(__uint_as_float(r[k + 2]), __uint_as_float(r[k + 3])), c2, make_float2(-l4.z, -l4.w));
+    float2 e0 = make_float2(ex2_approx(a.x), ex2_approx(a.y));
+    float2 e1 = make_float2(ex2_approx(b.x), ex2_approx(b.y));
+    if constexpr (MASK) {
+      e0.x = (k >= lim && l4.x != INFINITY) ? e0.x : 0.0f;
+      e0.y = (k + 1 >= lim && l4.y != INFINITY) ? e0.y : 0.0f;
+      e1.x = (k + 2 >= lim && l4.z != INFINITY) ? e1.x : 0.0f;
+      e1.y = (k + 3 >= lim && l4.w != INFINITY) ? e1.y : 0.0f;
+    }
+    sum[0] = fadd2(sum[0], e0);
+    sum[1] = fadd2(sum[1], e1);
+  }
+}
+
+// One S^T tile's columns of this thread's key; the next columns load while
+// these are added.
+template <int NT, bool MASK, class Release>
+__device__ __forceinline__ void add_tile(uint32_t t_s, const float* ls, float2 c2, int c_lo, float2 (&sum)[2],
+                                         Release release) {
+  if constexpr (NT == 16) {
+    uint32_t r[16];
+    tmem_ld_32x32b_x16(t_s, r);
+    tmem_wait_ld(r);
+    release();
+    add_columns<16, MASK>(r, ls, c2, c_lo, sum);
+  } else {
+    uint32_t r0[32], r1[32];
+    tmem_ld_32x32b_x32(t_s, r0);
+    tmem_wait_ld(r0);
+    tmem_ld_32x32b_x32(t_s + 32, r1);
+    add_columns<32, MASK>(r0, ls, c2, c_lo, sum);
+    tmem_wait_ld(r1);
+    tmem_ld_32x32b_x32(t_s + 64, r0);
+    add_columns<32, MASK>(r1, ls + 32, c2, c_lo - 32, sum);
+    tmem_wait_ld(r0);
+    tmem_ld_32x32b_x32(t_s + 96, r1);
+    add_columns<32, MASK>(r0, ls + 64, c2, c_lo - 64, sum);
+    tmem_wait_ld(r1);
+    release();
+    add_columns<32, MASK>(r1, ls + 96, c2, c_lo - 96, sum);
+  }
+}
 
 template <int D, int NT, bool BF16, bool CAUSAL>
 __global__ void __launch_bounds__(kThr, 1) weights_kernel(const __grid_constant__ Params p) {
@@ -294,18 +364,17 @@ __global__ void __launch_bounds__(kThr, 1) weights_kernel(const __grid_constant_
       if (page >= 0)
         tma_load_4d(dst0 + ks * C::kKStage, &p.tm_k, b_k_full(ks), ch * 64, w.g, key & ((1 << p.c.page_log2) - 1), page);
       ++k_cnt;
-      for (int i = w.t0; i < w.t1; ++i) {
+      Tiles<CAUSAL> it(p, w, line);
+      for (int i = w.t0; i < w.t1; ++i, it.next()) {
         const int qs = q_cnt % C::kQS;
         if (!mbar_wait_warp(b_q_empty(qs), ((q_cnt / C::kQS) & 1) ^ 1, wc,
                             ATTN_DEVERR_WAIT_TIMEOUT_SITE(kSiteQEmpty))) { ok = false; break; }
         if (lane == 0) {
-          int part, tok;
-          line.tile(w, i, part, tok);
           mbar_arrive_expect_tx(b_q_full(qs), C::kChunks * p.heads * p.span * 128);
 #pragma unroll
           for (int c = 0; c < C::kChunks; ++c)
             tma_load_4d(sQ + qs * C::kQStage + c * NT * 128, &p.tm_q, b_q_full(qs), c * 64,
-                        w.g * p.group + part * p.heads, w.row_q + tok, 0);
+                        w.g * p.group + it.part * p.heads, w.row_q + it.tok, 0);
         }
         ++q_cnt;
       }
@@ -335,18 +404,17 @@ __global__ void __launch_bounds__(kThr, 1) weights_kernel(const __grid_constant_
         const int ks = k_cnt % C::kKS;
         if (!mbar_wait(b_k_full(ks), (k_cnt / C::kKS) & 1, wc, ATTN_DEVERR_WAIT_TIMEOUT_SITE(kSiteKFull))) break;
         ++k_cnt;
-        for (int i = w.t0; i < w.t1 && ok; ++i) {
+        Tiles<CAUSAL> it(p, w, line);
+        for (int i = w.t0; i < w.t1 && ok; ++i, it.next()) {
           const int qs = q_cnt % C::kQS;
           if (!mbar_wait(b_q_full(qs), (q_cnt / C::kQS) & 1, wc, ATTN_DEVERR_WAIT_TIMEOUT_SITE(kSiteQFull))) {
             ok = false;
             break;
           }
           ++q_cnt;
-          int part, tok;
-          line.tile(w, i, part, tok);
 #pragma unroll
           for (int x = 0; x < 2; ++x) {
-            if (!line.active(w, x, tok)) continue;
+            if (!it.active(x)) continue;
             const int sb = s_cnt[x] & 1;
             if (!mbar_wait(b_s_free(x, sb), ((s_cnt[x] >> 1) & 1) ^ 1, wc, ATTN_DEVERR_WAIT_TIMEOUT_SITE(kSiteSFree))) {
               ok = false;
@@ -381,10 +449,12 @@ __global__ void __launch_bounds__(kThr, 1) weights_kernel(const __grid_constant_
     float* lse_s = reinterpret_cast<float*>(smem + C::kOffL) + (warp - 2) * 2 * NT;
     constexpr int NC = (NT + 31) / 32;
     int col_tok[NC], col_head[NC];
+    long long col_at[NC];
 #pragma unroll
     for (int k = 0; k < NC; ++k) {
       col_tok[k] = (lane + 32 * k) / p.heads;
       col_head[k] = lane + 32 * k - col_tok[k] * p.heads;
+      col_at[k] = static_cast<long long>(col_head[k]) * p.total + col_tok[k];
     }
     const float2 c2 = make_float2(p.scale_log2, p.scale_log2);
     uint32_t s_cnt = 0;
@@ -392,37 +462,38 @@ __global__ void __launch_bounds__(kThr, 1) weights_kernel(const __grid_constant_
     bool ok = true;
     for (bool more = line.next(w, true); more && ok; more = line.next(w, false)) {
       const int key = w.kb * kKeys + x * 128 + lrow;
-      float2 sum = make_float2(0.0f, 0.0f);
-      // this lane's lse columns of query tile i; +inf where the column is no
-      // query or its query saw no key
-      auto load_lse = [&](int i, float (&l)[NC]) {
-        int part, tok;
-        line.tile(w, i, part, tok);
-        const int n_heads = min(p.heads, p.group - part * p.heads);
-        const float* base = p.lse + static_cast<long long>(w.g * p.group + part * p.heads) * p.total + w.row_q + tok;
+      float2 sum[2] = {make_float2(0.0f, 0.0f), make_float2(0.0f, 0.0f)};
+      Tiles<CAUSAL> it(p, w, line);
+      // this lane's lse columns of the query tile at `f`, -inf where the column
+      // is no query; used a tile later, so that the loads are hidden
+      auto load_lse = [&](const Tiles<CAUSAL>& f, float (&l)[NC]) {
+        const int n_heads = min(p.heads, p.group - f.part * p.heads);
+        const float* base = p.lse + static_cast<long long>(w.g * p.group + f.part * p.heads) * p.total + w.row_q + f.tok;
 #pragma unroll
         for (int k = 0; k < NC; ++k) {
-          l[k] = INFINITY;
-          if (lane + 32 * k < NT && col_tok[k] < p.span && col_head[k] < n_heads && tok + col_tok[k] < w.q_len) {
-            const float v = __ldg(base + static_cast<long long>(col_head[k]) * p.total + col_tok[k]);
-            if (v != -INFINITY) l[k] = v * kLog2e;
-          }
+          l[k] = -INFINITY;
+          if (lane + 32 * k < NT && col_tok[k] < p.span && col_head[k] < n_heads && f.tok + col_tok[k] < w.q_len)
+            l[k] = __ldg(base + col_at[k]);
         }
       };
       float l_next[NC];
-      if (w.t0 < w.t1) load_lse(w.t0, l_next);
+      if (w.t0 < w.t1) load_lse(it, l_next);
+      const bool whole = w.t1 - w.t0 == w.n;
+      float* out = p.weights + (static_cast<long long>(w.b) * p.c.hkv + w.g) * p.len + key;
+      const bool mine = whole && key < w.k_len;
+      const float old = mine && p.decay != 0.0f ? *out : 0.0f;
       for (int i = w.t0; i < w.t1; ++i) {
-        int part, tok;
-        line.tile(w, i, part, tok);
         const int sb = s_cnt & 1;
-        const bool act = line.active(w, x, tok);
+        const bool act = it.active(x);
+        const int tok = it.tok, n_heads = min(p.heads, p.group - it.part * p.heads);
         float* ls = lse_s + sb * NT;   // its last readers are two tiles back
         if (act) {
 #pragma unroll
           for (int k = 0; k < NC; ++k)
-            if (lane + 32 * k < NT) ls[lane + 32 * k] = l_next[k];
+            if (lane + 32 * k < NT) ls[lane + 32 * k] = l_next[k] == -INFINITY ? INFINITY : l_next[k] * kLog2e;
         }
-        if (i + 1 < w.t1) load_lse(i + 1, l_next);
+        it.next();
+        if (i + 1 < w.t1) load_lse(it, l_next);
         if (!act) continue;
         __syncwarp();
         if (!mbar_wait_warp(b_s_full(x, sb), (s_cnt >> 1) & 1, wc, ATTN_DEVERR_WAIT_TIMEOUT_SITE(kSiteSFull))) {
@@ -432,50 +503,22 @@ __global__ void __launch_bounds__(kThr, 1) weights_kernel(const __grid_constant_
         ++s_cnt;
         tc_fence_after();
         // columns this key sees: from c_lo (causal), those that are queries
-        const int n_heads = min(p.heads, p.group - part * p.heads);
         int c_lo = 0;
         if (CAUSAL) c_lo = max(0, (key - (w.k_len - w.q_len) - tok)) * p.heads;
         const bool full = (!CAUSAL || w.kb * kKeys + x * 128 + 127 - (w.k_len - w.q_len) <= tok) &&
                           tok + p.span <= w.q_len && n_heads == p.heads && p.heads * p.span == NT;
-        constexpr int CB = NT < 32 ? NT : 32;   // columns per TMEM load
-#pragma unroll
-        for (int c0 = 0; c0 < NT; c0 += CB) {
-          uint32_t r[CB];
-          if constexpr (CB == 32) tmem_ld_32x32b_x32(t_s + sb * NT + c0, r);
-          else tmem_ld_32x32b_x16(t_s + sb * NT + c0, r);
-          tmem_wait_ld(r);
-          if (c0 + CB == NT) {
-            // the buffer is in registers: the next scores may overwrite it
-            tc_fence_before();
-            __syncwarp();
-            if (lane == 0) mbar_arrive(b_s_free(x, sb));
-          }
-#pragma unroll
-          for (int k = 0; k < CB; k += 4) {
-            const float4 l4 = *reinterpret_cast<const float4*>(ls + c0 + k);
-            const float2 a = ffma2(make_float2(__uint_as_float(r[k]), __uint_as_float(r[k + 1])), c2, make_float2(-l4.x, -l4.y));
-            const float2 b = ffma2(make_float2(__uint_as_float(r[k + 2]), __uint_as_float(r[k + 3])), c2, make_float2(-l4.z, -l4.w));
-            float2 e0 = make_float2(ex2_approx(a.x), ex2_approx(a.y));
-            float2 e1 = make_float2(ex2_approx(b.x), ex2_approx(b.y));
-            if (!full) {
-              // dropped by index and by lse = +inf, whatever the score
-              if (c0 + k < c_lo || l4.x == INFINITY) e0.x = 0.0f;
-              if (c0 + k + 1 < c_lo || l4.y == INFINITY) e0.y = 0.0f;
-              if (c0 + k + 2 < c_lo || l4.z == INFINITY) e1.x = 0.0f;
-              if (c0 + k + 3 < c_lo || l4.w == INFINITY) e1.y = 0.0f;
-            }
-            sum = fadd2(sum, fadd2(e0, e1));
-          }
-        }
+        auto release = [&] {   // the scores are in registers: the buffer may be overwritten
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(b_s_free(x, sb));
+        };
+        if (full) add_tile<NT, false>(t_s + sb * NT, ls, c2, c_lo, sum, release);
+        else add_tile<NT, true>(t_s + sb * NT, ls, c2, c_lo, sum, release);
       }
       if (!ok) break;
-      const bool whole = w.t1 - w.t0 == w.n;
-      const float s = sum.x + sum.y;
+      const float s = (sum[0].x + sum[0].y) + (sum[1].x + sum[1].y);
       if (whole) {
-        if (key < w.k_len) {
-          float* out = p.weights + (static_cast<long long>(w.b) * p.c.hkv + w.g) * p.len + key;
-          *out = (p.decay != 0.0f ? p.decay * *out : 0.0f) + s;
-        }
+        if (mine) *out = p.decay * old + s;
       } else {
         p.part[(2 * blockIdx.x + (w.t0 == 0 ? 1 : 0)) * kKeys + x * 128 + lrow] = s;
         if (w.t0 == 0 && warp == 2 && lane == 0)
