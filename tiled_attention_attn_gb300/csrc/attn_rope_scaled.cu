@@ -11,10 +11,14 @@
 // position.  An fp32 product t * f_p would be off by t f_p 2^-24 radians,
 // 2^-7 at position 131072.
 //
-// Bound by HBM: x read once, y written once.  A block takes a few rows
-// (tokens): it first forms the rows' (cos, sin) tables in shared memory, once
-// for all heads, and their places in the cache, then moves 16-byte words (two
-// per thread and item: the 8 pairs' members), several items in flight.
+// Bound by HBM: x read once, y written once.  A warp takes a row (token), or
+// with few rows a part of its heads: it finds the token's place, forms the
+// pairs' (cos, sin) once for all heads in its part of shared memory, and moves
+// 16-byte words, four loads in flight per lane.  No block-wide barrier: the
+// other 31 warps of the SM (registers held to 64) hide each one's start.  Twice
+// the loads in flight at half the warps ran slower: 16,384 rows of 32 heads of
+// 128, half of each rotated, 45.2 us (5.9 TB/s) against 52.8; smaller batches
+// at more warps too (51.7).
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 #include <cuda_runtime.h>
@@ -29,7 +33,7 @@ namespace attn {
 namespace {
 
 constexpr int kThreads = 256;
-constexpr int kMaxRows = 8;      // rows per block
+constexpr int kWarps = kThreads / 32;
 constexpr int kMaxPairs = 256;   // rot_dim <= 512
 
 // One tensor of the call.  Rows of `heads` heads; dst is contiguous (place 0)
@@ -39,15 +43,15 @@ struct Seg {
   uint16_t* dst;
   long long src_token, src_head;
   int heads, place, rotate;
-  int per;    // items per head
-  int items;  // heads * per
+  int per;             // items per head
+  unsigned int magic;  // ceil(2^32 / per): x / per = umulhi(x, magic) for the small x it is used on
 };
 
 struct RopeParams {
   Seg seg[3];
-  int n_seg, items;             // items per row, all segments
-  unsigned long long rows;
-  int rows_per_block, d, rot, gptj, in_place;
+  int n_seg;
+  int rows, parts;              // warps per row
+  int d, rot, in_place;
   float amplitude, sin_sign;    // sin_sign: -1 for the gradient
   const int* cu;                // packed rows, or null: rows of L per sequence
   int L, B, total;
@@ -128,117 +132,119 @@ __device__ __forceinline__ void locate(const RopeParams& p, long long row, int& 
   }
 }
 
-// VEC: items are 8 pairs (two 16-byte words) or 8 copied features; else one
+// Items of a head.  VEC: 8 pairs in two 16-byte words (GPT-NeoX: features 8e ..
+// and half + 8e ..), 4 pairs in one (GPT-J), or 8 copied features; else one
 // pair or one feature.
-template <bool BF16, bool VEC>
-__global__ void __launch_bounds__(kThreads) rope_kernel(const __grid_constant__ RopeParams p) {
-  extern __shared__ float2 cs[];   // [row][pair] (A cos, A sin)
-  __shared__ int s_pos[kMaxRows];
-  __shared__ long long s_at[kMaxRows];
-  const int tid = threadIdx.x;
-  const long long row0 = static_cast<long long>(blockIdx.x) * p.rows_per_block;
-  const int nr = static_cast<int>(min(static_cast<long long>(p.rows_per_block), static_cast<long long>(p.rows) - row0));
-  if (tid < nr) locate(p, row0 + tid, s_pos[tid], s_at[tid]);
+template <bool BF16, bool GPTJ, bool VEC>
+__global__ void __launch_bounds__(kThreads, 4) rope_kernel(const __grid_constant__ RopeParams p) {
+  // (A cos, A sin) of the row's pairs, per warp.  VEC: word i of item e (two
+  // pairs) at [i][e], so that neighbouring items are neighbouring words
+  extern __shared__ float4 tables[];
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int half = p.rot >> 1;
+  constexpr int PI = !VEC ? 1 : GPTJ ? 4 : 8;   // pairs per item
+  constexpr int W = VEC ? 8 : 1;                // features per word
+  constexpr bool kTwo = !GPTJ || !VEC;          // the pair's members are apart
+  constexpr int U = !VEC ? 2 : GPTJ ? 4 : 2;    // items in flight
+  const int groups = half / PI;
+  float2* cs = reinterpret_cast<float2*>(tables) + warp * half;
+  const float4* cs4 = reinterpret_cast<const float4*>(cs);
   if (p.append && blockIdx.x == 0) {
     // offsets that no row lookup meets
     int first;
-    for (int b = tid; b < p.B; b += kThreads) chunk_len(p.cu, b, p.total, first, p.err);
+    for (int b = threadIdx.x; b < p.B; b += kThreads) chunk_len(p.cu, b, p.total, first, p.err);
   }
-  __syncthreads();
-  const int half = p.rot >> 1;
-  for (int e = tid; e < nr * half; e += kThreads) {
-    const int r = e / half, i = e - r * half;
-    const unsigned long long turn = p.turns[i] * static_cast<unsigned long long>(static_cast<long long>(s_pos[r]));
-    float sn, c;
-    sincospif(static_cast<float>(static_cast<int>(turn >> 32)) * 4.656612873077393e-10f, &sn, &c);   // 2^-31
-    cs[e] = make_float2(c * p.amplitude, sn * p.amplitude * p.sin_sign);
-  }
-  __syncthreads();
-
-  const int n = nr * p.items;
-  constexpr int U = VEC ? 4 : 1;   // items in flight per thread
-  const int groups = VEC ? half / 8 : half;
-  for (int base = tid; base < n; base += kThreads * U) {
-    uint4 va[U], vb[U];
-    float sa[U], sb[U];
-    const uint16_t* src[U];
-    uint16_t* dst[U];
-    int row[U], g[U], oa[U], ob[U];   // g: pair group, or -1: copied
-#pragma unroll
-    for (int u = 0; u < U; ++u) {
-      const int it = base + u * kThreads;
-      src[u] = nullptr;
-      if (it >= n) continue;
-      const int r = it / p.items;
-      int rem = it - r * p.items;
-      const long long at = s_at[r];
-      if (at < 0) continue;
-      int k = 0;
-      while (k + 1 < p.n_seg && rem >= p.seg[k].items) rem -= p.seg[k++].items;
-      const Seg& s = p.seg[k];
-      const int h = rem / s.per, e = rem - h * s.per;
-      row[u] = r;
-      src[u] = s.src + (row0 + r) * s.src_token + h * s.src_head;
-      dst[u] = s.place == 0 ? s.dst + ((row0 + r) * s.heads + h) * p.d : s.dst + at + h * p.cache.s_head;
-      g[u] = (s.rotate && e < groups) ? e : -1;
-      if constexpr (VEC) {
-        if (g[u] >= 0) {
-          // GPT-NeoX pairs (8g + e, half + 8g + e); GPT-J pairs (16g + 2e, 16g + 2e + 1)
-          oa[u] = p.gptj ? 16 * e : 8 * e;
-          ob[u] = p.gptj ? 16 * e + 8 : half + 8 * e;
-          vb[u] = *reinterpret_cast<const uint4*>(src[u] + ob[u]);
-        } else {
-          oa[u] = s.rotate ? p.rot + 8 * (e - groups) : 8 * e;
-        }
-        va[u] = *reinterpret_cast<const uint4*>(src[u] + oa[u]);
-      } else {
-        if (g[u] >= 0) {
-          oa[u] = p.gptj ? 2 * e : e;
-          ob[u] = p.gptj ? 2 * e + 1 : half + e;
-          sb[u] = ld1<BF16>(src[u] + ob[u]);
-        } else {
-          oa[u] = s.rotate ? p.rot + (e - groups) : e;
-        }
-        sa[u] = ld1<BF16>(src[u] + oa[u]);
-      }
+  const long long tasks = static_cast<long long>(p.rows) * p.parts;
+  for (long long task = static_cast<long long>(blockIdx.x) * kWarps + warp; task < tasks;
+       task += static_cast<long long>(gridDim.x) * kWarps) {
+    const int row = static_cast<int>(task / p.parts), part = static_cast<int>(task - static_cast<long long>(row) * p.parts);
+    int pos;
+    long long at;
+    locate(p, row, pos, at);
+    if (at < 0) continue;
+    __syncwarp();   // the table's readers of the row before
+    for (int i = lane; i < half; i += 32) {
+      const unsigned long long turn = p.turns[i] * static_cast<unsigned long long>(static_cast<long long>(pos));
+      float sn, c;
+      sincospif(static_cast<float>(static_cast<int>(turn >> 32)) * 4.656612873077393e-10f, &sn, &c);   // 2^-31
+      const int to = VEC ? (((i % PI) >> 1) * groups + i / PI) * 2 + (i & 1) : i;
+      cs[to] = make_float2(c * p.amplitude, sn * p.amplitude * p.sin_sign);
     }
+    __syncwarp();
+    for (int k = 0; k < p.n_seg; ++k) {
+      const Seg& s = p.seg[k];
+      const uint16_t* src = s.src + row * s.src_token;
+      uint16_t* dst = s.place == 0 ? s.dst + static_cast<long long>(row) * s.heads * p.d : s.dst + at;
+      const long long dst_head = s.place == 0 ? p.d : p.cache.s_head;
+      const int turned = s.rotate ? groups : 0;   // items below this are rotated
+      const int first = s.rotate ? p.rot : 0;     // first copied feature
+      const int stride = 32 * p.parts, start = lane + 32 * part;
+      const int dh = s.per == 1 ? stride : __umulhi(stride, s.magic), de = stride - dh * s.per;
+      int h = s.per == 1 ? start : __umulhi(start, s.magic), e = start - h * s.per;
+      while (h < s.heads) {
+        uint4 va[U], vb[U];
+        float sa[U], sb[U];
+        int hh[U], ee[U];
 #pragma unroll
-    for (int u = 0; u < U; ++u) {
-      if (src[u] == nullptr) continue;
-      if constexpr (VEC) {
-        if (g[u] < 0) {
-          *reinterpret_cast<uint4*>(dst[u] + oa[u]) = va[u];
-          continue;
-        }
-        const float2* t = cs + row[u] * half + 8 * g[u];
-        uint32_t a[4] = {va[u].x, va[u].y, va[u].z, va[u].w}, b[4] = {vb[u].x, vb[u].y, vb[u].z, vb[u].w};
-        if (p.gptj) {
-#pragma unroll
-          for (int e = 0; e < 4; ++e) {
-            const float2 x = unpack<BF16>(a[e]), y = unpack<BF16>(b[e]);
-            const float2 ta = t[e], tb = t[4 + e];
-            a[e] = pack<BF16>(x.x * ta.x - x.y * ta.y, x.x * ta.y + x.y * ta.x);
-            b[e] = pack<BF16>(y.x * tb.x - y.y * tb.y, y.x * tb.y + y.y * tb.x);
+        for (int u = 0; u < U; ++u) {
+          hh[u] = h;
+          ee[u] = e;
+          if (h < s.heads) {
+            const bool t = e < turned;
+            const uint16_t* x = src + h * s.src_head + (t ? (GPTJ ? 2 * PI * e : PI * e) : first + W * (e - turned));
+            if constexpr (VEC) {
+              va[u] = *reinterpret_cast<const uint4*>(x);
+              if (kTwo && t) vb[u] = *reinterpret_cast<const uint4*>(x + half);
+            } else {
+              sa[u] = ld1<BF16>(x);
+              if (t) sb[u] = ld1<BF16>(x + (GPTJ ? 1 : half));
+            }
           }
-        } else {
-#pragma unroll
-          for (int e = 0; e < 4; ++e) {
-            const float2 x = unpack<BF16>(a[e]), y = unpack<BF16>(b[e]);
-            const float2 t0 = t[2 * e], t1 = t[2 * e + 1];
-            a[e] = pack<BF16>(x.x * t0.x - y.x * t0.y, x.y * t1.x - y.y * t1.y);
-            b[e] = pack<BF16>(x.x * t0.y + y.x * t0.x, x.y * t1.y + y.y * t1.x);
+          h += dh;
+          e += de;
+          if (e >= s.per) {
+            e -= s.per;
+            ++h;
           }
         }
-        *reinterpret_cast<uint4*>(dst[u] + oa[u]) = make_uint4(a[0], a[1], a[2], a[3]);
-        *reinterpret_cast<uint4*>(dst[u] + ob[u]) = make_uint4(b[0], b[1], b[2], b[3]);
-      } else {
-        if (g[u] < 0) {
-          st1<BF16>(dst[u] + oa[u], sa[u]);
-          continue;
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+          if (hh[u] >= s.heads) continue;
+          const int g = ee[u];
+          const bool t = g < turned;
+          uint16_t* y = dst + hh[u] * dst_head + (t ? (GPTJ ? 2 * PI * g : PI * g) : first + W * (g - turned));
+          if constexpr (VEC) {
+            uint32_t a[4] = {va[u].x, va[u].y, va[u].z, va[u].w};
+            if (t) {
+              if constexpr (GPTJ) {
+#pragma unroll
+                for (int i = 0; i < 2; ++i) {
+                  const float4 c = cs4[i * groups + g];
+                  const float2 x = unpack<BF16>(a[2 * i]), z = unpack<BF16>(a[2 * i + 1]);
+                  a[2 * i] = pack<BF16>(x.x * c.x - x.y * c.y, x.x * c.y + x.y * c.x);
+                  a[2 * i + 1] = pack<BF16>(z.x * c.z - z.y * c.w, z.x * c.w + z.y * c.z);
+                }
+              } else {
+                uint32_t b[4] = {vb[u].x, vb[u].y, vb[u].z, vb[u].w};
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                  const float4 c = cs4[i * groups + g];
+                  const float2 x = unpack<BF16>(a[i]), z = unpack<BF16>(b[i]);
+                  a[i] = pack<BF16>(x.x * c.x - z.x * c.y, x.y * c.z - z.y * c.w);
+                  b[i] = pack<BF16>(x.x * c.y + z.x * c.x, x.y * c.w + z.y * c.z);
+                }
+                *reinterpret_cast<uint4*>(y + half) = make_uint4(b[0], b[1], b[2], b[3]);
+              }
+            }
+            *reinterpret_cast<uint4*>(y) = make_uint4(a[0], a[1], a[2], a[3]);
+          } else if (t) {
+            const float2 c = cs[g];
+            st1<BF16>(y, sa[u] * c.x - sb[u] * c.y);
+            st1<BF16>(y + (GPTJ ? 1 : half), sa[u] * c.y + sb[u] * c.x);
+          } else {
+            st1<BF16>(y, sa[u]);
+          }
         }
-        const float2 t = cs[row[u] * half + g[u]];
-        st1<BF16>(dst[u] + oa[u], sa[u] * t.x - sb[u] * t.y);
-        st1<BF16>(dst[u] + ob[u], sa[u] * t.y + sb[u] * t.x);
       }
     }
   }
@@ -255,41 +261,41 @@ int fill_turns(RopeParams& p, int rot_dim, int d, const double* freqs, float amp
     p.turns[i] = f >= 1.0 ? 0ull : static_cast<unsigned long long>(f * 18446744073709551616.0);
   }
   p.rot = rot_dim;
-  p.gptj = interleaved;
   p.amplitude = amplitude;
   return ATTN_OK;
 }
 
-int launch(RopeParams& p, bool vec, bool bf16, cudaStream_t stream) {
+template <bool BF16, bool GPTJ>
+void run(const RopeParams& p, bool vec, int grid, size_t smem, cudaStream_t stream) {
+  if (vec) rope_kernel<BF16, GPTJ, true><<<grid, kThreads, smem, stream>>>(p);
+  else rope_kernel<BF16, GPTJ, false><<<grid, kThreads, smem, stream>>>(p);
+}
+
+int launch(RopeParams& p, bool vec, bool bf16, bool gptj, cudaStream_t stream) {
   int dev = 0;
   if (cudaGetDevice(&dev) != cudaSuccess) return ATTN_ELAUNCH;
   DeviceInfo info;
   if (int rc = device_info(dev, info)) return rc;
   if (!info.supported) return ATTN_EUNSUPPORTED;
   p.err = info.err_word;
-  p.items = 0;
-  const int group = vec ? 8 : 1;
+  const int pairs = !vec ? 1 : gptj ? 4 : 8, feats = vec ? 8 : 1;
+  int items = 0;
   for (int k = 0; k < p.n_seg; ++k) {
     Seg& s = p.seg[k];
     // in place the features past rot_dim stay where they are
-    s.per = s.rotate ? p.rot / 2 / group + (p.in_place && s.place == 0 ? 0 : (p.d - p.rot) / group) : p.d / group;
-    s.items = s.heads * s.per;
-    p.items += s.items;
+    s.per = s.rotate ? p.rot / 2 / pairs + (p.in_place && s.place == 0 ? 0 : (p.d - p.rot) / feats) : p.d / feats;
+    s.magic = static_cast<unsigned int>((0x100000000ull + s.per - 1) / s.per);
+    items = std::max(items, s.heads * s.per);
   }
-  // few rows: one per block, so that every SM takes part; many: up to 8
-  p.rows_per_block = static_cast<int>(
-      std::min<unsigned long long>(kMaxRows, std::max<unsigned long long>(1, p.rows / (4ull * info.sm_count))));
-  const unsigned long long grid = (p.rows + p.rows_per_block - 1) / p.rows_per_block;
-  if (grid > 0x7fffffffull) return ATTN_EINVAL;
-  const size_t smem = static_cast<size_t>(p.rows_per_block) * (p.rot / 2) * sizeof(float2);
-  const int g = static_cast<int>(grid);
-  if (vec) {
-    if (bf16) rope_kernel<true, true><<<g, kThreads, smem, stream>>>(p);
-    else rope_kernel<false, true><<<g, kThreads, smem, stream>>>(p);
-  } else {
-    if (bf16) rope_kernel<true, false><<<g, kThreads, smem, stream>>>(p);
-    else rope_kernel<false, false><<<g, kThreads, smem, stream>>>(p);
-  }
+  // a warp per row once the rows fill the GPU's warps; below that a row's
+  // items are shared by up to 8 warps, of at least one item a lane
+  const long long slots = 16LL * kWarps * info.sm_count / 4;
+  p.parts = static_cast<int>(std::max<long long>(1, std::min<long long>({8, slots / std::max(p.rows, 1), (items + 31) / 32})));
+  const long long tasks = static_cast<long long>(p.rows) * p.parts;
+  const int grid = static_cast<int>(std::min<long long>((tasks + kWarps - 1) / kWarps, 4LL * info.sm_count));
+  const size_t smem = static_cast<size_t>(kWarps) * (p.rot / 2) * sizeof(float2);
+  if (bf16) gptj ? run<true, true>(p, vec, grid, smem, stream) : run<true, false>(p, vec, grid, smem, stream);
+  else gptj ? run<false, true>(p, vec, grid, smem, stream) : run<false, false>(p, vec, grid, smem, stream);
   if (cudaGetLastError() != cudaSuccess) return ATTN_ELAUNCH;
   count_launch();
   return ATTN_OK;
@@ -327,14 +333,15 @@ int attn_rotary_scaled(const void* x, void* y, int B, int L, int H, int d, int r
   p = RopeParams{};
   p.d = d;
   if (int rc = fill_turns(p, rot_dim, d, freqs, amplitude, interleaved)) return rc;
-  p.rows = packed ? static_cast<unsigned long long>(total) : static_cast<unsigned long long>(B) * L;
-  if (p.rows > 0x7fffffffull || p.rows * H > (1ull << 40) / d) return ATTN_EINVAL;
-  if (static_cast<long long>(H) * d > (1 << 26)) return ATTN_EINVAL;   // a block's items are 32-bit
+  const unsigned long long rows = packed ? static_cast<unsigned long long>(total) : static_cast<unsigned long long>(B) * L;
+  if (rows > 0x7fffffffull || rows * H > (1ull << 40) / d) return ATTN_EINVAL;
+  if (static_cast<long long>(H) * d > (1 << 26)) return ATTN_EINVAL;   // a row's items are 32-bit
+  p.rows = static_cast<int>(rows);
   const bool same = x == y;
   if (same && (x_stride_head != d || x_stride_token != static_cast<long long>(H) * d)) return ATTN_EINVAL;
-  if (!same && overlap(x, extent(p.rows, x_stride_token, H, x_stride_head, d), y, p.rows * H * d * 2))
+  if (!same && overlap(x, extent(rows, x_stride_token, H, x_stride_head, d), y, rows * H * d * 2))
     return ATTN_EINVAL;
-  if (p.rows == 0) return ATTN_OK;
+  if (rows == 0) return ATTN_OK;
   p.in_place = same;
   p.sin_sign = inverse ? -1.0f : 1.0f;
   p.cu = cu_seqlens_or_null;
@@ -347,7 +354,7 @@ int attn_rotary_scaled(const void* x, void* y, int B, int L, int H, int d, int r
   p.seg[0] = Seg{static_cast<const uint16_t*>(x), static_cast<uint16_t*>(y), x_stride_token, x_stride_head, H, 0, 1, 0, 0};
   const bool vec = rot_dim % 16 == 0 && d % 8 == 0 && x_stride_token % 8 == 0 && x_stride_head % 8 == 0 &&
                    ptr_aligned(x, 16) && ptr_aligned(y, 16);
-  return launch(p, vec, fp16 == 0, stream);
+  return launch(p, vec, fp16 == 0, interleaved != 0, stream);
 }
 
 int attn_cache_append(const void* q, const void* k, const void* v, void* q_out, long long q_stride_token,
@@ -396,7 +403,7 @@ int attn_cache_append(const void* q, const void* k, const void* v, void* q_out, 
   p.total = total;
   p.positions = positions_or_null;
   p.append = 1;
-  return launch(p, !freqs_or_null || rot_dim % 16 == 0, cache->fp16 == 0, stream);
+  return launch(p, !freqs_or_null || rot_dim % 16 == 0, cache->fp16 == 0, freqs_or_null && interleaved != 0, stream);
 }
 
 }  // extern "C"
