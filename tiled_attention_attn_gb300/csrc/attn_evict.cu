@@ -3,33 +3,41 @@
 // and the heaviest of the others are kept, in order, and their rows moved to
 // the front.
 //
-// Selection (evict_select_kernel, one block per sequence and head): the
+// Selection (evict_select_kernel, one cluster per sequence and head): the
 // weights' bit patterns are mapped to unsigned integers of the same order, and
-// the k-th largest is found digit by digit (8 bits, most significant first): a
-// histogram of the digit over the keys that match the digits so far, then the
-// digit whose count from above passes k.  Keys above it are kept, and the
-// first of those equal to it, so that exactly k are; a prefix sum over the
-// keys in order gives each kept key its place.
+// the k-th largest is found digit by digit (11, 11 and 10 bits, most
+// significant first): a histogram of the digit over the keys that match the
+// digits so far, then the digit whose count from above passes k.  Keys above
+// it are kept, and the first of those equal to it, so that exactly k are;
+// counts of the warps before (and of the CTAs before, over distributed shared
+// memory) give each kept key its place in order.  The weights are read from
+// HBM once and stay in shared memory.
 //
-// Moving (evict_move_kernel): row s of the kept keys goes from key kept[s] >= s
-// to key s.  A block owns a 64-byte column of the rows of one (sequence, head,
-// K or V) and walks the rows in order, a batch at a time, every load of a batch
-// before its stores: a store to key s can only meet loads of keys kept[s'] = s
-// with s' <= s, which came in the same batch or an earlier one, so rows may
-// move in place.  Bound by HBM: each kept row read and written once.
+// Moving (evict_move_kernel): row s of the kept keys goes from key kept[s] to
+// key s.  Into other pages, blocks take rows in any order.  In place (some page
+// is written where it lies) a block owns a 32-byte column of the rows of one
+// (sequence, head, K or V) and walks the rows in order, a batch at a time,
+// every load of a batch before its stores: kept[s] >= s, so a store to key s
+// can only meet loads of keys kept[s'] = s with s' <= s, which came in the same
+// batch or an earlier one.  Bound by HBM: each kept row read and written once.
 #include <cuda_runtime.h>
 
 #include <algorithm>
 #include <cstdint>
 
 #include "attn_paged.h"
+#include "ptx.cuh"
 
 namespace attn {
 namespace {
 
 constexpr int kSelThreads = 1024;
+constexpr int kSelWarps = kSelThreads / 32;
+constexpr int kBins = 2048;            // 11-bit digits
+constexpr int kMaxKeys = 48 * 1024;    // weights that a CTA keeps in shared memory; more are read again
 constexpr int kMoveThreads = 256;
-constexpr int kMoveRows = 4;   // rows in flight per thread
+constexpr int kMoveRows = 4;           // rows in flight per thread, in any order
+constexpr int kWalkRows = 8;           // and in place
 
 struct EvictParams {
   const float* weights;
@@ -40,6 +48,7 @@ struct EvictParams {
   const int* dst_table;
   int dst_stride, dst_max_pages;
   int weights_len, weights_out_len, budget, recent, d;
+  int key_slots;        // weights per CTA that shared memory holds
   int* err;
 };
 
@@ -85,111 +94,245 @@ __device__ __forceinline__ int block_scan(int x, int* warp_sums, int* sum) {
   return x;
 }
 
+__device__ __forceinline__ int ld_dsmem_s32(uint32_t a) {
+  int v;
+  asm volatile("ld.shared::cluster.s32 %0, [%1];" : "=r"(v) : "r"(a) : "memory");
+  return v;
+}
+
+// Grid (CTAs of a cluster, heads, sequences).  Every CTA of a cluster takes the
+// same path, so all reach each cluster barrier.
 __global__ void __launch_bounds__(kSelThreads) evict_select_kernel(const __grid_constant__ EvictParams p) {
-  __shared__ int hist[256];
+  extern __shared__ uint32_t keys[];
+  __shared__ int hist[kBins];
   __shared__ int warp_sums[32];
+  __shared__ int n_gt[kSelWarps + 1], n_eq[kSelWarps + 1];   // per warp; last: the CTA's
   __shared__ uint32_t s_prefix;
   __shared__ int s_need;
-  const int g = blockIdx.x, b = blockIdx.y, tid = threadIdx.x;
+  const int CS = gridDim.x, rank = blockIdx.x;
+  const int g = blockIdx.y, b = blockIdx.z, tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  grid_launch_dependents();
   const int n = evict_len(p, b), m = min(n, p.budget);
   const long long row = static_cast<long long>(b) * p.c.hkv + g;
   const float* w = p.weights + row * p.weights_len;
   int* kept = p.kept + row * p.budget;
-  if (g == 0 && tid == 0) p.seqlens_out[b] = m;
-  for (int s = m + tid; s < p.budget; s += kSelThreads) kept[s] = -1;
+  if (g == 0 && rank == 0 && tid == 0) p.seqlens_out[b] = m;
+  const int t0 = rank * kSelThreads + tid, step = CS * kSelThreads;
+  for (int s = m + t0; s < p.budget; s += step) kept[s] = -1;
   if (n <= p.budget) {
-    for (int s = tid; s < n; s += kSelThreads) kept[s] = s;
+    for (int s = t0; s < n; s += step) kept[s] = s;
     return;
   }
   const int cand = n - p.recent;       // keys that compete
   const int k = p.budget - p.recent;   // of which this many stay
-  for (int s = tid; s < p.recent; s += kSelThreads) kept[k + s] = cand + s;
+  for (int s = t0; s < p.recent; s += step) kept[k + s] = cand + s;
   if (k == 0) return;
-  uint32_t prefix = 0;
+  // this CTA's keys [lo, hi)
+  const int per = ((cand + CS - 1) / CS + 31) & ~31;
+  const int lo = min(rank * per, cand), hi = min(lo + per, cand);
+  const bool held = per <= p.key_slots;
+  if (held) {
+    for (int j = lo + tid; j < hi; j += kSelThreads) keys[j - lo] = order_key(__ldg(w + j));
+  }
+  auto key_at = [&](int j) { return held ? keys[j - lo] : order_key(__ldg(w + j)); };
+  uint32_t prefix = 0, mask = 0;
   int need = k;   // still to take among the keys that match the prefix
-  for (int shift = 24; shift >= 0; shift -= 8) {
-    if (tid < 256) hist[tid] = 0;
+#pragma unroll 1
+  for (int shift = 21;; shift = shift == 21 ? 10 : 0) {
+    const uint32_t digit = shift == 0 ? 0x3ffu : 0x7ffu;
+    for (int i = tid; i < kBins; i += kSelThreads) hist[i] = 0;
     __syncthreads();
-    const uint32_t mask = shift == 24 ? 0u : 0xffffffffu << (shift + 8);
-    for (int j = tid; j < cand; j += kSelThreads) {
-      const uint32_t u = order_key(__ldg(w + j));
-      if ((u & mask) == prefix) atomicAdd(&hist[(u >> shift) & 255], 1);
+    for (int j = lo + tid; j < hi; j += kSelThreads) {
+      const uint32_t u = key_at(j);
+      if ((u & mask) == prefix) atomicAdd(&hist[(u >> shift) & digit], 1);
     }
     __syncthreads();
+    // bins from the largest digit down, two a thread, over the whole cluster
+    const int d1 = kBins - 1 - 2 * tid;
+    int c1 = hist[d1], c0 = hist[d1 - 1];
+    if (CS > 1) {
+      cluster_sync();
+      c1 = c0 = 0;
+      const uint32_t a = smem_u32(&hist[d1 - 1]);
+      for (int r = 0; r < CS; ++r) {
+        const uint32_t x = mapa_shared(a, r);
+        c0 += ld_dsmem_s32(x);
+        c1 += ld_dsmem_s32(x + 4);
+      }
+      cluster_sync();   // the peers' counts have been read
+    }
     int sum;
-    const int c = tid < 256 ? hist[255 - tid] : 0;   // from the largest digit down
-    const int above = block_scan(c, warp_sums, &sum);
-    if (tid < 256 && above >= need && above - c < need) {
-      s_prefix = prefix | static_cast<uint32_t>(255 - tid) << shift;
-      s_need = need - (above - c);
+    const int above = block_scan(c0 + c1, warp_sums, &sum);
+    if (above >= need && above - (c0 + c1) < need) {
+      const int before = above - (c0 + c1);
+      const bool first = before + c1 >= need;
+      s_prefix = prefix | static_cast<uint32_t>(first ? d1 : d1 - 1) << shift;
+      s_need = need - (first ? before : before + c1);
     }
     __syncthreads();
     prefix = s_prefix;
     need = s_need;
+    mask |= digit << shift;
     __syncthreads();
+    if (shift == 0) break;
   }
-  // keys above the threshold, and the first `need` of those equal to it
-  int above0 = 0, equal0 = 0;
-  for (int j0 = 0; j0 < cand; j0 += kSelThreads) {
-    const int j = j0 + tid;
-    const uint32_t u = j < cand ? order_key(__ldg(w + j)) : 0u;
-    const int gt = j < cand && u > prefix, eq = j < cand && u == prefix;
-    int n_gt, n_eq;
-    const int a = above0 + block_scan(gt, warp_sums, &n_gt);
-    const int e = equal0 + block_scan(eq, warp_sums, &n_eq);
-    // a, e: keys above / equal up to and with this one
-    if (gt || (eq && e <= need)) kept[a + min(e, need) - 1] = j;
-    above0 += n_gt;
-    equal0 += n_eq;
+  // keys above the threshold, and the first `need` of those equal to it: counts
+  // of each warp's run of keys, then their places
+  const int run = ((per + kSelWarps - 1) / kSelWarps + 31) & ~31;
+  const int r0 = min(lo + warp * run, hi), r1 = min(r0 + run, hi);
+  int gt = 0, eq = 0;
+  for (int j = r0; j < r1; j += 32) {
+    const bool in = j + lane < r1;
+    const uint32_t u = in ? key_at(j + lane) : 0u;
+    gt += __popc(__ballot_sync(0xffffffffu, in && u > prefix));
+    eq += __popc(__ballot_sync(0xffffffffu, in && u == prefix));
+  }
+  if (lane == 0) {
+    n_gt[warp] = gt;
+    n_eq[warp] = eq;
+  }
+  __syncthreads();
+  if (warp == 0) {   // exclusive sums over the warps
+    int a = n_gt[lane], e = n_eq[lane];
+    const int a0 = a, e0 = e;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int x = __shfl_up_sync(0xffffffffu, a, o), y = __shfl_up_sync(0xffffffffu, e, o);
+      if (lane >= o) {
+        a += x;
+        e += y;
+      }
+    }
+    n_gt[lane] = a - a0;
+    n_eq[lane] = e - e0;
+    if (lane == 31) {
+      n_gt[kSelWarps] = a;
+      n_eq[kSelWarps] = e;
+    }
+  }
+  __syncthreads();
+  gt = n_gt[warp];
+  eq = n_eq[warp];
+  if (CS > 1) {
+    cluster_sync();
+    for (int r = 0; r < rank; ++r) {
+      gt += ld_dsmem_s32(mapa_shared(smem_u32(&n_gt[kSelWarps]), r));
+      eq += ld_dsmem_s32(mapa_shared(smem_u32(&n_eq[kSelWarps]), r));
+    }
+    cluster_sync();   // no CTA leaves before its counts have been read
+  }
+  const uint32_t below = (1u << lane) - 1u;
+  for (int j = r0; j < r1; j += 32) {
+    const bool in = j + lane < r1;
+    const uint32_t u = in ? key_at(j + lane) : 0u;
+    const bool is_gt = in && u > prefix, is_eq = in && u == prefix;
+    const uint32_t bg = __ballot_sync(0xffffffffu, is_gt), be = __ballot_sync(0xffffffffu, is_eq);
+    const int e = eq + __popc(be & below);   // equal keys before this one
+    if (is_gt || (is_eq && e < need)) kept[gt + __popc(bg & below) + min(e, need)] = j + lane;
+    gt += __popc(bg);
+    eq += __popc(be);
   }
 }
 
+// Grid (blocks, heads, sequences); the last block of x moves the weights.
 __global__ void __launch_bounds__(kMoveThreads) evict_move_kernel(const __grid_constant__ EvictParams p) {
-  const int n_col = p.d / 32;   // 64-byte columns
+  const int blocks = gridDim.x - 1;
   const int g = blockIdx.y, b = blockIdx.z, tid = threadIdx.x;
   const int n = evict_len(p, b), m = min(n, p.budget);
   const long long row = static_cast<long long>(b) * p.c.hkv + g;
   const int* kept = p.kept + row * p.budget;
-  if (static_cast<int>(blockIdx.x) == 2 * n_col) {
+  const int lg = p.c.page_log2, pm = (1 << lg) - 1;
+  const int* src_row = p.c.table + static_cast<long long>(b) * p.c.table_stride;
+  const int* dst_row = p.dst_table + static_cast<long long>(b) * p.dst_stride;
+  // whether any page is written where it lies
+  bool lies = src_row == dst_row;
+  if (!lies) {
+    bool same = false;
+    for (int i = tid; i < min((m + pm) >> lg, p.dst_max_pages); i += kMoveThreads) same |= src_row[i] == dst_row[i];
+    lies = __syncthreads_or(same);
+  }
+  grid_wait_prerequisites();   // `kept` is written
+  if (static_cast<int>(blockIdx.x) == blocks) {
     // the weights themselves, in the same order
     const float* w = p.weights + row * p.weights_len;
     float* out = p.weights_out + row * p.weights_out_len;
-    for (int s0 = 0; s0 < m; s0 += kMoveThreads) {
-      const int s = s0 + tid;
-      const float x = s < m ? w[__ldg(kept + s)] : 0.0f;
+    for (int s0 = 0; s0 < m; s0 += kMoveThreads * kWalkRows) {
+      float x[kWalkRows];
+#pragma unroll
+      for (int u = 0; u < kWalkRows; ++u) {
+        const int s = s0 + u * kMoveThreads + tid;
+        x[u] = s < m ? w[__ldcg(kept + s)] : 0.0f;
+      }
       __syncthreads();
-      if (s < m) out[s] = x;
+#pragma unroll
+      for (int u = 0; u < kWalkRows; ++u)
+        if (s0 + u * kMoveThreads + tid < m) out[s0 + u * kMoveThreads + tid] = x[u];
     }
     __syncthreads();
     for (int s = m + tid; s < p.weights_out_len; s += kMoveThreads) out[s] = 0.0f;
     return;
   }
-  const int which = blockIdx.x / n_col, col = blockIdx.x % n_col;
-  uint16_t* base = (which == 0 ? p.c.k : p.c.v) + g * p.c.s_head + col * 32 + (tid & 3) * 8;
-  const int pm = (1 << p.c.page_log2) - 1;
-  constexpr int kRows = kMoveThreads / 4;
-  const int* dst_row = p.dst_table + static_cast<long long>(b) * p.dst_stride;
-  for (int s0 = 0; s0 < m; s0 += kRows * kMoveRows) {
-    uint4 x[kMoveRows];
-    uint16_t* to[kMoveRows];
+  if (lies && n <= p.budget && src_row == dst_row) return;   // nothing moves
+  // offsets of row s's source and place; false where it stays or has no page
+  auto places = [&](int s, long long& from, long long& to) {
+    const int j = __ldcg(kept + s);
+    const int f = paged_page(p.c, b, j >> lg, p.err);
+    const int t = (s >> lg) < p.dst_max_pages ? __ldg(dst_row + (s >> lg)) : -1;
+    if (t < 0 || t >= p.c.num_pages) {
+      atomicCAS(p.err, 0, ATTN_DEVERR_BAD_PAGE);
+      return false;
+    }
+    from = f * p.c.s_page + (j & pm) * p.c.s_token;
+    to = t * p.c.s_page + (s & pm) * p.c.s_token;
+    return f >= 0 && from != to;
+  };
+  if (!lies) {
+    // whole rows of K and V, 16 bytes a thread
+    const int lanes = p.d / 8, rows = kMoveThreads / lanes;
+    const long long at = g * p.c.s_head + tid % lanes * 8;
+    for (int s0 = blockIdx.x * rows * kMoveRows; s0 < m; s0 += blocks * rows * kMoveRows) {
+      uint4 x[kMoveRows], y[kMoveRows];
+      long long to[kMoveRows];
 #pragma unroll
-    for (int u = 0; u < kMoveRows; ++u) {
-      to[u] = nullptr;
-      const int s = s0 + u * kRows + (tid >> 2);
-      if (s >= m) continue;
-      const int j = __ldg(kept + s);
-      const int from = paged_page(p.c, b, j >> p.c.page_log2, p.err);
-      const int page = (s >> p.c.page_log2) < p.dst_max_pages ? __ldg(dst_row + (s >> p.c.page_log2)) : -1;
-      if (page < 0 || page >= p.c.num_pages) atomicCAS(p.err, 0, ATTN_DEVERR_BAD_PAGE);
-      else if (from >= 0 && !(from == page && j == s)) {
-        x[u] = *reinterpret_cast<const uint4*>(base + from * p.c.s_page + (j & pm) * p.c.s_token);
-        to[u] = base + page * p.c.s_page + (s & pm) * p.c.s_token;
+      for (int u = 0; u < kMoveRows; ++u) {
+        const int s = s0 + u * rows + tid / lanes;
+        long long from;
+        to[u] = -1;
+        if (s < m && places(s, from, to[u])) {
+          x[u] = *reinterpret_cast<const uint4*>(p.c.k + from + at);
+          y[u] = *reinterpret_cast<const uint4*>(p.c.v + from + at);
+        } else {
+          to[u] = -1;
+        }
       }
+#pragma unroll
+      for (int u = 0; u < kMoveRows; ++u)
+        if (to[u] >= 0) {
+          *reinterpret_cast<uint4*>(p.c.k + to[u] + at) = x[u];
+          *reinterpret_cast<uint4*>(p.c.v + to[u] + at) = y[u];
+        }
+    }
+    return;
+  }
+  const int n_col = p.d / 16;   // 32-byte columns
+  if (static_cast<int>(blockIdx.x) >= 2 * n_col) return;
+  const int which = blockIdx.x / n_col, col = blockIdx.x - which * n_col;
+  uint16_t* base = (which == 0 ? p.c.k : p.c.v) + g * p.c.s_head + col * 16 + (tid & 1) * 8;
+  constexpr int kRows = kMoveThreads / 2;
+  for (int s0 = 0; s0 < m; s0 += kRows * kWalkRows) {
+    uint4 x[kWalkRows];
+    long long to[kWalkRows];
+#pragma unroll
+    for (int u = 0; u < kWalkRows; ++u) {
+      const int s = s0 + u * kRows + (tid >> 1);
+      long long from;
+      if (s < m && places(s, from, to[u])) x[u] = *reinterpret_cast<const uint4*>(base + from);
+      else to[u] = -1;
     }
     __syncthreads();
 #pragma unroll
-    for (int u = 0; u < kMoveRows; ++u)
-      if (to[u]) *reinterpret_cast<uint4*>(to[u]) = x[u];
+    for (int u = 0; u < kWalkRows; ++u)
+      if (to[u] >= 0) *reinterpret_cast<uint4*>(base + to[u]) = x[u];
     __syncthreads();
   }
 }
@@ -233,11 +376,40 @@ extern "C" int attn_cache_evict(const float* weights, int weights_len, int* kept
   p.recent = recent;
   p.d = cache->head_dim;
   p.err = info.err_word;
-  evict_select_kernel<<<dim3(p.c.hkv, B), kSelThreads, 0, stream>>>(p);
-  if (cudaGetLastError() != cudaSuccess) return ATTN_ELAUNCH;
+  // CTAs of a cluster per (sequence, head): as many as fill the SMs, up to 8,
+  // of at least 2,048 keys each
+  const long long longest = std::min<long long>(weights_len, static_cast<long long>(cache->max_pages) * cache->page_size);
+  int cs = 8;
+  while (cs > 1 && (static_cast<long long>(B) * p.c.hkv * cs > info.sm_count || longest < 2048LL * cs)) cs /= 2;
+  p.key_slots = static_cast<int>(std::min<long long>(kMaxKeys, (longest + cs - 1) / cs + 32));
+  const int smem = p.key_slots * 4;
+  static bool attr_done[64] = {};
+  if (dev >= 64 || !attr_done[dev]) {
+    if (cudaFuncSetAttribute(evict_select_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (kMaxKeys + 32) * 4) !=
+        cudaSuccess)
+      return ATTN_ELAUNCH;
+    if (dev < 64) attr_done[dev] = true;
+  }
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(cs, p.c.hkv, B);
+  cfg.blockDim = dim3(kSelThreads);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = stream;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim.x = cs;
+  attr[0].val.clusterDim.y = 1;
+  attr[0].val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  if (cudaLaunchKernelEx(&cfg, evict_select_kernel, p) != cudaSuccess) return ATTN_ELAUNCH;
   count_launch();
-  evict_move_kernel<<<dim3(2 * p.d / 32 + 1, p.c.hkv, B), kMoveThreads, 0, stream>>>(p);
-  if (cudaGetLastError() != cudaSuccess) return ATTN_ELAUNCH;
+  cfg.gridDim = dim3(2 * p.d / 16 + 1, p.c.hkv, B);
+  cfg.blockDim = dim3(kMoveThreads);
+  cfg.dynamicSmemBytes = 0;
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  if (cudaLaunchKernelEx(&cfg, evict_move_kernel, p) != cudaSuccess) return ATTN_ELAUNCH;
   count_launch();
   return ATTN_OK;
 }

@@ -289,7 +289,7 @@ int launch(RopeParams& p, bool vec, bool bf16, bool gptj, cudaStream_t stream) {
   }
   // a warp per row once the rows fill the GPU's warps; below that a row's
   // items are shared by up to 8 warps, of at least one item a lane
-  const long long slots = 16LL * kWarps * info.sm_count / 4;
+  const long long slots = 4LL * kWarps * info.sm_count;   // resident warps
   p.parts = static_cast<int>(std::max<long long>(1, std::min<long long>({8, slots / std::max(p.rows, 1), (items + 31) / 32})));
   const long long tasks = static_cast<long long>(p.rows) * p.parts;
   const int grid = static_cast<int>(std::min<long long>((tasks + kWarps - 1) / kWarps, 4LL * info.sm_count));
