@@ -33,6 +33,7 @@ namespace {
 
 constexpr int kSelThreads = 1024;
 constexpr int kSelWarps = kSelThreads / 32;
+constexpr int kMaxCluster = 8;
 constexpr int kBins = 2048;            // 11-bit digits
 constexpr int kMaxKeys = 48 * 1024;    // weights that a CTA keeps in shared memory; more are read again
 constexpr int kMoveThreads = 256;
@@ -131,8 +132,21 @@ __global__ void __launch_bounds__(kSelThreads) evict_select_kernel(const __grid_
   const int per = ((cand + CS - 1) / CS + 31) & ~31;
   const int lo = min(rank * per, cand), hi = min(lo + per, cand);
   const bool held = per <= p.key_slots;
-  if (held) {
-    for (int j = lo + tid; j < hi; j += kSelThreads) keys[j - lo] = order_key(__ldg(w + j));
+  for (int i = tid; i < kBins; i += kSelThreads) hist[i] = 0;
+  __syncthreads();
+  // the weights, eight loads in flight, and the first digit's histogram
+  for (int j0 = lo + tid; j0 < hi; j0 += 8 * kSelThreads) {
+    float x[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) x[i] = j0 + i * kSelThreads < hi ? __ldg(w + j0 + i * kSelThreads) : 0.0f;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      const int j = j0 + i * kSelThreads;
+      if (j >= hi) break;
+      const uint32_t u = order_key(x[i]);
+      if (held) keys[j - lo] = u;
+      atomicAdd(&hist[u >> 21], 1);
+    }
   }
   auto key_at = [&](int j) { return held ? keys[j - lo] : order_key(__ldg(w + j)); };
   uint32_t prefix = 0, mask = 0;
@@ -140,11 +154,13 @@ __global__ void __launch_bounds__(kSelThreads) evict_select_kernel(const __grid_
 #pragma unroll 1
   for (int shift = 21;; shift = shift == 21 ? 10 : 0) {
     const uint32_t digit = shift == 0 ? 0x3ffu : 0x7ffu;
-    for (int i = tid; i < kBins; i += kSelThreads) hist[i] = 0;
-    __syncthreads();
-    for (int j = lo + tid; j < hi; j += kSelThreads) {
-      const uint32_t u = key_at(j);
-      if ((u & mask) == prefix) atomicAdd(&hist[(u >> shift) & digit], 1);
+    if (shift != 21) {
+      for (int i = tid; i < kBins; i += kSelThreads) hist[i] = 0;
+      __syncthreads();
+      for (int j = lo + tid; j < hi; j += kSelThreads) {
+        const uint32_t u = key_at(j);
+        if ((u & mask) == prefix) atomicAdd(&hist[(u >> shift) & digit], 1);
+      }
     }
     __syncthreads();
     // bins from the largest digit down, two a thread, over the whole cluster
@@ -152,12 +168,19 @@ __global__ void __launch_bounds__(kSelThreads) evict_select_kernel(const __grid_
     int c1 = hist[d1], c0 = hist[d1 - 1];
     if (CS > 1) {
       cluster_sync();
-      c1 = c0 = 0;
       const uint32_t a = smem_u32(&hist[d1 - 1]);
-      for (int r = 0; r < CS; ++r) {
-        const uint32_t x = mapa_shared(a, r);
-        c0 += ld_dsmem_s32(x);
-        c1 += ld_dsmem_s32(x + 4);
+      int x0[kMaxCluster], x1[kMaxCluster];   // every peer's load in flight
+#pragma unroll
+      for (int r = 0; r < kMaxCluster; ++r) {
+        const uint32_t x = mapa_shared(a, r < CS ? r : rank);
+        x0[r] = ld_dsmem_s32(x);
+        x1[r] = ld_dsmem_s32(x + 4);
+      }
+      c1 = c0 = 0;
+#pragma unroll
+      for (int r = 0; r < kMaxCluster; ++r) {
+        c0 += r < CS ? x0[r] : 0;
+        c1 += r < CS ? x1[r] : 0;
       }
       cluster_sync();   // the peers' counts have been read
     }
@@ -261,7 +284,7 @@ __global__ void __launch_bounds__(kMoveThreads) evict_move_kernel(const __grid_c
 #pragma unroll
       for (int u = 0; u < kWalkRows; ++u) {
         const int s = s0 + u * kMoveThreads + tid;
-        x[u] = s < m ? w[__ldcg(kept + s)] : 0.0f;
+        x[u] = s < m ? w[kept[s]] : 0.0f;
       }
       __syncthreads();
 #pragma unroll
@@ -275,7 +298,7 @@ __global__ void __launch_bounds__(kMoveThreads) evict_move_kernel(const __grid_c
   if (lies && n <= p.budget && src_row == dst_row) return;   // nothing moves
   // offsets of row s's source and place; false where it stays or has no page
   auto places = [&](int s, long long& from, long long& to) {
-    const int j = __ldcg(kept + s);
+    const int j = kept[s];
     const int f = paged_page(p.c, b, j >> lg, p.err);
     const int t = (s >> lg) < p.dst_max_pages ? __ldg(dst_row + (s >> lg)) : -1;
     if (t < 0 || t >= p.c.num_pages) {
@@ -290,26 +313,34 @@ __global__ void __launch_bounds__(kMoveThreads) evict_move_kernel(const __grid_c
     // whole rows of K and V, 16 bytes a thread
     const int lanes = p.d / 8, rows = kMoveThreads / lanes;
     const long long at = g * p.c.s_head + tid % lanes * 8;
-    for (int s0 = blockIdx.x * rows * kMoveRows; s0 < m; s0 += blocks * rows * kMoveRows) {
-      uint4 x[kMoveRows], y[kMoveRows];
-      long long to[kMoveRows];
+    const int step = blocks * rows * kMoveRows;
+    long long from[kMoveRows], to[kMoveRows];
+    auto find = [&](int s0) {
 #pragma unroll
       for (int u = 0; u < kMoveRows; ++u) {
         const int s = s0 + u * rows + tid / lanes;
-        long long from;
-        to[u] = -1;
-        if (s < m && places(s, from, to[u])) {
-          x[u] = *reinterpret_cast<const uint4*>(p.c.k + from + at);
-          y[u] = *reinterpret_cast<const uint4*>(p.c.v + from + at);
-        } else {
-          to[u] = -1;
+        if (s >= m || !places(s, from[u], to[u])) to[u] = -1;
+      }
+    };
+    int s0 = blockIdx.x * rows * kMoveRows;
+    if (s0 < m) find(s0);
+    for (; s0 < m; s0 += step) {
+      uint4 x[kMoveRows], y[kMoveRows];
+      long long put[kMoveRows];
+#pragma unroll
+      for (int u = 0; u < kMoveRows; ++u) {
+        put[u] = to[u];
+        if (to[u] >= 0) {
+          x[u] = *reinterpret_cast<const uint4*>(p.c.k + from[u] + at);
+          y[u] = *reinterpret_cast<const uint4*>(p.c.v + from[u] + at);
         }
       }
+      if (s0 + step < m) find(s0 + step);   // while the rows are on their way
 #pragma unroll
       for (int u = 0; u < kMoveRows; ++u)
-        if (to[u] >= 0) {
-          *reinterpret_cast<uint4*>(p.c.k + to[u] + at) = x[u];
-          *reinterpret_cast<uint4*>(p.c.v + to[u] + at) = y[u];
+        if (put[u] >= 0) {
+          *reinterpret_cast<uint4*>(p.c.k + put[u] + at) = x[u];
+          *reinterpret_cast<uint4*>(p.c.v + put[u] + at) = y[u];
         }
     }
     return;
@@ -379,7 +410,7 @@ extern "C" int attn_cache_evict(const float* weights, int weights_len, int* kept
   // CTAs of a cluster per (sequence, head): as many as fill the SMs, up to 8,
   // of at least 2,048 keys each
   const long long longest = std::min<long long>(weights_len, static_cast<long long>(cache->max_pages) * cache->page_size);
-  int cs = 8;
+  int cs = kMaxCluster;
   while (cs > 1 && (static_cast<long long>(B) * p.c.hkv * cs > info.sm_count || longest < 2048LL * cs)) cs /= 2;
   p.key_slots = static_cast<int>(std::min<long long>(kMaxKeys, (longest + cs - 1) / cs + 32));
   const int smem = p.key_slots * 4;
@@ -404,7 +435,13 @@ extern "C" int attn_cache_evict(const float* weights, int weights_len, int* kept
   cfg.numAttrs = 1;
   if (cudaLaunchKernelEx(&cfg, evict_select_kernel, p) != cudaSuccess) return ATTN_ELAUNCH;
   count_launch();
-  cfg.gridDim = dim3(2 * p.d / 16 + 1, p.c.hkv, B);
+  // blocks per (sequence, head): the columns of K and V in place; in any order
+  // up to eight blocks per SM in all, of at least one batch of rows
+  const int batch = kMoveThreads / (p.d / 8) * kMoveRows;
+  const long long heads = static_cast<long long>(B) * p.c.hkv;
+  const int blocks = static_cast<int>(std::max<long long>(
+      2 * p.d / 16, std::min<long long>((budget + batch - 1) / batch, 8LL * info.sm_count / heads)));
+  cfg.gridDim = dim3(blocks + 1, p.c.hkv, B);
   cfg.blockDim = dim3(kMoveThreads);
   cfg.dynamicSmemBytes = 0;
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
