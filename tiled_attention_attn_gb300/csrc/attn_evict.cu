@@ -69,32 +69,6 @@ __device__ __forceinline__ int evict_len(const EvictParams& p, int b) {
   return 0;
 }
 
-// Inclusive prefix sum over the block; total in *sum.
-__device__ __forceinline__ int block_scan(int x, int* warp_sums, int* sum) {
-  const int lane = threadIdx.x & 31, w = threadIdx.x >> 5;
-#pragma unroll
-  for (int o = 1; o < 32; o <<= 1) {
-    const int y = __shfl_up_sync(0xffffffffu, x, o);
-    if (lane >= o) x += y;
-  }
-  if (lane == 31) warp_sums[w] = x;
-  __syncthreads();
-  if (w == 0) {
-    int s = warp_sums[lane];
-#pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-      const int y = __shfl_up_sync(0xffffffffu, s, o);
-      if (lane >= o) s += y;
-    }
-    warp_sums[lane] = s;
-  }
-  __syncthreads();
-  x += w > 0 ? warp_sums[w - 1] : 0;
-  *sum = warp_sums[31];
-  __syncthreads();
-  return x;
-}
-
 __device__ __forceinline__ int ld_dsmem_s32(uint32_t a) {
   int v;
   asm volatile("ld.shared::cluster.s32 %0, [%1];" : "=r"(v) : "r"(a) : "memory");
@@ -105,11 +79,11 @@ __device__ __forceinline__ int ld_dsmem_s32(uint32_t a) {
 // same path, so all reach each cluster barrier.
 __global__ void __launch_bounds__(kSelThreads) evict_select_kernel(const __grid_constant__ EvictParams p) {
   extern __shared__ uint32_t keys[];
-  __shared__ int hist[kBins];
-  __shared__ int warp_sums[32];
+  __shared__ __align__(8) int hist[kBins];
+  __shared__ int coarse[32], from_peer[kMaxCluster][64];
   __shared__ int n_gt[kSelWarps + 1], n_eq[kSelWarps + 1];   // per warp; last: the CTA's
   __shared__ uint32_t s_prefix;
-  __shared__ int s_need;
+  __shared__ int s_need, s_group;
   const int CS = gridDim.x, rank = blockIdx.x;
   const int g = blockIdx.y, b = blockIdx.z, tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   grid_launch_dependents();
@@ -163,36 +137,61 @@ __global__ void __launch_bounds__(kSelThreads) evict_select_kernel(const __grid_
       }
     }
     __syncthreads();
-    // bins from the largest digit down, two a thread, over the whole cluster
-    const int d1 = kBins - 1 - 2 * tid;
-    int c1 = hist[d1], c0 = hist[d1 - 1];
-    if (CS > 1) {
-      cluster_sync();
-      const uint32_t a = smem_u32(&hist[d1 - 1]);
-      int x0[kMaxCluster], x1[kMaxCluster];   // every peer's load in flight
-#pragma unroll
-      for (int r = 0; r < kMaxCluster; ++r) {
-        const uint32_t x = mapa_shared(a, r < CS ? r : rank);
-        x0[r] = ld_dsmem_s32(x);
-        x1[r] = ld_dsmem_s32(x + 4);
-      }
-      c1 = c0 = 0;
-#pragma unroll
-      for (int r = 0; r < kMaxCluster; ++r) {
-        c0 += r < CS ? x0[r] : 0;
-        c1 += r < CS ? x1[r] : 0;
-      }
-      cluster_sync();   // the peers' counts have been read
-    }
-    int sum;
-    const int above = block_scan(c0 + c1, warp_sums, &sum);
-    if (above >= need && above - (c0 + c1) < need) {
-      const int before = above - (c0 + c1);
-      const bool first = before + c1 >= need;
-      s_prefix = prefix | static_cast<uint32_t>(first ? d1 : d1 - 1) << shift;
-      s_need = need - (first ? before : before + c1);
+    // The digit, in two steps: which group of 64 bins, then which bin; each
+    // step adds one count per CTA and bin over the cluster (all 2,048 bins of
+    // every CTA would be 64 KB to read per CTA and digit).
+    {
+      const int2 two = reinterpret_cast<const int2*>(hist)[warp * 32 + lane];
+      const int c = __reduce_add_sync(0xffffffffu, two.x + two.y);
+      if (lane == 0) coarse[warp] = c;
     }
     __syncthreads();
+    if (CS > 1) cluster_sync();
+    if (warp < CS) from_peer[warp][lane] = ld_dsmem_s32(mapa_shared(smem_u32(&coarse[lane]), warp));
+    __syncthreads();
+    if (warp == 0) {
+      int c = 0;
+      for (int r = 0; r < CS; ++r) c += from_peer[r][lane];
+      int above = c;   // keys of this group and the larger ones
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) {
+        const int y = __shfl_down_sync(0xffffffffu, above, o);
+        if (lane + o < 32) above += y;
+      }
+      if (above >= need && above - c < need) {
+        s_group = lane;
+        s_need = need - (above - c);
+      }
+    }
+    __syncthreads();
+    if (tid < 64 * CS) {
+      const int i = tid & 63;
+      from_peer[tid >> 6][i] = ld_dsmem_s32(mapa_shared(smem_u32(&hist[s_group * 64 + i]), tid >> 6));
+    }
+    __syncthreads();
+    if (warp == 0) {
+      const int need2 = s_need;
+      int c0 = 0, c1 = 0;   // bins 2 lane and 2 lane + 1 of the group
+      for (int r = 0; r < CS; ++r) {
+        c0 += from_peer[r][2 * lane];
+        c1 += from_peer[r][2 * lane + 1];
+      }
+      int above = c0 + c1;
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) {
+        const int y = __shfl_down_sync(0xffffffffu, above, o);
+        if (lane + o < 32) above += y;
+      }
+      const int before = above - (c0 + c1);
+      __syncwarp();
+      if (above >= need2 && before < need2) {
+        const bool upper = before + c1 >= need2;
+        s_prefix = prefix | static_cast<uint32_t>(s_group * 64 + 2 * lane + (upper ? 1 : 0)) << shift;
+        s_need = need2 - (upper ? before : before + c1);
+      }
+    }
+    __syncthreads();
+    if (CS > 1 && shift != 0) cluster_sync();   // the peers' counts have been read
     prefix = s_prefix;
     need = s_need;
     mask |= digit << shift;
@@ -238,10 +237,11 @@ __global__ void __launch_bounds__(kSelThreads) evict_select_kernel(const __grid_
   eq = n_eq[warp];
   if (CS > 1) {
     cluster_sync();
-    for (int r = 0; r < rank; ++r) {
-      gt += ld_dsmem_s32(mapa_shared(smem_u32(&n_gt[kSelWarps]), r));
-      eq += ld_dsmem_s32(mapa_shared(smem_u32(&n_eq[kSelWarps]), r));
-    }
+    // lane r: the counts of CTA r, of which those before this one are added
+    const int x = lane < CS ? ld_dsmem_s32(mapa_shared(smem_u32(&n_gt[kSelWarps]), lane)) : 0;
+    const int y = lane < CS ? ld_dsmem_s32(mapa_shared(smem_u32(&n_eq[kSelWarps]), lane)) : 0;
+    gt += __reduce_add_sync(0xffffffffu, lane < rank ? x : 0);
+    eq += __reduce_add_sync(0xffffffffu, lane < rank ? y : 0);
     cluster_sync();   // no CTA leaves before its counts have been read
   }
   const uint32_t below = (1u << lane) - 1u;
