@@ -5,7 +5,8 @@ single tokens over the pages, accumulated attention weights, and eviction.
 Like the rest of the binding this marshals arguments only; every step runs in
 the library's kernels.  Outputs and scratch memory are allocated by torch on
 the call's stream, so calls on several streams, or captured in several graphs,
-share nothing.
+share nothing.  Every operator takes ``stream`` by name (default: the current
+stream of its tensors' device).
 
 Caches: ``k_pages`` and ``v_pages`` are (num_pages, page_size, Hkv, d) views,
 strided as the caller likes as long as the features are contiguous (slices of
@@ -16,8 +17,8 @@ j % page_size of page page_table[b, j // page_size].
 
 from __future__ import annotations
 
-import contextlib
 import ctypes
+import functools
 import math
 from typing import Optional, Tuple
 
@@ -57,15 +58,31 @@ def declare(L) -> None:
 _HALF = (torch.bfloat16, torch.float16)
 
 
-@contextlib.contextmanager
-def _on(device: torch.device, stream: Optional[torch.cuda.Stream]):
-    """The device, with allocations on the call's stream."""
-    with torch.cuda.device(device):
-        if stream is None:
-            yield torch.cuda.current_stream(device).cuda_stream
-        else:
+def _placed(fn):
+    """Runs fn with the device of its first tensor current and, given ``stream``
+    (by name), on that stream, so that outputs and scratch memory are allocated
+    there too.  The usual call, on the current device and stream, enters no
+    context."""
+    name = fn.__code__.co_varnames[0]
+
+    @functools.wraps(fn)
+    def call(*args, stream: Optional[torch.cuda.Stream] = None, **kw):
+        dev = (args[0] if args else kw[name]).device
+        if dev.type != "cuda" or (stream is None and dev.index == torch.cuda.current_device()):
+            return fn(*args, **kw)
+        with torch.cuda.device(dev):
+            if stream is None:
+                return fn(*args, **kw)
+            if stream.device != dev:
+                raise ValueError(f"the stream is on {stream.device}, the tensors on {dev}")
             with torch.cuda.stream(stream):
-                yield stream.cuda_stream
+                return fn(*args, **kw)
+
+    return call
+
+
+def _stream(device: torch.device) -> int:
+    return torch._C._cuda_getCurrentRawStream(device.index)
 
 
 def _check_int(t: torch.Tensor, name: str, device, shape) -> None:
@@ -97,7 +114,7 @@ def _cache(k_pages: torch.Tensor, v_pages: Optional[torch.Tensor], page_table: t
     n, P, hkv, d = k_pages.shape
     sp, st, sh, _ = k_pages.stride()
     # strides of an axis of one entry address nothing: any valid value serves
-    sp, st, sh = (s if m > 1 else max(8, d) for s, m in ((sp, n), (st, P), (sh, hkv)))
+    sp, sh = sp if n > 1 else max(8, d), sh if hkv > 1 else max(8, d)
     ts = page_table.stride(0) if B > 1 else max_pages
     return _PagedKV(k_pages.data_ptr(), v_pages.data_ptr() if v_pages is not None else None, page_table.data_ptr(),
                     seqlens_k.data_ptr(), sp, st, sh, ts, max_pages, n, P, hkv, d, int(k_pages.dtype == torch.float16))
@@ -153,10 +170,10 @@ def rotary_freqs(rot_dim: int, base: float = 10000.0, scaling: Optional[str] = N
     raise ValueError(f"unknown scaling {scaling!r}")
 
 
+@_placed
 def rotary_scaled(x: torch.Tensor, freqs: torch.Tensor, amplitude: float = 1.0, interleaved: bool = False,
                   cu_seqlens: Optional[torch.Tensor] = None, offsets: Optional[torch.Tensor] = None,
-                  positions: Optional[torch.Tensor] = None, inverse: bool = False, out: Optional[torch.Tensor] = None,
-                  stream: Optional[torch.cuda.Stream] = None) -> torch.Tensor:
+                  positions: Optional[torch.Tensor] = None, inverse: bool = False, out: Optional[torch.Tensor] = None) -> torch.Tensor:
     """Rotary embedding of x with the given frequencies (``rotary_freqs``; a
     float64 host tensor of rot_dim / 2 radians per position) times ``amplitude``;
     ``inverse`` turns the other way, which is its gradient.
@@ -205,17 +222,17 @@ def rotary_scaled(x: torch.Tensor, freqs: torch.Tensor, amplitude: float = 1.0, 
         _check_int(offsets, "offsets", dev, (B,))
     if B == 0 or H == 0:
         raise ValueError("x has no sequences or no heads")
-    with _on(dev, stream) as s:
-        if out is None:
-            out = torch.empty(x.shape, dtype=x.dtype, device=dev)
-        elif out.shape != x.shape or out.dtype != x.dtype or out.device != dev or not out.is_contiguous():
-            raise ValueError("out must be a contiguous tensor shaped like x")
-        rc = _attn.lib().attn_rotary_scaled(
-            x.data_ptr() or None, out.data_ptr() or None, B, L, H, d, rot, f.data_ptr(), float(amplitude),
-            int(bool(interleaved)), int(bool(inverse)), st, sh,
-            cu_seqlens.data_ptr() if cu_seqlens is not None else None, total,
-            offsets.data_ptr() if offsets is not None else None,
-            positions.data_ptr() if positions is not None else None, int(x.dtype == torch.float16), s) if rows else 0
+    s = _stream(dev)
+    if out is None:
+        out = torch.empty(x.shape, dtype=x.dtype, device=dev)
+    elif out.shape != x.shape or out.dtype != x.dtype or out.device != dev or not out.is_contiguous():
+        raise ValueError("out must be a contiguous tensor shaped like x")
+    rc = _attn.lib().attn_rotary_scaled(
+        x.data_ptr() or None, out.data_ptr() or None, B, L, H, d, rot, f.data_ptr(), float(amplitude),
+        int(bool(interleaved)), int(bool(inverse)), st, sh,
+        cu_seqlens.data_ptr() if cu_seqlens is not None else None, total,
+        offsets.data_ptr() if offsets is not None else None,
+        positions.data_ptr() if positions is not None else None, int(x.dtype == torch.float16), s) if rows else 0
     _check_rc(rc, "attn_rotary_scaled")
     return out
 
@@ -252,12 +269,12 @@ def rotary_scaled_func(x: torch.Tensor, freqs: torch.Tensor, amplitude: float = 
     return _RotaryScaledFunction.apply(x, freqs, float(amplitude), bool(interleaved), cu_seqlens, offsets, positions)
 
 
+@_placed
 def cache_append(k: torch.Tensor, v: torch.Tensor, k_pages: torch.Tensor, v_pages: torch.Tensor,
                  page_table: torch.Tensor, seqlens_k: torch.Tensor, cu_seqlens: torch.Tensor,
                  q: Optional[torch.Tensor] = None, freqs: Optional[torch.Tensor] = None, amplitude: float = 1.0,
                  interleaved: bool = False, positions: Optional[torch.Tensor] = None,
-                 q_out: Optional[torch.Tensor] = None,
-                 stream: Optional[torch.cuda.Stream] = None) -> Optional[torch.Tensor]:
+                 q_out: Optional[torch.Tensor] = None) -> Optional[torch.Tensor]:
     """Writes the new tokens' k and v, (total, Hkv, d) with offsets
     ``cu_seqlens`` (int32, B + 1), into the pages; ``seqlens_k`` counts them
     already (they are each sequence's last keys).  With ``freqs`` the keys, and
@@ -288,19 +305,19 @@ def cache_append(k: torch.Tensor, v: torch.Tensor, k_pages: torch.Tensor, v_page
     if positions is not None:
         _check_int(positions, "positions", dev, (total,))
     f, rot = (None, 0) if freqs is None else _freqs(freqs, d)
-    with _on(dev, stream) as s:
-        if q is not None and q_out is None:
-            q_out = torch.empty(q.shape, dtype=q.dtype, device=dev)
-        elif q is None and q_out is not None:
-            raise ValueError("q_out without q")
-        elif q is not None and (q_out.shape != q.shape or q_out.dtype != q.dtype or q_out.device != dev
-                                or not q_out.is_contiguous()):
-            raise ValueError("q_out must be a contiguous tensor shaped like q")
-        rc = _attn.lib().attn_cache_append(
-            q.data_ptr() if q is not None else None, k.data_ptr() or None, v.data_ptr() or None,
-            q_out.data_ptr() if q is not None else None, *strides, B, q.shape[1] if q is not None else 0, total,
-            ctypes.byref(c), cu_seqlens.data_ptr(), rot, f.data_ptr() if f is not None else None, float(amplitude),
-            int(bool(interleaved)), positions.data_ptr() if positions is not None else None, s) if total else 0
+    s = _stream(dev)
+    if q is not None and q_out is None:
+        q_out = torch.empty(q.shape, dtype=q.dtype, device=dev)
+    elif q is None and q_out is not None:
+        raise ValueError("q_out without q")
+    elif q is not None and (q_out.shape != q.shape or q_out.dtype != q.dtype or q_out.device != dev
+                            or not q_out.is_contiguous()):
+        raise ValueError("q_out must be a contiguous tensor shaped like q")
+    rc = _attn.lib().attn_cache_append(
+        q.data_ptr() if q is not None else None, k.data_ptr() or None, v.data_ptr() or None,
+        q_out.data_ptr() if q is not None else None, *strides, B, q.shape[1] if q is not None else 0, total,
+        ctypes.byref(c), cu_seqlens.data_ptr(), rot, f.data_ptr() if f is not None else None, float(amplitude),
+        int(bool(interleaved)), positions.data_ptr() if positions is not None else None, s) if total else 0
     _check_rc(rc, "attn_cache_append")
     return q_out
 
@@ -333,11 +350,11 @@ def _outputs(q, out, lse):
     return out, lse
 
 
+@_placed
 def attn_fwd_paged(q: torch.Tensor, k_pages: torch.Tensor, v_pages: torch.Tensor, page_table: torch.Tensor,
                    seqlens_k: torch.Tensor, cu_seqlens: torch.Tensor, causal: bool = True,
                    scale: Optional[float] = None, out: Optional[torch.Tensor] = None,
-                   lse: Optional[torch.Tensor] = None,
-                   stream: Optional[torch.cuda.Stream] = None) -> Tuple[torch.Tensor, torch.Tensor]:
+                   lse: Optional[torch.Tensor] = None) -> Tuple[torch.Tensor, torch.Tensor]:
     """Attention of a chunk of new tokens over a paged cache: q (total, Hq, d)
     with offsets ``cu_seqlens`` (int32, B + 1) against the ``seqlens_k`` keys of
     each sequence; causal aligns bottom-right (the queries are the last
@@ -349,20 +366,20 @@ def attn_fwd_paged(q: torch.Tensor, k_pages: torch.Tensor, v_pages: torch.Tensor
     _check_int(cu_seqlens, "cu_seqlens", q.device, (B + 1,))
     if scale is None:
         scale = 1.0 / math.sqrt(c.head_dim)
-    with _on(q.device, stream) as s:
-        out, lse = _outputs(q, out, lse)
-        ws = _workspace(q.device, c.head_dim, _CHUNK)
-        rc = _attn.lib().attn_fwd_paged(q.data_ptr(), out.data_ptr(), lse.data_ptr(), B, q.shape[1], q.shape[0],
-                                        ctypes.byref(c), cu_seqlens.data_ptr(), int(bool(causal)), float(scale),
-                                        ws.data_ptr(), ws.numel(), s) if q.shape[0] else 0
+    s = _stream(q.device)
+    out, lse = _outputs(q, out, lse)
+    ws = _workspace(q.device, c.head_dim, _CHUNK)
+    rc = _attn.lib().attn_fwd_paged(q.data_ptr(), out.data_ptr(), lse.data_ptr(), B, q.shape[1], q.shape[0],
+                                    ctypes.byref(c), cu_seqlens.data_ptr(), int(bool(causal)), float(scale),
+                                    ws.data_ptr(), ws.numel(), s) if q.shape[0] else 0
     _check_rc(rc, "attn_fwd_paged")
     return out, lse
 
 
+@_placed
 def attn_decode_paged(q: torch.Tensor, k_pages: torch.Tensor, v_pages: torch.Tensor, page_table: torch.Tensor,
                       seqlens_k: torch.Tensor, scale: Optional[float] = None, out: Optional[torch.Tensor] = None,
-                      lse: Optional[torch.Tensor] = None,
-                      stream: Optional[torch.cuda.Stream] = None) -> Tuple[torch.Tensor, torch.Tensor]:
+                      lse: Optional[torch.Tensor] = None) -> Tuple[torch.Tensor, torch.Tensor]:
     """One decoding step over a paged cache: q (B, Hq, d) holds one query per
     sequence, which sees all of its seqlens_k[b] keys.  Returns O (B, Hq, d)
     and lse (Hq, B) float32."""
@@ -372,19 +389,19 @@ def attn_decode_paged(q: torch.Tensor, k_pages: torch.Tensor, v_pages: torch.Ten
         raise ValueError("q holds one row per sequence of page_table")
     if scale is None:
         scale = 1.0 / math.sqrt(c.head_dim)
-    with _on(q.device, stream) as s:
-        out, lse = _outputs(q, out, lse)
-        ws = _workspace(q.device, c.head_dim, _DECODE)
-        rc = _attn.lib().attn_decode_paged(q.data_ptr(), out.data_ptr(), lse.data_ptr(), q.shape[0], q.shape[1],
-                                           ctypes.byref(c), float(scale), ws.data_ptr(), ws.numel(), s)
+    s = _stream(q.device)
+    out, lse = _outputs(q, out, lse)
+    ws = _workspace(q.device, c.head_dim, _DECODE)
+    rc = _attn.lib().attn_decode_paged(q.data_ptr(), out.data_ptr(), lse.data_ptr(), q.shape[0], q.shape[1],
+                                       ctypes.byref(c), float(scale), ws.data_ptr(), ws.numel(), s)
     _check_rc(rc, "attn_decode_paged")
     return out, lse
 
 
+@_placed
 def key_weights(q: torch.Tensor, k_pages: torch.Tensor, lse: torch.Tensor, page_table: torch.Tensor,
                 seqlens_k: torch.Tensor, cu_seqlens: torch.Tensor, causal: bool = True, scale: Optional[float] = None,
-                decay: float = 1.0, weights: Optional[torch.Tensor] = None,
-                stream: Optional[torch.cuda.Stream] = None) -> torch.Tensor:
+                decay: float = 1.0, weights: Optional[torch.Tensor] = None) -> torch.Tensor:
     """Adds the attention weight that each cached key receives from the queries
     q to ``weights`` (B, Hkv, n) float32, summed over the queries and over the
     query heads of the key's head: weights = decay * weights + added.  q,
@@ -401,24 +418,24 @@ def key_weights(q: torch.Tensor, k_pages: torch.Tensor, lse: torch.Tensor, page_
         raise ValueError(f"lse must be a contiguous float32 tensor of shape {(Hq, T)}")
     if scale is None:
         scale = 1.0 / math.sqrt(d)
-    with _on(dev, stream) as s:
-        if weights is None:
-            weights = torch.zeros((B, c.num_kv_heads, c.max_pages * c.page_size), dtype=torch.float32, device=dev)
-        if weights.dim() != 3 or weights.shape[:2] != (B, c.num_kv_heads) or weights.dtype != torch.float32 or \
-                weights.device != dev or not weights.is_contiguous():
-            raise ValueError("weights must be a contiguous float32 tensor (B, Hkv, n)")
-        ws = _workspace(dev, d, _WEIGHTS)
-        rc = _attn.lib().attn_key_weights(q.data_ptr() or None, lse.data_ptr() or None, weights.data_ptr() or None,
-                                          weights.shape[2], B, Hq, T, ctypes.byref(c), cu_seqlens.data_ptr(),
-                                          int(bool(causal)), float(scale), float(decay), ws.data_ptr(), ws.numel(), s)
+    s = _stream(dev)
+    if weights is None:
+        weights = torch.zeros((B, c.num_kv_heads, c.max_pages * c.page_size), dtype=torch.float32, device=dev)
+    if weights.dim() != 3 or weights.shape[:2] != (B, c.num_kv_heads) or weights.dtype != torch.float32 or \
+            weights.device != dev or not weights.is_contiguous():
+        raise ValueError("weights must be a contiguous float32 tensor (B, Hkv, n)")
+    ws = _workspace(dev, d, _WEIGHTS)
+    rc = _attn.lib().attn_key_weights(q.data_ptr() or None, lse.data_ptr() or None, weights.data_ptr() or None,
+                                      weights.shape[2], B, Hq, T, ctypes.byref(c), cu_seqlens.data_ptr(),
+                                      int(bool(causal)), float(scale), float(decay), ws.data_ptr(), ws.numel(), s)
     _check_rc(rc, "attn_key_weights")
     return weights
 
 
+@_placed
 def cache_evict(weights: torch.Tensor, k_pages: torch.Tensor, v_pages: torch.Tensor, page_table: torch.Tensor,
                 seqlens_k: torch.Tensor, budget: int, recent: int = 0, dst_page_table: Optional[torch.Tensor] = None,
-                weights_out: Optional[torch.Tensor] = None,
-                stream: Optional[torch.cuda.Stream] = None) -> Tuple[torch.Tensor, torch.Tensor, torch.Tensor]:
+                weights_out: Optional[torch.Tensor] = None) -> Tuple[torch.Tensor, torch.Tensor, torch.Tensor]:
     """Cuts every sequence back to ``budget`` keys per key/value head: its last
     ``recent`` keys and the heaviest others by ``weights`` (B, Hkv, n) float32,
     ties to the lower index, in the order of the cache.  The kept rows move to
@@ -445,13 +462,13 @@ def cache_evict(weights: torch.Tensor, k_pages: torch.Tensor, v_pages: torch.Ten
             raise ValueError("dst_page_table must be an int32 CUDA tensor (B, m) with contiguous rows")
         dst, dm = dst_page_table.data_ptr(), dst_page_table.shape[1]
         ds = dst_page_table.stride(0) if B > 1 else dm
-    with _on(dev, stream) as s:
-        kept = torch.empty((B, hkv, budget), dtype=torch.int32, device=dev)
-        seqlens = torch.empty(B, dtype=torch.int32, device=dev)
-        if weights_out is None:
-            weights_out = torch.empty((B, hkv, budget), dtype=torch.float32, device=dev)
-        rc = _attn.lib().attn_cache_evict(weights.data_ptr() or None, weights.shape[2], kept.data_ptr(),
-                                          seqlens.data_ptr(), weights_out.data_ptr(), weights_out.shape[2], B,
-                                          ctypes.byref(c), dst, ds, dm, int(budget), int(recent), s)
+    s = _stream(dev)
+    kept = torch.empty((B, hkv, budget), dtype=torch.int32, device=dev)
+    seqlens = torch.empty(B, dtype=torch.int32, device=dev)
+    if weights_out is None:
+        weights_out = torch.empty((B, hkv, budget), dtype=torch.float32, device=dev)
+    rc = _attn.lib().attn_cache_evict(weights.data_ptr() or None, weights.shape[2], kept.data_ptr(),
+                                      seqlens.data_ptr(), weights_out.data_ptr(), weights_out.shape[2], B,
+                                      ctypes.byref(c), dst, ds, dm, int(budget), int(recent), s)
     _check_rc(rc, "attn_cache_evict")
     return kept, seqlens, weights_out
