@@ -85,10 +85,14 @@ struct Line {
     if (mb <= 0) return 0;
     const long long last = (w.k_len + kBN - 1) / kBN;
     if (!CAUSAL) return sum + last * mb;
+    if (mb <= 32) {   // short chunks: one by one, without the closed form's divisions
+      for (int i = 0; i < mb; ++i) sum += tiles(w, i);
+      return sum;
+    }
     // whole blocks: ceil((off + (i + 1) tok) / kBN), from the first that sees a key
     const int whole = min(mb, w.n_mb - 1);
-    const long long off = static_cast<long long>(w.k_len) - w.q_len, step = tok();
-    const long long i0 = off + step > 0 ? 0 : (-off) / step;   // off + (i0 + 1) step > 0
+    const int off = w.k_len - w.q_len, step = tok();
+    const int i0 = off + step > 0 ? 0 : (-off) / step;   // off + (i0 + 1) step > 0
     if (whole > i0) sum += floor_sum(whole - i0, kBN, step, off + (i0 + 1) * step + kBN - 1);
     if (mb == w.n_mb) sum += last;
     return sum;
@@ -537,12 +541,13 @@ __global__ void __launch_bounds__(kThreads, 1) fwd_kernel(const __grid_constant_
 }
 
 // Joins the pieces of the unit that block x's CTA began: M = max m_s, w_s =
-// 2^(m_s - M) l_s, O = sum w_s O_s / sum w_s.  Block (CTA, sub-tile, 16
-// columns), one thread per row; a programmatic dependent of the forward.
+// 2^(m_s - M) l_s, O = sum w_s O_s / sum w_s.  Block (CTA, sub-tile, 64
+// columns), one thread per row and 16 columns; a programmatic dependent of the
+// forward.
 template <int D, bool BF16>
-__global__ void __launch_bounds__(kBM) fwd_merge_kernel(const __grid_constant__ Params p) {
+__global__ void __launch_bounds__(4 * kBM) fwd_merge_kernel(const __grid_constant__ Params p) {
   using T = typename IO<BF16>::T;
-  const int c0 = blockIdx.x, t = blockIdx.y, cb = blockIdx.z, row = threadIdx.x;
+  const int c0 = blockIdx.x, t = blockIdx.y, cb = blockIdx.z * 4 + threadIdx.x / kBM, row = threadIdx.x % kBM;
   grid_wait_prerequisites();
   const int4 rec = __ldcg(p.rec + c0);
   const int pieces = rec.w;
@@ -617,8 +622,8 @@ cudaError_t launch(const Params& p, int grid, cudaStream_t stream) {
   e = cudaGetLastError();
   if (e != cudaSuccess) return e;
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(grid, kNSub, D / 16);
-  cfg.blockDim = dim3(kBM);
+  cfg.gridDim = dim3(grid, kNSub, D / 64);
+  cfg.blockDim = dim3(4 * kBM);
   cfg.stream = stream;
   cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;

@@ -32,19 +32,20 @@ __device__ __forceinline__ long long block_prefix(long long mine, long long* war
 // sum over i < n of floor((a i + b) / m), for a, b >= 0: the whole multiples of
 // m in a and b are summed directly; of what is left, points under a line of
 // slope a / m < 1 are counted by columns of the transposed line, as in
-// Euclid's algorithm.
-__device__ inline long long floor_sum(long long n, long long m, long long a, long long b) {
+// Euclid's algorithm.  a n + b fits in 32 bits.
+__device__ inline long long floor_sum(unsigned n, unsigned m, unsigned a, unsigned b) {
   long long sum = 0;
   while (n > 0) {
-    sum += n * (n - 1) / 2 * (a / m) + n * (b / m);
-    a %= m;
-    b %= m;
-    const long long top = a * n + b;   // the line's end, in m-ths
+    const unsigned qa = a / m, qb = b / m;
+    sum += static_cast<long long>(n) * (n - 1) / 2 * qa + static_cast<long long>(n) * qb;
+    a -= qa * m;
+    b -= qb * m;
+    const unsigned top = a * n + b;   // the line's end, in m-ths
     if (top < m) break;
     // rows 1 .. top / m, each crossed at the column where the line reaches it
     n = top / m;
-    b = top % m;
-    const long long t = m;
+    b = top - n * m;
+    const unsigned t = m;
     m = a;
     a = t;
   }

@@ -346,16 +346,22 @@ __global__ void __launch_bounds__(kThr, 1) weights_kernel(const __grid_constant_
     const int pg = lane % n_pg, ch = (lane / n_pg) % C::kChunks, x = lane / (n_pg * C::kChunks);
     const bool has = lane < 2 * C::kChunks * n_pg;
     const uint32_t dst0 = sK + x * C::kKTile + ch * 16384 + pg * box * 128;
-    Walk w = w0;
-    bool ok = true;
-    for (bool more = line.next(w, true); more && ok; more = line.next(w, false)) {
+    // the page of this lane's box of a unit, -1: none to load
+    auto page_of = [&](const Walk& u) {
+      const int key = u.kb * kKeys + x * 128 + pg * box;
+      if (!has || key >= u.k_len || u.t1 <= u.t0) return -1;
+      const int id = paged_page(p.c, u.b, key >> p.c.page_log2, p.err);
+      return id < 0 ? p.c.num_pages : id;   // no page: rows past the pool read as zeros
+    };
+    Walk w = w0, ahead;   // the next unit, whose page is read while this one is issued
+    bool ok = true, more = line.next(w, true), more_ahead = false;
+    int page = more ? page_of(w) : -1, page_ahead = -1;
+    for (; more && ok; w = ahead, more = more_ahead, page = page_ahead) {
+      ahead = w;
+      more_ahead = line.next(ahead, false);
+      page_ahead = more_ahead ? page_of(ahead) : -1;
       if (w.t1 <= w.t0) continue;
       const int key = w.kb * kKeys + x * 128 + pg * box;
-      int page = -1;
-      if (has && key < w.k_len) {
-        page = paged_page(p.c, w.b, key >> p.c.page_log2, p.err);
-        if (page < 0) page = p.c.num_pages;   // no page: rows past the pool read as zeros
-      }
       const int ks = k_cnt % C::kKS;
       if (!mbar_wait_warp(b_k_empty(ks), ((k_cnt / C::kKS) & 1) ^ 1, wc, ATTN_DEVERR_WAIT_TIMEOUT_SITE(kSiteKEmpty))) break;
       const uint32_t n_box = __popc(__ballot_sync(0xffffffffu, page >= 0));
