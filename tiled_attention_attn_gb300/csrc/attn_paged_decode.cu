@@ -298,7 +298,6 @@ __global__ void __launch_bounds__(kThreads, 1) decode_kernel(const __grid_consta
     bool ok = true;
     for (bool more = next_unit<KS>(p, w, true); more && ok; more = next_unit<KS>(p, w, false)) {
       if (w.t1 <= w.t0) continue;
-      int page = page_at(w, w.t0);
       const int qs = q_cnt & 1;
       if (!mbar_wait_warp(b_q_empty(qs), ((q_cnt >> 1) & 1) ^ 1, wc, ATTN_DEVERR_WAIT_TIMEOUT_SITE(kSiteQEmpty))) break;
       const int g = w.hc / p.parts, part = w.hc - g * p.parts;
@@ -309,6 +308,7 @@ __global__ void __launch_bounds__(kThreads, 1) decode_kernel(const __grid_consta
                       w.b, 0);
       }
       ++q_cnt;
+      int page = page_at(w, w.t0);
       for (int t = w.t0; t < w.t1; ++t) {
         const int st = kv_cnt % kStages;
         const int next = t + 1 < w.t1 ? page_at(w, t + 1) : -1;

@@ -148,6 +148,58 @@ struct PCfg {
   static_assert(kSmem <= 227 * 1024, "shared memory");
 };
 
+// softmax_tile of a tile some of whose keys are hidden (diagonal and ragged
+// tiles): keys past `lim` are dropped by index.  The scores are read from TMEM
+// twice, 32 columns at a time in rolled loops, instead of held in 128
+// registers: an eighth of the code, which a short call fetches cold (one tile of
+// 64 rows: MASKED_COLD).
+template <bool BF16, int D>
+__device__ __forceinline__ void softmax_masked(uint32_t t_s, uint32_t t_o, int lim, float c_log2, RowState& st, bool first) {
+  float mx = -INFINITY;
+#pragma unroll 1
+  for (int c0 = 0; c0 < kBN; c0 += 32) {
+    uint32_t r[32];
+    tmem_ld_32x32b_x32(t_s + c0, r);
+    tmem_wait_ld(r);
+#pragma unroll
+    for (int i = 0; i < 32; ++i) mx = fmaxf(mx, c0 + i <= lim ? __uint_as_float(r[i]) : -INFINITY);
+  }
+  const float m_tile = (mx == -INFINITY) ? -INFINITY : mx * c_log2, m_old = st.m;
+  const bool resc = m_tile > m_old && (first || m_old == -INFINITY || m_tile - m_old > 8.0f);
+  if (resc) st.m = m_tile;
+  const float moff = (st.m == -INFINITY) ? 0.0f : st.m;
+  float sum = 0.0f;
+  // P of columns c0 .. c0 + 31 goes to words c0 / 2 .., below the scores still to be read
+#pragma unroll 1
+  for (int c0 = 0; c0 < kBN; c0 += 32) {
+    uint32_t r[32], pk[16];
+    tmem_ld_32x32b_x32(t_s + c0, r);
+    tmem_wait_ld(r);
+#pragma unroll
+    for (int i = 0; i < 16; ++i) {
+      const float a = c0 + 2 * i <= lim ? ex2_approx(__uint_as_float(r[2 * i]) * c_log2 - moff) : 0.0f;
+      const float b = c0 + 2 * i + 1 <= lim ? ex2_approx(__uint_as_float(r[2 * i + 1]) * c_log2 - moff) : 0.0f;
+      sum += a + b;
+      pk[i] = pack2<BF16>(a, b);
+    }
+    tmem_st_32x32b_x16(t_s + c0 / 2, pk);
+  }
+  const float r = resc ? ((m_old == -INFINITY) ? 0.0f : ex2_approx(m_old - st.m)) : 1.0f;
+  st.l = st.l * r + sum;
+  if (!first && __any_sync(0xffffffffu, resc)) {
+#pragma unroll 1
+    for (int c = 0; c < D / 16; ++c) {
+      uint32_t o[16];
+      tmem_ld_32x32b_x16(t_o + c * 16, o);
+      tmem_wait_ld(o);
+#pragma unroll
+      for (int i = 0; i < 16; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * r);
+      tmem_st_32x32b_x16(t_o + c * 16, o);
+    }
+  }
+  tmem_wait_st();
+}
+
 template <int D, bool BF16, bool CAUSAL>
 __global__ void __launch_bounds__(kThreads, 1) fwd_kernel(const __grid_constant__ Params p) {
   using C = PCfg<D>;
@@ -223,8 +275,8 @@ __global__ void __launch_bounds__(kThreads, 1) fwd_kernel(const __grid_constant_
   if (begin >= before && begin < before + mine) {
     long long at = before;
     for (w0.b = b_lo; w0.b < b_hi; ++w0.b) {
-      line.load(w0);
-      const long long cost = line.cost(w0);
+      if (strip > 1) line.load(w0);   // else still there
+      const long long cost = strip > 1 ? line.cost(w0) : mine;
       if (begin < at + cost) {
         const long long per = line.before(w0, w0.n_mb);
         const int hc = static_cast<int>((begin - at) / per);
@@ -288,7 +340,6 @@ __global__ void __launch_bounds__(kThreads, 1) fwd_kernel(const __grid_constant_
         const int id = paged_page(p.c, w.b, key >> p.c.page_log2, p.err);
         return id < 0 ? p.c.num_pages : id;   // no page: rows past the pool read as zeros
       };
-      int page = page_at(0);
       if (!mbar_wait_warp(b_q_empty, (q_cnt & 1) ^ 1, wc, ATTN_DEVERR_WAIT_TIMEOUT_SITE(kSiteQEmpty))) break;
       const int g = w.hc / p.parts, head0 = g * p.group + (w.hc - g * p.parts) * p.heads;
       if (lane == 0) {
@@ -299,6 +350,7 @@ __global__ void __launch_bounds__(kThreads, 1) fwd_kernel(const __grid_constant_
                         w.row_q + w.mb * line.tok() + t * p.span, 0);
       }
       ++q_cnt;
+      int page = page_at(0);
       for (int i = 0; i <= n; ++i) {
         const int st = kv_cnt % C::kNS;
         const int next = page_at(i + 1);
@@ -453,7 +505,7 @@ __global__ void __launch_bounds__(kThreads, 1) fwd_kernel(const __grid_constant_
             }
             fence_proxy_async_smem();
           }
-          softmax_tile<true, BF16, D>(t_s, t_o, lim, c_log2, st, n_act == 0);
+          softmax_masked<BF16, D>(t_s, t_o, lim, c_log2, st, n_act == 0);
         } else {
           softmax_tile<false, BF16, D>(t_s, t_o, lim, c_log2, st, n_act == 0);
         }
@@ -475,7 +527,7 @@ __global__ void __launch_bounds__(kThreads, 1) fwd_kernel(const __grid_constant_
         // O = u / l, lse = m / log2(e) + ln l
         T* dst = out + (static_cast<size_t>(w.row_q + qrow) * p.Hq + head0 + r_head) * D;
         const bool v8 = (reinterpret_cast<uintptr_t>(p.o) & 31) == 0;
-#pragma unroll
+#pragma unroll 1
         for (int c = 0; c < D / 32; ++c) {
           uint32_t o[32];
           if (n_act > 0) {
@@ -506,7 +558,7 @@ __global__ void __launch_bounds__(kThreads, 1) fwd_kernel(const __grid_constant_
         // 4-column group are 512 contiguous bytes
         const size_t slot = static_cast<size_t>(2 * blockIdx.x + (w.t0 == 0 ? 1 : 0)) * kNSub + t;
         if (n_act > 0) {
-#pragma unroll
+#pragma unroll 1
           for (int c = 0; c < D / 32; ++c) {
             uint32_t o[32];
             tmem_ld_32x32b_x32(t_o + c * 32, o);
