@@ -52,6 +52,7 @@ constexpr int kWarpMMA = 1;
 constexpr int kKeys = 128;   // keys per tile
 constexpr int kNQ = 16;      // head columns
 constexpr int kStages = 3;
+constexpr int kMinSteps = 4;   // pieces of a cut unit are at least about this long
 constexpr int kTile = kKeys * 128 * 2;   // one stage of K or of V: two 64-column chunks
 constexpr int kChunk = kTile / 2;
 
@@ -122,10 +123,7 @@ __device__ __forceinline__ bool next_unit(const Params& p, Walk& w, bool first) 
     }
   }
   while (w.b < p.B && w.p < w.end) {
-    const long long lo = w.begin - w.p, hi = w.end - w.p;
-    w.t0 = lo > 0 ? static_cast<int>(min(lo, static_cast<long long>(w.T))) : 0;
-    w.t1 = static_cast<int>(min(hi, static_cast<long long>(w.T)));
-    if (w.t0 < w.t1 || (w.T == 0 && lo <= 0)) return true;
+    if (part_of<kMinSteps>(w.p, w.T, w.begin, w.end, w.t0, w.t1)) return true;
     w.p += w.T + 1;
     if (++w.hc == nh) {
       w.hc = 0;
@@ -234,14 +232,11 @@ __global__ void __launch_bounds__(kThreads, 1) decode_kernel(const __grid_consta
   const int nh = p.c.hkv * p.parts;
   const int strip = (p.B + kThreads - 1) / kThreads;
   const int b_lo = min(tid * strip, p.B), b_hi = min(b_lo + strip, p.B);
-  long long mine = 0;
+  long long mine = 0, total, units;
   for (int b = b_lo; b < b_hi; ++b) mine += static_cast<long long>(nh) * (steps_of<KS>(paged_len(p.c, b, p.err)) + 1);
-  long long total;
-  const long long before = block_prefix<kThreads>(mine, warp_sums, total);
-  // equal ranges, but of at least kMinSteps: below that the merge of more
-  // pieces costs more than the steps it saves
-  constexpr int kMinSteps = 4;
-  const long long range = max((total + gridDim.x - 1) / gridDim.x, static_cast<long long>(kMinSteps));
+  const long long before = block_prefix<kThreads>(
+      mine, static_cast<int>(min(static_cast<long long>(nh) * (b_hi - b_lo), 1LL << 24)), warp_sums, total, units);
+  const long long range = range_of<kMinSteps>(total, units);
   const long long begin = blockIdx.x * range, end = min(begin + range, total);
   if (begin >= before && begin < before + mine) {
     long long at = before;

@@ -40,7 +40,7 @@ namespace attn {
 namespace pfwd {
 
 constexpr int kUnitCost = 2;   // a unit's fixed cost (Q, first S, epilogue) in tiles
-constexpr int kMinTiles = 6;   // a range's least length: below it more pieces cost more than they save
+constexpr int kMinTiles = 6;   // pieces of a cut unit are at least about this long
 
 struct Params {
   CUtensorMap tm_q;    // q (total, Hq, d) as (d, Hq, total, 1), box 64 x heads x span x 1
@@ -103,6 +103,9 @@ struct Line {
     w.n_mb = (w.q_len + tok() - 1) / tok();
   }
   __device__ long long cost(const Walk& w) const { return before(w, w.n_mb) * units_per_block(); }
+  __device__ int units(const Walk& w) const {
+    return static_cast<int>(min(static_cast<long long>(w.n_mb) * units_per_block(), 1LL << 24));
+  }
   __device__ void advance(Walk& w) const {
     w.p += w.n + kUnitCost;
     if (++w.mb == w.n_mb) {
@@ -121,10 +124,7 @@ struct Line {
   __device__ bool next(Walk& w, bool first) const {
     if (!first) advance(w);
     while (w.b < p.B && w.p < w.end) {
-      const long long lo = w.begin - w.p, hi = w.end - w.p;
-      w.t0 = lo > 0 ? static_cast<int>(min(lo, static_cast<long long>(w.n))) : 0;
-      w.t1 = static_cast<int>(min(hi, static_cast<long long>(w.n)));
-      if (w.t0 < w.t1 || (w.n == 0 && lo <= 0)) return true;
+      if (part_of<kMinTiles>(w.p, w.n, w.begin, w.end, w.t0, w.t1)) return true;
       advance(w);
     }
     return false;
@@ -263,14 +263,15 @@ __global__ void __launch_bounds__(kThreads, 1) fwd_kernel(const __grid_constant_
   Walk w0;
   const int strip = (p.B + kThreads - 1) / kThreads;
   const int b_lo = min(tid * strip, p.B), b_hi = min(b_lo + strip, p.B);
-  long long mine = 0;
+  long long mine = 0, total, units;
+  int count = 0;
   for (w0.b = b_lo; w0.b < b_hi; ++w0.b) {
     line.load(w0);
     mine += line.cost(w0);
+    count = min(count + line.units(w0), 1 << 24);   // (for a mean: the largest need not be exact)
   }
-  long long total;
-  const long long before = block_prefix<kThreads>(mine, warp_sums, total);
-  const long long range = max((total + gridDim.x - 1) / gridDim.x, static_cast<long long>(kMinTiles));
+  const long long before = block_prefix<kThreads>(mine, count, warp_sums, total, units);
+  const long long range = range_of<kMinTiles>(total, units);
   const long long begin = blockIdx.x * range, end = min(begin + range, total);
   if (begin >= before && begin < before + mine) {
     long long at = before;

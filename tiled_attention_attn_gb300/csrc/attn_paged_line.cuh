@@ -6,10 +6,13 @@
 
 namespace attn {
 
-// The sum of `mine` over the threads before this one, and over all of them.
-// Has one __syncthreads; warp_sums holds kThreads / 32 entries.
+// The sum of `mine` over the threads before this one, and the sums of `mine`
+// and of `units` over all of them.  Has one __syncthreads; warp_sums holds
+// 2 kThreads / 32 entries.
 template <int kThreads>
-__device__ __forceinline__ long long block_prefix(long long mine, long long* warp_sums, long long& total) {
+__device__ __forceinline__ long long block_prefix(long long mine, int units, long long* warp_sums, long long& total,
+                                                  long long& total_units) {
+  constexpr int kW = kThreads / 32;
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   long long incl = mine;
 #pragma unroll
@@ -17,16 +20,48 @@ __device__ __forceinline__ long long block_prefix(long long mine, long long* war
     const long long y = __shfl_up_sync(0xffffffffu, incl, o);
     if (lane >= o) incl += y;
   }
-  if (lane == 31) warp_sums[warp] = incl;
+  units = __reduce_add_sync(0xffffffffu, units);
+  if (lane == 31) {
+    warp_sums[warp] = incl;
+    warp_sums[kW + warp] = units;
+  }
   __syncthreads();
   long long before = incl - mine;
-  total = 0;
+  total = total_units = 0;
 #pragma unroll
-  for (int w = 0; w < kThreads / 32; ++w) {
+  for (int w = 0; w < kW; ++w) {
     if (w < warp) before += warp_sums[w];
     total += warp_sums[w];
+    total_units += warp_sums[kW + w];
   }
   return before;
+}
+
+// The length of a CTA's range: equal shares, but not below the mean unit, nor,
+// when units are longer than that, below kLeast: shorter pieces cost more than
+// they save (their merge, and a start each).  Units of up to kLeast are not
+// cut: they belong to the range that they start in.
+template <int kLeast>
+__device__ __forceinline__ long long range_of(long long total, long long units) {
+  const long long share = (total + gridDim.x - 1) / gridDim.x;
+  if (share >= kLeast) return share;
+  return max(share, min(static_cast<long long>(kLeast), units > 0 ? total / units : 1));
+}
+
+// A unit of n steps that starts at p on the line: the steps [t0, t1) that fall
+// to the range [begin, end); false where none does.  A unit of none falls to
+// the range that it starts in.
+template <int kLeast>
+__device__ __forceinline__ bool part_of(long long p, int n, long long begin, long long end, int& t0, int& t1) {
+  const long long lo = begin - p, hi = end - p;
+  if (n <= kLeast) {
+    t0 = 0;
+    t1 = n;
+    return lo <= 0 && hi > 0;
+  }
+  t0 = lo > 0 ? static_cast<int>(min(lo, static_cast<long long>(n))) : 0;
+  t1 = hi > 0 ? static_cast<int>(min(hi, static_cast<long long>(n))) : 0;
+  return t0 < t1;
 }
 
 // sum over i < n of floor((a i + b) / m), for a, b >= 0: the whole multiples of
