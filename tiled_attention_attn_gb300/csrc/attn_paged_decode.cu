@@ -46,9 +46,10 @@
 namespace attn {
 namespace pdec {
 
-constexpr int kThreads = 192;
-constexpr int kWarpTMA = 0;
+constexpr int kThreads = 224;
+constexpr int kWarpTMA = 0;    // loads Q and K
 constexpr int kWarpMMA = 1;
+constexpr int kWarpTMAV = 6;   // loads V
 constexpr int kKeys = 128;   // keys per tile
 constexpr int kNQ = 16;      // head columns
 constexpr int kStages = 3;
@@ -70,7 +71,7 @@ struct Cfg {
   static constexpr int kOffP = kOffQ + 2 * kQ;            // two P^T buffers
   static constexpr int kOffRed = kOffP + 2 * kP;          // [parity][warp][kNQ] floats
   static constexpr int kOffBar = kOffRed + 2 * 4 * kNQ * 4;
-  static constexpr int kNBars = 2 * kStages + 14;
+  static constexpr int kNBars = 3 * kStages + 14;
   static constexpr int kOffMisc = kOffBar + kNBars * 8;
   static constexpr int kSmem = kOffMisc + 256 + 1024;
   static_assert(kSmem <= 227 * 1024, "shared memory");
@@ -173,9 +174,10 @@ __global__ void __launch_bounds__(kThreads, 1) decode_kernel(const __grid_consta
   const uint32_t sK = sbase + C::kOffK, sV = sbase + C::kOffV, sQ = sbase + C::kOffQ, sP = sbase + C::kOffP;
   float* red = reinterpret_cast<float*>(smem + C::kOffRed);
   const uint32_t bar0 = sbase + C::kOffBar;
-  auto b_kv_full = [&](int s) { return bar0 + 8 * s; };
-  auto b_kv_empty = [&](int s) { return bar0 + 8 * (kStages + s); };
-  const uint32_t bar1 = bar0 + 8 * 2 * kStages;
+  auto b_k_full = [&](int s) { return bar0 + 8 * s; };
+  auto b_v_full = [&](int s) { return bar0 + 8 * (kStages + s); };
+  auto b_kv_empty = [&](int s) { return bar0 + 8 * (2 * kStages + s); };
+  const uint32_t bar1 = bar0 + 8 * 3 * kStages;
   auto b_q_full = [&](int s) { return bar1 + 8 * s; };
   auto b_q_empty = [&](int s) { return bar1 + 8 * (2 + s); };
   auto b_s_full = [&](int s) { return bar1 + 8 * (4 + s); };
@@ -198,7 +200,8 @@ __global__ void __launch_bounds__(kThreads, 1) decode_kernel(const __grid_consta
     *start_b = p.B;
     *start_p = 0;
     for (int s = 0; s < kStages; ++s) {
-      mbar_init(b_kv_full(s), 1);
+      mbar_init(b_k_full(s), 1);
+      mbar_init(b_v_full(s), 1);
       mbar_init(b_kv_empty(s), 1);
     }
     for (int s = 0; s < 2; ++s) {
@@ -271,16 +274,17 @@ __global__ void __launch_bounds__(kThreads, 1) decode_kernel(const __grid_consta
     w0.p += static_cast<long long>(w0.hc) * (w0.T + 1);
   }
 
-  if (warp == kWarpTMA) {
+  if (warp == kWarpTMA || warp == kWarpTMAV) {
     // ------------------------------------------------------------------ TMA producer
     uint32_t q_cnt = 0, kv_cnt = 0;
     const int box = min(1 << p.c.page_log2, kKeys);   // tokens per box
     const int n_pg = kKeys / box;                     // boxes along a tile
-    // this lane's box: page `pg` of a tile, chunk `ch`, of K or V
+    // this lane's box: page `pg` of a tile, chunk `ch`
     const int pg = lane % n_pg, ch = (lane / n_pg) & 1;
-    const bool of_v = lane >= 2 * n_pg, has = lane < 4 * n_pg;
+    const bool of_v = warp == kWarpTMAV, has = lane < 2 * n_pg;
     const CUtensorMap* map = of_v ? &p.tm_v : &p.tm_k;
     const uint32_t dst0 = (of_v ? sV : sK) + ch * kChunk + pg * box * 128;
+    auto b_full = [&](int s) { return of_v ? b_v_full(s) : b_k_full(s); };
     const int key_off = (kTPS == 1 ? 0 : ch * kKeys) + pg * box;
     const int col = kTPS == 1 ? ch * 64 : 0;
     auto page_at = [&](const Walk& w, int t) {   // the page of this lane's box in step t, -1: past the last key
@@ -293,16 +297,18 @@ __global__ void __launch_bounds__(kThreads, 1) decode_kernel(const __grid_consta
     bool ok = true;
     for (bool more = next_unit<KS>(p, w, true); more && ok; more = next_unit<KS>(p, w, false)) {
       if (w.t1 <= w.t0) continue;
-      const int qs = q_cnt & 1;
-      if (!mbar_wait_warp(b_q_empty(qs), ((q_cnt >> 1) & 1) ^ 1, wc, ATTN_DEVERR_WAIT_TIMEOUT_SITE(kSiteQEmpty))) break;
       const int g = w.hc / p.parts, part = w.hc - g * p.parts;
-      if (lane == 0) {
-        mbar_arrive_expect_tx(b_q_full(qs), (DA / 64) * p.heads * 128);
-        for (int c = 0; c < DA / 64; ++c)
-          tma_load_4d(sQ + qs * C::kQ + c * C::kQChunk, &p.tm_q, b_q_full(qs), c * 64, g * p.group + part * p.heads,
-                      w.b, 0);
+      if (!of_v) {
+        const int qs = q_cnt & 1;
+        if (!mbar_wait_warp(b_q_empty(qs), ((q_cnt >> 1) & 1) ^ 1, wc, ATTN_DEVERR_WAIT_TIMEOUT_SITE(kSiteQEmpty))) break;
+        if (lane == 0) {
+          mbar_arrive_expect_tx(b_q_full(qs), (DA / 64) * p.heads * 128);
+          for (int c = 0; c < DA / 64; ++c)
+            tma_load_4d(sQ + qs * C::kQ + c * C::kQChunk, &p.tm_q, b_q_full(qs), c * 64, g * p.group + part * p.heads,
+                        w.b, 0);
+        }
+        ++q_cnt;
       }
-      ++q_cnt;
       int page = page_at(w, w.t0);
       for (int t = w.t0; t < w.t1; ++t) {
         const int st = kv_cnt % kStages;
@@ -310,10 +316,10 @@ __global__ void __launch_bounds__(kThreads, 1) decode_kernel(const __grid_consta
         if (!mbar_wait_warp(b_kv_empty(st), ((kv_cnt / kStages) & 1) ^ 1, wc,
                             ATTN_DEVERR_WAIT_TIMEOUT_SITE(kSiteKEmpty))) { ok = false; break; }
         const uint32_t n_box = __popc(__ballot_sync(0xffffffffu, page >= 0));
-        if (lane == 0) mbar_arrive_expect_tx(b_kv_full(st), n_box * box * 128);
+        if (lane == 0) mbar_arrive_expect_tx(b_full(st), n_box * box * 128);
         __syncwarp();
         if (page >= 0)
-          tma_load_4d(dst0 + st * kTile, map, b_kv_full(st), col, g,
+          tma_load_4d(dst0 + st * kTile, map, b_full(st), col, g,
                       (t * KS + key_off) & ((1 << p.c.page_log2) - 1), page);
         page = next;
         ++kv_cnt;
@@ -323,7 +329,7 @@ __global__ void __launch_bounds__(kThreads, 1) decode_kernel(const __grid_consta
       // let the loads already issued land before the CTA exits
       for (int s = 0; s < kStages; ++s) {
         const uint32_t n = (kv_cnt + kStages - 1 - s) / kStages;
-        if (n > 0) mbar_wait(b_kv_full(s), (n - 1) & 1, wc, ATTN_DEVERR_WAIT_TIMEOUT_SITE(kSiteDrain), false);
+        if (n > 0) mbar_wait(b_full(s), (n - 1) & 1, wc, ATTN_DEVERR_WAIT_TIMEOUT_SITE(kSiteDrain), false);
       }
       for (int s = 0; s < 2; ++s) {
         const uint32_t n = (q_cnt + 1 - s) / 2;
@@ -340,7 +346,7 @@ __global__ void __launch_bounds__(kThreads, 1) decode_kernel(const __grid_consta
       const uint64_t dv0 = sdesc_sw128(sV, kChunk, 1024);
       const uint64_t dp0 = sdesc_sw128(sP, 16, 1024);
       const uint32_t t_u = tmem + 2 * kTPS * kNQ;   // u^T columns
-      uint32_t q_cnt = 0, kv_cnt = 0, s_cnt = 0, p_cnt = 0, units_done = 0;
+      uint32_t q_cnt = 0, kv_cnt = 0, v_cnt = 0, s_cnt = 0, p_cnt = 0, units_done = 0;
       bool ok = true;
       Walk w = w0;
       for (bool more = next_unit<KS>(p, w, true); more && ok; more = next_unit<KS>(p, w, false)) {
@@ -353,6 +359,8 @@ __global__ void __launch_bounds__(kThreads, 1) decode_kernel(const __grid_consta
         // and V) is released after it.  Before a unit's first product, which
         // overwrites u^T, the previous unit's epilogue must have read it
         auto do_pv = [&](int vst, int pb, bool first) -> bool {
+          if (!mbar_wait(b_v_full(vst), (v_cnt / kStages) & 1, wc, ATTN_DEVERR_WAIT_TIMEOUT_SITE(kSiteVFull))) return false;
+          ++v_cnt;
           if (!mbar_wait(b_p_full(pb), (p_cnt >> 1) & 1, wc, ATTN_DEVERR_WAIT_TIMEOUT_SITE(kSitePFull))) return false;
           ++p_cnt;
           if (first && units_done > 0 &&
@@ -374,7 +382,7 @@ __global__ void __launch_bounds__(kThreads, 1) decode_kernel(const __grid_consta
         for (int t = w.t0; t < w.t1; ++t) {
           const int st = kv_cnt % kStages;
           const int nt = kTPS == 1 ? 1 : (w.n - t * KS > kKeys ? 2 : 1);
-          if (!mbar_wait(b_kv_full(st), (kv_cnt / kStages) & 1, wc, ATTN_DEVERR_WAIT_TIMEOUT_SITE(kSiteKFull))) {
+          if (!mbar_wait(b_k_full(st), (kv_cnt / kStages) & 1, wc, ATTN_DEVERR_WAIT_TIMEOUT_SITE(kSiteKFull))) {
             ok = false;
             break;
           }
@@ -546,9 +554,9 @@ __global__ void __launch_bounds__(kThreads, 1) decode_kernel(const __grid_consta
         }
         if (t * KS + KS > w.n) {
           // the sequence's last step: rows of V past its last key become zero,
-          // once the stage's loads have landed (they have: its S is here)
+          // once the stage's V has landed
           const int st = steps_total % kStages;
-          if (!mbar_wait_warp(b_kv_full(st), (steps_total / kStages) & 1, wc,
+          if (!mbar_wait_warp(b_v_full(st), (steps_total / kStages) & 1, wc,
                               ATTN_DEVERR_WAIT_TIMEOUT_SITE(kSiteVFull))) { ok = false; break; }
 #pragma unroll
           for (int y = 0; y < 2; ++y)
