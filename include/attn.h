@@ -488,7 +488,8 @@ int attn_decode_paged(const void *q, void *o, float *lse, int B, int Hq, const a
  * {0, 1, ..., B}); a query with lse = -inf adds nothing.  weights (B,
  * num_kv_heads, weights_len) fp32, entries j >= seqlens_k[b] are left as they
  * are; decay = 0 does not read what was there.  weights_len at least
- * every seqlens_k[b] (a longer sequence is taken as bad).  cache->v is not
+ * every seqlens_k[b] (a longer sequence is taken as bad); scale 0 or at least
+ * 2^-20.  cache->v is not
  * read and may be null.  The sums' order depends on the lengths alone: the same
  * call gives the same bits.  workspace as above, for ATTN_PAGED_WEIGHTS.
  */

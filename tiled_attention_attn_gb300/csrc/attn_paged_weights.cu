@@ -12,6 +12,15 @@
 // query tile serves both key tiles, which halves what the ring draws from L2.
 // Each key tile has its warpgroup and two S^T buffers in TMEM.
 //
+// The lse is a column's, the same for all threads.  Read from shared memory it
+// costs as much of the 128 bytes a clock that an SM returns to registers as the
+// scores themselves (with TMEM's 64 KB a tile, 2,300 clocks a query tile).  So
+// the MMA subtracts it: K gets 16 more features (ALPHA, 1, 1, 0 ...), and a
+// query row -lse / scale in three pieces of the 16-bit type, each the rest that
+// the one before leaves (24 bits and more), times those.  One MMA more a tile,
+// and the thread's work is a multiplication, an exponential and an addition a
+// score.
+//
 // NT, the columns of a query tile: 128 for chunks; 16 when a sequence has few
 // rows (one token's heads), where a 128-row box would fetch mostly other
 // sequences' queries.  The sums are fp32 in a fixed order.
@@ -27,6 +36,7 @@
 #include <cuda_runtime.h>
 
 #include <cstdint>
+#include <type_traits>
 
 #include "attn_paged.h"
 #include "attn_paged_launch.h"
@@ -37,12 +47,15 @@
 namespace attn {
 namespace pwts {
 
-constexpr int kThr = 320;        // TMA warp, MMA warp, two warpgroups of four warps
-constexpr int kWTma = 0;
+// warps 0 and 2 load K (a key tile each), warp 1 issues the MMAs, warp 3 loads
+// Q, and the warps from kWSum sum
 constexpr int kWMma = 1;
+constexpr int kWQ = 3;
+constexpr int kWSum = 4;
 constexpr int kKeys = 256;       // keys per unit
 constexpr int kMinTiles = 4;     // pieces of a cut unit are at least about this long
 constexpr float kLog2e = 1.4426950408889634f;
+constexpr float kFar = 2.0e9f;     // exp2(-kFar scale log2 e) is 0 for every scale from 2^-20
 
 struct Params {
   CUtensorMap tm_q;    // (d, Hq, total, 1), box 64 x heads x span x 1
@@ -56,7 +69,10 @@ struct Params {
   int* err;
   unsigned long long timeout_ns;
   int B, Hq, total, len, group, heads, parts, span;
+  unsigned long long span_inv;   // ceil(2^40 / span)
   float scale_log2, decay;
+  float inv_scale;   // 1 / scale; 1 for scale 0 (then the products are left out)
+  int products;
 };
 
 struct Walk {
@@ -74,12 +90,20 @@ struct Line {
   __device__ int tokens(const Walk& w, int kb) const {
     return CAUSAL ? min(w.q_len, w.k_len - kb * kKeys) : w.q_len;
   }
-  __device__ int tiles(const Walk& w, int kb) const { return (tokens(w, kb) + p.span - 1) / p.span * p.parts; }
+  // x / span, exact below 2^32 / span: a multiplication, where the roles walk
+  // units a division of some 200 cycles would show
+  __device__ int by_span(int x) const { return static_cast<int>((static_cast<unsigned long long>(x) * p.span_inv) >> 40); }
+  __device__ int tiles(const Walk& w, int kb) const { return by_span(tokens(w, kb) + p.span - 1) * p.parts; }
   // cost of the units before kb of one head: query tiles, and one for K
   __device__ long long before(const Walk& w, int kb) const {
     if (kb <= 0) return 0;
-    const long long all = (w.q_len + p.span - 1) / p.span;
+    const long long all = by_span(w.q_len + p.span - 1);
     long long sum;
+    if (kb <= 32) {   // few: one by one, without the closed form's divisions
+      sum = kb;
+      for (int i = 0; i < kb; ++i) sum += tiles(w, i);
+      return sum;
+    }
     if (!CAUSAL) {
       sum = all * kb;
     } else {
@@ -136,11 +160,11 @@ struct Tiles {
   int part, tok, tok0, q_len, span;
   int tok_min[2];   // key tile x is seen by a tile that starts at tok >= tok_min[x]
   __device__ Tiles(const Params& p, const Walk& w, const Line<CAUSAL>& line) {
-    const int t = line.tokens(w, w.kb), per = (t + p.span - 1) / p.span;
+    const int per = line.by_span(line.tokens(w, w.kb) + p.span - 1);   // tiles of a head part
     span = p.span;
     q_len = w.q_len;
-    tok0 = w.q_len - t;
-    part = per > 0 ? w.t0 / per : 0;
+    tok0 = w.q_len - line.tokens(w, w.kb);
+    part = p.parts > 1 && per > 0 ? w.t0 / per : 0;
     tok = tok0 + (w.t0 - part * per) * p.span;
 #pragma unroll
     for (int x = 0; x < 2; ++x) {
@@ -159,6 +183,18 @@ struct Tiles {
   __device__ bool active(int x) const { return tok >= (x == 0 ? tok_min[0] : tok_min[1]); }
 };
 
+// Coefficient of the first piece of lse / scale: fp16 reaches 65504 times it.
+template <bool BF16>
+constexpr float kAlpha = BF16 ? 1.0f : 32768.0f;
+
+// Byte offset of row r of a tile of 16 features without swizzle: 8 x 16-byte
+// core matrices, the two of a row group side by side.
+__device__ __forceinline__ int lse_row(int r) { return (r >> 3) * 256 + (r & 7) * 16; }
+__device__ __forceinline__ uint64_t lse_desc(uint32_t saddr) {
+  return static_cast<uint64_t>((saddr & 0x3FFFFu) >> 4) | static_cast<uint64_t>(128 >> 4) << 16 |
+         static_cast<uint64_t>(256 >> 4) << 32 | static_cast<uint64_t>(1) << 46;
+}
+
 template <int D, int NT>
 struct WCfg {
   static constexpr int kChunks = D / 64;
@@ -169,78 +205,78 @@ struct WCfg {
   static constexpr int kQS = NT == 128 ? (D == 128 ? 2 : 4) : 4;
   static constexpr int kOffK = 0;
   static constexpr int kOffQ = kOffK + kKS * kKStage;
-  static constexpr int kOffL = kOffQ + kQS * kQStage;     // lse columns, times log2 e: [warp][parity][NT]
-  static constexpr int kOffBar = kOffL + 8 * 2 * NT * 4;
-  static constexpr int kNBars = 2 * kKS + 2 * kQS + 8 + 1;
+  static constexpr int kOffA = kOffQ + kQS * kQStage;     // the 16 more features: of the keys ...
+  static constexpr int kOffL = kOffA + 128 * 32;          // ... and of each stage's query rows
+  static constexpr int kThr = 32 * (kWSum + 8);
+  static constexpr int kOffBar = kOffL + kQS * NT * 32;
+  static constexpr int kNBars = 3 * kKS + 2 * kQS + 8 + 1;
   static constexpr int kOffMisc = kOffBar + (kNBars + 1) / 2 * 16;
-  static constexpr int kSmem = kOffMisc + 256 + 1024;
+  static constexpr int kSmem = kOffMisc + 384 + 1024;   // (2 sums a warp from kOffMisc + 32)
   static constexpr uint32_t kTmemCols = 4 * NT;           // [key tile][buffer]
   static_assert(kSmem <= 227 * 1024, "shared memory");
 };
 
-// Adds exp2(s c - lse) of CB columns to sum; MASK drops those before column
-// c_lo - c0 and those whose lse is +inf, whatever their score.
+// Adds exp2(c (s - lse / scale)) of CB columns to sum; MASK drops those outside
+// [lo, hi), whatever their score.
 template <int CB, bool MASK>
-__device__ __forceinline__ void add_columns(const uint32_t (&r)[CB], const float* ls, float2 c2, int lim, float2 (&sum)[2]) {
+__device__ __forceinline__ void add_columns(const uint32_t (&r)[CB], float2 c2, int lo, int hi, float2 (&sum)[2]) {
 #pragma unroll
   for (int k = 0; k < CB; k += 4) {
-    const float4 l4 = *reinterpret_cast<const float4*>(ls + k);
-    const float2 a = ffma2(make_float2(__uint_as_float(r[k]), __uint_as_float(r[k + 1])), c2, make_float2(-l4.x, -l4.y));
-    const float2 b = ffma2(make_float2(__uint_as_float(r[k + 2]), __uint_as_float(r[k + 3])), c2, make_float2(-l4.z, -l4.w));
+    const float2 a = fmul2(make_float2(__uint_as_float(r[k]), __uint_as_float(r[k + 1])), c2);
+    const float2 b = fmul2(make_float2(__uint_as_float(r[k + 2]), __uint_as_float(r[k + 3])), c2);
     float2 e0 = make_float2(ex2_approx(a.x), ex2_approx(a.y));
     float2 e1 = make_float2(ex2_approx(b.x), ex2_approx(b.y));
     if constexpr (MASK) {
-      e0.x = (k >= lim && l4.x != INFINITY) ? e0.x : 0.0f;
-      e0.y = (k + 1 >= lim && l4.y != INFINITY) ? e0.y : 0.0f;
-      e1.x = (k + 2 >= lim && l4.z != INFINITY) ? e1.x : 0.0f;
-      e1.y = (k + 3 >= lim && l4.w != INFINITY) ? e1.y : 0.0f;
+      e0.x = (k >= lo && k < hi) ? e0.x : 0.0f;
+      e0.y = (k + 1 >= lo && k + 1 < hi) ? e0.y : 0.0f;
+      e1.x = (k + 2 >= lo && k + 2 < hi) ? e1.x : 0.0f;
+      e1.y = (k + 3 >= lo && k + 3 < hi) ? e1.y : 0.0f;
     }
     sum[0] = fadd2(sum[0], e0);
     sum[1] = fadd2(sum[1], e1);
   }
 }
 
-// One S^T tile's columns of this thread's key; the next columns load while
+// The columns of an S^T tile, of this thread's key; the next ones load while
 // these are added.
 template <int NT, bool MASK, class Release>
-__device__ __forceinline__ void add_tile(uint32_t t_s, const float* ls, float2 c2, int c_lo, float2 (&sum)[2],
-                                         Release release) {
+__device__ __forceinline__ void add_tile(uint32_t t_s, float2 c2, int lo, int hi, float2 (&sum)[2], Release release) {
   if constexpr (NT == 16) {
     uint32_t r[16];
     tmem_ld_32x32b_x16(t_s, r);
     tmem_wait_ld(r);
     release();
-    add_columns<16, MASK>(r, ls, c2, c_lo, sum);
+    add_columns<16, MASK>(r, c2, lo, hi, sum);
   } else {
     uint32_t r0[32], r1[32];
     tmem_ld_32x32b_x32(t_s, r0);
     tmem_wait_ld(r0);
-    tmem_ld_32x32b_x32(t_s + 32, r1);
-    add_columns<32, MASK>(r0, ls, c2, c_lo, sum);
-    tmem_wait_ld(r1);
-    tmem_ld_32x32b_x32(t_s + 64, r0);
-    add_columns<32, MASK>(r1, ls + 32, c2, c_lo - 32, sum);
-    tmem_wait_ld(r0);
-    tmem_ld_32x32b_x32(t_s + 96, r1);
-    add_columns<32, MASK>(r0, ls + 64, c2, c_lo - 64, sum);
-    tmem_wait_ld(r1);
-    release();
-    add_columns<32, MASK>(r1, ls + 96, c2, c_lo - 96, sum);
+#pragma unroll
+    for (int c0 = 0; c0 < NT; c0 += 64) {
+      tmem_ld_32x32b_x32(t_s + c0 + 32, r1);
+      add_columns<32, MASK>(r0, c2, lo - c0, hi - c0, sum);
+      tmem_wait_ld(r1);
+      if (c0 + 64 < NT) tmem_ld_32x32b_x32(t_s + c0 + 64, r0);
+      else release();
+      add_columns<32, MASK>(r1, c2, lo - c0 - 32, hi - c0 - 32, sum);
+      if (c0 + 64 < NT) tmem_wait_ld(r0);
+    }
   }
 }
 
 template <int D, int NT, bool BF16, bool CAUSAL>
-__global__ void __launch_bounds__(kThr, 1) weights_kernel(const __grid_constant__ Params p) {
+__global__ void __launch_bounds__(WCfg<D, NT>::kThr, 1) weights_kernel(const __grid_constant__ Params p) {
   using C = WCfg<D, NT>;
+  constexpr int kThr = C::kThr;
   extern __shared__ __align__(1024) uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const uint32_t sbase = smem_u32(smem);
   const uint32_t sK = sbase + C::kOffK, sQ = sbase + C::kOffQ;
   const uint32_t bar0 = sbase + C::kOffBar;
-  auto b_k_full = [&](int s) { return bar0 + 8 * s; };
-  auto b_k_empty = [&](int s) { return bar0 + 8 * (C::kKS + s); };
-  const uint32_t bar1 = bar0 + 16 * C::kKS;
+  auto b_k_full = [&](int x, int s) { return bar0 + 8 * (x * C::kKS + s); };
+  auto b_k_empty = [&](int s) { return bar0 + 8 * (2 * C::kKS + s); };
+  const uint32_t bar1 = bar0 + 24 * C::kKS;
   auto b_q_full = [&](int s) { return bar1 + 8 * s; };
   auto b_q_empty = [&](int s) { return bar1 + 8 * (C::kQS + s); };
   const uint32_t bar2 = bar1 + 16 * C::kQS;
@@ -258,22 +294,23 @@ __global__ void __launch_bounds__(kThr, 1) weights_kernel(const __grid_constant_
     *abort_flag = 0;
     start[0] = p.B;
     for (int s = 0; s < C::kKS; ++s) {
-      mbar_init(b_k_full(s), 1);
+      mbar_init(b_k_full(0, s), 1);
+      mbar_init(b_k_full(1, s), 1);
       mbar_init(b_k_empty(s), 1);
     }
     for (int s = 0; s < C::kQS; ++s) {
-      mbar_init(b_q_full(s), 1);
+      mbar_init(b_q_full(s), 2);   // the tile, and its lse features
       mbar_init(b_q_empty(s), 1);
     }
     for (int x = 0; x < 2; ++x)
       for (int s = 0; s < 2; ++s) {
         mbar_init(b_s_full(x, s), 1);
-        mbar_init(b_s_free(x, s), 4);   // the four warps of the key tile
+        mbar_init(b_s_free(x, s), 4);   // the warps that read the buffer
       }
     mbar_init(b_drain, 1);
     fence_mbar_init();
   }
-  if (warp == kWTma && lane == 0) {
+  if (warp == 0 && lane == 0) {
     tma_prefetch_desc(&p.tm_q);
     tma_prefetch_desc(&p.tm_k);
   }
@@ -281,6 +318,19 @@ __global__ void __launch_bounds__(kThr, 1) weights_kernel(const __grid_constant_
     tmem_alloc(smem_u32(tmem_slot), C::kTmemCols);
     tmem_relinquish();
   }
+
+  // the features that take the lse: (ALPHA, 1, 1, 0 ...) for every key; of the
+  // query rows only the first three change
+  using T = typename std::conditional<BF16, __nv_bfloat16, __half>::type;
+  for (int i = tid; i < 128; i += kThr) {
+    const T a(kAlpha<BF16>), one(1.0f), zero(0.0f);
+    T f[8] = {a, one, one, zero, zero, zero, zero, zero};
+    *reinterpret_cast<uint4*>(smem + C::kOffA + lse_row(i)) = *reinterpret_cast<const uint4*>(f);
+    *reinterpret_cast<uint4*>(smem + C::kOffA + lse_row(i) + 128) = make_uint4(0, 0, 0, 0);
+  }
+  for (int i = tid; i < C::kQS * NT * 2; i += kThr)
+    reinterpret_cast<uint4*>(smem + C::kOffL)[i] = make_uint4(0, 0, 0, 0);
+  fence_proxy_async_smem();
 
   const Line<CAUSAL> line{p};
   Walk w0;
@@ -338,14 +388,14 @@ __global__ void __launch_bounds__(kThr, 1) weights_kernel(const __grid_constant_
     w0.n = line.tiles(w0, w0.kb);
   }
 
-  if (warp == kWTma) {
-    // ------------------------------------------------------------------ TMA producer
-    uint32_t k_cnt = 0, q_cnt = 0;
+  if (warp == 0 || warp == 2) {
+    // ------------------------------------------------------------------ TMA producer of key tile x
+    const int x = warp >> 1;
+    uint32_t k_cnt = 0;
     const int box = min(1 << p.c.page_log2, 128);   // tokens per box
-    const int n_pg = 128 / box;                     // boxes along a key tile
-    // this lane's box of K: key tile x, feature chunk, page
-    const int pg = lane % n_pg, ch = (lane / n_pg) % C::kChunks, x = lane / (n_pg * C::kChunks);
-    const bool has = lane < 2 * C::kChunks * n_pg;
+    const int n_pg = 128 / box;                     // boxes along the tile
+    const int pg = lane % n_pg, ch = lane / n_pg;   // this lane's box: page, feature chunk
+    const bool has = lane < C::kChunks * n_pg;
     const uint32_t dst0 = sK + x * C::kKTile + ch * 16384 + pg * box * 128;
     // the page of this lane's box of a unit, -1: none to load
     auto page_of = [&](const Walk& u) {
@@ -355,9 +405,9 @@ __global__ void __launch_bounds__(kThr, 1) weights_kernel(const __grid_constant_
       return id < 0 ? p.c.num_pages : id;   // no page: rows past the pool read as zeros
     };
     Walk w = w0, ahead;   // the next unit, whose page is read while this one is issued
-    bool ok = true, more = line.next(w, true), more_ahead = false;
+    bool more = line.next(w, true), more_ahead = false;
     int page = more ? page_of(w) : -1, page_ahead = -1;
-    for (; more && ok; w = ahead, more = more_ahead, page = page_ahead) {
+    for (; more; w = ahead, more = more_ahead, page = page_ahead) {
       ahead = w;
       more_ahead = line.next(ahead, false);
       page_ahead = more_ahead ? page_of(ahead) : -1;
@@ -366,32 +416,72 @@ __global__ void __launch_bounds__(kThr, 1) weights_kernel(const __grid_constant_
       const int ks = k_cnt % C::kKS;
       if (!mbar_wait_warp(b_k_empty(ks), ((k_cnt / C::kKS) & 1) ^ 1, wc, ATTN_DEVERR_WAIT_TIMEOUT_SITE(kSiteKEmpty))) break;
       const uint32_t n_box = __popc(__ballot_sync(0xffffffffu, page >= 0));
-      if (lane == 0) mbar_arrive_expect_tx(b_k_full(ks), n_box * box * 128);
+      if (lane == 0) mbar_arrive_expect_tx(b_k_full(x, ks), n_box * box * 128);
       __syncwarp();
       if (page >= 0)
-        tma_load_4d(dst0 + ks * C::kKStage, &p.tm_k, b_k_full(ks), ch * 64, w.g, key & ((1 << p.c.page_log2) - 1), page);
+        tma_load_4d(dst0 + ks * C::kKStage, &p.tm_k, b_k_full(x, ks), ch * 64, w.g, key & ((1 << p.c.page_log2) - 1), page);
       ++k_cnt;
-      Tiles<CAUSAL> it(p, w, line);
-      for (int i = w.t0; i < w.t1; ++i, it.next()) {
-        const int qs = q_cnt % C::kQS;
-        if (!mbar_wait_warp(b_q_empty(qs), ((q_cnt / C::kQS) & 1) ^ 1, wc,
-                            ATTN_DEVERR_WAIT_TIMEOUT_SITE(kSiteQEmpty))) { ok = false; break; }
-        if (lane == 0) {
-          mbar_arrive_expect_tx(b_q_full(qs), C::kChunks * p.heads * p.span * 128);
-#pragma unroll
-          for (int c = 0; c < C::kChunks; ++c)
-            tma_load_4d(sQ + qs * C::kQStage + c * NT * 128, &p.tm_q, b_q_full(qs), c * 64,
-                        w.g * p.group + it.part * p.heads, w.row_q + it.tok, 0);
-        }
-        ++q_cnt;
-      }
     }
     if (lane == 0 && *abort_flag) {
       // let the loads already issued land before the CTA exits
       for (int s = 0; s < C::kKS; ++s) {
         const uint32_t n = (k_cnt + C::kKS - 1 - s) / C::kKS;
-        if (n > 0) mbar_wait(b_k_full(s), (n - 1) & 1, wc, ATTN_DEVERR_WAIT_TIMEOUT_SITE(kSiteDrain), false);
+        if (n > 0) mbar_wait(b_k_full(x, s), (n - 1) & 1, wc, ATTN_DEVERR_WAIT_TIMEOUT_SITE(kSiteDrain), false);
       }
+    }
+  } else if (warp == kWQ) {
+    // ------------------------------------------------------------------ query tiles and their lse features
+    constexpr int NC = (NT + 31) / 32;   // lane's rows are lane, lane + 32, ...
+    int row_tok[NC], row_head[NC];
+#pragma unroll
+    for (int k = 0; k < NC; ++k) {
+      row_tok[k] = (lane + 32 * k) / p.heads;
+      row_head[k] = lane + 32 * k - row_tok[k] * p.heads;
+    }
+    uint32_t q_cnt = 0;
+    bool ok = true;
+    Walk w = w0;
+    for (bool more = line.next(w, true); more && ok; more = line.next(w, false)) {
+      Tiles<CAUSAL> it(p, w, line);
+      for (int i = w.t0; i < w.t1; ++i, it.next()) {
+        const int qs = q_cnt % C::kQS, head0 = w.g * p.group + it.part * p.heads, row0 = w.row_q + it.tok;
+        float l[NC];   // on its way while the stage is waited for
+#pragma unroll
+        for (int k = 0; k < NC; ++k) {
+          l[k] = -INFINITY;
+          if (lane + 32 * k < NT && row_tok[k] < p.span && it.tok + row_tok[k] < w.q_len)
+            l[k] = __ldg(p.lse + static_cast<long long>(head0 + row_head[k]) * p.total + row0 + row_tok[k]);
+        }
+        if (!mbar_wait_warp(b_q_empty(qs), ((q_cnt / C::kQS) & 1) ^ 1, wc, ATTN_DEVERR_WAIT_TIMEOUT_SITE(kSiteQEmpty))) {
+          ok = false;
+          break;
+        }
+        if (lane == 0) {
+          mbar_arrive_expect_tx(b_q_full(qs), C::kChunks * p.heads * p.span * 128);
+#pragma unroll
+          for (int c = 0; c < C::kChunks; ++c)
+            tma_load_4d(sQ + qs * C::kQStage + c * NT * 128, &p.tm_q, b_q_full(qs), c * 64, head0, row0, 0);
+        }
+#pragma unroll
+        for (int k = 0; k < NC; ++k) {
+          // -lse / scale, within what the pieces hold; no query, or one that saw no key: far below
+          const float v = l[k] == -INFINITY ? -kFar : fminf(fmaxf(-l[k] * p.inv_scale, -kFar), kFar);
+          const T p0 = T(v * (1.0f / kAlpha<BF16>));
+          const float r1 = l[k] != l[k] ? l[k] : v - static_cast<float>(p0) * kAlpha<BF16>;
+          const T p1 = T(r1);
+          const T p2 = T(r1 - static_cast<float>(p1));
+          T f[4] = {p0, p1, p2, T(0.0f)};
+          if (lane + 32 * k < NT)
+            *reinterpret_cast<uint2*>(smem + C::kOffL + qs * NT * 32 + lse_row(lane + 32 * k)) = *reinterpret_cast<const uint2*>(f);
+        }
+        fence_proxy_async_smem();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(b_q_full(qs));
+        ++q_cnt;
+      }
+    }
+    if (lane == 0 && *abort_flag) {
+      // let the loads already issued land before the CTA exits
       for (int s = 0; s < C::kQS; ++s) {
         const uint32_t n = (q_cnt + C::kQS - 1 - s) / C::kQS;
         if (n > 0) mbar_wait(b_q_full(s), (n - 1) & 1, wc, ATTN_DEVERR_WAIT_TIMEOUT_SITE(kSiteDrain), false);
@@ -403,13 +493,16 @@ __global__ void __launch_bounds__(kThr, 1) weights_kernel(const __grid_constant_
       constexpr uint32_t kIdesc = idesc_f16_f32acc(128, NT, BF16, false);
       const uint64_t dk0 = sdesc_sw128(sK, 16, 1024);
       const uint64_t dq0 = sdesc_sw128(sQ, 16, 1024);
+      const uint64_t da0 = lse_desc(sbase + C::kOffA), dl0 = lse_desc(sbase + C::kOffL);
       uint32_t k_cnt = 0, q_cnt = 0, s_cnt[2] = {0, 0};
       bool ok = true;
       Walk w = w0;
       for (bool more = line.next(w, true); more && ok; more = line.next(w, false)) {
         if (w.t1 <= w.t0) continue;
         const int ks = k_cnt % C::kKS;
-        if (!mbar_wait(b_k_full(ks), (k_cnt / C::kKS) & 1, wc, ATTN_DEVERR_WAIT_TIMEOUT_SITE(kSiteKFull))) break;
+        if (!mbar_wait(b_k_full(0, ks), (k_cnt / C::kKS) & 1, wc, ATTN_DEVERR_WAIT_TIMEOUT_SITE(kSiteKFull)) ||
+            !mbar_wait(b_k_full(1, ks), (k_cnt / C::kKS) & 1, wc, ATTN_DEVERR_WAIT_TIMEOUT_SITE(kSiteKFull)))
+          break;
         ++k_cnt;
         Tiles<CAUSAL> it(p, w, line);
         for (int i = w.t0; i < w.t1 && ok; ++i, it.next()) {
@@ -429,12 +522,17 @@ __global__ void __launch_bounds__(kThr, 1) weights_kernel(const __grid_constant_
             }
             ++s_cnt[x];
             tc_fence_after();
+            // the products, then -lse / scale: the larger accumulator last, as every
+            // addition of the tensor core truncates to fp32
+            if (p.products) {
 #pragma unroll
-            for (int kk = 0; kk < D / 16; ++kk) {
-              const uint64_t a = dk0 + ((ks * C::kKStage + x * C::kKTile + (kk >> 2) * 16384 + (kk & 3) * 32) >> 4);
-              const uint64_t b = dq0 + ((qs * C::kQStage + (kk >> 2) * NT * 128 + (kk & 3) * 32) >> 4);
-              umma_ss(tmem + (2 * x + sb) * NT, a, b, kIdesc, kk > 0 ? 1u : 0u);
+              for (int kk = 0; kk < D / 16; ++kk) {
+                const uint64_t a = dk0 + ((ks * C::kKStage + x * C::kKTile + (kk >> 2) * 16384 + (kk & 3) * 32) >> 4);
+                const uint64_t b = dq0 + ((qs * C::kQStage + (kk >> 2) * NT * 128 + (kk & 3) * 32) >> 4);
+                umma_ss(tmem + (2 * x + sb) * NT, a, b, kIdesc, kk > 0 ? 1u : 0u);
+              }
             }
+            umma_ss(tmem + (2 * x + sb) * NT, da0, dl0 + ((qs * NT * 32) >> 4), kIdesc, p.products ? 1u : 0u);
             umma_commit(b_s_full(x, sb));
           }
           umma_commit(b_q_empty(qs));
@@ -446,89 +544,58 @@ __global__ void __launch_bounds__(kThr, 1) weights_kernel(const __grid_constant_
       mbar_wait(b_drain, 0, wc, ATTN_DEVERR_WAIT_TIMEOUT_SITE(kSiteDrain), false);
     }
   } else {
-    // ------------------------------------------------------------------ one warpgroup per key tile
-    const int x = (warp - 2) >> 2;
+    // ------------------------------------------------------------------ sums: one warpgroup per key tile
+    const int x = (warp - kWSum) >> 2;
     const int quarter = warp & 3;
     const int lrow = quarter * 32 + lane;   // TMEM lane: key of the tile
     const uint32_t t_s = tmem + (static_cast<uint32_t>(quarter * 32) << 16) + 2 * x * NT;
-    // each warp keeps the tile's lse columns for itself: lane's columns are
-    // lane, lane + 32, ...
-    float* lse_s = reinterpret_cast<float*>(smem + C::kOffL) + (warp - 2) * 2 * NT;
-    constexpr int NC = (NT + 31) / 32;
-    int col_tok[NC], col_head[NC];
-    long long col_at[NC];
-#pragma unroll
-    for (int k = 0; k < NC; ++k) {
-      col_tok[k] = (lane + 32 * k) / p.heads;
-      col_head[k] = lane + 32 * k - col_tok[k] * p.heads;
-      col_at[k] = static_cast<long long>(col_head[k]) * p.total + col_tok[k];
-    }
     const float2 c2 = make_float2(p.scale_log2, p.scale_log2);
     uint32_t s_cnt = 0;
-    Walk w = w0;
     bool ok = true;
-    for (bool more = line.next(w, true); more && ok; more = line.next(w, false)) {
-      const int key = w.kb * kKeys + x * 128 + lrow;
+    auto out_of = [&](const Walk& u) {
+      return p.weights + (static_cast<long long>(u.b) * p.c.hkv + u.g) * p.len + u.kb * kKeys + x * 128 + lrow;
+    };
+    auto old_of = [&](const Walk& u) {
+      return p.decay != 0.0f && u.t1 - u.t0 == u.n && u.kb * kKeys + x * 128 + lrow < u.k_len ? *out_of(u) : 0.0f;
+    };
+    Walk w = w0, ahead;   // the next unit, whose old weights are read while this one is summed
+    bool more = line.next(w, true), more_ahead = false;
+    float old = more ? old_of(w) : 0.0f, old_ahead = 0.0f;
+    for (; more && ok; w = ahead, more = more_ahead, old = old_ahead) {
+      ahead = w;
+      more_ahead = line.next(ahead, false);
+      if (more_ahead) old_ahead = old_of(ahead);
+      const int key = w.kb * kKeys + x * 128 + lrow, off = w.k_len - w.q_len;
       float2 sum[2] = {make_float2(0.0f, 0.0f), make_float2(0.0f, 0.0f)};
       Tiles<CAUSAL> it(p, w, line);
-      // this lane's lse columns of the query tile at `f`, -inf where the column
-      // is no query; used a tile later, so that the loads are hidden
-      auto load_lse = [&](const Tiles<CAUSAL>& f, float (&l)[NC]) {
-        const int n_heads = min(p.heads, p.group - f.part * p.heads);
-        const float* base = p.lse + static_cast<long long>(w.g * p.group + f.part * p.heads) * p.total + w.row_q + f.tok;
-#pragma unroll
-        for (int k = 0; k < NC; ++k) {
-          l[k] = -INFINITY;
-          if (lane + 32 * k < NT && col_tok[k] < p.span && col_head[k] < n_heads && f.tok + col_tok[k] < w.q_len)
-            l[k] = __ldg(base + col_at[k]);
-        }
-      };
-      float l_next[NC];
-      if (w.t0 < w.t1) load_lse(it, l_next);
-      const bool whole = w.t1 - w.t0 == w.n;
-      float* out = p.weights + (static_cast<long long>(w.b) * p.c.hkv + w.g) * p.len + key;
-      const bool mine = whole && key < w.k_len;
-      const float old = mine && p.decay != 0.0f ? *out : 0.0f;
-      for (int i = w.t0; i < w.t1; ++i) {
+      for (int i = w.t0; i < w.t1; ++i, it.next()) {
+        if (!it.active(x)) continue;
         const int sb = s_cnt & 1;
-        const bool act = it.active(x);
-        const int tok = it.tok, n_heads = min(p.heads, p.group - it.part * p.heads);
-        float* ls = lse_s + sb * NT;   // its last readers are two tiles back
-        if (act) {
-#pragma unroll
-          for (int k = 0; k < NC; ++k)
-            if (lane + 32 * k < NT) ls[lane + 32 * k] = l_next[k] == -INFINITY ? INFINITY : l_next[k] * kLog2e;
-        }
-        it.next();
-        if (i + 1 < w.t1) load_lse(it, l_next);
-        if (!act) continue;
-        __syncwarp();
         if (!mbar_wait_warp(b_s_full(x, sb), (s_cnt >> 1) & 1, wc, ATTN_DEVERR_WAIT_TIMEOUT_SITE(kSiteSFull))) {
           ok = false;
           break;
         }
         ++s_cnt;
         tc_fence_after();
-        // columns this key sees: from c_lo (causal), those that are queries
-        int c_lo = 0;
-        if (CAUSAL) c_lo = max(0, (key - (w.k_len - w.q_len) - tok)) * p.heads;
-        const bool full = (!CAUSAL || w.kb * kKeys + x * 128 + 127 - (w.k_len - w.q_len) <= tok) &&
-                          tok + p.span <= w.q_len && n_heads == p.heads && p.heads * p.span == NT;
+        // columns this key sees: from c_lo (causal) to the chunk's end
+        const int c_lo = CAUSAL ? max(0, key - off - it.tok) * p.heads : 0;
+        const int c_hi = min(p.span, w.q_len - it.tok) * p.heads;
+        const bool full = (!CAUSAL || w.kb * kKeys + x * 128 + 127 - off <= it.tok) && c_hi == NT;
         auto release = [&] {   // the scores are in registers: the buffer may be overwritten
           tc_fence_before();
           __syncwarp();
           if (lane == 0) mbar_arrive(b_s_free(x, sb));
         };
-        if (full) add_tile<NT, false>(t_s + sb * NT, ls, c2, c_lo, sum, release);
-        else add_tile<NT, true>(t_s + sb * NT, ls, c2, c_lo, sum, release);
+        if (full) add_tile<NT, false>(t_s + sb * NT, c2, 0, NT, sum, release);
+        else add_tile<NT, true>(t_s + sb * NT, c2, c_lo, c_hi, sum, release);
       }
       if (!ok) break;
       const float s = (sum[0].x + sum[0].y) + (sum[1].x + sum[1].y);
-      if (whole) {
-        if (mine) *out = p.decay * old + s;
+      if (w.t1 - w.t0 == w.n) {
+        if (key < w.k_len) *out_of(w) = p.decay * old + s;
       } else {
         p.part[(2 * blockIdx.x + (w.t0 == 0 ? 1 : 0)) * kKeys + x * 128 + lrow] = s;
-        if (w.t0 == 0 && warp == 2 && lane == 0)
+        if (w.t0 == 0 && warp == kWSum && lane == 0)
           p.rec[blockIdx.x] = make_int4(w.b, w.g, w.kb,
                                         static_cast<int>((w.p + w.n - 1) / range) - static_cast<int>(blockIdx.x) + 1);
       }
@@ -569,7 +636,7 @@ cudaError_t launch(const Params& p, int grid, cudaStream_t stream) {
     if (e != cudaSuccess) return e;
     if (dev >= 0 && dev < 64) attr_done[dev] = true;
   }
-  weights_kernel<D, NT, BF16, CAUSAL><<<grid, kThr, smem, stream>>>(p);
+  weights_kernel<D, NT, BF16, CAUSAL><<<grid, WCfg<D, NT>::kThr, smem, stream>>>(p);
   e = cudaGetLastError();
   if (e != cudaSuccess) return e;
   cudaLaunchConfig_t cfg = {};
@@ -607,10 +674,11 @@ int paged_weights(const void* q, const float* lse, float* weights, int weights_l
   // few rows per sequence: tiles of 16 columns
   const bool few = static_cast<long long>(total) * p.group <= 16LL * B;
   const int nt = few ? 16 : 128;
-  p.parts = (p.group + nt - 1) / nt;
-  p.heads = (p.group + p.parts - 1) / p.parts;
-  p.parts = (p.group + p.heads - 1) / p.heads;
+  // equal parts of a group, so that every row of a tile is a query head of it
+  for (p.heads = p.group < nt ? p.group : nt; p.group % p.heads != 0;) --p.heads;
+  p.parts = p.group / p.heads;
   p.span = nt / p.heads;
+  p.span_inv = ((1ull << 40) + p.span - 1) / p.span;
   // with no rows at all nothing is loaded through the map
   const int rows = total > 0 ? total : 1;
   if (int rc = tile_map(q, bf16, d, Hq, rows, 1, d, static_cast<long long>(Hq) * d,
@@ -630,7 +698,9 @@ int paged_weights(const void* q, const float* lse, float* weights, int weights_l
   p.Hq = Hq;
   p.total = total;
   p.len = weights_len;
-  p.scale_log2 = scale * pwts::kLog2e;
+  p.products = scale > 0.0f;
+  p.inv_scale = scale > 0.0f ? 1.0f / scale : 1.0f;
+  p.scale_log2 = (scale > 0.0f ? scale : 1.0f) * pwts::kLog2e;
   p.decay = decay;
   cudaError_t e;
   if (d == 64) e = few ? pwts::pick<64, 16>(p, bf16, causal, sms, stream) : pwts::pick<64, 128>(p, bf16, causal, sms, stream);
