@@ -93,6 +93,7 @@ struct Params {
   int* err;
   unsigned long long timeout_ns;
   int B, Hq, group, heads, parts;   // heads per unit; units per key/value head
+  int cuts;            // the table can hold a unit long enough to be cut
   float scale_log2;
 };
 
@@ -738,7 +739,8 @@ cudaError_t launch(const Params& p, int grid, cudaStream_t stream) {
   }
   decode_kernel<GT, BF16, DA><<<grid, kThreads, smem, stream>>>(p);
   e = cudaGetLastError();
-  if (e != cudaSuccess) return e;
+  count_launch();
+  if (e != cudaSuccess || !p.cuts) return e;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(grid, p.heads);
   cfg.blockDim = dim3(128);
@@ -748,6 +750,7 @@ cudaError_t launch(const Params& p, int grid, cudaStream_t stream) {
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
+  count_launch();
   return cudaLaunchKernelEx(&cfg, decode_merge_kernel<BF16, DA>, p);
 }
 
@@ -796,14 +799,12 @@ int paged_decode(const void* q, void* o, float* lse, int B, int Hq, const PagedK
   p.timeout_ns = wait_timeout_ns();
   p.B = B;
   p.Hq = Hq;
+  p.cuts = (c.max_pages << c.page_log2) > pdec::kMinSteps * (d == 64 ? 256 : 128);
   p.scale_log2 = scale * 1.4426950408889634f;
   cudaError_t e;
   if (d == 64) e = bf16 ? pdec::pick<true, 64>(p, sms, stream) : pdec::pick<false, 64>(p, sms, stream);
   else e = bf16 ? pdec::pick<true, 128>(p, sms, stream) : pdec::pick<false, 128>(p, sms, stream);
-  if (e != cudaSuccess) return ATTN_ELAUNCH;
-  count_launch();
-  count_launch();
-  return ATTN_OK;
+  return e == cudaSuccess ? ATTN_OK : ATTN_ELAUNCH;
 }
 
 }  // namespace attn

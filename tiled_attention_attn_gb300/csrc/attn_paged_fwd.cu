@@ -58,6 +58,7 @@ struct Params {
   int B, Hq, total, group;
   int heads, parts;    // query heads per unit, units per key/value head
   int span;            // tokens per sub-tile
+  int cuts;            // the table can hold a unit long enough to be cut
   float scale_log2;
 };
 
@@ -673,7 +674,8 @@ cudaError_t launch(const Params& p, int grid, cudaStream_t stream) {
   }
   fwd_kernel<D, BF16, CAUSAL><<<grid, kThreads, smem, stream>>>(p);
   e = cudaGetLastError();
-  if (e != cudaSuccess) return e;
+  count_launch();
+  if (e != cudaSuccess || !p.cuts) return e;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(grid, kNSub, D / 64);
   cfg.blockDim = dim3(4 * kBM);
@@ -683,6 +685,7 @@ cudaError_t launch(const Params& p, int grid, cudaStream_t stream) {
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
+  count_launch();
   return cudaLaunchKernelEx(&cfg, fwd_merge_kernel<D, BF16>, p);
 }
 
@@ -724,6 +727,7 @@ int paged_fwd(const void* q, void* o, float* lse, int B, int Hq, int total, cons
   p.B = B;
   p.Hq = Hq;
   p.total = total;
+  p.cuts = (c.max_pages << c.page_log2) > pfwd::kMinTiles * kBN;
   p.scale_log2 = scale * 1.4426950408889634f;
   cudaError_t e;
   if (d == 64) {
@@ -733,10 +737,7 @@ int paged_fwd(const void* q, void* o, float* lse, int B, int Hq, int total, cons
     if (causal) e = bf16 ? pfwd::launch<128, true, true>(p, sms, stream) : pfwd::launch<128, false, true>(p, sms, stream);
     else e = bf16 ? pfwd::launch<128, true, false>(p, sms, stream) : pfwd::launch<128, false, false>(p, sms, stream);
   }
-  if (e != cudaSuccess) return ATTN_ELAUNCH;
-  count_launch();
-  count_launch();
-  return ATTN_OK;
+  return e == cudaSuccess ? ATTN_OK : ATTN_ELAUNCH;
 }
 
 }  // namespace attn

@@ -71,6 +71,7 @@ struct Params {
   int B, Hq, total, len, group, heads, parts, span;
   unsigned long long span_inv;   // ceil(2^40 / span)
   float scale_log2, decay;
+  int cuts;          // the chunk can be long enough for a unit to be cut
   float inv_scale;   // 1 / scale; 1 for scale 0 (then the products are left out)
   int products;
 };
@@ -638,7 +639,8 @@ cudaError_t launch(const Params& p, int grid, cudaStream_t stream) {
   }
   weights_kernel<D, NT, BF16, CAUSAL><<<grid, WCfg<D, NT>::kThr, smem, stream>>>(p);
   e = cudaGetLastError();
-  if (e != cudaSuccess) return e;
+  count_launch();
+  if (e != cudaSuccess || !p.cuts) return e;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(grid);
   cfg.blockDim = dim3(kKeys);
@@ -648,6 +650,7 @@ cudaError_t launch(const Params& p, int grid, cudaStream_t stream) {
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
+  count_launch();
   return cudaLaunchKernelEx(&cfg, weights_merge_kernel, p);
 }
 
@@ -698,6 +701,7 @@ int paged_weights(const void* q, const float* lse, float* weights, int weights_l
   p.Hq = Hq;
   p.total = total;
   p.len = weights_len;
+  p.cuts = static_cast<long long>((total + p.span - 1) / p.span) * p.parts > pwts::kMinTiles;
   p.products = scale > 0.0f;
   p.inv_scale = scale > 0.0f ? 1.0f / scale : 1.0f;
   p.scale_log2 = (scale > 0.0f ? scale : 1.0f) * pwts::kLog2e;
@@ -705,10 +709,7 @@ int paged_weights(const void* q, const float* lse, float* weights, int weights_l
   cudaError_t e;
   if (d == 64) e = few ? pwts::pick<64, 16>(p, bf16, causal, sms, stream) : pwts::pick<64, 128>(p, bf16, causal, sms, stream);
   else e = few ? pwts::pick<128, 16>(p, bf16, causal, sms, stream) : pwts::pick<128, 128>(p, bf16, causal, sms, stream);
-  if (e != cudaSuccess) return ATTN_ELAUNCH;
-  count_launch();
-  count_launch();
-  return ATTN_OK;
+  return e == cudaSuccess ? ATTN_OK : ATTN_ELAUNCH;
 }
 
 }  // namespace attn

@@ -86,7 +86,7 @@ def _stream(device: torch.device) -> int:
 
 
 def _check_int(t: torch.Tensor, name: str, device, shape) -> None:
-    if t.dtype != torch.int32 or t.device != device or not t.is_contiguous() or tuple(t.shape) != tuple(shape):
+    if t.dtype != torch.int32 or t.device != device or not t.is_contiguous() or t.shape != shape:
         raise ValueError(f"{name} must be a contiguous int32 tensor of shape {tuple(shape)} on {device}")
 
 
@@ -97,27 +97,28 @@ def _check_rc(rc: int, what: str) -> None:
 
 def _cache(k_pages: torch.Tensor, v_pages: Optional[torch.Tensor], page_table: torch.Tensor,
            seqlens_k: torch.Tensor) -> _PagedKV:
-    dev = k_pages.device
-    if k_pages.dtype not in _HALF:
+    dev, dtype, shape, strides = k_pages.device, k_pages.dtype, k_pages.shape, k_pages.stride()
+    if dtype not in _HALF:
         raise TypeError("k_pages and v_pages must be bfloat16 or float16")
-    if dev.type != "cuda" or k_pages.dim() != 4 or k_pages.stride(3) != 1:
+    if dev.type != "cuda" or len(shape) != 4 or strides[3] != 1:
         raise ValueError("k_pages is a CUDA tensor (num_pages, page_size, Hkv, d) with contiguous features")
+    v = None
     if v_pages is not None:
-        if v_pages.dtype != k_pages.dtype:
+        if v_pages.dtype != dtype:
             raise TypeError("k_pages and v_pages must share one dtype")
-        if v_pages.device != dev or v_pages.shape != k_pages.shape or v_pages.stride() != k_pages.stride():
+        if v_pages.device != dev or v_pages.shape != shape or v_pages.stride() != strides:
             raise ValueError("v_pages must be laid out like k_pages")
+        v = v_pages.data_ptr()
     if page_table.dtype != torch.int32 or page_table.device != dev or page_table.dim() != 2 or page_table.stride(1) != 1:
         raise ValueError("page_table must be an int32 CUDA tensor (B, max_pages) with contiguous rows")
     B, max_pages = page_table.shape
     _check_int(seqlens_k, "seqlens_k", dev, (B,))
-    n, P, hkv, d = k_pages.shape
-    sp, st, sh, _ = k_pages.stride()
+    n, P, hkv, d = shape
+    sp, st, sh, _ = strides
     # strides of an axis of one entry address nothing: any valid value serves
     sp, sh = sp if n > 1 else max(8, d), sh if hkv > 1 else max(8, d)
-    ts = page_table.stride(0) if B > 1 else max_pages
-    return _PagedKV(k_pages.data_ptr(), v_pages.data_ptr() if v_pages is not None else None, page_table.data_ptr(),
-                    seqlens_k.data_ptr(), sp, st, sh, ts, max_pages, n, P, hkv, d, int(k_pages.dtype == torch.float16))
+    return _PagedKV(k_pages.data_ptr(), v, page_table.data_ptr(), seqlens_k.data_ptr(), sp, st, sh,
+                    page_table.stride(0) if B > 1 else max_pages, max_pages, n, P, hkv, d, int(dtype == torch.float16))
 
 
 def _check_q(q: torch.Tensor, c: _PagedKV, k_pages: torch.Tensor) -> None:
@@ -341,11 +342,13 @@ def _workspace(device: torch.device, d: int, call: int) -> torch.Tensor:
 
 def _outputs(q, out, lse):
     T, Hq, _ = q.shape
-    out = torch.empty_like(q) if out is None else out
-    lse = torch.empty((Hq, T), dtype=torch.float32, device=q.device) if lse is None else lse
-    if out.shape != q.shape or out.dtype != q.dtype or out.device != q.device or not out.is_contiguous():
+    if out is None:
+        out = torch.empty_like(q)
+    elif out.shape != q.shape or out.dtype != q.dtype or out.device != q.device or not out.is_contiguous():
         raise ValueError("out must be a contiguous tensor shaped like q")
-    if tuple(lse.shape) != (Hq, T) or lse.dtype != torch.float32 or lse.device != q.device or not lse.is_contiguous():
+    if lse is None:
+        lse = torch.empty((Hq, T), dtype=torch.float32, device=q.device)
+    elif lse.shape != (Hq, T) or lse.dtype != torch.float32 or lse.device != q.device or not lse.is_contiguous():
         raise ValueError(f"lse must be a contiguous float32 tensor of shape {(Hq, T)}")
     return out, lse
 
@@ -414,7 +417,7 @@ def key_weights(q: torch.Tensor, k_pages: torch.Tensor, lse: torch.Tensor, page_
     B, dev = page_table.shape[0], q.device
     _check_int(cu_seqlens, "cu_seqlens", dev, (B + 1,))
     T, Hq, d = q.shape
-    if tuple(lse.shape) != (Hq, T) or lse.dtype != torch.float32 or lse.device != dev or not lse.is_contiguous():
+    if lse.shape != (Hq, T) or lse.dtype != torch.float32 or lse.device != dev or not lse.is_contiguous():
         raise ValueError(f"lse must be a contiguous float32 tensor of shape {(Hq, T)}")
     if scale is None:
         scale = 1.0 / math.sqrt(d)
