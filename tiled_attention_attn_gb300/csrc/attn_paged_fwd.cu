@@ -595,13 +595,13 @@ __global__ void __launch_bounds__(kThreads, 1) fwd_kernel(const __grid_constant_
 }
 
 // Joins the pieces of the unit that block x's CTA began: M = max m_s, w_s =
-// 2^(m_s - M) l_s, O = sum w_s O_s / sum w_s.  Block (CTA, sub-tile, 64
-// columns), one thread per row and 16 columns; a programmatic dependent of the
-// forward.
+// 2^(m_s - M) l_s, O = sum w_s O_s / sum w_s.  Block (CTA, sub-tile, 32
+// columns), one thread per row and 16 columns, two pieces (the usual count) in
+// flight; a programmatic dependent of the forward.
 template <int D, bool BF16>
-__global__ void __launch_bounds__(4 * kBM) fwd_merge_kernel(const __grid_constant__ Params p) {
+__global__ void __launch_bounds__(2 * kBM, 4) fwd_merge_kernel(const __grid_constant__ Params p) {
   using T = typename IO<BF16>::T;
-  const int c0 = blockIdx.x, t = blockIdx.y, cb = blockIdx.z * 4 + threadIdx.x / kBM, row = threadIdx.x % kBM;
+  const int c0 = blockIdx.x, t = blockIdx.y, cb = blockIdx.z * 2 + threadIdx.x / kBM, row = threadIdx.x % kBM;
   grid_wait_prerequisites();
   const int4 rec = __ldcg(p.rec + c0);
   const int pieces = rec.w;
@@ -612,36 +612,41 @@ __global__ void __launch_bounds__(4 * kBM) fwd_merge_kernel(const __grid_constan
   const int qrow = (2 * rec.z + t) * p.span + r_tok;
   const int g = rec.y / p.parts, part = rec.y - g * p.parts;
   if (r_tok >= p.span || qrow >= q_len || r_head >= p.group - part * p.heads) return;
-  const float2* ml = reinterpret_cast<const float2*>(p.part_ml);
+  // piece s of this row: the first on the CTA's slot for a unit that goes on,
+  // the others on the next CTAs' slots for one that came
+  const float2* ml = reinterpret_cast<const float2*>(p.part_ml) + row;
   auto slot = [&](int s) { return static_cast<size_t>(s == 0 ? 2 * c0 + 1 : 2 * (c0 + s)) * kNSub + t; };
-  float M = -INFINITY, L = 0.0f, acc[16];
+  float M = -INFINITY;
+#pragma unroll 4
+  for (int s = 0; s < pieces; ++s) M = fmaxf(M, __ldcg(ml + slot(s) * kBM).x);
+  float L = 0.0f, acc[16];
 #pragma unroll
   for (int i = 0; i < 16; ++i) acc[i] = 0.0f;
-  for (int s0 = 0; s0 < pieces; s0 += 4) {
-    float2 mlv[4];
-    float4 x[4][4];
+  if (M != -INFINITY) {
+    for (int s0 = 0; s0 < pieces; s0 += 2) {
+      float2 mlv[2];
+      float4 x[2][4];
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {   // four pieces in flight
-      const bool in = s0 + i < pieces;
-      const size_t sl = slot(in ? s0 + i : 0);
-      mlv[i] = in ? __ldcg(ml + sl * kBM + row) : make_float2(-INFINITY, 0.0f);
+      for (int i = 0; i < 2; ++i) {
+        const bool in = s0 + i < pieces;
+        const size_t sl = slot(in ? s0 + i : 0);
+        mlv[i] = in ? __ldcg(ml + sl * kBM) : make_float2(-INFINITY, 0.0f);
 #pragma unroll
-      for (int c = 0; c < 4; ++c)
-        x[i][c] = in ? __ldcg(p.part_o + (sl * (D / 4) + cb * 4 + c) * kBM + row) : make_float4(0, 0, 0, 0);
-    }
+        for (int c = 0; c < 4; ++c)
+          x[i][c] = in ? __ldcg(p.part_o + (sl * (D / 4) + cb * 4 + c) * kBM + row) : make_float4(0, 0, 0, 0);
+      }
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      if (mlv[i].x == -INFINITY) continue;   // a piece that saw no key (its O_s was never written)
-      const float mn = fmaxf(M, mlv[i].x);
-      const float r = (M == -INFINITY) ? 0.0f : ex2_approx(M - mn), wt = ex2_approx(mlv[i].x - mn) * mlv[i].y;
-      M = mn;
-      L = L * r + wt;
+      for (int i = 0; i < 2; ++i) {
+        if (mlv[i].x == -INFINITY) continue;   // a piece that saw no key (its O_s was never written)
+        const float wt = ex2_approx(mlv[i].x - M) * mlv[i].y;
+        L += wt;
 #pragma unroll
-      for (int c = 0; c < 4; ++c) {
-        acc[4 * c] = acc[4 * c] * r + wt * x[i][c].x;
-        acc[4 * c + 1] = acc[4 * c + 1] * r + wt * x[i][c].y;
-        acc[4 * c + 2] = acc[4 * c + 2] * r + wt * x[i][c].z;
-        acc[4 * c + 3] = acc[4 * c + 3] * r + wt * x[i][c].w;
+        for (int c = 0; c < 4; ++c) {
+          acc[4 * c] += wt * x[i][c].x;
+          acc[4 * c + 1] += wt * x[i][c].y;
+          acc[4 * c + 2] += wt * x[i][c].z;
+          acc[4 * c + 3] += wt * x[i][c].w;
+        }
       }
     }
   }
@@ -677,8 +682,8 @@ cudaError_t launch(const Params& p, int grid, cudaStream_t stream) {
   count_launch();
   if (e != cudaSuccess || !p.cuts) return e;
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(grid, kNSub, D / 64);
-  cfg.blockDim = dim3(4 * kBM);
+  cfg.gridDim = dim3(grid, kNSub, D / 32);
+  cfg.blockDim = dim3(2 * kBM);
   cfg.stream = stream;
   cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
