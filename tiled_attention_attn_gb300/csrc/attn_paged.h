@@ -50,14 +50,17 @@ inline int paged_check(const attn_paged_kv* c, int B, bool need_v, PagedKV& out)
 }
 
 #if defined(__CUDACC__)
-// Keys of sequence b: 0 (and the error recorded) when out of range.
-__device__ __forceinline__ int paged_len(const PagedKV& c, int b, int* err) {
-  const int n = __ldg(c.seqlens + b);
+// A key count as it was read: 0 (and the error recorded) when out of range.
+__device__ __forceinline__ int checked_len(const PagedKV& c, int n, int* err) {
   if (n < 0 || n > (c.max_pages << c.page_log2)) {
     atomicCAS(err, 0, ATTN_DEVERR_BAD_SEQLENS);
     return 0;
   }
   return n;
+}
+// Keys of sequence b.
+__device__ __forceinline__ int paged_len(const PagedKV& c, int b, int* err) {
+  return checked_len(c, __ldg(c.seqlens + b), err);
 }
 // Page i of sequence b, or -1 (and the error recorded) when it is not one.
 __device__ __forceinline__ int paged_page(const PagedKV& c, int b, int i, int* err) {
@@ -78,6 +81,19 @@ __device__ __forceinline__ int chunk_len(const int* cu, int b, int total, int& r
     return 0;
   }
   return e - a;
+}
+// New tokens and keys of sequence b: all three reads on their way before any
+// is looked at.
+__device__ __forceinline__ void chunk_and_keys(const PagedKV& c, const int* cu, int b, int total, int& q_len, int& row,
+                                               int& k_len, int* err) {
+  const int a = __ldg(cu + b), e = __ldg(cu + b + 1), n = __ldg(c.seqlens + b);
+  row = a;
+  q_len = e - a;
+  if (a < 0 || e < a || e > total) {
+    atomicCAS(err, 0, ATTN_DEVERR_BAD_SEQLENS);
+    q_len = 0;
+  }
+  k_len = checked_len(c, n, err);
 }
 #endif
 

@@ -99,8 +99,7 @@ struct Line {
     return sum;
   }
   __device__ void load(Walk& w) const {
-    w.q_len = chunk_len(p.cu, w.b, p.total, w.row_q, p.err);
-    w.k_len = paged_len(p.c, w.b, p.err);
+    chunk_and_keys(p.c, p.cu, w.b, p.total, w.q_len, w.row_q, w.k_len, p.err);
     w.n_mb = (w.q_len + tok() - 1) / tok();
   }
   __device__ long long cost(const Walk& w) const { return before(w, w.n_mb) * units_per_block(); }

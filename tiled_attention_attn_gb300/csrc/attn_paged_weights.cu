@@ -47,11 +47,13 @@
 namespace attn {
 namespace pwts {
 
-// warps 0 and 2 load K (a key tile each), warp 1 issues the MMAs, warp 3 loads
-// Q, and the warps from kWSum sum
-constexpr int kWMma = 1;
+// warps 0 and 2 load K and warps 1 and 4 issue the MMAs (a key tile each: with
+// one token a sequence, a unit is one tile of 9 small MMAs per key tile, and one
+// issuer's waits and walk over units were what it took: 57 -> 48 us), warp 3
+// loads Q, and the warps from kWSum sum
+constexpr int kWMma = 1, kWMma1 = 4;
 constexpr int kWQ = 3;
-constexpr int kWSum = 4;
+constexpr int kWSum = 5;
 constexpr int kKeys = 256;       // keys per unit
 constexpr int kMinTiles = 4;     // pieces of a cut unit are at least about this long
 constexpr float kLog2e = 1.4426950408889634f;
@@ -117,8 +119,7 @@ struct Line {
     return sum * p.parts + kb;
   }
   __device__ void load(Walk& w) const {
-    w.q_len = chunk_len(p.cu, w.b, p.total, w.row_q, p.err);
-    w.k_len = paged_len(p.c, w.b, p.err);
+    chunk_and_keys(p.c, p.cu, w.b, p.total, w.q_len, w.row_q, w.k_len, p.err);
     if (w.k_len > p.len) {
       atomicCAS(p.err, 0, ATTN_DEVERR_BAD_SEQLENS);
       w.k_len = 0;
@@ -210,7 +211,7 @@ struct WCfg {
   static constexpr int kOffL = kOffA + 128 * 32;          // ... and of each stage's query rows
   static constexpr int kThr = 32 * (kWSum + 8);
   static constexpr int kOffBar = kOffL + kQS * NT * 32;
-  static constexpr int kNBars = 3 * kKS + 2 * kQS + 8 + 1;
+  static constexpr int kNBars = 3 * kKS + 2 * kQS + 8 + 2;
   static constexpr int kOffMisc = kOffBar + (kNBars + 1) / 2 * 16;
   static constexpr int kSmem = kOffMisc + 384 + 1024;   // (2 sums a warp from kOffMisc + 32)
   static constexpr uint32_t kTmemCols = 4 * NT;           // [key tile][buffer]
@@ -283,7 +284,7 @@ __global__ void __launch_bounds__(WCfg<D, NT>::kThr, 1) weights_kernel(const __g
   const uint32_t bar2 = bar1 + 16 * C::kQS;
   auto b_s_full = [&](int x, int s) { return bar2 + 8 * (2 * x + s); };
   auto b_s_free = [&](int x, int s) { return bar2 + 32 + 8 * (2 * x + s); };
-  const uint32_t b_drain = bar2 + 64;
+  auto b_drain = [&](int x) { return bar2 + 64 + 8 * x; };
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + C::kOffMisc);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + C::kOffMisc + 4);
   volatile int* start = reinterpret_cast<volatile int*>(smem + C::kOffMisc + 8);   // b, g, kb
@@ -297,18 +298,19 @@ __global__ void __launch_bounds__(WCfg<D, NT>::kThr, 1) weights_kernel(const __g
     for (int s = 0; s < C::kKS; ++s) {
       mbar_init(b_k_full(0, s), 1);
       mbar_init(b_k_full(1, s), 1);
-      mbar_init(b_k_empty(s), 1);
+      mbar_init(b_k_empty(s), 2);   // the two issuers
     }
     for (int s = 0; s < C::kQS; ++s) {
       mbar_init(b_q_full(s), 2);   // the tile, and its lse features
-      mbar_init(b_q_empty(s), 1);
+      mbar_init(b_q_empty(s), 2);
     }
     for (int x = 0; x < 2; ++x)
       for (int s = 0; s < 2; ++s) {
         mbar_init(b_s_full(x, s), 1);
         mbar_init(b_s_free(x, s), 4);   // the warps that read the buffer
       }
-    mbar_init(b_drain, 1);
+    mbar_init(b_drain(0), 1);
+    mbar_init(b_drain(1), 1);
     fence_mbar_init();
   }
   if (warp == 0 && lane == 0) {
@@ -488,24 +490,35 @@ __global__ void __launch_bounds__(WCfg<D, NT>::kThr, 1) weights_kernel(const __g
         if (n > 0) mbar_wait(b_q_full(s), (n - 1) & 1, wc, ATTN_DEVERR_WAIT_TIMEOUT_SITE(kSiteDrain), false);
       }
     }
-  } else if (warp == kWMma) {
-    // ------------------------------------------------------------------ MMA issuer
+  } else if (warp == kWMma || warp == kWMma1) {
+    // ------------------------------------------------------------------ MMA issuer of key tile x
+    const int x = warp == kWMma1 ? 1 : 0;
     if (lane == 0) {
       constexpr uint32_t kIdesc = idesc_f16_f32acc(128, NT, BF16, false);
       const uint64_t dk0 = sdesc_sw128(sK, 16, 1024);
       const uint64_t dq0 = sdesc_sw128(sQ, 16, 1024);
       const uint64_t da0 = lse_desc(sbase + C::kOffA), dl0 = lse_desc(sbase + C::kOffL);
-      uint32_t k_cnt = 0, q_cnt = 0, s_cnt[2] = {0, 0};
+      uint32_t k_cnt = 0, q_cnt = 0, s_cnt = 0;
       bool ok = true;
-      Walk w = w0;
-      for (bool more = line.next(w, true); more && ok; more = line.next(w, false)) {
-        if (w.t1 <= w.t0) continue;
+      // the next unit and its tiles, worked out while the tensor core is busy
+      // with this one's first tile
+      Walk w = w0, ahead;
+      bool more = line.next(w, true), more_ahead = false;
+      ahead = w;
+      Tiles<CAUSAL> it(p, w, line), it_ahead = it;
+      for (; more && ok; w = ahead, it = it_ahead, more = more_ahead) {
+        auto look_ahead = [&] {
+          ahead = w;
+          more_ahead = line.next(ahead, false);
+          if (more_ahead) it_ahead = Tiles<CAUSAL>(p, ahead, line);
+        };
+        if (w.t1 <= w.t0) {
+          look_ahead();
+          continue;
+        }
         const int ks = k_cnt % C::kKS;
-        if (!mbar_wait(b_k_full(0, ks), (k_cnt / C::kKS) & 1, wc, ATTN_DEVERR_WAIT_TIMEOUT_SITE(kSiteKFull)) ||
-            !mbar_wait(b_k_full(1, ks), (k_cnt / C::kKS) & 1, wc, ATTN_DEVERR_WAIT_TIMEOUT_SITE(kSiteKFull)))
-          break;
+        if (!mbar_wait(b_k_full(x, ks), (k_cnt / C::kKS) & 1, wc, ATTN_DEVERR_WAIT_TIMEOUT_SITE(kSiteKFull))) break;
         ++k_cnt;
-        Tiles<CAUSAL> it(p, w, line);
         for (int i = w.t0; i < w.t1 && ok; ++i, it.next()) {
           const int qs = q_cnt % C::kQS;
           if (!mbar_wait(b_q_full(qs), (q_cnt / C::kQS) & 1, wc, ATTN_DEVERR_WAIT_TIMEOUT_SITE(kSiteQFull))) {
@@ -513,15 +526,13 @@ __global__ void __launch_bounds__(WCfg<D, NT>::kThr, 1) weights_kernel(const __g
             break;
           }
           ++q_cnt;
-#pragma unroll
-          for (int x = 0; x < 2; ++x) {
-            if (!it.active(x)) continue;
-            const int sb = s_cnt[x] & 1;
-            if (!mbar_wait(b_s_free(x, sb), ((s_cnt[x] >> 1) & 1) ^ 1, wc, ATTN_DEVERR_WAIT_TIMEOUT_SITE(kSiteSFree))) {
+          if (it.active(x)) {
+            const int sb = s_cnt & 1;
+            if (!mbar_wait(b_s_free(x, sb), ((s_cnt >> 1) & 1) ^ 1, wc, ATTN_DEVERR_WAIT_TIMEOUT_SITE(kSiteSFree))) {
               ok = false;
               break;
             }
-            ++s_cnt[x];
+            ++s_cnt;
             tc_fence_after();
             // the products, then -lse / scale: the larger accumulator last, as every
             // addition of the tensor core truncates to fp32
@@ -537,12 +548,12 @@ __global__ void __launch_bounds__(WCfg<D, NT>::kThr, 1) weights_kernel(const __g
             umma_commit(b_s_full(x, sb));
           }
           umma_commit(b_q_empty(qs));
+          if (i == w.t1 - 1) umma_commit(b_k_empty(ks));
+          if (i == w.t0) look_ahead();
         }
-        if (!ok) break;
-        umma_commit(b_k_empty(ks));
       }
-      umma_commit(b_drain);
-      mbar_wait(b_drain, 0, wc, ATTN_DEVERR_WAIT_TIMEOUT_SITE(kSiteDrain), false);
+      umma_commit(b_drain(x));
+      mbar_wait(b_drain(x), 0, wc, ATTN_DEVERR_WAIT_TIMEOUT_SITE(kSiteDrain), false);
     }
   } else {
     // ------------------------------------------------------------------ sums: one warpgroup per key tile
