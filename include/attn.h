@@ -363,7 +363,10 @@ int attn_rotary_packed(const void *x, void *y, int B, int L, int h_total, int h_
  *                 are read; the others may hold anything.
  *   seqlens_k     int32 (B): keys of each sequence, 0 .. max_pages * page_size.
  * What lies in the pages past a sequence's last key is never used, whatever
- * its value (a NaN included).
+ * its value (a NaN included).  A key that the causal mask hides from a query
+ * does not reach that query's softmax, whatever its score; its value is
+ * weighted by zero, so a key that some query of the chunk sees needs finite
+ * values.
  *
  * The host reads neither array.  A sequence whose key count is out of range
  * is taken as having no keys, and ATTN_DEVERR_BAD_SEQLENS is recorded; a page
@@ -413,7 +416,7 @@ typedef struct attn_paged_kv {
  *       B = 1, L = rows).
  * The angle is reduced to a fraction of a turn in 64-bit fixed point before
  * the sine and cosine in fp32, so it is as exact at position 2^31 as near 0.
- * Returns ATTN_OK, ATTN_EINVAL or ATTN_ELAUNCH.
+ * Returns ATTN_OK, ATTN_EINVAL, ATTN_EUNSUPPORTED (device) or ATTN_ELAUNCH.
  */
 int attn_rotary_scaled(const void *x, void *y, int B, int L, int H, int d, int rot_dim, const double *freqs,
                        float amplitude, int interleaved, int inverse, long long x_stride_token,

@@ -4,6 +4,9 @@ lengths, groups, page sizes, layouts and masks where they can go wrong.
 Tolerances are derived in paged_reference."""
 
 import math
+import os
+import subprocess
+import sys
 
 import pytest
 import torch
@@ -467,6 +470,37 @@ def test_two_streams_and_two_graphs():
         for a, b in zip(want, outs):
             assert all(torch.equal(x, y) for x, y in zip(a[:4], b[:4]))
     ok()
+
+
+def test_the_first_call_of_a_process_is_captured():
+    # nothing of the library has run before the capture
+    script = """
+import torch
+from tests.paged_reference import Cache, check_attention, cu_of
+from tiled_attention_attn_gb300 import attn
+c = Cache([3000, 70], 2, 64, 32, torch.float16, seed=1)
+q = torch.randn(42, 4, 64, generator=torch.Generator().manual_seed(1)).half().cuda()
+cu = cu_of([40, 2])
+f, a = attn.rotary_freqs(64)
+torch.cuda.synchronize()
+gr = torch.cuda.CUDAGraph()
+with torch.cuda.graph(gr):
+    r = attn.cache_append(q[:, :2], q[:, 2:], *c.args(), cu, q=q, freqs=f, amplitude=a)
+    o, lse = attn.attn_fwd_paged(r, *c.args(), cu)
+    o2, lse2 = attn.attn_decode_paged(r[:2], *c.args())
+    w = attn.key_weights(r, c.k, lse, c.table, c.seqlens, cu)
+for _ in range(2):
+    gr.replay()
+torch.cuda.synchronize()
+assert attn.get_error() == 0
+check_attention(o, lse, r, c, [40, 2], True, 0.125)
+check_attention(o2, lse2, r[:2], c, [1, 1], True, 0.125)
+assert abs(float(w.double().sum()) - 42 * 4) < 1e-2
+print("done")
+"""
+    root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+    r = subprocess.run([sys.executable, "-c", script], cwd=root, capture_output=True, text=True, timeout=300)
+    assert r.returncode == 0 and "done" in r.stdout, r.stdout + r.stderr
 
 
 def test_the_same_inputs_give_the_same_bits():

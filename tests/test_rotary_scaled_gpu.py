@@ -123,6 +123,18 @@ def test_gradient_of_an_expanded_output_and_of_packed_rows():
     ref.check_turn(x.grad[:14], one, pos, f, a, False, -1.0)
 
 
+def test_gradient_of_the_gradient():
+    # the operator is linear: d/dx of <R^T dy, e> with respect to dy is R e
+    f, a = attn.rotary_freqs(64, scaling="ntk", factor=4.0)
+    x = rand(1, 21, 2, 64, dtype=HF).requires_grad_()
+    dy = rand(1, 21, 2, 64, dtype=HF, seed=3).requires_grad_()
+    e = rand(1, 21, 2, 64, dtype=HF, seed=4)
+    g, = torch.autograd.grad(attn.rotary_scaled_func(x, f, a), x, dy, create_graph=True)
+    gg, = torch.autograd.grad(g, dy, e)
+    torch.cuda.synchronize()
+    ref.check_turn(gg.view(21, 2, 64), e.view(21, 2, 64), torch.arange(21).cuda(), f, a, False)
+
+
 def test_backward_in_a_graph_beside_an_eager_one():
     f, a = attn.rotary_freqs(64, scaling="linear", factor=2.0)
     x = rand(1, 40, 2, 64, dtype=BF).requires_grad_()

@@ -739,8 +739,9 @@ cudaError_t launch(const Params& p, int grid, cudaStream_t stream) {
   }
   decode_kernel<GT, BF16, DA><<<grid, kThreads, smem, stream>>>(p);
   e = cudaGetLastError();
+  if (e != cudaSuccess) return e;
   count_launch();
-  if (e != cudaSuccess || !p.cuts) return e;
+  if (!p.cuts) return cudaSuccess;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(grid, p.heads);
   cfg.blockDim = dim3(128);
@@ -750,8 +751,9 @@ cudaError_t launch(const Params& p, int grid, cudaStream_t stream) {
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  count_launch();
-  return cudaLaunchKernelEx(&cfg, decode_merge_kernel<BF16, DA>, p);
+  e = cudaLaunchKernelEx(&cfg, decode_merge_kernel<BF16, DA>, p);
+  if (e == cudaSuccess) count_launch();
+  return e;
 }
 
 template <bool BF16, int DA>

@@ -678,8 +678,9 @@ cudaError_t launch(const Params& p, int grid, cudaStream_t stream) {
   }
   fwd_kernel<D, BF16, CAUSAL><<<grid, kThreads, smem, stream>>>(p);
   e = cudaGetLastError();
+  if (e != cudaSuccess) return e;
   count_launch();
-  if (e != cudaSuccess || !p.cuts) return e;
+  if (!p.cuts) return cudaSuccess;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(grid, kNSub, D / 32);
   cfg.blockDim = dim3(2 * kBM);
@@ -689,8 +690,9 @@ cudaError_t launch(const Params& p, int grid, cudaStream_t stream) {
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  count_launch();
-  return cudaLaunchKernelEx(&cfg, fwd_merge_kernel<D, BF16>, p);
+  e = cudaLaunchKernelEx(&cfg, fwd_merge_kernel<D, BF16>, p);
+  if (e == cudaSuccess) count_launch();
+  return e;
 }
 
 size_t rec_bytes(int sms) { return (static_cast<size_t>(sms) * sizeof(int4) + 255) / 256 * 256; }

@@ -71,7 +71,7 @@ struct Params {
   int* err;
   unsigned long long timeout_ns;
   int B, Hq, total, len, group, heads, parts, span;
-  unsigned long long span_inv;   // ceil(2^40 / span)
+  unsigned long long span_inv;   // ceil(2^64 / span), span > 1
   float scale_log2, decay;
   int cuts;          // the chunk can be long enough for a unit to be cut
   float inv_scale;   // 1 / scale; 1 for scale 0 (then the products are left out)
@@ -93,9 +93,9 @@ struct Line {
   __device__ int tokens(const Walk& w, int kb) const {
     return CAUSAL ? min(w.q_len, w.k_len - kb * kKeys) : w.q_len;
   }
-  // x / span, exact below 2^32 / span: a multiplication, where the roles walk
+  // x / span, exact for every 32-bit x: a multiplication, where the roles walk
   // units a division of some 200 cycles would show
-  __device__ int by_span(int x) const { return static_cast<int>((static_cast<unsigned long long>(x) * p.span_inv) >> 40); }
+  __device__ int by_span(int x) const { return p.span == 1 ? x : static_cast<int>(__umul64hi(x, p.span_inv)); }
   __device__ int tiles(const Walk& w, int kb) const { return by_span(tokens(w, kb) + p.span - 1) * p.parts; }
   // cost of the units before kb of one head: query tiles, and one for K
   __device__ long long before(const Walk& w, int kb) const {
@@ -650,8 +650,9 @@ cudaError_t launch(const Params& p, int grid, cudaStream_t stream) {
   }
   weights_kernel<D, NT, BF16, CAUSAL><<<grid, WCfg<D, NT>::kThr, smem, stream>>>(p);
   e = cudaGetLastError();
+  if (e != cudaSuccess) return e;
   count_launch();
-  if (e != cudaSuccess || !p.cuts) return e;
+  if (!p.cuts) return cudaSuccess;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(grid);
   cfg.blockDim = dim3(kKeys);
@@ -661,8 +662,9 @@ cudaError_t launch(const Params& p, int grid, cudaStream_t stream) {
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  count_launch();
-  return cudaLaunchKernelEx(&cfg, weights_merge_kernel, p);
+  e = cudaLaunchKernelEx(&cfg, weights_merge_kernel, p);
+  if (e == cudaSuccess) count_launch();
+  return e;
 }
 
 template <int D, int NT>
@@ -692,7 +694,7 @@ int paged_weights(const void* q, const float* lse, float* weights, int weights_l
   for (p.heads = p.group < nt ? p.group : nt; p.group % p.heads != 0;) --p.heads;
   p.parts = p.group / p.heads;
   p.span = nt / p.heads;
-  p.span_inv = ((1ull << 40) + p.span - 1) / p.span;
+  p.span_inv = ~0ull / p.span + 1;   // (span = 1: not used)
   // with no rows at all nothing is loaded through the map
   const int rows = total > 0 ? total : 1;
   if (int rc = tile_map(q, bf16, d, Hq, rows, 1, d, static_cast<long long>(Hq) * d,

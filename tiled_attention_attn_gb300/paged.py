@@ -239,17 +239,14 @@ def rotary_scaled(x: torch.Tensor, freqs: torch.Tensor, amplitude: float = 1.0, 
 
 
 class _RotaryScaledFunction(torch.autograd.Function):
-    """The rotation forward, its inverse (times the same amplitude) backward."""
+    """The rotation forward, its inverse (times the same amplitude) backward;
+    the backward is the same operator turned round, so it has a gradient too."""
 
     @staticmethod
-    def forward(ctx, x, freqs, amplitude, interleaved, cu_seqlens, offsets, positions):
+    def forward(ctx, x, freqs, amplitude, interleaved, cu_seqlens, offsets, positions, inverse):
         ctx.save_for_backward(*(t for t in (cu_seqlens, offsets, positions) if t is not None))
         ctx.given = [t is not None for t in (cu_seqlens, offsets, positions)]
-        ctx.args = (freqs, amplitude, interleaved)
-        return _RotaryScaledFunction.turn(x, *ctx.args, cu_seqlens, offsets, positions, False)
-
-    @staticmethod
-    def turn(x, freqs, amplitude, interleaved, cu_seqlens, offsets, positions, inverse):
+        ctx.args = (freqs, amplitude, interleaved, inverse)
         # rows outside every sequence are zero, in the output and in the gradient
         out = torch.zeros(x.shape, dtype=x.dtype, device=x.device) if cu_seqlens is not None else None
         return rotary_scaled(x, freqs, amplitude, interleaved, cu_seqlens, offsets, positions, inverse, out)
@@ -258,7 +255,9 @@ class _RotaryScaledFunction(torch.autograd.Function):
     def backward(ctx, dy):
         saved = iter(ctx.saved_tensors)
         cu, off, pos = (next(saved) if g else None for g in ctx.given)
-        return (_RotaryScaledFunction.turn(dy.contiguous(), *ctx.args, cu, off, pos, True),) + (None,) * 6
+        freqs, amplitude, interleaved, inverse = ctx.args
+        return (_RotaryScaledFunction.apply(dy.contiguous(), freqs, amplitude, interleaved, cu, off, pos,
+                                            not inverse),) + (None,) * 7
 
 
 def rotary_scaled_func(x: torch.Tensor, freqs: torch.Tensor, amplitude: float = 1.0, interleaved: bool = False,
@@ -267,7 +266,8 @@ def rotary_scaled_func(x: torch.Tensor, freqs: torch.Tensor, amplitude: float = 
     """``rotary_scaled`` with a gradient for x (the frequencies are constants).
     With ``cu_seqlens``, rows outside every sequence are zero and get no
     gradient."""
-    return _RotaryScaledFunction.apply(x, freqs, float(amplitude), bool(interleaved), cu_seqlens, offsets, positions)
+    return _RotaryScaledFunction.apply(x, freqs, float(amplitude), bool(interleaved), cu_seqlens, offsets, positions,
+                                       False)
 
 
 @_placed
