@@ -151,8 +151,9 @@ struct PCfg {
 // softmax_tile of a tile some of whose keys are hidden (diagonal and ragged
 // tiles): keys past `lim` are dropped by index.  The scores are read from TMEM
 // twice, 32 columns at a time in rolled loops, instead of held in 128
-// registers: an eighth of the code, which a short call fetches cold (one tile of
-// 64 rows: MASKED_COLD).
+// registers: an eighth of the code, which a short call fetches cold, for one more
+// read of the tile (8 chunks of 512 tokens over their own keys, four query heads a
+// key/value head: 37.2 us against 41.1 with the 128-register form).
 template <bool BF16, int D>
 __device__ __forceinline__ void softmax_masked(uint32_t t_s, uint32_t t_o, int lim, float c_log2, RowState& st, bool first) {
   float mx = -INFINITY;
