@@ -16,11 +16,12 @@
 // each load one box (64 features x the tokens of a page) of K or V at the page
 // that the lane has read from the table, one step ahead.
 //
-// Work: the steps of all (sequence, head group) units, one after the other,
-// cut into equal ranges, one per CTA, wherever the cut falls (the host does not
-// know the lengths, and ragged caches need no other balancing).  A unit that
-// reaches over a cut leaves fp32 partials, at most two per CTA, which a second
-// launch (decode_merge_kernel) joins.
+// Work: the steps of all (sequence, head group) units, one after the other (the
+// key/value heads side by side, heads_abreast), cut into equal ranges, one per
+// CTA, wherever the cut falls (the host does not know the lengths, and ragged
+// caches need no other balancing).  A unit that reaches over a cut leaves fp32
+// partials, at most two per CTA, which a second launch (decode_merge_kernel)
+// joins.
 //
 // Slots past a sequence's last key may hold anything: their scores are dropped
 // by index, and their rows of V are zeroed in shared memory before the product
@@ -93,6 +94,7 @@ struct Params {
   int* err;
   unsigned long long timeout_ns;
   int B, Hq, group, heads, parts;   // heads per unit; units per key/value head
+  int abreast;         // unit groups that walk the line side by side (heads_abreast)
   int cuts;            // the table can hold a unit long enough to be cut
   float scale_log2;
 };
@@ -100,7 +102,7 @@ struct Params {
 // The CTA's walk over units: (b, hc) in order, unit at position p of the line
 // of steps with T steps and one more for its fixed cost.
 struct Walk {
-  int b, hc;
+  int b, hc;          // hc: group of p.abreast units; this CTA's is hc * abreast + its place
   long long p, end;   // unit start; end of this CTA's range
   long long begin;
   int n, T;           // keys, steps
@@ -113,7 +115,7 @@ __device__ __forceinline__ int steps_of(int n) { return (n + KS - 1) / KS; }
 // The next unit that has something to do here; false at the range's end.
 template <int KS>
 __device__ __forceinline__ bool next_unit(const Params& p, Walk& w, bool first) {
-  const int nh = p.c.hkv * p.parts;
+  const int nh = p.c.hkv * p.parts / p.abreast;
   if (!first) {
     w.p += w.T + 1;
     if (++w.hc == nh) {
@@ -233,15 +235,17 @@ __global__ void __launch_bounds__(kThreads, 1) decode_kernel(const __grid_consta
   fence_proxy_async_smem();
 
   // the line of steps: each thread a strip of sequences, then a prefix sum
-  const int nh = p.c.hkv * p.parts;
+  const int nh = p.c.hkv * p.parts / p.abreast;
+  const int place = blockIdx.x % p.abreast, ranges = gridDim.x / p.abreast, range_id = blockIdx.x / p.abreast;
   const int strip = (p.B + kThreads - 1) / kThreads;
   const int b_lo = min(tid * strip, p.B), b_hi = min(b_lo + strip, p.B);
   long long mine = 0, total, units;
   for (int b = b_lo; b < b_hi; ++b) mine += static_cast<long long>(nh) * (steps_of<KS>(paged_len(p.c, b, p.err)) + 1);
   const long long before = block_prefix<kThreads>(
       mine, static_cast<int>(min(static_cast<long long>(nh) * (b_hi - b_lo), 1LL << 24)), warp_sums, total, units);
-  const long long range = range_of<kMinSteps>(total, units);
-  const long long begin = blockIdx.x * range, end = min(begin + range, total);
+  const long long range = range_of<kMinSteps>(total, units, ranges);
+  // (SMs past the last whole range idle)
+  const long long begin = range_id < ranges ? range_id * range : total, end = min(begin + range, total);
   if (begin >= before && begin < before + mine) {
     long long at = before;
     for (int b = b_lo; b < b_hi; ++b) {
@@ -298,7 +302,7 @@ __global__ void __launch_bounds__(kThreads, 1) decode_kernel(const __grid_consta
     bool ok = true;
     for (bool more = next_unit<KS>(p, w, true); more && ok; more = next_unit<KS>(p, w, false)) {
       if (w.t1 <= w.t0) continue;
-      const int g = w.hc / p.parts, part = w.hc - g * p.parts;
+      const int unit = w.hc * p.abreast + place, g = unit / p.parts, part = unit - g * p.parts;
       if (!of_v) {
         const int qs = q_cnt & 1;
         if (!mbar_wait_warp(b_q_empty(qs), ((q_cnt >> 1) & 1) ^ 1, wc, ATTN_DEVERR_WAIT_TIMEOUT_SITE(kSiteQEmpty))) break;
@@ -482,7 +486,7 @@ __global__ void __launch_bounds__(kThreads, 1) decode_kernel(const __grid_consta
     };
     Walk w = w0;
     for (bool more = next_unit<KS>(p, w, true); more && ok; more = next_unit<KS>(p, w, false)) {
-      const int g = w.hc / p.parts, part = w.hc - g * p.parts;
+      const int unit = w.hc * p.abreast + place, g = unit / p.parts, part = unit - g * p.parts;
       const int head0 = g * p.group + part * p.heads;
       const int G = min(p.heads, p.group - part * p.heads);   // heads of this unit
       const size_t orow0 = static_cast<size_t>(w.b) * p.Hq + head0;   // first output row (b, head)
@@ -637,9 +641,9 @@ __global__ void __launch_bounds__(kThreads, 1) decode_kernel(const __grid_consta
               (lv > 0.0f) ? mv * 0.69314718055994531f + __logf(lv) : -INFINITY;
         else
           p.part_ml[slot * kNQ + lane] = make_float2(lv > 0.0f ? mv : -INFINITY, lv);
-        // the unit's pieces lie on CTAs p / range ... (p + T - 1) / range
+        // the unit's pieces lie on the ranges p / range ... (p + T - 1) / range
         if (!whole && w.t0 == 0 && lane == 0)
-          p.rec[blockIdx.x] = make_int4(w.b, w.hc, static_cast<int>((w.p + w.T - 1) / range) - static_cast<int>(blockIdx.x) + 1, 0);
+          p.rec[blockIdx.x] = make_int4(w.b, unit, static_cast<int>((w.p + w.T - 1) / range) - range_id + 1, 0);
       }
     }
   }
@@ -671,7 +675,7 @@ __global__ void __launch_bounds__(128) decode_merge_kernel(const __grid_constant
   float M = -INFINITY, L = 0.0f, acc[E];
 #pragma unroll
   for (int e = 0; e < E; ++e) acc[e] = 0.0f;
-  auto slot = [&](int s) { return s == 0 ? 2 * c + 1 : 2 * (c + s); };
+  auto slot = [&](int s) { return s == 0 ? 2 * c + 1 : 2 * (c + s * p.abreast); };
   for (int s0 = w; s0 < pieces; s0 += 16) {
     float2 ml[4];
     float x[4][E];
@@ -801,6 +805,7 @@ int paged_decode(const void* q, void* o, float* lse, int B, int Hq, const PagedK
   p.timeout_ns = wait_timeout_ns();
   p.B = B;
   p.Hq = Hq;
+  p.abreast = heads_abreast(c.hkv * p.parts, sms);
   p.cuts = (c.max_pages << c.page_log2) > pdec::kMinSteps * (d == 64 ? 256 : 128);
   p.scale_log2 = scale * 1.4426950408889634f;
   cudaError_t e;

@@ -272,7 +272,7 @@ __global__ void __launch_bounds__(kThreads, 1) fwd_kernel(const __grid_constant_
     count = min(count + line.units(w0), 1 << 24);   // (for a mean: the largest need not be exact)
   }
   const long long before = block_prefix<kThreads>(mine, count, warp_sums, total, units);
-  const long long range = range_of<kMinTiles>(total, units);
+  const long long range = range_of<kMinTiles>(total, units, gridDim.x);
   const long long begin = blockIdx.x * range, end = min(begin + range, total);
   if (begin >= before && begin < before + mine) {
     long long at = before;

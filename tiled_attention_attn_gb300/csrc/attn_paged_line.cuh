@@ -1,10 +1,22 @@
 // Cutting a batch's work into equal ranges on the device: the units of all
-// sequences form a line, each as long as its cost, and CTA c takes what lies
-// in [c range, (c + 1) range).
+// sequences form a line, each as long as its cost, and range r of them is what
+// lies in [r range, (r + 1) range).
 #pragma once
 #include <cuda_runtime.h>
 
 namespace attn {
+
+// How many key/value heads (units of a sequence, equally long) walk the line
+// side by side, each on a CTA of its own: the heads of a token lie next to one
+// another in memory, and CTAs that read them at the same time keep to open DRAM
+// rows.  The largest divisor of `heads` that leaves at most 5 % of the SMs idle.
+// (One token over 32 caches of ~3,550 keys, 8 heads of 64: 47.1 us
+// against 58.4 one head after the other.)
+inline int heads_abreast(int heads, int sms) {
+  for (int m = heads; m > 1; --m)
+    if (heads % m == 0 && m <= sms && 20 * (sms / m) * m >= 19 * sms) return m;
+  return 1;
+}
 
 // The sum of `mine` over the threads before this one, and the sums of `mine`
 // and of `units` over all of them.  Has one __syncthreads; warp_sums holds
@@ -37,13 +49,13 @@ __device__ __forceinline__ long long block_prefix(long long mine, int units, lon
   return before;
 }
 
-// The length of a CTA's range: equal shares, but not below the mean unit, nor,
+// The length of a range: equal shares, but not below the mean unit, nor,
 // when units are longer than that, below kLeast: shorter pieces cost more than
 // they save (their merge, and a start each).  Units of up to kLeast are not
 // cut: they belong to the range that they start in.
 template <int kLeast>
-__device__ __forceinline__ long long range_of(long long total, long long units) {
-  const long long share = (total + gridDim.x - 1) / gridDim.x;
+__device__ __forceinline__ long long range_of(long long total, long long units, int ranges) {
+  const long long share = (total + ranges - 1) / ranges;
   if (share >= kLeast) return share;
   return max(share, min(static_cast<long long>(kLeast), units > 0 ? total / units : 1));
 }

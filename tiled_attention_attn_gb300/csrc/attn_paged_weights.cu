@@ -73,13 +73,14 @@ struct Params {
   int B, Hq, total, len, group, heads, parts, span;
   unsigned long long span_inv;   // ceil(2^64 / span), span > 1
   float scale_log2, decay;
+  int abreast;       // key/value heads that walk the line side by side (heads_abreast)
   int cuts;          // the chunk can be long enough for a unit to be cut
   float inv_scale;   // 1 / scale; 1 for scale 0 (then the products are left out)
   int products;
 };
 
 struct Walk {
-  int b, g, kb;
+  int b, g, kb;              // g: this CTA's head of a group of p.abreast
   int q_len, k_len, row_q, n_kb;
   long long p, begin, end;   // unit start on the line; this CTA's range
   int n, t0, t1;             // query tiles of the unit; this CTA's part
@@ -126,16 +127,16 @@ struct Line {
     }
     w.n_kb = (w.k_len + kKeys - 1) / kKeys;
   }
-  __device__ long long cost(const Walk& w) const { return before(w, w.n_kb) * p.c.hkv; }
+  __device__ long long cost(const Walk& w) const { return before(w, w.n_kb) * (p.c.hkv / p.abreast); }
   __device__ int units(const Walk& w) const {
-    return static_cast<int>(min(static_cast<long long>(w.n_kb) * p.c.hkv, 1LL << 24));
+    return static_cast<int>(min(static_cast<long long>(w.n_kb) * (p.c.hkv / p.abreast), 1LL << 24));
   }
   __device__ void advance(Walk& w) const {
     w.p += w.n + 1;
     if (++w.kb == w.n_kb) {
       w.kb = 0;
-      if (++w.g == p.c.hkv) {
-        w.g = 0;
+      if ((w.g += p.abreast) >= p.c.hkv) {
+        w.g = blockIdx.x % p.abreast;
         while (++w.b < p.B) {
           load(w);
           if (w.n_kb > 0) break;
@@ -347,8 +348,10 @@ __global__ void __launch_bounds__(WCfg<D, NT>::kThr, 1) weights_kernel(const __g
     count = min(count + line.units(w0), 1 << 24);   // (for a mean: the largest need not be exact)
   }
   const long long before = block_prefix<kThr>(mine, count, warp_sums, total, units);
-  const long long range = range_of<kMinTiles>(total, units);
-  const long long begin = blockIdx.x * range, end = min(begin + range, total);
+  const long long range = range_of<kMinTiles>(total, units, gridDim.x / p.abreast);
+  const int range_id = blockIdx.x / p.abreast;   // (SMs past the last whole range idle)
+  const long long begin = range_id < static_cast<int>(gridDim.x) / p.abreast ? range_id * range : total;
+  const long long end = min(begin + range, total);
   if (begin >= before && begin < before + mine) {
     long long at = before;
     for (w0.b = b_lo; w0.b < b_hi; ++w0.b) {
@@ -364,7 +367,7 @@ __global__ void __launch_bounds__(WCfg<D, NT>::kThr, 1) weights_kernel(const __g
           if (at + line.before(w0, mid) <= begin) lo = mid; else hi = mid;
         }
         start[0] = w0.b;
-        start[1] = g;
+        start[1] = g * p.abreast + blockIdx.x % p.abreast;
         start[2] = lo;
         *start_p = at + line.before(w0, lo);
         break;
@@ -609,7 +612,7 @@ __global__ void __launch_bounds__(WCfg<D, NT>::kThr, 1) weights_kernel(const __g
         p.part[(2 * blockIdx.x + (w.t0 == 0 ? 1 : 0)) * kKeys + x * 128 + lrow] = s;
         if (w.t0 == 0 && warp == kWSum && lane == 0)
           p.rec[blockIdx.x] = make_int4(w.b, w.g, w.kb,
-                                        static_cast<int>((w.p + w.n - 1) / range) - static_cast<int>(blockIdx.x) + 1);
+                                        static_cast<int>((w.p + w.n - 1) / range) - range_id + 1);
       }
     }
   }
@@ -630,7 +633,7 @@ __global__ void __launch_bounds__(kKeys) weights_merge_kernel(const __grid_const
   if (rec.w <= 1) return;
   const int key = rec.z * kKeys + threadIdx.x;
   float s = __ldcg(p.part + (2 * c + 1) * kKeys + threadIdx.x);
-  for (int i = 1; i < rec.w; ++i) s += __ldcg(p.part + 2 * (c + i) * kKeys + threadIdx.x);
+  for (int i = 1; i < rec.w; ++i) s += __ldcg(p.part + 2 * (c + i * p.abreast) * kKeys + threadIdx.x);
   if (key >= __ldg(p.c.seqlens + rec.x)) return;
   float* out = p.weights + (static_cast<long long>(rec.x) * p.c.hkv + rec.y) * p.len + key;
   *out = (p.decay != 0.0f ? p.decay * *out : 0.0f) + s;
@@ -714,6 +717,7 @@ int paged_weights(const void* q, const float* lse, float* weights, int weights_l
   p.Hq = Hq;
   p.total = total;
   p.len = weights_len;
+  p.abreast = heads_abreast(c.hkv, sms);
   p.cuts = static_cast<long long>((total + p.span - 1) / p.span) * p.parts > pwts::kMinTiles;
   p.products = scale > 0.0f;
   p.inv_scale = scale > 0.0f ? 1.0f / scale : 1.0f;
