@@ -72,7 +72,7 @@ struct Cfg {
   static constexpr int kOffP = kOffQ + 2 * kQ;            // two P^T buffers
   static constexpr int kOffRed = kOffP + 2 * kP;          // [parity][warp][kNQ] floats
   static constexpr int kOffBar = kOffRed + 2 * 4 * kNQ * 4;
-  static constexpr int kNBars = 3 * kStages + 14;
+  static constexpr int kNBars = 4 * kStages + 14;
   static constexpr int kOffMisc = kOffBar + kNBars * 8;
   static constexpr int kSmem = kOffMisc + 256 + 1024;
   static_assert(kSmem <= 227 * 1024, "shared memory");
@@ -179,8 +179,12 @@ __global__ void __launch_bounds__(kThreads, 1) decode_kernel(const __grid_consta
   const uint32_t bar0 = sbase + C::kOffBar;
   auto b_k_full = [&](int s) { return bar0 + 8 * s; };
   auto b_v_full = [&](int s) { return bar0 + 8 * (kStages + s); };
-  auto b_kv_empty = [&](int s) { return bar0 + 8 * (2 * kStages + s); };
-  const uint32_t bar1 = bar0 + 8 * 3 * kStages;
+  // head dimension 64 frees K's stage as soon as S^T is computed (131,072 keys
+  // 50.1 -> 48.3 us); at 128 both are freed together, K running ahead of V
+  // costs there (85.3 -> 88.6 us)
+  auto b_v_empty = [&](int s) { return bar0 + 8 * (2 * kStages + s); };
+  auto b_k_empty = [&](int s) { return DA == 64 ? bar0 + 8 * (3 * kStages + s) : b_v_empty(s); };
+  const uint32_t bar1 = bar0 + 8 * 4 * kStages;
   auto b_q_full = [&](int s) { return bar1 + 8 * s; };
   auto b_q_empty = [&](int s) { return bar1 + 8 * (2 + s); };
   auto b_s_full = [&](int s) { return bar1 + 8 * (4 + s); };
@@ -205,7 +209,8 @@ __global__ void __launch_bounds__(kThreads, 1) decode_kernel(const __grid_consta
     for (int s = 0; s < kStages; ++s) {
       mbar_init(b_k_full(s), 1);
       mbar_init(b_v_full(s), 1);
-      mbar_init(b_kv_empty(s), 1);
+      mbar_init(b_v_empty(s), 1);
+      if constexpr (DA == 64) mbar_init(b_k_empty(s), 1);
     }
     for (int s = 0; s < 2; ++s) {
       mbar_init(b_q_full(s), 1);
@@ -290,6 +295,7 @@ __global__ void __launch_bounds__(kThreads, 1) decode_kernel(const __grid_consta
     const CUtensorMap* map = of_v ? &p.tm_v : &p.tm_k;
     const uint32_t dst0 = (of_v ? sV : sK) + ch * kChunk + pg * box * 128;
     auto b_full = [&](int s) { return of_v ? b_v_full(s) : b_k_full(s); };
+    auto b_empty = [&](int s) { return of_v ? b_v_empty(s) : b_k_empty(s); };
     const int key_off = (kTPS == 1 ? 0 : ch * kKeys) + pg * box;
     const int col = kTPS == 1 ? ch * 64 : 0;
     auto page_at = [&](const Walk& w, int t) {   // the page of this lane's box in step t, -1: past the last key
@@ -318,7 +324,7 @@ __global__ void __launch_bounds__(kThreads, 1) decode_kernel(const __grid_consta
       for (int t = w.t0; t < w.t1; ++t) {
         const int st = kv_cnt % kStages;
         const int next = t + 1 < w.t1 ? page_at(w, t + 1) : -1;
-        if (!mbar_wait_warp(b_kv_empty(st), ((kv_cnt / kStages) & 1) ^ 1, wc,
+        if (!mbar_wait_warp(b_empty(st), ((kv_cnt / kStages) & 1) ^ 1, wc,
                             ATTN_DEVERR_WAIT_TIMEOUT_SITE(kSiteKEmpty))) { ok = false; break; }
         const uint32_t n_box = __popc(__ballot_sync(0xffffffffu, page >= 0));
         if (lane == 0) mbar_arrive_expect_tx(b_full(st), n_box * box * 128);
@@ -360,8 +366,8 @@ __global__ void __launch_bounds__(kThreads, 1) decode_kernel(const __grid_consta
         if (!mbar_wait(b_q_full(qs), (q_cnt >> 1) & 1, wc, ATTN_DEVERR_WAIT_TIMEOUT_SITE(kSiteQFull))) break;
         ++q_cnt;
         tc_fence_after();
-        // u^T += V^T P^T of the step in stage vst, P^T buffer pb; the stage (K
-        // and V) is released after it.  Before a unit's first product, which
+        // u^T += V^T P^T of the step in stage vst, P^T buffer pb; V (and K: see
+        // b_k_empty) is released after it.  Before a unit's first product, which
         // overwrites u^T, the previous unit's epilogue must have read it
         auto do_pv = [&](int vst, int pb, bool first) -> bool {
           if (!mbar_wait(b_v_full(vst), (v_cnt / kStages) & 1, wc, ATTN_DEVERR_WAIT_TIMEOUT_SITE(kSiteVFull))) return false;
@@ -378,7 +384,7 @@ __global__ void __launch_bounds__(kThreads, 1) decode_kernel(const __grid_consta
             const uint64_t b = dp0 + ((pb * C::kP + (kk >> 2) * C::kPChunk + (kk & 3) * 32) >> 4);
             umma_ss(t_u, a, b, kIdescO, (first && kk == 0) ? 0u : 1u);
           }
-          umma_commit(b_kv_empty(vst));
+          umma_commit(b_v_empty(vst));
           umma_commit(b_p_free(pb));
           return true;
         };
@@ -407,6 +413,7 @@ __global__ void __launch_bounds__(kThreads, 1) decode_kernel(const __grid_consta
             }
           }
           umma_commit(b_s_full(sb));
+          if constexpr (DA == 64) umma_commit(b_k_empty(st));
           ++s_cnt;
           if (prev_pb >= 0) {
             if (!do_pv(prev_st, prev_pb, first_pv)) {
