@@ -258,8 +258,10 @@ __global__ void __launch_bounds__(kSelThreads, 2) evict_select_kernel(const __gr
   }
 }
 
-// Grid (blocks, heads, sequences); the last block of x moves the weights.
-__global__ void __launch_bounds__(kMoveThreads) evict_move_kernel(const __grid_constant__ EvictParams p) {
+// Grid (blocks, heads, sequences); the last block of x moves the weights.  Four
+// blocks per SM (64 registers): 32 x 4096 keys in place 103 us against 124 with
+// three.
+__global__ void __launch_bounds__(kMoveThreads, 4) evict_move_kernel(const __grid_constant__ EvictParams p) {
   const int blocks = gridDim.x - 1;
   const int g = blockIdx.y, b = blockIdx.z, tid = threadIdx.x;
   const int n = evict_len(p, b), m = min(n, p.budget);
