@@ -53,6 +53,12 @@ CHUNKS = [
     ([1024], [3000], 8, 2, 128, 32, BF, "nhd", True),
     ([1] * 70, [1 + 11 * i for i in range(70)], 4, 2, 64, 16, BF, "nhd", True),
     ([600, 0, 2, 900], [600, 77, 4000, 1500], 12, 12, 64, 16, HF, "nhd", False),
+    # many blocks of queries, so that ranges start deep inside a chunk: fewer and more keys than queries
+    ([3000, 700], [3001, 5000], 16, 1, 64, 64, BF, "nhd", True),
+    ([2500, 1200], [900, 1300], 11, 1, 64, 32, HF, "nhd", True),
+    ([1500], [4000], 32, 1, 128, 128, BF, "nhd", False),
+    # more sequences than a block has threads
+    ([i % 4 for i in range(700)], [(7 * i) % 90 for i in range(700)], 4, 2, 64, 16, HF, "nhd", True),
 ]
 
 
@@ -130,6 +136,12 @@ DECODES = [
     ([33 * i % 611 for i in range(500)], 4, 2, 64, 16, BF, "nhd"),
     ([20000] + [3] * 40, 8, 1, 128, 32, BF, "nhd"),         # one long among many short
     ([0, 0, 0], 2, 1, 64, 16, BF, "nhd"),
+    # key/value heads side by side in groups: 32 in four of 8, 14 at once, a prime number, none that fits
+    ([3000, 17, 900], 32, 32, 64, 16, HF, "nhd"),
+    ([2000, 1], 28, 14, 128, 32, BF, "nhd"),
+    ([5000, 300], 7, 7, 64, 64, HF, "hnd"),
+    ([1200, 640], 74, 37, 64, 16, BF, "nhd"),
+    ([(5 * i) % 41 for i in range(5000)], 2, 1, 64, 16, HF, "nhd"),
 ]
 
 
@@ -229,6 +241,14 @@ WEIGHTS = [
     ([20], [500], 71, 1, 64, 32, HF, "nhd", True, 1.0),
     ([9, 3], [300, 70], 160, 1, 64, 16, BF, "nhd", True, 0.0),
     ([2, 900, 1], [3000, 900, 64], 4, 1, 128, 16, BF, "nhd", True, 1.0),
+    # ranges that start deep inside a long cache, few and many queries a tile
+    ([900, 3], [12000, 9000], 4, 2, 64, 128, HF, "nhd", True, 1.0),
+    ([1500], [9500], 3, 1, 64, 64, HF, "nhd", False, 0.5),
+    ([2000], [700], 20, 1, 64, 32, HF, "nhd", True, 1.0),
+    ([i % 3 for i in range(900)], [(7 * i) % 90 for i in range(900)], 4, 2, 64, 16, HF, "nhd", True, 1.0),
+    ([1, 2], [3000, 700], 24, 1, 64, 16, BF, "nhd", True, 1.0),
+    ([1] * 3, [2000, 17, 900], 64, 32, 64, 16, HF, "nhd", True, 1.0),
+    ([40, 1], [2000, 300], 7, 7, 128, 64, BF, "hnd", True, 0.0),
 ]
 
 
@@ -348,6 +368,23 @@ def test_evict(case, in_place, kind):
     assert torch.equal(c.k[~written], k0[~written]) and torch.equal(c.v[~written], v0[~written])
 
 
+@pytest.mark.parametrize("kind", ["plain", "ties"])
+def test_evict_from_more_keys_than_a_cluster_holds(kind):
+    n = 500_000
+    c = Cache([n], 1, 64, 256, BF, seed=3, poison=False)
+    w = evict_weights(c, c.table.shape[1] * 256, kind, 5)
+    k0 = c.k.clone()
+    kept, seqlens, wout = attn.cache_evict(w, c.k, c.v, c.table, c.seqlens, 7001, 1001)
+    ok()
+    want = ref.evict(w[0, 0].tolist(), n, 7001, 1001)
+    assert seqlens.tolist() == [7001] and kept[0, 0].tolist() == want
+    idx = torch.tensor(want, device="cuda")
+    j = torch.arange(7001, device="cuda")
+    got = c.k[c.table[0, j // 256].long(), j % 256]
+    assert torch.equal(got, k0[c.table[0, idx // 256].long(), idx % 256])
+    assert torch.equal(wout[0, 0], w[0, 0, idx])
+
+
 def test_evict_weights_in_place():
     c = Cache([500, 80], 2, 64, 16, BF, seed=1, poison=False)
     w = evict_weights(c, 520, "plain", 1)
@@ -442,7 +479,8 @@ def test_two_streams_and_two_graphs():
         o1, l1 = attn.attn_decode_paged(q1, *c.args(), stream=stream)
         o2, l2 = attn.attn_fwd_paged(q2, *c.args(), cu, stream=stream)
         w = attn.key_weights(q2, c.k, l2, c.table, c.seqlens, cu, stream=stream)
-        return o1, l1, o2, l2, w
+        kept, n, _ = attn.cache_evict(w, c.k, c.v, c.table, c.seqlens, 1 << 20, stream=stream)   # (moves nothing)
+        return o1, l1, o2, l2, w, kept[..., :100].clone(), n
 
     want = [both(*x) for x in cases]
     torch.cuda.synchronize()
@@ -468,7 +506,7 @@ def test_two_streams_and_two_graphs():
                 gr.replay()
         torch.cuda.synchronize()
         for a, b in zip(want, outs):
-            assert all(torch.equal(x, y) for x, y in zip(a[:4], b[:4]))
+            assert all(torch.equal(x, y) for x, y in zip(a, b))
     ok()
 
 
