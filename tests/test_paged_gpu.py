@@ -7,6 +7,7 @@ import math
 import os
 import subprocess
 import sys
+import threading
 
 import pytest
 import torch
@@ -507,6 +508,49 @@ def test_two_streams_and_two_graphs():
         torch.cuda.synchronize()
         for a, b in zip(want, outs):
             assert all(torch.equal(x, y) for x, y in zip(a, b))
+    ok()
+
+
+def test_two_threads_on_one_stream():
+    """Calls of two threads that interleave on a stream: each has its own
+    scratch memory between its kernels."""
+    cs = [Cache([40000, 500], 2, 128, 16, BF, seed=s) for s in (1, 2)]
+    qs = [queries([1, 1], 8, 128, BF, s) for s in (1, 2)]
+    want = [attn.attn_decode_paged(q, *c.args()) for c, q in zip(cs, qs)]
+    torch.cuda.synchronize()
+    got = [None, None]
+
+    def work(i):
+        got[i] = [attn.attn_decode_paged(qs[i], *cs[i].args()) for _ in range(200)]
+
+    threads = [threading.Thread(target=work, args=(i,)) for i in range(2)]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    torch.cuda.synchronize()
+    for i in range(2):
+        assert all(torch.equal(o, want[i][0]) and torch.equal(lse, want[i][1]) for o, lse in got[i])
+    ok()
+
+
+def test_many_streams_and_eager_calls_beside_a_graph():
+    c = Cache([20000, 500], 2, 64, 16, BF, seed=1)
+    q = queries([1, 1], 8, 64, BF, 1)
+    want = attn.attn_decode_paged(q, *c.args())
+    gr = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(gr):
+        out = attn.attn_decode_paged(q, *c.args())
+    streams = [torch.cuda.Stream() for _ in range(12)]   # more than the kept scratch buffers
+    torch.cuda.synchronize()
+    for _ in range(3):
+        got = []
+        gr.replay()
+        for s in streams:
+            got.append(attn.attn_decode_paged(q, *c.args(), stream=s))
+        torch.cuda.synchronize()
+        for o, lse in got + [out]:
+            assert torch.equal(o, want[0]) and torch.equal(lse, want[1])
     ok()
 
 

@@ -4,8 +4,8 @@ single tokens over the pages, accumulated attention weights, and eviction.
 
 Like the rest of the binding this marshals arguments only; every step runs in
 the library's kernels.  Outputs and scratch memory are allocated by torch on
-the call's stream, so calls on several streams, or captured in several graphs,
-share nothing.  Every operator takes ``stream`` by name (default: the current
+the call's stream; calls on several streams, from several threads, or captured
+in several graphs share nothing.  Every operator takes ``stream`` by name (default: the current
 stream of its tensors' device).
 
 Caches: ``k_pages`` and ``v_pages`` are (num_pages, page_size, Hkv, d) views,
@@ -20,6 +20,7 @@ from __future__ import annotations
 import ctypes
 import functools
 import math
+import threading
 from typing import Optional, Tuple
 
 import torch
@@ -324,20 +325,31 @@ def cache_append(k: torch.Tensor, v: torch.Tensor, k_pages: torch.Tensor, v_page
 
 
 _ws_bytes: dict = {}
-
-
+_ws_kept = threading.local()
 _CHUNK, _DECODE, _WEIGHTS = 0, 1, 2   # ATTN_PAGED_*
 
 
-def _workspace(device: torch.device, d: int, call: int) -> torch.Tensor:
-    key = (device.index, d, call)
-    n = _ws_bytes.get(key)
+def _workspace(device: torch.device, stream: int, d: int, call: int) -> torch.Tensor:
+    """Scratch memory of one call.  Each thread keeps what it used last on a
+    stream (calls of a thread on a stream are ordered; at most 8 are kept); a
+    captured call gets memory of its own, which its graph keeps."""
+    kept = _ws_kept.__dict__
+    key = (device.index, stream, d, call)
+    capturing = torch.cuda.is_current_stream_capturing()
+    if not capturing and key in kept:
+        return kept[key]
+    n = _ws_bytes.get((device.index, d, call))
     if n is None:
         n = _attn.lib().attn_paged_workspace_bytes(d, call)
         if n < 0:
             raise _attn.AttnError(int(n), "attn_paged_workspace_bytes")
-        _ws_bytes[key] = n
-    return torch.empty(n, dtype=torch.uint8, device=device)
+        _ws_bytes[(device.index, d, call)] = n
+    ws = torch.empty(n, dtype=torch.uint8, device=device)
+    if not capturing:
+        if len(kept) >= 8:
+            del kept[next(iter(kept))]
+        kept[key] = ws
+    return ws
 
 
 def _outputs(q, out, lse):
@@ -371,7 +383,7 @@ def attn_fwd_paged(q: torch.Tensor, k_pages: torch.Tensor, v_pages: torch.Tensor
         scale = 1.0 / math.sqrt(c.head_dim)
     s = _stream(q.device)
     out, lse = _outputs(q, out, lse)
-    ws = _workspace(q.device, c.head_dim, _CHUNK)
+    ws = _workspace(q.device, s, c.head_dim, _CHUNK)
     rc = _attn.lib().attn_fwd_paged(q.data_ptr(), out.data_ptr(), lse.data_ptr(), B, q.shape[1], q.shape[0],
                                     ctypes.byref(c), cu_seqlens.data_ptr(), int(bool(causal)), float(scale),
                                     ws.data_ptr(), ws.numel(), s) if q.shape[0] else 0
@@ -394,7 +406,7 @@ def attn_decode_paged(q: torch.Tensor, k_pages: torch.Tensor, v_pages: torch.Ten
         scale = 1.0 / math.sqrt(c.head_dim)
     s = _stream(q.device)
     out, lse = _outputs(q, out, lse)
-    ws = _workspace(q.device, c.head_dim, _DECODE)
+    ws = _workspace(q.device, s, c.head_dim, _DECODE)
     rc = _attn.lib().attn_decode_paged(q.data_ptr(), out.data_ptr(), lse.data_ptr(), q.shape[0], q.shape[1],
                                        ctypes.byref(c), float(scale), ws.data_ptr(), ws.numel(), s)
     _check_rc(rc, "attn_decode_paged")
@@ -427,7 +439,7 @@ def key_weights(q: torch.Tensor, k_pages: torch.Tensor, lse: torch.Tensor, page_
     if weights.dim() != 3 or weights.shape[:2] != (B, c.num_kv_heads) or weights.dtype != torch.float32 or \
             weights.device != dev or not weights.is_contiguous():
         raise ValueError("weights must be a contiguous float32 tensor (B, Hkv, n)")
-    ws = _workspace(dev, d, _WEIGHTS)
+    ws = _workspace(dev, s, d, _WEIGHTS)
     rc = _attn.lib().attn_key_weights(q.data_ptr() or None, lse.data_ptr() or None, weights.data_ptr() or None,
                                       weights.shape[2], B, Hq, T, ctypes.byref(c), cu_seqlens.data_ptr(),
                                       int(bool(causal)), float(scale), float(decay), ws.data_ptr(), ws.numel(), s)
