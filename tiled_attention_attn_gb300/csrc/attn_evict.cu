@@ -79,9 +79,11 @@ __device__ __forceinline__ int ld_dsmem_s32(uint32_t a) {
 // same path, so all reach each cluster barrier.  32 registers, so that two CTAs
 // share an SM (256 heads in one wave: 32 x 4096 keys 104 -> 99.5 us).
 __global__ void __launch_bounds__(kSelThreads, 2) evict_select_kernel(const __grid_constant__ EvictParams p) {
-  extern __shared__ uint32_t keys[];
-  __shared__ __align__(8) int hist[kBins];
-  __shared__ int coarse[32], from_peer[kMaxCluster][64];
+  extern __shared__ __align__(16) uint32_t keys[];
+  // counts of each digit apart, so that a peer may still read one digit's while
+  // the next digit is counted
+  __shared__ __align__(8) int hists[3][kBins];
+  __shared__ int coarses[3][32], from_peer[kMaxCluster][64];
   __shared__ int n_gt[kSelWarps + 1], n_eq[kSelWarps + 1];   // per warp; last: the CTA's
   __shared__ uint32_t s_prefix;
   __shared__ int s_need, s_group;
@@ -107,7 +109,9 @@ __global__ void __launch_bounds__(kSelThreads, 2) evict_select_kernel(const __gr
   const int per = ((cand + CS - 1) / CS + 31) & ~31;
   const int lo = min(rank * per, cand), hi = min(lo + per, cand);
   const bool held = per <= p.key_slots;
-  for (int i = tid; i < kBins; i += kSelThreads) hist[i] = 0;
+  for (int i = tid; i < 3 * kBins; i += kSelThreads) hists[0][i] = 0;
+  const int quads = lo + ((hi - lo + 3) & ~3);   // the keys by fours
+  if (held && hi + tid < quads) keys[hi + tid - lo] = 0;   // below every key
   __syncthreads();
   // the weights, eight loads in flight, and the first digit's histogram
   for (int j0 = lo + tid; j0 < hi; j0 += 8 * kSelThreads) {
@@ -120,21 +124,32 @@ __global__ void __launch_bounds__(kSelThreads, 2) evict_select_kernel(const __gr
       if (j >= hi) break;
       const uint32_t u = order_key(x[i]);
       if (held) keys[j - lo] = u;
-      atomicAdd(&hist[u >> 21], 1);
+      atomicAdd(&hists[0][u >> 21], 1);
     }
   }
-  auto key_at = [&](int j) { return held ? keys[j - lo] : order_key(__ldg(w + j)); };
+  // keys j .. j + 3; 0, which is below every key, past the last
+  auto four_at = [&](int j) {
+    if (held) return *reinterpret_cast<const uint4*>(keys + (j - lo));
+    auto one = [&](int i) { return i < hi ? order_key(__ldg(w + i)) : 0u; };
+    return make_uint4(one(j), one(j + 1), one(j + 2), one(j + 3));
+  };
   uint32_t prefix = 0, mask = 0;
   int need = k;   // still to take among the keys that match the prefix
 #pragma unroll 1
-  for (int shift = 21;; shift = shift == 21 ? 10 : 0) {
+  for (int shift = 21, digits = 0;; shift = shift == 21 ? 10 : 0, ++digits) {
     const uint32_t digit = shift == 0 ? 0x3ffu : 0x7ffu;
+    int *hist = hists[digits], *coarse = coarses[digits];
     if (shift != 21) {
-      for (int i = tid; i < kBins; i += kSelThreads) hist[i] = 0;
-      __syncthreads();
-      for (int j = lo + tid; j < hi; j += kSelThreads) {
-        const uint32_t u = key_at(j);
+      // no key's first digit is 0, so the zeros past the last match no prefix
+      auto count = [&](uint32_t u) {
         if ((u & mask) == prefix) atomicAdd(&hist[(u >> shift) & digit], 1);
+      };
+      for (int j = lo + 4 * tid; j < quads; j += 4 * kSelThreads) {
+        const uint4 u = four_at(j);
+        count(u.x);
+        count(u.y);
+        count(u.z);
+        count(u.w);
       }
     }
     __syncthreads();
@@ -146,8 +161,8 @@ __global__ void __launch_bounds__(kSelThreads, 2) evict_select_kernel(const __gr
       const int c = __reduce_add_sync(0xffffffffu, two.x + two.y);
       if (lane == 0) coarse[warp] = c;
     }
-    __syncthreads();
     if (CS > 1) cluster_sync();
+    else __syncthreads();
     if (warp < CS) from_peer[warp][lane] = ld_dsmem_s32(mapa_shared(smem_u32(&coarse[lane]), warp));
     __syncthreads();
     if (warp == 0) {
@@ -192,7 +207,6 @@ __global__ void __launch_bounds__(kSelThreads, 2) evict_select_kernel(const __gr
       }
     }
     __syncthreads();
-    if (CS > 1 && shift != 0) cluster_sync();   // the peers' counts have been read
     prefix = s_prefix;
     need = s_need;
     mask |= digit << shift;
@@ -201,15 +215,16 @@ __global__ void __launch_bounds__(kSelThreads, 2) evict_select_kernel(const __gr
   }
   // keys above the threshold, and the first `need` of those equal to it: counts
   // of each warp's run of keys, then their places
-  const int run = ((per + kSelWarps - 1) / kSelWarps + 31) & ~31;
-  const int r0 = min(lo + warp * run, hi), r1 = min(r0 + run, hi);
+  const int run = ((per + kSelWarps - 1) / kSelWarps + 127) & ~127;
+  const int r0 = min(lo + warp * run, quads), r1 = min(r0 + run, quads);
   int gt = 0, eq = 0;
-  for (int j = r0; j < r1; j += 32) {
-    const bool in = j + lane < r1;
-    const uint32_t u = in ? key_at(j + lane) : 0u;
-    gt += __popc(__ballot_sync(0xffffffffu, in && u > prefix));
-    eq += __popc(__ballot_sync(0xffffffffu, in && u == prefix));
+  for (int j = r0 + 4 * lane; j < r1; j += 128) {
+    const uint4 u = four_at(j);
+    gt += (u.x > prefix) + (u.y > prefix) + (u.z > prefix) + (u.w > prefix);
+    eq += (u.x == prefix) + (u.y == prefix) + (u.z == prefix) + (u.w == prefix);
   }
+  gt = __reduce_add_sync(0xffffffffu, gt);
+  eq = __reduce_add_sync(0xffffffffu, eq);
   if (lane == 0) {
     n_gt[warp] = gt;
     n_eq[warp] = eq;
@@ -243,19 +258,41 @@ __global__ void __launch_bounds__(kSelThreads, 2) evict_select_kernel(const __gr
     const int y = lane < CS ? ld_dsmem_s32(mapa_shared(smem_u32(&n_eq[kSelWarps]), lane)) : 0;
     gt += __reduce_add_sync(0xffffffffu, lane < rank ? x : 0);
     eq += __reduce_add_sync(0xffffffffu, lane < rank ? y : 0);
-    cluster_sync();   // no CTA leaves before its counts have been read
+    cluster_arrive();
   }
-  const uint32_t below = (1u << lane) - 1u;
-  for (int j = r0; j < r1; j += 32) {
-    const bool in = j + lane < r1;
-    const uint32_t u = in ? key_at(j + lane) : 0u;
-    const bool is_gt = in && u > prefix, is_eq = in && u == prefix;
-    const uint32_t bg = __ballot_sync(0xffffffffu, is_gt), be = __ballot_sync(0xffffffffu, is_eq);
-    const int e = eq + __popc(be & below);   // equal keys before this one
-    if (is_gt || (is_eq && e < need)) kept[gt + __popc(bg & below) + min(e, need)] = j + lane;
-    gt += __popc(bg);
-    eq += __popc(be);
+  for (int j0 = r0; j0 < r1; j0 += 128) {
+    const int j = j0 + 4 * lane;
+    const uint4 u = j < r1 ? four_at(j) : make_uint4(0, 0, 0, 0);
+    const uint32_t x[4] = {u.x, u.y, u.z, u.w};
+    int c = 0;   // above in the low half, equal in the high half
+#pragma unroll
+    for (int i = 0; i < 4; ++i) c += (x[i] > prefix) + ((x[i] == prefix) << 16);
+    int to = c;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int y = __shfl_up_sync(0xffffffffu, to, o);
+      if (lane >= o) to += y;
+    }
+    const int all = __shfl_sync(0xffffffffu, to, 31);
+    to -= c;
+    int above = gt + (to & 0xffff), e = eq + (to >> 16);   // before this lane's keys
+    if (c != 0) {
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        if (x[i] > prefix) {
+          kept[above + min(e, need)] = j + i;
+          ++above;
+        } else if (x[i] == prefix) {
+          if (e < need) kept[above + e] = j + i;
+          ++e;
+        }
+      }
+    }
+    __syncwarp();
+    gt += all & 0xffff;
+    eq += all >> 16;
   }
+  if (CS > 1) cluster_wait();   // no CTA leaves before its counts have been read
 }
 
 // Grid (blocks, heads, sequences); the last block of x moves the weights.  Four
