@@ -276,19 +276,13 @@ __global__ void __launch_bounds__(kSelThreads, 2) evict_select_kernel(const __gr
     const int all = __shfl_sync(0xffffffffu, to, 31);
     to -= c;
     int above = gt + (to & 0xffff), e = eq + (to >> 16);   // before this lane's keys
-    if (c != 0) {
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        if (x[i] > prefix) {
-          kept[above + min(e, need)] = j + i;
-          ++above;
-        } else if (x[i] == prefix) {
-          if (e < need) kept[above + e] = j + i;
-          ++e;
-        }
-      }
+    for (int i = 0; i < 4; ++i) {
+      const bool is_gt = x[i] > prefix, is_eq = x[i] == prefix;
+      if (is_gt || (is_eq && e < need)) kept[above + min(e, need)] = j + i;
+      above += is_gt;
+      e += is_eq;
     }
-    __syncwarp();
     gt += all & 0xffff;
     eq += all >> 16;
   }
