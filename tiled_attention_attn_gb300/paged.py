@@ -331,8 +331,9 @@ _CHUNK, _DECODE, _WEIGHTS = 0, 1, 2   # ATTN_PAGED_*
 
 def _workspace(device: torch.device, stream: int, d: int, call: int) -> torch.Tensor:
     """Scratch memory of one call.  Each thread keeps what it used last on a
-    stream (calls of a thread on a stream are ordered; at most 8 are kept); a
-    captured call gets memory of its own, which its graph keeps."""
+    stream (calls of a thread on a stream are ordered; at most 8 are kept, of up
+    to 41 MB each); a captured call gets memory of its own, which its graph
+    keeps."""
     kept = _ws_kept.__dict__
     key = (device.index, stream, d, call)
     capturing = torch.cuda.is_current_stream_capturing()
