@@ -488,13 +488,14 @@ int attn_decode_paged(const void *q, void *o, float *lse, int B, int Hq, const a
  * over the heads h of group g and the queries i of sequence b that see key j.
  * q, cu_seqlens_q, causal and scale as attn_fwd_paged was given them and lse
  * (Hq, total_q) as it returned it (or attn_decode_paged, with cu_seqlens_q =
- * {0, 1, ..., B}); a query with lse = -inf adds nothing.  weights (B,
+ * {0, 1, ..., B}); a query with lse = -inf or +inf adds nothing, whatever its q
+ * holds (set -inf to leave a query out); a NaN gives NaN weights.  weights (B,
  * num_kv_heads, weights_len) fp32, entries j >= seqlens_k[b] are left as they
  * are; decay = 0 does not read what was there.  weights_len at least
  * every seqlens_k[b] (a longer sequence is taken as bad); scale 0 or at least
- * 2^-20.  cache->v is not
- * read and may be null.  The sums' order depends on the lengths alone: the same
- * call gives the same bits.  workspace as above, for ATTN_PAGED_WEIGHTS.
+ * 2^-20; in fp16 |q . k| at most 2^29.  cache->v is not read and may be null.
+ * The sums' order depends on the lengths alone: the same call gives the same
+ * bits.  workspace as above, for ATTN_PAGED_WEIGHTS.
  */
 int attn_key_weights(const void *q, const float *lse, float *weights, int weights_len, int B, int Hq, int total_q,
                      const attn_paged_kv *cache, const int *cu_seqlens_q, int causal, float scale, float decay,

@@ -1,0 +1,106 @@
+"""Values at which the paged-cache operators can go wrong: queries left out of
+the key weights, scores far from the ordinary, NaN in keys and queries that are
+seen, many light keys, positions far out.  Tolerances are derived here or in
+paged_reference."""
+
+import math
+from fractions import Fraction
+
+import pytest
+import torch
+
+from . import paged_reference as ref
+from .paged_reference import INF, Cache, cu_of
+from tiled_attention_attn_gb300 import attn, paged
+
+pytestmark = pytest.mark.gpu
+BF, HF = torch.bfloat16, torch.float16
+
+
+@pytest.fixture(scope="module", autouse=True)
+def _lib(attn_lib):
+    if not torch.cuda.is_available():
+        pytest.skip("no CUDA device")
+    attn.set_wait_timeout_ns(2_000_000_000)
+    return attn_lib
+
+
+def queries(lens, hq, d, dtype, seed):
+    return torch.randn(sum(lens), hq, d, generator=torch.Generator().manual_seed(seed)).to(dtype).cuda()
+
+
+def ok():
+    torch.cuda.synchronize()
+    assert attn.get_error() == attn.ATTN_OK, hex(attn.last_device_error())
+
+
+# ---------------------------------------------------------------- key weights
+
+def check_key_weights(w, q, c, lse, lq, causal, scale):
+    """Bar, relative to the sum: the scores' error; lse / scale added to the
+    score in fp32 (up to four truncated additions of a magnitude of |lse| +
+    |score|, 2^-23 each); the exponential of a sum within 2^-22; m G additions."""
+    at = 0
+    for b, m in enumerate(lq):
+        k = c.rows(c.k, b)
+        lb = lse[:, at:at + m]
+        r = ref.key_weights(q[at:at + m], k, lb, causal, scale)
+        fin = lb[torch.isfinite(lb) & (lb.abs() < 1e30)]
+        big = float(fin.abs().max()) if fin.numel() else 0.0
+        ds = ref.score_error(q[at:at + m], k, scale) + big * 2.0 ** -21
+        rel = math.expm1(2 * ds) + 2.0 ** -16 + m * (q.shape[1] // c.hkv) * 2.0 ** -24
+        err = (w[b, :, :c.lens[b]].double() - r).abs()
+        bar = rel * r + 2.0 ** -126
+        assert bool((err <= bar).all()), (b, float((err / bar).max()))
+        at += m
+
+
+LEFT_OUT = [
+    # new tokens, keys, Hq, Hkv, d, page, causal: tiles of 128 columns, of 16 (one token each), both forms of each
+    ([300, 40], [500, 40], 8, 2, 128, 16, True),
+    ([300, 130], [700, 300], 4, 4, 64, 32, False),
+    ([1, 1, 1, 1, 1], [5, 129, 700, 3000, 260], 8, 2, 128, 16, True),
+    ([1, 1, 1], [256, 2000, 17], 5, 1, 64, 64, False),
+    ([40, 3], [9000, 300], 3, 1, 64, 64, True),
+]
+
+
+@pytest.mark.parametrize("dtype", [BF, HF], ids=["bf16", "fp16"])
+@pytest.mark.parametrize("value", [-INF, INF, 3.4e38])
+@pytest.mark.parametrize("case", LEFT_OUT, ids=[f"case{i}" for i in range(len(LEFT_OUT))])
+def test_queries_left_out_add_nothing(case, value, dtype):
+    # lse = -inf leaves a query out, whatever the query holds; +inf and the
+    # type's largest value give weights of zero by the formula
+    lq, lk, hq, hkv, d, page, causal = case
+    c = Cache(lk, hkv, d, page, dtype, seed=2)
+    q = queries(lq, hq, d, dtype, 3)
+    scale = 1.0 / math.sqrt(d)
+    _, lse = attn.attn_fwd_paged(q, *c.args(), cu_of(lq), causal=causal)
+    g = torch.Generator().manual_seed(5)
+    out = (torch.rand(lse.shape, generator=g) < 0.3).cuda()
+    out[:, 0] = True                       # all heads of a token
+    out[0] |= torch.arange(lse.shape[1], device="cuda") % 2 == 0
+    lse[out] = value
+    given = q.clone()
+    if value == -INF:
+        given[out.t()] = torch.tensor([float("nan"), INF, -INF, 1.0], dtype=dtype, device="cuda").repeat(d // 4)
+    w = attn.key_weights(given, c.k, lse, c.table, c.seqlens, cu_of(lq), causal=causal)
+    ok()
+    check_key_weights(w, q, c, lse, lq, causal, scale)
+
+
+@pytest.mark.parametrize("dtype", [BF, HF], ids=["bf16", "fp16"])
+@pytest.mark.parametrize("scale, q_gain, k_gain", [(0.0, 1.0, 1.0), (2.0 ** -20, 1.0, 1.0), (2.0 ** -20, 1000.0, 20000.0),
+                                                   (2.0 ** -10, 1.0, 1.0), (2.0 ** -10, 100.0, 300.0), (0.125, 8.0, 8.0),
+                                                   (2.0, 1.0, 1.0), (2.0, 3.0, 4.0)])
+@pytest.mark.parametrize("lq, lk", [([200, 30], [300, 500]), ([1, 1], [300, 500])], ids=["chunk", "decode"])
+def test_key_weights_of_any_scale(lq, lk, scale, q_gain, k_gain, dtype):
+    # scale 0 (no products), the smallest scale, |lse| into the hundreds and
+    # |lse / scale| past 4e8
+    c = Cache(lk, 2, 64, 16, dtype, seed=6)
+    c.k.mul_(k_gain).clamp_(-60000.0, 60000.0)   # (finite in fp16: 20000 x 3.3 would not be)
+    q = queries(lq, 6, 64, dtype, 7) * q_gain
+    _, lse = attn.attn_fwd_paged(q, *c.args(), cu_of(lq), scale=scale)
+    w = attn.key_weights(q, c.k, lse, c.table, c.seqlens, cu_of(lq), scale=scale)
+    ok()
+    check_key_weights(w, q, c, lse, lq, True, scale)

@@ -82,7 +82,7 @@ int attn_key_weights(const void* q, const float* lse, float* weights, int weight
   using namespace attn;
   PagedKV c;
   if (int rc = check(cache, B, false, q, lse, Hq, total_q, causal, scale, workspace, workspace_bytes, c)) return rc;
-  // (a scale below 2^-20 would put lse / scale out of the 16-bit pieces' range)
+  // (below 2^-20 a left-out query's -kFar scale, in fp16, would come near exp2's range)
   if (scale != 0.0f && scale < 0x1p-20f) return ATTN_EINVAL;
   if (!weights || !cu_seqlens_q || !ptr_aligned(weights, 4) || weights_len <= 0 || !std::isfinite(decay)) return ATTN_EINVAL;
   DeviceInfo info;

@@ -15,11 +15,15 @@
 // The lse is a column's, the same for all threads.  Read from shared memory it
 // costs as much of the 128 bytes a clock that an SM returns to registers as the
 // scores themselves (with TMEM's 64 KB a tile, 2,300 clocks a query tile).  So
-// the MMA subtracts it: K gets 16 more features (ALPHA, 1, 1, 0 ...), and a
+// the MMA subtracts it: K gets 16 more features (ALPHA, BETA, 1, 0 ...), and a
 // query row -lse / scale in three pieces of the 16-bit type, each the rest that
 // the one before leaves (24 bits and more), times those.  One MMA more a tile,
 // and the thread's work is a multiplication, an exponential and an addition a
 // score.
+//
+// A query with an infinite lse is left out: a number far below any score takes
+// the place of -lse / scale, and its row of Q is zeroed in shared memory, so that
+// it adds nothing whatever it holds (a NaN included).
 //
 // NT, the columns of a query tile: 128 for chunks; 16 when a sequence has few
 // rows (one token's heads), where a 128-row box would fetch mostly other
@@ -57,7 +61,6 @@ constexpr int kWSum = 5;
 constexpr int kKeys = 256;       // keys per unit
 constexpr int kMinTiles = 4;     // pieces of a cut unit are at least about this long
 constexpr float kLog2e = 1.4426950408889634f;
-constexpr float kFar = 2.0e9f;     // exp2(-kFar scale log2 e) is 0 for every scale from 2^-20
 
 struct Params {
   CUtensorMap tm_q;    // (d, Hq, total, 1), box 64 x heads x span x 1
@@ -186,9 +189,19 @@ struct Tiles {
   __device__ bool active(int x) const { return tok >= (x == 0 ? tok_min[0] : tok_min[1]); }
 };
 
-// Coefficient of the first piece of lse / scale: fp16 reaches 65504 times it.
+// lse / scale = kAlpha p0 + kBeta p1 + p2, pieces in the 16-bit type.  bf16 has
+// the range of fp32.  In fp16 |p0| <= 65504, and half its largest step times
+// kAlpha, 2^19, is the most that is left for p1: 2^14 with kBeta, whose half step
+// times kBeta, 2^8, is left for p2.
 template <bool BF16>
 constexpr float kAlpha = BF16 ? 1.0f : 32768.0f;
+template <bool BF16>
+constexpr float kBeta = BF16 ? 1.0f : 32.0f;
+// The largest |lse / scale|, exactly kAlpha times a p0: about 2^31 in fp16.
+// exp2(-kFar scale log2 e) is 0 for every scale from 2^-20, so a larger lse gives
+// the formula's weights, 0 or infinity, for scores up to kFar / 2.
+template <bool BF16>
+constexpr float kFar = BF16 ? 0x1p120f : 61024.0f * 32768.0f;
 
 // Byte offset of row r of a tile of 16 features without swizzle: 8 x 16-byte
 // core matrices, the two of a row group side by side.
@@ -212,7 +225,7 @@ struct WCfg {
   static constexpr int kOffL = kOffA + 128 * 32;          // ... and of each stage's query rows
   static constexpr int kThr = 32 * (kWSum + 8);
   static constexpr int kOffBar = kOffL + kQS * NT * 32;
-  static constexpr int kNBars = 3 * kKS + 2 * kQS + 8 + 2;
+  static constexpr int kNBars = 3 * kKS + 3 * kQS + 8 + 2;
   static constexpr int kOffMisc = kOffBar + (kNBars + 1) / 2 * 16;
   static constexpr int kSmem = kOffMisc + 384 + 1024;   // (2 sums a warp from kOffMisc + 32)
   static constexpr uint32_t kTmemCols = 4 * NT;           // [key tile][buffer]
@@ -267,6 +280,19 @@ __device__ __forceinline__ void add_tile(uint32_t t_s, float2 c2, int lo, int hi
   }
 }
 
+// Zeroes this lane's rows of a query tile whose lse is infinite (bit k of `out`:
+// row lane + 32 k), once the tile has landed.  Rare, and out of line: inlined it
+// costs every call (a decoding step's weights 49.6 us against 48.7).
+__device__ __noinline__ bool zero_rows(uint32_t bar, uint32_t parity, WaitCtl wc, uint8_t* tile, int chunk, int chunks,
+                                       uint32_t out) {
+  if (!mbar_wait_warp(bar, parity, wc, ATTN_DEVERR_WAIT_TIMEOUT_SITE(kSiteQFull))) return false;
+  for (int r = threadIdx.x & 31; out; r += 32, out >>= 1)
+    if (out & 1)
+      for (int y = 0; y < 8 * chunks; ++y)
+        *reinterpret_cast<uint4*>(tile + (y >> 3) * chunk + r * 128 + (y & 7) * 16) = make_uint4(0, 0, 0, 0);
+  return true;
+}
+
 template <int D, int NT, bool BF16, bool CAUSAL>
 __global__ void __launch_bounds__(WCfg<D, NT>::kThr, 1) weights_kernel(const __grid_constant__ Params p) {
   using C = WCfg<D, NT>;
@@ -286,6 +312,7 @@ __global__ void __launch_bounds__(WCfg<D, NT>::kThr, 1) weights_kernel(const __g
   auto b_s_full = [&](int x, int s) { return bar2 + 8 * (2 * x + s); };
   auto b_s_free = [&](int x, int s) { return bar2 + 32 + 8 * (2 * x + s); };
   auto b_drain = [&](int x) { return bar2 + 64 + 8 * x; };
+  auto b_l_full = [&](int s) { return bar2 + 80 + 8 * s; };
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + C::kOffMisc);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + C::kOffMisc + 4);
   volatile int* start = reinterpret_cast<volatile int*>(smem + C::kOffMisc + 8);   // b, g, kb
@@ -302,8 +329,9 @@ __global__ void __launch_bounds__(WCfg<D, NT>::kThr, 1) weights_kernel(const __g
       mbar_init(b_k_empty(s), 2);   // the two issuers
     }
     for (int s = 0; s < C::kQS; ++s) {
-      mbar_init(b_q_full(s), 2);   // the tile, and its lse features
+      mbar_init(b_q_full(s), 1);
       mbar_init(b_q_empty(s), 2);
+      mbar_init(b_l_full(s), 1);   // the lse features (and zeroed rows)
     }
     for (int x = 0; x < 2; ++x)
       for (int s = 0; s < 2; ++s) {
@@ -323,12 +351,12 @@ __global__ void __launch_bounds__(WCfg<D, NT>::kThr, 1) weights_kernel(const __g
     tmem_relinquish();
   }
 
-  // the features that take the lse: (ALPHA, 1, 1, 0 ...) for every key; of the
+  // the features that take the lse: (ALPHA, BETA, 1, 0 ...) for every key; of the
   // query rows only the first three change
   using T = typename std::conditional<BF16, __nv_bfloat16, __half>::type;
   for (int i = tid; i < 128; i += kThr) {
-    const T a(kAlpha<BF16>), one(1.0f), zero(0.0f);
-    T f[8] = {a, one, one, zero, zero, zero, zero, zero};
+    const T a(kAlpha<BF16>), b(kBeta<BF16>), one(1.0f), zero(0.0f);
+    T f[8] = {a, b, one, zero, zero, zero, zero, zero};
     *reinterpret_cast<uint4*>(smem + C::kOffA + lse_row(i)) = *reinterpret_cast<const uint4*>(f);
     *reinterpret_cast<uint4*>(smem + C::kOffA + lse_row(i) + 128) = make_uint4(0, 0, 0, 0);
   }
@@ -454,7 +482,7 @@ __global__ void __launch_bounds__(WCfg<D, NT>::kThr, 1) weights_kernel(const __g
         float l[NC];   // on its way while the stage is waited for
 #pragma unroll
         for (int k = 0; k < NC; ++k) {
-          l[k] = -INFINITY;
+          l[k] = 0.0f;   // rows past the chunk: their columns are dropped by index
           if (lane + 32 * k < NT && row_tok[k] < p.span && it.tok + row_tok[k] < w.q_len)
             l[k] = __ldg(p.lse + static_cast<long long>(head0 + row_head[k]) * p.total + row0 + row_tok[k]);
         }
@@ -468,22 +496,32 @@ __global__ void __launch_bounds__(WCfg<D, NT>::kThr, 1) weights_kernel(const __g
           for (int c = 0; c < C::kChunks; ++c)
             tma_load_4d(sQ + qs * C::kQStage + c * NT * 128, &p.tm_q, b_q_full(qs), c * 64, head0, row0, 0);
         }
+        ++q_cnt;
+        uint32_t out = 0;   // this lane's queries that are left out
+#pragma unroll
+        for (int k = 0; k < NC; ++k) out |= isinf(l[k]) ? 1u << k : 0u;
+        if (__any_sync(0xffffffffu, out != 0) &&
+            !zero_rows(b_q_full(qs), ((q_cnt - 1) / C::kQS) & 1, wc, smem + C::kOffQ + qs * C::kQStage, NT * 128,
+                       C::kChunks, out)) {
+          ok = false;
+          break;
+        }
 #pragma unroll
         for (int k = 0; k < NC; ++k) {
-          // -lse / scale, within what the pieces hold; no query, or one that saw no key: far below
-          const float v = l[k] == -INFINITY ? -kFar : fminf(fmaxf(-l[k] * p.inv_scale, -kFar), kFar);
-          const T p0 = T(v * (1.0f / kAlpha<BF16>));
-          const float r1 = l[k] != l[k] ? l[k] : v - static_cast<float>(p0) * kAlpha<BF16>;
-          const T p1 = T(r1);
-          const T p2 = T(r1 - static_cast<float>(p1));
+          // -lse / scale, within what the pieces hold; of a query left out far below every score
+          constexpr float kF = kFar<BF16>, kA = kAlpha<BF16>, kB = kBeta<BF16>;
+          const float v = isinf(l[k]) ? -kF : fminf(fmaxf(-l[k] * p.inv_scale, -kF), kF);
+          const T p0 = T(v * (1.0f / kA));
+          const float r1 = l[k] != l[k] ? l[k] : v - static_cast<float>(p0) * kA;
+          const T p1 = T(r1 * (1.0f / kB));
+          const T p2 = T(r1 - static_cast<float>(p1) * kB);
           T f[4] = {p0, p1, p2, T(0.0f)};
           if (lane + 32 * k < NT)
             *reinterpret_cast<uint2*>(smem + C::kOffL + qs * NT * 32 + lse_row(lane + 32 * k)) = *reinterpret_cast<const uint2*>(f);
         }
         fence_proxy_async_smem();
         __syncwarp();
-        if (lane == 0) mbar_arrive(b_q_full(qs));
-        ++q_cnt;
+        if (lane == 0) mbar_arrive(b_l_full(qs));
       }
     }
     if (lane == 0 && *abort_flag) {
@@ -524,7 +562,8 @@ __global__ void __launch_bounds__(WCfg<D, NT>::kThr, 1) weights_kernel(const __g
         ++k_cnt;
         for (int i = w.t0; i < w.t1 && ok; ++i, it.next()) {
           const int qs = q_cnt % C::kQS;
-          if (!mbar_wait(b_q_full(qs), (q_cnt / C::kQS) & 1, wc, ATTN_DEVERR_WAIT_TIMEOUT_SITE(kSiteQFull))) {
+          if (!mbar_wait(b_l_full(qs), (q_cnt / C::kQS) & 1, wc, ATTN_DEVERR_WAIT_TIMEOUT_SITE(kSiteQFull)) ||
+              !mbar_wait(b_q_full(qs), (q_cnt / C::kQS) & 1, wc, ATTN_DEVERR_WAIT_TIMEOUT_SITE(kSiteQFull))) {
             ok = false;
             break;
           }

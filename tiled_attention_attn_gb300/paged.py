@@ -423,6 +423,7 @@ def key_weights(q: torch.Tensor, k_pages: torch.Tensor, lse: torch.Tensor, page_
     query heads of the key's head: weights = decay * weights + added.  q,
     cu_seqlens, causal and scale as the attention call had them, lse (Hq, total)
     as it returned it; after ``attn_decode_paged`` cu_seqlens is 0, 1, ..., B.
+    A query whose lse is infinite is left out, whatever it holds.
     Entries past seqlens_k[b] are left as they are.  Without ``weights`` a new
     zeroed (B, Hkv, max_pages * page_size) tensor is returned."""
     c = _cache(k_pages, None, page_table, seqlens_k)
