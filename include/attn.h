@@ -461,7 +461,8 @@ long long attn_paged_workspace_bytes(int d, int call);
  * sequence b's queries cu_seqlens_q[b] .. cu_seqlens_q[b + 1] - 1; lse (Hq,
  * total_q) fp32.  Causal aligns bottom-right: query i of Lq_b sees key j iff
  * j <= i + seqlens_k[b] - Lq_b.  A query that sees no key gives O = 0 and
- * lse = -inf; rows outside every sequence are left as they are.  Hq a multiple
+ * lse = -inf, one that sees a NaN score NaN; rows outside every sequence are
+ * left as they are.  Hq a multiple
  * of num_kv_heads, scale finite and not negative, B <= 65535.
  * workspace: 256-byte aligned, attn_paged_workspace_bytes(d,
  * ATTN_PAGED_CHUNK) bytes.
@@ -473,7 +474,8 @@ int attn_fwd_paged(const void *q, void *o, float *lse, int B, int Hq, int total_
 /*
  * attn_decode_paged -- one decoding step over a paged cache: attn_decode with
  * the keys in pages, one query per sequence.  q, o (B, Hq, d) contiguous, lse
- * (Hq, B) fp32; a sequence without keys gives O = 0 and lse = -inf.  Any Hq
+ * (Hq, B) fp32; a sequence without keys gives O = 0 and lse = -inf, a NaN score
+ * NaN.  Any Hq
  * that is a multiple of num_kv_heads; B <= 65535.  workspace as above, for
  * ATTN_PAGED_DECODE.
  */

@@ -104,3 +104,50 @@ def test_key_weights_of_any_scale(lq, lk, scale, q_gain, k_gain, dtype):
     w = attn.key_weights(q, c.k, lse, c.table, c.seqlens, cu_of(lq), scale=scale)
     ok()
     check_key_weights(w, q, c, lse, lq, True, scale)
+
+
+# ---------------------------------------------------------------- NaN that is seen
+
+def where_key(c, b, j):
+    return int(c.table[b, j // c.page]), j % c.page
+
+
+@pytest.mark.parametrize("dtype", [BF, HF], ids=["bf16", "fp16"])
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("n, j", [(60, 3), (700, 699), (40000, 5), (40000, 39990)])
+def test_nan_reaches_every_query_that_sees_it(n, j, d, dtype):
+    """A NaN in a key makes O and lse of the queries that see it NaN, as the
+    formula does, also where the cache is cut into pieces; nothing else."""
+    nan = float("nan")
+    c = Cache([n, 300], 2, d, 16, dtype, seed=4)
+    q1, q2, cu = queries([1, 1], 8, d, dtype, 5), queries([20, 9], 8, d, dtype, 6), cu_of([20, 9])
+    want1, want2 = attn.attn_decode_paged(q1, *c.args()), attn.attn_fwd_paged(q2, *c.args(), cu)
+    page, slot = where_key(c, 0, j)
+    c.k[page, slot, 0] = nan                       # the first head's key
+    o, lse = attn.attn_decode_paged(q1, *c.args())
+    ok()
+    assert bool(o[0, :4].isnan().all()) and bool(lse[:4, 0].isnan().all())
+    keep = torch.ones(2, 8, dtype=torch.bool, device="cuda")
+    keep[0, :4] = False
+    assert torch.equal(o[keep], want1[0][keep]) and torch.equal(lse.t()[keep], want1[1].t()[keep])
+    o, lse = attn.attn_fwd_paged(q2, *c.args(), cu)
+    ok()
+    sees = torch.arange(20, device="cuda") >= j - (n - 20)
+    gone = torch.zeros(29, 8, dtype=torch.bool, device="cuda")
+    gone[:20, :4] = sees[:, None]
+    assert bool(o[gone].isnan().all()) and bool(lse.t()[gone].isnan().all())
+    assert torch.equal(o[~gone], want2[0][~gone]) and torch.equal(lse.t()[~gone], want2[1].t()[~gone])
+
+
+@pytest.mark.parametrize("n", [60, 40000])
+def test_nan_in_a_query(n):
+    c = Cache([n, 300], 2, 128, 16, BF, seed=4)
+    q1, q2, cu = queries([1, 1], 8, 128, BF, 5), queries([20, 9], 8, 128, BF, 6), cu_of([20, 9])
+    want1, want2 = attn.attn_decode_paged(q1, *c.args()), attn.attn_fwd_paged(q2, *c.args(), cu)
+    q1[0, 3, 70] = q2[4, 5, 0] = float("nan")
+    for q, (o0, l0), (o, lse) in ((q1, want1, attn.attn_decode_paged(q1, *c.args())),
+                                  (q2, want2, attn.attn_fwd_paged(q2, *c.args(), cu))):
+        ok()
+        gone = q.isnan().any(-1)
+        assert bool(o[gone].isnan().all()) and bool(lse.t()[gone].isnan().all())
+        assert torch.equal(o[~gone], o0[~gone]) and torch.equal(lse.t()[~gone], l0.t()[~gone])

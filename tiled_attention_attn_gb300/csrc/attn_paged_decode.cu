@@ -630,7 +630,7 @@ __global__ void __launch_bounds__(kThreads, 1) decode_kernel(const __grid_consta
 #pragma unroll
         for (int h = 0; h < GT; ++h) {
           if (h >= G) break;
-          const float v = (l[h] > 0.0f) ? o[h] / l[h] : 0.0f;
+          const float v = (l[h] != 0.0f) ? o[h] / l[h] : 0.0f;   // 0: saw no key; a NaN stays one
           if (whole) reinterpret_cast<T*>(p.o)[(orow0 + h) * DA + lrow] = T(v);
           else p.part_o[(static_cast<size_t>(slot) * kNQ + h) * DA + lrow] = v;
         }
@@ -645,9 +645,9 @@ __global__ void __launch_bounds__(kThreads, 1) decode_kernel(const __grid_consta
           }
         if (whole)
           p.lse[static_cast<size_t>(head0 + lane) * p.B + w.b] =
-              (lv > 0.0f) ? mv * 0.69314718055994531f + __logf(lv) : -INFINITY;
+              (lv != 0.0f) ? mv * 0.69314718055994531f + __logf(lv) : -INFINITY;
         else
-          p.part_ml[slot * kNQ + lane] = make_float2(lv > 0.0f ? mv : -INFINITY, lv);
+          p.part_ml[slot * kNQ + lane] = make_float2(mv, lv);
         // the unit's pieces lie on the ranges p / range ... (p + T - 1) / range
         if (!whole && w.t0 == 0 && lane == 0)
           p.rec[blockIdx.x] = make_int4(w.b, unit, static_cast<int>((w.p + w.T - 1) / range) - range_id + 1, 0);
@@ -701,7 +701,7 @@ __global__ void __launch_bounds__(128) decode_merge_kernel(const __grid_constant
     }
 #pragma unroll
     for (int u = 0; u < 4; ++u) {
-      if (ml[u].x == -INFINITY) continue;
+      if (ml[u].y == 0.0f) continue;   // (l of NaN: the sums become NaN, whatever m)
       const float mn = fmaxf(M, ml[u].x);
       const float r = M == -INFINITY ? 0.0f : ex2_approx(M - mn), wt = ex2_approx(ml[u].x - mn) * ml[u].y;
       M = mn;
@@ -723,16 +723,16 @@ __global__ void __launch_bounds__(128) decode_merge_kernel(const __grid_constant
     float Lt = 0.0f, at = 0.0f;
 #pragma unroll
     for (int k = 0; k < 4; ++k) {
-      if (s_m[k] == -INFINITY) continue;
+      if (s_l[k] == 0.0f) continue;
       const float r = ex2_approx(s_m[k] - Mx);
       Lt += s_l[k] * r;
       at += s_o[k][i] * r;
     }
     using T = typename std::conditional<BF16, __nv_bfloat16, __half>::type;
     const int head = g * p.group + part * p.heads + h;
-    reinterpret_cast<T*>(p.o)[(static_cast<size_t>(rec.x) * p.Hq + head) * DA + i] = T(Lt > 0.0f ? at / Lt : 0.0f);
+    reinterpret_cast<T*>(p.o)[(static_cast<size_t>(rec.x) * p.Hq + head) * DA + i] = T(Lt != 0.0f ? at / Lt : 0.0f);
     if (i == 0)
-      p.lse[static_cast<size_t>(head) * p.B + rec.x] = Lt > 0.0f ? Mx * 0.69314718055994531f + __logf(Lt) : -INFINITY;
+      p.lse[static_cast<size_t>(head) * p.B + rec.x] = Lt != 0.0f ? Mx * 0.69314718055994531f + __logf(Lt) : -INFINITY;
   }
 }
 

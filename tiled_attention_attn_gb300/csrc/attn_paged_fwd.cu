@@ -524,7 +524,7 @@ __global__ void __launch_bounds__(kThreads, 1) fwd_kernel(const __grid_constant_
         tc_fence_after();
       }
       const bool whole = w.t1 - w.t0 == w.n;
-      const float inv_l = (n_act > 0 && st.l > 0.0f) ? 1.0f / st.l : 0.0f;
+      const float inv_l = (st.l != 0.0f) ? 1.0f / st.l : 0.0f;   // 0: saw no key; a NaN stays one
       if (whole) {
         // O = u / l, lse = m / log2(e) + ln l
         T* dst = out + (static_cast<size_t>(w.row_q + qrow) * p.Hq + head0 + r_head) * D;
@@ -554,7 +554,7 @@ __global__ void __launch_bounds__(kThreads, 1) fwd_kernel(const __grid_constant_
         }
         if (row_valid)
           p.lse[static_cast<size_t>(head0 + r_head) * p.total + w.row_q + qrow] =
-              (st.l > 0.0f) ? st.m * 0.69314718055994531f + __logf(st.l) : -INFINITY;
+              (st.l != 0.0f) ? st.m * 0.69314718055994531f + __logf(st.l) : -INFINITY;
       } else {
         // a piece: O_s = u_s / l_s and (m, l) in fp32; a warp's 32 rows of one
         // 4-column group are 512 contiguous bytes
@@ -575,8 +575,7 @@ __global__ void __launch_bounds__(kThreads, 1) fwd_kernel(const __grid_constant_
           }
         }
         if (row_valid)
-          reinterpret_cast<float2*>(p.part_ml)[slot * kBM + row] =
-              make_float2(inv_l > 0.0f ? st.m : -INFINITY, inv_l > 0.0f ? st.l : 0.0f);
+          reinterpret_cast<float2*>(p.part_ml)[slot * kBM + row] = make_float2(st.m, st.l);
         // the unit's pieces lie on CTAs p / range ... (p + n - 1) / range
         if (w.t0 == 0 && warp == 0 && lane == 0)
           p.rec[blockIdx.x] = make_int4(w.b, w.hc, w.mb,
@@ -622,35 +621,33 @@ __global__ void __launch_bounds__(2 * kBM, 4) fwd_merge_kernel(const __grid_cons
   float L = 0.0f, acc[16];
 #pragma unroll
   for (int i = 0; i < 16; ++i) acc[i] = 0.0f;
-  if (M != -INFINITY) {
-    for (int s0 = 0; s0 < pieces; s0 += 2) {
-      float2 mlv[2];
-      float4 x[2][4];
+  for (int s0 = 0; s0 < pieces; s0 += 2) {
+    float2 mlv[2];
+    float4 x[2][4];
 #pragma unroll
-      for (int i = 0; i < 2; ++i) {
-        const bool in = s0 + i < pieces;
-        const size_t sl = slot(in ? s0 + i : 0);
-        mlv[i] = in ? __ldcg(ml + sl * kBM) : make_float2(-INFINITY, 0.0f);
+    for (int i = 0; i < 2; ++i) {
+      const bool in = s0 + i < pieces;
+      const size_t sl = slot(in ? s0 + i : 0);
+      mlv[i] = in ? __ldcg(ml + sl * kBM) : make_float2(-INFINITY, 0.0f);
 #pragma unroll
-        for (int c = 0; c < 4; ++c)
-          x[i][c] = in ? __ldcg(p.part_o + (sl * (D / 4) + cb * 4 + c) * kBM + row) : make_float4(0, 0, 0, 0);
-      }
+      for (int c = 0; c < 4; ++c)
+        x[i][c] = in ? __ldcg(p.part_o + (sl * (D / 4) + cb * 4 + c) * kBM + row) : make_float4(0, 0, 0, 0);
+    }
 #pragma unroll
-      for (int i = 0; i < 2; ++i) {
-        if (mlv[i].x == -INFINITY) continue;   // a piece that saw no key (its O_s was never written)
-        const float wt = ex2_approx(mlv[i].x - M) * mlv[i].y;
-        L += wt;
+    for (int i = 0; i < 2; ++i) {
+      if (mlv[i].y == 0.0f) continue;   // a piece that saw no key (its O_s was never written)
+      const float wt = ex2_approx(mlv[i].x - M) * mlv[i].y;   // (l of NaN: NaN, whatever m)
+      L += wt;
 #pragma unroll
-        for (int c = 0; c < 4; ++c) {
-          acc[4 * c] += wt * x[i][c].x;
-          acc[4 * c + 1] += wt * x[i][c].y;
-          acc[4 * c + 2] += wt * x[i][c].z;
-          acc[4 * c + 3] += wt * x[i][c].w;
-        }
+      for (int c = 0; c < 4; ++c) {
+        acc[4 * c] += wt * x[i][c].x;
+        acc[4 * c + 1] += wt * x[i][c].y;
+        acc[4 * c + 2] += wt * x[i][c].z;
+        acc[4 * c + 3] += wt * x[i][c].w;
       }
     }
   }
-  const float inv = (L > 0.0f) ? 1.0f / L : 0.0f;
+  const float inv = (L != 0.0f) ? 1.0f / L : 0.0f;
   const int head = g * p.group + part * p.heads + r_head;
   uint4* d4 = reinterpret_cast<uint4*>(reinterpret_cast<T*>(p.o) +
                                        (static_cast<size_t>(row_q + qrow) * p.Hq + head) * D + cb * 16);
@@ -662,7 +659,7 @@ __global__ void __launch_bounds__(2 * kBM, 4) fwd_merge_kernel(const __grid_cons
                        pack2<BF16>(acc[8 * i + 6] * inv, acc[8 * i + 7] * inv));
   if (cb == 0)
     p.lse[static_cast<size_t>(head) * p.total + row_q + qrow] =
-        (L > 0.0f) ? M * 0.69314718055994531f + __logf(L) : -INFINITY;
+        (L != 0.0f) ? M * 0.69314718055994531f + __logf(L) : -INFINITY;
 }
 
 template <int D, bool BF16, bool CAUSAL>
