@@ -151,3 +151,49 @@ def test_nan_in_a_query(n):
         gone = q.isnan().any(-1)
         assert bool(o[gone].isnan().all()) and bool(lse.t()[gone].isnan().all())
         assert torch.equal(o[~gone], o0[~gone]) and torch.equal(lse.t()[~gone], l0.t()[~gone])
+
+
+# ---------------------------------------------------------------- many light keys
+
+@pytest.mark.parametrize("heavy", [0.0, 1.0])
+@pytest.mark.parametrize("decode", [True, False], ids=["decode", "chunk"])
+@pytest.mark.parametrize("d", [64, 128])
+def test_many_light_keys_count_in_fp16(d, decode, heavy):
+    """One heavy key of value `heavy` before 65,535 of value 1 and weight e^-17.5
+    (2^-25.2) each, 1.6e-3 of the sum together: O = (heavy + light) / (1 + light).
+    Sequences (all on the same pages) or queries so many that no unit is cut.
+    Bar of O: its rounding, half a step (2^-11 of it); of a weight half a step too,
+    or, below the normal range, 2^-32 of the largest; and of u, which the tensor
+    core accumulates key by key in fp32, truncating, 2^-23 of its magnitude a key
+    (with heavy = 1 that alone is 8e-3: products so far below u are not in its
+    reach)."""
+    n, page, light = 65536, 64, 17.5
+    k = torch.zeros(n // page, page, 1, d, dtype=HF, device="cuda")
+    k[0, 0, 0, 0] = light
+    v = torch.ones_like(k)
+    v[0, 0] = heavy
+    scale = 1.0 / math.sqrt(d)
+    sms = torch.cuda.get_device_properties(0).multi_processor_count
+    table = torch.arange(n // page, dtype=torch.int32, device="cuda")[None]
+    B, m = (2 * sms, 1) if decode else (1, 256 * sms)
+    q = torch.zeros(B * m, 1, d, dtype=HF, device="cuda")
+    q[..., 0] = 1.0 / scale
+    top = light * float(q[0, 0, 0]) * scale
+    lens = torch.full((B,), n, dtype=torch.int32, device="cuda")
+    table = table.repeat(B, 1)
+    if decode:
+        o, lse = attn.attn_decode_paged(q, k, v, table, lens)
+    else:
+        o, lse = attn.attn_fwd_paged(q, k, v, table, lens, cu_of([m]), causal=False)
+    ok()
+    light_sum = (n - 1) * math.exp(-top)
+    total = 1.0 + light_sum
+    want = (heavy + light_sum) / total
+    bar = 2.0 ** -11 * (want + heavy) + n * 2.0 ** -32 + want * n * 2.0 ** -23 + 2.0 ** -25
+    # the sum of exponentials: a thread adds up to n / 128 + 128 terms or partial
+    # sums in fp32 to one that stays about the total, each addition off by up to
+    # 2^-24 of it (a weight of 2^-25.2 beside 1 is lost in one)
+    sums = (n / 128 + 128) * 2.0 ** -24
+    assert float((o.double() - want).abs().max()) <= bar + want * sums
+    assert heavy or light_sum > 20 * bar        # (what is at stake is well above the bar)
+    assert float((lse.double() - (top + math.log(total))).abs().max()) <= top * 2.0 ** -22 + 2.0 ** -18 + sums

@@ -224,8 +224,8 @@ struct RowState {
 // MASK, updates (m, l), writes P to TMEM and, when the max moved by more than
 // 2^8, rescales u in TMEM.  The previous tile's P.V has completed by then
 // (the commit that signalled this S was issued after it), and this tile's P.V
-// is issued only after this thread arrives.
-template <bool MASK, bool BF16, int D>
+// is issued only after this thread arrives.  P and l are relative to m - LIFT.
+template <bool MASK, bool BF16, int D, int LIFT = 0>
 __device__ __forceinline__ void softmax_tile(uint32_t t_s, uint32_t t_o, int lim, float c_log2, RowState& st,
                                              bool first) {
   // S in two halves: the second half loads while the first half's max is
@@ -272,7 +272,7 @@ __device__ __forceinline__ void softmax_tile(uint32_t t_s, uint32_t t_o, int lim
     resc = true;
     st.m = m_tile;
   }
-  const float moff = (st.m == -INFINITY) ? 0.0f : st.m;
+  const float moff = (st.m == -INFINITY) ? 0.0f : st.m - static_cast<float>(LIFT);
   // p = exp2(s * c - m): the argument with packed fp32x2 FMA, one ex2 per
   // element, row sums with packed adds; P packed to 16-bit pairs and stored
   // 32 columns at a time

@@ -19,6 +19,16 @@ struct PagedKV {
 
 constexpr int kPagedMaxB = 65535;
 
+// Softmax weights, which are at most 2^8 of the running maximum's (it lags by up
+// to that), are held times 2^kLift for the second product; so are their sums l
+// until the unit's end, where kDrop takes the factor out.  fp16 then keeps weights
+// down to 2^-32 of the maximum (2^-25 as they are): 65,535 keys of 2^-25.2 each are
+// 1.6e-3 of l, and were nothing in u.  bf16 has the range of fp32.
+template <bool BF16>
+constexpr int kLift = BF16 ? 0 : 7;
+template <bool BF16>
+constexpr float kDrop = BF16 ? 1.0f : 0x1p-7f;
+
 inline bool ptr_aligned(const void* p, uintptr_t a) { return (reinterpret_cast<uintptr_t>(p) % a) == 0; }
 
 // Checks the host struct and fills `out`.  need_v: the values are used.

@@ -8,7 +8,7 @@
 // online softmax: running maximum m, sum l and accumulator u, rescaled by
 // 2^(m_old - m_new); m may lag by up to 2^8, which cancels in u / l.  P is
 // rounded to the cache's 16-bit type for the second product (half a step of
-// each weight); S, m, l, u and the pieces' partial results are fp32.
+// each weight; kLift); S, m, l, u and the pieces' partial results are fp32.
 //
 // Bound by HBM: K and V of every sequence once.  A ring of three stages of 64
 // KB (K and V of a step) keeps up to 192 KB per SM in flight.  A page holds at
@@ -553,7 +553,7 @@ __global__ void __launch_bounds__(kThreads, 1) decode_kernel(const __grid_consta
         if (steps_total >= 2 && !pv_wait(steps_total - 2)) { ok = false; break; }
 #pragma unroll
         for (int h = 0; h < GT; ++h) {
-          const float mh = (m[h] == -INFINITY) ? 0.0f : m[h];
+          const float mh = (m[h] == -INFINITY) ? 0.0f : m[h] - kLift<BF16>;
           float e_sum = 0.0f;
 #pragma unroll
           for (int y = 0; y < kTPS; ++y) {
@@ -640,7 +640,7 @@ __global__ void __launch_bounds__(kThreads, 1) decode_kernel(const __grid_consta
 #pragma unroll
         for (int h = 0; h < GT; ++h)
           if (h == lane) {
-            lv = l[h];
+            lv = l[h] * kDrop<BF16>;
             mv = m[h];
           }
         if (whole)

@@ -7,7 +7,7 @@
 // heads of a key/value head share a tile, so that a key tile is read once for
 // all of them: 128 / heads tokens x heads rows (any group; rows left over are
 // zero queries).  P is rounded to the 16-bit type for the second product
-// (half a step of each weight); everything else is fp32.
+// (half a step of each weight; kLift); everything else is fp32.
 //
 // Pages: a 128-key tile is 128 / min(page_size, 128) boxes of 64 features for
 // K and as many for V; each lane of the producer warp loads one box at the page
@@ -168,7 +168,7 @@ __device__ __forceinline__ void softmax_masked(uint32_t t_s, uint32_t t_o, int l
   const float m_tile = (mx == -INFINITY) ? -INFINITY : mx * c_log2, m_old = st.m;
   const bool resc = m_tile > m_old && (first || m_old == -INFINITY || m_tile - m_old > 8.0f);
   if (resc) st.m = m_tile;
-  const float moff = (st.m == -INFINITY) ? 0.0f : st.m;
+  const float moff = (st.m == -INFINITY) ? 0.0f : st.m - kLift<BF16>;
   float sum = 0.0f;
   // P of columns c0 .. c0 + 31 goes to words c0 / 2 .., below the scores still to be read
 #pragma unroll 1
@@ -509,7 +509,7 @@ __global__ void __launch_bounds__(kThreads, 1) fwd_kernel(const __grid_constant_
           }
           softmax_masked<BF16, D>(t_s, t_o, lim, c_log2, st, n_act == 0);
         } else {
-          softmax_tile<false, BF16, D>(t_s, t_o, lim, c_log2, st, n_act == 0);
+          softmax_tile<false, BF16, D, kLift<BF16>>(t_s, t_o, lim, c_log2, st, n_act == 0);
         }
         tc_fence_before();
         __syncwarp();
@@ -554,7 +554,7 @@ __global__ void __launch_bounds__(kThreads, 1) fwd_kernel(const __grid_constant_
         }
         if (row_valid)
           p.lse[static_cast<size_t>(head0 + r_head) * p.total + w.row_q + qrow] =
-              (st.l != 0.0f) ? st.m * 0.69314718055994531f + __logf(st.l) : -INFINITY;
+              (st.l != 0.0f) ? st.m * 0.69314718055994531f + __logf(st.l * kDrop<BF16>) : -INFINITY;
       } else {
         // a piece: O_s = u_s / l_s and (m, l) in fp32; a warp's 32 rows of one
         // 4-column group are 512 contiguous bytes
@@ -575,7 +575,7 @@ __global__ void __launch_bounds__(kThreads, 1) fwd_kernel(const __grid_constant_
           }
         }
         if (row_valid)
-          reinterpret_cast<float2*>(p.part_ml)[slot * kBM + row] = make_float2(st.m, st.l);
+          reinterpret_cast<float2*>(p.part_ml)[slot * kBM + row] = make_float2(st.m, st.l * kDrop<BF16>);
         // the unit's pieces lie on CTAs p / range ... (p + n - 1) / range
         if (w.t0 == 0 && warp == 0 && lane == 0)
           p.rec[blockIdx.x] = make_int4(w.b, w.hc, w.mb,
