@@ -415,7 +415,8 @@ typedef struct attn_paged_kv {
  *       negative; then offsets are not allowed and cu_seqlens not needed:
  *       B = 1, L = rows).
  * The angle is reduced to a fraction of a turn in 64-bit fixed point before
- * the sine and cosine in fp32, so it is as exact at position 2^31 as near 0.
+ * the sine and cosine in fp32, so it is as exact at position 2^31 as near 0
+ * (for frequencies up to 2^40 radians per position).
  * Returns ATTN_OK, ATTN_EINVAL, ATTN_EUNSUPPORTED (device) or ATTN_ELAUNCH.
  */
 int attn_rotary_scaled(const void *x, void *y, int B, int L, int H, int d, int rot_dim, const double *freqs,

@@ -4,12 +4,13 @@
 //
 // Pair p of a token at position t turns by a = t f_p:
 //   A (x1 cos a - x2 sin a, x1 sin a + x2 cos a),
-// its gradient by -a.  The angle: f_p / 2 pi is held as a 64-bit fixed-point
-// fraction of a turn, t times it modulo 2^64 is the fraction that the pair has
-// turned at position t (whole turns fall out of the product), and its top 32
-// bits give sincospi's argument in [-1, 1) with an error of 2^-25, at any
-// position.  An fp32 product t * f_p would be off by t f_p 2^-24 radians,
-// 2^-7 at position 131072.
+// its gradient by -a.  The angle: f_p / 2 pi, formed in two doubles, is held as a
+// 64-bit fixed-point fraction of a turn, t times it modulo 2^64 is the fraction
+// that the pair has turned at position t (whole turns fall out of the product),
+// and its top 32 bits give sincospi's argument in [-1, 1).  The fraction is off by
+// t (2^-63 + |f_p| 2^-105) turns, 2^-32 at position 2^31 (for |f_p| up to 2^40),
+// the argument by the 2^-25 of its rounding to fp32.  An fp32 product t * f_p
+// would be off by t f_p 2^-24 radians, 2^-7 at position 131072.
 //
 // Bound by HBM: x read once, y written once.  A warp takes a row (token), or
 // with few rows a part of its heads: it finds the token's place, forms the
@@ -250,15 +251,32 @@ __global__ void __launch_bounds__(kThreads, 4) rope_kernel(const __grid_constant
   }
 }
 
+// The fraction of x in 64-bit fixed point, modulo 1 (both steps are exact but for
+// what lies below 2^-64).
+unsigned long long fixed_fraction(double x) {
+  const double h = x - std::nearbyint(x);   // [-0.5, 0.5]
+  const auto v = static_cast<unsigned long long>(std::fabs(h) * 18446744073709551616.0);
+  return h < 0.0 ? 0 - v : v;
+}
+
+// f / 2 pi modulo 1: 1 / 2 pi in two doubles, the product's high part and, by the
+// fused multiplication and addition, what it leaves.  (The high part comes from
+// std::fma too, so that no compiler fuses it into the subtraction that takes its
+// fraction.)
+unsigned long long turn_of(double f) {
+  constexpr double kHigh = 0.15915494309189533577, kLow = -9.839338337591243e-18;   // 1 / (2 pi)
+  const double high = std::fma(f, kHigh, 0.0);
+  const double low = std::fma(f, kLow, std::fma(f, kHigh, -high));
+  return fixed_fraction(high) + fixed_fraction(low);
+}
+
 // Checks the rotation's arguments and fills the turn table.
 int fill_turns(RopeParams& p, int rot_dim, int d, const double* freqs, float amplitude, int interleaved) {
   if (rot_dim <= 0 || rot_dim > d || (rot_dim & 1) || rot_dim > 2 * kMaxPairs || !freqs) return ATTN_EINVAL;
   if (!std::isfinite(amplitude) || (interleaved != 0 && interleaved != 1)) return ATTN_EINVAL;
   for (int i = 0; i < rot_dim / 2; ++i) {
     if (!std::isfinite(freqs[i])) return ATTN_EINVAL;
-    const double t = freqs[i] * 0.15915494309189533577;   // 1 / (2 pi)
-    const double f = t - std::floor(t);                   // [0, 1]
-    p.turns[i] = f >= 1.0 ? 0ull : static_cast<unsigned long long>(f * 18446744073709551616.0);
+    p.turns[i] = turn_of(freqs[i]);
   }
   p.rot = rot_dim;
   p.amplitude = amplitude;
