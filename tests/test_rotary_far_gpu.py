@@ -73,3 +73,17 @@ def test_angles_at_far_positions(freqs):
     y = attn.rotary_scaled(x, torch.tensor(freqs, dtype=torch.float64), positions=p)
     torch.cuda.synchronize()
     check(y, pos, freqs)
+
+
+def test_positions_that_offsets_carry_past_32_bits():
+    f = [1.0, 0.1, 0.01, 0.001]
+    x = torch.zeros(2, 5, 1, 8, dtype=HF, device="cuda")
+    x[..., :4] = 1.0
+    off = torch.tensor([(1 << 31) - 3, 7], dtype=torch.int32, device="cuda")
+    y = attn.rotary_scaled(x, torch.tensor(f, dtype=torch.float64), offsets=off)
+    z = attn.rotary_scaled(x.view(10, 1, 8), torch.tensor(f, dtype=torch.float64), offsets=off,
+                           cu_seqlens=torch.tensor([0, 5, 10], dtype=torch.int32, device="cuda"))
+    torch.cuda.synchronize()
+    pos = [(1 << 31) - 3 + i for i in range(5)] + [7 + i for i in range(5)]
+    check(y.view(10, 1, 8), pos, f)
+    assert torch.equal(z, y.view(10, 1, 8))

@@ -91,7 +91,7 @@ __device__ __forceinline__ void st1(uint16_t* p, float x) {
 
 // A row's place: its rotary position and, appending, where its token lies in
 // the pages (elements from the cache's base; negative: the row is skipped).
-__device__ __forceinline__ void locate(const RopeParams& p, long long row, int& pos, long long& at) {
+__device__ __forceinline__ void locate(const RopeParams& p, long long row, long long& pos, long long& at) {
   at = 0;
   pos = 0;
   int b, i, n = 0;
@@ -117,7 +117,7 @@ __device__ __forceinline__ void locate(const RopeParams& p, long long row, int& 
     }
     i = static_cast<int>(row - first);
   }
-  pos = i + (p.offsets ? __ldg(p.offsets + b) : 0);
+  pos = static_cast<long long>(i) + (p.offsets ? __ldg(p.offsets + b) : 0);   // (past 2^31, if so)
   if (p.append) {
     const int len = paged_len(p.cache, b, p.err);
     const int key = len - n + i;
@@ -159,13 +159,12 @@ __global__ void __launch_bounds__(kThreads, 4) rope_kernel(const __grid_constant
   for (long long task = static_cast<long long>(blockIdx.x) * kWarps + warp; task < tasks;
        task += static_cast<long long>(gridDim.x) * kWarps) {
     const int row = static_cast<int>(task / p.parts), part = static_cast<int>(task - static_cast<long long>(row) * p.parts);
-    int pos;
-    long long at;
+    long long pos, at;
     locate(p, row, pos, at);
     if (at < 0) continue;
     __syncwarp();   // the table's readers of the row before
     for (int i = lane; i < half; i += 32) {
-      const unsigned long long turn = p.turns[i] * static_cast<unsigned long long>(static_cast<long long>(pos));
+      const unsigned long long turn = p.turns[i] * static_cast<unsigned long long>(pos);
       float sn, c;
       sincospif(static_cast<float>(static_cast<int>(turn >> 32)) * 4.656612873077393e-10f, &sn, &c);   // 2^-31
       const int to = VEC ? (((i % PI) >> 1) * groups + i / PI) * 2 + (i & 1) : i;
