@@ -87,3 +87,17 @@ def test_positions_that_offsets_carry_past_32_bits():
     pos = [(1 << 31) - 3 + i for i in range(5)] + [7 + i for i in range(5)]
     check(y.view(10, 1, 8), pos, f)
     assert torch.equal(z, y.view(10, 1, 8))
+
+
+def test_frequencies_changed_before_the_backward_are_refused():
+    f, a = attn.rotary_freqs(64)
+    x = torch.randn(1, 8, 2, 64, generator=torch.Generator().manual_seed(1)).half().cuda().requires_grad_()
+    y = attn.rotary_scaled_func(x, f, a)
+    f.mul_(0.5)
+    with pytest.raises(RuntimeError, match="inplace"):
+        y.sum().backward()
+    y = attn.rotary_scaled_func(x, f.tolist(), a)      # a sequence of numbers serves too
+    y.sum().backward()
+    want = attn.rotary_scaled(torch.ones_like(x), f, a, inverse=True)
+    torch.cuda.synchronize()
+    assert torch.equal(x.grad, want)

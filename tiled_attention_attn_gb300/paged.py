@@ -6,7 +6,7 @@ Like the rest of the binding this marshals arguments only; every step runs in
 the library's kernels.  Outputs and scratch memory are allocated by torch on
 the call's stream; calls on several streams, from several threads, or captured
 in several graphs share nothing.  Every operator takes ``stream`` by name (default: the current
-stream of its tensors' device).
+stream of its tensors' device); the one with a gradient runs on the current stream.
 
 Caches: ``k_pages`` and ``v_pages`` are (num_pages, page_size, Hkv, d) views,
 strided as the caller likes as long as the features are contiguous (slices of
@@ -245,18 +245,22 @@ class _RotaryScaledFunction(torch.autograd.Function):
 
     @staticmethod
     def forward(ctx, x, freqs, amplitude, interleaved, cu_seqlens, offsets, positions, inverse):
-        ctx.save_for_backward(*(t for t in (cu_seqlens, offsets, positions) if t is not None))
-        ctx.given = [t is not None for t in (cu_seqlens, offsets, positions)]
-        ctx.args = (freqs, amplitude, interleaved, inverse)
         # rows outside every sequence are zero, in the output and in the gradient
         out = torch.zeros(x.shape, dtype=x.dtype, device=x.device) if cu_seqlens is not None else None
-        return rotary_scaled(x, freqs, amplitude, interleaved, cu_seqlens, offsets, positions, inverse, out)
+        y = rotary_scaled(x, freqs, amplitude, interleaved, cu_seqlens, offsets, positions, inverse, out)
+        # (freqs too, so that a change of theirs before the backward is an error)
+        ctx.save_for_backward(_freqs(freqs, x.shape[-1])[0],
+                              *(t for t in (cu_seqlens, offsets, positions) if t is not None))
+        ctx.given = [t is not None for t in (cu_seqlens, offsets, positions)]
+        ctx.args = (amplitude, interleaved, inverse)
+        return y
 
     @staticmethod
     def backward(ctx, dy):
-        saved = iter(ctx.saved_tensors)
-        cu, off, pos = (next(saved) if g else None for g in ctx.given)
-        freqs, amplitude, interleaved, inverse = ctx.args
+        freqs, *rest = ctx.saved_tensors
+        rest = iter(rest)
+        cu, off, pos = (next(rest) if g else None for g in ctx.given)
+        amplitude, interleaved, inverse = ctx.args
         return (_RotaryScaledFunction.apply(dy.contiguous(), freqs, amplitude, interleaved, cu, off, pos,
                                             not inverse),) + (None,) * 7
 
@@ -264,8 +268,9 @@ class _RotaryScaledFunction(torch.autograd.Function):
 def rotary_scaled_func(x: torch.Tensor, freqs: torch.Tensor, amplitude: float = 1.0, interleaved: bool = False,
                        cu_seqlens: Optional[torch.Tensor] = None, offsets: Optional[torch.Tensor] = None,
                        positions: Optional[torch.Tensor] = None) -> torch.Tensor:
-    """``rotary_scaled`` with a gradient for x (the frequencies are constants).
-    With ``cu_seqlens``, rows outside every sequence are zero and get no
+    """``rotary_scaled`` with a gradient for x (the frequencies are constants:
+    changing them in place before the backward is an error), on the current
+    stream.  With ``cu_seqlens``, rows outside every sequence are zero and get no
     gradient."""
     return _RotaryScaledFunction.apply(x, freqs, float(amplitude), bool(interleaved), cu_seqlens, offsets, positions,
                                        False)
