@@ -335,24 +335,24 @@ _CHUNK, _DECODE, _WEIGHTS = 0, 1, 2   # ATTN_PAGED_*
 
 
 def _workspace(device: torch.device, stream: int, d: int, call: int) -> torch.Tensor:
-    """Scratch memory of one call.  Each thread keeps what it used last on a
-    stream (calls of a thread on a stream are ordered; at most 8 are kept, of up
-    to 41 MB each); a captured call gets memory of its own, which its graph
-    keeps."""
-    kept = _ws_kept.__dict__
-    key = (device.index, stream, d, call)
-    capturing = torch.cuda.is_current_stream_capturing()
-    if not capturing and key in kept:
-        return kept[key]
+    """Scratch memory of one call.  Each thread keeps one buffer per stream that it
+    has used (its calls on a stream are ordered, whichever they are; at most 8
+    are kept, of up to 41 MB each); a captured call gets memory of its own, which
+    its graph keeps."""
     n = _ws_bytes.get((device.index, d, call))
     if n is None:
         n = _attn.lib().attn_paged_workspace_bytes(d, call)
         if n < 0:
             raise _attn.AttnError(int(n), "attn_paged_workspace_bytes")
         _ws_bytes[(device.index, d, call)] = n
-    ws = torch.empty(n, dtype=torch.uint8, device=device)
-    if not capturing:
-        if len(kept) >= 8:
+    if torch.cuda.is_current_stream_capturing():
+        return torch.empty(n, dtype=torch.uint8, device=device)
+    kept = _ws_kept.__dict__
+    key = (device.index, stream)
+    ws = kept.get(key)
+    if ws is None or ws.numel() < n:
+        ws = torch.empty(n, dtype=torch.uint8, device=device)
+        if key not in kept and len(kept) >= 8:
             del kept[next(iter(kept))]
         kept[key] = ws
     return ws
