@@ -67,3 +67,16 @@ def test_repeated_calls_allocate_nothing():
     for f, w in zip(calls, want):
         assert all(torch.equal(a, b) for a, b in zip(f.results(), w))
     assert attn.get_error() == attn.ATTN_OK
+
+
+def test_the_stream_used_last_keeps_its_memory():
+    f = Calls(128, 1)
+    hot, others = torch.cuda.Stream(), [torch.cuda.Stream() for _ in range(20)]
+    for s in others:
+        f(hot)
+        f(s)
+    torch.cuda.synchronize()
+    before = allocations()
+    f(hot)
+    torch.cuda.synchronize()
+    assert allocations() == before

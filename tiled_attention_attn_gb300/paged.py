@@ -336,8 +336,8 @@ _CHUNK, _DECODE, _WEIGHTS = 0, 1, 2   # ATTN_PAGED_*
 
 def _workspace(device: torch.device, stream: int, d: int, call: int) -> torch.Tensor:
     """Scratch memory of one call.  Each thread keeps one buffer per stream that it
-    has used (its calls on a stream are ordered, whichever they are; at most 8
-    are kept, of up to 41 MB each); a captured call gets memory of its own, which
+    has used (its calls on a stream are ordered, whichever they are), for the 8
+    streams used last, of up to 41 MB each; a captured call gets memory of its own, which
     its graph keeps."""
     n = _ws_bytes.get((device.index, d, call))
     if n is None:
@@ -349,12 +349,12 @@ def _workspace(device: torch.device, stream: int, d: int, call: int) -> torch.Te
         return torch.empty(n, dtype=torch.uint8, device=device)
     kept = _ws_kept.__dict__
     key = (device.index, stream)
-    ws = kept.get(key)
+    ws = kept.pop(key, None)
     if ws is None or ws.numel() < n:
         ws = torch.empty(n, dtype=torch.uint8, device=device)
-        if key not in kept and len(kept) >= 8:
-            del kept[next(iter(kept))]
-        kept[key] = ws
+        if len(kept) >= 8:
+            del kept[next(iter(kept))]   # the stream used longest ago
+    kept[key] = ws   # last in the dict's order
     return ws
 
 
