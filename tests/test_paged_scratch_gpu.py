@@ -80,3 +80,18 @@ def test_the_stream_used_last_keeps_its_memory():
     f(hot)
     torch.cuda.synchronize()
     assert allocations() == before
+
+
+def test_nothing_is_kept_for_streams_that_torch_does_not_own():
+    # the handle of such a stream may come back as another stream's
+    f = Calls(128, 1)
+    f()
+    want = f.results()
+    inner = torch.cuda.Stream()
+    s = torch.cuda.ExternalStream(inner.cuda_stream)
+    for _ in range(3):
+        s.wait_stream(torch.cuda.current_stream())
+        before = allocations()
+        f(s)
+        assert allocations() == before + 3
+        assert all(torch.equal(a, b) for a, b in zip(f.results(), want))

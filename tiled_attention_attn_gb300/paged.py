@@ -337,15 +337,18 @@ _CHUNK, _DECODE, _WEIGHTS = 0, 1, 2   # ATTN_PAGED_*
 def _workspace(device: torch.device, stream: int, d: int, call: int) -> torch.Tensor:
     """Scratch memory of one call.  Each thread keeps one buffer per stream that it
     has used (its calls on a stream are ordered, whichever they are), for the 8
-    streams used last, of up to 41 MB each; a captured call gets memory of its own, which
-    its graph keeps."""
+    streams used last, of up to 41 MB each.  A captured call gets memory of its
+    own, which its graph keeps.  Nothing is kept for a stream that torch does not
+    own: its handle may come back as another stream's while the last call runs."""
     n = _ws_bytes.get((device.index, d, call))
     if n is None:
         n = _attn.lib().attn_paged_workspace_bytes(d, call)
         if n < 0:
             raise _attn.AttnError(int(n), "attn_paged_workspace_bytes")
         _ws_bytes[(device.index, d, call)] = n
-    if torch.cuda.is_current_stream_capturing():
+    # (torch names a stream of another owner by its handle, and its own by an index)
+    foreign = stream != 0 and torch._C._cuda_getCurrentStream(device.index)[0] == stream
+    if foreign or torch.cuda.is_current_stream_capturing():
         return torch.empty(n, dtype=torch.uint8, device=device)
     kept = _ws_kept.__dict__
     key = (device.index, stream)
