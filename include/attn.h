@@ -517,7 +517,8 @@ int attn_key_weights(const void *q, const float *lse, float *weights, int weight
  *                ascending order, -1 from m on.
  *   seqlens_out  int32 (B), written: m.  Not seqlens_k itself.
  *   weights_out  fp32 (B, num_kv_heads, weights_out_len >= budget), written:
- *                the kept keys' weights, 0 from m on; may be weights itself.
+ *                the kept keys' weights, 0 from m on; disjoint from weights,
+ *                or weights itself.
  *   dst_page_table   null: rows move within the sequence's own pages (in
  *                place; pages past the m-th key are free afterwards).  Else the
  *                pages to write, row b at dst_page_table + b * dst_stride, dst_max_pages

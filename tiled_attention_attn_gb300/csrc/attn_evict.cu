@@ -420,6 +420,8 @@ extern "C" int attn_cache_evict(const float* weights, int weights_len, int* kept
     if (!ptr_aligned(x, 4)) return ATTN_EINVAL;
   if (budget < 1 || recent < 0 || recent > budget || weights_out_len < budget || budget > (1 << 30)) return ATTN_EINVAL;
   if (seqlens_out == cache->seqlens_k || (weights_out == weights && weights_out_len != weights_len)) return ATTN_EINVAL;
+  const unsigned long long rows = 4ull * B * p.c.hkv;   // bytes of an entry of every row
+  if (weights_out != weights && overlap(weights, rows * weights_len, weights_out, rows * weights_out_len)) return ATTN_EINVAL;
   if (dst_page_table) {
     if (dst_max_pages <= 0 || dst_stride < dst_max_pages ||
         static_cast<long long>(dst_max_pages) * cache->page_size < std::min<long long>(

@@ -30,6 +30,11 @@ template <bool BF16>
 constexpr float kDrop = BF16 ? 1.0f : 0x1p-7f;
 
 inline bool ptr_aligned(const void* p, uintptr_t a) { return (reinterpret_cast<uintptr_t>(p) % a) == 0; }
+// Whether [a, a + na) and [b, b + nb) share bytes.
+inline bool overlap(const void* a, unsigned long long na, const void* b, unsigned long long nb) {
+  const uintptr_t x = reinterpret_cast<uintptr_t>(a), y = reinterpret_cast<uintptr_t>(b);
+  return x < y + nb && y < x + na;
+}
 
 // Checks the host struct and fills `out`.  need_v: the values are used.
 inline int paged_check(const attn_paged_kv* c, int B, bool need_v, PagedKV& out) {

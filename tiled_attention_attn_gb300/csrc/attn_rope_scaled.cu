@@ -318,11 +318,6 @@ int launch(RopeParams& p, bool vec, bool bf16, bool gptj, cudaStream_t stream) {
   return ATTN_OK;
 }
 
-// Whether [a, a + na) and [b, b + nb) share bytes.
-bool overlap(const void* a, unsigned long long na, const void* b, unsigned long long nb) {
-  const uintptr_t x = reinterpret_cast<uintptr_t>(a), y = reinterpret_cast<uintptr_t>(b);
-  return x < y + nb && y < x + na;
-}
 // Bytes from the first to past the last element of a strided (rows, heads, d) tensor.
 unsigned long long extent(unsigned long long rows, long long st, int heads, long long sh, int d) {
   return rows == 0 ? 0 : 2 * ((rows - 1) * st + (heads - 1) * sh + d);
