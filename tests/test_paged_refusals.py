@@ -26,3 +26,15 @@ def test_eviction_weights_overlap(attn_lib, w, n, wo, no, bad):
         pytest.skip("accepted: the addresses are made up")
     rc = evict(attn_lib, w=w, n=n, wo=wo, no=no, kept=1 << 20, lens=1 << 21)
     assert (rc == attn.ATTN_EINVAL) == bad
+
+
+@pytest.mark.parametrize("original", [1, 4, 6, 7, 40, 4096])
+def test_yarn_of_short_contexts(original):
+    # by the number of turns within the original context: below one f / factor, above 32 f
+    plain, _ = attn.rotary_freqs(64)
+    f, amp = attn.rotary_freqs(64, scaling="yarn", factor=8.0, original_len=original)
+    assert abs(amp - (0.1 * math.log(8.0) + 1.0)) < 1e-15
+    turns = plain * original / (2 * math.pi)
+    assert torch.allclose(f[turns < 1.0] * 8.0, plain[turns < 1.0], rtol=1e-12)
+    assert torch.equal(f[turns > 32.0], plain[turns > 32.0])
+    assert bool((f <= plain).all()) and bool((f >= plain / 8.0 * (1 - 1e-12)).all())

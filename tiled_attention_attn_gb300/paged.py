@@ -168,6 +168,7 @@ def rotary_freqs(rot_dim: int, base: float = 10000.0, scaling: Optional[str] = N
         lo = max(math.floor(pair_of(beta_fast)), 0)
         hi = min(math.ceil(pair_of(beta_slow)), rot_dim // 2 - 1)
         ramp = ((i - lo) / max(hi - lo, 1e-3)).clamp(0.0, 1.0)
+        ramp[f * original_len < 2.0 * math.pi * beta_slow] = 1.0   # (also where a short context leaves lo = hi)
         return f * (1.0 - ramp) + f / factor * ramp, 0.1 * math.log(factor) + 1.0
     raise ValueError(f"unknown scaling {scaling!r}")
 
