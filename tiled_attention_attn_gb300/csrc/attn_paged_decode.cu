@@ -7,8 +7,9 @@
 // so that each softmax thread owns one key.  The statistics are those of the
 // online softmax: running maximum m, sum l and accumulator u, rescaled by
 // 2^(m_old - m_new); m may lag by up to 2^8, which cancels in u / l.  P is
-// rounded to the cache's 16-bit type for the second product (half a step of
-// each weight; kLift); S, m, l, u and the pieces' partial results are fp32.
+// rounded to the cache's 16-bit type for the second product, whose operands
+// tcgen05.mma takes in one type (half a step of each weight, as much again as the
+// rounding of O; kLift); S, m, l, u and the pieces' partial results are fp32.
 //
 // Bound by HBM: K and V of every sequence once.  A ring of three stages of 64
 // KB (K and V of a step) keeps up to 192 KB per SM in flight.  A page holds at

@@ -6,8 +6,10 @@
 // through one ring of TMA stages.  A row is a (token, query head) pair: the
 // heads of a key/value head share a tile, so that a key tile is read once for
 // all of them: 128 / heads tokens x heads rows (any group; rows left over are
-// zero queries).  P is rounded to the 16-bit type for the second product
-// (half a step of each weight; kLift); everything else is fp32.
+// zero queries).  P is rounded to the 16-bit type for the second product,
+// whose operands tcgen05.mma takes in one type (half a step of each weight; the
+// rest of the rounding as a third product would cost half as many MMAs again;
+// kLift); everything else is fp32.
 //
 // Pages: a 128-key tile is 128 / min(page_size, 128) boxes of 64 features for
 // K and as many for V; each lane of the producer warp loads one box at the page
