@@ -5,8 +5,9 @@ single tokens over the pages, accumulated attention weights, and eviction.
 Like the rest of the binding this marshals arguments only; every step runs in
 the library's kernels.  Outputs and scratch memory are allocated by torch on
 the call's stream; calls on several streams, from several threads, or captured
-in several graphs share nothing.  Every operator takes ``stream`` by name (default: the current
-stream of its tensors' device); the one with a gradient runs on the current stream.
+in several graphs share nothing.  Every operator takes ``stream`` by name
+(default: the current stream of its tensors' device); the one with a gradient
+runs on the current stream.
 
 Caches: ``k_pages`` and ``v_pages`` are (num_pages, page_size, Hkv, d) views,
 strided as the caller likes as long as the features are contiguous (slices of
@@ -272,7 +273,8 @@ def rotary_scaled_func(x: torch.Tensor, freqs: torch.Tensor, amplitude: float = 
     """``rotary_scaled`` with a gradient for x (the frequencies are constants:
     changing them in place before the backward is an error), on the current
     stream.  With ``cu_seqlens``, rows outside every sequence are zero and get no
-    gradient."""
+    gradient.  A backward that is captured into a CUDA graph needs, as with any
+    operator of torch, that no eager graph of the same leaves is alive."""
     return _RotaryScaledFunction.apply(x, freqs, float(amplitude), bool(interleaved), cu_seqlens, offsets, positions,
                                        False)
 
