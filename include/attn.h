@@ -533,6 +533,129 @@ int attn_cache_evict(const float *weights, int weights_len, int *kept, int *seql
                      int dst_max_pages, int budget, int recent, cudaStream_t stream);
 
 /*
+ * ---- norms of heads with rotary embedding -----------------------------------
+ *
+ * attn_qk_norm_rotary -- the root-mean-square norm of every head of the queries
+ * and the keys and their rotary embedding, in one pass.  A head x of d features
+ * becomes
+ *     y = R(a) (w x / sqrt(mean x^2 + eps))
+ * with R(a) the rotation of attn_rotary_scaled (times `amplitude`; features from
+ * rot_dim on are normed only) by a_p = positions[axis_of_pair[p]][row] * freqs[p].
+ * All of it in fp32, rounded once.
+ *   q, k      (rows, Hq, d) and (rows, Hk, d); element (row, head, feature) at
+ *             row * stride_token + head * stride_head + feature, strides multiples
+ *             of 8 and at least d.  Hk = 0: no keys (k and k_out are not read).
+ *   q_out, k_out   contiguous; disjoint from q, k and one another, or q (k) itself
+ *             where that is contiguous.
+ *   *_weight  d weights, of the tensors' type or, weight_fp32 = 1, fp32; null: ones.
+ *   freqs     HOST array of rot_dim / 2 finite doubles, copied before the call
+ *             returns; axis_of_pair HOST array of rot_dim / 2 ints in [0, axes),
+ *             null: all 0 (1 <= axes <= 8).  rot_dim = 0: no rotation.
+ *   positions device int32 (axes, rows), any values.
+ * d a multiple of 16 up to 512, rot_dim a multiple of 16; data pointers 16-byte
+ * aligned.  Returns ATTN_OK, ATTN_EINVAL, ATTN_EUNSUPPORTED (d, rot_dim, a device
+ * that is not sm_103) or ATTN_ELAUNCH.
+ */
+int attn_qk_norm_rotary(const void *q, const void *k, void *q_out, void *k_out, long long q_stride_token,
+                        long long q_stride_head, long long k_stride_token, long long k_stride_head, int rows, int Hq,
+                        int Hk, int d, const void *q_weight_or_null, const void *k_weight_or_null, int weight_fp32,
+                        float eps, int rot_dim, const double *freqs, const int *axis_of_pair_or_null, int axes,
+                        float amplitude, int interleaved, const int *positions, int fp16, cudaStream_t stream);
+
+/*
+ * attn_qk_norm_rotary_bwd -- its gradients.  dq_out, dk_out: gradients of the
+ * outputs, contiguous; q, k and the rest as the forward had them.  Writes dq (rows,
+ * Hq, d) and dk, contiguous (disjoint from the inputs, or dq_out (dk_out) itself,
+ * or q (k) itself where that is contiguous), and the weights' gradients, d values
+ * of the weights' type, summed over rows and heads in fp32 (null: not wanted).  The
+ * sums' order depends on the sizes alone: the same call gives the same bits.
+ * workspace: 256-byte aligned, attn_qk_norm_workspace_bytes(d) bytes; not needed
+ * (may be null) when neither weight gradient is wanted.
+ */
+int attn_qk_norm_rotary_bwd(const void *dq_out, const void *dk_out, const void *q, const void *k, void *dq, void *dk,
+                            void *dq_weight_or_null, void *dk_weight_or_null, long long q_stride_token,
+                            long long q_stride_head, long long k_stride_token, long long k_stride_head, int rows, int Hq,
+                            int Hk, int d, const void *q_weight_or_null, const void *k_weight_or_null, int weight_fp32,
+                            float eps, int rot_dim, const double *freqs, const int *axis_of_pair_or_null, int axes,
+                            float amplitude, int interleaved, const int *positions, int fp16, void *workspace,
+                            long long workspace_bytes, cudaStream_t stream);
+long long attn_qk_norm_workspace_bytes(int d);
+
+/*
+ * ---- paged caches of 8-bit floating point -----------------------------------
+ *
+ * attn_paged_kv8 describes a paged cache (as attn_paged_kv, above) that holds the
+ * row of a token and head, d features x, as e4m3 values v and one fp32 scale s,
+ * x ~ v s:
+ *     s = max(max |x| / 448, 2^-126),  v = x / s rounded to the nearest e4m3 value
+ * (a row with an infinity or a NaN: s = NaN, v = 0).  A HOST struct:
+ *   k, v      first byte of the key and of the value pages; feature f of (page,
+ *             token, head) at stride_page * page + stride_token * token +
+ *             stride_head * head + f bytes, strides positive multiples of 16, the
+ *             same for k and v; 16-byte aligned.
+ *   k_scales, v_scales   fp32, element (page, token, head) at scale_stride_page *
+ *             page + scale_stride_token * token + scale_stride_head * head.
+ *   the others as in attn_paged_kv, with its rules for what the host does not
+ *   read: key counts, offsets and pages out of range, slots past the last key.
+ * What a query does not see never reaches its outputs, NaN rows included, as long
+ * as v holds no NaN itself (attn_cache_append_fp8 writes none).
+ */
+typedef struct attn_paged_kv8 {
+  void *k;
+  void *v;
+  float *k_scales;
+  float *v_scales;
+  const int *page_table;
+  const int *seqlens_k;
+  long long stride_page, stride_token, stride_head;
+  long long scale_stride_page, scale_stride_token, scale_stride_head;
+  int table_stride, max_pages, num_pages, page_size;
+  int num_kv_heads, head_dim;
+} attn_paged_kv8;
+
+/*
+ * attn_cache_append_fp8 -- attn_cache_append into such a cache: the new tokens'
+ * keys, rotated in fp32 (with freqs), and values are quantised as they are
+ * written, the queries rotated and rounded to their own type.  Arguments as
+ * attn_cache_append; fp16: the type of q, k, v and q_out (0 bf16, 1 fp16);
+ * rot_dim a multiple of 16.
+ */
+int attn_cache_append_fp8(const void *q, const void *k, const void *v, void *q_out, long long q_stride_token,
+                          long long k_stride_token, long long v_stride_token, int B, int Hq, int total,
+                          const attn_paged_kv8 *cache, const int *cu_seqlens, int rot_dim, const double *freqs_or_null,
+                          float amplitude, int interleaved, const int *positions_or_null, int fp16, cudaStream_t stream);
+
+/*
+ * attn_cache_read_fp8 -- keys and values read back: row i of sequence b (rows
+ * cu_seqlens[b] .. cu_seqlens[b + 1] - 1 of k and v, contiguous (total, Hkv, d),
+ * bf16 or fp16 = 1) is key starts[b] + i (device int32 (B), null: 0), v s rounded
+ * once.  A row whose key is not one of the sequence's is left as it is and records
+ * ATTN_DEVERR_BAD_SEQLENS; rows outside every sequence are left as they are.
+ */
+int attn_cache_read_fp8(void *k, void *v, int B, int total, const attn_paged_kv8 *cache, const int *cu_seqlens,
+                        const int *starts_or_null, int fp16, cudaStream_t stream);
+
+/*
+ * attn_tree_fp8 -- attention of trees of drafted tokens over such a cache, and of
+ * single tokens.  q, o (total, Hq, d) contiguous (bf16, or fp16 = 1); sequence b's
+ * T new tokens, rows cu_seqlens[b] .. cu_seqlens[b + 1] - 1 (null: one row per
+ * sequence, total = B), are its last T keys, at most max_tokens <= 64 of them (a
+ * sequence with more has none, and records ATTN_DEVERR_BAD_SEQLENS).  Token i sees
+ * every key before them, and of the T keys those t with bit t of tree_mask[row of
+ * i] set (device int64 (total); its ancestors and itself, as a rule); null: the
+ * chain t <= i.
+ *     o = softmax(scale q . K) V over what it sees,  lse (Hq, total) fp32;
+ * a token that sees nothing gives o = 0 and lse = -inf, one that sees a NaN score
+ * NaN; rows outside every sequence are left as they are.  Hq a multiple of
+ * num_kv_heads, scale finite and not negative.  workspace: 256-byte aligned,
+ * attn_fp8_workspace_bytes(d) bytes.  The same call gives the same bits.
+ */
+int attn_tree_fp8(const void *q, void *o, float *lse, int B, int Hq, int total, int max_tokens,
+                  const attn_paged_kv8 *cache, const int *cu_seqlens_or_null, const long long *tree_mask_or_null,
+                  float scale, int fp16, void *workspace, long long workspace_bytes, cudaStream_t stream);
+long long attn_fp8_workspace_bytes(int d);
+
+/*
  * Padded batches around the varlen forward (the flash-attention
  * training-integration page, §2.5: drop the padded positions, run the
  * variable-length call, put the outputs back).  Each call enqueues device

@@ -10,18 +10,25 @@ from .attn import (  # noqa: F401
     AttnError,
     attn_bwd,
     attn_decode,
+    attn_decode_fp8,
     attn_decode_paged,
     attn_func,
     attn_func_padded,
     attn_fwd,
     attn_fwd_paged,
+    attn_tree_fp8,
     cache_append,
+    cache_append_fp8,
     cache_evict,
+    cache_read_fp8,
     get_error,
     key_weights,
     last_device_error,
     lib,
     plan,
+    qk_norm_rotary,
+    qk_norm_rotary_bwd,
+    qk_norm_rotary_func,
     rotary_freqs,
     rotary_scaled,
     rotary_scaled_func,

@@ -129,6 +129,8 @@ def lib(path: Optional[str] = None):
         L.attn_selftest_plan_cache.argtypes = [i, i, i, ip, ip]
         L.attn_selftest_plan_cache.restype = i
         _paged.declare(L)
+        _qknorm.declare(L)
+        _fp8.declare(L)
         if path is None:
             _lib = L
         return L
@@ -811,4 +813,19 @@ from .paged import (  # noqa: E402,F401
     rotary_freqs,
     rotary_scaled,
     rotary_scaled_func,
+)
+
+# norms of heads with rotary embedding; paged caches of 8-bit floating point
+from . import fp8 as _fp8  # noqa: E402
+from . import qknorm as _qknorm  # noqa: E402
+from .fp8 import (  # noqa: E402,F401
+    attn_decode_fp8,
+    attn_tree_fp8,
+    cache_append_fp8,
+    cache_read_fp8,
+)
+from .qknorm import (  # noqa: E402,F401
+    qk_norm_rotary,
+    qk_norm_rotary_bwd,
+    qk_norm_rotary_func,
 )

@@ -29,6 +29,7 @@
 #include <cstdint>
 
 #include "attn_paged.h"
+#include "attn_turns.cuh"
 
 namespace attn {
 namespace {
@@ -64,20 +65,6 @@ struct RopeParams {
   unsigned long long turns[kMaxPairs];   // f_p / 2 pi, fixed point
 };
 
-template <bool BF16>
-__device__ __forceinline__ float2 unpack(uint32_t w) {
-  if constexpr (BF16) return make_float2(__uint_as_float(w << 16), __uint_as_float(w & 0xffff0000u));
-  return __half22float2(*reinterpret_cast<const __half2*>(&w));
-}
-template <bool BF16>
-__device__ __forceinline__ uint32_t pack(float a, float b) {
-  if constexpr (BF16) {
-    const __nv_bfloat162 r = __floats2bfloat162_rn(a, b);
-    return *reinterpret_cast<const uint32_t*>(&r);
-  }
-  const __half2 r = __floats2half2_rn(a, b);
-  return *reinterpret_cast<const uint32_t*>(&r);
-}
 template <bool BF16>
 __device__ __forceinline__ float ld1(const uint16_t* p) {
   if constexpr (BF16) return __bfloat162float(__ushort_as_bfloat16(*p));
@@ -164,11 +151,9 @@ __global__ void __launch_bounds__(kThreads, 4) rope_kernel(const __grid_constant
     if (at < 0) continue;
     __syncwarp();   // the table's readers of the row before
     for (int i = lane; i < half; i += 32) {
-      const unsigned long long turn = p.turns[i] * static_cast<unsigned long long>(pos);
-      float sn, c;
-      sincospif(static_cast<float>(static_cast<int>(turn >> 32)) * 4.656612873077393e-10f, &sn, &c);   // 2^-31
+      const float2 t = turned(p.turns[i], pos);
       const int to = VEC ? (((i % PI) >> 1) * groups + i / PI) * 2 + (i & 1) : i;
-      cs[to] = make_float2(c * p.amplitude, sn * p.amplitude * p.sin_sign);
+      cs[to] = make_float2(t.x * p.amplitude, t.y * p.amplitude * p.sin_sign);
     }
     __syncwarp();
     for (int k = 0; k < p.n_seg; ++k) {
@@ -250,25 +235,6 @@ __global__ void __launch_bounds__(kThreads, 4) rope_kernel(const __grid_constant
   }
 }
 
-// The fraction of x in 64-bit fixed point, modulo 1 (both steps are exact but for
-// what lies below 2^-64).
-unsigned long long fixed_fraction(double x) {
-  const double h = x - std::nearbyint(x);   // [-0.5, 0.5]
-  const auto v = static_cast<unsigned long long>(std::fabs(h) * 18446744073709551616.0);
-  return h < 0.0 ? 0 - v : v;
-}
-
-// f / 2 pi modulo 1: 1 / 2 pi in two doubles, the product's high part and, by the
-// fused multiplication and addition, what it leaves.  (The high part comes from
-// std::fma too, so that no compiler fuses it into the subtraction that takes its
-// fraction.)
-unsigned long long turn_of(double f) {
-  constexpr double kHigh = 0.15915494309189533577, kLow = -9.839338337591243e-18;   // 1 / (2 pi)
-  const double high = std::fma(f, kHigh, 0.0);
-  const double low = std::fma(f, kLow, std::fma(f, kHigh, -high));
-  return fixed_fraction(high) + fixed_fraction(low);
-}
-
 // Checks the rotation's arguments and fills the turn table.
 int fill_turns(RopeParams& p, int rot_dim, int d, const double* freqs, float amplitude, int interleaved) {
   if (rot_dim <= 0 || rot_dim > d || (rot_dim & 1) || rot_dim > 2 * kMaxPairs || !freqs) return ATTN_EINVAL;
@@ -316,11 +282,6 @@ int launch(RopeParams& p, bool vec, bool bf16, bool gptj, cudaStream_t stream) {
   if (cudaGetLastError() != cudaSuccess) return ATTN_ELAUNCH;
   count_launch();
   return ATTN_OK;
-}
-
-// Bytes from the first to past the last element of a strided (rows, heads, d) tensor.
-unsigned long long extent(unsigned long long rows, long long st, int heads, long long sh, int d) {
-  return rows == 0 ? 0 : 2 * ((rows - 1) * st + (heads - 1) * sh + d);
 }
 
 }  // namespace

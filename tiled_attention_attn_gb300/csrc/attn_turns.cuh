@@ -1,0 +1,93 @@
+// What the kernels with a rotation share: 16-bit features in 32-bit words, the
+// rotation of an item (16 features, 8 pairs), the fixed-point turns of a
+// frequency (see attn_rope_scaled.cu) and the angle that a position makes of them.
+#pragma once
+#include <cuda_bf16.h>
+#include <cuda_fp16.h>
+#include <cuda_runtime.h>
+
+#include <cmath>
+#include <cstdint>
+
+namespace attn {
+
+template <bool BF16>
+__device__ __forceinline__ float2 unpack(uint32_t w) {
+  if constexpr (BF16) return make_float2(__uint_as_float(w << 16), __uint_as_float(w & 0xffff0000u));
+  return __half22float2(*reinterpret_cast<const __half2*>(&w));
+}
+template <bool BF16>
+__device__ __forceinline__ uint32_t pack(float a, float b) {
+  if constexpr (BF16) {
+    const __nv_bfloat162 r = __floats2bfloat162_rn(a, b);
+    return *reinterpret_cast<const uint32_t*>(&r);
+  }
+  const __half2 r = __floats2half2_rn(a, b);
+  return *reinterpret_cast<const uint32_t*>(&r);
+}
+
+// (cos, sin) of the fraction of a turn that position pos makes.
+__device__ __forceinline__ float2 turned(unsigned long long turns, long long pos) {
+  const unsigned long long turn = turns * static_cast<unsigned long long>(pos);
+  float sn, c;
+  sincospif(static_cast<float>(static_cast<int>(turn >> 32)) * 4.656612873077393e-10f, &sn, &c);   // 2^-31
+  return make_float2(c, sn);
+}
+
+// The 16 features of two words.
+template <bool BF16>
+__device__ __forceinline__ void widen(const uint4& a, const uint4& b, float (&x)[16]) {
+  const uint32_t u[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    const float2 f = unpack<BF16>(u[i]);
+    x[2 * i] = f.x;
+    x[2 * i + 1] = f.y;
+  }
+}
+template <bool BF16>
+__device__ __forceinline__ void narrow(const float (&x)[16], uint4& a, uint4& b) {
+  a = make_uint4(pack<BF16>(x[0], x[1]), pack<BF16>(x[2], x[3]), pack<BF16>(x[4], x[5]), pack<BF16>(x[6], x[7]));
+  b = make_uint4(pack<BF16>(x[8], x[9]), pack<BF16>(x[10], x[11]), pack<BF16>(x[12], x[13]), pack<BF16>(x[14], x[15]));
+}
+
+// Turns the item's 8 pairs by cs (sign -1: back).  GPT-NeoX: pair i is (x[i],
+// x[8 + i]); GPT-J: (x[2i], x[2i + 1]).
+template <bool GPTJ>
+__device__ __forceinline__ void turn(float (&x)[16], const float2 (&cs)[8], float sign) {
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    float& a = x[GPTJ ? 2 * i : i];
+    float& b = x[GPTJ ? 2 * i + 1 : 8 + i];
+    const float c = cs[i].x, s = cs[i].y * sign, u = a;
+    a = u * c - b * s;
+    b = u * s + b * c;
+  }
+}
+
+// The fraction of x in 64-bit fixed point, modulo 1 (both steps are exact but for
+// what lies below 2^-64).
+inline unsigned long long fixed_fraction(double x) {
+  const double h = x - std::nearbyint(x);   // [-0.5, 0.5]
+  const auto v = static_cast<unsigned long long>(std::fabs(h) * 18446744073709551616.0);
+  return h < 0.0 ? 0 - v : v;
+}
+
+// f / 2 pi modulo 1: 1 / 2 pi in two doubles, the product's high part and, by the
+// fused multiplication and addition, what it leaves.  (The high part comes from
+// std::fma too, so that no compiler fuses it into the subtraction that takes its
+// fraction.)
+inline unsigned long long turn_of(double f) {
+  constexpr double kHigh = 0.15915494309189533577, kLow = -9.839338337591243e-18;   // 1 / (2 pi)
+  const double high = std::fma(f, kHigh, 0.0);
+  const double low = std::fma(f, kLow, std::fma(f, kHigh, -high));
+  return fixed_fraction(high) + fixed_fraction(low);
+}
+
+// Bytes from the first to past the last element of a strided (rows, heads, d)
+// tensor of 16-bit elements.
+inline unsigned long long extent(unsigned long long rows, long long st, int heads, long long sh, int d) {
+  return rows == 0 ? 0 : 2 * ((rows - 1) * st + (heads - 1) * sh + d);
+}
+
+}  // namespace attn
