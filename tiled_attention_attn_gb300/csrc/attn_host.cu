@@ -842,6 +842,25 @@ int tile_map(const void* ptr, bool bf16, int d, int H, int L, int N, long long s
   return r == CUDA_SUCCESS ? ATTN_OK : ATTN_EINVAL;
 }
 
+int byte_map(const void* ptr, int d, int H, int L, int N, long long s_h, long long s_l, long long s_n, int box_l,
+             int swizzle, CUtensorMap& out) {
+  {
+    std::lock_guard<std::mutex> lock(g_mu);
+    if (!get_encode()) return ATTN_ELAUNCH;
+  }
+  const cuuint64_t dims[4] = {static_cast<cuuint64_t>(d), static_cast<cuuint64_t>(H), static_cast<cuuint64_t>(L),
+                              static_cast<cuuint64_t>(N)};
+  const cuuint64_t strides[3] = {static_cast<cuuint64_t>(s_h), static_cast<cuuint64_t>(s_l), static_cast<cuuint64_t>(s_n)};
+  const cuuint32_t box[4] = {static_cast<cuuint32_t>(d), 1, static_cast<cuuint32_t>(box_l), 1};
+  const cuuint32_t es[4] = {1, 1, 1, 1};
+  const CUresult r = g_encode(&out, CU_TENSOR_MAP_DATA_TYPE_UINT8, 4, const_cast<void*>(ptr), dims, strides, box, es,
+                              CU_TENSOR_MAP_INTERLEAVE_NONE,
+                              swizzle == 128 ? CU_TENSOR_MAP_SWIZZLE_128B
+                              : swizzle == 64 ? CU_TENSOR_MAP_SWIZZLE_64B : CU_TENSOR_MAP_SWIZZLE_NONE,
+                              CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  return r == CUDA_SUCCESS ? ATTN_OK : ATTN_EINVAL;
+}
+
 unsigned long long wait_timeout_ns() { return g_timeout_ns.load(); }
 unsigned long long* trace_buffer(int* events_per_stream) {
   std::lock_guard<std::mutex> lock(g_mu);

@@ -1,0 +1,7 @@
+#include "attn_tree_fp8_kernel.cuh"
+
+namespace attn {
+namespace tree {
+cudaError_t launch_d128(const Params& p, int cols, int grid, cudaStream_t stream) { return pick<128>(p, cols, grid, stream); }
+}  // namespace tree
+}  // namespace attn

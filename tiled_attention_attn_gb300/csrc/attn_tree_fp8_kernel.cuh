@@ -1,0 +1,1055 @@
+// Attention of single tokens and of trees of drafted tokens over a paged cache of
+// 8-bit floating point, on tensor cores (attn_tree_fp8).
+//
+// The new tokens' query heads that share a key/value head, T tokens x G heads, are
+// the columns of transposed products, as in the 16-bit decode kernel:
+//   S^T = K Q^T    (M = 128 keys, N columns, K = d)
+//   u^T += V^T P^T (M = d, N columns, K = 128 keys)
+// with the online softmax's running maximum m, sum l and accumulator u per column;
+// m may lag by up to 2^8, which cancels in u / l.
+//
+// K stays in e4m3 from HBM to the tensor core (kind::f8f6f4): what has 16 bits is
+// the query, and it is small.  A query row, times the power of two that brings its
+// largest value into (224, 448], is held as a sum of e4m3 values, two for bf16 and
+// three for fp16 (4 significant bits each, so 8 and 11 exactly; down to 2^-10,
+// which is 2^-17.8 of the largest), and S^T sums the products in fp32.  The key's
+// scale and the row's power of two are applied to S.
+//
+// V is widened to fp16, which holds e4m3 exactly, by four warps between the TMA's
+// stage and the second product: P in e4m3 would lose the light keys of a long
+// cache.  A value's scale goes into its weight: P' = p vs / R in fp16, R a power of
+// two at least the largest scale so far, so P' <= p; u is rescaled where R grows, as
+// where m grows.  l sums p itself.  P' is held times 2^7 as in the 16-bit kernel
+// (kLift).
+//
+// Bound by HBM: per key and head d bytes of K and of V, and 8 of scales.  TMA
+// stages of 16 KB of K and 16 of V (three or four in flight), per page one box per
+// tile; a warp brings the scales with 4-byte asynchronous copies.  Shared memory is
+// the next limit: per 128 keys of 128 features 32 KB written by TMA, 32 KB of K read
+// by the MMA (twice 16), V read (16), written (32) and read again (32): 1,150 cycles
+// of 128 bytes against the 1,400 that HBM takes for them.
+//
+// Work is cut as in the 16-bit decode kernel: the steps of all (sequence, unit) on
+// one line, equal ranges per CTA, pieces of a cut unit joined by tree_merge_kernel.
+// A unit has up to 64 columns; a tree with more takes several units per head, which
+// walk the line side by side and share the cache's lines in L2.
+//
+// Slots past a sequence's last key may hold anything: their scores are dropped by
+// index, their V is zeroed as it is widened.
+//
+// Head dimension 64: a step covers two tiles, one P.V serves both (M = 128 spans
+// the two tiles' d; the product's diagonal blocks are u_a and u_b).
+#pragma once
+#include <cuda_bf16.h>
+#include <cuda_fp16.h>
+#include <cuda_fp8.h>
+#include <cuda_runtime.h>
+
+#include <cstdint>
+
+#include "attn_paged_line.cuh"
+#include "attn_params.h"
+#include "attn_tree_fp8.h"
+#include "ptx.cuh"
+
+namespace attn {
+namespace tree {
+
+// Warps: K's TMA, the MMA, four of softmax, V's TMA and the scales, the queries,
+// four that widen V, and four more of softmax where a unit has 64 columns.
+constexpr int kWarpK = 0, kWarpMMA = 1, kWarpV = 6, kWarpQ = 7, kWarpWiden = 8, kWarpSoft2 = 12;
+constexpr int kRaw = kKeys * 128;       // a stage of K, or of V, in bytes
+constexpr int kWide = kKeys * 128 * 2;  // a step's V in fp16: two chunks of 128-byte rows
+constexpr int kWideChunk = kWide / 2;
+constexpr int kRing = 4;                // stages of scales
+constexpr float kPLift = 7.0f;          // log2 of the factor of P'
+constexpr float kPDrop = 0x1p-7f;
+
+// GT columns per group of four softmax warps, SG groups.
+template <int GT_, int SG_, int DA>
+struct Cfg {
+  static constexpr int GT = GT_, SG = SG_;
+  static constexpr int N = GT * SG < 16 ? 16 : GT * SG;
+  static constexpr int kThreads = 32 * (SG == 1 ? 12 : 16);
+  static constexpr int kTPS = 128 / DA;            // tiles per step
+  static constexpr int KS = kKeys * kTPS;          // keys per step
+  static constexpr int kRows = kTPS * N;           // rows of P^T (the P.V's N)
+  static constexpr int kStages = N == 16 ? 4 : (N == 64 && DA == 64 ? 2 : 3);
+  static constexpr int kQSlots = N == 64 ? 1 : 2;
+  static constexpr int kQPiece = N * DA;
+  static constexpr int kQ = 3 * kQPiece;
+  static constexpr int kPChunk = kRows * 128;
+  static constexpr int kP = 2 * kPChunk;
+  static constexpr int kOffK = 0;
+  static constexpr int kOffV = kOffK + kStages * kRaw;
+  static constexpr int kOffW = kOffV + kStages * kRaw;     // V in fp16, two buffers
+  static constexpr int kOffP = kOffW + 2 * kWide;          // P^T, two buffers
+  static constexpr int kOffQ = kOffP + 2 * kP;
+  static constexpr int kOffScale = kOffQ + kQSlots * kQ;   // [kRing][k, v][KS] floats
+  static constexpr int kOffMask = kOffScale + kRing * 2 * KS * 4;   // [slot][N] 64-bit words
+  static constexpr int kOffCol = kOffMask + kQSlots * N * 8;        // [slot][N] floats
+  static constexpr int kOffRed = kOffCol + kQSlots * N * 4;         // [group][parity][GT + 1][4] floats
+  static constexpr int kOffBar = kOffRed + SG * 2 * (GT + 1) * 16;
+  static constexpr int kNBars = 4 * kStages + 14 + 2 * kRing + 2 + 2 * SG;
+  static constexpr int kOffMisc = kOffBar + (kNBars * 8 + 15) / 16 * 16;
+  static constexpr int kSmem = kOffMisc + 512 + 1024;
+  static_assert(kSmem <= 227 * 1024, "shared memory");
+  // S^T: two buffers of kTPS tiles, then u^T (kRows columns)
+  static constexpr int kUsedCols = 3 * kTPS * N;
+  static constexpr uint32_t kTmemCols = kUsedCols <= 64 ? 64 : kUsedCols <= 128 ? 128 : kUsedCols <= 256 ? 256 : 512;
+};
+
+// The CTA's walk over units: (b, hc) in order, unit at position p of the line
+// of steps with T steps and one more for its fixed cost.
+struct Walk {
+  int b, hc;          // hc: group of p.abreast units; this CTA's is hc * abreast + its place
+  long long p, end;   // unit start; end of this CTA's range
+  long long begin;
+  int n, T;           // keys, steps
+  int cols, row0, ctx;   // columns (token, head) of a key/value head; first row of q; keys before the new tokens
+  int t0, t1;         // this CTA's steps of the unit
+};
+
+// Keys and new tokens of sequence b; one without new tokens takes no time, so it
+// has no keys either.
+__device__ __forceinline__ void sequence(const Params& p, int b, int& n, int& tokens, int& row0) {
+  if (p.cu == nullptr) {
+    tokens = 1;
+    row0 = b;
+    n = paged_len(p.c.t, b, p.err);
+    return;
+  }
+  chunk_and_keys(p.c.t, p.cu, b, p.total, tokens, row0, n, p.err);
+  if (tokens > p.max_tokens) {
+    atomicCAS(p.err, 0, ATTN_DEVERR_BAD_SEQLENS);
+    tokens = 0;
+  }
+  if (tokens == 0) n = 0;
+}
+
+template <int KS>
+__device__ __forceinline__ int steps_of(int n) { return (n + KS - 1) / KS; }
+
+template <int KS>
+__device__ __forceinline__ void enter(const Params& p, Walk& w) {
+  int tokens;
+  sequence(p, w.b, w.n, tokens, w.row0);
+  w.T = steps_of<KS>(w.n);
+  w.cols = tokens * p.group;
+  w.ctx = w.n - tokens;
+}
+
+// The next unit that has something to do here; false at the range's end.
+template <int KS>
+__device__ __forceinline__ bool next_unit(const Params& p, Walk& w, bool first) {
+  const int nh = p.c.t.hkv * p.parts / p.abreast;
+  while (true) {
+    if (!first) {
+      w.p += w.T + 1;
+      if (++w.hc == nh) {
+        w.hc = 0;
+        if (++w.b < p.B) enter<KS>(p, w);
+      }
+    }
+    first = false;
+    if (w.b >= p.B || w.p >= w.end) return false;
+    if (part_of<kMinSteps>(w.p, w.T, w.begin, w.end, w.t0, w.t1)) return true;
+  }
+}
+
+// A unit's place among the heads: key/value head and first column.
+struct Unit {
+  int g, col0, cols;   // cols: of this unit, none where the sequence's tree ends before
+};
+template <int N>
+__device__ __forceinline__ Unit unit_of(const Params& p, const Walk& w, int place) {
+  const int unit = w.hc * p.abreast + place;
+  Unit u;
+  u.g = unit / p.parts;
+  u.col0 = (unit - u.g * p.parts) * N;
+  u.cols = min(N, w.cols - u.col0);
+  return u;
+}
+
+// Byte offset of byte `at` of row `row` in a K-major tile of rows of ROW bytes (128
+// or 64) under the swizzle of that width.
+template <int ROW>
+__device__ __forceinline__ uint32_t swizzled(int row, int at) {
+  const int x = ROW == 128 ? (row & 7) : ((row >> 1) & 3);
+  return static_cast<uint32_t>(row * ROW + ((((at >> 4) ^ x) << 4) | (at & 15)));
+}
+
+// Shared-memory matrix descriptor of a K-major tile of e4m3 rows of ROW bytes: as
+// sdesc_sw128, with the swizzle mode of the row's width (2: 128 bytes, 4: 64).
+template <int ROW>
+__device__ __forceinline__ uint64_t sdesc_rows(uint32_t saddr) {
+  const uint64_t d = sdesc_sw128(saddr, 16, 8 * ROW);
+  return ROW == 128 ? d : (d & ~(7ull << 61)) | (4ull << 61);
+}
+
+// D[tmem] (+)= A[smem] * B[smem]^T, 8-bit operands, fp32 accumulation.
+__device__ __forceinline__ void umma_ss_f8(uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc, uint32_t idesc,
+                                           uint32_t accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "setp.ne.b32 p, %4, 0;\n\t"
+      "tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], %1, %2, %3, p;\n\t}"
+      :: "r"(d_tmem), "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(accumulate)
+      : "memory");
+}
+// kind::f8f6f4, e4m3 operands, both K-major.
+__host__ __device__ constexpr uint32_t idesc_e4m3(int M, int N) {
+  return (1u << 4) | (static_cast<uint32_t>(N >> 3) << 17) | (static_cast<uint32_t>(M >> 4) << 24);
+}
+
+// 4-byte asynchronous copy to shared memory, and the arrival of this thread's
+// copies so far on a barrier that counts its threads.
+__device__ __forceinline__ void copy4(uint32_t dst, const float* src) {
+  asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" :: "r"(dst), "l"(src) : "memory");
+}
+__device__ __forceinline__ void copies_arrive(uint32_t bar) {
+  asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" :: "r"(bar) : "memory");
+}
+
+__device__ __forceinline__ void tld16(uint32_t taddr, float (&x)[16]) {
+  uint32_t r[16];
+  tmem_ld_32x32b_x16(taddr, r);
+  tmem_wait_ld(r);
+#pragma unroll
+  for (int i = 0; i < 16; ++i) x[i] = __uint_as_float(r[i]);
+}
+__device__ __forceinline__ void tst16(uint32_t taddr, const float (&x)[16]) {
+  uint32_t r[16];
+#pragma unroll
+  for (int i = 0; i < 16; ++i) r[i] = __float_as_uint(x[i]);
+  tmem_st_32x32b_x16(taddr, r);
+}
+
+// Two e4m3 values as the fp16 pair.
+__device__ __forceinline__ uint32_t widen2(uint32_t x) {
+  const __half2_raw h = __nv_cvt_fp8x2_to_halfraw2(static_cast<__nv_fp8x2_storage_t>(x & 0xffffu), __NV_E4M3);
+  return static_cast<uint32_t>(h.x) | static_cast<uint32_t>(h.y) << 16;
+}
+// Two floats as the nearest e4m3 pair, which is taken off them.
+__device__ __forceinline__ uint32_t take2(float& a, float& b) {
+  const uint32_t v = __nv_cvt_float2_to_fp8x2(make_float2(a, b), __NV_SATFINITE, __NV_E4M3);
+  const uint32_t h = widen2(v);
+  const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&h));
+  a -= f.x;
+  b -= f.y;
+  return v;
+}
+
+template <int GT, int SG, int DA>
+__global__ void __launch_bounds__(Cfg<GT, SG, DA>::kThreads, 1) tree_kernel(const __grid_constant__ Params p) {
+  using C = Cfg<GT, SG, DA>;
+  constexpr int N = C::N, kTPS = C::kTPS, KS = C::KS, kStages = C::kStages, kSlots = C::kQSlots, kThreads = C::kThreads;
+  extern __shared__ __align__(1024) uint8_t smem_raw[];
+  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const uint32_t sbase = smem_u32(smem);
+  uint32_t bar_at = sbase + C::kOffBar;
+  auto take = [&](int n) { const uint32_t a = bar_at; bar_at += 8 * n; return a; };
+  const uint32_t b_k_full = take(kStages), b_k_empty = take(kStages), b_v_full = take(kStages), b_v_empty = take(kStages);
+  const uint32_t b_q_full = take(2), b_q_empty = take(2), b_s_full = take(2), b_p_full = take(2), b_w_full = take(2);
+  const uint32_t b_pv_done = take(2);   // the P.V that read P^T and V buffer i has completed (one phase per use)
+  const uint32_t b_c_full = take(kRing), b_c_empty = take(kRing);
+  const uint32_t b_o_free = take(1), b_drain = take(1), b_red = take(SG), b_xch = take(SG);
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + C::kOffMisc);
+  volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + C::kOffMisc + 4);
+  volatile int* start_b = reinterpret_cast<volatile int*>(smem + C::kOffMisc + 8);
+  volatile long long* start_p = reinterpret_cast<volatile long long*>(smem + C::kOffMisc + 16);
+  long long* warp_sums = reinterpret_cast<long long*>(smem + C::kOffMisc + 32);   // 2 kThreads / 32
+  WaitCtl wc{p.err, abort_flag, p.timeout_ns};
+
+  if (tid == 0) {
+    *abort_flag = 0;
+    *start_b = p.B;
+    *start_p = 0;
+    for (int s = 0; s < kStages; ++s) {
+      mbar_init(b_k_full + 8 * s, 1);
+      mbar_init(b_k_empty + 8 * s, 1);
+      mbar_init(b_v_full + 8 * s, 1);
+      mbar_init(b_v_empty + 8 * s, 4);   // the four warps that widen
+    }
+    for (int s = 0; s < 2; ++s) {
+      mbar_init(b_q_full + 8 * s, 1);
+      mbar_init(b_q_empty + 8 * s, 1 + 4 * SG);   // the MMA, the softmax warps
+      mbar_init(b_s_full + 8 * s, 1);
+      mbar_init(b_p_full + 8 * s, 4 * SG);
+      mbar_init(b_w_full + 8 * s, 4);
+      mbar_init(b_pv_done + 8 * s, 1);
+    }
+    for (int s = 0; s < kRing; ++s) {
+      mbar_init(b_c_full + 8 * s, 32);   // the copying warp's lanes
+      mbar_init(b_c_empty + 8 * s, 4 * SG);
+    }
+    mbar_init(b_o_free, 4 * SG);
+    mbar_init(b_drain, 1);
+    for (int s = 0; s < SG; ++s) {
+      mbar_init(b_red + 8 * s, 4);
+      mbar_init(b_xch + 8 * s, 2);
+    }
+    fence_mbar_init();
+  }
+  if (warp == kWarpMMA) {
+    tmem_alloc(smem_u32(tmem_slot), C::kTmemCols);
+    tmem_relinquish();
+  }
+  if (warp == kWarpK && lane == 0) {
+    tma_prefetch_desc(&p.tm_k);
+    tma_prefetch_desc(&p.tm_v);
+  }
+
+  // the line of steps: each thread a strip of sequences, then a prefix sum
+  const int nh = p.c.t.hkv * p.parts / p.abreast;
+  const int place = blockIdx.x % p.abreast, ranges = gridDim.x / p.abreast, range_id = blockIdx.x / p.abreast;
+  const int strip = (p.B + kThreads - 1) / kThreads;
+  const int b_lo = min(tid * strip, p.B), b_hi = min(b_lo + strip, p.B);
+  auto cost_of = [&](int b) {
+    int n, tokens, row0;
+    sequence(p, b, n, tokens, row0);
+    return static_cast<long long>(nh) * (steps_of<KS>(n) + 1);
+  };
+  long long mine = 0, total, units;
+  for (int b = b_lo; b < b_hi; ++b) mine += cost_of(b);
+  const long long before = block_prefix<kThreads>(
+      mine, static_cast<int>(min(static_cast<long long>(nh) * (b_hi - b_lo), 1LL << 24)), warp_sums, total, units);
+  const long long range = range_of<kMinSteps>(total, units, ranges);
+  // (SMs past the last whole range idle)
+  const long long begin = range_id < ranges ? range_id * range : total, end = min(begin + range, total);
+  if (begin >= before && begin < before + mine) {
+    long long at = before;
+    for (int b = b_lo; b < b_hi; ++b) {
+      const long long cost = cost_of(b);
+      if (begin < at + cost) {
+        *start_b = b;
+        *start_p = at;
+        break;
+      }
+      at += cost;
+    }
+  }
+  if (tid == 0) p.rec[blockIdx.x] = make_int4(0, 0, 0, 0);
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = *tmem_slot;
+  grid_launch_dependents();
+  Walk w = {};
+  w.b = *start_b;
+  w.begin = begin;
+  w.end = end;
+  w.p = *start_p;
+  if (w.b < p.B) {
+    enter<KS>(p, w);
+    w.hc = static_cast<int>((begin - w.p) / (w.T + 1));
+    w.p += static_cast<long long>(w.hc) * (w.T + 1);
+  }
+
+  if (warp == kWarpK || warp == kWarpV) {
+    // ------------------------------------------------------------------ TMA producers
+    uint32_t cnt = 0;
+    const int box = min(1 << p.c.t.page_log2, kKeys);   // tokens per box
+    const int n_pg = kKeys / box;                       // boxes along a tile
+    // this lane's box: page `pg` of tile `y` of the step
+    const int pg = lane % n_pg, y = lane / n_pg;
+    const bool of_v = warp == kWarpV, has = lane < kTPS * n_pg;
+    const CUtensorMap* map = of_v ? &p.tm_v : &p.tm_k;
+    const uint32_t dst0 = sbase + (of_v ? C::kOffV : C::kOffK) + (y * kKeys + pg * box) * DA;
+    const uint32_t b_full = of_v ? b_v_full : b_k_full, b_empty = of_v ? b_v_empty : b_k_empty;
+    const int key_off = y * kKeys + pg * box;
+    auto page_at = [&](int t) {   // the page of this lane's box in step t, -1: past the last key
+      const int key = t * KS + key_off;
+      if (!has || key >= w.n) return -1;
+      const int id = paged_page(p.c.t, w.b, key >> p.c.t.page_log2, p.err);
+      return id < 0 ? p.c.t.num_pages : id;   // no page: rows past the pool read as zeros
+    };
+    // V's warp also brings the scales: key 32 i + lane of the step
+    constexpr int KL = KS / 32;
+    int key_page[KL];
+    auto key_pages_at = [&](int t) {
+#pragma unroll
+      for (int i = 0; i < KL; ++i) {
+        const int key = t * KS + 32 * i + lane;
+        key_page[i] = key < w.n ? paged_page(p.c.t, w.b, key >> p.c.t.page_log2, p.err) : -1;
+      }
+    };
+    bool ok = true;
+    for (bool more = next_unit<KS>(p, w, true); more && ok; more = next_unit<KS>(p, w, false)) {
+      const Unit u = unit_of<N>(p, w, place);
+      if (w.t1 <= w.t0 || u.cols <= 0) continue;
+      int page = page_at(w.t0);
+      if (of_v) key_pages_at(w.t0);
+      for (int t = w.t0; t < w.t1; ++t) {
+        const int st = cnt % kStages;
+        const int next = t + 1 < w.t1 ? page_at(t + 1) : -1;
+        if (of_v) {
+          const int ring = cnt % kRing;
+          if (!mbar_wait_warp(b_c_empty + 8 * ring, ((cnt / kRing) & 1) ^ 1, wc,
+                              ATTN_DEVERR_WAIT_TIMEOUT_SITE(kSiteSFree))) { ok = false; break; }
+          const uint32_t dst = sbase + C::kOffScale + ring * (2 * KS * 4);
+#pragma unroll
+          for (int i = 0; i < KL; ++i) {
+            if (key_page[i] < 0) continue;
+            const int slot = (t * KS + 32 * i + lane) & ((1 << p.c.t.page_log2) - 1);
+            const long long at = key_page[i] * p.c.c_page + slot * p.c.c_token + u.g * p.c.c_head;
+            copy4(dst + (32 * i + lane) * 4, p.c.ks + at);
+            copy4(dst + (KS + 32 * i + lane) * 4, p.c.vs + at);
+          }
+          copies_arrive(b_c_full + 8 * ring);
+          if (t + 1 < w.t1) key_pages_at(t + 1);
+        }
+        if (!mbar_wait_warp(b_empty + 8 * st, ((cnt / kStages) & 1) ^ 1, wc,
+                            ATTN_DEVERR_WAIT_TIMEOUT_SITE(kSiteKEmpty))) { ok = false; break; }
+        const uint32_t n_box = __popc(__ballot_sync(0xffffffffu, page >= 0));
+        if (lane == 0) mbar_arrive_expect_tx(b_full + 8 * st, n_box * box * DA);
+        __syncwarp();
+        if (page >= 0)
+          tma_load_4d(dst0 + st * kRaw, map, b_full + 8 * st, 0, u.g, (t * KS + key_off) & ((1 << p.c.t.page_log2) - 1), page);
+        page = next;
+        ++cnt;
+      }
+    }
+    asm volatile("cp.async.wait_all;" ::: "memory");
+    if (lane == 0 && *abort_flag) {
+      // let the loads already issued land before the CTA exits
+      for (int s = 0; s < kStages; ++s) {
+        const uint32_t n = (cnt + kStages - 1 - s) / kStages;
+        if (n > 0) mbar_wait(b_full + 8 * s, (n - 1) & 1, wc, ATTN_DEVERR_WAIT_TIMEOUT_SITE(kSiteDrain), false);
+      }
+    }
+  } else if (warp == kWarpQ) {
+    // ------------------------------------------------------------------ queries
+    constexpr int E = DA / 32;      // features per lane
+    constexpr int kBatch = 8;       // rows in flight
+    uint32_t cnt = 0;
+    bool ok = true;
+    for (bool more = next_unit<KS>(p, w, true); more && ok; more = next_unit<KS>(p, w, false)) {
+      const Unit u = unit_of<N>(p, w, place);
+      if (w.t1 <= w.t0 || u.cols <= 0) continue;
+      const int slot = cnt % kSlots;
+      uint8_t* dst = smem + C::kOffQ + slot * C::kQ;
+      float* col = reinterpret_cast<float*>(smem + C::kOffCol) + slot * N;
+      unsigned long long* mask = reinterpret_cast<unsigned long long*>(smem + C::kOffMask) + slot * N;
+      if (!mbar_wait_warp(b_q_empty + 8 * slot, ((cnt / kSlots) & 1) ^ 1, wc,
+                          ATTN_DEVERR_WAIT_TIMEOUT_SITE(kSiteQEmpty))) break;
+      for (int c = lane; c < N; c += 32) {
+        unsigned long long bits = 0;
+        if (c < u.cols) {
+          const int token = (u.col0 + c) / p.group;
+          bits = p.mask ? static_cast<unsigned long long>(__ldg(p.mask + w.row0 + token)) : (2ull << token) - 1;
+        }
+        mask[c] = bits;
+      }
+#pragma unroll 1
+      for (int c0 = 0; c0 < N; c0 += kBatch) {
+        uint2 raw[kBatch];
+#pragma unroll
+        for (int i = 0; i < kBatch; ++i) {
+          raw[i] = make_uint2(0, 0);
+          if (c0 + i < u.cols) {
+            const int cc = u.col0 + c0 + i, token = cc / p.group, head = u.g * p.group + cc - token * p.group;
+            const uint16_t* src = p.q + (static_cast<long long>(w.row0 + token) * p.Hq + head) * DA + E * lane;
+            if constexpr (E == 4) raw[i] = __ldg(reinterpret_cast<const uint2*>(src));
+            else raw[i].x = __ldg(reinterpret_cast<const uint32_t*>(src));
+          }
+        }
+#pragma unroll
+        for (int i = 0; i < kBatch; ++i) {
+          const int c = c0 + i;
+          float x[4];
+#pragma unroll
+          for (int h = 0; h < 2; ++h) {
+            const uint32_t v = h == 0 ? raw[i].x : raw[i].y;
+            const float2 f = p.fp16 ? __half22float2(*reinterpret_cast<const __half2*>(&v))
+                                    : make_float2(__uint_as_float(v << 16), __uint_as_float(v & 0xffff0000u));
+            x[2 * h] = f.x;
+            x[2 * h + 1] = f.y;
+          }
+          uint32_t top = 0;   // as bits: a NaN counts above infinity
+#pragma unroll
+          for (int e = 0; e < 4; ++e) top = max(top, __float_as_uint(x[e]) & 0x7fffffffu);
+          top = __reduce_max_sync(0xffffffffu, top);
+          // 2^k with max 2^k in (224, 448]: 448 = 1.75 2^8
+          int k = 135 - static_cast<int>(top >> 23) - ((top & 0x7fffffu) > 0x600000u ? 1 : 0);
+          k = min(k, 120);   // (rows below 2^-112)
+          const float up = __uint_as_float(static_cast<uint32_t>(max(127 + k, 1)) << 23);
+          const float down = __uint_as_float(static_cast<uint32_t>(min(127 - k, 254)) << 23);
+          const bool finite = top < 0x7f800000u;
+          if (lane == 0) col[c] = p.scale_log2 * down;
+#pragma unroll
+          for (int e = 0; e < 4; ++e) x[e] = finite ? x[e] * up : __uint_as_float(0x7fffffffu);
+#pragma unroll
+          for (int s = 0; s < 3; ++s) {
+            const uint32_t a = take2(x[0], x[1]);
+            uint8_t* at = dst + s * C::kQPiece + swizzled<DA>(c, E * lane);
+            if constexpr (E == 4) *reinterpret_cast<uint32_t*>(at) = a | take2(x[2], x[3]) << 16;
+            else *reinterpret_cast<uint16_t*>(at) = static_cast<uint16_t>(a);
+          }
+        }
+      }
+      fence_proxy_async_smem();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(b_q_full + 8 * slot);
+      ++cnt;
+    }
+  } else if (warp == kWarpMMA) {
+    // ------------------------------------------------------------------ MMA issuer
+    if (lane == 0) {
+      constexpr uint32_t kIdescS = idesc_e4m3(kKeys, N);
+      constexpr uint32_t kIdescO = idesc_f16_f32acc(128, C::kRows, false, false) | (1u << 15);   // A = V read MN-major
+      const int pieces = p.fp16 ? 3 : 2;
+      const uint64_t dq0 = sdesc_rows<DA>(sbase + C::kOffQ);
+      const uint64_t dk0 = sdesc_rows<DA>(sbase + C::kOffK);
+      const uint64_t dv0 = sdesc_sw128(sbase + C::kOffW, kWideChunk, 1024);
+      const uint64_t dp0 = sdesc_sw128(sbase + C::kOffP, 16, 1024);
+      const uint32_t t_u = tmem + 2 * kTPS * N;   // u^T columns
+      uint32_t q_cnt = 0, k_cnt = 0, pv_cnt = 0, units_done = 0;
+      bool ok = true;
+      for (bool more = next_unit<KS>(p, w, true); more && ok; more = next_unit<KS>(p, w, false)) {
+        const Unit u = unit_of<N>(p, w, place);
+        if (w.t1 <= w.t0 || u.cols <= 0) continue;
+        const int qs = q_cnt % kSlots;
+        if (!mbar_wait(b_q_full + 8 * qs, (q_cnt / kSlots) & 1, wc, ATTN_DEVERR_WAIT_TIMEOUT_SITE(kSiteQFull))) break;
+        ++q_cnt;
+        tc_fence_after();
+        // u^T += V^T P^T of the next step in line.  Before a unit's first product,
+        // which overwrites u^T, the previous unit's epilogue must have read it
+        auto do_pv = [&](bool first) -> bool {
+          const int b = pv_cnt & 1;
+          if (!mbar_wait(b_w_full + 8 * b, (pv_cnt >> 1) & 1, wc, ATTN_DEVERR_WAIT_TIMEOUT_SITE(kSiteVFull))) return false;
+          if (!mbar_wait(b_p_full + 8 * b, (pv_cnt >> 1) & 1, wc, ATTN_DEVERR_WAIT_TIMEOUT_SITE(kSitePFull))) return false;
+          ++pv_cnt;
+          if (first && units_done > 0 &&
+              !mbar_wait(b_o_free, (units_done - 1) & 1, wc, ATTN_DEVERR_WAIT_TIMEOUT_SITE(kSiteODone)))
+            return false;
+          tc_fence_after();
+#pragma unroll
+          for (int kk = 0; kk < kKeys / 16; ++kk) {
+            const uint64_t a = dv0 + ((b * kWide + kk * 2048) >> 4);
+            const uint64_t x = dp0 + ((b * C::kP + (kk >> 2) * C::kPChunk + (kk & 3) * 32) >> 4);
+            umma_ss(t_u, a, x, kIdescO, (first && kk == 0) ? 0u : 1u);
+          }
+          umma_commit(b_pv_done + 8 * b);
+          return true;
+        };
+        bool first_pv = true;
+        for (int t = w.t0; t < w.t1; ++t) {
+          const int st = k_cnt % kStages, sb = k_cnt & 1;
+          const int nt = kTPS == 1 ? 1 : (w.n - t * KS > kKeys ? 2 : 1);
+          if (!mbar_wait(b_k_full + 8 * st, (k_cnt / kStages) & 1, wc, ATTN_DEVERR_WAIT_TIMEOUT_SITE(kSiteKFull))) {
+            ok = false;
+            break;
+          }
+          ++k_cnt;
+          tc_fence_after();
+          // S^T of the step's tiles into buffer sb: its previous contents (two
+          // steps back) were consumed, since this thread has waited for that step's P
+          for (int x = 0; x < nt; ++x)
+            for (int s = 0; s < pieces; ++s) {
+#pragma unroll
+              for (int kk = 0; kk < DA / 32; ++kk) {
+                const uint64_t a = dk0 + ((st * kRaw + x * (kKeys * DA) + kk * 32) >> 4);
+                const uint64_t b = dq0 + ((qs * C::kQ + s * C::kQPiece + kk * 32) >> 4);
+                umma_ss_f8(tmem + (sb * kTPS + x) * N, a, b, kIdescS, (s > 0 || kk > 0) ? 1u : 0u);
+              }
+            }
+          umma_commit(b_s_full + 8 * sb);
+          umma_commit(b_k_empty + 8 * st);
+          if (t > w.t0) {
+            if (!do_pv(first_pv)) {
+              ok = false;
+              break;
+            }
+            first_pv = false;
+          }
+        }
+        if (!ok) break;
+        // the unit's last step
+        if (!do_pv(first_pv)) break;
+        umma_commit(b_q_empty + 8 * qs);
+        ++units_done;
+      }
+      umma_commit(b_drain);
+      mbar_wait(b_drain, 0, wc, ATTN_DEVERR_WAIT_TIMEOUT_SITE(kSiteDrain), false);
+    }
+  } else {
+    // waits until the P.V of this CTA's step i (over all units) has completed:
+    // phase i >> 1 of pv_done(i & 1); phases of one buffer are observed in order
+    // and never fall two behind (step i + 2 writes the buffer only after this)
+    uint32_t done_seen[2] = {0, 0};
+    auto pv_wait = [&](uint32_t i) -> bool {
+      const int b = i & 1;
+      while (done_seen[b] <= (i >> 1)) {
+        if (!mbar_wait_warp(b_pv_done + 8 * b, done_seen[b] & 1, wc, ATTN_DEVERR_WAIT_TIMEOUT_SITE(kSitePvDone)))
+          return false;
+        ++done_seen[b];
+      }
+      return true;
+    };
+    uint32_t step = 0;   // steps so far, all units
+    bool ok = true;
+    if (warp >= kWarpWiden && warp < kWarpWiden + 4) {
+      // ---------------------------------------------------------------- V to fp16
+      const int me = tid - 32 * kWarpWiden;
+      constexpr int PER = DA / 16;   // lanes per row
+      for (bool more = next_unit<KS>(p, w, true); more && ok; more = next_unit<KS>(p, w, false)) {
+        const Unit u = unit_of<N>(p, w, place);
+        if (w.t1 <= w.t0 || u.cols <= 0) continue;
+        for (int t = w.t0; t < w.t1; ++t) {
+          const int st = step % kStages;
+          if (!mbar_wait_warp(b_v_full + 8 * st, (step / kStages) & 1, wc, ATTN_DEVERR_WAIT_TIMEOUT_SITE(kSiteVFull))) {
+            ok = false;
+            break;
+          }
+          const uint4* src = reinterpret_cast<const uint4*>(smem + C::kOffV + st * kRaw);
+          uint4 x[8];
+#pragma unroll
+          for (int i = 0; i < 8; ++i) x[i] = src[me + 128 * i];
+          if (step >= 2 && !pv_wait(step - 2)) { ok = false; break; }
+          uint8_t* dst = smem + C::kOffW + (step & 1) * kWide;
+#pragma unroll
+          for (int i = 0; i < 8; ++i) {
+            const int at = me + 128 * i, key = at / PER, c = at % PER;   // key of the step, 16 features from 16 c on
+            uint4 lo = make_uint4(0, 0, 0, 0), hi = lo;
+            if (t * KS + key < w.n) {
+              lo = make_uint4(widen2(x[i].x), widen2(x[i].x >> 16), widen2(x[i].y), widen2(x[i].y >> 16));
+              hi = make_uint4(widen2(x[i].z), widen2(x[i].z >> 16), widen2(x[i].w), widen2(x[i].w >> 16));
+            }
+            // chunk: a tile at d = 64, half of the features at 128
+            const int chunk = kTPS == 2 ? key >> 7 : c >> 2, row = key & 127, unit = 2 * (c & 3);
+            uint8_t* base = dst + chunk * kWideChunk + row * 128;
+            // the lanes of the second chunk store their words in the other order, so
+            // that eight lanes meet eight different words of the banks
+            const bool swap = kTPS == 1 && c >= 4;
+            *reinterpret_cast<uint4*>(base + (((unit + (swap ? 1 : 0)) ^ (row & 7)) << 4)) = swap ? hi : lo;
+            *reinterpret_cast<uint4*>(base + (((unit + (swap ? 0 : 1)) ^ (row & 7)) << 4)) = swap ? lo : hi;
+          }
+          fence_proxy_async_smem();
+          __syncwarp();
+          if (lane == 0) {
+            mbar_arrive(b_v_empty + 8 * st);
+            mbar_arrive(b_w_full + 8 * (step & 1));
+          }
+          ++step;
+        }
+      }
+    } else {
+      // ---------------------------------------------------------------- softmax warps
+      const int grp = warp >= kWarpSoft2 ? 1 : 0;
+      const int sw = warp - (grp ? kWarpSoft2 : 2);  // softmax warp 0..3 of its group
+      const int quarter = warp & 3;                  // TMEM lane quarter this warp may address
+      const int lrow = quarter * 32 + lane;          // TMEM lane: key of the tile (S^T), d (u^T)
+      constexpr int CH = GT < 16 ? GT : 16, NC = GT / CH;   // columns at a time
+      const int gcol = grp * GT;                     // first column of the group
+      const uint32_t t_lane = tmem + (static_cast<uint32_t>(quarter * 32) << 16);
+      // u^T columns this thread's lane holds: at DA = 64 lanes 64-127 keep u_b
+      const uint32_t t_u = t_lane + 2 * kTPS * N + ((kTPS == 2 && lrow >= 64) ? N : 0) + gcol;
+      float4* red = reinterpret_cast<float4*>(smem + C::kOffRed) + grp * 2 * (GT + 1);   // [parity][GT + 1], a float per warp
+      const uint32_t bar_red = b_red + 8 * grp, bar_xch = b_xch + 8 * grp;
+      uint32_t q_cnt = 0, red_cnt = 0, xch_cnt = 0;
+      // hands a warp's GT + 1 values over to the group; then red[par * (GT + 1) + h] has the four warps'
+      auto exchange = [&](const float (&v)[GT], float extra) -> bool {
+        float* mine_at = reinterpret_cast<float*>(red + (red_cnt & 1) * (GT + 1)) + sw;
+        if (lane == 0) {
+#pragma unroll
+          for (int h = 0; h < GT; ++h) mine_at[4 * h] = v[h];
+          mine_at[4 * GT] = extra;
+        }
+        __syncwarp();
+        if (lane == 0) mbar_arrive(bar_red);
+        if (!mbar_wait_warp(bar_red, red_cnt & 1, wc, ATTN_DEVERR_WAIT_TIMEOUT_SITE(kSiteXchg))) return false;
+        ++red_cnt;
+        return true;
+      };
+      auto warp_max = [](float x) {
+        float y;
+        asm volatile("redux.sync.max.f32 %0, %1, 0xffffffff;" : "=f"(y) : "f"(x));
+        return y;
+      };
+      for (bool more = next_unit<KS>(p, w, true); more && ok; more = next_unit<KS>(p, w, false)) {
+        const Unit u = unit_of<N>(p, w, place);
+        if (u.cols <= 0) continue;
+        const int G = min(GT, u.cols - gcol);   // this group's columns (may be none)
+        // row of q and head of this group's column h
+        auto out_row = [&](int h, int& head) {
+          const int cc = u.col0 + gcol + h, token = cc / p.group;
+          head = u.g * p.group + cc - token * p.group;
+          return w.row0 + token;
+        };
+        if (w.T == 0) {
+          // a sequence without keys: O = 0, lse = -inf
+          for (int h = 0; h < G; ++h) {
+            int head;
+            const long long row = out_row(h, head);
+            if (lrow < DA) p.o[(row * p.Hq + head) * DA + lrow] = 0;
+            if (lrow == 0) p.lse[static_cast<long long>(head) * p.total + row] = -INFINITY;
+          }
+          continue;
+        }
+        if (w.t1 <= w.t0) continue;
+        const int qs = q_cnt % kSlots;
+        if (!mbar_wait_warp(b_q_full + 8 * qs, (q_cnt / kSlots) & 1, wc, ATTN_DEVERR_WAIT_TIMEOUT_SITE(kSiteQFull))) break;
+        ++q_cnt;
+        const float* col = reinterpret_cast<const float*>(smem + C::kOffCol) + qs * N + gcol;
+        const unsigned long long* mask = reinterpret_cast<const unsigned long long*>(smem + C::kOffMask) + qs * N + gcol;
+        float m[GT], l[GT], R = 0.0f, inv_r = 0.0f;
+#pragma unroll
+        for (int h = 0; h < GT; ++h) {
+          m[h] = -INFINITY;
+          l[h] = 0.0f;
+        }
+        for (int t = w.t0; t < w.t1; ++t) {
+          const int sb = step & 1, ring = step % kRing;
+          if (!mbar_wait_warp(b_c_full + 8 * ring, (step / kRing) & 1, wc, ATTN_DEVERR_WAIT_TIMEOUT_SITE(kSiteSFree))) {
+            ok = false;
+            break;
+          }
+          // this thread's key in each tile of the step: its scales, and the columns that see it
+          const float* scales = reinterpret_cast<const float*>(smem + C::kOffScale) + ring * 2 * KS;
+          float ks[kTPS], vs[kTPS], v_max = -INFINITY;
+          uint32_t vis[kTPS];
+#pragma unroll
+          for (int y = 0; y < kTPS; ++y) {
+            const int key = t * KS + y * kKeys + lrow, at = key - w.ctx;   // at: place among the new tokens
+            ks[y] = scales[y * kKeys + lrow];
+            vs[y] = scales[KS + y * kKeys + lrow];
+            vis[y] = key < w.n ? 0xffffffffu : 0u;
+            if (key < w.n) {
+              v_max = fmaxf(v_max, vs[y]);
+              if (at >= 0) {
+                uint32_t bits = 0;
+#pragma unroll
+                for (int h = 0; h < GT; ++h) bits |= static_cast<uint32_t>((mask[h] >> at) & 1) << h;
+                vis[y] = bits;
+              }
+            }
+          }
+          __syncwarp();
+          if (lane == 0) mbar_arrive(b_c_empty + 8 * ring);
+          if (!mbar_wait_warp(b_s_full + 8 * sb, (step >> 1) & 1, wc, ATTN_DEVERR_WAIT_TIMEOUT_SITE(kSiteSFull))) {
+            ok = false;
+            break;
+          }
+          tc_fence_after();
+          const uint32_t t_s = t_lane + sb * kTPS * N + gcol;
+          float s[kTPS][16];   // (the last columns' as they are, for NC = 1)
+          {
+            float x[GT];
+#pragma unroll
+            for (int c = 0; c < NC; ++c) {
+#pragma unroll
+              for (int y = 0; y < kTPS; ++y) {
+                tld16(t_s + y * N + c * 16, s[y]);
+#pragma unroll
+                for (int i = 0; i < CH; ++i) {
+                  const float v = (vis[y] >> (c * CH + i)) & 1 ? s[y][i] * ks[y] : -INFINITY;
+                  x[c * CH + i] = y == 0 ? v : fmaxf(x[c * CH + i], v);
+                }
+              }
+            }
+#pragma unroll
+            for (int h = 0; h < GT; ++h) x[h] = warp_max(x[h]);
+            if (!exchange(x, warp_max(v_max))) { ok = false; break; }
+          }
+          const float4* got = red + ((red_cnt - 1) & 1) * (GT + 1);
+          auto top4 = [](const float4& v) { return fmaxf(fmaxf(v.x, v.y), fmaxf(v.z, v.w)); };
+          // the values' reference: the power of two above the largest scale so far
+          float rr = 1.0f;
+          {
+            const float top = top4(got[GT]);
+            if (top >= R && top > 0.0f) {
+              const float next = __uint_as_float(min((__float_as_uint(top) >> 23) + 1, 253u) << 23);
+              rr = R * __uint_as_float((254u - (__float_as_uint(next) >> 23)) << 23);
+              R = next;
+              inv_r = __uint_as_float((254u - (__float_as_uint(next) >> 23)) << 23);
+            }
+          }
+          // P^T of these keys into buffer sb, once the P.V that read it two
+          // steps back has completed
+          if (step >= 2 && !pv_wait(step - 2)) { ok = false; break; }
+          float f[kTPS];
+#pragma unroll
+          for (int y = 0; y < kTPS; ++y) f[y] = vs[y] * inv_r;
+#pragma unroll
+          for (int c = 0; c < NC; ++c) {
+            if constexpr (NC > 1) {
+#pragma unroll
+              for (int y = 0; y < kTPS; ++y) tld16(t_s + y * N + c * 16, s[y]);
+            }
+            // running max (scaled units): rescale only when it grows by more than 2^8
+            float r[16], cs[CH];
+            bool any = rr != 1.0f;
+#pragma unroll
+            for (int i = 0; i < 16; ++i) r[i] = rr;
+#pragma unroll
+            for (int i = 0; i < CH; ++i) {
+              const int h = c * CH + i;
+              cs[i] = col[h];
+              const float top = top4(got[h]);
+              const float mt = (top == -INFINITY) ? -INFINITY : top * cs[i];
+              if (mt > m[h] && (m[h] == -INFINITY || mt - m[h] > 8.0f)) {
+                const float q = (m[h] == -INFINITY) ? 0.0f : ex2_approx(m[h] - mt);
+                l[h] *= q;
+                r[i] *= q;
+                m[h] = mt;
+                any = true;
+              }
+            }
+            // u^T rescale (rare): needs the previous step's P.V complete.  m and R are
+            // the same in every thread, so the decision is too; the vote keeps the
+            // warp-collective TMEM accesses below uniform regardless.
+            any = __any_sync(0xffffffffu, any);
+            if (t > w.t0 && any) {
+              if (!pv_wait(step - 1)) { ok = false; break; }
+              tc_fence_after();
+              float o[16];
+              tld16(t_u + c * 16, o);
+#pragma unroll
+              for (int i = 0; i < CH; ++i) o[i] *= r[i];
+              tst16(t_u + c * 16, o);
+              tmem_wait_st();
+            }
+#pragma unroll
+            for (int i = 0; i < CH; ++i) {
+              const int h = c * CH + i;
+              const float mh = (m[h] == -INFINITY) ? 0.0f : m[h] - kPLift;
+#pragma unroll
+              for (int y = 0; y < kTPS; ++y) {
+                const bool on = (vis[y] >> h) & 1;
+                const float e = on ? ex2_approx(s[y][i] * ks[y] * cs[i] - mh) : 0.0f;
+                l[h] += e;
+                uint8_t* pbuf = smem + C::kOffP + sb * C::kP + (lrow >> 6) * C::kPChunk;
+                *reinterpret_cast<__half*>(pbuf + swizzled<128>(y * N + gcol + h, 2 * (lrow & 63))) =
+                    __float2half_rn(on ? e * f[y] : 0.0f);
+              }
+            }
+          }
+          if (!ok) break;
+          fence_proxy_async_smem();
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(b_p_full + 8 * sb);
+          ++step;
+        }
+        if (!ok) break;
+        if (lane == 0) mbar_arrive(b_q_empty + 8 * qs);   // (what it read of the slot: the columns' factors and masks)
+        // the piece's exp-sums over all its keys, then u^T R / l
+#pragma unroll
+        for (int h = 0; h < GT; ++h) {
+#pragma unroll
+          for (int o = 16; o > 0; o >>= 1) l[h] += __shfl_xor_sync(0xffffffffu, l[h], o);
+        }
+        if (!exchange(l, 0.0f)) break;
+        {
+          const float4* got = red + ((red_cnt - 1) & 1) * (GT + 1);
+#pragma unroll
+          for (int h = 0; h < GT; ++h) l[h] = (got[h].x + got[h].y) + (got[h].z + got[h].w);
+        }
+        if (!pv_wait(step - 1)) break;
+        tc_fence_after();
+        const bool whole = w.t0 == 0 && w.t1 == w.T;
+        const int slot = 2 * blockIdx.x + (w.t0 == 0 ? 1 : 0);
+        // u = u_a + u_b at head dimension 64: lanes 64-127 hand u_b over in the rows of
+        // this group's columns in the first P^T buffer, idle now that every P.V so far
+        // has completed; this group writes them next after its next exchange
+        auto handed = [&](int h, int i) {
+          return reinterpret_cast<float*>(smem + C::kOffP + (i >> 5) * C::kPChunk + (gcol + h) * 128 + (i & 31) * 4);
+        };
+        if constexpr (kTPS == 2) {
+          if (lrow >= 64) {
+#pragma unroll
+            for (int c = 0; c < NC; ++c) {
+              float o[16];
+              tld16(t_u + c * 16, o);
+#pragma unroll
+              for (int i = 0; i < CH; ++i) *handed(c * CH + i, lrow - 64) = o[i];
+            }
+            __syncwarp();
+            if (lane == 0) mbar_arrive(bar_xch);
+          } else {
+            if (!mbar_wait_warp(bar_xch, xch_cnt & 1, wc, ATTN_DEVERR_WAIT_TIMEOUT_SITE(kSiteXchg))) break;
+          }
+          ++xch_cnt;
+        }
+        if (kTPS == 1 || lrow < 64) {
+#pragma unroll
+          for (int c = 0; c < NC; ++c) {
+            float o[16];
+            tld16(t_u + c * 16, o);
+#pragma unroll
+            for (int i = 0; i < CH; ++i) {
+              const int h = c * CH + i;
+              if (h >= G) break;
+              if constexpr (kTPS == 2) o[i] += *handed(h, lrow);
+              const float v = (l[h] != 0.0f) ? o[i] / l[h] * R : 0.0f;   // 0: saw no key; a NaN stays one
+              if (whole) {
+                int head;
+                const long long at = (static_cast<long long>(out_row(h, head)) * p.Hq + head) * DA + lrow;
+                p.o[at] = p.fp16 ? __half_as_ushort(__float2half_rn(v)) : __bfloat16_as_ushort(__float2bfloat16_rn(v));
+              } else {
+                p.part_o[(static_cast<size_t>(slot) * N + gcol + h) * DA + lrow] = v;
+              }
+            }
+          }
+        }
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(b_o_free);   // u^T may be overwritten by the next unit
+        if (sw == 0 && lane < G) {
+          float lv = 0.0f, mv = -INFINITY;
+#pragma unroll
+          for (int h = 0; h < GT; ++h)
+            if (h == lane) {
+              lv = l[h] * kPDrop;
+              mv = m[h];
+            }
+          if (whole) {
+            int head;
+            const long long row = out_row(lane, head);
+            p.lse[static_cast<long long>(head) * p.total + row] =
+                (lv != 0.0f) ? mv * 0.69314718055994531f + __logf(lv) : -INFINITY;
+          } else {
+            p.part_ml[slot * N + gcol + lane] = make_float2(mv, lv);
+          }
+        }
+        // the unit's pieces lie on the ranges p / range ... (p + T - 1) / range
+        if (!whole && w.t0 == 0 && tid == 64)
+          p.rec[blockIdx.x] = make_int4(w.b, w.hc * p.abreast + place,
+                                        static_cast<int>((w.p + w.T - 1) / range) - range_id + 1, u.cols);
+      }
+    }
+  }
+  tc_fence_before();
+  __syncthreads();
+  if (warp == kWarpMMA) {
+    __syncwarp();
+    tc_fence_after();
+    tmem_dealloc(tmem, C::kTmemCols);
+  }
+}
+
+// Joins the pieces of the unit that block x's CTA began, for columns y, y + gridDim.y, ...
+// of the unit: M = max m_s, w_s = 2^(m_s - M) l_s, O = sum w_s O_s / sum w_s.  Four
+// warps take every fourth piece, a lane DA / 32 features; a programmatic
+// dependent of the attention kernel.
+template <int N, int DA>
+__global__ void __launch_bounds__(128) tree_merge_kernel(const __grid_constant__ Params p) {
+  constexpr int E = DA / 32;
+  __shared__ float s_m[4], s_l[4];
+  __shared__ float s_o[4][DA];
+  const int c = blockIdx.x, w = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  grid_wait_prerequisites();
+  const int4 rec = __ldcg(p.rec + c);
+  const int pieces = rec.z;
+  if (pieces <= 1) return;
+  const int g = rec.y / p.parts, col0 = (rec.y - g * p.parts) * N;
+  const int row0 = p.cu ? __ldg(p.cu + rec.x) : rec.x;
+  for (int h = blockIdx.y; h < rec.w; h += gridDim.y) {
+    float M = -INFINITY, L = 0.0f, acc[E];
+#pragma unroll
+    for (int e = 0; e < E; ++e) acc[e] = 0.0f;
+    auto slot = [&](int s) { return s == 0 ? 2 * c + 1 : 2 * (c + s * p.abreast); };
+    for (int s0 = w; s0 < pieces; s0 += 16) {
+      float2 ml[4];
+      float x[4][E];
+#pragma unroll
+      for (int u = 0; u < 4; ++u) {   // four pieces in flight
+        const int s = s0 + 4 * u;
+        const bool in = s < pieces;
+        ml[u] = in ? __ldcg(p.part_ml + slot(s) * N + h) : make_float2(-INFINITY, 0.0f);
+        const float* src = p.part_o + (static_cast<size_t>(in ? slot(s) : 0) * N + h) * DA + lane * E;
+#pragma unroll
+        for (int e = 0; e < E; e += 2) {
+          const float2 v = in ? __ldcg(reinterpret_cast<const float2*>(src + e)) : make_float2(0.0f, 0.0f);
+          x[u][e] = v.x;
+          x[u][e + 1] = v.y;
+        }
+      }
+#pragma unroll
+      for (int u = 0; u < 4; ++u) {
+        if (ml[u].y == 0.0f) continue;   // (l of NaN: the sums become NaN, whatever m)
+        const float mn = fmaxf(M, ml[u].x);
+        const float r = M == -INFINITY ? 0.0f : ex2_approx(M - mn), wt = ex2_approx(ml[u].x - mn) * ml[u].y;
+        M = mn;
+        L = L * r + wt;
+#pragma unroll
+        for (int e = 0; e < E; ++e) acc[e] = acc[e] * r + wt * x[u][e];
+      }
+    }
+    if (lane == 0) {
+      s_m[w] = M;
+      s_l[w] = L;
+    }
+#pragma unroll
+    for (int e = 0; e < E; ++e) s_o[w][lane * E + e] = acc[e];
+    __syncthreads();
+    const int i = threadIdx.x;
+    if (i < DA) {
+      const float Mx = fmaxf(fmaxf(s_m[0], s_m[1]), fmaxf(s_m[2], s_m[3]));
+      float Lt = 0.0f, at = 0.0f;
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        if (s_l[k] == 0.0f) continue;
+        const float r = ex2_approx(s_m[k] - Mx);
+        Lt += s_l[k] * r;
+        at += s_o[k][i] * r;
+      }
+      const int token = (col0 + h) / p.group, head = g * p.group + (col0 + h) - token * p.group;
+      const long long row = row0 + token;
+      const float v = Lt != 0.0f ? at / Lt : 0.0f;
+      p.o[(row * p.Hq + head) * DA + i] =
+          p.fp16 ? __half_as_ushort(__float2half_rn(v)) : __bfloat16_as_ushort(__float2bfloat16_rn(v));
+      if (i == 0)
+        p.lse[static_cast<long long>(head) * p.total + row] =
+            Lt != 0.0f ? Mx * 0.69314718055994531f + __logf(Lt) : -INFINITY;
+    }
+    __syncthreads();
+  }
+}
+
+template <int GT, int SG, int DA>
+cudaError_t launch(const Params& p, int cols, int grid, cudaStream_t stream) {
+  using C = Cfg<GT, SG, DA>;
+  static bool attr_done[64] = {};   // per instantiation
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  if (dev < 0 || dev >= 64 || !attr_done[dev]) {
+    e = cudaFuncSetAttribute(tree_kernel<GT, SG, DA>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmem);
+    if (e != cudaSuccess) return e;
+    if (dev >= 0 && dev < 64) attr_done[dev] = true;
+  }
+  tree_kernel<GT, SG, DA><<<grid, C::kThreads, C::kSmem, stream>>>(p);
+  e = cudaGetLastError();
+  if (e != cudaSuccess) return e;
+  count_launch();
+  if (!p.cuts) return cudaSuccess;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(grid, cols < 16 ? cols : 16);
+  cfg.blockDim = dim3(128);
+  cfg.stream = stream;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  e = cudaLaunchKernelEx(&cfg, tree_merge_kernel<C::N, DA>, p);
+  if (e == cudaSuccess) count_launch();
+  return e;
+}
+
+template <int DA>
+cudaError_t pick(const Params& p, int cols, int grid, cudaStream_t stream) {
+  if (cols <= 1) return launch<1, 1, DA>(p, cols, grid, stream);
+  if (cols <= 2) return launch<2, 1, DA>(p, cols, grid, stream);
+  if (cols <= 4) return launch<4, 1, DA>(p, cols, grid, stream);
+  if (cols <= 8) return launch<8, 1, DA>(p, cols, grid, stream);
+  if (cols <= 16) return launch<16, 1, DA>(p, cols, grid, stream);
+  if (cols <= 32) return launch<32, 1, DA>(p, cols, grid, stream);
+  return launch<32, 2, DA>(p, cols, grid, stream);
+}
+
+}  // namespace tree
+}  // namespace attn
