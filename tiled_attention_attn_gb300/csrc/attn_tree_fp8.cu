@@ -65,7 +65,7 @@ int attn_tree_fp8(const void* q, void* o, float* lse, int B, int Hq, int total, 
   const int page = cache->page_size, box = std::min(page, tree::kKeys);
   for (int i = 0; i < 2; ++i)
     if (int rc = byte_map(i == 0 ? p.c.k : p.c.v, d, p.c.t.hkv, page, p.c.t.num_pages, p.c.s_head, p.c.s_token, p.c.s_page,
-                          box, i == 0 ? d : 0, i == 0 ? p.tm_k : p.tm_v))
+                          box, i == 0 || d == 128 ? d : 0, i == 0 ? p.tm_k : p.tm_v))
       return rc;
   char* ws = static_cast<char*>(workspace);
   p.rec = reinterpret_cast<int4*>(ws);
@@ -86,11 +86,12 @@ int attn_tree_fp8(const void* q, void* o, float* lse, int B, int Hq, int total, 
   // a unit holds up to 64 columns (token, head) of a key/value head; more of them
   // are cut into units that each read the keys
   const long long cols = static_cast<long long>(p.max_tokens) * p.group;
-  if (cols > (1 << 24)) return ATTN_EINVAL;
+  if (cols > (1 << 20)) return ATTN_EINVAL;
   p.parts = static_cast<int>((cols + tree::kMostCols - 1) / tree::kMostCols);
   p.abreast = heads_abreast(p.c.t.hkv * p.parts, sms);
   p.cuts = (p.c.t.max_pages << p.c.t.page_log2) > tree::kMinSteps * (d == 64 ? 256 : 128);
   p.fp16 = fp16;
+  p.inv_group = 1.0f / static_cast<float>(p.group);
   p.scale_log2 = scale * 1.4426950408889634f;
   const int most = static_cast<int>(std::min<long long>(cols, tree::kMostCols));
   const cudaError_t e = d == 64 ? tree::launch_d64(p, most, sms, stream) : tree::launch_d128(p, most, sms, stream);

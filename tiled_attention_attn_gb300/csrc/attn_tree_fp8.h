@@ -10,7 +10,7 @@ namespace attn {
 namespace tree {
 
 constexpr int kKeys = 128;     // keys per tile
-constexpr int kMostCols = 64;  // columns (token, head) of a unit
+constexpr int kMostCols = 32;  // columns (token, head) of a unit
 constexpr int kMinSteps = 4;   // pieces of a cut unit are at least about this long
 
 struct Params {
@@ -33,6 +33,7 @@ struct Params {
   int cuts;            // the table can hold a unit long enough to be cut
   int fp16;
   float scale_log2;
+  float inv_group;
 };
 
 // cols: the most columns that a unit of the call has.

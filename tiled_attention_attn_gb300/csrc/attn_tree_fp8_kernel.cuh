@@ -56,7 +56,7 @@ namespace attn {
 namespace tree {
 
 // Warps: K's TMA, the MMA, four of softmax, V's TMA and the scales, the queries,
-// four that widen V, and four more of softmax where a unit has 64 columns.
+// four that widen V, and four more of softmax.
 constexpr int kWarpK = 0, kWarpMMA = 1, kWarpV = 6, kWarpQ = 7, kWarpWiden = 8, kWarpSoft2 = 12;
 constexpr int kRaw = kKeys * 128;       // a stage of K, or of V, in bytes
 constexpr int kWide = kKeys * 128 * 2;  // a step's V in fp16: two chunks of 128-byte rows
@@ -65,17 +65,23 @@ constexpr int kRing = 4;                // stages of scales
 constexpr float kPLift = 7.0f;          // log2 of the factor of P'
 constexpr float kPDrop = 0x1p-7f;
 
-// GT columns per group of four softmax warps, SG groups.
+// Two groups of four softmax warps, GT columns each: of 32 and 64 columns (SG = 2)
+// each takes half; up to 16 columns (SG = 1, TG = 2) they take turns, step by step,
+// with maxima, sums and accumulators of their own that are joined at the unit's end
+// (one group's chain of waits is longer than a step takes to arrive).
 template <int GT_, int SG_, int DA>
 struct Cfg {
-  static constexpr int GT = GT_, SG = SG_;
+  static constexpr int GT = GT_, SG = SG_, TG = 3 - SG;
   static constexpr int N = GT * SG < 16 ? 16 : GT * SG;
-  static constexpr int kThreads = 32 * (SG == 1 ? 12 : 16);
+  static constexpr int kThreads = 32 * 16;
   static constexpr int kTPS = 128 / DA;            // tiles per step
   static constexpr int KS = kKeys * kTPS;          // keys per step
   static constexpr int kRows = kTPS * N;           // rows of P^T (the P.V's N)
-  static constexpr int kStages = N == 16 ? 4 : (N == 64 && DA == 64 ? 2 : 3);
+  static constexpr int kStages = N == 16 && DA == 128 ? 4 : (N == 64 && DA == 64 ? 2 : 3);
   static constexpr int kQSlots = N == 64 ? 1 : 2;
+  // the queries' pieces as further columns of S^T, where tensor memory holds them
+  static constexpr bool kWideS = !(N == 64 && DA == 64);
+  static constexpr int kSCols = kWideS ? 3 * N : N;   // columns of S^T per tile
   static constexpr int kQPiece = N * DA;
   static constexpr int kQ = 3 * kQPiece;
   static constexpr int kPChunk = kRows * 128;
@@ -89,14 +95,18 @@ struct Cfg {
   static constexpr int kOffMask = kOffScale + kRing * 2 * KS * 4;   // [slot][N] 64-bit words
   static constexpr int kOffCol = kOffMask + kQSlots * N * 8;        // [slot][N] floats
   static constexpr int kOffRed = kOffCol + kQSlots * N * 4;         // [group][parity][GT + 1][4] floats
-  static constexpr int kOffBar = kOffRed + SG * 2 * (GT + 1) * 16;
-  static constexpr int kNBars = 4 * kStages + 14 + 2 * kRing + 2 + 2 * SG;
+  static constexpr int kOffMax = kOffRed + 2 * 2 * (GT + 1) * 16;  // running maxima, [softmax warp][GT] floats
+  static constexpr int kOffFin = kOffMax + 8 * GT * 4;   // the second group's (m, l) and R
+  static constexpr int kOffFactor = (kOffFin + (2 * GT + 1) * 4 + 15) / 16 * 16;   // [softmax warp][GT][4] floats
+  static constexpr int kOffBar = kOffFactor + 8 * GT * 16;
+  static constexpr int kNBars = 4 * kStages + 12 + kRing + 7;
   static constexpr int kOffMisc = kOffBar + (kNBars * 8 + 15) / 16 * 16;
   static constexpr int kSmem = kOffMisc + 512 + 1024;
-  static_assert(kSmem <= 227 * 1024, "shared memory");
-  // S^T: two buffers of kTPS tiles, then u^T (kRows columns)
-  static constexpr int kUsedCols = 3 * kTPS * N;
-  static constexpr uint32_t kTmemCols = kUsedCols <= 64 ? 64 : kUsedCols <= 128 ? 128 : kUsedCols <= 256 ? 256 : 512;
+  // S^T: two buffers of kTPS tiles, then u^T (kRows columns) of each group with its own
+  static constexpr int kColU = 2 * kTPS * kSCols;
+  static constexpr int kUsedCols = kColU + TG * kRows;
+  static constexpr uint32_t kTmemCols = kUsedCols <= 128 ? 128 : kUsedCols <= 256 ? 256 : 512;
+  static_assert(kSmem <= 227 * 1024 && kUsedCols <= 512, "shared and tensor memory");
 };
 
 // The CTA's walk over units: (b, hc) in order, unit at position p of the line
@@ -157,6 +167,25 @@ __device__ __forceinline__ bool next_unit(const Params& p, Walk& w, bool first) 
   }
 }
 
+// The table's entry for a key, read a step before it is used so that nothing waits
+// for it, and the page that it names.  -1: past the last key; no page: num_pages
+// (its rows lie past the pool and read as zeros).
+__device__ __forceinline__ int entry_of(const Params& p, const Walk& w, int key) {
+  return key < w.n ? __ldg(p.c.t.table + static_cast<long long>(w.b) * p.c.t.table_stride + (key >> p.c.t.page_log2)) : -1;
+}
+__device__ __forceinline__ int page_of(const Params& p, const Walk& w, int entry, int key) {
+  if (key >= w.n) return -1;
+  if (entry >= 0 && entry < p.c.t.num_pages) return entry;
+  atomicCAS(p.err, 0, ATTN_DEVERR_BAD_PAGE);
+  return p.c.t.num_pages;
+}
+
+// cc / p.group for cc < 2^20: the rounding of the product (2^-23 of it, twice) stays
+// below the half that keeps it off the quotient's borders.
+__device__ __forceinline__ int token_of(const Params& p, int cc) {
+  return static_cast<int>((static_cast<float>(cc) + 0.5f) * p.inv_group);
+}
+
 // A unit's place among the heads: key/value head and first column.
 struct Unit {
   int g, col0, cols;   // cols: of this unit, none where the sequence's tree ends before
@@ -211,12 +240,65 @@ __device__ __forceinline__ void copies_arrive(uint32_t bar) {
   asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" :: "r"(bar) : "memory");
 }
 
-__device__ __forceinline__ void tld16(uint32_t taddr, float (&x)[16]) {
-  uint32_t r[16];
-  tmem_ld_32x32b_x16(taddr, r);
-  tmem_wait_ld(r);
+// The waits of this kernel (ptx.cuh's in fewer instructions: many warps run code of
+// their own here, and fetching it counts): every lane polls, the limit is looked at
+// with each failed poll.
+__device__ __forceinline__ bool wait(uint32_t bar, uint32_t parity, const WaitCtl& w, int code) {
+  if (mbar_try_wait(bar, parity)) return true;
+  const uint64_t t0 = global_timer_ns();
+#pragma unroll 1
+  while (!mbar_try_wait(bar, parity)) {
+    if (*w.abort_flag) return false;
+    if (global_timer_ns() - t0 > w.timeout_ns) {
+      report_error(w, code);
+      return false;
+    }
+  }
+  return true;
+}
+__device__ __forceinline__ bool wait_warp(uint32_t bar, uint32_t parity, const WaitCtl& w, int code) {
+  return __all_sync(0xffffffffu, wait(bar, parity, w, code));
+}
+
+// W consecutive 32-bit columns of this thread's TMEM lane (W = 1, 4, 8 or 16); the
+// values are there after tld_wait.
+template <int W>
+__device__ __forceinline__ void tld_start(uint32_t taddr, float (&x)[W]) {
+  if constexpr (W == 1) {
+    asm volatile("tcgen05.ld.sync.aligned.32x32b.x1.b32 {%0}, [%1];" : "=f"(x[0]) : "r"(taddr));
+  } else if constexpr (W == 4) {
+    asm volatile("tcgen05.ld.sync.aligned.32x32b.x4.b32 {%0, %1, %2, %3}, [%4];"
+                 : "=f"(x[0]), "=f"(x[1]), "=f"(x[2]), "=f"(x[3]) : "r"(taddr));
+  } else if constexpr (W == 8) {
+    asm volatile("tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
+                 : "=f"(x[0]), "=f"(x[1]), "=f"(x[2]), "=f"(x[3]), "=f"(x[4]), "=f"(x[5]), "=f"(x[6]), "=f"(x[7])
+                 : "r"(taddr));
+  } else {
+    static_assert(W == 16, "columns");
+    asm volatile("tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15}, [%16];"
+                 : "=f"(x[0]), "=f"(x[1]), "=f"(x[2]), "=f"(x[3]), "=f"(x[4]), "=f"(x[5]), "=f"(x[6]), "=f"(x[7]),
+                   "=f"(x[8]), "=f"(x[9]), "=f"(x[10]), "=f"(x[11]), "=f"(x[12]), "=f"(x[13]), "=f"(x[14]), "=f"(x[15])
+                 : "r"(taddr));
+  }
+}
+// Waits for this thread's loads, and ties the values to the wait, so that no use of
+// them can be scheduled above it.
+template <int W>
+__device__ __forceinline__ void tie(float (&x)[W]) {
 #pragma unroll
-  for (int i = 0; i < 16; ++i) x[i] = __uint_as_float(r[i]);
+  for (int i = 0; i < W; ++i) asm volatile("" : "+f"(x[i]));
+}
+template <int W>
+__device__ __forceinline__ void tld_wait(float (&x)[W], float (&y)[W]) {
+  asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
+  tie<W>(x);
+  tie<W>(y);
+}
+template <int W>
+__device__ __forceinline__ void tld(uint32_t taddr, float (&x)[W]) {
+  tld_start<W>(taddr, x);
+  asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
+  tie<W>(x);
 }
 __device__ __forceinline__ void tst16(uint32_t taddr, const float (&x)[16]) {
   uint32_t r[16];
@@ -225,10 +307,35 @@ __device__ __forceinline__ void tst16(uint32_t taddr, const float (&x)[16]) {
   tmem_st_32x32b_x16(taddr, r);
 }
 
+__device__ __forceinline__ void store_half(uint32_t at, float x) {
+  asm volatile("st.shared.b16 [%0], %1;" :: "r"(at), "h"(__half_as_ushort(__float2half_rn(x))) : "memory");
+}
+
+// Combines n columns (a power of two, at most 32) over the warp's lanes: each
+// exchange halves the columns that a lane holds, n - 1 shuffles and the rest of five
+// instead of 5 n.  Returns the result of column lane >> (5 - log2 n).
+template <int n, typename Op>
+__device__ __forceinline__ float fold_columns(float (&v)[n], int lane, Op op) {
+  int o = 16;
+#pragma unroll
+  for (int half = n / 2; half > 0; half >>= 1, o >>= 1) {
+    const bool upper = lane & o;
+#pragma unroll
+    for (int i = 0; i < half; ++i) {
+      const float keep = upper ? v[i + half] : v[i], give = upper ? v[i] : v[i + half];
+      v[i] = op(keep, __shfl_xor_sync(0xffffffffu, give, o));
+    }
+  }
+#pragma unroll
+  for (; o > 0; o >>= 1) v[0] = op(v[0], __shfl_xor_sync(0xffffffffu, v[0], o));
+  return v[0];
+}
+
 // Two e4m3 values as the fp16 pair.
 __device__ __forceinline__ uint32_t widen2(uint32_t x) {
-  const __half2_raw h = __nv_cvt_fp8x2_to_halfraw2(static_cast<__nv_fp8x2_storage_t>(x & 0xffffu), __NV_E4M3);
-  return static_cast<uint32_t>(h.x) | static_cast<uint32_t>(h.y) << 16;
+  uint32_t h;
+  asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(h) : "h"(static_cast<unsigned short>(x)));
+  return h;
 }
 // Two floats as the nearest e4m3 pair, which is taken off them.
 __device__ __forceinline__ uint32_t take2(float& a, float& b) {
@@ -243,9 +350,10 @@ __device__ __forceinline__ uint32_t take2(float& a, float& b) {
 template <int GT, int SG, int DA>
 __global__ void __launch_bounds__(Cfg<GT, SG, DA>::kThreads, 1) tree_kernel(const __grid_constant__ Params p) {
   using C = Cfg<GT, SG, DA>;
-  constexpr int N = C::N, kTPS = C::kTPS, KS = C::KS, kStages = C::kStages, kSlots = C::kQSlots, kThreads = C::kThreads;
+  constexpr int N = C::N, kTPS = C::kTPS, KS = C::KS, TG = C::TG, kStages = C::kStages, kSlots = C::kQSlots, kThreads = C::kThreads;
   extern __shared__ __align__(1024) uint8_t smem_raw[];
-  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  // (by an offset, not through an integer: the accesses stay ones of shared memory)
+  uint8_t* smem = smem_raw + ((1024 - (smem_u32(smem_raw) & 1023)) & 1023);
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const uint32_t sbase = smem_u32(smem);
   uint32_t bar_at = sbase + C::kOffBar;
@@ -253,8 +361,8 @@ __global__ void __launch_bounds__(Cfg<GT, SG, DA>::kThreads, 1) tree_kernel(cons
   const uint32_t b_k_full = take(kStages), b_k_empty = take(kStages), b_v_full = take(kStages), b_v_empty = take(kStages);
   const uint32_t b_q_full = take(2), b_q_empty = take(2), b_s_full = take(2), b_p_full = take(2), b_w_full = take(2);
   const uint32_t b_pv_done = take(2);   // the P.V that read P^T and V buffer i has completed (one phase per use)
-  const uint32_t b_c_full = take(kRing), b_c_empty = take(kRing);
-  const uint32_t b_o_free = take(1), b_drain = take(1), b_red = take(SG), b_xch = take(SG);
+  const uint32_t b_c_full = take(kRing);
+  const uint32_t b_o_free = take(1), b_drain = take(1), b_red = take(2), b_xch = take(2), b_fin = take(1);
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + C::kOffMisc);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + C::kOffMisc + 4);
   volatile int* start_b = reinterpret_cast<volatile int*>(smem + C::kOffMisc + 8);
@@ -274,19 +382,19 @@ __global__ void __launch_bounds__(Cfg<GT, SG, DA>::kThreads, 1) tree_kernel(cons
     }
     for (int s = 0; s < 2; ++s) {
       mbar_init(b_q_full + 8 * s, 1);
-      mbar_init(b_q_empty + 8 * s, 1 + 4 * SG);   // the MMA, the softmax warps
+      mbar_init(b_q_empty + 8 * s, 1 + 8);   // the MMA, the softmax warps
       mbar_init(b_s_full + 8 * s, 1);
       mbar_init(b_p_full + 8 * s, 4 * SG);
       mbar_init(b_w_full + 8 * s, 4);
       mbar_init(b_pv_done + 8 * s, 1);
     }
     for (int s = 0; s < kRing; ++s) {
-      mbar_init(b_c_full + 8 * s, 32);   // the copying warp's lanes
-      mbar_init(b_c_empty + 8 * s, 4 * SG);
+      mbar_init(b_c_full + 8 * s, 128);   // the copying threads
     }
-    mbar_init(b_o_free, 4 * SG);
+    mbar_init(b_o_free, 4 * SG);   // the softmax warps that read u^T
     mbar_init(b_drain, 1);
-    for (int s = 0; s < SG; ++s) {
+    mbar_init(b_fin, 1);
+    for (int s = 0; s < 2; ++s) {
       mbar_init(b_red + 8 * s, 4);
       mbar_init(b_xch + 8 * s, 2);
     }
@@ -359,59 +467,27 @@ __global__ void __launch_bounds__(Cfg<GT, SG, DA>::kThreads, 1) tree_kernel(cons
     const uint32_t dst0 = sbase + (of_v ? C::kOffV : C::kOffK) + (y * kKeys + pg * box) * DA;
     const uint32_t b_full = of_v ? b_v_full : b_k_full, b_empty = of_v ? b_v_empty : b_k_empty;
     const int key_off = y * kKeys + pg * box;
-    auto page_at = [&](int t) {   // the page of this lane's box in step t, -1: past the last key
-      const int key = t * KS + key_off;
-      if (!has || key >= w.n) return -1;
-      const int id = paged_page(p.c.t, w.b, key >> p.c.t.page_log2, p.err);
-      return id < 0 ? p.c.t.num_pages : id;   // no page: rows past the pool read as zeros
-    };
-    // V's warp also brings the scales: key 32 i + lane of the step
-    constexpr int KL = KS / 32;
-    int key_page[KL];
-    auto key_pages_at = [&](int t) {
-#pragma unroll
-      for (int i = 0; i < KL; ++i) {
-        const int key = t * KS + 32 * i + lane;
-        key_page[i] = key < w.n ? paged_page(p.c.t, w.b, key >> p.c.t.page_log2, p.err) : -1;
-      }
-    };
+    auto box_entry = [&](int t) { return has ? entry_of(p, w, t * KS + key_off) : -1; };
     bool ok = true;
     for (bool more = next_unit<KS>(p, w, true); more && ok; more = next_unit<KS>(p, w, false)) {
       const Unit u = unit_of<N>(p, w, place);
       if (w.t1 <= w.t0 || u.cols <= 0) continue;
-      int page = page_at(w.t0);
-      if (of_v) key_pages_at(w.t0);
+      int entry = box_entry(w.t0);
       for (int t = w.t0; t < w.t1; ++t) {
         const int st = cnt % kStages;
-        const int next = t + 1 < w.t1 ? page_at(t + 1) : -1;
-        if (of_v) {
-          const int ring = cnt % kRing;
-          if (!mbar_wait_warp(b_c_empty + 8 * ring, ((cnt / kRing) & 1) ^ 1, wc,
-                              ATTN_DEVERR_WAIT_TIMEOUT_SITE(kSiteSFree))) { ok = false; break; }
-          const uint32_t dst = sbase + C::kOffScale + ring * (2 * KS * 4);
-#pragma unroll
-          for (int i = 0; i < KL; ++i) {
-            if (key_page[i] < 0) continue;
-            const int slot = (t * KS + 32 * i + lane) & ((1 << p.c.t.page_log2) - 1);
-            const long long at = key_page[i] * p.c.c_page + slot * p.c.c_token + u.g * p.c.c_head;
-            copy4(dst + (32 * i + lane) * 4, p.c.ks + at);
-            copy4(dst + (KS + 32 * i + lane) * 4, p.c.vs + at);
-          }
-          copies_arrive(b_c_full + 8 * ring);
-          if (t + 1 < w.t1) key_pages_at(t + 1);
-        }
-        if (!mbar_wait_warp(b_empty + 8 * st, ((cnt / kStages) & 1) ^ 1, wc,
+        const int next = t + 1 < w.t1 ? box_entry(t + 1) : -1;
+        if (!wait_warp(b_empty + 8 * st, ((cnt / kStages) & 1) ^ 1, wc,
                             ATTN_DEVERR_WAIT_TIMEOUT_SITE(kSiteKEmpty))) { ok = false; break; }
+        const int page = has ? page_of(p, w, entry, t * KS + key_off) : -1;
         const uint32_t n_box = __popc(__ballot_sync(0xffffffffu, page >= 0));
         if (lane == 0) mbar_arrive_expect_tx(b_full + 8 * st, n_box * box * DA);
         __syncwarp();
         if (page >= 0)
           tma_load_4d(dst0 + st * kRaw, map, b_full + 8 * st, 0, u.g, (t * KS + key_off) & ((1 << p.c.t.page_log2) - 1), page);
-        page = next;
+        entry = next;
         ++cnt;
       }
     }
-    asm volatile("cp.async.wait_all;" ::: "memory");
     if (lane == 0 && *abort_flag) {
       // let the loads already issued land before the CTA exits
       for (int s = 0; s < kStages; ++s) {
@@ -422,7 +498,6 @@ __global__ void __launch_bounds__(Cfg<GT, SG, DA>::kThreads, 1) tree_kernel(cons
   } else if (warp == kWarpQ) {
     // ------------------------------------------------------------------ queries
     constexpr int E = DA / 32;      // features per lane
-    constexpr int kBatch = 8;       // rows in flight
     uint32_t cnt = 0;
     bool ok = true;
     for (bool more = next_unit<KS>(p, w, true); more && ok; more = next_unit<KS>(p, w, false)) {
@@ -432,61 +507,64 @@ __global__ void __launch_bounds__(Cfg<GT, SG, DA>::kThreads, 1) tree_kernel(cons
       uint8_t* dst = smem + C::kOffQ + slot * C::kQ;
       float* col = reinterpret_cast<float*>(smem + C::kOffCol) + slot * N;
       unsigned long long* mask = reinterpret_cast<unsigned long long*>(smem + C::kOffMask) + slot * N;
-      if (!mbar_wait_warp(b_q_empty + 8 * slot, ((cnt / kSlots) & 1) ^ 1, wc,
+      if (!wait_warp(b_q_empty + 8 * slot, ((cnt / kSlots) & 1) ^ 1, wc,
                           ATTN_DEVERR_WAIT_TIMEOUT_SITE(kSiteQEmpty))) break;
-      for (int c = lane; c < N; c += 32) {
-        unsigned long long bits = 0;
+      // Row by row, the next two on their way, in a short loop: it runs once per unit,
+      // so fetching its code counts.  (Columns past u.cols hold anything: nothing reads
+      // their results.)
+      int head;
+      auto place_of = [&](int c) {   // row of q, and head
+        const int cc = u.col0 + c, token = token_of(p, cc);
+        head = u.g * p.group + cc - token * p.group;
+        return w.row0 + token;
+      };
+      auto load = [&](int c) {
+        uint2 v = make_uint2(0, 0);
         if (c < u.cols) {
-          const int token = (u.col0 + c) / p.group;
-          bits = p.mask ? static_cast<unsigned long long>(__ldg(p.mask + w.row0 + token)) : (2ull << token) - 1;
+          const long long row = place_of(c);
+          const uint16_t* src = p.q + (row * p.Hq + head) * DA + E * lane;
+          if constexpr (E == 4) v = __ldg(reinterpret_cast<const uint2*>(src));
+          else v.x = __ldg(reinterpret_cast<const uint32_t*>(src));
         }
-        mask[c] = bits;
-      }
+        return v;
+      };
+      uint2 next = load(0), after = load(1);
 #pragma unroll 1
-      for (int c0 = 0; c0 < N; c0 += kBatch) {
-        uint2 raw[kBatch];
+      for (int c = 0; c < u.cols; ++c) {
+        const uint2 now = next;
+        next = after;
+        after = load(c + 2);
+        float x[4];
 #pragma unroll
-        for (int i = 0; i < kBatch; ++i) {
-          raw[i] = make_uint2(0, 0);
-          if (c0 + i < u.cols) {
-            const int cc = u.col0 + c0 + i, token = cc / p.group, head = u.g * p.group + cc - token * p.group;
-            const uint16_t* src = p.q + (static_cast<long long>(w.row0 + token) * p.Hq + head) * DA + E * lane;
-            if constexpr (E == 4) raw[i] = __ldg(reinterpret_cast<const uint2*>(src));
-            else raw[i].x = __ldg(reinterpret_cast<const uint32_t*>(src));
-          }
+        for (int h = 0; h < 2; ++h) {
+          const uint32_t v = h == 0 ? now.x : now.y;
+          const float2 f = p.fp16 ? __half22float2(*reinterpret_cast<const __half2*>(&v))
+                                  : make_float2(__uint_as_float(v << 16), __uint_as_float(v & 0xffff0000u));
+          x[2 * h] = f.x;
+          x[2 * h + 1] = f.y;
         }
+        uint32_t top = 0;   // as bits: a NaN counts above infinity
 #pragma unroll
-        for (int i = 0; i < kBatch; ++i) {
-          const int c = c0 + i;
-          float x[4];
+        for (int e = 0; e < 4; ++e) top = max(top, __float_as_uint(x[e]) & 0x7fffffffu);
+        top = __reduce_max_sync(0xffffffffu, top);
+        // 2^k with max 2^k in (224, 448]: 448 = 1.75 2^8
+        int k = 135 - static_cast<int>(top >> 23) - ((top & 0x7fffffu) > 0x600000u ? 1 : 0);
+        k = min(k, 120);   // (rows below 2^-112)
+        const float up = __uint_as_float(static_cast<uint32_t>(max(127 + k, 1)) << 23);
+        const float down = __uint_as_float(static_cast<uint32_t>(min(127 - k, 254)) << 23);
+        if (lane == 0) {
+          const int row = place_of(c);
+          col[c] = fmaxf(p.scale_log2 * down, 0x1p-126f);   // (positive: -inf stays -inf)
+          mask[c] = p.mask ? static_cast<unsigned long long>(__ldg(p.mask + row)) : (2ull << (row - w.row0)) - 1;
+        }
+        uint8_t* at = dst + swizzled<DA>(c, E * lane);
 #pragma unroll
-          for (int h = 0; h < 2; ++h) {
-            const uint32_t v = h == 0 ? raw[i].x : raw[i].y;
-            const float2 f = p.fp16 ? __half22float2(*reinterpret_cast<const __half2*>(&v))
-                                    : make_float2(__uint_as_float(v << 16), __uint_as_float(v & 0xffff0000u));
-            x[2 * h] = f.x;
-            x[2 * h + 1] = f.y;
-          }
-          uint32_t top = 0;   // as bits: a NaN counts above infinity
-#pragma unroll
-          for (int e = 0; e < 4; ++e) top = max(top, __float_as_uint(x[e]) & 0x7fffffffu);
-          top = __reduce_max_sync(0xffffffffu, top);
-          // 2^k with max 2^k in (224, 448]: 448 = 1.75 2^8
-          int k = 135 - static_cast<int>(top >> 23) - ((top & 0x7fffffu) > 0x600000u ? 1 : 0);
-          k = min(k, 120);   // (rows below 2^-112)
-          const float up = __uint_as_float(static_cast<uint32_t>(max(127 + k, 1)) << 23);
-          const float down = __uint_as_float(static_cast<uint32_t>(min(127 - k, 254)) << 23);
-          const bool finite = top < 0x7f800000u;
-          if (lane == 0) col[c] = p.scale_log2 * down;
-#pragma unroll
-          for (int e = 0; e < 4; ++e) x[e] = finite ? x[e] * up : __uint_as_float(0x7fffffffu);
-#pragma unroll
-          for (int s = 0; s < 3; ++s) {
-            const uint32_t a = take2(x[0], x[1]);
-            uint8_t* at = dst + s * C::kQPiece + swizzled<DA>(c, E * lane);
-            if constexpr (E == 4) *reinterpret_cast<uint32_t*>(at) = a | take2(x[2], x[3]) << 16;
-            else *reinterpret_cast<uint16_t*>(at) = static_cast<uint16_t>(a);
-          }
+        for (int e = 0; e < 4; ++e) x[e] = top < 0x7f800000u ? x[e] * up : __uint_as_float(0x7fffffffu);
+#pragma unroll 1
+        for (int s = 0; s < 3; ++s, at += C::kQPiece) {
+          const uint32_t a = take2(x[0], x[1]);
+          if constexpr (E == 4) *reinterpret_cast<uint32_t*>(at) = a | take2(x[2], x[3]) << 16;
+          else *reinterpret_cast<uint16_t*>(at) = static_cast<uint16_t>(a);
         }
       }
       fence_proxy_async_smem();
@@ -497,48 +575,49 @@ __global__ void __launch_bounds__(Cfg<GT, SG, DA>::kThreads, 1) tree_kernel(cons
   } else if (warp == kWarpMMA) {
     // ------------------------------------------------------------------ MMA issuer
     if (lane == 0) {
-      constexpr uint32_t kIdescS = idesc_e4m3(kKeys, N);
+      const uint32_t idesc_s = idesc_e4m3(kKeys, C::kWideS ? N * (p.fp16 ? 3 : 2) : N);
       constexpr uint32_t kIdescO = idesc_f16_f32acc(128, C::kRows, false, false) | (1u << 15);   // A = V read MN-major
-      const int pieces = p.fp16 ? 3 : 2;
+      const int passes = C::kWideS ? 1 : p.fp16 ? 3 : 2;   // over K: the pieces' products summed by the MMA, or by the softmax
       const uint64_t dq0 = sdesc_rows<DA>(sbase + C::kOffQ);
       const uint64_t dk0 = sdesc_rows<DA>(sbase + C::kOffK);
       const uint64_t dv0 = sdesc_sw128(sbase + C::kOffW, kWideChunk, 1024);
       const uint64_t dp0 = sdesc_sw128(sbase + C::kOffP, 16, 1024);
-      const uint32_t t_u = tmem + 2 * kTPS * N;   // u^T columns
+      const uint32_t t_u = tmem + C::kColU;   // u^T columns
       uint32_t q_cnt = 0, k_cnt = 0, pv_cnt = 0, units_done = 0;
       bool ok = true;
       for (bool more = next_unit<KS>(p, w, true); more && ok; more = next_unit<KS>(p, w, false)) {
         const Unit u = unit_of<N>(p, w, place);
         if (w.t1 <= w.t0 || u.cols <= 0) continue;
         const int qs = q_cnt % kSlots;
-        if (!mbar_wait(b_q_full + 8 * qs, (q_cnt / kSlots) & 1, wc, ATTN_DEVERR_WAIT_TIMEOUT_SITE(kSiteQFull))) break;
+        if (!wait(b_q_full + 8 * qs, (q_cnt / kSlots) & 1, wc, ATTN_DEVERR_WAIT_TIMEOUT_SITE(kSiteQFull))) break;
         ++q_cnt;
         tc_fence_after();
-        // u^T += V^T P^T of the next step in line.  Before a unit's first product,
-        // which overwrites u^T, the previous unit's epilogue must have read it
-        auto do_pv = [&](bool first) -> bool {
+        // u^T += V^T P^T of the next step in line.  Before a unit's first products,
+        // which overwrite u^T, the previous unit's epilogue must have read it
+        int pv_unit = 0;
+        auto do_pv = [&]() -> bool {
+          const bool first = pv_unit++ < TG;
           const int b = pv_cnt & 1;
-          if (!mbar_wait(b_w_full + 8 * b, (pv_cnt >> 1) & 1, wc, ATTN_DEVERR_WAIT_TIMEOUT_SITE(kSiteVFull))) return false;
-          if (!mbar_wait(b_p_full + 8 * b, (pv_cnt >> 1) & 1, wc, ATTN_DEVERR_WAIT_TIMEOUT_SITE(kSitePFull))) return false;
+          if (!wait(b_w_full + 8 * b, (pv_cnt >> 1) & 1, wc, ATTN_DEVERR_WAIT_TIMEOUT_SITE(kSiteVFull))) return false;
+          if (!wait(b_p_full + 8 * b, (pv_cnt >> 1) & 1, wc, ATTN_DEVERR_WAIT_TIMEOUT_SITE(kSitePFull))) return false;
           ++pv_cnt;
-          if (first && units_done > 0 &&
-              !mbar_wait(b_o_free, (units_done - 1) & 1, wc, ATTN_DEVERR_WAIT_TIMEOUT_SITE(kSiteODone)))
+          if (pv_unit == 1 && units_done > 0 &&
+              !wait(b_o_free, (units_done - 1) & 1, wc, ATTN_DEVERR_WAIT_TIMEOUT_SITE(kSiteODone)))
             return false;
           tc_fence_after();
 #pragma unroll
           for (int kk = 0; kk < kKeys / 16; ++kk) {
             const uint64_t a = dv0 + ((b * kWide + kk * 2048) >> 4);
             const uint64_t x = dp0 + ((b * C::kP + (kk >> 2) * C::kPChunk + (kk & 3) * 32) >> 4);
-            umma_ss(t_u, a, x, kIdescO, (first && kk == 0) ? 0u : 1u);
+            umma_ss(t_u + (TG == 2 ? b * C::kRows : 0), a, x, kIdescO, (first && kk == 0) ? 0u : 1u);
           }
           umma_commit(b_pv_done + 8 * b);
           return true;
         };
-        bool first_pv = true;
         for (int t = w.t0; t < w.t1; ++t) {
           const int st = k_cnt % kStages, sb = k_cnt & 1;
           const int nt = kTPS == 1 ? 1 : (w.n - t * KS > kKeys ? 2 : 1);
-          if (!mbar_wait(b_k_full + 8 * st, (k_cnt / kStages) & 1, wc, ATTN_DEVERR_WAIT_TIMEOUT_SITE(kSiteKFull))) {
+          if (!wait(b_k_full + 8 * st, (k_cnt / kStages) & 1, wc, ATTN_DEVERR_WAIT_TIMEOUT_SITE(kSiteKFull))) {
             ok = false;
             break;
           }
@@ -547,27 +626,26 @@ __global__ void __launch_bounds__(Cfg<GT, SG, DA>::kThreads, 1) tree_kernel(cons
           // S^T of the step's tiles into buffer sb: its previous contents (two
           // steps back) were consumed, since this thread has waited for that step's P
           for (int x = 0; x < nt; ++x)
-            for (int s = 0; s < pieces; ++s) {
+            for (int s = 0; s < passes; ++s) {
 #pragma unroll
               for (int kk = 0; kk < DA / 32; ++kk) {
                 const uint64_t a = dk0 + ((st * kRaw + x * (kKeys * DA) + kk * 32) >> 4);
                 const uint64_t b = dq0 + ((qs * C::kQ + s * C::kQPiece + kk * 32) >> 4);
-                umma_ss_f8(tmem + (sb * kTPS + x) * N, a, b, kIdescS, (s > 0 || kk > 0) ? 1u : 0u);
+                umma_ss_f8(tmem + (sb * kTPS + x) * C::kSCols, a, b, idesc_s, (s > 0 || kk > 0) ? 1u : 0u);
               }
             }
           umma_commit(b_s_full + 8 * sb);
           umma_commit(b_k_empty + 8 * st);
           if (t > w.t0) {
-            if (!do_pv(first_pv)) {
+            if (!do_pv()) {
               ok = false;
               break;
             }
-            first_pv = false;
           }
         }
         if (!ok) break;
         // the unit's last step
-        if (!do_pv(first_pv)) break;
+        if (!do_pv()) break;
         umma_commit(b_q_empty + 8 * qs);
         ++units_done;
       }
@@ -575,56 +653,97 @@ __global__ void __launch_bounds__(Cfg<GT, SG, DA>::kThreads, 1) tree_kernel(cons
       mbar_wait(b_drain, 0, wc, ATTN_DEVERR_WAIT_TIMEOUT_SITE(kSiteDrain), false);
     }
   } else {
-    // waits until the P.V of this CTA's step i (over all units) has completed:
-    // phase i >> 1 of pv_done(i & 1); phases of one buffer are observed in order
-    // and never fall two behind (step i + 2 writes the buffer only after this)
-    uint32_t done_seen[2] = {0, 0};
+    // waits until the P.V of this CTA's step i (over all units) has completed: phase
+    // i >> 1 of pv_done(i & 1).  The next phase, step i + 2's, does not complete before
+    // the caller has handed over that step's operand, so the parity tells them apart
     auto pv_wait = [&](uint32_t i) -> bool {
-      const int b = i & 1;
-      while (done_seen[b] <= (i >> 1)) {
-        if (!mbar_wait_warp(b_pv_done + 8 * b, done_seen[b] & 1, wc, ATTN_DEVERR_WAIT_TIMEOUT_SITE(kSitePvDone)))
-          return false;
-        ++done_seen[b];
-      }
-      return true;
+      return wait_warp(b_pv_done + 8 * (i & 1), (i >> 1) & 1, wc, ATTN_DEVERR_WAIT_TIMEOUT_SITE(kSitePvDone));
     };
     uint32_t step = 0;   // steps so far, all units
     bool ok = true;
     if (warp >= kWarpWiden && warp < kWarpWiden + 4) {
-      // ---------------------------------------------------------------- V to fp16
+      // ---------------------------------------------------------------- V to fp16, and the scales
       const int me = tid - 32 * kWarpWiden;
-      constexpr int PER = DA / 16;   // lanes per row
+      // Of head dimension 128 a thread takes 16 features of rows 16 i + row: eight lanes
+      // 4 words of two rows that differ in bits 0 and 2, so that they meet eight different
+      // words of the banks in the swizzled stage as well as in the fp16 tile.  Of 64, 16
+      // features of rows 32 i + row (tile i / 4): eight lanes two rows side by side.
+      const int row = kTPS == 1 ? 8 * (me >> 6) + (((me >> 4) & 3) ^ (((me >> 2) & 1) * 5)) : me >> 2;
+      const int c = kTPS == 1 ? 4 * ((me >> 3) & 1) + (me & 3) : me & 3;
+      const uint32_t from = kTPS == 1 ? swizzled<128>(row, 16 * c) : row * 64 + 16 * c;
+      const uint32_t to = (kTPS == 1 ? (c >> 2) * kWideChunk : 0) + row * 128 + ((2 * (c & 3) ^ (row & 7)) << 4);   // (the second word: bit 4 flipped)
+      // The scales are copied two steps ahead, over the units' ends: a walk of their
+      // own, whose table entries are read a step before that.  Key 128 i + me of the
+      // step.  Their ring needs no barrier for its empty stages: the stage of step i + 2
+      // was step i - 2's, whose P.V has completed when this is reached.
+      Walk wa = w;
+      Unit ua = {};
+      int ta = 0, entry[kTPS];
+      bool on = true;
+      uint32_t copied = 0;
+      auto settle = [&](bool first) {
+        do {
+          on = next_unit<KS>(p, wa, first);
+          first = false;
+          if (!on) return;
+          ua = unit_of<N>(p, wa, place);
+        } while (wa.t1 <= wa.t0 || ua.cols <= 0);
+        ta = wa.t0;
+      };
+      auto entries = [&]() {
+#pragma unroll
+        for (int i = 0; i < kTPS; ++i) entry[i] = on ? entry_of(p, wa, ta * KS + kKeys * i + me) : -1;
+      };
+      auto copy_scales = [&]() {
+        if (!on) return;
+        const uint32_t dst = sbase + C::kOffScale + (copied % kRing) * (2 * KS * 4) + me * 4;
+#pragma unroll
+        for (int i = 0; i < kTPS; ++i) {
+          const int key = ta * KS + kKeys * i + me, page = page_of(p, wa, entry[i], key);
+          if (page < 0 || page == p.c.t.num_pages) continue;
+          const int slot = key & ((1 << p.c.t.page_log2) - 1);
+          const long long at = page * p.c.c_page + slot * p.c.c_token + ua.g * p.c.c_head;
+          copy4(dst + kKeys * i * 4, p.c.ks + at);
+          copy4(dst + (KS + kKeys * i) * 4, p.c.vs + at);
+        }
+        copies_arrive(b_c_full + 8 * (copied % kRing));
+        ++copied;
+        if (++ta == wa.t1) settle(false);
+        entries();
+      };
+      settle(true);
+      entries();
+#pragma unroll 1
+      for (int i = 0; i < 2; ++i) copy_scales();
       for (bool more = next_unit<KS>(p, w, true); more && ok; more = next_unit<KS>(p, w, false)) {
         const Unit u = unit_of<N>(p, w, place);
         if (w.t1 <= w.t0 || u.cols <= 0) continue;
         for (int t = w.t0; t < w.t1; ++t) {
           const int st = step % kStages;
-          if (!mbar_wait_warp(b_v_full + 8 * st, (step / kStages) & 1, wc, ATTN_DEVERR_WAIT_TIMEOUT_SITE(kSiteVFull))) {
+          if (step >= 2 && !pv_wait(step - 2)) { ok = false; break; }
+          if (!wait_warp(b_v_full + 8 * st, (step / kStages) & 1, wc, ATTN_DEVERR_WAIT_TIMEOUT_SITE(kSiteVFull))) {
             ok = false;
             break;
           }
-          const uint4* src = reinterpret_cast<const uint4*>(smem + C::kOffV + st * kRaw);
+          const uint8_t* src = smem + C::kOffV + st * kRaw + from;
+          uint8_t* dst = smem + C::kOffW + (step & 1) * kWide + to;
+          const int left = w.n - t * KS;   // keys from here on
           uint4 x[8];
 #pragma unroll
-          for (int i = 0; i < 8; ++i) x[i] = src[me + 128 * i];
-          if (step >= 2 && !pv_wait(step - 2)) { ok = false; break; }
-          uint8_t* dst = smem + C::kOffW + (step & 1) * kWide;
+          for (int i = 0; i < 8; ++i) x[i] = *reinterpret_cast<const uint4*>(src + i * 2048);
+          if (left < KS) {
+            // rows past the last key may hold anything: 0 * NaN would be NaN
+#pragma unroll
+            for (int i = 0; i < 8; ++i)
+              if ((kTPS == 1 ? 16 * i : 32 * i) + row >= left) x[i] = make_uint4(0, 0, 0, 0);
+          }
 #pragma unroll
           for (int i = 0; i < 8; ++i) {
-            const int at = me + 128 * i, key = at / PER, c = at % PER;   // key of the step, 16 features from 16 c on
-            uint4 lo = make_uint4(0, 0, 0, 0), hi = lo;
-            if (t * KS + key < w.n) {
-              lo = make_uint4(widen2(x[i].x), widen2(x[i].x >> 16), widen2(x[i].y), widen2(x[i].y >> 16));
-              hi = make_uint4(widen2(x[i].z), widen2(x[i].z >> 16), widen2(x[i].w), widen2(x[i].w >> 16));
-            }
-            // chunk: a tile at d = 64, half of the features at 128
-            const int chunk = kTPS == 2 ? key >> 7 : c >> 2, row = key & 127, unit = 2 * (c & 3);
-            uint8_t* base = dst + chunk * kWideChunk + row * 128;
-            // the lanes of the second chunk store their words in the other order, so
-            // that eight lanes meet eight different words of the banks
-            const bool swap = kTPS == 1 && c >= 4;
-            *reinterpret_cast<uint4*>(base + (((unit + (swap ? 1 : 0)) ^ (row & 7)) << 4)) = swap ? hi : lo;
-            *reinterpret_cast<uint4*>(base + (((unit + (swap ? 0 : 1)) ^ (row & 7)) << 4)) = swap ? lo : hi;
+            uint8_t* y = kTPS == 1 ? dst + i * 2048 : dst + (i >> 2) * kWideChunk + (i & 3) * 4096;
+            *reinterpret_cast<uint4*>(y) =
+                make_uint4(widen2(x[i].x), widen2(x[i].x >> 16), widen2(x[i].y), widen2(x[i].y >> 16));
+            *reinterpret_cast<uint4*>(smem + ((y - smem) ^ 16)) =
+                make_uint4(widen2(x[i].z), widen2(x[i].z >> 16), widen2(x[i].w), widen2(x[i].w >> 16));
           }
           fence_proxy_async_smem();
           __syncwarp();
@@ -632,9 +751,11 @@ __global__ void __launch_bounds__(Cfg<GT, SG, DA>::kThreads, 1) tree_kernel(cons
             mbar_arrive(b_v_empty + 8 * st);
             mbar_arrive(b_w_full + 8 * (step & 1));
           }
+          copy_scales();
           ++step;
         }
       }
+      asm volatile("cp.async.wait_all;" ::: "memory");
     } else {
       // ---------------------------------------------------------------- softmax warps
       const int grp = warp >= kWarpSoft2 ? 1 : 0;
@@ -642,31 +763,54 @@ __global__ void __launch_bounds__(Cfg<GT, SG, DA>::kThreads, 1) tree_kernel(cons
       const int quarter = warp & 3;                  // TMEM lane quarter this warp may address
       const int lrow = quarter * 32 + lane;          // TMEM lane: key of the tile (S^T), d (u^T)
       constexpr int CH = GT < 16 ? GT : 16, NC = GT / CH;   // columns at a time
-      const int gcol = grp * GT;                     // first column of the group
+      constexpr int LD = CH < 4 ? 4 : CH;            // as they are read
+      const int gcol = SG == 2 ? grp * GT : 0;       // first column of the group
       const uint32_t t_lane = tmem + (static_cast<uint32_t>(quarter * 32) << 16);
       // u^T columns this thread's lane holds: at DA = 64 lanes 64-127 keep u_b
-      const uint32_t t_u = t_lane + 2 * kTPS * N + ((kTPS == 2 && lrow >= 64) ? N : 0) + gcol;
+      const uint32_t t_u = t_lane + C::kColU + ((kTPS == 2 && lrow >= 64) ? N : 0) + gcol + (TG == 2 ? grp * C::kRows : 0);
       float4* red = reinterpret_cast<float4*>(smem + C::kOffRed) + grp * 2 * (GT + 1);   // [parity][GT + 1], a float per warp
       const uint32_t bar_red = b_red + 8 * grp, bar_xch = b_xch + 8 * grp;
-      uint32_t q_cnt = 0, red_cnt = 0, xch_cnt = 0;
-      // hands a warp's GT + 1 values over to the group; then red[par * (GT + 1) + h] has the four warps'
-      auto exchange = [&](const float (&v)[GT], float extra) -> bool {
-        float* mine_at = reinterpret_cast<float*>(red + (red_cnt & 1) * (GT + 1)) + sw;
-        if (lane == 0) {
-#pragma unroll
-          for (int h = 0; h < GT; ++h) mine_at[4 * h] = v[h];
-          mine_at[4 * GT] = extra;
-        }
+      uint32_t q_cnt = 0, red_cnt = 0, xch_cnt = 0, units_done = 0;
+      float* m = reinterpret_cast<float*>(smem + C::kOffMax) + (4 * grp + sw) * GT;   // this warp's copy of the maxima
+      // A warp hands GT + 1 values over to the group: column h by put(h, v) of one
+      // lane, then meet(); then red[par * (GT + 1) + h] has the four warps'
+      auto put = [&](int h, float v) { reinterpret_cast<float*>(red + (red_cnt & 1) * (GT + 1))[4 * h + sw] = v; };
+      constexpr int kOwn = CH == 16 ? 1 : CH == 8 ? 2 : CH == 4 ? 3 : CH == 2 ? 4 : 5;   // log2 of the lanes per column of fold_columns
+      auto put_folded = [&](int c, float v) {
+        if ((lane & ((1 << kOwn) - 1)) == 0) put(c * CH + (lane >> kOwn), v);
+      };
+      auto meet = [&]() -> bool {
         __syncwarp();
         if (lane == 0) mbar_arrive(bar_red);
-        if (!mbar_wait_warp(bar_red, red_cnt & 1, wc, ATTN_DEVERR_WAIT_TIMEOUT_SITE(kSiteXchg))) return false;
+        if (!wait_warp(bar_red, red_cnt & 1, wc, ATTN_DEVERR_WAIT_TIMEOUT_SITE(kSiteXchg))) return false;
         ++red_cnt;
         return true;
       };
-      auto warp_max = [](float x) {
-        float y;
-        asm volatile("redux.sync.max.f32 %0, %1, 0xffffffff;" : "=f"(y) : "f"(x));
-        return y;
+      // S^T of LD columns, the pieces' products summed, times the key's scale; -inf
+      // where the bits say that a column does not see the key
+      auto scores = [&](uint32_t at, float scale, bool all, uint32_t bits, float (&x)[LD]) {
+        if constexpr (C::kWideS) {
+          float y[LD];
+          tld_start<LD>(at, x);
+          tld_start<LD>(at + N, y);
+          tld_wait<LD>(x, y);
+#pragma unroll
+          for (int i = 0; i < LD; ++i) x[i] += y[i];
+          if (p.fp16) {
+            tld<LD>(at + 2 * N, y);
+#pragma unroll
+            for (int i = 0; i < LD; ++i) x[i] += y[i];
+          }
+        } else {
+          tld<LD>(at, x);
+        }
+#pragma unroll
+        for (int i = 0; i < LD; ++i) x[i] *= scale;
+        if (!all) {
+#pragma unroll
+          for (int i = 0; i < CH; ++i)
+            if (!((bits >> i) & 1)) x[i] = -INFINITY;
+        }
       };
       for (bool more = next_unit<KS>(p, w, true); more && ok; more = next_unit<KS>(p, w, false)) {
         const Unit u = unit_of<N>(p, w, place);
@@ -674,13 +818,13 @@ __global__ void __launch_bounds__(Cfg<GT, SG, DA>::kThreads, 1) tree_kernel(cons
         const int G = min(GT, u.cols - gcol);   // this group's columns (may be none)
         // row of q and head of this group's column h
         auto out_row = [&](int h, int& head) {
-          const int cc = u.col0 + gcol + h, token = cc / p.group;
+          const int cc = u.col0 + gcol + h, token = token_of(p, cc);
           head = u.g * p.group + cc - token * p.group;
           return w.row0 + token;
         };
         if (w.T == 0) {
           // a sequence without keys: O = 0, lse = -inf
-          for (int h = 0; h < G; ++h) {
+          for (int h = 0; h < G && (SG == 2 || grp == 0); ++h) {
             int head;
             const long long row = out_row(h, head);
             if (lrow < DA) p.o[(row * p.Hq + head) * DA + lrow] = 0;
@@ -690,25 +834,32 @@ __global__ void __launch_bounds__(Cfg<GT, SG, DA>::kThreads, 1) tree_kernel(cons
         }
         if (w.t1 <= w.t0) continue;
         const int qs = q_cnt % kSlots;
-        if (!mbar_wait_warp(b_q_full + 8 * qs, (q_cnt / kSlots) & 1, wc, ATTN_DEVERR_WAIT_TIMEOUT_SITE(kSiteQFull))) break;
+        if (!wait_warp(b_q_full + 8 * qs, (q_cnt / kSlots) & 1, wc, ATTN_DEVERR_WAIT_TIMEOUT_SITE(kSiteQFull))) break;
         ++q_cnt;
         const float* col = reinterpret_cast<const float*>(smem + C::kOffCol) + qs * N + gcol;
         const unsigned long long* mask = reinterpret_cast<const unsigned long long*>(smem + C::kOffMask) + qs * N + gcol;
-        float m[GT], l[GT], R = 0.0f, inv_r = 0.0f;
+        float l[GT], R = 0.0f, inv_r = 0.0f;
 #pragma unroll
-        for (int h = 0; h < GT; ++h) {
-          m[h] = -INFINITY;
-          l[h] = 0.0f;
-        }
+        for (int h = 0; h < GT; ++h) l[h] = 0.0f;
+        if (lane < GT) m[lane] = -INFINITY;
+        __syncwarp();
+        const uint32_t step0 = step;   // of the unit
+        int first_t = -1;              // this group's first step
         for (int t = w.t0; t < w.t1; ++t) {
+          if (TG == 2 && static_cast<int>(step & 1) != grp) {   // the other group's
+            ++step;
+            continue;
+          }
+          if (first_t < 0) first_t = t;
           const int sb = step & 1, ring = step % kRing;
-          if (!mbar_wait_warp(b_c_full + 8 * ring, (step / kRing) & 1, wc, ATTN_DEVERR_WAIT_TIMEOUT_SITE(kSiteSFree))) {
+          if (!wait_warp(b_c_full + 8 * ring, (step / kRing) & 1, wc, ATTN_DEVERR_WAIT_TIMEOUT_SITE(kSiteSFree))) {
             ok = false;
             break;
           }
           // this thread's key in each tile of the step: its scales, and the columns that see it
           const float* scales = reinterpret_cast<const float*>(smem + C::kOffScale) + ring * 2 * KS;
-          float ks[kTPS], vs[kTPS], v_max = -INFINITY;
+          float ks[kTPS], vs[kTPS];
+          uint32_t v_max = 0;   // bits
           uint32_t vis[kTPS];
 #pragma unroll
           for (int y = 0; y < kTPS; ++y) {
@@ -717,42 +868,40 @@ __global__ void __launch_bounds__(Cfg<GT, SG, DA>::kThreads, 1) tree_kernel(cons
             vs[y] = scales[KS + y * kKeys + lrow];
             vis[y] = key < w.n ? 0xffffffffu : 0u;
             if (key < w.n) {
-              v_max = fmaxf(v_max, vs[y]);
+              if (vs[y] > 0.0f) v_max = max(v_max, __float_as_uint(vs[y]));   // (not a NaN)
               if (at >= 0) {
                 uint32_t bits = 0;
-#pragma unroll
+#pragma unroll 1
                 for (int h = 0; h < GT; ++h) bits |= static_cast<uint32_t>((mask[h] >> at) & 1) << h;
                 vis[y] = bits;
               }
             }
           }
-          __syncwarp();
-          if (lane == 0) mbar_arrive(b_c_empty + 8 * ring);
-          if (!mbar_wait_warp(b_s_full + 8 * sb, (step >> 1) & 1, wc, ATTN_DEVERR_WAIT_TIMEOUT_SITE(kSiteSFull))) {
+          if (!wait_warp(b_s_full + 8 * sb, (step >> 1) & 1, wc, ATTN_DEVERR_WAIT_TIMEOUT_SITE(kSiteSFull))) {
             ok = false;
             break;
           }
           tc_fence_after();
-          const uint32_t t_s = t_lane + sb * kTPS * N + gcol;
-          float s[kTPS][16];   // (the last columns' as they are, for NC = 1)
-          {
-            float x[GT];
+          const uint32_t t_s = t_lane + sb * kTPS * C::kSCols + gcol;
+          float s[kTPS][LD];   // (the last columns', where there are more)
+          bool all = vis[0] == 0xffffffffu;   // every column sees every key of this warp
+          if constexpr (kTPS == 2) all = all && vis[1] == 0xffffffffu;
+          all = __all_sync(0xffffffffu, all);
 #pragma unroll
-            for (int c = 0; c < NC; ++c) {
+          for (int c = 0; c < NC; ++c) {
+            float x[CH];
 #pragma unroll
-              for (int y = 0; y < kTPS; ++y) {
-                tld16(t_s + y * N + c * 16, s[y]);
+            for (int y = 0; y < kTPS; ++y) {
+              scores(t_s + y * C::kSCols + c * 16, ks[y], all, vis[y] >> (c * CH), s[y]);
 #pragma unroll
-                for (int i = 0; i < CH; ++i) {
-                  const float v = (vis[y] >> (c * CH + i)) & 1 ? s[y][i] * ks[y] : -INFINITY;
-                  x[c * CH + i] = y == 0 ? v : fmaxf(x[c * CH + i], v);
-                }
-              }
+              for (int i = 0; i < CH; ++i) x[i] = y == 0 ? s[y][i] : fmaxf(x[i], s[y][i]);
             }
-#pragma unroll
-            for (int h = 0; h < GT; ++h) x[h] = warp_max(x[h]);
-            if (!exchange(x, warp_max(v_max))) { ok = false; break; }
+            put_folded(c, fold_columns<CH>(x, lane, [](float a, float b) { return fmaxf(a, b); }));
           }
+          // (scales are not negative, so their bits are in order)
+          const uint32_t v_top = __reduce_max_sync(0xffffffffu, v_max);
+          if (lane == 0) put(GT, __uint_as_float(v_top));
+          if (!meet()) { ok = false; break; }
           const float4* got = red + ((red_cnt - 1) & 1) * (GT + 1);
           auto top4 = [](const float4& v) { return fmaxf(fmaxf(v.x, v.y), fmaxf(v.z, v.w)); };
           // the values' reference: the power of two above the largest scale so far
@@ -772,58 +921,97 @@ __global__ void __launch_bounds__(Cfg<GT, SG, DA>::kThreads, 1) tree_kernel(cons
           float f[kTPS];
 #pragma unroll
           for (int y = 0; y < kTPS; ++y) f[y] = vs[y] * inv_r;
+          // (no weight of a slot past the last key; a NaN among the scales is dealt with below)
+          bool strange = false;
+#pragma unroll
+          for (int y = 0; y < kTPS; ++y) {
+            if (vis[y] == 0) f[y] = 0.0f;
+            if (!(f[y] <= 4.0f)) {
+              strange = true;
+              f[y] = 0.0f;
+            }
+          }
+          // where P^T of this thread's key lies: row r at (pbuf ^ (r & 7) << 4) + 128 r
+          const uint32_t pbuf = sbase + C::kOffP + sb * C::kP + (lrow >> 6) * C::kPChunk + gcol * 128 +
+                                ((lrow & 63) >> 3 << 4) + 2 * (lrow & 7);
 #pragma unroll
           for (int c = 0; c < NC; ++c) {
             if constexpr (NC > 1) {
 #pragma unroll
-              for (int y = 0; y < kTPS; ++y) tld16(t_s + y * N + c * 16, s[y]);
+              for (int y = 0; y < kTPS; ++y) {
+                scores(t_s + y * C::kSCols + c * 16, ks[y], all, vis[y] >> (c * CH), s[y]);
+              }
             }
             // running max (scaled units): rescale only when it grows by more than 2^8
-            float r[16], cs[CH];
+            // (loads first, and no branches among them: a load behind a condition would
+            // wait for the one before)
+            float mt[CH], old[CH], cs[CH];
+#pragma unroll
+            for (int i = 0; i < CH; ++i) {
+              mt[i] = top4(got[c * CH + i]);
+              cs[i] = col[c * CH + i];
+              old[i] = m[c * CH + i];
+            }
             bool any = rr != 1.0f;
 #pragma unroll
-            for (int i = 0; i < 16; ++i) r[i] = rr;
-#pragma unroll
             for (int i = 0; i < CH; ++i) {
-              const int h = c * CH + i;
-              cs[i] = col[h];
-              const float top = top4(got[h]);
-              const float mt = (top == -INFINITY) ? -INFINITY : top * cs[i];
-              if (mt > m[h] && (m[h] == -INFINITY || mt - m[h] > 8.0f)) {
-                const float q = (m[h] == -INFINITY) ? 0.0f : ex2_approx(m[h] - mt);
-                l[h] *= q;
+              mt[i] *= cs[i];   // (-inf where no column sees a key)
+              // grows past old + 8, or past -inf at all
+              const bool grows = mt[i] > fmaxf(old[i] + 8.0f, -3.0e38f);
+              mt[i] = grows ? mt[i] : old[i];
+              any |= grows;
+            }
+            // m and R are the same in every thread, so the decision is too; the vote
+            // keeps the warp-collective TMEM accesses below uniform regardless.
+            any = __any_sync(0xffffffffu, any);
+            if (any) {
+              float r[16];
+#pragma unroll
+              for (int i = 0; i < 16; ++i) r[i] = rr;
+#pragma unroll
+              for (int i = 0; i < CH; ++i) {
+                const float q = old[i] == mt[i] ? 1.0f : ex2_approx(old[i] - mt[i]);   // (from -inf: 0)
+                l[c * CH + i] *= q;
                 r[i] *= q;
-                m[h] = mt;
-                any = true;
+              }
+              __syncwarp();
+#pragma unroll
+              for (int i = 0; i < CH; ++i)
+                if (lane == i) m[c * CH + i] = mt[i];
+              __syncwarp();
+              // u^T rescale (rare): needs this group's last P.V complete
+              if (t > first_t) {
+                if (TG == 1 && !pv_wait(step - 1)) { ok = false; break; }
+                tc_fence_after();
+                float o[16];
+                tld<16>(t_u + c * 16, o);
+#pragma unroll
+                for (int i = 0; i < CH; ++i) o[i] *= r[i];
+                tst16(t_u + c * 16, o);
+                tmem_wait_st();
               }
             }
-            // u^T rescale (rare): needs the previous step's P.V complete.  m and R are
-            // the same in every thread, so the decision is too; the vote keeps the
-            // warp-collective TMEM accesses below uniform regardless.
-            any = __any_sync(0xffffffffu, any);
-            if (t > w.t0 && any) {
-              if (!pv_wait(step - 1)) { ok = false; break; }
-              tc_fence_after();
-              float o[16];
-              tld16(t_u + c * 16, o);
-#pragma unroll
-              for (int i = 0; i < CH; ++i) o[i] *= r[i];
-              tst16(t_u + c * 16, o);
-              tmem_wait_st();
-            }
 #pragma unroll
             for (int i = 0; i < CH; ++i) {
               const int h = c * CH + i;
-              const float mh = (m[h] == -INFINITY) ? 0.0f : m[h] - kPLift;
+              const float mh = fmaxf(mt[i], -3.0e38f) - kPLift;   // (finite)
 #pragma unroll
               for (int y = 0; y < kTPS; ++y) {
-                const bool on = (vis[y] >> h) & 1;
-                const float e = on ? ex2_approx(s[y][i] * ks[y] * cs[i] - mh) : 0.0f;
+                const float e = ex2_approx(fmaf(s[y][i], cs[i], -mh));
                 l[h] += e;
-                uint8_t* pbuf = smem + C::kOffP + sb * C::kP + (lrow >> 6) * C::kPChunk;
-                *reinterpret_cast<__half*>(pbuf + swizzled<128>(y * N + gcol + h, 2 * (lrow & 63))) =
-                    __float2half_rn(on ? e * f[y] : 0.0f);
+                store_half((pbuf ^ ((h & 7) << 4)) + (y * N + h) * 128, e * f[y]);
               }
+            }
+          }
+          if (strange) {
+            // a value's scale that is no number reaches the columns that see its key
+#pragma unroll 1
+            for (int i = 0; i < kTPS * GT; ++i) {
+              const int y = i / GT, h = i - y * GT;
+              const float v = y == 0 ? vs[0] : vs[kTPS - 1];
+              const uint32_t seen = y == 0 ? vis[0] : vis[kTPS - 1];
+              if (!(v * inv_r <= 4.0f) && ((seen >> h) & 1))
+                store_half((pbuf ^ ((h & 7) << 4)) + (y * N + h) * 128, __uint_as_float(0x7fffffffu));
             }
           }
           if (!ok) break;
@@ -835,85 +1023,128 @@ __global__ void __launch_bounds__(Cfg<GT, SG, DA>::kThreads, 1) tree_kernel(cons
         }
         if (!ok) break;
         if (lane == 0) mbar_arrive(b_q_empty + 8 * qs);   // (what it read of the slot: the columns' factors and masks)
-        // the piece's exp-sums over all its keys, then u^T R / l
+        // the piece's exp-sums over all its keys, then u^T R / l (rolled over the
+        // columns: this code runs once per unit)
 #pragma unroll
-        for (int h = 0; h < GT; ++h) {
+        for (int c = 0; c < NC; ++c) {
+          float v[CH];
 #pragma unroll
-          for (int o = 16; o > 0; o >>= 1) l[h] += __shfl_xor_sync(0xffffffffu, l[h], o);
+          for (int i = 0; i < CH; ++i) v[i] = l[c * CH + i];
+          put_folded(c, fold_columns<CH>(v, lane, [](float a, float b) { return a + b; }));
         }
-        if (!exchange(l, 0.0f)) break;
-        {
-          const float4* got = red + ((red_cnt - 1) & 1) * (GT + 1);
-#pragma unroll
-          for (int h = 0; h < GT; ++h) l[h] = (got[h].x + got[h].y) + (got[h].z + got[h].w);
+        if (!meet()) break;
+        const float4* got = red + ((red_cnt - 1) & 1) * (GT + 1);
+        auto sum_of = [&](int h) {
+          const float4 v = got[h];
+          return (v.x + v.y) + (v.z + v.w);
+        };
+        float* fin_m = reinterpret_cast<float*>(smem + C::kOffFin);
+        float* fin_l = fin_m + GT;
+        float* fin_r = fin_l + GT;
+        if (TG == 2 && grp == 1) {
+          // hands its maxima and sums over (of no step: -inf and 0), once the first group
+          // has read those of the unit before
+          if (units_done > 0 &&
+              !wait_warp(b_o_free, (units_done - 1) & 1, wc, ATTN_DEVERR_WAIT_TIMEOUT_SITE(kSiteODone)))
+            break;
+          if (sw == 0) {
+            if (lane < GT) {
+              fin_m[lane] = m[lane];
+              fin_l[lane] = sum_of(lane);
+            }
+            if (lane == 0) *fin_r = R;
+            __syncwarp();
+            if (lane == 0) mbar_arrive(b_fin);
+          }
+          ++units_done;
+          continue;
         }
         if (!pv_wait(step - 1)) break;
+        if (TG == 2) {
+          if (step - step0 >= 2 && !pv_wait(step - 2)) break;
+          if (!wait_warp(b_fin, units_done & 1, wc, ATTN_DEVERR_WAIT_TIMEOUT_SITE(kSiteMerge))) break;
+        }
         tc_fence_after();
         const bool whole = w.t0 == 0 && w.t1 == w.T;
         const int slot = 2 * blockIdx.x + (w.t0 == 0 ? 1 : 0);
+        // A column's maximum and sum, and the factors of the groups' u^T over the sum
+        // (0: it has none); a lane per column, left in shared memory for the warp
+        float4* factors = reinterpret_cast<float4*>(smem + C::kOffFactor) + (4 * grp + sw) * GT;
+        if (lane < GT) {
+          float lh = sum_of(lane), mx = m[lane];
+          float w0 = lh != 0.0f ? R : 0.0f, w1 = 0.0f;
+          if constexpr (TG == 2) {
+            const float m1 = fin_m[lane], l1 = fin_l[lane];
+            if (l1 != 0.0f) {
+              const float top = lh != 0.0f ? fmaxf(mx, m1) : m1;
+              const float a = lh != 0.0f ? ex2_approx(mx - top) : 0.0f, b = ex2_approx(m1 - top);
+              w0 *= a;
+              w1 = b * *fin_r;
+              lh = (lh != 0.0f ? lh * a : 0.0f) + l1 * b;
+              mx = top;
+            }
+          }
+          const float inv = lh != 0.0f ? 1.0f / lh : 0.0f;   // 0: saw no key; a NaN stays one
+          factors[lane] = make_float4(mx, lh * kPDrop, w0 * inv, w1 * inv);
+        }
+        __syncwarp();
+        auto joined = [&](int h) {
+          const float4 f = factors[h];
+          float a[1], b[1];
+          tld_start<1>(t_u + h, a);
+          if constexpr (TG == 2) tld_start<1>(t_u + C::kRows + h, b);
+          else b[0] = 0.0f;
+          tld_wait<1>(a, b);
+          return (f.z != 0.0f ? a[0] * f.z : 0.0f) + (f.w != 0.0f ? b[0] * f.w : 0.0f);
+        };
         // u = u_a + u_b at head dimension 64: lanes 64-127 hand u_b over in the rows of
-        // this group's columns in the first P^T buffer, idle now that every P.V so far
-        // has completed; this group writes them next after its next exchange
+        // this group's columns in the first P^T buffer, idle now that every P.V that read
+        // it has completed; this group writes them next after its next meeting
         auto handed = [&](int h, int i) {
           return reinterpret_cast<float*>(smem + C::kOffP + (i >> 5) * C::kPChunk + (gcol + h) * 128 + (i & 31) * 4);
         };
         if constexpr (kTPS == 2) {
           if (lrow >= 64) {
-#pragma unroll
-            for (int c = 0; c < NC; ++c) {
-              float o[16];
-              tld16(t_u + c * 16, o);
-#pragma unroll
-              for (int i = 0; i < CH; ++i) *handed(c * CH + i, lrow - 64) = o[i];
+#pragma unroll 1
+            for (int h = 0; h < G; ++h) {
+              *handed(h, lrow - 64) = joined(h);
             }
             __syncwarp();
             if (lane == 0) mbar_arrive(bar_xch);
           } else {
-            if (!mbar_wait_warp(bar_xch, xch_cnt & 1, wc, ATTN_DEVERR_WAIT_TIMEOUT_SITE(kSiteXchg))) break;
+            if (!wait_warp(bar_xch, xch_cnt & 1, wc, ATTN_DEVERR_WAIT_TIMEOUT_SITE(kSiteXchg))) break;
           }
           ++xch_cnt;
         }
         if (kTPS == 1 || lrow < 64) {
-#pragma unroll
-          for (int c = 0; c < NC; ++c) {
-            float o[16];
-            tld16(t_u + c * 16, o);
-#pragma unroll
-            for (int i = 0; i < CH; ++i) {
-              const int h = c * CH + i;
-              if (h >= G) break;
-              if constexpr (kTPS == 2) o[i] += *handed(h, lrow);
-              const float v = (l[h] != 0.0f) ? o[i] / l[h] * R : 0.0f;   // 0: saw no key; a NaN stays one
-              if (whole) {
-                int head;
-                const long long at = (static_cast<long long>(out_row(h, head)) * p.Hq + head) * DA + lrow;
-                p.o[at] = p.fp16 ? __half_as_ushort(__float2half_rn(v)) : __bfloat16_as_ushort(__float2bfloat16_rn(v));
-              } else {
-                p.part_o[(static_cast<size_t>(slot) * N + gcol + h) * DA + lrow] = v;
-              }
+#pragma unroll 1
+          for (int h = 0; h < G; ++h) {
+            float v = joined(h);
+            if constexpr (kTPS == 2) v += *handed(h, lrow);
+            if (whole) {
+              int head;
+              const long long at = (static_cast<long long>(out_row(h, head)) * p.Hq + head) * DA + lrow;
+              p.o[at] = p.fp16 ? __half_as_ushort(__float2half_rn(v)) : __bfloat16_as_ushort(__float2bfloat16_rn(v));
+            } else {
+              p.part_o[(static_cast<size_t>(slot) * N + gcol + h) * DA + lrow] = v;
             }
+          }
+        }
+        if (sw == 0 && lane < G) {
+          const float mx = factors[lane].x, lh = factors[lane].y;
+          if (whole) {
+            int head;
+            const long long row = out_row(lane, head);
+            p.lse[static_cast<long long>(head) * p.total + row] =
+                (lh != 0.0f) ? mx * 0.69314718055994531f + __logf(lh) : -INFINITY;
+          } else {
+            p.part_ml[slot * N + gcol + lane] = make_float2(mx, lh);
           }
         }
         tc_fence_before();
         __syncwarp();
         if (lane == 0) mbar_arrive(b_o_free);   // u^T may be overwritten by the next unit
-        if (sw == 0 && lane < G) {
-          float lv = 0.0f, mv = -INFINITY;
-#pragma unroll
-          for (int h = 0; h < GT; ++h)
-            if (h == lane) {
-              lv = l[h] * kPDrop;
-              mv = m[h];
-            }
-          if (whole) {
-            int head;
-            const long long row = out_row(lane, head);
-            p.lse[static_cast<long long>(head) * p.total + row] =
-                (lv != 0.0f) ? mv * 0.69314718055994531f + __logf(lv) : -INFINITY;
-          } else {
-            p.part_ml[slot * N + gcol + lane] = make_float2(mv, lv);
-          }
-        }
+        ++units_done;
         // the unit's pieces lie on the ranges p / range ... (p + T - 1) / range
         if (!whole && w.t0 == 0 && tid == 64)
           p.rec[blockIdx.x] = make_int4(w.b, w.hc * p.abreast + place,
@@ -996,7 +1227,7 @@ __global__ void __launch_bounds__(128) tree_merge_kernel(const __grid_constant__
         Lt += s_l[k] * r;
         at += s_o[k][i] * r;
       }
-      const int token = (col0 + h) / p.group, head = g * p.group + (col0 + h) - token * p.group;
+      const int token = token_of(p, col0 + h), head = g * p.group + (col0 + h) - token * p.group;
       const long long row = row0 + token;
       const float v = Lt != 0.0f ? at / Lt : 0.0f;
       p.o[(row * p.Hq + head) * DA + i] =
@@ -1047,8 +1278,7 @@ cudaError_t pick(const Params& p, int cols, int grid, cudaStream_t stream) {
   if (cols <= 4) return launch<4, 1, DA>(p, cols, grid, stream);
   if (cols <= 8) return launch<8, 1, DA>(p, cols, grid, stream);
   if (cols <= 16) return launch<16, 1, DA>(p, cols, grid, stream);
-  if (cols <= 32) return launch<32, 1, DA>(p, cols, grid, stream);
-  return launch<32, 2, DA>(p, cols, grid, stream);
+  return launch<16, 2, DA>(p, cols, grid, stream);
 }
 
 }  // namespace tree
