@@ -27,7 +27,7 @@ SOURCES = ["attn_host.cu", "attn_noalloc.cu", "attn_pad.cu", "attn_rotary.cu", "
            "attn_pair_d128.cu", "attn_decode_tc.cu", "attn_kernels_rope.cu", "attn_kernels_sorted.cu",
            "attn_rope_scaled.cu", "attn_paged.cu", "attn_paged_decode.cu", "attn_paged_fwd.cu", "attn_paged_weights.cu", "attn_evict.cu",
            "attn_norm.cu", "attn_cache_fp8.cu", "attn_tree_fp8.cu", "attn_tree_fp8_d64.cu",
-           "attn_tree_fp8_d128.cu"]
+           "attn_tree_fp8_d128.cu", "attn_tree_fp8_rows_d64.cu", "attn_tree_fp8_rows_d128.cu"]
 
 
 def nvcc() -> str:

@@ -15,9 +15,9 @@ namespace tree {
 namespace {
 
 size_t rec_bytes(int sms) { return (static_cast<size_t>(sms) * sizeof(int4) + 255) / 256 * 256; }
-size_t ml_bytes(int sms) { return static_cast<size_t>(2 * sms) * kMostCols * sizeof(float2); }
+size_t ml_bytes(int sms) { return static_cast<size_t>(2 * sms) * kRowsPerUnit * sizeof(float2); }
 long long workspace(int sms, int d) {
-  return static_cast<long long>(rec_bytes(sms) + ml_bytes(sms) + static_cast<size_t>(2 * sms) * kMostCols * d * sizeof(float));
+  return static_cast<long long>(rec_bytes(sms) + ml_bytes(sms) + static_cast<size_t>(2 * sms) * kRowsPerUnit * d * sizeof(float));
 }
 
 int device(DeviceInfo& info) {
@@ -83,18 +83,23 @@ int attn_tree_fp8(const void* q, void* o, float* lse, int B, int Hq, int total, 
   p.total = total;
   p.max_tokens = cu_seqlens_or_null ? max_tokens : 1;
   p.group = Hq / p.c.t.hkv;
-  // a unit holds up to 64 columns (token, head) of a key/value head; more of them
-  // are cut into units that each read the keys
+  // Up to 32 columns (token, head) of a key/value head are a unit of the kernel that has
+  // them as columns; more are rows, 128 to a unit, and the units of a head each read the
+  // keys.
   const long long cols = static_cast<long long>(p.max_tokens) * p.group;
   if (cols > (1 << 20)) return ATTN_EINVAL;
-  p.parts = static_cast<int>((cols + tree::kMostCols - 1) / tree::kMostCols);
+  const bool rows = cols > tree::kMostCols;
+  const int unit = rows ? tree::kRowsPerUnit : tree::kMostCols;
+  p.parts = static_cast<int>((cols + unit - 1) / unit);
   p.abreast = heads_abreast(p.c.t.hkv * p.parts, sms);
-  p.cuts = (p.c.t.max_pages << p.c.t.page_log2) > tree::kMinSteps * (d == 64 ? 256 : 128);
+  p.cuts = (p.c.t.max_pages << p.c.t.page_log2) > tree::kMinSteps * (d == 64 && !rows ? 256 : 128);
   p.fp16 = fp16;
   p.inv_group = 1.0f / static_cast<float>(p.group);
   p.scale_log2 = scale * 1.4426950408889634f;
-  const int most = static_cast<int>(std::min<long long>(cols, tree::kMostCols));
-  const cudaError_t e = d == 64 ? tree::launch_d64(p, most, sms, stream) : tree::launch_d128(p, most, sms, stream);
+  const int most = static_cast<int>(std::min<long long>(cols, unit));
+  cudaError_t e;
+  if (rows) e = d == 64 ? tree::launch_rows_d64(p, most, sms, stream) : tree::launch_rows_d128(p, most, sms, stream);
+  else e = d == 64 ? tree::launch_d64(p, most, sms, stream) : tree::launch_d128(p, most, sms, stream);
   return e == cudaSuccess ? ATTN_OK : ATTN_ELAUNCH;
 }
 

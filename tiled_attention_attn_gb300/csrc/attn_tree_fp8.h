@@ -10,7 +10,8 @@ namespace attn {
 namespace tree {
 
 constexpr int kKeys = 128;     // keys per tile
-constexpr int kMostCols = 32;  // columns (token, head) of a unit
+constexpr int kMostCols = 32;      // columns (token, head) of a unit of attn_tree_fp8_kernel.cuh
+constexpr int kRowsPerUnit = 128;  // and of attn_tree_fp8_rows.cuh, which has them as rows
 constexpr int kMinSteps = 4;   // pieces of a cut unit are at least about this long
 
 struct Params {
@@ -39,6 +40,9 @@ struct Params {
 // cols: the most columns that a unit of the call has.
 cudaError_t launch_d64(const Params& p, int cols, int grid, cudaStream_t stream);
 cudaError_t launch_d128(const Params& p, int cols, int grid, cudaStream_t stream);
+// Units of up to kRowsPerUnit columns, as rows.
+cudaError_t launch_rows_d64(const Params& p, int cols, int grid, cudaStream_t stream);
+cudaError_t launch_rows_d128(const Params& p, int cols, int grid, cudaStream_t stream);
 
 }  // namespace tree
 }  // namespace attn

@@ -40,30 +40,14 @@
 // Head dimension 64: a step covers two tiles, one P.V serves both (M = 128 spans
 // the two tiles' d; the product's diagonal blocks are u_a and u_b).
 #pragma once
-#include <cuda_bf16.h>
-#include <cuda_fp16.h>
-#include <cuda_fp8.h>
-#include <cuda_runtime.h>
-
-#include <cstdint>
-
-#include "attn_paged_line.cuh"
-#include "attn_params.h"
-#include "attn_tree_fp8.h"
-#include "ptx.cuh"
+#include "attn_tree_fp8_parts.cuh"
 
 namespace attn {
 namespace tree {
 
-// Warps: K's TMA, the MMA, four of softmax, V's TMA and the scales, the queries,
-// four that widen V, and four more of softmax.
-constexpr int kWarpK = 0, kWarpMMA = 1, kWarpV = 6, kWarpQ = 7, kWarpWiden = 8, kWarpSoft2 = 12;
 constexpr int kRaw = kKeys * 128;       // a stage of K, or of V, in bytes
-constexpr int kWide = kKeys * 128 * 2;  // a step's V in fp16: two chunks of 128-byte rows
-constexpr int kWideChunk = kWide / 2;
-constexpr int kRing = 4;                // stages of scales
-constexpr float kPLift = 7.0f;          // log2 of the factor of P'
-constexpr float kPDrop = 0x1p-7f;
+constexpr int kWide = 2 * kRaw;         // a step's V in fp16: two chunks of 128-byte rows
+constexpr int kWideChunk = kRaw;
 
 // Two groups of four softmax warps, GT columns each: of 32 and 64 columns (SG = 2)
 // each takes half; up to 16 columns (SG = 1, TG = 2) they take turns, step by step,
@@ -73,7 +57,6 @@ template <int GT_, int SG_, int DA>
 struct Cfg {
   static constexpr int GT = GT_, SG = SG_, TG = 3 - SG;
   static constexpr int N = GT * SG < 16 ? 16 : GT * SG;
-  static constexpr int kThreads = 32 * 16;
   static constexpr int kTPS = 128 / DA;            // tiles per step
   static constexpr int KS = kKeys * kTPS;          // keys per step
   static constexpr int kRows = kTPS * N;           // rows of P^T (the P.V's N)
@@ -109,248 +92,10 @@ struct Cfg {
   static_assert(kSmem <= 227 * 1024 && kUsedCols <= 512, "shared and tensor memory");
 };
 
-// The CTA's walk over units: (b, hc) in order, unit at position p of the line
-// of steps with T steps and one more for its fixed cost.
-struct Walk {
-  int b, hc;          // hc: group of p.abreast units; this CTA's is hc * abreast + its place
-  long long p, end;   // unit start; end of this CTA's range
-  long long begin;
-  int n, T;           // keys, steps
-  int cols, row0, ctx;   // columns (token, head) of a key/value head; first row of q; keys before the new tokens
-  int t0, t1;         // this CTA's steps of the unit
-};
-
-// Keys and new tokens of sequence b; one without new tokens takes no time, so it
-// has no keys either.
-__device__ __forceinline__ void sequence(const Params& p, int b, int& n, int& tokens, int& row0) {
-  if (p.cu == nullptr) {
-    tokens = 1;
-    row0 = b;
-    n = paged_len(p.c.t, b, p.err);
-    return;
-  }
-  chunk_and_keys(p.c.t, p.cu, b, p.total, tokens, row0, n, p.err);
-  if (tokens > p.max_tokens) {
-    atomicCAS(p.err, 0, ATTN_DEVERR_BAD_SEQLENS);
-    tokens = 0;
-  }
-  if (tokens == 0) n = 0;
-}
-
-template <int KS>
-__device__ __forceinline__ int steps_of(int n) { return (n + KS - 1) / KS; }
-
-template <int KS>
-__device__ __forceinline__ void enter(const Params& p, Walk& w) {
-  int tokens;
-  sequence(p, w.b, w.n, tokens, w.row0);
-  w.T = steps_of<KS>(w.n);
-  w.cols = tokens * p.group;
-  w.ctx = w.n - tokens;
-}
-
-// The next unit that has something to do here; false at the range's end.
-template <int KS>
-__device__ __forceinline__ bool next_unit(const Params& p, Walk& w, bool first) {
-  const int nh = p.c.t.hkv * p.parts / p.abreast;
-  while (true) {
-    if (!first) {
-      w.p += w.T + 1;
-      if (++w.hc == nh) {
-        w.hc = 0;
-        if (++w.b < p.B) enter<KS>(p, w);
-      }
-    }
-    first = false;
-    if (w.b >= p.B || w.p >= w.end) return false;
-    if (part_of<kMinSteps>(w.p, w.T, w.begin, w.end, w.t0, w.t1)) return true;
-  }
-}
-
-// The table's entry for a key, read a step before it is used so that nothing waits
-// for it, and the page that it names.  -1: past the last key; no page: num_pages
-// (its rows lie past the pool and read as zeros).
-__device__ __forceinline__ int entry_of(const Params& p, const Walk& w, int key) {
-  return key < w.n ? __ldg(p.c.t.table + static_cast<long long>(w.b) * p.c.t.table_stride + (key >> p.c.t.page_log2)) : -1;
-}
-__device__ __forceinline__ int page_of(const Params& p, const Walk& w, int entry, int key) {
-  if (key >= w.n) return -1;
-  if (entry >= 0 && entry < p.c.t.num_pages) return entry;
-  atomicCAS(p.err, 0, ATTN_DEVERR_BAD_PAGE);
-  return p.c.t.num_pages;
-}
-
-// cc / p.group for cc < 2^20: the rounding of the product (2^-23 of it, twice) stays
-// below the half that keeps it off the quotient's borders.
-__device__ __forceinline__ int token_of(const Params& p, int cc) {
-  return static_cast<int>((static_cast<float>(cc) + 0.5f) * p.inv_group);
-}
-
-// A unit's place among the heads: key/value head and first column.
-struct Unit {
-  int g, col0, cols;   // cols: of this unit, none where the sequence's tree ends before
-};
-template <int N>
-__device__ __forceinline__ Unit unit_of(const Params& p, const Walk& w, int place) {
-  const int unit = w.hc * p.abreast + place;
-  Unit u;
-  u.g = unit / p.parts;
-  u.col0 = (unit - u.g * p.parts) * N;
-  u.cols = min(N, w.cols - u.col0);
-  return u;
-}
-
-// Byte offset of byte `at` of row `row` in a K-major tile of rows of ROW bytes (128
-// or 64) under the swizzle of that width.
-template <int ROW>
-__device__ __forceinline__ uint32_t swizzled(int row, int at) {
-  const int x = ROW == 128 ? (row & 7) : ((row >> 1) & 3);
-  return static_cast<uint32_t>(row * ROW + ((((at >> 4) ^ x) << 4) | (at & 15)));
-}
-
-// Shared-memory matrix descriptor of a K-major tile of e4m3 rows of ROW bytes: as
-// sdesc_sw128, with the swizzle mode of the row's width (2: 128 bytes, 4: 64).
-template <int ROW>
-__device__ __forceinline__ uint64_t sdesc_rows(uint32_t saddr) {
-  const uint64_t d = sdesc_sw128(saddr, 16, 8 * ROW);
-  return ROW == 128 ? d : (d & ~(7ull << 61)) | (4ull << 61);
-}
-
-// D[tmem] (+)= A[smem] * B[smem]^T, 8-bit operands, fp32 accumulation.
-__device__ __forceinline__ void umma_ss_f8(uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc, uint32_t idesc,
-                                           uint32_t accumulate) {
-  asm volatile(
-      "{\n\t.reg .pred p;\n\t"
-      "setp.ne.b32 p, %4, 0;\n\t"
-      "tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], %1, %2, %3, p;\n\t}"
-      :: "r"(d_tmem), "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(accumulate)
-      : "memory");
-}
-// kind::f8f6f4, e4m3 operands, both K-major.
-__host__ __device__ constexpr uint32_t idesc_e4m3(int M, int N) {
-  return (1u << 4) | (static_cast<uint32_t>(N >> 3) << 17) | (static_cast<uint32_t>(M >> 4) << 24);
-}
-
-// 4-byte asynchronous copy to shared memory, and the arrival of this thread's
-// copies so far on a barrier that counts its threads.
-__device__ __forceinline__ void copy4(uint32_t dst, const float* src) {
-  asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" :: "r"(dst), "l"(src) : "memory");
-}
-__device__ __forceinline__ void copies_arrive(uint32_t bar) {
-  asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" :: "r"(bar) : "memory");
-}
-
-// The waits of this kernel (ptx.cuh's in fewer instructions: many warps run code of
-// their own here, and fetching it counts): every lane polls, the limit is looked at
-// with each failed poll.
-__device__ __forceinline__ bool wait(uint32_t bar, uint32_t parity, const WaitCtl& w, int code) {
-  if (mbar_try_wait(bar, parity)) return true;
-  const uint64_t t0 = global_timer_ns();
-#pragma unroll 1
-  while (!mbar_try_wait(bar, parity)) {
-    if (*w.abort_flag) return false;
-    if (global_timer_ns() - t0 > w.timeout_ns) {
-      report_error(w, code);
-      return false;
-    }
-  }
-  return true;
-}
-__device__ __forceinline__ bool wait_warp(uint32_t bar, uint32_t parity, const WaitCtl& w, int code) {
-  return __all_sync(0xffffffffu, wait(bar, parity, w, code));
-}
-
-// W consecutive 32-bit columns of this thread's TMEM lane (W = 1, 4, 8 or 16); the
-// values are there after tld_wait.
-template <int W>
-__device__ __forceinline__ void tld_start(uint32_t taddr, float (&x)[W]) {
-  if constexpr (W == 1) {
-    asm volatile("tcgen05.ld.sync.aligned.32x32b.x1.b32 {%0}, [%1];" : "=f"(x[0]) : "r"(taddr));
-  } else if constexpr (W == 4) {
-    asm volatile("tcgen05.ld.sync.aligned.32x32b.x4.b32 {%0, %1, %2, %3}, [%4];"
-                 : "=f"(x[0]), "=f"(x[1]), "=f"(x[2]), "=f"(x[3]) : "r"(taddr));
-  } else if constexpr (W == 8) {
-    asm volatile("tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
-                 : "=f"(x[0]), "=f"(x[1]), "=f"(x[2]), "=f"(x[3]), "=f"(x[4]), "=f"(x[5]), "=f"(x[6]), "=f"(x[7])
-                 : "r"(taddr));
-  } else {
-    static_assert(W == 16, "columns");
-    asm volatile("tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15}, [%16];"
-                 : "=f"(x[0]), "=f"(x[1]), "=f"(x[2]), "=f"(x[3]), "=f"(x[4]), "=f"(x[5]), "=f"(x[6]), "=f"(x[7]),
-                   "=f"(x[8]), "=f"(x[9]), "=f"(x[10]), "=f"(x[11]), "=f"(x[12]), "=f"(x[13]), "=f"(x[14]), "=f"(x[15])
-                 : "r"(taddr));
-  }
-}
-// Waits for this thread's loads, and ties the values to the wait, so that no use of
-// them can be scheduled above it.
-template <int W>
-__device__ __forceinline__ void tie(float (&x)[W]) {
-#pragma unroll
-  for (int i = 0; i < W; ++i) asm volatile("" : "+f"(x[i]));
-}
-template <int W>
-__device__ __forceinline__ void tld_wait(float (&x)[W], float (&y)[W]) {
-  asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
-  tie<W>(x);
-  tie<W>(y);
-}
-template <int W>
-__device__ __forceinline__ void tld(uint32_t taddr, float (&x)[W]) {
-  tld_start<W>(taddr, x);
-  asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
-  tie<W>(x);
-}
-__device__ __forceinline__ void tst16(uint32_t taddr, const float (&x)[16]) {
-  uint32_t r[16];
-#pragma unroll
-  for (int i = 0; i < 16; ++i) r[i] = __float_as_uint(x[i]);
-  tmem_st_32x32b_x16(taddr, r);
-}
-
-__device__ __forceinline__ void store_half(uint32_t at, float x) {
-  asm volatile("st.shared.b16 [%0], %1;" :: "r"(at), "h"(__half_as_ushort(__float2half_rn(x))) : "memory");
-}
-
-// Combines n columns (a power of two, at most 32) over the warp's lanes: each
-// exchange halves the columns that a lane holds, n - 1 shuffles and the rest of five
-// instead of 5 n.  Returns the result of column lane >> (5 - log2 n).
-template <int n, typename Op>
-__device__ __forceinline__ float fold_columns(float (&v)[n], int lane, Op op) {
-  int o = 16;
-#pragma unroll
-  for (int half = n / 2; half > 0; half >>= 1, o >>= 1) {
-    const bool upper = lane & o;
-#pragma unroll
-    for (int i = 0; i < half; ++i) {
-      const float keep = upper ? v[i + half] : v[i], give = upper ? v[i] : v[i + half];
-      v[i] = op(keep, __shfl_xor_sync(0xffffffffu, give, o));
-    }
-  }
-#pragma unroll
-  for (; o > 0; o >>= 1) v[0] = op(v[0], __shfl_xor_sync(0xffffffffu, v[0], o));
-  return v[0];
-}
-
-// Two e4m3 values as the fp16 pair.
-__device__ __forceinline__ uint32_t widen2(uint32_t x) {
-  uint32_t h;
-  asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(h) : "h"(static_cast<unsigned short>(x)));
-  return h;
-}
-// Two floats as the nearest e4m3 pair, which is taken off them.
-__device__ __forceinline__ uint32_t take2(float& a, float& b) {
-  const uint32_t v = __nv_cvt_float2_to_fp8x2(make_float2(a, b), __NV_SATFINITE, __NV_E4M3);
-  const uint32_t h = widen2(v);
-  const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&h));
-  a -= f.x;
-  b -= f.y;
-  return v;
-}
-
 template <int GT, int SG, int DA>
-__global__ void __launch_bounds__(Cfg<GT, SG, DA>::kThreads, 1) tree_kernel(const __grid_constant__ Params p) {
+__global__ void __launch_bounds__(kThreads, 1) tree_kernel(const __grid_constant__ Params p) {
   using C = Cfg<GT, SG, DA>;
-  constexpr int N = C::N, kTPS = C::kTPS, KS = C::KS, TG = C::TG, kStages = C::kStages, kSlots = C::kQSlots, kThreads = C::kThreads;
+  constexpr int N = C::N, kTPS = C::kTPS, KS = C::KS, TG = C::TG, kStages = C::kStages, kSlots = C::kQSlots;
   extern __shared__ __align__(1024) uint8_t smem_raw[];
   // (by an offset, not through an integer: the accesses stay ones of shared memory)
   uint8_t* smem = smem_raw + ((1024 - (smem_u32(smem_raw) & 1023)) & 1023);
@@ -409,95 +154,24 @@ __global__ void __launch_bounds__(Cfg<GT, SG, DA>::kThreads, 1) tree_kernel(cons
     tma_prefetch_desc(&p.tm_v);
   }
 
-  // the line of steps: each thread a strip of sequences, then a prefix sum
-  const int nh = p.c.t.hkv * p.parts / p.abreast;
-  const int place = blockIdx.x % p.abreast, ranges = gridDim.x / p.abreast, range_id = blockIdx.x / p.abreast;
-  const int strip = (p.B + kThreads - 1) / kThreads;
-  const int b_lo = min(tid * strip, p.B), b_hi = min(b_lo + strip, p.B);
-  auto cost_of = [&](int b) {
-    int n, tokens, row0;
-    sequence(p, b, n, tokens, row0);
-    return static_cast<long long>(nh) * (steps_of<KS>(n) + 1);
-  };
-  long long mine = 0, total, units;
-  for (int b = b_lo; b < b_hi; ++b) mine += cost_of(b);
-  const long long before = block_prefix<kThreads>(
-      mine, static_cast<int>(min(static_cast<long long>(nh) * (b_hi - b_lo), 1LL << 24)), warp_sums, total, units);
-  const long long range = range_of<kMinSteps>(total, units, ranges);
-  // (SMs past the last whole range idle)
-  const long long begin = range_id < ranges ? range_id * range : total, end = min(begin + range, total);
-  if (begin >= before && begin < before + mine) {
-    long long at = before;
-    for (int b = b_lo; b < b_hi; ++b) {
-      const long long cost = cost_of(b);
-      if (begin < at + cost) {
-        *start_b = b;
-        *start_p = at;
-        break;
-      }
-      at += cost;
-    }
-  }
-  if (tid == 0) p.rec[blockIdx.x] = make_int4(0, 0, 0, 0);
+  const Line line = find_line<KS>(p, start_b, start_p, warp_sums);
+  const int place = line.place;
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = *tmem_slot;
   grid_launch_dependents();
-  Walk w = {};
-  w.b = *start_b;
-  w.begin = begin;
-  w.end = end;
-  w.p = *start_p;
-  if (w.b < p.B) {
-    enter<KS>(p, w);
-    w.hc = static_cast<int>((begin - w.p) / (w.T + 1));
-    w.p += static_cast<long long>(w.hc) * (w.T + 1);
-  }
+  Walk w = enter_line<KS>(p, line, *start_b, *start_p);
 
-  if (warp == kWarpK || warp == kWarpV) {
-    // ------------------------------------------------------------------ TMA producers
-    uint32_t cnt = 0;
-    const int box = min(1 << p.c.t.page_log2, kKeys);   // tokens per box
-    const int n_pg = kKeys / box;                       // boxes along a tile
-    // this lane's box: page `pg` of tile `y` of the step
-    const int pg = lane % n_pg, y = lane / n_pg;
-    const bool of_v = warp == kWarpV, has = lane < kTPS * n_pg;
-    const CUtensorMap* map = of_v ? &p.tm_v : &p.tm_k;
-    const uint32_t dst0 = sbase + (of_v ? C::kOffV : C::kOffK) + (y * kKeys + pg * box) * DA;
-    const uint32_t b_full = of_v ? b_v_full : b_k_full, b_empty = of_v ? b_v_empty : b_k_empty;
-    const int key_off = y * kKeys + pg * box;
-    auto box_entry = [&](int t) { return has ? entry_of(p, w, t * KS + key_off) : -1; };
-    bool ok = true;
-    for (bool more = next_unit<KS>(p, w, true); more && ok; more = next_unit<KS>(p, w, false)) {
-      const Unit u = unit_of<N>(p, w, place);
-      if (w.t1 <= w.t0 || u.cols <= 0) continue;
-      int entry = box_entry(w.t0);
-      for (int t = w.t0; t < w.t1; ++t) {
-        const int st = cnt % kStages;
-        const int next = t + 1 < w.t1 ? box_entry(t + 1) : -1;
-        if (!wait_warp(b_empty + 8 * st, ((cnt / kStages) & 1) ^ 1, wc,
-                            ATTN_DEVERR_WAIT_TIMEOUT_SITE(kSiteKEmpty))) { ok = false; break; }
-        const int page = has ? page_of(p, w, entry, t * KS + key_off) : -1;
-        const uint32_t n_box = __popc(__ballot_sync(0xffffffffu, page >= 0));
-        if (lane == 0) mbar_arrive_expect_tx(b_full + 8 * st, n_box * box * DA);
-        __syncwarp();
-        if (page >= 0)
-          tma_load_4d(dst0 + st * kRaw, map, b_full + 8 * st, 0, u.g, (t * KS + key_off) & ((1 << p.c.t.page_log2) - 1), page);
-        entry = next;
-        ++cnt;
-      }
-    }
-    if (lane == 0 && *abort_flag) {
-      // let the loads already issued land before the CTA exits
-      for (int s = 0; s < kStages; ++s) {
-        const uint32_t n = (cnt + kStages - 1 - s) / kStages;
-        if (n > 0) mbar_wait(b_full + 8 * s, (n - 1) & 1, wc, ATTN_DEVERR_WAIT_TIMEOUT_SITE(kSiteDrain), false);
-      }
-    }
+  if (warp == kWarpK) {
+    produce<DA, kTPS, N, kStages>(p, w, place, &p.tm_k, sbase + C::kOffK, b_k_full, b_k_empty, wc);
+  } else if (warp == kWarpV) {
+    produce<DA, kTPS, N, kStages>(p, w, place, &p.tm_v, sbase + C::kOffV, b_v_full, b_v_empty, wc);
+  } else if (warp >= kWarpWiden && warp < kWarpWiden + 4) {
+    widen_and_scales<DA, kTPS, N, kStages>(p, w, place, smem, C::kOffV, C::kOffW, C::kOffScale, b_v_full, b_v_empty,
+                                           b_w_full, b_pv_done, b_c_full, wc);
   } else if (warp == kWarpQ) {
     // ------------------------------------------------------------------ queries
-    constexpr int E = DA / 32;      // features per lane
     uint32_t cnt = 0;
     bool ok = true;
     for (bool more = next_unit<KS>(p, w, true); more && ok; more = next_unit<KS>(p, w, false)) {
@@ -509,64 +183,7 @@ __global__ void __launch_bounds__(Cfg<GT, SG, DA>::kThreads, 1) tree_kernel(cons
       unsigned long long* mask = reinterpret_cast<unsigned long long*>(smem + C::kOffMask) + slot * N;
       if (!wait_warp(b_q_empty + 8 * slot, ((cnt / kSlots) & 1) ^ 1, wc,
                           ATTN_DEVERR_WAIT_TIMEOUT_SITE(kSiteQEmpty))) break;
-      // Row by row, the next two on their way, in a short loop: it runs once per unit,
-      // so fetching its code counts.  (Columns past u.cols hold anything: nothing reads
-      // their results.)
-      int head;
-      auto place_of = [&](int c) {   // row of q, and head
-        const int cc = u.col0 + c, token = token_of(p, cc);
-        head = u.g * p.group + cc - token * p.group;
-        return w.row0 + token;
-      };
-      auto load = [&](int c) {
-        uint2 v = make_uint2(0, 0);
-        if (c < u.cols) {
-          const long long row = place_of(c);
-          const uint16_t* src = p.q + (row * p.Hq + head) * DA + E * lane;
-          if constexpr (E == 4) v = __ldg(reinterpret_cast<const uint2*>(src));
-          else v.x = __ldg(reinterpret_cast<const uint32_t*>(src));
-        }
-        return v;
-      };
-      uint2 next = load(0), after = load(1);
-#pragma unroll 1
-      for (int c = 0; c < u.cols; ++c) {
-        const uint2 now = next;
-        next = after;
-        after = load(c + 2);
-        float x[4];
-#pragma unroll
-        for (int h = 0; h < 2; ++h) {
-          const uint32_t v = h == 0 ? now.x : now.y;
-          const float2 f = p.fp16 ? __half22float2(*reinterpret_cast<const __half2*>(&v))
-                                  : make_float2(__uint_as_float(v << 16), __uint_as_float(v & 0xffff0000u));
-          x[2 * h] = f.x;
-          x[2 * h + 1] = f.y;
-        }
-        uint32_t top = 0;   // as bits: a NaN counts above infinity
-#pragma unroll
-        for (int e = 0; e < 4; ++e) top = max(top, __float_as_uint(x[e]) & 0x7fffffffu);
-        top = __reduce_max_sync(0xffffffffu, top);
-        // 2^k with max 2^k in (224, 448]: 448 = 1.75 2^8
-        int k = 135 - static_cast<int>(top >> 23) - ((top & 0x7fffffu) > 0x600000u ? 1 : 0);
-        k = min(k, 120);   // (rows below 2^-112)
-        const float up = __uint_as_float(static_cast<uint32_t>(max(127 + k, 1)) << 23);
-        const float down = __uint_as_float(static_cast<uint32_t>(min(127 - k, 254)) << 23);
-        if (lane == 0) {
-          const int row = place_of(c);
-          col[c] = fmaxf(p.scale_log2 * down, 0x1p-126f);   // (positive: -inf stays -inf)
-          mask[c] = p.mask ? static_cast<unsigned long long>(__ldg(p.mask + row)) : (2ull << (row - w.row0)) - 1;
-        }
-        uint8_t* at = dst + swizzled<DA>(c, E * lane);
-#pragma unroll
-        for (int e = 0; e < 4; ++e) x[e] = top < 0x7f800000u ? x[e] * up : __uint_as_float(0x7fffffffu);
-#pragma unroll 1
-        for (int s = 0; s < 3; ++s, at += C::kQPiece) {
-          const uint32_t a = take2(x[0], x[1]);
-          if constexpr (E == 4) *reinterpret_cast<uint32_t*>(at) = a | take2(x[2], x[3]) << 16;
-          else *reinterpret_cast<uint16_t*>(at) = static_cast<uint16_t>(a);
-        }
-      }
+      convert_queries<DA>(p, w, u, 0, 1, dst, C::kQPiece, col, mask);
       fence_proxy_async_smem();
       __syncwarp();
       if (lane == 0) mbar_arrive(b_q_full + 8 * slot);
@@ -653,110 +270,10 @@ __global__ void __launch_bounds__(Cfg<GT, SG, DA>::kThreads, 1) tree_kernel(cons
       mbar_wait(b_drain, 0, wc, ATTN_DEVERR_WAIT_TIMEOUT_SITE(kSiteDrain), false);
     }
   } else {
-    // waits until the P.V of this CTA's step i (over all units) has completed: phase
-    // i >> 1 of pv_done(i & 1).  The next phase, step i + 2's, does not complete before
-    // the caller has handed over that step's operand, so the parity tells them apart
-    auto pv_wait = [&](uint32_t i) -> bool {
-      return wait_warp(b_pv_done + 8 * (i & 1), (i >> 1) & 1, wc, ATTN_DEVERR_WAIT_TIMEOUT_SITE(kSitePvDone));
-    };
+    auto pv_wait = [&](uint32_t i) { return wait_pv(b_pv_done, i, wc); };
     uint32_t step = 0;   // steps so far, all units
     bool ok = true;
-    if (warp >= kWarpWiden && warp < kWarpWiden + 4) {
-      // ---------------------------------------------------------------- V to fp16, and the scales
-      const int me = tid - 32 * kWarpWiden;
-      // Of head dimension 128 a thread takes 16 features of rows 16 i + row: eight lanes
-      // 4 words of two rows that differ in bits 0 and 2, so that they meet eight different
-      // words of the banks in the swizzled stage as well as in the fp16 tile.  Of 64, 16
-      // features of rows 32 i + row (tile i / 4): eight lanes two rows side by side.
-      const int row = kTPS == 1 ? 8 * (me >> 6) + (((me >> 4) & 3) ^ (((me >> 2) & 1) * 5)) : me >> 2;
-      const int c = kTPS == 1 ? 4 * ((me >> 3) & 1) + (me & 3) : me & 3;
-      const uint32_t from = kTPS == 1 ? swizzled<128>(row, 16 * c) : row * 64 + 16 * c;
-      const uint32_t to = (kTPS == 1 ? (c >> 2) * kWideChunk : 0) + row * 128 + ((2 * (c & 3) ^ (row & 7)) << 4);   // (the second word: bit 4 flipped)
-      // The scales are copied two steps ahead, over the units' ends: a walk of their
-      // own, whose table entries are read a step before that.  Key 128 i + me of the
-      // step.  Their ring needs no barrier for its empty stages: the stage of step i + 2
-      // was step i - 2's, whose P.V has completed when this is reached.
-      Walk wa = w;
-      Unit ua = {};
-      int ta = 0, entry[kTPS];
-      bool on = true;
-      uint32_t copied = 0;
-      auto settle = [&](bool first) {
-        do {
-          on = next_unit<KS>(p, wa, first);
-          first = false;
-          if (!on) return;
-          ua = unit_of<N>(p, wa, place);
-        } while (wa.t1 <= wa.t0 || ua.cols <= 0);
-        ta = wa.t0;
-      };
-      auto entries = [&]() {
-#pragma unroll
-        for (int i = 0; i < kTPS; ++i) entry[i] = on ? entry_of(p, wa, ta * KS + kKeys * i + me) : -1;
-      };
-      auto copy_scales = [&]() {
-        if (!on) return;
-        const uint32_t dst = sbase + C::kOffScale + (copied % kRing) * (2 * KS * 4) + me * 4;
-#pragma unroll
-        for (int i = 0; i < kTPS; ++i) {
-          const int key = ta * KS + kKeys * i + me, page = page_of(p, wa, entry[i], key);
-          if (page < 0 || page == p.c.t.num_pages) continue;
-          const int slot = key & ((1 << p.c.t.page_log2) - 1);
-          const long long at = page * p.c.c_page + slot * p.c.c_token + ua.g * p.c.c_head;
-          copy4(dst + kKeys * i * 4, p.c.ks + at);
-          copy4(dst + (KS + kKeys * i) * 4, p.c.vs + at);
-        }
-        copies_arrive(b_c_full + 8 * (copied % kRing));
-        ++copied;
-        if (++ta == wa.t1) settle(false);
-        entries();
-      };
-      settle(true);
-      entries();
-#pragma unroll 1
-      for (int i = 0; i < 2; ++i) copy_scales();
-      for (bool more = next_unit<KS>(p, w, true); more && ok; more = next_unit<KS>(p, w, false)) {
-        const Unit u = unit_of<N>(p, w, place);
-        if (w.t1 <= w.t0 || u.cols <= 0) continue;
-        for (int t = w.t0; t < w.t1; ++t) {
-          const int st = step % kStages;
-          if (step >= 2 && !pv_wait(step - 2)) { ok = false; break; }
-          if (!wait_warp(b_v_full + 8 * st, (step / kStages) & 1, wc, ATTN_DEVERR_WAIT_TIMEOUT_SITE(kSiteVFull))) {
-            ok = false;
-            break;
-          }
-          const uint8_t* src = smem + C::kOffV + st * kRaw + from;
-          uint8_t* dst = smem + C::kOffW + (step & 1) * kWide + to;
-          const int left = w.n - t * KS;   // keys from here on
-          uint4 x[8];
-#pragma unroll
-          for (int i = 0; i < 8; ++i) x[i] = *reinterpret_cast<const uint4*>(src + i * 2048);
-          if (left < KS) {
-            // rows past the last key may hold anything: 0 * NaN would be NaN
-#pragma unroll
-            for (int i = 0; i < 8; ++i)
-              if ((kTPS == 1 ? 16 * i : 32 * i) + row >= left) x[i] = make_uint4(0, 0, 0, 0);
-          }
-#pragma unroll
-          for (int i = 0; i < 8; ++i) {
-            uint8_t* y = kTPS == 1 ? dst + i * 2048 : dst + (i >> 2) * kWideChunk + (i & 3) * 4096;
-            *reinterpret_cast<uint4*>(y) =
-                make_uint4(widen2(x[i].x), widen2(x[i].x >> 16), widen2(x[i].y), widen2(x[i].y >> 16));
-            *reinterpret_cast<uint4*>(smem + ((y - smem) ^ 16)) =
-                make_uint4(widen2(x[i].z), widen2(x[i].z >> 16), widen2(x[i].w), widen2(x[i].w >> 16));
-          }
-          fence_proxy_async_smem();
-          __syncwarp();
-          if (lane == 0) {
-            mbar_arrive(b_v_empty + 8 * st);
-            mbar_arrive(b_w_full + 8 * (step & 1));
-          }
-          copy_scales();
-          ++step;
-        }
-      }
-      asm volatile("cp.async.wait_all;" ::: "memory");
-    } else {
+    {
       // ---------------------------------------------------------------- softmax warps
       const int grp = warp >= kWarpSoft2 ? 1 : 0;
       const int sw = warp - (grp ? kWarpSoft2 : 2);  // softmax warp 0..3 of its group
@@ -1148,7 +665,7 @@ __global__ void __launch_bounds__(Cfg<GT, SG, DA>::kThreads, 1) tree_kernel(cons
         // the unit's pieces lie on the ranges p / range ... (p + T - 1) / range
         if (!whole && w.t0 == 0 && tid == 64)
           p.rec[blockIdx.x] = make_int4(w.b, w.hc * p.abreast + place,
-                                        static_cast<int>((w.p + w.T - 1) / range) - range_id + 1, u.cols);
+                                        static_cast<int>((w.p + w.T - 1) / line.range) - line.range_id + 1, u.cols);
       }
     }
   }
@@ -1161,114 +678,11 @@ __global__ void __launch_bounds__(Cfg<GT, SG, DA>::kThreads, 1) tree_kernel(cons
   }
 }
 
-// Joins the pieces of the unit that block x's CTA began, for columns y, y + gridDim.y, ...
-// of the unit: M = max m_s, w_s = 2^(m_s - M) l_s, O = sum w_s O_s / sum w_s.  Four
-// warps take every fourth piece, a lane DA / 32 features; a programmatic
-// dependent of the attention kernel.
-template <int N, int DA>
-__global__ void __launch_bounds__(128) tree_merge_kernel(const __grid_constant__ Params p) {
-  constexpr int E = DA / 32;
-  __shared__ float s_m[4], s_l[4];
-  __shared__ float s_o[4][DA];
-  const int c = blockIdx.x, w = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  grid_wait_prerequisites();
-  const int4 rec = __ldcg(p.rec + c);
-  const int pieces = rec.z;
-  if (pieces <= 1) return;
-  const int g = rec.y / p.parts, col0 = (rec.y - g * p.parts) * N;
-  const int row0 = p.cu ? __ldg(p.cu + rec.x) : rec.x;
-  for (int h = blockIdx.y; h < rec.w; h += gridDim.y) {
-    float M = -INFINITY, L = 0.0f, acc[E];
-#pragma unroll
-    for (int e = 0; e < E; ++e) acc[e] = 0.0f;
-    auto slot = [&](int s) { return s == 0 ? 2 * c + 1 : 2 * (c + s * p.abreast); };
-    for (int s0 = w; s0 < pieces; s0 += 16) {
-      float2 ml[4];
-      float x[4][E];
-#pragma unroll
-      for (int u = 0; u < 4; ++u) {   // four pieces in flight
-        const int s = s0 + 4 * u;
-        const bool in = s < pieces;
-        ml[u] = in ? __ldcg(p.part_ml + slot(s) * N + h) : make_float2(-INFINITY, 0.0f);
-        const float* src = p.part_o + (static_cast<size_t>(in ? slot(s) : 0) * N + h) * DA + lane * E;
-#pragma unroll
-        for (int e = 0; e < E; e += 2) {
-          const float2 v = in ? __ldcg(reinterpret_cast<const float2*>(src + e)) : make_float2(0.0f, 0.0f);
-          x[u][e] = v.x;
-          x[u][e + 1] = v.y;
-        }
-      }
-#pragma unroll
-      for (int u = 0; u < 4; ++u) {
-        if (ml[u].y == 0.0f) continue;   // (l of NaN: the sums become NaN, whatever m)
-        const float mn = fmaxf(M, ml[u].x);
-        const float r = M == -INFINITY ? 0.0f : ex2_approx(M - mn), wt = ex2_approx(ml[u].x - mn) * ml[u].y;
-        M = mn;
-        L = L * r + wt;
-#pragma unroll
-        for (int e = 0; e < E; ++e) acc[e] = acc[e] * r + wt * x[u][e];
-      }
-    }
-    if (lane == 0) {
-      s_m[w] = M;
-      s_l[w] = L;
-    }
-#pragma unroll
-    for (int e = 0; e < E; ++e) s_o[w][lane * E + e] = acc[e];
-    __syncthreads();
-    const int i = threadIdx.x;
-    if (i < DA) {
-      const float Mx = fmaxf(fmaxf(s_m[0], s_m[1]), fmaxf(s_m[2], s_m[3]));
-      float Lt = 0.0f, at = 0.0f;
-#pragma unroll
-      for (int k = 0; k < 4; ++k) {
-        if (s_l[k] == 0.0f) continue;
-        const float r = ex2_approx(s_m[k] - Mx);
-        Lt += s_l[k] * r;
-        at += s_o[k][i] * r;
-      }
-      const int token = token_of(p, col0 + h), head = g * p.group + (col0 + h) - token * p.group;
-      const long long row = row0 + token;
-      const float v = Lt != 0.0f ? at / Lt : 0.0f;
-      p.o[(row * p.Hq + head) * DA + i] =
-          p.fp16 ? __half_as_ushort(__float2half_rn(v)) : __bfloat16_as_ushort(__float2bfloat16_rn(v));
-      if (i == 0)
-        p.lse[static_cast<long long>(head) * p.total + row] =
-            Lt != 0.0f ? Mx * 0.69314718055994531f + __logf(Lt) : -INFINITY;
-    }
-    __syncthreads();
-  }
-}
-
 template <int GT, int SG, int DA>
 cudaError_t launch(const Params& p, int cols, int grid, cudaStream_t stream) {
   using C = Cfg<GT, SG, DA>;
-  static bool attr_done[64] = {};   // per instantiation
-  int dev = 0;
-  cudaError_t e = cudaGetDevice(&dev);
-  if (e != cudaSuccess) return e;
-  if (dev < 0 || dev >= 64 || !attr_done[dev]) {
-    e = cudaFuncSetAttribute(tree_kernel<GT, SG, DA>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmem);
-    if (e != cudaSuccess) return e;
-    if (dev >= 0 && dev < 64) attr_done[dev] = true;
-  }
-  tree_kernel<GT, SG, DA><<<grid, C::kThreads, C::kSmem, stream>>>(p);
-  e = cudaGetLastError();
-  if (e != cudaSuccess) return e;
-  count_launch();
-  if (!p.cuts) return cudaSuccess;
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(grid, cols < 16 ? cols : 16);
-  cfg.blockDim = dim3(128);
-  cfg.stream = stream;
-  cudaLaunchAttribute attr[1];
-  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr[0].val.programmaticStreamSerializationAllowed = 1;
-  cfg.attrs = attr;
-  cfg.numAttrs = 1;
-  e = cudaLaunchKernelEx(&cfg, tree_merge_kernel<C::N, DA>, p);
-  if (e == cudaSuccess) count_launch();
-  return e;
+  static bool done[64] = {};   // per instantiation
+  return launch_with_merge<C::N, DA>(tree_kernel<GT, SG, DA>, C::kSmem, done, p, cols, grid, stream);
 }
 
 template <int DA>

@@ -1,0 +1,490 @@
+// The attention over caches of 8-bit floating point for trees with many columns
+// (token, head) per key/value head: they are the rows of the products,
+//   S = Q K^T   (M = 128 rows, N = 128 keys, K = d; e4m3, Q's pieces one after another)
+//   u += P V    (M = 128 rows, N = d, K = 128 keys; P in tensor memory)
+// so that a softmax thread owns a row and needs no other thread for its maximum and
+// sum.  (With the columns on N, as in attn_tree_fp8_kernel.cuh, their maxima over the
+// keys are exchanges between threads: 64 tokens of 4 heads over 16,384 keys took 579 us.)
+//
+// Two groups of four softmax warps take the steps of 128 keys in turns, each with
+// maxima, sums and an accumulator of its own, joined at the unit's end.  P overwrites
+// the S that it comes from.  The rest is as in attn_tree_fp8_kernel.cuh: V widened to
+// fp16 by four warps, weights in fp16 times their value's scale over R, R a power of
+// two above the scales so far.
+#pragma once
+#include "attn_tree_fp8_parts.cuh"
+
+namespace attn {
+namespace tree {
+
+template <int DA>
+struct RowsCfg {
+  using T = Tiles<DA, 1>;
+  static constexpr int kStages = DA == 128 ? 3 : 4;
+  static constexpr int kQPiece = 128 * DA;
+  static constexpr int kOffK = 0;
+  static constexpr int kOffV = kOffK + kStages * T::kRaw;
+  static constexpr int kOffW = kOffV + kStages * T::kRaw;
+  static constexpr int kOffQ = kOffW + 2 * T::kWide;
+  static constexpr int kOffScale = kOffQ + 3 * kQPiece;          // [kRing][k, v][128] floats
+  static constexpr int kOffF = kOffScale + kRing * 2 * 128 * 4;  // [softmax warp][128] floats: vs / R
+  static constexpr int kOffMask = kOffF + 8 * 128 * 4;           // [128] 64-bit words
+  static constexpr int kOffCol = kOffMask + 128 * 8;             // [128] floats
+  static constexpr int kOffFin = kOffCol + 128 * 4;              // the second group's (m, l) per row, then R
+  static constexpr int kOffBar = kOffFin + 128 * 8 + 16;
+  static constexpr int kNBars = 4 * kStages + 10 + kRing + 3;
+  static constexpr int kOffMisc = kOffBar + (kNBars * 8 + 15) / 16 * 16;
+  static constexpr int kSmem = kOffMisc + 512 + 1024;
+  static_assert(kSmem <= 227 * 1024, "shared memory");
+  static constexpr uint32_t kTmemCols = 512;   // S: two buffers of 128 columns; u: two of d
+  static constexpr int kColU = 256;
+};
+
+__device__ __forceinline__ uint32_t low_bits(int n) { return n <= 0 ? 0u : n >= 32 ? 0xffffffffu : (1u << n) - 1; }
+
+// 32 columns of this thread's lane; the values are there after the wait.
+__device__ __forceinline__ void tld32(uint32_t taddr, float (&x)[32]) {
+  uint32_t r[32];
+  tmem_ld_32x32b_x32(taddr, r);
+  tmem_wait_ld(r);
+#pragma unroll
+  for (int i = 0; i < 32; ++i) x[i] = __uint_as_float(r[i]);
+}
+
+template <int DA>
+__global__ void __launch_bounds__(kThreads, 1) tree_rows_kernel(const __grid_constant__ Params p) {
+  using C = RowsCfg<DA>;
+  using T = Tiles<DA, 1>;
+  constexpr int N = kRowsPerUnit, KS = 128, kStages = C::kStages;
+  extern __shared__ __align__(1024) uint8_t smem_raw[];
+  // (by an offset, not through an integer: the accesses stay ones of shared memory)
+  uint8_t* smem = smem_raw + ((1024 - (smem_u32(smem_raw) & 1023)) & 1023);
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const uint32_t sbase = smem_u32(smem);
+  uint32_t bar_at = sbase + C::kOffBar;
+  auto take = [&](int n) { const uint32_t a = bar_at; bar_at += 8 * n; return a; };
+  const uint32_t b_k_full = take(kStages), b_k_empty = take(kStages), b_v_full = take(kStages), b_v_empty = take(kStages);
+  const uint32_t b_s_full = take(2), b_p_full = take(2), b_w_full = take(2), b_pv_done = take(2), b_q_full = take(1),
+                 b_q_empty = take(1), b_c_full = take(kRing), b_o_free = take(1), b_drain = take(1), b_fin = take(1);
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + C::kOffMisc);
+  volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + C::kOffMisc + 4);
+  volatile int* start_b = reinterpret_cast<volatile int*>(smem + C::kOffMisc + 8);
+  volatile long long* start_p = reinterpret_cast<volatile long long*>(smem + C::kOffMisc + 16);
+  long long* warp_sums = reinterpret_cast<long long*>(smem + C::kOffMisc + 32);   // 2 kThreads / 32
+  WaitCtl wc{p.err, abort_flag, p.timeout_ns};
+
+  if (tid == 0) {
+    *abort_flag = 0;
+    *start_b = p.B;
+    *start_p = 0;
+    for (int s = 0; s < kStages; ++s) {
+      mbar_init(b_k_full + 8 * s, 1);
+      mbar_init(b_k_empty + 8 * s, 1);
+      mbar_init(b_v_full + 8 * s, 1);
+      mbar_init(b_v_empty + 8 * s, 4);   // the four warps that widen
+    }
+    for (int s = 0; s < 2; ++s) {
+      mbar_init(b_s_full + 8 * s, 1);
+      mbar_init(b_p_full + 8 * s, 4);    // a group's softmax warps
+      mbar_init(b_w_full + 8 * s, 4);
+      mbar_init(b_pv_done + 8 * s, 1);
+    }
+    for (int s = 0; s < kRing; ++s) mbar_init(b_c_full + 8 * s, 128);
+    mbar_init(b_q_full, 8);    // the softmax warps, which convert the queries
+    mbar_init(b_q_empty, 1 + 8);   // the MMA, and the softmax warps
+    mbar_init(b_o_free, 4);
+    mbar_init(b_drain, 1);
+    mbar_init(b_fin, 4);
+    fence_mbar_init();
+  }
+  if (warp == kWarpMMA) {
+    tmem_alloc(smem_u32(tmem_slot), C::kTmemCols);
+    tmem_relinquish();
+  }
+  if (warp == kWarpK && lane == 0) {
+    tma_prefetch_desc(&p.tm_k);
+    tma_prefetch_desc(&p.tm_v);
+  }
+  const Line line = find_line<KS>(p, start_b, start_p, warp_sums);
+  const int place = line.place;
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = *tmem_slot;
+  grid_launch_dependents();
+  Walk w = enter_line<KS>(p, line, *start_b, *start_p);
+
+  if (warp == kWarpK) {
+    produce<DA, 1, N, kStages>(p, w, place, &p.tm_k, sbase + C::kOffK, b_k_full, b_k_empty, wc);
+  } else if (warp == kWarpV) {
+    produce<DA, 1, N, kStages>(p, w, place, &p.tm_v, sbase + C::kOffV, b_v_full, b_v_empty, wc);
+  } else if (warp >= kWarpWiden && warp < kWarpWiden + 4) {
+    widen_and_scales<DA, 1, N, kStages>(p, w, place, smem, C::kOffV, C::kOffW, C::kOffScale, b_v_full, b_v_empty, b_w_full,
+                                        b_pv_done, b_c_full, wc);
+  } else if (warp == kWarpMMA) {
+    // ------------------------------------------------------------------ MMA issuer
+    if (lane == 0) {
+      constexpr uint32_t kIdescS = idesc_e4m3(128, 128);
+      constexpr uint32_t kIdescO = idesc_f16_f32acc(128, DA, false, true);   // B = V read MN-major
+      const int pieces = p.fp16 ? 3 : 2;
+      const uint64_t dq0 = sdesc_rows<DA>(sbase + C::kOffQ);
+      const uint64_t dk0 = sdesc_rows<DA>(sbase + C::kOffK);
+      const uint64_t dv0 = sdesc_sw128(sbase + C::kOffW, T::kWideChunk, 1024);
+      uint32_t k_cnt = 0, pv_cnt = 0, units_done = 0;
+      bool ok = true;
+      for (bool more = next_unit<KS>(p, w, true); more && ok; more = next_unit<KS>(p, w, false)) {
+        const Unit u = unit_of<N>(p, w, place);
+        if (w.t1 <= w.t0 || u.cols <= 0) continue;
+        if (!wait(b_q_full, units_done & 1, wc, ATTN_DEVERR_WAIT_TIMEOUT_SITE(kSiteQFull))) break;
+        tc_fence_after();
+        // u += P V of the next step in line, into its group's accumulator.  Before a
+        // unit's first products, which overwrite them, the previous unit's epilogue must
+        // have read both
+        int pv_unit = 0;
+        auto do_pv = [&]() -> bool {
+          const int b = pv_cnt & 1;
+          const bool first = pv_unit++ < 2;
+          if (!wait(b_w_full + 8 * b, (pv_cnt >> 1) & 1, wc, ATTN_DEVERR_WAIT_TIMEOUT_SITE(kSiteVFull))) return false;
+          if (!wait(b_p_full + 8 * b, (pv_cnt >> 1) & 1, wc, ATTN_DEVERR_WAIT_TIMEOUT_SITE(kSitePFull))) return false;
+          ++pv_cnt;
+          if (pv_unit == 1 && units_done > 0 &&
+              !wait(b_o_free, (units_done - 1) & 1, wc, ATTN_DEVERR_WAIT_TIMEOUT_SITE(kSiteODone)))
+            return false;
+          tc_fence_after();
+#pragma unroll
+          for (int kk = 0; kk < kKeys / 16; ++kk)
+            umma_ts(tmem + C::kColU + b * DA, tmem + b * 128 + kk * 8, dv0 + ((b * T::kWide + kk * 2048) >> 4), kIdescO,
+                    (first && kk == 0) ? 0u : 1u);
+          umma_commit(b_pv_done + 8 * b);
+          return true;
+        };
+        for (int t = w.t0; t < w.t1; ++t) {
+          const int st = k_cnt % kStages, sb = k_cnt & 1;
+          if (!wait(b_k_full + 8 * st, (k_cnt / kStages) & 1, wc, ATTN_DEVERR_WAIT_TIMEOUT_SITE(kSiteKFull))) {
+            ok = false;
+            break;
+          }
+          ++k_cnt;
+          tc_fence_after();
+          // S into buffer sb, after the P.V that reads the P there (issued before, and
+          // MMAs run in the order of their issue)
+          for (int s = 0; s < pieces; ++s) {
+#pragma unroll
+            for (int kk = 0; kk < DA / 32; ++kk)
+              umma_ss_f8(tmem + sb * 128, dq0 + ((s * C::kQPiece + kk * 32) >> 4), dk0 + ((st * T::kRaw + kk * 32) >> 4),
+                         kIdescS, (s > 0 || kk > 0) ? 1u : 0u);
+          }
+          umma_commit(b_s_full + 8 * sb);
+          umma_commit(b_k_empty + 8 * st);
+          if (t > w.t0 && !do_pv()) {
+            ok = false;
+            break;
+          }
+        }
+        if (!ok) break;
+        // the unit's last step
+        if (!do_pv()) break;
+        umma_commit(b_q_empty);
+        ++units_done;
+      }
+      umma_commit(b_drain);
+      mbar_wait(b_drain, 0, wc, ATTN_DEVERR_WAIT_TIMEOUT_SITE(kSiteDrain), false);
+    }
+  } else if (warp != kWarpQ) {
+    // ------------------------------------------------------------------ softmax warps
+    const int grp = warp >= kWarpSoft2 ? 1 : 0;
+    const int sw = grp ? 4 + warp - kWarpSoft2 : warp - 2;   // softmax warp 0..7
+    const int quarter = warp & 3;                  // TMEM lane quarter this warp may address
+    const int row = quarter * 32 + lane;           // of the unit
+    const uint32_t t_lane = tmem + (static_cast<uint32_t>(quarter * 32) << 16);
+    const uint32_t t_s = t_lane + grp * 128;
+    const uint32_t t_u = t_lane + C::kColU;
+    float* factor = reinterpret_cast<float*>(smem + C::kOffF) + sw * 128;   // this warp's copy of vs / R
+    float2* fin = reinterpret_cast<float2*>(smem + C::kOffFin);
+    float* fin_r = reinterpret_cast<float*>(smem + C::kOffFin + 128 * 8);
+    uint32_t step = 0, units_done = 0;
+    bool ok = true;
+    for (bool more = next_unit<KS>(p, w, true); more && ok; more = next_unit<KS>(p, w, false)) {
+      const Unit u = unit_of<N>(p, w, place);
+      if (u.cols <= 0) continue;
+      const int cc = u.col0 + row, token = token_of(p, cc), head = u.g * p.group + cc - token * p.group;
+      const long long q_row = w.row0 + token;
+      const bool mine = row < u.cols;
+      uint16_t* out = p.o + (q_row * p.Hq + head) * DA;
+      if (w.T == 0) {
+        // a sequence without keys: O = 0, lse = -inf
+        if (grp == 0 && mine) {
+          for (int i = 0; i < DA; i += 8) *reinterpret_cast<uint4*>(out + i) = make_uint4(0, 0, 0, 0);
+          p.lse[static_cast<long long>(head) * p.total + q_row] = -INFINITY;
+        }
+        continue;
+      }
+      if (w.t1 <= w.t0) continue;
+      // the queries, by all eight warps, once the unit before is done with the last
+      if (!wait_warp(b_q_empty, (units_done & 1) ^ 1, wc, ATTN_DEVERR_WAIT_TIMEOUT_SITE(kSiteQEmpty))) break;
+      convert_queries<DA>(p, w, u, sw, 8, smem + C::kOffQ, C::kQPiece, reinterpret_cast<float*>(smem + C::kOffCol),
+                          reinterpret_cast<unsigned long long*>(smem + C::kOffMask));
+      fence_proxy_async_smem();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(b_q_full);
+      if (!wait_warp(b_q_full, units_done & 1, wc, ATTN_DEVERR_WAIT_TIMEOUT_SITE(kSiteQFull))) break;
+      const float cs = mine ? reinterpret_cast<const float*>(smem + C::kOffCol)[row] : 1.0f;
+      const unsigned long long mask = mine ? reinterpret_cast<const unsigned long long*>(smem + C::kOffMask)[row] : 0;
+      __syncwarp();
+      if (lane == 0) mbar_arrive(b_q_empty);
+      // warps without a row leave their part of P as it is: rows of their own alone
+      const bool idle = quarter * 32 >= u.cols;
+      float m = -INFINITY, l = 0.0f, R = 0.0f, inv_r = 0.0f;
+      const uint32_t step0 = step;
+      int first_t = -1;
+      for (int t = w.t0; t < w.t1; ++t) {
+        if (static_cast<int>(step & 1) != grp) {   // the other group's
+          ++step;
+          continue;
+        }
+        if (first_t < 0) first_t = t;
+        const int ring = step % kRing;
+        if (!wait_warp(b_c_full + 8 * ring, (step / kRing) & 1, wc, ATTN_DEVERR_WAIT_TIMEOUT_SITE(kSiteSFree)) ||
+            !wait_warp(b_s_full + 8 * grp, (step >> 1) & 1, wc, ATTN_DEVERR_WAIT_TIMEOUT_SITE(kSiteSFull))) {
+          ok = false;
+          break;
+        }
+        tc_fence_after();
+        if (idle) {
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(b_p_full + 8 * grp);
+          ++step;
+          continue;
+        }
+        const float* ks = reinterpret_cast<const float*>(smem + C::kOffScale) + ring * 2 * 128;
+        const int k0 = t * KS;
+        // the values' reference and factors: four keys per lane, for the warp
+        float rr = 1.0f;
+        uint32_t strange;   // bit i: the lane's key i has no number for a scale
+        {
+          const float4 v4 = reinterpret_cast<const float4*>(ks + 128)[lane];
+          float v[4] = {v4.x, v4.y, v4.z, v4.w};
+          uint32_t top = 0;
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            v[i] = k0 + 4 * lane + i < w.n ? v[i] : 0.0f;
+            top = v[i] > 0.0f ? max(top, __float_as_uint(v[i])) : top;
+          }
+          top = __reduce_max_sync(0xffffffffu, top);
+          if (top >= __float_as_uint(R) && top > 0) {
+            const uint32_t e = min((top >> 23) + 1, 253u);
+            inv_r = __uint_as_float((254u - e) << 23);
+            rr = R * inv_r;
+            R = __uint_as_float(e << 23);
+          }
+          strange = 0;
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            v[i] *= inv_r;
+            if (!(v[i] <= 4.0f)) {
+              strange |= 1u << i;
+              v[i] = 0.0f;
+            }
+          }
+          reinterpret_cast<float4*>(factor)[lane] = make_float4(v[0], v[1], v[2], v[3]);
+          __syncwarp();
+        }
+        // which keys this row sees: all, but in the tiles that hold new tokens or the end
+        const bool all = k0 + KS <= min(w.ctx, w.n);
+        uint32_t vis[4] = {0xffffffffu, 0xffffffffu, 0xffffffffu, 0xffffffffu};
+        if (!all) {
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            const int at = 32 * i + k0 - w.ctx;   // the word's first key among the new tokens
+            const uint32_t tree = at >= 64 ? 0u : at >= 0 ? static_cast<uint32_t>(mask >> at)
+                                  : at > -32 ? static_cast<uint32_t>(mask) << -at : 0u;
+            vis[i] = (low_bits(-at) | tree) & low_bits(w.n - k0 - 32 * i);
+          }
+        }
+        auto scores = [&](int c, float (&s)[32]) {
+          tld32(t_s + 32 * c, s);
+#pragma unroll
+          for (int i = 0; i < 8; ++i) {
+            const float4 k4 = reinterpret_cast<const float4*>(ks)[8 * c + i];
+            s[4 * i] *= k4.x;
+            s[4 * i + 1] *= k4.y;
+            s[4 * i + 2] *= k4.z;
+            s[4 * i + 3] *= k4.w;
+          }
+          if (!all) {
+#pragma unroll
+            for (int i = 0; i < 32; ++i)
+              if (!((vis[c] >> i) & 1)) s[i] = -INFINITY;
+          }
+        };
+        float top = -INFINITY;
+#pragma unroll
+        for (int c = 0; c < 4; ++c) {
+          float s[32], a = -INFINITY, b = -INFINITY;
+          scores(c, s);
+#pragma unroll
+          for (int i = 0; i < 32; i += 4) {
+            a = fmax3(a, s[i], s[i + 1]);
+            b = fmax3(b, s[i + 2], s[i + 3]);
+          }
+          top = fmax3(top, a, b);
+        }
+        // running max (scaled units): rescale only when it grows by more than 2^8, or past -inf at all
+        const float mt = top * cs;
+        const bool grows = mt > fmaxf(m + 8.0f, -3.0e38f);
+        if (__any_sync(0xffffffffu, grows || rr != 1.0f)) {
+          const float q = grows ? ex2_approx(m - mt) : 1.0f, f = q * rr;   // (from -inf: 0)
+          l *= q;
+          m = grows ? mt : m;
+          if (t > first_t) {
+            // (this group's last P.V has completed: its s_full came after)
+            if (!wait_pv(b_pv_done, step - 2, wc)) { ok = false; break; }
+            tc_fence_after();
+#pragma unroll 1
+            for (int c = 0; c < DA; c += 32) {
+              uint32_t o[32];
+              tmem_ld_32x32b_x32(t_u + grp * DA + c, o);
+              tmem_wait_ld(o);
+#pragma unroll
+              for (int i = 0; i < 32; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * f);
+              tmem_st_32x32b_x32(t_u + grp * DA + c, o);
+            }
+          }
+        }
+        const float mh = fmaxf(m, -3.0e38f) - kPLift;   // (finite)
+        float l4[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll
+        for (int c = 0; c < 4; ++c) {
+          float s[32];
+          scores(c, s);
+          uint32_t pk[16];
+#pragma unroll
+          for (int i = 0; i < 8; ++i) {
+            const float4 f4 = reinterpret_cast<const float4*>(factor)[8 * c + i];
+            const float e0 = ex2_approx(fmaf(s[4 * i], cs, -mh)), e1 = ex2_approx(fmaf(s[4 * i + 1], cs, -mh));
+            const float e2 = ex2_approx(fmaf(s[4 * i + 2], cs, -mh)), e3 = ex2_approx(fmaf(s[4 * i + 3], cs, -mh));
+            l4[0] += e0;
+            l4[1] += e1;
+            l4[2] += e2;
+            l4[3] += e3;
+            pk[2 * i] = pack2<false>(e0 * f4.x, e1 * f4.y);
+            pk[2 * i + 1] = pack2<false>(e2 * f4.z, e3 * f4.w);
+          }
+          tmem_st_32x32b_x16(t_s + 16 * c, pk);   // P over the part of S that has been read
+        }
+        l += (l4[0] + l4[1]) + (l4[2] + l4[3]);
+        if (__any_sync(0xffffffffu, strange != 0)) {
+          // a value's scale that is no number reaches the rows that see its key
+          uint32_t hit = 0;
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+#pragma unroll 1
+            for (int j = 0; j < 32; ++j)
+              hit |= __shfl_sync(0xffffffffu, strange, 8 * i + (j >> 2)) >> (j & 3) & vis[i] >> j & 1u;
+          }
+          uint32_t one[1];
+          tmem_wait_st();
+          asm volatile("tcgen05.ld.sync.aligned.32x32b.x1.b32 {%0}, [%1];\n\ttcgen05.wait::ld.sync.aligned;"
+                       : "=r"(one[0]) : "r"(t_s) : "memory");
+          if (hit) one[0] = 0x7fff7fffu;
+          asm volatile("tcgen05.st.sync.aligned.32x32b.x1.b32 [%0], {%1};" :: "r"(t_s), "r"(one[0]) : "memory");
+        }
+        tmem_wait_st();
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(b_p_full + 8 * grp);
+        ++step;
+      }
+      if (!ok) break;
+      if (grp == 1) {
+        // hands its maxima and sums over (of no step: -inf and 0), once the first group
+        // has read those of the unit before
+        if (units_done > 0 &&
+            !wait_warp(b_o_free, (units_done - 1) & 1, wc, ATTN_DEVERR_WAIT_TIMEOUT_SITE(kSiteODone)))
+          break;
+        fin[row] = make_float2(m, l);
+        if (sw == 4 && lane == 0) *fin_r = R;   // (the same in every warp that has rows, and the first has)
+        __syncwarp();
+        if (lane == 0) mbar_arrive(b_fin);
+        ++units_done;
+        continue;
+      }
+      if (!wait_pv(b_pv_done, step - 1, wc)) break;
+      if (step - step0 >= 2 && !wait_pv(b_pv_done, step - 2, wc)) break;
+      if (!wait_warp(b_fin, units_done & 1, wc, ATTN_DEVERR_WAIT_TIMEOUT_SITE(kSiteMerge))) break;
+      tc_fence_after();
+      if (!idle) {
+        const float2 other = fin[row];
+        float w0 = l != 0.0f ? R : 0.0f, w1 = 0.0f;
+        if (other.y != 0.0f) {
+          const float mx = l != 0.0f ? fmaxf(m, other.x) : other.x;
+          const float a = l != 0.0f ? ex2_approx(m - mx) : 0.0f, b = ex2_approx(other.x - mx);
+          w0 *= a;
+          w1 = b * *fin_r;
+          l = (l != 0.0f ? l * a : 0.0f) + other.y * b;
+          m = mx;
+        }
+        const float inv = l != 0.0f ? 1.0f / l : 0.0f;   // 0: saw no key; a NaN stays one
+        w0 *= inv;
+        w1 *= inv;
+        const bool whole = w.t0 == 0 && w.t1 == w.T;
+        const int slot = 2 * blockIdx.x + (w.t0 == 0 ? 1 : 0);
+        float* part = p.part_o + (static_cast<size_t>(slot) * N + row) * DA;
+#pragma unroll 1
+        for (int c = 0; c < DA; c += 16) {
+          float a[16], b[16];
+          tld_start<16>(t_u + c, a);
+          tld_start<16>(t_u + DA + c, b);
+          tld_wait<16>(a, b);
+#pragma unroll
+          for (int i = 0; i < 16; ++i) a[i] = (w0 != 0.0f ? a[i] * w0 : 0.0f) + (w1 != 0.0f ? b[i] * w1 : 0.0f);
+          if (mine && whole) {
+            uint32_t v[8];
+#pragma unroll
+            for (int i = 0; i < 8; ++i)
+              v[i] = p.fp16 ? pack2<false>(a[2 * i], a[2 * i + 1]) : pack2<true>(a[2 * i], a[2 * i + 1]);
+            reinterpret_cast<uint4*>(out + c)[0] = make_uint4(v[0], v[1], v[2], v[3]);
+            reinterpret_cast<uint4*>(out + c)[1] = make_uint4(v[4], v[5], v[6], v[7]);
+          } else if (mine) {
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+              reinterpret_cast<float4*>(part + c)[i] = make_float4(a[4 * i], a[4 * i + 1], a[4 * i + 2], a[4 * i + 3]);
+          }
+        }
+        if (mine) {
+          l *= kPDrop;
+          if (whole)
+            p.lse[static_cast<long long>(head) * p.total + q_row] =
+                (l != 0.0f) ? m * 0.69314718055994531f + __logf(l) : -INFINITY;
+          else
+            p.part_ml[slot * N + row] = make_float2(m, l);
+        }
+        // the unit's pieces lie on the ranges p / range ... (p + T - 1) / range
+        if (!whole && w.t0 == 0 && row == 0)
+          p.rec[blockIdx.x] = make_int4(w.b, w.hc * p.abreast + place,
+                                        static_cast<int>((w.p + w.T - 1) / line.range) - line.range_id + 1, u.cols);
+      }
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(b_o_free);   // u may be overwritten by the next unit
+      ++units_done;
+    }
+  }
+  tc_fence_before();
+  __syncthreads();
+  if (warp == kWarpMMA) {
+    __syncwarp();
+    tc_fence_after();
+    tmem_dealloc(tmem, C::kTmemCols);
+  }
+}
+
+template <int DA>
+cudaError_t launch_rows(const Params& p, int cols, int grid, cudaStream_t stream) {
+  static bool done[64] = {};   // per instantiation
+  return launch_with_merge<kRowsPerUnit, DA>(tree_rows_kernel<DA>, RowsCfg<DA>::kSmem, done, p, cols, grid, stream);
+}
+
+}  // namespace tree
+}  // namespace attn
