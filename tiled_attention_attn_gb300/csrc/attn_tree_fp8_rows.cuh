@@ -6,9 +6,11 @@
 // sum.  (With the columns on N, as in attn_tree_fp8_kernel.cuh, their maxima over the
 // keys are exchanges between threads: 64 tokens of 4 heads over 16,384 keys took 579 us.)
 //
-// Two groups of four softmax warps take the steps of 128 keys in turns, each with
-// maxima, sums and an accumulator of its own, joined at the unit's end.  P overwrites
-// the S that it comes from.  The rest is as in attn_tree_fp8_kernel.cuh: V widened to
+// Two groups of four softmax warps take 64 of a step's 128 keys each, with maxima, sums
+// and an accumulator of their own, joined at the unit's end, while S of the next step and
+// P V of the last run.  P overwrites the S that it comes from.  (Taking whole steps in
+// turns, a group waited for the P V and the S that have to follow its P: 220 us for the
+// 64 tokens.)  The rest is as in attn_tree_fp8_kernel.cuh: V widened to
 // fp16 by four warps, weights in fp16 times their value's scale over R, R a power of
 // two above the scales so far.
 #pragma once
@@ -27,8 +29,8 @@ struct RowsCfg {
   static constexpr int kOffW = kOffV + kStages * T::kRaw;
   static constexpr int kOffQ = kOffW + 2 * T::kWide;
   static constexpr int kOffScale = kOffQ + 3 * kQPiece;          // [kRing][k, v][128] floats
-  static constexpr int kOffF = kOffScale + kRing * 2 * 128 * 4;  // [softmax warp][128] floats: vs / R
-  static constexpr int kOffMask = kOffF + 8 * 128 * 4;           // [128] 64-bit words
+  static constexpr int kOffF = kOffScale + kRing * 2 * 128 * 4;  // [softmax warp][64] floats: vs / R
+  static constexpr int kOffMask = kOffF + 8 * 64 * 4;           // [128] 64-bit words
   static constexpr int kOffCol = kOffMask + 128 * 8;             // [128] floats
   static constexpr int kOffFin = kOffCol + 128 * 4;              // the second group's (m, l) per row, then R
   static constexpr int kOffBar = kOffFin + 128 * 8 + 16;
@@ -41,15 +43,6 @@ struct RowsCfg {
 };
 
 __device__ __forceinline__ uint32_t low_bits(int n) { return n <= 0 ? 0u : n >= 32 ? 0xffffffffu : (1u << n) - 1; }
-
-// 32 columns of this thread's lane; the values are there after the wait.
-__device__ __forceinline__ void tld32(uint32_t taddr, float (&x)[32]) {
-  uint32_t r[32];
-  tmem_ld_32x32b_x32(taddr, r);
-  tmem_wait_ld(r);
-#pragma unroll
-  for (int i = 0; i < 32; ++i) x[i] = __uint_as_float(r[i]);
-}
 
 template <int DA>
 __global__ void __launch_bounds__(kThreads, 1) tree_rows_kernel(const __grid_constant__ Params p) {
@@ -85,7 +78,7 @@ __global__ void __launch_bounds__(kThreads, 1) tree_rows_kernel(const __grid_con
     }
     for (int s = 0; s < 2; ++s) {
       mbar_init(b_s_full + 8 * s, 1);
-      mbar_init(b_p_full + 8 * s, 4);    // a group's softmax warps
+      mbar_init(b_p_full + 8 * s, 8);    // the softmax warps
       mbar_init(b_w_full + 8 * s, 4);
       mbar_init(b_pv_done + 8 * s, 1);
     }
@@ -137,24 +130,24 @@ __global__ void __launch_bounds__(kThreads, 1) tree_rows_kernel(const __grid_con
         if (w.t1 <= w.t0 || u.cols <= 0) continue;
         if (!wait(b_q_full, units_done & 1, wc, ATTN_DEVERR_WAIT_TIMEOUT_SITE(kSiteQFull))) break;
         tc_fence_after();
-        // u += P V of the next step in line, into its group's accumulator.  Before a
-        // unit's first products, which overwrite them, the previous unit's epilogue must
-        // have read both
-        int pv_unit = 0;
+        // u += P V of the next step in line, each group's keys into its accumulator.
+        // Before a unit's first products, which overwrite them, the previous unit's
+        // epilogue must have read both
+        bool first = true;
         auto do_pv = [&]() -> bool {
           const int b = pv_cnt & 1;
-          const bool first = pv_unit++ < 2;
           if (!wait(b_w_full + 8 * b, (pv_cnt >> 1) & 1, wc, ATTN_DEVERR_WAIT_TIMEOUT_SITE(kSiteVFull))) return false;
           if (!wait(b_p_full + 8 * b, (pv_cnt >> 1) & 1, wc, ATTN_DEVERR_WAIT_TIMEOUT_SITE(kSitePFull))) return false;
           ++pv_cnt;
-          if (pv_unit == 1 && units_done > 0 &&
+          if (first && units_done > 0 &&
               !wait(b_o_free, (units_done - 1) & 1, wc, ATTN_DEVERR_WAIT_TIMEOUT_SITE(kSiteODone)))
             return false;
           tc_fence_after();
 #pragma unroll
           for (int kk = 0; kk < kKeys / 16; ++kk)
-            umma_ts(tmem + C::kColU + b * DA, tmem + b * 128 + kk * 8, dv0 + ((b * T::kWide + kk * 2048) >> 4), kIdescO,
-                    (first && kk == 0) ? 0u : 1u);
+            umma_ts(tmem + C::kColU + (kk >> 2) * DA, tmem + b * 128 + (kk >> 2) * 64 + (kk & 3) * 8,
+                    dv0 + ((b * T::kWide + kk * 2048) >> 4), kIdescO, (first && (kk & 3) == 0) ? 0u : 1u);
+          first = false;
           umma_commit(b_pv_done + 8 * b);
           return true;
         };
@@ -197,9 +190,8 @@ __global__ void __launch_bounds__(kThreads, 1) tree_rows_kernel(const __grid_con
     const int quarter = warp & 3;                  // TMEM lane quarter this warp may address
     const int row = quarter * 32 + lane;           // of the unit
     const uint32_t t_lane = tmem + (static_cast<uint32_t>(quarter * 32) << 16);
-    const uint32_t t_s = t_lane + grp * 128;
     const uint32_t t_u = t_lane + C::kColU;
-    float* factor = reinterpret_cast<float*>(smem + C::kOffF) + sw * 128;   // this warp's copy of vs / R
+    float* factor = reinterpret_cast<float*>(smem + C::kOffF) + sw * 64;   // this warp's copy of vs / R
     float2* fin = reinterpret_cast<float2*>(smem + C::kOffFin);
     float* fin_r = reinterpret_cast<float*>(smem + C::kOffFin + 128 * 8);
     uint32_t step = 0, units_done = 0;
@@ -235,17 +227,10 @@ __global__ void __launch_bounds__(kThreads, 1) tree_rows_kernel(const __grid_con
       // warps without a row leave their part of P as it is: rows of their own alone
       const bool idle = quarter * 32 >= u.cols;
       float m = -INFINITY, l = 0.0f, R = 0.0f, inv_r = 0.0f;
-      const uint32_t step0 = step;
-      int first_t = -1;
       for (int t = w.t0; t < w.t1; ++t) {
-        if (static_cast<int>(step & 1) != grp) {   // the other group's
-          ++step;
-          continue;
-        }
-        if (first_t < 0) first_t = t;
-        const int ring = step % kRing;
+        const int sb = step & 1, ring = step % kRing;
         if (!wait_warp(b_c_full + 8 * ring, (step / kRing) & 1, wc, ATTN_DEVERR_WAIT_TIMEOUT_SITE(kSiteSFree)) ||
-            !wait_warp(b_s_full + 8 * grp, (step >> 1) & 1, wc, ATTN_DEVERR_WAIT_TIMEOUT_SITE(kSiteSFull))) {
+            !wait_warp(b_s_full + 8 * sb, (step >> 1) & 1, wc, ATTN_DEVERR_WAIT_TIMEOUT_SITE(kSiteSFull))) {
           ok = false;
           break;
         }
@@ -253,22 +238,23 @@ __global__ void __launch_bounds__(kThreads, 1) tree_rows_kernel(const __grid_con
         if (idle) {
           tc_fence_before();
           __syncwarp();
-          if (lane == 0) mbar_arrive(b_p_full + 8 * grp);
+          if (lane == 0) mbar_arrive(b_p_full + 8 * sb);
           ++step;
           continue;
         }
-        const float* ks = reinterpret_cast<const float*>(smem + C::kOffScale) + ring * 2 * 128;
-        const int k0 = t * KS;
-        // the values' reference and factors: four keys per lane, for the warp
+        const uint32_t t_s = t_lane + sb * 128 + grp * 64;   // this group's keys
+        const float* ks = reinterpret_cast<const float*>(smem + C::kOffScale) + ring * 2 * 128 + grp * 64;
+        const int k0 = t * KS + grp * 64;
+        // the values' reference and factors: two keys per lane, for the warp
         float rr = 1.0f;
-        uint32_t strange;   // bit i: the lane's key i has no number for a scale
+        uint32_t strange = 0;   // bit i: the lane's key i has no number for a scale
         {
-          const float4 v4 = reinterpret_cast<const float4*>(ks + 128)[lane];
-          float v[4] = {v4.x, v4.y, v4.z, v4.w};
+          const float2 v2 = reinterpret_cast<const float2*>(ks + 128)[lane];
+          float v[2] = {v2.x, v2.y};
           uint32_t top = 0;
 #pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            v[i] = k0 + 4 * lane + i < w.n ? v[i] : 0.0f;
+          for (int i = 0; i < 2; ++i) {
+            v[i] = k0 + 2 * lane + i < w.n ? v[i] : 0.0f;
             top = v[i] > 0.0f ? max(top, __float_as_uint(v[i])) : top;
           }
           top = __reduce_max_sync(0xffffffffu, top);
@@ -278,56 +264,62 @@ __global__ void __launch_bounds__(kThreads, 1) tree_rows_kernel(const __grid_con
             rr = R * inv_r;
             R = __uint_as_float(e << 23);
           }
-          strange = 0;
 #pragma unroll
-          for (int i = 0; i < 4; ++i) {
+          for (int i = 0; i < 2; ++i) {
             v[i] *= inv_r;
             if (!(v[i] <= 4.0f)) {
               strange |= 1u << i;
               v[i] = 0.0f;
             }
           }
-          reinterpret_cast<float4*>(factor)[lane] = make_float4(v[0], v[1], v[2], v[3]);
+          reinterpret_cast<float2*>(factor)[lane] = make_float2(v[0], v[1]);
           __syncwarp();
         }
         // which keys this row sees: all, but in the tiles that hold new tokens or the end
-        const bool all = k0 + KS <= min(w.ctx, w.n);
-        uint32_t vis[4] = {0xffffffffu, 0xffffffffu, 0xffffffffu, 0xffffffffu};
+        const bool all = k0 + 64 <= min(w.ctx, w.n);
+        uint32_t vis[2] = {0xffffffffu, 0xffffffffu};
         if (!all) {
 #pragma unroll
-          for (int i = 0; i < 4; ++i) {
+          for (int i = 0; i < 2; ++i) {
             const int at = 32 * i + k0 - w.ctx;   // the word's first key among the new tokens
             const uint32_t tree = at >= 64 ? 0u : at >= 0 ? static_cast<uint32_t>(mask >> at)
                                   : at > -32 ? static_cast<uint32_t>(mask) << -at : 0u;
             vis[i] = (low_bits(-at) | tree) & low_bits(w.n - k0 - 32 * i);
           }
         }
-        auto scores = [&](int c, float (&s)[32]) {
-          tld32(t_s + 32 * c, s);
+        // S of 16 keys at a time, the next 16 on their way from tensor memory; scaled(c,
+        // s): times the keys' scales, -inf where this row does not see the key
+        auto scaled = [&](int c, float (&s)[16]) {
 #pragma unroll
-          for (int i = 0; i < 8; ++i) {
-            const float4 k4 = reinterpret_cast<const float4*>(ks)[8 * c + i];
-            s[4 * i] *= k4.x;
-            s[4 * i + 1] *= k4.y;
-            s[4 * i + 2] *= k4.z;
-            s[4 * i + 3] *= k4.w;
+          for (int i = 0; i < 4; ++i) {
+            const float4 k4 = reinterpret_cast<const float4*>(ks)[4 * c + i];
+            const float2 x = fmul2(make_float2(s[4 * i], s[4 * i + 1]), make_float2(k4.x, k4.y));
+            const float2 y = fmul2(make_float2(s[4 * i + 2], s[4 * i + 3]), make_float2(k4.z, k4.w));
+            s[4 * i] = x.x, s[4 * i + 1] = x.y, s[4 * i + 2] = y.x, s[4 * i + 3] = y.y;
           }
           if (!all) {
 #pragma unroll
-            for (int i = 0; i < 32; ++i)
-              if (!((vis[c] >> i) & 1)) s[i] = -INFINITY;
+            for (int i = 0; i < 16; ++i)
+              if (!((vis[c >> 1] >> (16 * (c & 1) + i)) & 1)) s[i] = -INFINITY;
           }
         };
+        float buf[2][16];
+        tld_start<16>(t_s, buf[0]);
         float top = -INFINITY;
 #pragma unroll
         for (int c = 0; c < 4; ++c) {
-          float s[32], a = -INFINITY, b = -INFINITY;
-          scores(c, s);
+          float (&s)[16] = buf[c & 1];
+          asm volatile("tcgen05.wait::ld.sync.aligned;");
+          tie<16>(s);
+          tld_start<16>(t_s + 16 * ((c + 1) & 3), buf[(c + 1) & 1]);   // (the last: the first again, for the second pass)
+          scaled(c, s);
+          float a = s[0], b = s[1];
 #pragma unroll
-          for (int i = 0; i < 32; i += 4) {
+          for (int i = 2; i < 14; i += 4) {
             a = fmax3(a, s[i], s[i + 1]);
             b = fmax3(b, s[i + 2], s[i + 3]);
           }
+          a = fmax3(a, s[14], s[15]);
           top = fmax3(top, a, b);
         }
         // running max (scaled units): rescale only when it grows by more than 2^8, or past -inf at all
@@ -337,9 +329,8 @@ __global__ void __launch_bounds__(kThreads, 1) tree_rows_kernel(const __grid_con
           const float q = grows ? ex2_approx(m - mt) : 1.0f, f = q * rr;   // (from -inf: 0)
           l *= q;
           m = grows ? mt : m;
-          if (t > first_t) {
-            // (this group's last P.V has completed: its s_full came after)
-            if (!wait_pv(b_pv_done, step - 2, wc)) { ok = false; break; }
+          if (t > w.t0) {
+            if (!wait_pv(b_pv_done, step - 1, wc)) { ok = false; break; }
             tc_fence_after();
 #pragma unroll 1
             for (int c = 0; c < DA; c += 32) {
@@ -353,35 +344,44 @@ __global__ void __launch_bounds__(kThreads, 1) tree_rows_kernel(const __grid_con
           }
         }
         const float mh = fmaxf(m, -3.0e38f) - kPLift;   // (finite)
-        float l4[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+        const float2 cs2 = make_float2(cs, cs), mh2 = make_float2(-mh, -mh);
+        float2 la = make_float2(0.0f, 0.0f), lb = la;
 #pragma unroll
         for (int c = 0; c < 4; ++c) {
-          float s[32];
-          scores(c, s);
-          uint32_t pk[16];
+          float (&s)[16] = buf[c & 1];
+          asm volatile("tcgen05.wait::ld.sync.aligned;");
+          tie<16>(s);
+          if (c < 3) tld_start<16>(t_s + 16 * (c + 1), buf[(c + 1) & 1]);
+          scaled(c, s);
+          uint32_t pk[8];
 #pragma unroll
-          for (int i = 0; i < 8; ++i) {
-            const float4 f4 = reinterpret_cast<const float4*>(factor)[8 * c + i];
-            const float e0 = ex2_approx(fmaf(s[4 * i], cs, -mh)), e1 = ex2_approx(fmaf(s[4 * i + 1], cs, -mh));
-            const float e2 = ex2_approx(fmaf(s[4 * i + 2], cs, -mh)), e3 = ex2_approx(fmaf(s[4 * i + 3], cs, -mh));
-            l4[0] += e0;
-            l4[1] += e1;
-            l4[2] += e2;
-            l4[3] += e3;
-            pk[2 * i] = pack2<false>(e0 * f4.x, e1 * f4.y);
-            pk[2 * i + 1] = pack2<false>(e2 * f4.z, e3 * f4.w);
+          for (int i = 0; i < 4; ++i) {
+            const float4 f4 = reinterpret_cast<const float4*>(factor)[4 * c + i];
+            float2 x = ffma2(make_float2(s[4 * i], s[4 * i + 1]), cs2, mh2);
+            float2 y = ffma2(make_float2(s[4 * i + 2], s[4 * i + 3]), cs2, mh2);
+            x = make_float2(ex2_approx(x.x), ex2_approx(x.y));
+            y = make_float2(ex2_approx(y.x), ex2_approx(y.y));
+            la = fadd2(la, x);
+            lb = fadd2(lb, y);
+            x = fmul2(x, make_float2(f4.x, f4.y));
+            y = fmul2(y, make_float2(f4.z, f4.w));
+            pk[2 * i] = pack2<false>(x.x, x.y);
+            pk[2 * i + 1] = pack2<false>(y.x, y.y);
           }
-          tmem_st_32x32b_x16(t_s + 16 * c, pk);   // P over the part of S that has been read
+          // P over the part of S that has been read (this chunk's 16 columns take 8, so
+          // the chunk on its way lies behind them)
+          asm volatile("tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"r"(t_s + 8 * c),
+                       "r"(pk[0]), "r"(pk[1]), "r"(pk[2]), "r"(pk[3]), "r"(pk[4]), "r"(pk[5]), "r"(pk[6]), "r"(pk[7]));
         }
-        l += (l4[0] + l4[1]) + (l4[2] + l4[3]);
+        l += (la.x + la.y) + (lb.x + lb.y);
         if (__any_sync(0xffffffffu, strange != 0)) {
           // a value's scale that is no number reaches the rows that see its key
           uint32_t hit = 0;
 #pragma unroll
-          for (int i = 0; i < 4; ++i) {
+          for (int i = 0; i < 2; ++i) {
 #pragma unroll 1
             for (int j = 0; j < 32; ++j)
-              hit |= __shfl_sync(0xffffffffu, strange, 8 * i + (j >> 2)) >> (j & 3) & vis[i] >> j & 1u;
+              hit |= __shfl_sync(0xffffffffu, strange, 16 * i + (j >> 1)) >> (j & 1) & vis[i] >> j & 1u;
           }
           uint32_t one[1];
           tmem_wait_st();
@@ -393,13 +393,13 @@ __global__ void __launch_bounds__(kThreads, 1) tree_rows_kernel(const __grid_con
         tmem_wait_st();
         tc_fence_before();
         __syncwarp();
-        if (lane == 0) mbar_arrive(b_p_full + 8 * grp);
+        if (lane == 0) mbar_arrive(b_p_full + 8 * sb);
         ++step;
       }
       if (!ok) break;
       if (grp == 1) {
-        // hands its maxima and sums over (of no step: -inf and 0), once the first group
-        // has read those of the unit before
+        // hands its maxima and sums over, once the first group has read those of the unit
+        // before
         if (units_done > 0 &&
             !wait_warp(b_o_free, (units_done - 1) & 1, wc, ATTN_DEVERR_WAIT_TIMEOUT_SITE(kSiteODone)))
           break;
@@ -411,7 +411,6 @@ __global__ void __launch_bounds__(kThreads, 1) tree_rows_kernel(const __grid_con
         continue;
       }
       if (!wait_pv(b_pv_done, step - 1, wc)) break;
-      if (step - step0 >= 2 && !wait_pv(b_pv_done, step - 2, wc)) break;
       if (!wait_warp(b_fin, units_done & 1, wc, ATTN_DEVERR_WAIT_TIMEOUT_SITE(kSiteMerge))) break;
       tc_fence_after();
       if (!idle) {
