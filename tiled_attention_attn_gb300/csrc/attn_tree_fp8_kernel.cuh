@@ -161,8 +161,11 @@ __global__ void __launch_bounds__(kThreads, 1) tree_kernel(const __grid_constant
   tc_fence_after();
   const uint32_t tmem = *tmem_slot;
   grid_launch_dependents();
+  const bool softmax = warp >= kWarpSoft2 || (warp >= kWarpSoft1 && warp < kWarpWiden);   // (by warpgroup)
   Walk w = enter_line<KS>(p, line, *start_b, *start_p);
 
+  if (!softmax) {
+  regs_dec<kRegsFew>();
   if (warp == kWarpK) {
     produce<DA, kTPS, N, kStages>(p, w, place, &p.tm_k, sbase + C::kOffK, b_k_full, b_k_empty, wc);
   } else if (warp == kWarpV) {
@@ -183,7 +186,7 @@ __global__ void __launch_bounds__(kThreads, 1) tree_kernel(const __grid_constant
       unsigned long long* mask = reinterpret_cast<unsigned long long*>(smem + C::kOffMask) + slot * N;
       if (!wait_warp(b_q_empty + 8 * slot, ((cnt / kSlots) & 1) ^ 1, wc,
                           ATTN_DEVERR_WAIT_TIMEOUT_SITE(kSiteQEmpty))) break;
-      convert_queries<DA>(p, w, u, 0, 1, dst, C::kQPiece, col, mask);
+      convert_queries<DA, 1>(p, w, u, 0, 1, dst, C::kQPiece, col, mask);
       fence_proxy_async_smem();
       __syncwarp();
       if (lane == 0) mbar_arrive(b_q_full + 8 * slot);
@@ -269,14 +272,16 @@ __global__ void __launch_bounds__(kThreads, 1) tree_kernel(const __grid_constant
       umma_commit(b_drain);
       mbar_wait(b_drain, 0, wc, ATTN_DEVERR_WAIT_TIMEOUT_SITE(kSiteDrain), false);
     }
+  }
   } else {
+  regs_inc<kRegsMany>();
     auto pv_wait = [&](uint32_t i) { return wait_pv(b_pv_done, i, wc); };
     uint32_t step = 0;   // steps so far, all units
     bool ok = true;
     {
       // ---------------------------------------------------------------- softmax warps
       const int grp = warp >= kWarpSoft2 ? 1 : 0;
-      const int sw = warp - (grp ? kWarpSoft2 : 2);  // softmax warp 0..3 of its group
+      const int sw = warp - (grp ? kWarpSoft2 : kWarpSoft1);  // softmax warp 0..3 of its group
       const int quarter = warp & 3;                  // TMEM lane quarter this warp may address
       const int lrow = quarter * 32 + lane;          // TMEM lane: key of the tile (S^T), d (u^T)
       constexpr int CH = GT < 16 ? GT : 16, NC = GT / CH;   // columns at a time
@@ -663,7 +668,7 @@ __global__ void __launch_bounds__(kThreads, 1) tree_kernel(const __grid_constant
         if (lane == 0) mbar_arrive(b_o_free);   // u^T may be overwritten by the next unit
         ++units_done;
         // the unit's pieces lie on the ranges p / range ... (p + T - 1) / range
-        if (!whole && w.t0 == 0 && tid == 64)
+        if (!whole && w.t0 == 0 && tid == 32 * kWarpSoft1)
           p.rec[blockIdx.x] = make_int4(w.b, w.hc * p.abreast + place,
                                         static_cast<int>((w.p + w.T - 1) / line.range) - line.range_id + 1, u.cols);
       }

@@ -18,10 +18,14 @@
 namespace attn {
 namespace tree {
 
-// Warps: K's TMA, the MMA, four of softmax, V's TMA, the queries, four that widen V,
-// and four more of softmax.
-constexpr int kWarpK = 0, kWarpMMA = 1, kWarpV = 6, kWarpQ = 7, kWarpWiden = 8, kWarpSoft2 = 12;
+// Warps: K's TMA, the MMA, V's TMA and the queries; four of softmax; four that widen V;
+// four more of softmax.
+constexpr int kWarpK = 0, kWarpMMA = 1, kWarpV = 2, kWarpQ = 3, kWarpSoft1 = 4, kWarpWiden = 8, kWarpSoft2 = 12;
 constexpr int kThreads = 512;
+// Registers: of the launch's 4 x 128 a thread per warpgroup, the softmax warps take what
+// the others do without.
+constexpr int kRegsFew = 88, kRegsMany = 168;
+static_assert(2 * (kRegsFew + kRegsMany) <= 512, "the launch's registers");
 constexpr int kRing = 4;                // stages of scales
 constexpr float kPLift = 7.0f;          // log2 of the factor of P'
 constexpr float kPDrop = 0x1p-7f;
@@ -498,10 +502,10 @@ __device__ __forceinline__ void widen_and_scales(const Params& p, Walk w, int pl
 
 // The rows of q that are columns c0, c0 + dc, ... of the unit, as e4m3 pieces (three of
 // `piece` bytes, rows of DA bytes, swizzled), their factors (scale, log2 e and the power
-// of two, in one) and masks.  A warp takes a row at a time, the next two on their way, in
-// a short loop: it runs once per unit, so fetching its code counts.  (Rows past u.cols
+// of two, in one) and masks.  A warp takes F rows at a time, the next 2 F on their
+// way, in a loop: it runs once per unit, so fetching its code counts.  (Rows past u.cols
 // hold anything: nothing reads their results.)
-template <int DA>
+template <int DA, int F>
 __device__ __forceinline__ void convert_queries(const Params& p, const Walk& w, const Unit& u, int c0, int dc, uint8_t* dst,
                                                 int piece, float* col, unsigned long long* mask) {
   constexpr int E = DA / 32;      // features per lane
@@ -522,43 +526,62 @@ __device__ __forceinline__ void convert_queries(const Params& p, const Walk& w, 
     }
     return v;
   };
-  uint2 next = load(c0), after = load(c0 + dc);
+  uint2 next[F], after[F];
+#pragma unroll
+  for (int f = 0; f < F; ++f) next[f] = load(c0 + f * dc);
+#pragma unroll
+  for (int f = 0; f < F; ++f) after[f] = load(c0 + (F + f) * dc);
 #pragma unroll 1
-  for (int c = c0; c < u.cols; c += dc) {
-    const uint2 now = next;
-    next = after;
-    after = load(c + 2 * dc);
-    float x[4];
+  for (int c = c0; c < u.cols; c += F * dc) {
+    float x[F][4];
+    uint32_t top[F];
 #pragma unroll
-    for (int h = 0; h < 2; ++h) {
-      const uint32_t v = h == 0 ? now.x : now.y;
-      const float2 f = p.fp16 ? __half22float2(*reinterpret_cast<const __half2*>(&v))
-                              : make_float2(__uint_as_float(v << 16), __uint_as_float(v & 0xffff0000u));
-      x[2 * h] = f.x;
-      x[2 * h + 1] = f.y;
+    for (int f = 0; f < F; ++f) {
+      const uint2 now = next[f];
+      next[f] = after[f];
+      after[f] = load(c + (2 * F + f) * dc);
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        const uint32_t v = h == 0 ? now.x : now.y;
+        const float2 t = p.fp16 ? __half22float2(*reinterpret_cast<const __half2*>(&v))
+                                : make_float2(__uint_as_float(v << 16), __uint_as_float(v & 0xffff0000u));
+        x[f][2 * h] = t.x;
+        x[f][2 * h + 1] = t.y;
+      }
+      top[f] = 0;   // as bits: a NaN counts above infinity
+#pragma unroll
+      for (int e = 0; e < 4; ++e) top[f] = max(top[f], __float_as_uint(x[f][e]) & 0x7fffffffu);
     }
-    uint32_t top = 0;   // as bits: a NaN counts above infinity
 #pragma unroll
-    for (int e = 0; e < 4; ++e) top = max(top, __float_as_uint(x[e]) & 0x7fffffffu);
-    top = __reduce_max_sync(0xffffffffu, top);
-    // 2^k with max 2^k in (224, 448]: 448 = 1.75 2^8
-    int k = 135 - static_cast<int>(top >> 23) - ((top & 0x7fffffu) > 0x600000u ? 1 : 0);
-    k = min(k, 120);   // (rows below 2^-112)
-    const float up = __uint_as_float(static_cast<uint32_t>(max(127 + k, 1)) << 23);
-    const float down = __uint_as_float(static_cast<uint32_t>(min(127 - k, 254)) << 23);
-    if (lane == 0) {
-      const int row = place_of(c);
-      col[c] = fmaxf(p.scale_log2 * down, 0x1p-126f);   // (positive: -inf stays -inf)
-      mask[c] = p.mask ? static_cast<unsigned long long>(__ldg(p.mask + row)) : (2ull << (row - w.row0)) - 1;
+    for (int f = 0; f < F; ++f) top[f] = __reduce_max_sync(0xffffffffu, top[f]);
+#pragma unroll
+    for (int f = 0; f < F; ++f) {
+      // 2^k with max 2^k in (224, 448]: 448 = 1.75 2^8
+      int k = 135 - static_cast<int>(top[f] >> 23) - ((top[f] & 0x7fffffu) > 0x600000u ? 1 : 0);
+      k = min(k, 120);   // (rows below 2^-112)
+      const float up = __uint_as_float(static_cast<uint32_t>(max(127 + k, 1)) << 23);
+      const float down = __uint_as_float(static_cast<uint32_t>(min(127 - k, 254)) << 23);
+      const int at = c + f * dc;
+      if (lane == 0 && at < u.cols) {
+        const int row = place_of(at);
+        col[at] = fmaxf(p.scale_log2 * down, 0x1p-126f);   // (positive: -inf stays -inf)
+        mask[at] = p.mask ? static_cast<unsigned long long>(__ldg(p.mask + row)) : (2ull << (row - w.row0)) - 1;
+      }
+#pragma unroll
+      for (int e = 0; e < 4; ++e) x[f][e] = top[f] < 0x7f800000u ? x[f][e] * up : __uint_as_float(0x7fffffffu);
     }
-    uint8_t* at = dst + swizzled<DA>(c, E * lane);
-#pragma unroll
-    for (int e = 0; e < 4; ++e) x[e] = top < 0x7f800000u ? x[e] * up : __uint_as_float(0x7fffffffu);
+    uint8_t* to = dst;
 #pragma unroll 1
-    for (int s = 0; s < 3; ++s, at += piece) {
-      const uint32_t a = take2(x[0], x[1]);
-      if constexpr (E == 4) *reinterpret_cast<uint32_t*>(at) = a | take2(x[2], x[3]) << 16;
-      else *reinterpret_cast<uint16_t*>(at) = static_cast<uint16_t>(a);
+    for (int s = 0; s < 3; ++s, to += piece) {
+#pragma unroll
+      for (int f = 0; f < F; ++f) {
+        const int at = c + f * dc;
+        const uint32_t a = take2(x[f][0], x[f][1]);
+        uint8_t* y = to + swizzled<DA>(at, E * lane);
+        if (F > 1 && at >= u.cols) continue;
+        if constexpr (E == 4) *reinterpret_cast<uint32_t*>(y) = a | take2(x[f][2], x[f][3]) << 16;
+        else *reinterpret_cast<uint16_t*>(y) = static_cast<uint16_t>(a);
+      }
     }
   }
 }

@@ -105,8 +105,11 @@ __global__ void __launch_bounds__(kThreads, 1) tree_rows_kernel(const __grid_con
   tc_fence_after();
   const uint32_t tmem = *tmem_slot;
   grid_launch_dependents();
+  const bool softmax = warp >= kWarpSoft2 || (warp >= kWarpSoft1 && warp < kWarpWiden);   // (by warpgroup)
   Walk w = enter_line<KS>(p, line, *start_b, *start_p);
 
+  if (!softmax) {
+  regs_dec<kRegsFew>();
   if (warp == kWarpK) {
     produce<DA, 1, N, kStages>(p, w, place, &p.tm_k, sbase + C::kOffK, b_k_full, b_k_empty, wc);
   } else if (warp == kWarpV) {
@@ -183,10 +186,12 @@ __global__ void __launch_bounds__(kThreads, 1) tree_rows_kernel(const __grid_con
       umma_commit(b_drain);
       mbar_wait(b_drain, 0, wc, ATTN_DEVERR_WAIT_TIMEOUT_SITE(kSiteDrain), false);
     }
-  } else if (warp != kWarpQ) {
+  }
+  } else {
+  regs_inc<kRegsMany>();
     // ------------------------------------------------------------------ softmax warps
     const int grp = warp >= kWarpSoft2 ? 1 : 0;
-    const int sw = grp ? 4 + warp - kWarpSoft2 : warp - 2;   // softmax warp 0..7
+    const int sw = grp ? 4 + warp - kWarpSoft2 : warp - kWarpSoft1;   // softmax warp 0..7
     const int quarter = warp & 3;                  // TMEM lane quarter this warp may address
     const int row = quarter * 32 + lane;           // of the unit
     const uint32_t t_lane = tmem + (static_cast<uint32_t>(quarter * 32) << 16);
@@ -214,7 +219,7 @@ __global__ void __launch_bounds__(kThreads, 1) tree_rows_kernel(const __grid_con
       if (w.t1 <= w.t0) continue;
       // the queries, by all eight warps, once the unit before is done with the last
       if (!wait_warp(b_q_empty, (units_done & 1) ^ 1, wc, ATTN_DEVERR_WAIT_TIMEOUT_SITE(kSiteQEmpty))) break;
-      convert_queries<DA>(p, w, u, sw, 8, smem + C::kOffQ, C::kQPiece, reinterpret_cast<float*>(smem + C::kOffCol),
+      convert_queries<DA, 4>(p, w, u, sw, 8, smem + C::kOffQ, C::kQPiece, reinterpret_cast<float*>(smem + C::kOffCol),
                           reinterpret_cast<unsigned long long*>(smem + C::kOffMask));
       fence_proxy_async_smem();
       __syncwarp();
@@ -287,40 +292,36 @@ __global__ void __launch_bounds__(kThreads, 1) tree_rows_kernel(const __grid_con
             vis[i] = (low_bits(-at) | tree) & low_bits(w.n - k0 - 32 * i);
           }
         }
-        // S of 16 keys at a time, the next 16 on their way from tensor memory; scaled(c,
-        // s): times the keys' scales, -inf where this row does not see the key
-        auto scaled = [&](int c, float (&s)[16]) {
+        // S of the 64 keys, times the keys' scales, -inf where this row does not see the key
+        float s[64];
+        {
+          uint32_t r[64];
+          tmem_ld_32x32b_x64(t_s, r);
+          tmem_wait_ld(r);
 #pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            const float4 k4 = reinterpret_cast<const float4*>(ks)[4 * c + i];
-            const float2 x = fmul2(make_float2(s[4 * i], s[4 * i + 1]), make_float2(k4.x, k4.y));
-            const float2 y = fmul2(make_float2(s[4 * i + 2], s[4 * i + 3]), make_float2(k4.z, k4.w));
+          for (int i = 0; i < 16; ++i) {
+            const float4 k4 = reinterpret_cast<const float4*>(ks)[i];
+            const float2 x = fmul2(make_float2(__uint_as_float(r[4 * i]), __uint_as_float(r[4 * i + 1])), make_float2(k4.x, k4.y));
+            const float2 y = fmul2(make_float2(__uint_as_float(r[4 * i + 2]), __uint_as_float(r[4 * i + 3])), make_float2(k4.z, k4.w));
             s[4 * i] = x.x, s[4 * i + 1] = x.y, s[4 * i + 2] = y.x, s[4 * i + 3] = y.y;
           }
-          if (!all) {
+        }
+        if (!all) {
 #pragma unroll
-            for (int i = 0; i < 16; ++i)
-              if (!((vis[c >> 1] >> (16 * (c & 1) + i)) & 1)) s[i] = -INFINITY;
+          for (int i = 0; i < 64; ++i)
+            if (!((vis[i >> 5] >> (i & 31)) & 1)) s[i] = -INFINITY;
+        }
+        float top = fmaxf(s[0], s[1]);
+        {
+          float a = fmaxf(s[2], s[3]), b = fmaxf(s[4], s[5]), c = fmaxf(s[6], s[7]);
+#pragma unroll
+          for (int i = 8; i < 64; i += 8) {
+            top = fmax3(top, s[i], s[i + 1]);
+            a = fmax3(a, s[i + 2], s[i + 3]);
+            b = fmax3(b, s[i + 4], s[i + 5]);
+            c = fmax3(c, s[i + 6], s[i + 7]);
           }
-        };
-        float buf[2][16];
-        tld_start<16>(t_s, buf[0]);
-        float top = -INFINITY;
-#pragma unroll
-        for (int c = 0; c < 4; ++c) {
-          float (&s)[16] = buf[c & 1];
-          asm volatile("tcgen05.wait::ld.sync.aligned;");
-          tie<16>(s);
-          tld_start<16>(t_s + 16 * ((c + 1) & 3), buf[(c + 1) & 1]);   // (the last: the first again, for the second pass)
-          scaled(c, s);
-          float a = s[0], b = s[1];
-#pragma unroll
-          for (int i = 2; i < 14; i += 4) {
-            a = fmax3(a, s[i], s[i + 1]);
-            b = fmax3(b, s[i + 2], s[i + 3]);
-          }
-          a = fmax3(a, s[14], s[15]);
-          top = fmax3(top, a, b);
+          top = fmaxf(fmax3(top, a, b), c);
         }
         // running max (scaled units): rescale only when it grows by more than 2^8, or past -inf at all
         const float mt = top * cs;
@@ -348,17 +349,12 @@ __global__ void __launch_bounds__(kThreads, 1) tree_rows_kernel(const __grid_con
         float2 la = make_float2(0.0f, 0.0f), lb = la;
 #pragma unroll
         for (int c = 0; c < 4; ++c) {
-          float (&s)[16] = buf[c & 1];
-          asm volatile("tcgen05.wait::ld.sync.aligned;");
-          tie<16>(s);
-          if (c < 3) tld_start<16>(t_s + 16 * (c + 1), buf[(c + 1) & 1]);
-          scaled(c, s);
           uint32_t pk[8];
 #pragma unroll
           for (int i = 0; i < 4; ++i) {
             const float4 f4 = reinterpret_cast<const float4*>(factor)[4 * c + i];
-            float2 x = ffma2(make_float2(s[4 * i], s[4 * i + 1]), cs2, mh2);
-            float2 y = ffma2(make_float2(s[4 * i + 2], s[4 * i + 3]), cs2, mh2);
+            float2 x = ffma2(make_float2(s[16 * c + 4 * i], s[16 * c + 4 * i + 1]), cs2, mh2);
+            float2 y = ffma2(make_float2(s[16 * c + 4 * i + 2], s[16 * c + 4 * i + 3]), cs2, mh2);
             x = make_float2(ex2_approx(x.x), ex2_approx(x.y));
             y = make_float2(ex2_approx(y.x), ex2_approx(y.y));
             la = fadd2(la, x);
@@ -368,8 +364,7 @@ __global__ void __launch_bounds__(kThreads, 1) tree_rows_kernel(const __grid_con
             pk[2 * i] = pack2<false>(x.x, x.y);
             pk[2 * i + 1] = pack2<false>(y.x, y.y);
           }
-          // P over the part of S that has been read (this chunk's 16 columns take 8, so
-          // the chunk on its way lies behind them)
+          // P over S, which is in registers
           asm volatile("tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"r"(t_s + 8 * c),
                        "r"(pk[0]), "r"(pk[1]), "r"(pk[2]), "r"(pk[3]), "r"(pk[4]), "r"(pk[5]), "r"(pk[6]), "r"(pk[7]));
         }
