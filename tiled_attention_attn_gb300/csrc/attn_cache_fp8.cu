@@ -8,15 +8,16 @@
 //   s = max(max |x| / 448, 2^-126),   v = e4m3(x / s), to nearest even;
 // a row with an infinity or a NaN has s = NaN and v = 0.  Keys are turned in fp32 first and
 // rounded once, to e4m3.  e4m3 being a floating type, v is off by at most 2^-4 of
-// itself, or 2^-10 s below 2^-6 s.  The quotient is the IEEE one: a product with
+// itself, or 2^-10 s below 2^-6 s.  The quotient is the rounded one: a product with
 // 1 / s is off by an ulp, which moves values that lie on a border between two
 // e4m3 values, and rows whose largest is a power of two have many of those.
 //
 // Bound by HBM: q, k and v read once; q written in 16 bits, k and v in 8 and a
-// scale per row.  A lane holds 16 features of a head as two 16-byte words that
-// contain its pairs whole, 4 or 8 lanes a head, so the row's maximum is 2 or 3
-// shuffles.  A warp takes a token (with few tokens a part of its heads), two heads
-// in flight per lane and step.
+// scale per row (reading back: the other way round).  A lane holds 16 features of a head
+// as two 16-byte words that contain its pairs whole, 4 or 8 lanes a head, so the row's
+// maximum is 2 or 3 shuffles.  A warp takes a token (with few tokens a part of its
+// heads); the next heads' loads, over the token's end, are on their way while one's are
+// worked on, the token's place is looked up behind them.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 #include <cuda_fp8.h>
@@ -41,8 +42,8 @@ struct AppendParams {
   const uint16_t* x[3];   // q (or null), k, v
   long long s_token[3];   // heads of a token are contiguous
   uint16_t* q_out;
-  int Hq;
-  int rows, parts, B;
+  int heads[3];
+  int rows, parts, B;     // warps per token
   int d, lg;              // log2 of the lanes per head
   int rot;
   float amplitude;
@@ -53,123 +54,178 @@ struct AppendParams {
   unsigned long long turns[kMaxPairs];
 };
 
-// The sequence that a packed row belongs to, its index there and the sequence's
-// rows; false outside every sequence.
-__device__ __forceinline__ bool find(const int* cu, int B, int total, int row, int& b, int& i, int& n, int* err) {
-  int lo = 0, hi = B;   // largest b with cu[b] <= row
+// x / s, inv the rounded 1 / s: the product, and one correction by its exact remainder
+// (P. Markstein, IBM J. Res. Dev. 34, 1990).
+__device__ __forceinline__ float2 quotients(float2 x, float s, float inv) {
+  const float2 i2 = make_float2(inv, inv), q = fmul2(x, i2);
+  return ffma2(ffma2(q, make_float2(-s, -s), x), i2, q);
+}
+
+// The last b < B with cu[b] <= row (0 if there is none), by the warp, 32 offsets at a
+// time.
+__device__ __forceinline__ int find(const int* cu, int B, int row, int lane) {
+  int lo = 0, hi = B;
   while (hi - lo > 1) {
-    const int mid = (lo + hi) >> 1;
-    if (__ldg(cu + mid) <= row) lo = mid; else hi = mid;
+    const int step = (hi - lo + 31) >> 5, at = lo + (lane + 1) * step;
+    const int n = __popc(__ballot_sync(0xffffffffu, at < hi && __ldg(cu + at) <= row));
+    hi = min(lo + (n + 1) * step, hi);
+    lo += n * step;
   }
-  b = lo;
-  int first;
-  n = chunk_len(cu, b, total, first, err);
-  i = row - first;
-  return i >= 0 && i < n;
+  return lo;
 }
 
 template <bool BF16, bool GPTJ>
-__global__ void __launch_bounds__(kThreads, 3) append_kernel(const __grid_constant__ AppendParams p) {
+__global__ void __launch_bounds__(kThreads, 2) append_kernel(const __grid_constant__ AppendParams p) {
   extern __shared__ float4 tables[];
-  constexpr int U = 2;   // heads in flight
+  constexpr int U = 2;   // heads per lane and step
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int lanes = 1 << p.lg, sub = lane >> p.lg, e = lane & (lanes - 1), per = 32 >> p.lg;
-  const int groups = p.rot >> 4;
+  const int groups = p.rot >> 4, half = p.rot >> 1;
   const bool turns_here = e < groups;
   const int lo = !GPTJ && turns_here ? 8 * e : 16 * e;
-  const int hi = !GPTJ && turns_here ? (p.rot >> 1) + 8 * e : lo + 8;
-  float2* cs_tab = reinterpret_cast<float2*>(tables) + warp * (p.rot >> 1);
+  const int hi = !GPTJ && turns_here ? half + 8 * e : lo + 8;
+  // the token's (A cos, A sin): of pair 8e + i at [i / 4][e] of float4s
+  float4* tab = tables + warp * (p.rot >> 2);
+  float* tab_f = reinterpret_cast<float*>(tab);
   if (blockIdx.x == 0) {
     // offsets that no row lookup meets
     int first;
     for (int b = threadIdx.x; b < p.B; b += kThreads) chunk_len(p.cu, b, p.rows, first, p.err);
   }
-  const long long tasks = static_cast<long long>(p.rows) * p.parts;
-  for (long long task = static_cast<long long>(blockIdx.x) * kWarps + warp; task < tasks;
-       task += static_cast<long long>(gridDim.x) * kWarps) {
-    const int row = static_cast<int>(task / p.parts), part = static_cast<int>(task - static_cast<long long>(row) * p.parts);
-    int b, i, n;
-    if (!find(p.cu, p.B, p.rows, row, b, i, n, p.err)) continue;
-    const int key = paged_len(p.c.t, b, p.err) - n + i;
-    if (key < 0) {
-      if (lane == 0) atomicCAS(p.err, 0, ATTN_DEVERR_BAD_SEQLENS);
-      continue;
-    }
-    const int page = paged_page(p.c.t, b, key >> p.c.t.page_log2, p.err);
-    if (page < 0) continue;
-    const int slot = key & ((1 << p.c.t.page_log2) - 1);
-    const int pos = p.positions ? __ldg(p.positions + row) : key;
-    __syncwarp();   // the table's readers of the token before
-    for (int t = lane; t < p.rot >> 1; t += 32) {
-      const float2 f = turned(p.turns[t], pos);
-      cs_tab[(((t & 7) >> 1) * groups + (t >> 3)) * 2 + (t & 1)] = make_float2(f.x * p.amplitude, f.y * p.amplitude);
-    }
-    __syncwarp();
-    float2 cs[8];
-    if (turns_here) {
+  const long long tasks = static_cast<long long>(p.rows) * p.parts, stride = static_cast<long long>(gridDim.x) * kWarps;
+  const int step = U * p.parts * per;
+  // steps j of a token: q's heads, k's, v's
+  const int steps_q = (p.heads[0] + step - 1) / step, steps_k = (p.heads[1] + step - 1) / step, steps = steps_q + 2 * steps_k;
+  struct Batch {
+    uint4 a[U], b[U];
+  };
+  auto part_of = [&](int j, int& h0) {   // which of q, k and v step j is of; its first head (of part 0)
+    const int k = j < steps_q ? 0 : j < steps_q + steps_k ? 1 : 2;
+    h0 = (k == 0 ? j : j - steps_q - (k == 2 ? steps_k : 0)) * step;
+    return k;
+  };
+  auto load = [&](int row, int part, int j, Batch& t) {
+    int h0;
+    const int k = part_of(j, h0);
+    const uint16_t* src = p.x[k] + row * p.s_token[k];
 #pragma unroll
-      for (int t = 0; t < 4; ++t) {
-        const float4 f = reinterpret_cast<const float4*>(cs_tab)[t * groups + e];
-        cs[2 * t] = make_float2(f.x, f.y);
-        cs[2 * t + 1] = make_float2(f.z, f.w);
+    for (int u = 0; u < U; ++u) {
+      const int h = h0 + (part + u * p.parts) * per + sub;
+      t.a[u] = t.b[u] = make_uint4(0, 0, 0, 0);
+      if (h < p.heads[k]) {
+        t.a[u] = *reinterpret_cast<const uint4*>(src + h * p.d + lo);
+        t.b[u] = *reinterpret_cast<const uint4*>(src + h * p.d + hi);
       }
     }
+  };
+  auto enter = [&](long long task, int& row, int& part) {
+    row = static_cast<int>(p.parts == 1 ? task : task / p.parts);
+    part = static_cast<int>(task - static_cast<long long>(row) * p.parts);
+  };
+  float2 cs[8];
+  Batch cur, next;
+  long long task = static_cast<long long>(blockIdx.x) * kWarps + warp;
+  int row = 0, part = 0;
+  if (task < tasks) {
+    enter(task, row, part);
+    load(row, part, 0, cur);
+  }
+  while (task < tasks) {
+    // the token's place
+    int page = -1, slot = 0, pos = 0;
+    {
+      const int b = find(p.cu, p.B, row, lane);
+      int m, first, len;
+      chunk_and_keys(p.c.t, p.cu, b, p.rows, m, first, len, p.err);
+      const int i = row - first;
+      if (i >= 0 && i < m) {
+        const int key = len - m + i;
+        if (key < 0) {
+          if (lane == 0) atomicCAS(p.err, 0, ATTN_DEVERR_BAD_SEQLENS);
+        } else {
+          page = paged_page(p.c.t, b, key >> p.c.t.page_log2, p.err);
+          slot = key & ((1 << p.c.t.page_log2) - 1);
+          pos = p.positions ? __ldg(p.positions + row) : key;
+        }
+      }
+    }
+    const long long task_n = task + stride;
+    int row_n = 0, part_n = 0;
+    if (task_n < tasks) enter(task_n, row_n, part_n);
+    {
+      if (p.rot && page >= 0) {
+        __syncwarp();   // the table's readers of the token before
 #pragma unroll 1
-    for (int k = 0; k < 3; ++k) {
-      const int heads = k == 0 ? p.Hq : p.c.t.hkv;
-      const uint16_t* x = p.x[k] + row * p.s_token[k];
-      uint8_t* dst = (k == 1 ? p.c.k : p.c.v) + page * p.c.s_page + slot * p.c.s_token;
-      float* scales = (k == 1 ? p.c.ks : p.c.vs) + page * p.c.c_page + slot * p.c.c_token;
-      for (int h0 = part * per; h0 < heads; h0 += U * p.parts * per) {
-        uint4 a[U], c[U];
-#pragma unroll
-        for (int u = 0; u < U; ++u) {
-          const int h = h0 + u * p.parts * per + sub;
-          a[u] = c[u] = make_uint4(0, 0, 0, 0);
-          if (h < heads) {
-            a[u] = *reinterpret_cast<const uint4*>(x + h * p.d + lo);
-            c[u] = *reinterpret_cast<const uint4*>(x + h * p.d + hi);
-          }
+        for (int t = lane; t < half; t += 32) {
+          const float2 f = turned(p.turns[t], pos);
+          const int to = ((((t & 7) >> 2) * groups + (t >> 3)) << 2) + (t & 3);
+          tab_f[to] = f.x * p.amplitude;
+          tab_f[to + half] = f.y * p.amplitude;
         }
-#pragma unroll
-        for (int u = 0; u < U; ++u) {
-          const int h = h0 + u * p.parts * per + sub;
-          float z[16];
-          widen<BF16>(a[u], c[u], z);
-          if (turns_here && k < 2) turn<GPTJ>(z, cs, 1.0f);
-          if (k == 0) {
-            if (h < heads) {
-              uint4 oa, ob;
-              narrow<BF16>(z, oa, ob);
-              uint16_t* y = p.q_out + (static_cast<long long>(row) * heads + h) * p.d;
-              *reinterpret_cast<uint4*>(y + lo) = oa;
-              *reinterpret_cast<uint4*>(y + hi) = ob;
-            }
-            continue;
-          }
-          // the row's largest magnitude, as bits: a NaN counts above infinity
-          uint32_t top = 0;
-#pragma unroll
-          for (int t = 0; t < 16; ++t) top = max(top, __float_as_uint(z[t]) & 0x7fffffffu);
-          for (int o = lanes >> 1; o > 0; o >>= 1) top = max(top, __shfl_xor_sync(0xffffffffu, top, o));
-          const bool finite = top < 0x7f800000u;
-          const float s = finite ? fmaxf(__uint_as_float(top) / kE4M3Top, kLeastScale) : __uint_as_float(0x7fffffffu);
-          uint32_t w[4];
-#pragma unroll
-          for (int t = 0; t < 4; ++t) {
-            const uint32_t l = __nv_cvt_float2_to_fp8x2(make_float2(z[4 * t] / s, z[4 * t + 1] / s), __NV_SATFINITE, __NV_E4M3);
-            const uint32_t r = __nv_cvt_float2_to_fp8x2(make_float2(z[4 * t + 2] / s, z[4 * t + 3] / s), __NV_SATFINITE, __NV_E4M3);
-            w[t] = finite ? l | r << 16 : 0;
-          }
-          if (h < heads) {
-            uint8_t* y = dst + h * p.c.s_head;
-            *reinterpret_cast<uint2*>(y + lo) = make_uint2(w[0], w[1]);
-            *reinterpret_cast<uint2*>(y + hi) = make_uint2(w[2], w[3]);
-            if (e == 0) scales[h * p.c.c_head] = s;
-          }
+        __syncwarp();
+        if (turns_here) {
+          const float4 c0 = tab[e], c1 = tab[groups + e], s0 = tab[2 * groups + e], s1 = tab[3 * groups + e];
+          cs[0] = make_float2(c0.x, c0.y), cs[1] = make_float2(c0.z, c0.w), cs[2] = make_float2(c1.x, c1.y);
+          cs[3] = make_float2(c1.z, c1.w), cs[4] = make_float2(s0.x, s0.y), cs[5] = make_float2(s0.z, s0.w);
+          cs[6] = make_float2(s1.x, s1.y), cs[7] = make_float2(s1.z, s1.w);
         }
       }
+#pragma unroll 1
+      for (int j = 0; j < steps; ++j) {
+        if (j + 1 < steps) load(row, part, j + 1, next);
+        else if (task_n < tasks) load(row_n, part_n, 0, next);
+        int h0;
+        const int k = part_of(j, h0);
+        if (page >= 0) {
+          uint8_t* dst = (k == 1 ? p.c.k : p.c.v) + page * p.c.s_page + slot * p.c.s_token;
+          float* scales = (k == 1 ? p.c.ks : p.c.vs) + page * p.c.c_page + slot * p.c.c_token;
+#pragma unroll
+          for (int u = 0; u < U; ++u) {
+            const int h = h0 + (part + u * p.parts) * per + sub;
+            const bool live = h < p.heads[k];
+            float2 z[8];
+            widen2x<BF16>(cur.a[u], cur.b[u], z);
+            if (turns_here && k < 2) turn2<GPTJ, false>(z, cs);
+            if (k == 0) {
+              if (live) {
+                uint4 oa, ob;
+                narrow2x<BF16>(z, oa, ob);
+                uint16_t* y = p.q_out + (static_cast<long long>(row) * p.heads[0] + h) * p.d;
+                *reinterpret_cast<uint4*>(y + lo) = oa;
+                *reinterpret_cast<uint4*>(y + hi) = ob;
+              }
+              continue;
+            }
+            // the row's largest magnitude, as bits: a NaN counts above infinity
+            uint32_t top = 0;
+#pragma unroll
+            for (int t = 0; t < 8; ++t)
+              top = max(top, max(__float_as_uint(z[t].x) & 0x7fffffffu, __float_as_uint(z[t].y) & 0x7fffffffu));
+            for (int o = lanes >> 1; o > 0; o >>= 1) top = max(top, __shfl_xor_sync(0xffffffffu, top, o));
+            const bool finite = top < 0x7f800000u;
+            const float s = finite ? fmaxf(__uint_as_float(top) / kE4M3Top, kLeastScale) : __uint_as_float(0x7fffffffu);
+            const float inv = 1.0f / s;
+            uint32_t w[4];
+#pragma unroll
+            for (int t = 0; t < 4; ++t) {
+              const uint32_t l = __nv_cvt_float2_to_fp8x2(quotients(z[2 * t], s, inv), __NV_SATFINITE, __NV_E4M3);
+              const uint32_t r = __nv_cvt_float2_to_fp8x2(quotients(z[2 * t + 1], s, inv), __NV_SATFINITE, __NV_E4M3);
+              w[t] = finite ? l | r << 16 : 0;
+            }
+            if (live) {
+              uint8_t* y = dst + h * p.c.s_head;
+              *reinterpret_cast<uint2*>(y + lo) = make_uint2(w[0], w[1]);
+              *reinterpret_cast<uint2*>(y + hi) = make_uint2(w[2], w[3]);
+              if (e == 0) scales[h * p.c.c_head] = s;
+            }
+          }
+        }
+        cur = next;
+      }
     }
+    task = task_n;
+    row = row_n;
+    part = part_n;
   }
 }
 
@@ -180,6 +236,7 @@ struct ReadParams {
   const int* starts;   // or null: 0
   int rows, parts, B;
   int d, lg;
+  int wide;            // k and v are 32-byte aligned
   PagedKV8 c;
   int* err;
 };
@@ -188,25 +245,37 @@ struct ReadParams {
 template <bool BF16>
 __device__ __forceinline__ void scaled(const uint4& x, float s, uint4& a, uint4& b) {
   const uint32_t u[4] = {x.x, x.y, x.z, x.w};
-  float z[16];
+  const float2 s2 = make_float2(s, s);
+  float2 z[8];
 #pragma unroll
   for (int t = 0; t < 4; ++t) {
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
       const __half2_raw h = __nv_cvt_fp8x2_to_halfraw2(static_cast<__nv_fp8x2_storage_t>(u[t] >> (16 * i)), __NV_E4M3);
-      const float2 f = __half22float2(__half2(h));
-      z[4 * t + 2 * i] = f.x * s;
-      z[4 * t + 2 * i + 1] = f.y * s;
+      z[2 * t + i] = fmul2(__half22float2(__half2(h)), s2);
     }
   }
-  narrow<BF16>(z, a, b);
+  narrow2x<BF16>(z, a, b);
+}
+// Stored as one 32-byte word where it is aligned (half a sector at a time is twice the
+// requests).
+template <bool BF16>
+__device__ __forceinline__ void store16(uint16_t* y, const uint4& x, float s, bool wide) {
+  uint4 a, b;
+  scaled<BF16>(x, s, a, b);
+  if (wide) {
+    const uint32_t v[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
+    st_global_v8(y, v);
+  } else {
+    reinterpret_cast<uint4*>(y)[0] = a;
+    reinterpret_cast<uint4*>(y)[1] = b;
+  }
 }
 
-// A warp reads a row (token), or with few rows a part of its heads: 16 values per
-// lane and load, keys and values of two steps in flight.
+// Keys and values of one head and 16 features per lane and step, the next step's on
+// their way.
 template <bool BF16>
 __global__ void __launch_bounds__(kThreads, 4) read_kernel(const __grid_constant__ ReadParams p) {
-  constexpr int U = 2;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int lanes = 1 << p.lg, sub = lane >> p.lg, e = lane & (lanes - 1), per = 32 >> p.lg, heads = p.c.t.hkv;
   if (blockIdx.x == 0) {
@@ -214,48 +283,50 @@ __global__ void __launch_bounds__(kThreads, 4) read_kernel(const __grid_constant
     for (int b = threadIdx.x; b < p.B; b += kThreads) chunk_len(p.cu, b, p.rows, first, p.err);
   }
   const long long tasks = static_cast<long long>(p.rows) * p.parts;
+  const int step = p.parts * per;
   for (long long task = static_cast<long long>(blockIdx.x) * kWarps + warp; task < tasks;
        task += static_cast<long long>(gridDim.x) * kWarps) {
-    const int row = static_cast<int>(task / p.parts), part = static_cast<int>(task - static_cast<long long>(row) * p.parts);
-    int b, i, n;
-    if (!find(p.cu, p.B, p.rows, row, b, i, n, p.err)) continue;
-    const long long at = static_cast<long long>(i) + (p.starts ? __ldg(p.starts + b) : 0);
-    if (at < 0 || at >= paged_len(p.c.t, b, p.err)) {
+    const int row = static_cast<int>(p.parts == 1 ? task : task / p.parts);
+    const int part = static_cast<int>(task - static_cast<long long>(row) * p.parts);
+    // the row's place
+    const int b = find(p.cu, p.B, row, lane);
+    int m, first, len;
+    chunk_and_keys(p.c.t, p.cu, b, p.rows, m, first, len, p.err);
+    const int i = row - first;
+    if (i < 0 || i >= m) continue;
+    const long long key = static_cast<long long>(i) + (p.starts ? __ldg(p.starts + b) : 0);
+    if (key < 0 || key >= len) {
       if (lane == 0) atomicCAS(p.err, 0, ATTN_DEVERR_BAD_SEQLENS);
       continue;
     }
-    const int key = static_cast<int>(at);
-    const int page = paged_page(p.c.t, b, key >> p.c.t.page_log2, p.err);
+    const int page = paged_page(p.c.t, b, static_cast<int>(key) >> p.c.t.page_log2, p.err);
     if (page < 0) continue;
-    const int slot = key & ((1 << p.c.t.page_log2) - 1);
-    const long long from = page * p.c.s_page + slot * p.c.s_token, scale = page * p.c.c_page + slot * p.c.c_token;
-    const long long to = static_cast<long long>(row) * heads;
-    for (int h0 = part * per; h0 < heads; h0 += U * p.parts * per) {
-      uint4 x[U][2];
-      float s[U][2];
-#pragma unroll
-      for (int u = 0; u < U; ++u) {
-        const int h = h0 + u * p.parts * per + sub;
-        if (h < heads) {
-          x[u][0] = *reinterpret_cast<const uint4*>(p.c.k + from + h * p.c.s_head + 16 * e);
-          x[u][1] = *reinterpret_cast<const uint4*>(p.c.v + from + h * p.c.s_head + 16 * e);
-          s[u][0] = p.c.ks[scale + h * p.c.c_head];
-          s[u][1] = p.c.vs[scale + h * p.c.c_head];
-        }
+    const int slot = static_cast<int>(key) & ((1 << p.c.t.page_log2) - 1);
+    const long long from = page * p.c.s_page + slot * p.c.s_token + 16 * e;
+    const long long scale = page * p.c.c_page + slot * p.c.c_token;
+    struct Item {
+      uint4 k, v;
+      float ks, vs;
+    };
+    auto load = [&](int h, Item& x) {
+      if (h < heads) {
+        x.k = *reinterpret_cast<const uint4*>(p.c.k + from + h * p.c.s_head);
+        x.v = *reinterpret_cast<const uint4*>(p.c.v + from + h * p.c.s_head);
+        x.ks = p.c.ks[scale + h * p.c.c_head];
+        x.vs = p.c.vs[scale + h * p.c.c_head];
       }
-#pragma unroll
-      for (int u = 0; u < U; ++u) {
-        const int h = h0 + u * p.parts * per + sub;
-        if (h >= heads) continue;
-#pragma unroll
-        for (int k = 0; k < 2; ++k) {
-          uint4 a, c;
-          scaled<BF16>(x[u][k], s[u][k], a, c);
-          uint4* y = reinterpret_cast<uint4*>((k == 0 ? p.k : p.v) + (to + h) * p.d + 16 * e);
-          y[0] = a;
-          y[1] = c;
-        }
+    };
+    Item cur, next;
+    int h = part * per + sub;
+    load(h, cur);
+    for (int h0 = part * per; h0 < heads; h0 += step, h += step) {
+      if (h0 + step < heads) load(h + step, next);
+      if (h < heads) {
+        const long long to = (static_cast<long long>(row) * heads + h) * p.d + 16 * e;
+        store16<BF16>(p.k + to, cur.k, cur.ks, p.wide != 0);
+        store16<BF16>(p.v + to, cur.v, cur.vs, p.wide != 0);
       }
+      cur = next;
     }
   }
 }
@@ -267,14 +338,14 @@ int device(DeviceInfo& info) {
   return info.supported ? ATTN_OK : ATTN_EUNSUPPORTED;
 }
 
-// Warps per row: one once the rows fill the GPU's warps, below that a row's heads
-// are shared by up to 8.
-int parts_of(int rows, int heads, int lg, int per_sm, int sms) {
+// Warps per row, and blocks: a warp per row once the rows fill the GPU's warps, below
+// that a row's heads are shared by up to 8.  (Runs of 8 rows per warp, their places
+// looked up at once, were slower: warps side by side then read places far apart.  Reading
+// 86,000 rows of 8 heads of 128 back 95 us against 83.)
+int shape(int rows, int heads, int lg, int per_sm, int sms, int& parts) {
   const long long slots = static_cast<long long>(per_sm) * kWarps * sms;
   const int per = 32 >> lg;
-  return static_cast<int>(std::max<long long>(1, std::min<long long>({8, slots / std::max(rows, 1), (heads + per - 1) / per})));
-}
-int grid_of(int rows, int parts, int per_sm, int sms) {
+  parts = static_cast<int>(std::max<long long>(1, std::min<long long>({8, slots / std::max(rows, 1), (heads + per - 1) / per})));
   const long long tasks = static_cast<long long>(rows) * parts;
   return static_cast<int>(std::min<long long>((tasks + kWarps - 1) / kWarps, static_cast<long long>(per_sm) * sms));
 }
@@ -324,7 +395,7 @@ int attn_cache_append_fp8(const void* q, const void* k, const void* v, void* q_o
   DeviceInfo info;
   if (int rc = device(info)) return rc;
   p.q_out = static_cast<uint16_t*>(q_out);
-  p.Hq = heads[0];
+  for (int i = 0; i < 3; ++i) p.heads[i] = heads[i];
   p.rows = total;
   p.B = B;
   p.d = d;
@@ -332,9 +403,7 @@ int attn_cache_append_fp8(const void* q, const void* k, const void* v, void* q_o
   p.cu = cu_seqlens;
   p.positions = positions_or_null;
   p.err = info.err_word;
-  constexpr int kPerSM = 3;
-  p.parts = parts_of(total, std::max(p.Hq, hkv), p.lg, kPerSM, info.sm_count);
-  const int grid = grid_of(total, p.parts, kPerSM, info.sm_count);
+  const int grid = shape(total, std::max(heads[0], hkv), p.lg, 2, info.sm_count, p.parts);
   const size_t smem = static_cast<size_t>(kWarps) * (p.rot / 2) * sizeof(float2);
   if (fp16 == 0) interleaved ? append_kernel<true, true><<<grid, kThreads, smem, stream>>>(p)
                              : append_kernel<true, false><<<grid, kThreads, smem, stream>>>(p);
@@ -362,14 +431,13 @@ int attn_cache_read_fp8(void* k, void* v, int B, int total, const attn_paged_kv8
   p.v = static_cast<uint16_t*>(v);
   p.cu = cu_seqlens;
   p.starts = starts_or_null;
+  p.wide = ptr_aligned(k, 32) && ptr_aligned(v, 32);
   p.rows = total;
   p.B = B;
   p.d = d;
   p.lg = d == 128 ? 3 : 2;
   p.err = info.err_word;
-  constexpr int kPerSM = 4;
-  p.parts = parts_of(total, hkv, p.lg, kPerSM, info.sm_count);
-  const int grid = grid_of(total, p.parts, kPerSM, info.sm_count);
+  const int grid = shape(total, hkv, p.lg, 4, info.sm_count, p.parts);
   if (fp16 == 0) read_kernel<true><<<grid, kThreads, 0, stream>>>(p);
   else read_kernel<false><<<grid, kThreads, 0, stream>>>(p);
   if (cudaGetLastError() != cudaSuccess) return ATTN_ELAUNCH;

@@ -65,21 +65,18 @@ struct Params {
 };
 
 template <bool BF16>
-__device__ __forceinline__ void load8(const void* base, bool fp32, int at, float (&w)[16], int to) {
-  if (fp32) {
-    const float4* p = reinterpret_cast<const float4*>(static_cast<const float*>(base) + at);
-    const float4 a = __ldg(p), b = __ldg(p + 1);
-    w[to] = a.x, w[to + 1] = a.y, w[to + 2] = a.z, w[to + 3] = a.w;
-    w[to + 4] = b.x, w[to + 5] = b.y, w[to + 6] = b.z, w[to + 7] = b.w;
-    return;
-  }
-  const uint4 v = __ldg(reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(base) + at));
-  const uint32_t u[4] = {v.x, v.y, v.z, v.w};
+__device__ __forceinline__ float weight(const void* w, bool fp32, int at) {
+  if (fp32) return __ldg(static_cast<const float*>(w) + at);
+  const unsigned short v = __ldg(static_cast<const unsigned short*>(w) + at);
+  return BF16 ? __bfloat162float(__ushort_as_bfloat16(v)) : __half2float(__ushort_as_half(v));
+}
+// An item's features times the weights, which lie in shared memory.
+__device__ __forceinline__ void scale_by(float2 (&x)[8], const float* w, int lo, int hi) {
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
-    const float2 f = unpack<BF16>(u[i]);
-    w[to + 2 * i] = f.x;
-    w[to + 2 * i + 1] = f.y;
+    const float4 v = *reinterpret_cast<const float4*>(w + (i < 2 ? lo + 4 * i : hi + 4 * i - 8));
+    x[2 * i] = fmul2(x[2 * i], make_float2(v.x, v.y));
+    x[2 * i + 1] = fmul2(x[2 * i + 1], make_float2(v.z, v.w));
   }
 }
 
@@ -102,142 +99,230 @@ __device__ __forceinline__ void place(const Params& p, int e, int& lo, int& hi, 
   }
 }
 
-// The token's (A cos, A sin), pair 8e + 2i, 8e + 2i + 1 as the float4 [i][e], so
-// that the lanes of a head read neighbouring words.
-__device__ __forceinline__ void fill_table(const Params& p, int row, float2* cs, int lane) {
-  const int groups = p.rot >> 4;
-  for (int i = lane; i < p.rot >> 1; i += 32) {
-    const int pos = __ldg(p.positions + static_cast<long long>(p.axis[i]) * p.rows + row);
-    const float2 t = turned(p.turns[i], pos);
-    cs[(((i & 7) >> 1) * groups + (i >> 3)) * 2 + (i & 1)] = make_float2(t.x * p.amplitude, t.y * p.amplitude);
-  }
-}
-
 template <bool BF16, bool GPTJ, bool BWD>
-__global__ void __launch_bounds__(kThreads, BWD ? 2 : 3) norm_kernel(const __grid_constant__ Params p) {
+__global__ void __launch_bounds__(kThreads, 2) norm_kernel(const __grid_constant__ Params p) {
   extern __shared__ float4 tables[];
-  constexpr int U = 2;   // heads in flight
+  // heads per lane and step; the next step's are on their way meanwhile
+  constexpr int U = BWD ? 1 : 2;
+  constexpr int P = 2;   // pairs per lane whose positions are read ahead
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int lanes = 1 << p.lg, sub = lane >> p.lg, e = lane & (lanes - 1), per = 32 >> p.lg;   // heads per warp and step
   const bool on = e < p.items;
-  float2* cs_tab = reinterpret_cast<float2*>(tables) + warp * (p.rot >> 1);
-  float* sums = reinterpret_cast<float*>(tables) + kWarps * p.rot;   // dw, [warp][2][d]
+  const int groups = p.rot >> 4, half = p.rot >> 1;
+  // the token's (A cos, A sin), and the weights: of pair 8e + i (feature lo + i, hi + i)
+  // at [i / 4][e] of float4s, so that the lanes of a head read neighbouring words
+  float4* tab = tables + warp * (p.rot >> 2);   // cos [2][groups], then sin
+  float* tab_f = reinterpret_cast<float*>(tab);
+  float* weights = reinterpret_cast<float*>(tables) + kWarps * p.rot;   // [2][d]
+  float* sums = weights + 2 * p.d;   // dw: of a thread and side, [side][4][thread] of float4s; at the end [warp][2][d]
   int lo, hi;
   bool turns_here;
   place<GPTJ>(p, on ? e : 0, lo, hi, turns_here);
+  for (int i = threadIdx.x; i < 2 * p.d; i += kThreads) {
+    const Side& s = p.side[i < p.d ? 0 : 1];
+    const int f = i < p.d ? i : i - p.d;
+    weights[i] = s.w == nullptr ? 1.0f : weight<BF16>(s.w, p.w32 != 0, f);
+  }
+  __syncthreads();
+  // Tokens: whole ones while there are enough for every warp, then parts of the rest.
+  const long long warps = static_cast<long long>(gridDim.x) * kWarps;
+  const int full = static_cast<int>(p.rows / warps * warps);
+  const long long tasks = full + static_cast<long long>(p.rows - full) * p.parts;
   float dw[16];
-  // (the backward takes the queries of all its tokens, then the keys: one set of
-  // weight sums in registers)
-#pragma unroll 1
-  for (int round = 0; round < (BWD ? 2 : 1); ++round) {
-    if constexpr (BWD) {
+  float4* mine = reinterpret_cast<float4*>(sums) + threadIdx.x;
+  if constexpr (BWD) {
 #pragma unroll
-      for (int i = 0; i < 16; ++i) dw[i] = 0.0f;
+    for (int i = 0; i < 16; ++i) dw[i] = 0.0f;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) mine[i * kThreads] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+  }
+  // the weight sums in registers are of one side, the other's wait in shared memory
+  auto put_sums = [&](int k) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) mine[(4 * k + i) * kThreads] = make_float4(dw[4 * i], dw[4 * i + 1], dw[4 * i + 2], dw[4 * i + 3]);
+  };
+  auto get_sums = [&](int k) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const float4 v = mine[(4 * k + i) * kThreads];
+      dw[4 * i] = v.x, dw[4 * i + 1] = v.y, dw[4 * i + 2] = v.z, dw[4 * i + 3] = v.w;
     }
-    const int k0 = BWD ? round : 0, k1 = BWD ? round + 1 : 2;
-    if (BWD && p.side[round].heads == 0) break;
-    const long long tasks = static_cast<long long>(p.rows) * p.parts;
-    for (long long task = static_cast<long long>(blockIdx.x) * kWarps + warp; task < tasks;
-         task += static_cast<long long>(gridDim.x) * kWarps) {
-      const int row = static_cast<int>(task / p.parts), part = static_cast<int>(task - static_cast<long long>(row) * p.parts);
-      __syncwarp();   // the table's readers of the token before
-      if (p.rot) fill_table(p, row, cs_tab, lane);
-      __syncwarp();
-      float2 cs[8];
-      if (turns_here) {
+  };
+  {
+    struct Batch {
+      uint4 xa[U], xb[U], ga[BWD ? U : 1], gb[BWD ? U : 1];
+    };
+    struct Task {
+      int row, part, parts;   // part of `parts` of a token's heads
+      int steps0, steps;      // steps of the queries' heads, and in all
+    };
+    auto enter = [&](long long task) {
+      Task t;
+      t.parts = task < full ? 1 : p.parts;
+      t.row = static_cast<int>(task);
+      t.part = 0;
+      if (t.parts > 1) {
+        const int rest = static_cast<int>(task - full);   // (below 8 warps' worth)
+        t.row = full + rest / t.parts;
+        t.part = rest % t.parts;
+      }
+      const int step = U * t.parts * per;
+      t.steps0 = (p.side[0].heads + step - 1) / step;
+      t.steps = t.steps0 + (p.side[1].heads + step - 1) / step;
+      return t;
+    };
+    auto load = [&](const Task& a, int j, Batch& t) {
+      const int k = j >= a.steps0, row = a.row;
+      const Side& s = p.side[k];
+      const uint16_t* x = s.x + row * s.s_token;
+      const int h0 = ((j - (k ? a.steps0 : 0)) * U * a.parts + a.part) * per + sub;
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          const float4 t = reinterpret_cast<const float4*>(cs_tab)[i * (p.rot >> 4) + (on ? e : 0)];
-          cs[2 * i] = make_float2(t.x, t.y);
-          cs[2 * i + 1] = make_float2(t.z, t.w);
+      for (int u = 0; u < U; ++u) {
+        const int h = h0 + u * a.parts * per;
+        t.xa[u] = t.xb[u] = make_uint4(0, 0, 0, 0);
+        if constexpr (BWD) t.ga[u] = t.gb[u] = make_uint4(0, 0, 0, 0);
+        if (h < s.heads && on) {
+          const uint16_t* src = x + h * s.s_head;
+          t.xa[u] = *reinterpret_cast<const uint4*>(src + lo);
+          t.xb[u] = *reinterpret_cast<const uint4*>(src + hi);
+          if constexpr (BWD) {
+            const uint16_t* g = s.dy + (static_cast<long long>(row) * s.heads + h) * p.d;
+            t.ga[u] = *reinterpret_cast<const uint4*>(g + lo);
+            t.gb[u] = *reinterpret_cast<const uint4*>(g + hi);
+          }
         }
       }
+    };
+    int pos[P];
+    auto position = [&](int i, int row) { return __ldg(p.positions + static_cast<long long>(p.axis[i]) * p.rows + row); };
+    auto positions = [&](int row) {
+#pragma unroll
+      for (int i = 0; i < P; ++i)
+        if (lane + 32 * i < half) pos[i] = position(lane + 32 * i, row);
+    };
+    float2 cs[8];   // cos, then sin, of pairs 2i and 2i + 1
+    Batch cur, next;
+    long long task = static_cast<long long>(blockIdx.x) * kWarps + warp;
+    Task at = {};
+    if (task < tasks) {
+      at = enter(task);
+      load(at, 0, cur);
+      if (p.rot) positions(at.row);
+    }
+    while (task < tasks) {
+      if (p.rot) {
+        __syncwarp();   // the table's readers of the token before
+        auto turn_pair = [&](int i, int position_i) {
+          const float2 t = turned(p.turns[i], position_i);
+          const int to = ((((i & 7) >> 2) * groups + (i >> 3)) << 2) + (i & 3);
+          tab_f[to] = t.x * p.amplitude;
+          tab_f[to + half] = t.y * p.amplitude;
+        };
+#pragma unroll
+        for (int i = 0; i < P; ++i)
+          if (lane + 32 * i < half) turn_pair(lane + 32 * i, pos[i]);
 #pragma unroll 1
-      for (int k = k0; k < k1; ++k) {
+        for (int i = lane + 32 * P; i < half; i += 32) turn_pair(i, position(i, at.row));
+        __syncwarp();
+        if (turns_here) {
+          const int eo = on ? e : 0;
+          const float4 c0 = tab[eo], c1 = tab[groups + eo], s0 = tab[2 * groups + eo], s1 = tab[3 * groups + eo];
+          cs[0] = make_float2(c0.x, c0.y), cs[1] = make_float2(c0.z, c0.w), cs[2] = make_float2(c1.x, c1.y);
+          cs[3] = make_float2(c1.z, c1.w), cs[4] = make_float2(s0.x, s0.y), cs[5] = make_float2(s0.z, s0.w);
+          cs[6] = make_float2(s1.x, s1.y), cs[7] = make_float2(s1.z, s1.w);
+        }
+      }
+      const long long task_n = task + warps;
+      Task then = {};
+      if (task_n < tasks) {
+        then = enter(task_n);
+        if (p.rot) positions(then.row);
+      }
+#pragma unroll 1
+      for (int j = 0; j < at.steps; ++j) {
+        if (j + 1 < at.steps) load(at, j + 1, next);
+        else if (task_n < tasks) load(then, 0, next);
+        const int k = j >= at.steps0;
+        if (BWD && (j == 0 || j == at.steps0)) {
+          if (j > 0) put_sums(0);
+          get_sums(k);
+        }
         const Side& s = p.side[k];
-        if (s.heads == 0) continue;
-        float w[16];
-        if (s.w != nullptr) {
-          load8<BF16>(s.w, p.w32 != 0, lo, w, 0);
-          load8<BF16>(s.w, p.w32 != 0, hi, w, 8);
-        } else {
+        const float* wk = weights + k * p.d;
+        const int h0 = ((j - (k ? at.steps0 : 0)) * U * at.parts + at.part) * per + sub;
+        uint16_t* out = s.out + static_cast<long long>(at.row) * s.heads * p.d;
 #pragma unroll
-          for (int i = 0; i < 16; ++i) w[i] = 1.0f;
-        }
-        const uint16_t* x = s.x + row * s.s_token;
-        const long long row_out = static_cast<long long>(row) * s.heads;
-        for (int h0 = part * per; h0 < s.heads; h0 += U * p.parts * per) {
-          uint4 xa[U], xb[U], ga[U], gb[U];
+        for (int u = 0; u < U; ++u) {
+          const int h = h0 + u * at.parts * per;
+          const bool live = h < s.heads && on;
+          float2 z[8];
+          widen2x<BF16>(cur.xa[u], cur.xb[u], z);
+          float2 sq = fmul2(z[0], z[0]);
 #pragma unroll
-          for (int u = 0; u < U; ++u) {
-            const int h = h0 + u * p.parts * per + sub;
-            xa[u] = xb[u] = make_uint4(0, 0, 0, 0);
-            if constexpr (BWD) ga[u] = gb[u] = make_uint4(0, 0, 0, 0);
-            if (h < s.heads && on) {
-              const uint16_t* src = x + h * s.s_head;
-              xa[u] = *reinterpret_cast<const uint4*>(src + lo);
-              xb[u] = *reinterpret_cast<const uint4*>(src + hi);
-              if constexpr (BWD) {
-                const uint16_t* g = s.dy + (row_out + h) * p.d;
-                ga[u] = *reinterpret_cast<const uint4*>(g + lo);
-                gb[u] = *reinterpret_cast<const uint4*>(g + hi);
+          for (int i = 1; i < 8; ++i) sq = ffma2(z[i], z[i], sq);
+          const float r = rsqrtf(fmaf(group_sum(sq.x + sq.y, lanes), p.inv_d, p.eps));
+          const float2 r2 = make_float2(r, r);
+#pragma unroll
+          for (int i = 0; i < 8; ++i) z[i] = fmul2(z[i], r2);
+          uint4 oa, ob;
+          if constexpr (!BWD) {
+            scale_by(z, wk, lo, hi);
+            if (turns_here) turn2<GPTJ, false>(z, cs);
+            narrow2x<BF16>(z, oa, ob);
+          } else {
+            float2 g[8];
+            widen2x<BF16>(cur.ga[u], cur.gb[u], g);
+            if (turns_here) turn2<GPTJ, true>(g, cs);
+            if (live) {   // (no head here: z = 0 / 0 where eps = 0)
+#pragma unroll
+              for (int i = 0; i < 8; ++i) {
+                const float2 t = ffma2(g[i], z[i], make_float2(dw[2 * i], dw[2 * i + 1]));
+                dw[2 * i] = t.x;
+                dw[2 * i + 1] = t.y;
               }
             }
+            scale_by(g, wk, lo, hi);
+            float2 dot = fmul2(g[0], z[0]);
+#pragma unroll
+            for (int i = 1; i < 8; ++i) dot = ffma2(g[i], z[i], dot);
+            const float m = group_sum(live ? dot.x + dot.y : 0.0f, lanes) * -p.inv_d;
+            const float2 m2 = make_float2(m, m);
+#pragma unroll
+            for (int i = 0; i < 8; ++i) g[i] = fmul2(r2, ffma2(z[i], m2, g[i]));
+            narrow2x<BF16>(g, oa, ob);
           }
-#pragma unroll
-          for (int u = 0; u < U; ++u) {
-            const int h = h0 + u * p.parts * per + sub;
-            const bool live = h < s.heads && on;
-            float z[16];
-            widen<BF16>(xa[u], xb[u], z);
-            float sum = 0.0f;
-#pragma unroll
-            for (int i = 0; i < 16; ++i) sum = fmaf(z[i], z[i], sum);
-            const float r = rsqrtf(fmaf(group_sum(sum, lanes), p.inv_d, p.eps));
-            uint4 oa, ob;
-            if constexpr (!BWD) {
-#pragma unroll
-              for (int i = 0; i < 16; ++i) z[i] = z[i] * r * w[i];
-              if (turns_here) turn<GPTJ>(z, cs, 1.0f);
-              narrow<BF16>(z, oa, ob);
-            } else {
-              float g[16];
-              widen<BF16>(ga[u], gb[u], g);
-              if (turns_here) turn<GPTJ>(g, cs, -1.0f);
-              float dot = 0.0f;
-#pragma unroll
-              for (int i = 0; i < 16; ++i) {
-                z[i] *= r;
-                if (live) dw[i] = fmaf(g[i], z[i], dw[i]);   // (no head here: z = 0 / 0 where eps = 0)
-                g[i] *= w[i];
-                dot = fmaf(g[i], z[i], dot);
-              }
-              const float m = group_sum(live ? dot : 0.0f, lanes) * p.inv_d;
-#pragma unroll
-              for (int i = 0; i < 16; ++i) g[i] = r * fmaf(-z[i], m, g[i]);
-              narrow<BF16>(g, oa, ob);
-            }
-            if (live) {
-              uint16_t* y = s.out + (row_out + h) * p.d;
-              *reinterpret_cast<uint4*>(y + lo) = oa;
-              *reinterpret_cast<uint4*>(y + hi) = ob;
-            }
+          if (live) {
+            uint16_t* y = out + h * p.d;
+            *reinterpret_cast<uint4*>(y + lo) = oa;
+            *reinterpret_cast<uint4*>(y + hi) = ob;
           }
         }
+        cur = next;
       }
-    }
-    if constexpr (BWD) {
-      // over the lanes that hold the same features; the warps are joined below
-#pragma unroll
-      for (int i = 0; i < 16; ++i) {
-        float v = dw[i];
-        for (int o = lanes; o < 32; o <<= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
-        if (sub == 0 && on) sums[(warp * 2 + round) * p.d + (i < 8 ? lo + i : hi + i - 8)] = v;
-      }
+      if constexpr (BWD) put_sums(at.steps > at.steps0);
+      task = task_n;
+      at = then;
     }
   }
   if constexpr (BWD) {
     if (p.partial == nullptr) return;
+    // over the lanes that hold the same features, then over the warps
+    float v[2][16];
+#pragma unroll
+    for (int k = 0; k < 2; ++k) {
+      get_sums(k);
+#pragma unroll
+      for (int i = 0; i < 16; ++i) {
+        v[k][i] = dw[i];
+        for (int o = lanes; o < 32; o <<= 1) v[k][i] += __shfl_xor_sync(0xffffffffu, v[k][i], o);
+      }
+    }
+    __syncthreads();   // (the threads' sums have been read)
+#pragma unroll
+    for (int k = 0; k < 2; ++k)
+#pragma unroll
+      for (int i = 0; i < 16; ++i)
+        if (sub == 0 && on) sums[(warp * 2 + k) * p.d + (i < 8 ? lo + i : hi + i - 8)] = v[k][i];
     __syncthreads();
     grid_launch_dependents();
     for (int i = threadIdx.x; i < 2 * p.d; i += kThreads) {
@@ -366,20 +451,29 @@ int device(DeviceInfo& info) {
   return info.supported ? ATTN_OK : ATTN_EUNSUPPORTED;
 }
 
-// Warps per token, and blocks: a warp per token once the tokens fill the GPU's
-// warps, below that a token's heads are shared by up to 8.
+// Blocks, and the parts of the tokens that are left when every warp has had as many
+// whole ones as the others (all of them, where there are fewer tokens than warps).
 int shape(Params& p, int sms, int per_sm) {
   const long long slots = static_cast<long long>(per_sm) * kWarps * sms;
   const int per = 32 >> p.lg, steps = (std::max(p.side[0].heads, p.side[1].heads) + per - 1) / per;
-  p.parts = static_cast<int>(std::max<long long>(1, std::min<long long>({8, slots / std::max(p.rows, 1), steps})));
-  const long long tasks = static_cast<long long>(p.rows) * p.parts;
-  return static_cast<int>(std::min<long long>((tasks + kWarps - 1) / kWarps, static_cast<long long>(per_sm) * sms));
+  const long long rest = std::max<long long>(p.rows % slots, 1);
+  p.parts = static_cast<int>(std::max<long long>(1, std::min<long long>({8, slots / rest, steps})));
+  if (p.rows >= slots) return per_sm * sms;
+  return static_cast<int>((static_cast<long long>(p.rows) * p.parts + kWarps - 1) / kWarps);
+}
+
+template <bool BWD>
+void smem_allowed(bool bf16, bool gptj) {
+  const auto f = bf16 ? (gptj ? norm_kernel<true, true, BWD> : norm_kernel<true, false, BWD>)
+                      : (gptj ? norm_kernel<false, true, BWD> : norm_kernel<false, false, BWD>);
+  cudaFuncSetAttribute(f, cudaFuncAttributeMaxDynamicSharedMemorySize, 64 * 1024);
 }
 
 template <bool BWD>
 void run(const Params& p, bool bf16, bool gptj, int grid, cudaStream_t stream) {
-  size_t smem = static_cast<size_t>(kWarps) * (p.rot / 2) * sizeof(float2);
-  if (BWD) smem += static_cast<size_t>(kWarps) * 2 * p.d * sizeof(float);   // (at most 48 KB)
+  size_t smem = (static_cast<size_t>(kWarps) * p.rot + 2 * p.d) * sizeof(float);
+  if (BWD) smem += std::max(static_cast<size_t>(kWarps) * 2 * p.d, static_cast<size_t>(kThreads) * 32) * sizeof(float);
+  if (smem > 48 * 1024) smem_allowed<BWD>(bf16, gptj);   // (d = 512)
   if (bf16) gptj ? norm_kernel<true, true, BWD><<<grid, kThreads, smem, stream>>>(p)
                  : norm_kernel<true, false, BWD><<<grid, kThreads, smem, stream>>>(p);
   else gptj ? norm_kernel<false, true, BWD><<<grid, kThreads, smem, stream>>>(p)
@@ -411,7 +505,7 @@ int attn_qk_norm_rotary(const void* q, const void* k, void* q_out, void* k_out, 
   for (int i = 0; i < 2; ++i) p.side[i].out = static_cast<uint16_t*>(out[i]);
   DeviceInfo info;
   if (int rc = device(info)) return rc;
-  const int grid = shape(p, info.sm_count, 3);
+  const int grid = shape(p, info.sm_count, 2);
   run<false>(p, fp16 == 0, interleaved != 0, grid, stream);
   if (cudaGetLastError() != cudaSuccess) return ATTN_ELAUNCH;
   count_launch();

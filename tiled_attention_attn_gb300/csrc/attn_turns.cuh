@@ -9,6 +9,8 @@
 #include <cmath>
 #include <cstdint>
 
+#include "ptx.cuh"
+
 namespace attn {
 
 template <bool BF16>
@@ -24,6 +26,44 @@ __device__ __forceinline__ uint32_t pack(float a, float b) {
   }
   const __half2 r = __floats2half2_rn(a, b);
   return *reinterpret_cast<const uint32_t*>(&r);
+}
+
+// The 16 features of two words as pairs of neighbours, for packed arithmetic.
+template <bool BF16>
+__device__ __forceinline__ void widen2x(const uint4& a, const uint4& b, float2 (&x)[8]) {
+  const uint32_t u[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
+#pragma unroll
+  for (int i = 0; i < 8; ++i) x[i] = unpack<BF16>(u[i]);
+}
+template <bool BF16>
+__device__ __forceinline__ void narrow2x(const float2 (&x)[8], uint4& a, uint4& b) {
+  a = make_uint4(pack<BF16>(x[0].x, x[0].y), pack<BF16>(x[1].x, x[1].y), pack<BF16>(x[2].x, x[2].y),
+                 pack<BF16>(x[3].x, x[3].y));
+  b = make_uint4(pack<BF16>(x[4].x, x[4].y), pack<BF16>(x[5].x, x[5].y), pack<BF16>(x[6].x, x[6].y),
+                 pack<BF16>(x[7].x, x[7].y));
+}
+
+// Turns the item's 8 pairs (BACK: back) by cs, the cosines of pairs 2i and 2i + 1 in
+// cs[i], the sines in cs[4 + i].  GPT-NeoX: pairs 2i and 2i + 1 are (x[i], x[4 + i]) by
+// components; GPT-J: pair i is the components of x[i].
+template <bool GPTJ, bool BACK>
+__device__ __forceinline__ void turn2(float2 (&x)[8], const float2 (&cs)[8]) {
+  if constexpr (GPTJ) {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      const float c = i & 1 ? cs[i >> 1].y : cs[i >> 1].x, t = i & 1 ? cs[4 + (i >> 1)].y : cs[4 + (i >> 1)].x;
+      const float s = BACK ? -t : t;
+      x[i] = ffma2(make_float2(x[i].y, x[i].y), make_float2(-s, c), fmul2(make_float2(x[i].x, x[i].x), make_float2(c, s)));
+    }
+  } else {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const float2 c = cs[i], s = BACK ? make_float2(-cs[4 + i].x, -cs[4 + i].y) : cs[4 + i];
+      const float2 a = x[i], b = x[4 + i];
+      x[i] = ffma2(b, make_float2(-s.x, -s.y), fmul2(a, c));
+      x[4 + i] = ffma2(a, s, fmul2(b, c));
+    }
+  }
 }
 
 // (cos, sin) of the fraction of a turn that position pos makes.
