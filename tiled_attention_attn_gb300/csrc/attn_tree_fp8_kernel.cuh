@@ -60,11 +60,9 @@ struct Cfg {
   static constexpr int kTPS = 128 / DA;            // tiles per step
   static constexpr int KS = kKeys * kTPS;          // keys per step
   static constexpr int kRows = kTPS * N;           // rows of P^T (the P.V's N)
-  static constexpr int kStages = N == 16 && DA == 128 ? 4 : (N == 64 && DA == 64 ? 2 : 3);
-  static constexpr int kQSlots = N == 64 ? 1 : 2;
-  // the queries' pieces as further columns of S^T, where tensor memory holds them
-  static constexpr bool kWideS = !(N == 64 && DA == 64);
-  static constexpr int kSCols = kWideS ? 3 * N : N;   // columns of S^T per tile
+  static constexpr int kStages = N == 16 && DA == 128 ? 4 : 3;
+  static constexpr int kQSlots = 2;
+  static constexpr int kSCols = 3 * N;   // columns of S^T per tile: the queries' pieces as further columns
   static constexpr int kQPiece = N * DA;
   static constexpr int kQ = 3 * kQPiece;
   static constexpr int kPChunk = kRows * 128;
@@ -119,30 +117,18 @@ __global__ void __launch_bounds__(kThreads, 1) tree_kernel(const __grid_constant
     *abort_flag = 0;
     *start_b = p.B;
     *start_p = 0;
-    for (int s = 0; s < kStages; ++s) {
-      mbar_init(b_k_full + 8 * s, 1);
-      mbar_init(b_k_empty + 8 * s, 1);
-      mbar_init(b_v_full + 8 * s, 1);
-      mbar_init(b_v_empty + 8 * s, 4);   // the four warps that widen
-    }
-    for (int s = 0; s < 2; ++s) {
-      mbar_init(b_q_full + 8 * s, 1);
-      mbar_init(b_q_empty + 8 * s, 1 + 8);   // the MMA, the softmax warps
-      mbar_init(b_s_full + 8 * s, 1);
-      mbar_init(b_p_full + 8 * s, 4 * SG);
-      mbar_init(b_w_full + 8 * s, 4);
-      mbar_init(b_pv_done + 8 * s, 1);
-    }
-    for (int s = 0; s < kRing; ++s) {
-      mbar_init(b_c_full + 8 * s, 128);   // the copying threads
-    }
-    mbar_init(b_o_free, 4 * SG);   // the softmax warps that read u^T
-    mbar_init(b_drain, 1);
-    mbar_init(b_fin, 1);
-    for (int s = 0; s < 2; ++s) {
-      mbar_init(b_red + 8 * s, 4);
-      mbar_init(b_xch + 8 * s, 2);
-    }
+  }
+  // barriers, a thread each
+  if (tid < C::kNBars) {
+    const uint32_t bar = sbase + C::kOffBar + 8 * tid;
+    auto in = [&](uint32_t first, int n) { return bar >= first && bar < first + 8 * n; };
+    const int arrivals = in(b_v_empty, kStages) || in(b_w_full, 2) || in(b_red, 2) ? 4   // the warps that widen; a group
+                         : in(b_q_empty, 2)                          ? 1 + 8     // the MMA, the softmax warps
+                         : in(b_p_full, 2) || in(b_o_free, 1)        ? 4 * SG    // the softmax warps of a step; those that read u^T
+                         : in(b_c_full, kRing)                       ? 128       // the copying threads
+                         : in(b_xch, 2)                              ? 2
+                                                                     : 1;
+    mbar_init(bar, arrivals);
     fence_mbar_init();
   }
   if (warp == kWarpMMA) {
@@ -195,9 +181,8 @@ __global__ void __launch_bounds__(kThreads, 1) tree_kernel(const __grid_constant
   } else if (warp == kWarpMMA) {
     // ------------------------------------------------------------------ MMA issuer
     if (lane == 0) {
-      const uint32_t idesc_s = idesc_e4m3(kKeys, C::kWideS ? N * (p.fp16 ? 3 : 2) : N);
+      const uint32_t idesc_s = idesc_e4m3(kKeys, N * (p.fp16 ? 3 : 2));
       constexpr uint32_t kIdescO = idesc_f16_f32acc(128, C::kRows, false, false) | (1u << 15);   // A = V read MN-major
-      const int passes = C::kWideS ? 1 : p.fp16 ? 3 : 2;   // over K: the pieces' products summed by the MMA, or by the softmax
       const uint64_t dq0 = sdesc_rows<DA>(sbase + C::kOffQ);
       const uint64_t dk0 = sdesc_rows<DA>(sbase + C::kOffK);
       const uint64_t dv0 = sdesc_sw128(sbase + C::kOffW, kWideChunk, 1024);
@@ -234,38 +219,32 @@ __global__ void __launch_bounds__(kThreads, 1) tree_kernel(const __grid_constant
           umma_commit(b_pv_done + 8 * b);
           return true;
         };
-        for (int t = w.t0; t < w.t1; ++t) {
+        // S^T of a step's tiles into its buffer, whose last contents were consumed:
+        // this thread has waited for that step's P
+        auto issue_s = [&](int t) -> bool {
           const int st = k_cnt % kStages, sb = k_cnt & 1;
           const int nt = kTPS == 1 ? 1 : (w.n - t * KS > kKeys ? 2 : 1);
-          if (!wait(b_k_full + 8 * st, (k_cnt / kStages) & 1, wc, ATTN_DEVERR_WAIT_TIMEOUT_SITE(kSiteKFull))) {
-            ok = false;
-            break;
-          }
+          if (!wait(b_k_full + 8 * st, (k_cnt / kStages) & 1, wc, ATTN_DEVERR_WAIT_TIMEOUT_SITE(kSiteKFull))) return false;
           ++k_cnt;
           tc_fence_after();
-          // S^T of the step's tiles into buffer sb: its previous contents (two
-          // steps back) were consumed, since this thread has waited for that step's P
-          for (int x = 0; x < nt; ++x)
-            for (int s = 0; s < passes; ++s) {
+          for (int x = 0; x < nt; ++x) {
 #pragma unroll
-              for (int kk = 0; kk < DA / 32; ++kk) {
-                const uint64_t a = dk0 + ((st * kRaw + x * (kKeys * DA) + kk * 32) >> 4);
-                const uint64_t b = dq0 + ((qs * C::kQ + s * C::kQPiece + kk * 32) >> 4);
-                umma_ss_f8(tmem + (sb * kTPS + x) * C::kSCols, a, b, idesc_s, (s > 0 || kk > 0) ? 1u : 0u);
-              }
-            }
-          umma_commit(b_s_full + 8 * sb);
-          umma_commit(b_k_empty + 8 * st);
-          if (t > w.t0) {
-            if (!do_pv()) {
-              ok = false;
-              break;
+            for (int kk = 0; kk < DA / 32; ++kk) {
+              const uint64_t a = dk0 + ((st * kRaw + x * (kKeys * DA) + kk * 32) >> 4);
+              const uint64_t b = dq0 + ((qs * C::kQ + kk * 32) >> 4);
+              umma_ss_f8(tmem + (sb * kTPS + x) * C::kSCols, a, b, idesc_s, kk > 0 ? 1u : 0u);
             }
           }
+          umma_commit(b_s_full + 8 * sb);
+          umma_commit(b_k_empty + 8 * st);
+          return true;
+        };
+        // S^T of a step goes before P.V of the one before it
+        for (int t = w.t0; t <= w.t1 && ok; ++t) {
+          if (t < w.t1) ok = issue_s(t);
+          if (ok && t > w.t0) ok = do_pv();
         }
         if (!ok) break;
-        // the unit's last step
-        if (!do_pv()) break;
         umma_commit(b_q_empty + 8 * qs);
         ++units_done;
       }
@@ -311,7 +290,7 @@ __global__ void __launch_bounds__(kThreads, 1) tree_kernel(const __grid_constant
       // S^T of LD columns, the pieces' products summed, times the key's scale; -inf
       // where the bits say that a column does not see the key
       auto scores = [&](uint32_t at, float scale, bool all, uint32_t bits, float (&x)[LD]) {
-        if constexpr (C::kWideS) {
+        {
           float y[LD];
           tld_start<LD>(at, x);
           tld_start<LD>(at + N, y);
@@ -323,8 +302,6 @@ __global__ void __launch_bounds__(kThreads, 1) tree_kernel(const __grid_constant
 #pragma unroll
             for (int i = 0; i < LD; ++i) x[i] += y[i];
           }
-        } else {
-          tld<LD>(at, x);
         }
 #pragma unroll
         for (int i = 0; i < LD; ++i) x[i] *= scale;
@@ -373,7 +350,7 @@ __global__ void __launch_bounds__(kThreads, 1) tree_kernel(const __grid_constant
             continue;
           }
           if (first_t < 0) first_t = t;
-          const int sb = step & 1, ring = step % kRing;
+          const int sb = step & 1, ring = step % kRing;   // buffer of S^T and of P^T; stage of the scales
           if (!wait_warp(b_c_full + 8 * ring, (step / kRing) & 1, wc, ATTN_DEVERR_WAIT_TIMEOUT_SITE(kSiteSFree))) {
             ok = false;
             break;

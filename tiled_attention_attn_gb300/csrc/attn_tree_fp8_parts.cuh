@@ -26,7 +26,7 @@ constexpr int kThreads = 512;
 // the others do without.
 constexpr int kRegsFew = 88, kRegsMany = 168;
 static_assert(2 * (kRegsFew + kRegsMany) <= 512, "the launch's registers");
-constexpr int kRing = 4;                // stages of scales
+constexpr int kRing = 8;                // stages of scales
 constexpr float kPLift = 7.0f;          // log2 of the factor of P'
 constexpr float kPDrop = 0x1p-7f;
 
@@ -276,6 +276,19 @@ struct Tiles {
   static constexpr int kRaw = KS * DA, kWide = 2 * kRaw, kWideChunk = kKeys * 128;
 };
 
+// a / b for a >= 0, b > 0: in 32 bits where that does, which every call of usual size
+// does, in a fifth of the instructions.
+__device__ __forceinline__ long long quotient(long long a, long long b) {
+  if (((a | b) >> 32) == 0) return static_cast<unsigned>(a) / static_cast<unsigned>(b);
+  return a / b;
+}
+// range_of (attn_paged_line.cuh) with these divisions.
+__device__ __forceinline__ long long range_length(long long total, long long units, int ranges) {
+  const long long share = quotient(total + ranges - 1, ranges);
+  if (share >= kMinSteps) return share;
+  return max(share, min(static_cast<long long>(kMinSteps), units > 0 ? quotient(total, units) : 1));
+}
+
 // Finds where this CTA's range of the line begins; __syncthreads, then enter_line.
 // The line of steps: each thread a strip of sequences, then a prefix sum.
 struct Line {
@@ -302,7 +315,7 @@ __device__ __forceinline__ Line find_line(const Params& p, volatile int* start_b
   for (int b = b_lo; b < b_hi; ++b) mine += cost_of(b);
   const long long before = block_prefix<kThreads>(
       mine, static_cast<int>(min(static_cast<long long>(nh) * (b_hi - b_lo), 1LL << 24)), warp_sums, total, units);
-  r.range = range_of<kMinSteps>(total, units, ranges);
+  r.range = range_length(total, units, ranges);
   // (SMs past the last whole range idle)
   r.begin = r.range_id < ranges ? r.range_id * r.range : total;
   r.end = min(r.begin + r.range, total);
@@ -331,7 +344,7 @@ __device__ __forceinline__ Walk enter_line(const Params& p, const Line& line, in
   w.p = start_p;
   if (w.b < p.B) {
     enter<KS>(p, w);
-    w.hc = static_cast<int>((w.begin - w.p) / (w.T + 1));
+    w.hc = static_cast<int>(quotient(w.begin - w.p, w.T + 1));
     w.p += static_cast<long long>(w.hc) * (w.T + 1);
   }
   return w;
@@ -411,10 +424,11 @@ __device__ __forceinline__ void widen_and_scales(const Params& p, Walk w, int pl
   const int c = DA == 128 ? 4 * ((me >> 3) & 1) + (me & 3) : me & 3;
   const uint32_t from = DA == 128 ? swizzled<128>(row, 16 * c) : row * 64 + 16 * c;
   const uint32_t to = (DA == 128 ? (c >> 2) * T::kWideChunk : 0) + row * 128 + ((2 * (c & 3) ^ (row & 7)) << 4);   // (the second word: bit 4 flipped)
-  // The scales are copied two steps ahead, over the units' ends: a walk of their
-  // own, whose table entries are read a step before that.  Key 128 i + me of the
-  // step.  Their ring needs no barrier for its empty stages: the stage of step i + 2
-  // was step i - 2's, whose P.V has completed when this is reached.
+  // The scales are copied kAhead steps ahead, over the units' ends: a walk of their own,
+  // whose table entries are read a step before that.  Key 128 i + me of the step.  Their
+  // ring needs no barrier for its empty stages: what the stage of step i + kAhead held was
+  // of a step up to i - 2, whose P.V has completed when this is reached.
+  constexpr int kAhead = kRing - 3;
   const uint32_t sbase = smem_u32(smem);
   Walk wa = w;
   Unit ua = {};
@@ -454,7 +468,7 @@ __device__ __forceinline__ void widen_and_scales(const Params& p, Walk w, int pl
   settle(true);
   entries();
 #pragma unroll 1
-  for (int i = 0; i < 2; ++i) copy_scales();
+  for (int i = 0; i < kAhead; ++i) copy_scales();
   uint32_t step = 0;
   bool ok = true;
   for (bool more = next_unit<KS>(p, w, true); more && ok; more = next_unit<KS>(p, w, false)) {

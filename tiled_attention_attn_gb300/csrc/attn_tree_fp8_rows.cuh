@@ -70,24 +70,17 @@ __global__ void __launch_bounds__(kThreads, 1) tree_rows_kernel(const __grid_con
     *abort_flag = 0;
     *start_b = p.B;
     *start_p = 0;
-    for (int s = 0; s < kStages; ++s) {
-      mbar_init(b_k_full + 8 * s, 1);
-      mbar_init(b_k_empty + 8 * s, 1);
-      mbar_init(b_v_full + 8 * s, 1);
-      mbar_init(b_v_empty + 8 * s, 4);   // the four warps that widen
-    }
-    for (int s = 0; s < 2; ++s) {
-      mbar_init(b_s_full + 8 * s, 1);
-      mbar_init(b_p_full + 8 * s, 8);    // the softmax warps
-      mbar_init(b_w_full + 8 * s, 4);
-      mbar_init(b_pv_done + 8 * s, 1);
-    }
-    for (int s = 0; s < kRing; ++s) mbar_init(b_c_full + 8 * s, 128);
-    mbar_init(b_q_full, 8);    // the softmax warps, which convert the queries
-    mbar_init(b_q_empty, 1 + 8);   // the MMA, and the softmax warps
-    mbar_init(b_o_free, 4);
-    mbar_init(b_drain, 1);
-    mbar_init(b_fin, 4);
+  }
+  // barriers, a thread each
+  if (tid < C::kNBars) {
+    const uint32_t bar = sbase + C::kOffBar + 8 * tid;
+    auto in = [&](uint32_t first, int n) { return bar >= first && bar < first + 8 * n; };
+    const int arrivals = in(b_v_empty, kStages) || in(b_w_full, 2) || in(b_o_free, 1) || in(b_fin, 1) ? 4   // the warps that widen; a group
+                         : in(b_p_full, 2) || in(b_q_full, 1) ? 8       // the softmax warps, which convert the queries too
+                         : in(b_q_empty, 1)                   ? 1 + 8   // the MMA, the softmax warps
+                         : in(b_c_full, kRing)                ? 128     // the copying threads
+                                                              : 1;
+    mbar_init(bar, arrivals);
     fence_mbar_init();
   }
   if (warp == kWarpMMA) {
