@@ -157,7 +157,7 @@ __global__ void __launch_bounds__(kThreads, 2) append_kernel(const __grid_consta
         __syncwarp();   // the table's readers of the token before
 #pragma unroll 1
         for (int t = lane; t < half; t += 32) {
-          const float2 f = turned(p.turns[t], pos);
+          const float2 f = turned_near(p.turns[t], pos);
           const int to = ((((t & 7) >> 2) * groups + (t >> 3)) << 2) + (t & 3);
           tab_f[to] = f.x * p.amplitude;
           tab_f[to + half] = f.y * p.amplitude;

@@ -213,7 +213,7 @@ __global__ void __launch_bounds__(kThreads, 2) norm_kernel(const __grid_constant
       if (p.rot) {
         __syncwarp();   // the table's readers of the token before
         auto turn_pair = [&](int i, int position_i) {
-          const float2 t = turned(p.turns[i], position_i);
+          const float2 t = turned_near(p.turns[i], position_i);
           const int to = ((((i & 7) >> 2) * groups + (i >> 3)) << 2) + (i & 3);
           tab_f[to] = t.x * p.amplitude;
           tab_f[to + half] = t.y * p.amplitude;
