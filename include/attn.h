@@ -594,7 +594,8 @@ long long attn_qk_norm_workspace_bytes(int d);
  *             stride_head * head + f bytes, strides positive multiples of 16, the
  *             same for k and v; 16-byte aligned.
  *   k_scales, v_scales   fp32, element (page, token, head) at scale_stride_page *
- *             page + scale_stride_token * token + scale_stride_head * head.
+ *             page + scale_stride_token * token + scale_stride_head * head;
+ *             scales are not negative.
  *   the others as in attn_paged_kv, with its rules for what the host does not
  *   read: key counts, offsets and pages out of range, slots past the last key.
  * What a query does not see never reaches its outputs, NaN rows included, as long

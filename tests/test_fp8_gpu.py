@@ -511,6 +511,48 @@ def test_streams_graphs_and_repeats():
     assert all(torch.equal(a, b) for (_, outs), w in zip(sets, want) for a, b in zip(outs, w))
 
 
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("hq", [2, 16])
+def test_many_short_sequences_repeat(hq, d):
+    """Units of a few steps, several to a block: the join of the two groups of softmax
+    warps at each unit's end."""
+    lens = [(37 * i) % 900 for i in range(600)]
+    c = Cache8(lens, 2, d, 64, 3)
+    q = queries(len(lens), hq, d, BF, 4)
+    want = attn.attn_decode_fp8(q, *c.args())
+    ok()
+    for _ in range(40):
+        got = attn.attn_decode_fp8(q, *c.args())
+        assert all(torch.equal(a, b) for a, b in zip(got, want))
+    ok()
+
+
+def test_pages_whose_offsets_pass_32_bits():
+    """The same rows at the far end of a pool of more than 4 GiB of keys, and in a small
+    one: the same bits."""
+    hkv, d, page, far, lens = 8, 128, 16, 266_000, [300, 17]
+    assert far * page * hkv * d > 1 << 32
+    f, _ = attn.rotary_freqs(d)
+    q, k, v = (queries(sum(lens), h, d, BF, 6 + h) for h in (16, hkv, hkv))
+    got = []
+    for first in (0, far):
+        n = first + 21
+        pages = [torch.empty((n, page, hkv, d), dtype=torch.uint8, device="cuda").view(E4M3) for _ in range(2)]
+        scales = [torch.empty((n, page, hkv), device="cuda") for _ in range(2)]
+        table = torch.full((2, 19), n - 1, dtype=torch.int32, device="cuda")
+        table[0] += -torch.arange(19, dtype=torch.int32, device="cuda")
+        table[1, :2] = torch.tensor([n - 21, n - 20], dtype=torch.int32)
+        cache = (*pages, *scales, table, torch.tensor(lens, dtype=torch.int32, device="cuda"))
+        qr = attn.cache_append_fp8(k, v, *cache, cu_of(lens), q=q, freqs=f)
+        out = attn.cache_read_fp8(*cache, cu_of(lens), sum(lens))
+        at = torch.tensor([lens[0] - 1, sum(lens) - 1], device="cuda")
+        got.append((qr, *out, *attn.attn_decode_fp8(qr[at].contiguous(), *cache),
+                    *attn.attn_tree_fp8(qr[at[1]:], *cache, torch.tensor([0, 0, 1], dtype=torch.int32, device="cuda"))))
+        ok()
+        del pages, scales, cache
+    assert all(torch.equal(a, b) for a, b in zip(*got))
+
+
 def test_nothing_to_do():
     c = Cache8([20], 1, 64, 16, 1)
     e = torch.empty(0, 1, 64, dtype=BF, device="cuda")

@@ -333,3 +333,47 @@ def test_streams_graphs_and_threads():
     for c, (_, out) in zip(sets, graphs):
         c.check_forward(out[:2])
         c.check_backward(out[2:])
+
+
+def test_rows_whose_offsets_pass_32_bits():
+    rows, h, d, tail = 525_000, 32, 128, 500
+    assert rows * h * d > 1 << 31
+    q, g = (torch.randn(rows, h, d, dtype=BF, device="cuda") for _ in range(2))
+    w = torch.randn(d, device="cuda")
+    f, _ = attn.rotary_freqs(d)
+    pos = torch.arange(rows, dtype=torch.int32, device="cuda")
+    y = attn.qk_norm_rotary(q, q_weight=w, freqs=f, positions=pos)[0]
+    dq = attn.qk_norm_rotary_bwd(g, None, q, q_weight=w, freqs=f, positions=pos)[0]
+    at = slice(rows - tail, rows)
+    assert torch.equal(y[at], attn.qk_norm_rotary(q[at], q_weight=w, freqs=f, positions=pos[at])[0])
+    assert torch.equal(dq[at], attn.qk_norm_rotary_bwd(g[at], None, q[at], q_weight=w, freqs=f, positions=pos[at])[0])
+    ok()
+
+
+def test_a_captured_training_step():
+    c = Case(300, 8, 2, 128, 64, 3, False, BF, F32)
+    leaves = [t.clone().requires_grad_() for t in c.args()[:4]]
+
+    def step():
+        y = attn.qk_norm_rotary_func(*leaves, *c.args()[4:], **c.kw())
+        torch.autograd.backward(y, (c.dq, c.dk))
+
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        for _ in range(2):
+            step()
+    torch.cuda.current_stream().wait_stream(side)
+    for t in leaves:
+        t.grad = None
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        step()
+    c.q.mul_(0.5)
+    with torch.no_grad():
+        leaves[0].copy_(c.q)
+    for _ in range(2):
+        g.replay()
+    ok()
+    want = attn.qk_norm_rotary_bwd(c.dq, c.dk, *c.args(), **c.kw())
+    assert all(torch.equal(t.grad, w) for t, w in zip(leaves, want))

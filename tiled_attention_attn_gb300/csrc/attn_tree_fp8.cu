@@ -1,5 +1,6 @@
 // Entry points of the attention over paged caches of 8-bit floating point
-// (attn_tree_fp8): argument checks; the kernel is in attn_tree_fp8_kernel.cuh.
+// (attn_tree_fp8): argument checks; the kernels are in
+// attn_tree_fp8_kernel.cuh and attn_tree_fp8_rows.cuh.
 #include <cuda_runtime.h>
 
 #include <algorithm>

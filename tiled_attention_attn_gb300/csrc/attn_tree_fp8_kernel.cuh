@@ -20,19 +20,25 @@
 // cache.  A value's scale goes into its weight: P' = p vs / R in fp16, R a power of
 // two at least the largest scale so far, so P' <= p; u is rescaled where R grows, as
 // where m grows.  l sums p itself.  P' is held times 2^7 as in the 16-bit kernel
-// (kLift).
+// (kPLift).  The rounding of P' to fp16, 2^-11 of it, is the only one below fp32
+// before O's own.
 //
 // Bound by HBM: per key and head d bytes of K and of V, and 8 of scales.  TMA
-// stages of 16 KB of K and 16 of V (three or four in flight), per page one box per
-// tile; a warp brings the scales with 4-byte asynchronous copies.  Shared memory is
-// the next limit: per 128 keys of 128 features 32 KB written by TMA, 32 KB of K read
-// by the MMA (twice 16), V read (16), written (32) and read again (32): 1,150 cycles
-// of 128 bytes against the 1,400 that HBM takes for them.
+// stages of 16 KB of K and 16 of V (three or four), per page one box per tile; the
+// warps that widen V bring the scales with 4-byte asynchronous copies, five steps
+// ahead.  The queries' pieces are further columns of S^T, whose parts the softmax
+// adds: at these widths the number of products counts, not their columns (a product per
+// piece, and all softmax warps on one step: 120 us for 32 caches of ~3,550 keys, 32
+// heads on 8 of 128).  Measured (device time, merge included): those caches
+// 60.7 us, of which the 236 MB take 35 at the copy rate; one of 131,072 keys 62.5 of
+// 41; the line itself runs at 5.1 to 5.9 TB/s, what is left is 7 us to the first S
+// (prologue, the walk, the queries' conversion), the epilogue and 3 to 4.5 of the merge.
 //
 // Work is cut as in the 16-bit decode kernel: the steps of all (sequence, unit) on
 // one line, equal ranges per CTA, pieces of a cut unit joined by tree_merge_kernel.
-// A unit has up to 64 columns; a tree with more takes several units per head, which
-// walk the line side by side and share the cache's lines in L2.
+// A unit has up to 32 columns; more are the rows of attn_tree_fp8_rows.cuh (48
+// columns as two units here, each reading the keys, took 83 us where that kernel
+// took 53).
 //
 // Slots past a sequence's last key may hold anything: their scores are dropped by
 // index, their V is zeroed as it is widened.
@@ -49,10 +55,12 @@ constexpr int kRaw = kKeys * 128;       // a stage of K, or of V, in bytes
 constexpr int kWide = 2 * kRaw;         // a step's V in fp16: two chunks of 128-byte rows
 constexpr int kWideChunk = kRaw;
 
-// Two groups of four softmax warps, GT columns each: of 32 and 64 columns (SG = 2)
-// each takes half; up to 16 columns (SG = 1, TG = 2) they take turns, step by step,
-// with maxima, sums and accumulators of their own that are joined at the unit's end
-// (one group's chain of waits is longer than a step takes to arrive).
+// Two groups of four softmax warps, GT columns each: of 32 columns (SG = 2) each takes
+// half; up to 16 columns (SG = 1, TG = 2) they take turns, step by step, with maxima,
+// sums and accumulators of their own that are joined at the unit's end (one group's
+// chain of waits is longer than a step takes to arrive).  Two buffers of S^T, so that a
+// group meets every phase of its buffer's barriers: with three it would see every
+// second, which parity cannot tell from the one before.
 template <int GT_, int SG_, int DA>
 struct Cfg {
   static constexpr int GT = GT_, SG = SG_, TG = 3 - SG;
@@ -151,504 +159,503 @@ __global__ void __launch_bounds__(kThreads, 1) tree_kernel(const __grid_constant
   Walk w = enter_line<KS>(p, line, *start_b, *start_p);
 
   if (!softmax) {
-  regs_dec<kRegsFew>();
-  if (warp == kWarpK) {
-    produce<DA, kTPS, N, kStages>(p, w, place, &p.tm_k, sbase + C::kOffK, b_k_full, b_k_empty, wc);
-  } else if (warp == kWarpV) {
-    produce<DA, kTPS, N, kStages>(p, w, place, &p.tm_v, sbase + C::kOffV, b_v_full, b_v_empty, wc);
-  } else if (warp >= kWarpWiden && warp < kWarpWiden + 4) {
-    widen_and_scales<DA, kTPS, N, kStages>(p, w, place, smem, C::kOffV, C::kOffW, C::kOffScale, b_v_full, b_v_empty,
-                                           b_w_full, b_pv_done, b_c_full, wc);
-  } else if (warp == kWarpQ) {
-    // ------------------------------------------------------------------ queries
-    uint32_t cnt = 0;
-    bool ok = true;
-    for (bool more = next_unit<KS>(p, w, true); more && ok; more = next_unit<KS>(p, w, false)) {
-      const Unit u = unit_of<N>(p, w, place);
-      if (w.t1 <= w.t0 || u.cols <= 0) continue;
-      const int slot = cnt % kSlots;
-      uint8_t* dst = smem + C::kOffQ + slot * C::kQ;
-      float* col = reinterpret_cast<float*>(smem + C::kOffCol) + slot * N;
-      unsigned long long* mask = reinterpret_cast<unsigned long long*>(smem + C::kOffMask) + slot * N;
-      if (!wait_warp(b_q_empty + 8 * slot, ((cnt / kSlots) & 1) ^ 1, wc,
-                          ATTN_DEVERR_WAIT_TIMEOUT_SITE(kSiteQEmpty))) break;
-      convert_queries<DA, 1>(p, w, u, 0, 1, dst, C::kQPiece, col, mask);
-      fence_proxy_async_smem();
-      __syncwarp();
-      if (lane == 0) mbar_arrive(b_q_full + 8 * slot);
-      ++cnt;
-    }
-  } else if (warp == kWarpMMA) {
-    // ------------------------------------------------------------------ MMA issuer
-    if (lane == 0) {
-      const uint32_t idesc_s = idesc_e4m3(kKeys, N * (p.fp16 ? 3 : 2));
-      constexpr uint32_t kIdescO = idesc_f16_f32acc(128, C::kRows, false, false) | (1u << 15);   // A = V read MN-major
-      const uint64_t dq0 = sdesc_rows<DA>(sbase + C::kOffQ);
-      const uint64_t dk0 = sdesc_rows<DA>(sbase + C::kOffK);
-      const uint64_t dv0 = sdesc_sw128(sbase + C::kOffW, kWideChunk, 1024);
-      const uint64_t dp0 = sdesc_sw128(sbase + C::kOffP, 16, 1024);
-      const uint32_t t_u = tmem + C::kColU;   // u^T columns
-      uint32_t q_cnt = 0, k_cnt = 0, pv_cnt = 0, units_done = 0;
+    regs_dec<kRegsFew>();
+    if (warp == kWarpK) {
+      produce<DA, kTPS, N, kStages>(p, w, place, &p.tm_k, sbase + C::kOffK, b_k_full, b_k_empty, wc);
+    } else if (warp == kWarpV) {
+      produce<DA, kTPS, N, kStages>(p, w, place, &p.tm_v, sbase + C::kOffV, b_v_full, b_v_empty, wc);
+    } else if (warp >= kWarpWiden && warp < kWarpWiden + 4) {
+      widen_and_scales<DA, kTPS, N, kStages>(p, w, place, smem, C::kOffV, C::kOffW, C::kOffScale, b_v_full, b_v_empty,
+                                             b_w_full, b_pv_done, b_c_full, wc);
+    } else if (warp == kWarpQ) {
+      // ------------------------------------------------------------------ queries
+      uint32_t cnt = 0;
       bool ok = true;
       for (bool more = next_unit<KS>(p, w, true); more && ok; more = next_unit<KS>(p, w, false)) {
         const Unit u = unit_of<N>(p, w, place);
         if (w.t1 <= w.t0 || u.cols <= 0) continue;
-        const int qs = q_cnt % kSlots;
-        if (!wait(b_q_full + 8 * qs, (q_cnt / kSlots) & 1, wc, ATTN_DEVERR_WAIT_TIMEOUT_SITE(kSiteQFull))) break;
-        ++q_cnt;
-        tc_fence_after();
-        // u^T += V^T P^T of the next step in line.  Before a unit's first products,
-        // which overwrite u^T, the previous unit's epilogue must have read it
-        int pv_unit = 0;
-        auto do_pv = [&]() -> bool {
-          const bool first = pv_unit++ < TG;
-          const int b = pv_cnt & 1;
-          if (!wait(b_w_full + 8 * b, (pv_cnt >> 1) & 1, wc, ATTN_DEVERR_WAIT_TIMEOUT_SITE(kSiteVFull))) return false;
-          if (!wait(b_p_full + 8 * b, (pv_cnt >> 1) & 1, wc, ATTN_DEVERR_WAIT_TIMEOUT_SITE(kSitePFull))) return false;
-          ++pv_cnt;
-          if (pv_unit == 1 && units_done > 0 &&
-              !wait(b_o_free, (units_done - 1) & 1, wc, ATTN_DEVERR_WAIT_TIMEOUT_SITE(kSiteODone)))
-            return false;
-          tc_fence_after();
-#pragma unroll
-          for (int kk = 0; kk < kKeys / 16; ++kk) {
-            const uint64_t a = dv0 + ((b * kWide + kk * 2048) >> 4);
-            const uint64_t x = dp0 + ((b * C::kP + (kk >> 2) * C::kPChunk + (kk & 3) * 32) >> 4);
-            umma_ss(t_u + (TG == 2 ? b * C::kRows : 0), a, x, kIdescO, (first && kk == 0) ? 0u : 1u);
-          }
-          umma_commit(b_pv_done + 8 * b);
-          return true;
-        };
-        // S^T of a step's tiles into its buffer, whose last contents were consumed:
-        // this thread has waited for that step's P
-        auto issue_s = [&](int t) -> bool {
-          const int st = k_cnt % kStages, sb = k_cnt & 1;
-          const int nt = kTPS == 1 ? 1 : (w.n - t * KS > kKeys ? 2 : 1);
-          if (!wait(b_k_full + 8 * st, (k_cnt / kStages) & 1, wc, ATTN_DEVERR_WAIT_TIMEOUT_SITE(kSiteKFull))) return false;
-          ++k_cnt;
-          tc_fence_after();
-          for (int x = 0; x < nt; ++x) {
-#pragma unroll
-            for (int kk = 0; kk < DA / 32; ++kk) {
-              const uint64_t a = dk0 + ((st * kRaw + x * (kKeys * DA) + kk * 32) >> 4);
-              const uint64_t b = dq0 + ((qs * C::kQ + kk * 32) >> 4);
-              umma_ss_f8(tmem + (sb * kTPS + x) * C::kSCols, a, b, idesc_s, kk > 0 ? 1u : 0u);
-            }
-          }
-          umma_commit(b_s_full + 8 * sb);
-          umma_commit(b_k_empty + 8 * st);
-          return true;
-        };
-        // S^T of a step goes before P.V of the one before it
-        for (int t = w.t0; t <= w.t1 && ok; ++t) {
-          if (t < w.t1) ok = issue_s(t);
-          if (ok && t > w.t0) ok = do_pv();
-        }
-        if (!ok) break;
-        umma_commit(b_q_empty + 8 * qs);
-        ++units_done;
+        const int slot = cnt % kSlots;
+        uint8_t* dst = smem + C::kOffQ + slot * C::kQ;
+        float* col = reinterpret_cast<float*>(smem + C::kOffCol) + slot * N;
+        unsigned long long* mask = reinterpret_cast<unsigned long long*>(smem + C::kOffMask) + slot * N;
+        if (!wait_warp(b_q_empty + 8 * slot, ((cnt / kSlots) & 1) ^ 1, wc,
+                            ATTN_DEVERR_WAIT_TIMEOUT_SITE(kSiteQEmpty))) break;
+        convert_queries<DA, 1>(p, w, u, 0, 1, dst, C::kQPiece, col, mask);
+        fence_proxy_async_smem();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(b_q_full + 8 * slot);
+        ++cnt;
       }
-      umma_commit(b_drain);
-      mbar_wait(b_drain, 0, wc, ATTN_DEVERR_WAIT_TIMEOUT_SITE(kSiteDrain), false);
+    } else if (warp == kWarpMMA) {
+      // ------------------------------------------------------------------ MMA issuer
+      if (lane == 0) {
+        const uint32_t idesc_s = idesc_e4m3(kKeys, N * (p.fp16 ? 3 : 2));
+        constexpr uint32_t kIdescO = idesc_f16_f32acc(128, C::kRows, false, false) | (1u << 15);   // A = V read MN-major
+        const uint64_t dq0 = sdesc_rows<DA>(sbase + C::kOffQ);
+        const uint64_t dk0 = sdesc_rows<DA>(sbase + C::kOffK);
+        const uint64_t dv0 = sdesc_sw128(sbase + C::kOffW, kWideChunk, 1024);
+        const uint64_t dp0 = sdesc_sw128(sbase + C::kOffP, 16, 1024);
+        const uint32_t t_u = tmem + C::kColU;   // u^T columns
+        uint32_t q_cnt = 0, k_cnt = 0, pv_cnt = 0, units_done = 0;
+        bool ok = true;
+        for (bool more = next_unit<KS>(p, w, true); more && ok; more = next_unit<KS>(p, w, false)) {
+          const Unit u = unit_of<N>(p, w, place);
+          if (w.t1 <= w.t0 || u.cols <= 0) continue;
+          const int qs = q_cnt % kSlots;
+          if (!wait(b_q_full + 8 * qs, (q_cnt / kSlots) & 1, wc, ATTN_DEVERR_WAIT_TIMEOUT_SITE(kSiteQFull))) break;
+          ++q_cnt;
+          tc_fence_after();
+          // u^T += V^T P^T of the next step in line.  Before a unit's first products,
+          // which overwrite u^T, the previous unit's epilogue must have read it
+          int pv_unit = 0;
+          auto do_pv = [&]() -> bool {
+            const bool first = pv_unit++ < TG;
+            const int b = pv_cnt & 1;
+            if (!wait(b_w_full + 8 * b, (pv_cnt >> 1) & 1, wc, ATTN_DEVERR_WAIT_TIMEOUT_SITE(kSiteVFull))) return false;
+            if (!wait(b_p_full + 8 * b, (pv_cnt >> 1) & 1, wc, ATTN_DEVERR_WAIT_TIMEOUT_SITE(kSitePFull))) return false;
+            ++pv_cnt;
+            if (pv_unit == 1 && units_done > 0 &&
+                !wait(b_o_free, (units_done - 1) & 1, wc, ATTN_DEVERR_WAIT_TIMEOUT_SITE(kSiteODone)))
+              return false;
+            tc_fence_after();
+#pragma unroll
+            for (int kk = 0; kk < kKeys / 16; ++kk) {
+              const uint64_t a = dv0 + ((b * kWide + kk * 2048) >> 4);
+              const uint64_t x = dp0 + ((b * C::kP + (kk >> 2) * C::kPChunk + (kk & 3) * 32) >> 4);
+              umma_ss(t_u + (TG == 2 ? b * C::kRows : 0), a, x, kIdescO, (first && kk == 0) ? 0u : 1u);
+            }
+            umma_commit(b_pv_done + 8 * b);
+            return true;
+          };
+          // S^T of a step's tiles into its buffer, whose last contents were consumed:
+          // this thread has waited for that step's P
+          auto issue_s = [&](int t) -> bool {
+            const int st = k_cnt % kStages, sb = k_cnt & 1;
+            const int nt = kTPS == 1 ? 1 : (w.n - t * KS > kKeys ? 2 : 1);
+            if (!wait(b_k_full + 8 * st, (k_cnt / kStages) & 1, wc, ATTN_DEVERR_WAIT_TIMEOUT_SITE(kSiteKFull))) return false;
+            ++k_cnt;
+            tc_fence_after();
+            for (int x = 0; x < nt; ++x) {
+#pragma unroll
+              for (int kk = 0; kk < DA / 32; ++kk) {
+                const uint64_t a = dk0 + ((st * kRaw + x * (kKeys * DA) + kk * 32) >> 4);
+                const uint64_t b = dq0 + ((qs * C::kQ + kk * 32) >> 4);
+                umma_ss_f8(tmem + (sb * kTPS + x) * C::kSCols, a, b, idesc_s, kk > 0 ? 1u : 0u);
+              }
+            }
+            umma_commit(b_s_full + 8 * sb);
+            umma_commit(b_k_empty + 8 * st);
+            return true;
+          };
+          // S^T of a step goes before P.V of the one before it
+          for (int t = w.t0; t <= w.t1 && ok; ++t) {
+            if (t < w.t1) ok = issue_s(t);
+            if (ok && t > w.t0) ok = do_pv();
+          }
+          if (!ok) break;
+          umma_commit(b_q_empty + 8 * qs);
+          ++units_done;
+        }
+        umma_commit(b_drain);
+        mbar_wait(b_drain, 0, wc, ATTN_DEVERR_WAIT_TIMEOUT_SITE(kSiteDrain), false);
+      }
     }
-  }
   } else {
-  regs_inc<kRegsMany>();
+    regs_inc<kRegsMany>();
     auto pv_wait = [&](uint32_t i) { return wait_pv(b_pv_done, i, wc); };
     uint32_t step = 0;   // steps so far, all units
     bool ok = true;
-    {
-      // ---------------------------------------------------------------- softmax warps
-      const int grp = warp >= kWarpSoft2 ? 1 : 0;
-      const int sw = warp - (grp ? kWarpSoft2 : kWarpSoft1);  // softmax warp 0..3 of its group
-      const int quarter = warp & 3;                  // TMEM lane quarter this warp may address
-      const int lrow = quarter * 32 + lane;          // TMEM lane: key of the tile (S^T), d (u^T)
-      constexpr int CH = GT < 16 ? GT : 16, NC = GT / CH;   // columns at a time
-      constexpr int LD = CH < 4 ? 4 : CH;            // as they are read
-      const int gcol = SG == 2 ? grp * GT : 0;       // first column of the group
-      const uint32_t t_lane = tmem + (static_cast<uint32_t>(quarter * 32) << 16);
-      // u^T columns this thread's lane holds: at DA = 64 lanes 64-127 keep u_b
-      const uint32_t t_u = t_lane + C::kColU + ((kTPS == 2 && lrow >= 64) ? N : 0) + gcol + (TG == 2 ? grp * C::kRows : 0);
-      float4* red = reinterpret_cast<float4*>(smem + C::kOffRed) + grp * 2 * (GT + 1);   // [parity][GT + 1], a float per warp
-      const uint32_t bar_red = b_red + 8 * grp, bar_xch = b_xch + 8 * grp;
-      uint32_t q_cnt = 0, red_cnt = 0, xch_cnt = 0, units_done = 0;
-      float* m = reinterpret_cast<float*>(smem + C::kOffMax) + (4 * grp + sw) * GT;   // this warp's copy of the maxima
-      // A warp hands GT + 1 values over to the group: column h by put(h, v) of one
-      // lane, then meet(); then red[par * (GT + 1) + h] has the four warps'
-      auto put = [&](int h, float v) { reinterpret_cast<float*>(red + (red_cnt & 1) * (GT + 1))[4 * h + sw] = v; };
-      constexpr int kOwn = CH == 16 ? 1 : CH == 8 ? 2 : CH == 4 ? 3 : CH == 2 ? 4 : 5;   // log2 of the lanes per column of fold_columns
-      auto put_folded = [&](int c, float v) {
-        if ((lane & ((1 << kOwn) - 1)) == 0) put(c * CH + (lane >> kOwn), v);
-      };
-      auto meet = [&]() -> bool {
-        __syncwarp();
-        if (lane == 0) mbar_arrive(bar_red);
-        if (!wait_warp(bar_red, red_cnt & 1, wc, ATTN_DEVERR_WAIT_TIMEOUT_SITE(kSiteXchg))) return false;
-        ++red_cnt;
-        return true;
-      };
-      // S^T of LD columns, the pieces' products summed, times the key's scale; -inf
-      // where the bits say that a column does not see the key
-      auto scores = [&](uint32_t at, float scale, bool all, uint32_t bits, float (&x)[LD]) {
-        {
-          float y[LD];
-          tld_start<LD>(at, x);
-          tld_start<LD>(at + N, y);
-          tld_wait<LD>(x, y);
+    // ---------------------------------------------------------------- softmax warps
+    const int grp = warp >= kWarpSoft2 ? 1 : 0;
+    const int sw = warp - (grp ? kWarpSoft2 : kWarpSoft1);  // softmax warp 0..3 of its group
+    const int quarter = warp & 3;                  // TMEM lane quarter this warp may address
+    const int lrow = quarter * 32 + lane;          // TMEM lane: key of the tile (S^T), d (u^T)
+    constexpr int CH = GT < 16 ? GT : 16, NC = GT / CH;   // columns at a time
+    constexpr int LD = CH < 4 ? 4 : CH;            // as they are read
+    const int gcol = SG == 2 ? grp * GT : 0;       // first column of the group
+    const uint32_t t_lane = tmem + (static_cast<uint32_t>(quarter * 32) << 16);
+    // u^T columns this thread's lane holds: at DA = 64 lanes 64-127 keep u_b
+    const uint32_t t_u = t_lane + C::kColU + ((kTPS == 2 && lrow >= 64) ? N : 0) + gcol + (TG == 2 ? grp * C::kRows : 0);
+    float4* red = reinterpret_cast<float4*>(smem + C::kOffRed) + grp * 2 * (GT + 1);   // [parity][GT + 1], a float per warp
+    const uint32_t bar_red = b_red + 8 * grp, bar_xch = b_xch + 8 * grp;
+    uint32_t q_cnt = 0, red_cnt = 0, xch_cnt = 0, units_done = 0;
+    float* m = reinterpret_cast<float*>(smem + C::kOffMax) + (4 * grp + sw) * GT;   // this warp's copy of the maxima
+    // A warp hands GT + 1 values over to the group: column h by put(h, v) of one
+    // lane, then meet(); then red[par * (GT + 1) + h] has the four warps'
+    auto put = [&](int h, float v) { reinterpret_cast<float*>(red + (red_cnt & 1) * (GT + 1))[4 * h + sw] = v; };
+    constexpr int kOwn = CH == 16 ? 1 : CH == 8 ? 2 : CH == 4 ? 3 : CH == 2 ? 4 : 5;   // log2 of the lanes per column of fold_columns
+    auto put_folded = [&](int c, float v) {
+      if ((lane & ((1 << kOwn) - 1)) == 0) put(c * CH + (lane >> kOwn), v);
+    };
+    auto meet = [&]() -> bool {
+      __syncwarp();
+      if (lane == 0) mbar_arrive(bar_red);
+      if (!wait_warp(bar_red, red_cnt & 1, wc, ATTN_DEVERR_WAIT_TIMEOUT_SITE(kSiteXchg))) return false;
+      ++red_cnt;
+      return true;
+    };
+    // S^T of LD columns, the pieces' products summed, times the key's scale; -inf
+    // where the bits say that a column does not see the key
+    auto scores = [&](uint32_t at, float scale, bool all, uint32_t bits, float (&x)[LD]) {
+      {
+        float y[LD];
+        tld_start<LD>(at, x);
+        tld_start<LD>(at + N, y);
+        tld_wait<LD>(x, y);
+#pragma unroll
+        for (int i = 0; i < LD; ++i) x[i] += y[i];
+        if (p.fp16) {
+          tld<LD>(at + 2 * N, y);
 #pragma unroll
           for (int i = 0; i < LD; ++i) x[i] += y[i];
-          if (p.fp16) {
-            tld<LD>(at + 2 * N, y);
-#pragma unroll
-            for (int i = 0; i < LD; ++i) x[i] += y[i];
-          }
         }
+      }
 #pragma unroll
-        for (int i = 0; i < LD; ++i) x[i] *= scale;
-        if (!all) {
+      for (int i = 0; i < LD; ++i) x[i] *= scale;
+      if (!all) {
 #pragma unroll
-          for (int i = 0; i < CH; ++i)
-            if (!((bits >> i) & 1)) x[i] = -INFINITY;
-        }
+        for (int i = 0; i < CH; ++i)
+          if (!((bits >> i) & 1)) x[i] = -INFINITY;
+      }
+    };
+    for (bool more = next_unit<KS>(p, w, true); more && ok; more = next_unit<KS>(p, w, false)) {
+      const Unit u = unit_of<N>(p, w, place);
+      if (u.cols <= 0) continue;
+      const int G = min(GT, u.cols - gcol);   // this group's columns (may be none)
+      // row of q and head of this group's column h
+      auto out_row = [&](int h, int& head) {
+        const int cc = u.col0 + gcol + h, token = token_of(p, cc);
+        head = u.g * p.group + cc - token * p.group;
+        return w.row0 + token;
       };
-      for (bool more = next_unit<KS>(p, w, true); more && ok; more = next_unit<KS>(p, w, false)) {
-        const Unit u = unit_of<N>(p, w, place);
-        if (u.cols <= 0) continue;
-        const int G = min(GT, u.cols - gcol);   // this group's columns (may be none)
-        // row of q and head of this group's column h
-        auto out_row = [&](int h, int& head) {
-          const int cc = u.col0 + gcol + h, token = token_of(p, cc);
-          head = u.g * p.group + cc - token * p.group;
-          return w.row0 + token;
-        };
-        if (w.T == 0) {
-          // a sequence without keys: O = 0, lse = -inf
-          for (int h = 0; h < G && (SG == 2 || grp == 0); ++h) {
-            int head;
-            const long long row = out_row(h, head);
-            if (lrow < DA) p.o[(row * p.Hq + head) * DA + lrow] = 0;
-            if (lrow == 0) p.lse[static_cast<long long>(head) * p.total + row] = -INFINITY;
-          }
+      if (w.T == 0) {
+        // a sequence without keys: O = 0, lse = -inf
+        for (int h = 0; h < G && (SG == 2 || grp == 0); ++h) {
+          int head;
+          const long long row = out_row(h, head);
+          if (lrow < DA) p.o[(row * p.Hq + head) * DA + lrow] = 0;
+          if (lrow == 0) p.lse[static_cast<long long>(head) * p.total + row] = -INFINITY;
+        }
+        continue;
+      }
+      if (w.t1 <= w.t0) continue;
+      const int qs = q_cnt % kSlots;
+      if (!wait_warp(b_q_full + 8 * qs, (q_cnt / kSlots) & 1, wc, ATTN_DEVERR_WAIT_TIMEOUT_SITE(kSiteQFull))) break;
+      ++q_cnt;
+      const float* col = reinterpret_cast<const float*>(smem + C::kOffCol) + qs * N + gcol;
+      const unsigned long long* mask = reinterpret_cast<const unsigned long long*>(smem + C::kOffMask) + qs * N + gcol;
+      float l[GT], R = 0.0f, inv_r = 0.0f;
+#pragma unroll
+      for (int h = 0; h < GT; ++h) l[h] = 0.0f;
+      if (lane < GT) m[lane] = -INFINITY;
+      __syncwarp();
+      const uint32_t step0 = step;   // of the unit
+      int first_t = -1;              // this group's first step
+      for (int t = w.t0; t < w.t1; ++t) {
+        if (TG == 2 && static_cast<int>(step & 1) != grp) {   // the other group's
+          ++step;
           continue;
         }
-        if (w.t1 <= w.t0) continue;
-        const int qs = q_cnt % kSlots;
-        if (!wait_warp(b_q_full + 8 * qs, (q_cnt / kSlots) & 1, wc, ATTN_DEVERR_WAIT_TIMEOUT_SITE(kSiteQFull))) break;
-        ++q_cnt;
-        const float* col = reinterpret_cast<const float*>(smem + C::kOffCol) + qs * N + gcol;
-        const unsigned long long* mask = reinterpret_cast<const unsigned long long*>(smem + C::kOffMask) + qs * N + gcol;
-        float l[GT], R = 0.0f, inv_r = 0.0f;
+        if (first_t < 0) first_t = t;
+        const int sb = step & 1, ring = step % kRing;   // buffer of S^T and of P^T; stage of the scales
+        if (!wait_warp(b_c_full + 8 * ring, (step / kRing) & 1, wc, ATTN_DEVERR_WAIT_TIMEOUT_SITE(kSiteSFree))) {
+          ok = false;
+          break;
+        }
+        // this thread's key in each tile of the step: its scales, and the columns that see it
+        const float* scales = reinterpret_cast<const float*>(smem + C::kOffScale) + ring * 2 * KS;
+        float ks[kTPS], vs[kTPS];
+        uint32_t v_max = 0;   // bits
+        uint32_t vis[kTPS];
 #pragma unroll
-        for (int h = 0; h < GT; ++h) l[h] = 0.0f;
-        if (lane < GT) m[lane] = -INFINITY;
-        __syncwarp();
-        const uint32_t step0 = step;   // of the unit
-        int first_t = -1;              // this group's first step
-        for (int t = w.t0; t < w.t1; ++t) {
-          if (TG == 2 && static_cast<int>(step & 1) != grp) {   // the other group's
-            ++step;
-            continue;
-          }
-          if (first_t < 0) first_t = t;
-          const int sb = step & 1, ring = step % kRing;   // buffer of S^T and of P^T; stage of the scales
-          if (!wait_warp(b_c_full + 8 * ring, (step / kRing) & 1, wc, ATTN_DEVERR_WAIT_TIMEOUT_SITE(kSiteSFree))) {
-            ok = false;
-            break;
-          }
-          // this thread's key in each tile of the step: its scales, and the columns that see it
-          const float* scales = reinterpret_cast<const float*>(smem + C::kOffScale) + ring * 2 * KS;
-          float ks[kTPS], vs[kTPS];
-          uint32_t v_max = 0;   // bits
-          uint32_t vis[kTPS];
-#pragma unroll
-          for (int y = 0; y < kTPS; ++y) {
-            const int key = t * KS + y * kKeys + lrow, at = key - w.ctx;   // at: place among the new tokens
-            ks[y] = scales[y * kKeys + lrow];
-            vs[y] = scales[KS + y * kKeys + lrow];
-            vis[y] = key < w.n ? 0xffffffffu : 0u;
-            if (key < w.n) {
-              if (vs[y] > 0.0f) v_max = max(v_max, __float_as_uint(vs[y]));   // (not a NaN)
-              if (at >= 0) {
-                uint32_t bits = 0;
+        for (int y = 0; y < kTPS; ++y) {
+          const int key = t * KS + y * kKeys + lrow, at = key - w.ctx;   // at: place among the new tokens
+          ks[y] = scales[y * kKeys + lrow];
+          vs[y] = scales[KS + y * kKeys + lrow];
+          vis[y] = key < w.n ? 0xffffffffu : 0u;
+          if (key < w.n) {
+            if (vs[y] > 0.0f) v_max = max(v_max, __float_as_uint(vs[y]));   // (not a NaN)
+            if (at >= 0) {
+              uint32_t bits = 0;
 #pragma unroll 1
-                for (int h = 0; h < GT; ++h) bits |= static_cast<uint32_t>((mask[h] >> at) & 1) << h;
-                vis[y] = bits;
-              }
+              for (int h = 0; h < GT; ++h) bits |= static_cast<uint32_t>((mask[h] >> at) & 1) << h;
+              vis[y] = bits;
             }
           }
-          if (!wait_warp(b_s_full + 8 * sb, (step >> 1) & 1, wc, ATTN_DEVERR_WAIT_TIMEOUT_SITE(kSiteSFull))) {
-            ok = false;
-            break;
-          }
-          tc_fence_after();
-          const uint32_t t_s = t_lane + sb * kTPS * C::kSCols + gcol;
-          float s[kTPS][LD];   // (the last columns', where there are more)
-          bool all = vis[0] == 0xffffffffu;   // every column sees every key of this warp
-          if constexpr (kTPS == 2) all = all && vis[1] == 0xffffffffu;
-          all = __all_sync(0xffffffffu, all);
+        }
+        if (!wait_warp(b_s_full + 8 * sb, (step >> 1) & 1, wc, ATTN_DEVERR_WAIT_TIMEOUT_SITE(kSiteSFull))) {
+          ok = false;
+          break;
+        }
+        tc_fence_after();
+        const uint32_t t_s = t_lane + sb * kTPS * C::kSCols + gcol;
+        float s[kTPS][LD];   // (the last columns', where there are more)
+        bool all = vis[0] == 0xffffffffu;   // every column sees every key of this warp
+        if constexpr (kTPS == 2) all = all && vis[1] == 0xffffffffu;
+        all = __all_sync(0xffffffffu, all);
 #pragma unroll
-          for (int c = 0; c < NC; ++c) {
-            float x[CH];
+        for (int c = 0; c < NC; ++c) {
+          float x[CH];
+#pragma unroll
+          for (int y = 0; y < kTPS; ++y) {
+            scores(t_s + y * C::kSCols + c * 16, ks[y], all, vis[y] >> (c * CH), s[y]);
+#pragma unroll
+            for (int i = 0; i < CH; ++i) x[i] = y == 0 ? s[y][i] : fmaxf(x[i], s[y][i]);
+          }
+          put_folded(c, fold_columns<CH>(x, lane, [](float a, float b) { return fmaxf(a, b); }));
+        }
+        // (scales are not negative, so their bits are in order)
+        const uint32_t v_top = __reduce_max_sync(0xffffffffu, v_max);
+        if (lane == 0) put(GT, __uint_as_float(v_top));
+        if (!meet()) { ok = false; break; }
+        const float4* got = red + ((red_cnt - 1) & 1) * (GT + 1);
+        auto top4 = [](const float4& v) { return fmaxf(fmaxf(v.x, v.y), fmaxf(v.z, v.w)); };
+        // the values' reference: the power of two above the largest scale so far
+        float rr = 1.0f;
+        {
+          const float top = top4(got[GT]);
+          if (top >= R && top > 0.0f) {
+            const float next = __uint_as_float(min((__float_as_uint(top) >> 23) + 1, 253u) << 23);
+            rr = R * __uint_as_float((254u - (__float_as_uint(next) >> 23)) << 23);
+            R = next;
+            inv_r = __uint_as_float((254u - (__float_as_uint(next) >> 23)) << 23);
+          }
+        }
+        // P^T of these keys into buffer sb, once the P.V that read it two
+        // steps back has completed
+        if (step >= 2 && !pv_wait(step - 2)) { ok = false; break; }
+        float f[kTPS];
+#pragma unroll
+        for (int y = 0; y < kTPS; ++y) f[y] = vs[y] * inv_r;
+        // (no weight of a slot past the last key; a NaN among the scales is dealt with below)
+        bool strange = false;
+#pragma unroll
+        for (int y = 0; y < kTPS; ++y) {
+          if (vis[y] == 0) f[y] = 0.0f;
+          if (!(f[y] <= 4.0f)) {
+            strange = true;
+            f[y] = 0.0f;
+          }
+        }
+        // where P^T of this thread's key lies: row r at (pbuf ^ (r & 7) << 4) + 128 r
+        const uint32_t pbuf = sbase + C::kOffP + sb * C::kP + (lrow >> 6) * C::kPChunk + gcol * 128 +
+                              ((lrow & 63) >> 3 << 4) + 2 * (lrow & 7);
+#pragma unroll
+        for (int c = 0; c < NC; ++c) {
+          if constexpr (NC > 1) {
 #pragma unroll
             for (int y = 0; y < kTPS; ++y) {
               scores(t_s + y * C::kSCols + c * 16, ks[y], all, vis[y] >> (c * CH), s[y]);
-#pragma unroll
-              for (int i = 0; i < CH; ++i) x[i] = y == 0 ? s[y][i] : fmaxf(x[i], s[y][i]);
-            }
-            put_folded(c, fold_columns<CH>(x, lane, [](float a, float b) { return fmaxf(a, b); }));
-          }
-          // (scales are not negative, so their bits are in order)
-          const uint32_t v_top = __reduce_max_sync(0xffffffffu, v_max);
-          if (lane == 0) put(GT, __uint_as_float(v_top));
-          if (!meet()) { ok = false; break; }
-          const float4* got = red + ((red_cnt - 1) & 1) * (GT + 1);
-          auto top4 = [](const float4& v) { return fmaxf(fmaxf(v.x, v.y), fmaxf(v.z, v.w)); };
-          // the values' reference: the power of two above the largest scale so far
-          float rr = 1.0f;
-          {
-            const float top = top4(got[GT]);
-            if (top >= R && top > 0.0f) {
-              const float next = __uint_as_float(min((__float_as_uint(top) >> 23) + 1, 253u) << 23);
-              rr = R * __uint_as_float((254u - (__float_as_uint(next) >> 23)) << 23);
-              R = next;
-              inv_r = __uint_as_float((254u - (__float_as_uint(next) >> 23)) << 23);
             }
           }
-          // P^T of these keys into buffer sb, once the P.V that read it two
-          // steps back has completed
-          if (step >= 2 && !pv_wait(step - 2)) { ok = false; break; }
-          float f[kTPS];
+          // running max (scaled units): rescale only when it grows by more than 2^8
+          // (loads first, and no branches among them: a load behind a condition would
+          // wait for the one before)
+          float mt[CH], old[CH], cs[CH];
 #pragma unroll
-          for (int y = 0; y < kTPS; ++y) f[y] = vs[y] * inv_r;
-          // (no weight of a slot past the last key; a NaN among the scales is dealt with below)
-          bool strange = false;
-#pragma unroll
-          for (int y = 0; y < kTPS; ++y) {
-            if (vis[y] == 0) f[y] = 0.0f;
-            if (!(f[y] <= 4.0f)) {
-              strange = true;
-              f[y] = 0.0f;
-            }
+          for (int i = 0; i < CH; ++i) {
+            mt[i] = top4(got[c * CH + i]);
+            cs[i] = col[c * CH + i];
+            old[i] = m[c * CH + i];
           }
-          // where P^T of this thread's key lies: row r at (pbuf ^ (r & 7) << 4) + 128 r
-          const uint32_t pbuf = sbase + C::kOffP + sb * C::kP + (lrow >> 6) * C::kPChunk + gcol * 128 +
-                                ((lrow & 63) >> 3 << 4) + 2 * (lrow & 7);
+          bool any = rr != 1.0f;
 #pragma unroll
-          for (int c = 0; c < NC; ++c) {
-            if constexpr (NC > 1) {
+          for (int i = 0; i < CH; ++i) {
+            mt[i] *= cs[i];   // (-inf where no column sees a key)
+            // grows past old + 8, or past -inf at all
+            const bool grows = mt[i] > fmaxf(old[i] + 8.0f, -3.0e38f);
+            mt[i] = grows ? mt[i] : old[i];
+            any |= grows;
+          }
+          // m and R are the same in every thread, so the decision is too; the vote
+          // keeps the warp-collective TMEM accesses below uniform regardless.
+          any = __any_sync(0xffffffffu, any);
+          if (any) {
+            float r[16];
 #pragma unroll
-              for (int y = 0; y < kTPS; ++y) {
-                scores(t_s + y * C::kSCols + c * 16, ks[y], all, vis[y] >> (c * CH), s[y]);
-              }
-            }
-            // running max (scaled units): rescale only when it grows by more than 2^8
-            // (loads first, and no branches among them: a load behind a condition would
-            // wait for the one before)
-            float mt[CH], old[CH], cs[CH];
+            for (int i = 0; i < 16; ++i) r[i] = rr;
 #pragma unroll
             for (int i = 0; i < CH; ++i) {
-              mt[i] = top4(got[c * CH + i]);
-              cs[i] = col[c * CH + i];
-              old[i] = m[c * CH + i];
+              const float q = old[i] == mt[i] ? 1.0f : ex2_approx(old[i] - mt[i]);   // (from -inf: 0)
+              l[c * CH + i] *= q;
+              r[i] *= q;
             }
-            bool any = rr != 1.0f;
+            __syncwarp();
 #pragma unroll
-            for (int i = 0; i < CH; ++i) {
-              mt[i] *= cs[i];   // (-inf where no column sees a key)
-              // grows past old + 8, or past -inf at all
-              const bool grows = mt[i] > fmaxf(old[i] + 8.0f, -3.0e38f);
-              mt[i] = grows ? mt[i] : old[i];
-              any |= grows;
-            }
-            // m and R are the same in every thread, so the decision is too; the vote
-            // keeps the warp-collective TMEM accesses below uniform regardless.
-            any = __any_sync(0xffffffffu, any);
-            if (any) {
-              float r[16];
+            for (int i = 0; i < CH; ++i)
+              if (lane == i) m[c * CH + i] = mt[i];
+            __syncwarp();
+            // u^T rescale (rare): needs this group's last P.V complete
+            if (t > first_t) {
+              if (TG == 1 && !pv_wait(step - 1)) { ok = false; break; }
+              tc_fence_after();
+              float o[16];
+              tld<16>(t_u + c * 16, o);
 #pragma unroll
-              for (int i = 0; i < 16; ++i) r[i] = rr;
-#pragma unroll
-              for (int i = 0; i < CH; ++i) {
-                const float q = old[i] == mt[i] ? 1.0f : ex2_approx(old[i] - mt[i]);   // (from -inf: 0)
-                l[c * CH + i] *= q;
-                r[i] *= q;
-              }
-              __syncwarp();
-#pragma unroll
-              for (int i = 0; i < CH; ++i)
-                if (lane == i) m[c * CH + i] = mt[i];
-              __syncwarp();
-              // u^T rescale (rare): needs this group's last P.V complete
-              if (t > first_t) {
-                if (TG == 1 && !pv_wait(step - 1)) { ok = false; break; }
-                tc_fence_after();
-                float o[16];
-                tld<16>(t_u + c * 16, o);
-#pragma unroll
-                for (int i = 0; i < CH; ++i) o[i] *= r[i];
-                tst16(t_u + c * 16, o);
-                tmem_wait_st();
-              }
-            }
-#pragma unroll
-            for (int i = 0; i < CH; ++i) {
-              const int h = c * CH + i;
-              const float mh = fmaxf(mt[i], -3.0e38f) - kPLift;   // (finite)
-#pragma unroll
-              for (int y = 0; y < kTPS; ++y) {
-                const float e = ex2_approx(fmaf(s[y][i], cs[i], -mh));
-                l[h] += e;
-                store_half((pbuf ^ ((h & 7) << 4)) + (y * N + h) * 128, e * f[y]);
-              }
+              for (int i = 0; i < CH; ++i) o[i] *= r[i];
+              tst16(t_u + c * 16, o);
+              tmem_wait_st();
             }
           }
-          if (strange) {
-            // a value's scale that is no number reaches the columns that see its key
+#pragma unroll
+          for (int i = 0; i < CH; ++i) {
+            const int h = c * CH + i;
+            const float mh = fmaxf(mt[i], -3.0e38f) - kPLift;   // (finite)
+#pragma unroll
+            for (int y = 0; y < kTPS; ++y) {
+              const float e = ex2_approx(fmaf(s[y][i], cs[i], -mh));
+              l[h] += e;
+              store_half((pbuf ^ ((h & 7) << 4)) + (y * N + h) * 128, e * f[y]);
+            }
+          }
+        }
+        if (strange) {
+          // a value's scale that is no number reaches the columns that see its key
 #pragma unroll 1
-            for (int i = 0; i < kTPS * GT; ++i) {
-              const int y = i / GT, h = i - y * GT;
-              const float v = y == 0 ? vs[0] : vs[kTPS - 1];
-              const uint32_t seen = y == 0 ? vis[0] : vis[kTPS - 1];
-              if (!(v * inv_r <= 4.0f) && ((seen >> h) & 1))
-                store_half((pbuf ^ ((h & 7) << 4)) + (y * N + h) * 128, __uint_as_float(0x7fffffffu));
-            }
+          for (int i = 0; i < kTPS * GT; ++i) {
+            const int y = i / GT, h = i - y * GT;
+            const float v = y == 0 ? vs[0] : vs[kTPS - 1];
+            const uint32_t seen = y == 0 ? vis[0] : vis[kTPS - 1];
+            if (!(v * inv_r <= 4.0f) && ((seen >> h) & 1))
+              store_half((pbuf ^ ((h & 7) << 4)) + (y * N + h) * 128, __uint_as_float(0x7fffffffu));
           }
-          if (!ok) break;
-          fence_proxy_async_smem();
-          tc_fence_before();
-          __syncwarp();
-          if (lane == 0) mbar_arrive(b_p_full + 8 * sb);
-          ++step;
         }
         if (!ok) break;
-        if (lane == 0) mbar_arrive(b_q_empty + 8 * qs);   // (what it read of the slot: the columns' factors and masks)
-        // the piece's exp-sums over all its keys, then u^T R / l (rolled over the
-        // columns: this code runs once per unit)
-#pragma unroll
-        for (int c = 0; c < NC; ++c) {
-          float v[CH];
-#pragma unroll
-          for (int i = 0; i < CH; ++i) v[i] = l[c * CH + i];
-          put_folded(c, fold_columns<CH>(v, lane, [](float a, float b) { return a + b; }));
-        }
-        if (!meet()) break;
-        const float4* got = red + ((red_cnt - 1) & 1) * (GT + 1);
-        auto sum_of = [&](int h) {
-          const float4 v = got[h];
-          return (v.x + v.y) + (v.z + v.w);
-        };
-        float* fin_m = reinterpret_cast<float*>(smem + C::kOffFin);
-        float* fin_l = fin_m + GT;
-        float* fin_r = fin_l + GT;
-        if (TG == 2 && grp == 1) {
-          // hands its maxima and sums over (of no step: -inf and 0), once the first group
-          // has read those of the unit before
-          if (units_done > 0 &&
-              !wait_warp(b_o_free, (units_done - 1) & 1, wc, ATTN_DEVERR_WAIT_TIMEOUT_SITE(kSiteODone)))
-            break;
-          if (sw == 0) {
-            if (lane < GT) {
-              fin_m[lane] = m[lane];
-              fin_l[lane] = sum_of(lane);
-            }
-            if (lane == 0) *fin_r = R;
-            __syncwarp();
-            if (lane == 0) mbar_arrive(b_fin);
-          }
-          ++units_done;
-          continue;
-        }
-        if (!pv_wait(step - 1)) break;
-        if (TG == 2) {
-          if (step - step0 >= 2 && !pv_wait(step - 2)) break;
-          if (!wait_warp(b_fin, units_done & 1, wc, ATTN_DEVERR_WAIT_TIMEOUT_SITE(kSiteMerge))) break;
-        }
-        tc_fence_after();
-        const bool whole = w.t0 == 0 && w.t1 == w.T;
-        const int slot = 2 * blockIdx.x + (w.t0 == 0 ? 1 : 0);
-        // A column's maximum and sum, and the factors of the groups' u^T over the sum
-        // (0: it has none); a lane per column, left in shared memory for the warp
-        float4* factors = reinterpret_cast<float4*>(smem + C::kOffFactor) + (4 * grp + sw) * GT;
-        if (lane < GT) {
-          float lh = sum_of(lane), mx = m[lane];
-          float w0 = lh != 0.0f ? R : 0.0f, w1 = 0.0f;
-          if constexpr (TG == 2) {
-            const float m1 = fin_m[lane], l1 = fin_l[lane];
-            if (l1 != 0.0f) {
-              const float top = lh != 0.0f ? fmaxf(mx, m1) : m1;
-              const float a = lh != 0.0f ? ex2_approx(mx - top) : 0.0f, b = ex2_approx(m1 - top);
-              w0 *= a;
-              w1 = b * *fin_r;
-              lh = (lh != 0.0f ? lh * a : 0.0f) + l1 * b;
-              mx = top;
-            }
-          }
-          const float inv = lh != 0.0f ? 1.0f / lh : 0.0f;   // 0: saw no key; a NaN stays one
-          factors[lane] = make_float4(mx, lh * kPDrop, w0 * inv, w1 * inv);
-        }
-        __syncwarp();
-        auto joined = [&](int h) {
-          const float4 f = factors[h];
-          float a[1], b[1];
-          tld_start<1>(t_u + h, a);
-          if constexpr (TG == 2) tld_start<1>(t_u + C::kRows + h, b);
-          else b[0] = 0.0f;
-          tld_wait<1>(a, b);
-          return (f.z != 0.0f ? a[0] * f.z : 0.0f) + (f.w != 0.0f ? b[0] * f.w : 0.0f);
-        };
-        // u = u_a + u_b at head dimension 64: lanes 64-127 hand u_b over in the rows of
-        // this group's columns in the first P^T buffer, idle now that every P.V that read
-        // it has completed; this group writes them next after its next meeting
-        auto handed = [&](int h, int i) {
-          return reinterpret_cast<float*>(smem + C::kOffP + (i >> 5) * C::kPChunk + (gcol + h) * 128 + (i & 31) * 4);
-        };
-        if constexpr (kTPS == 2) {
-          if (lrow >= 64) {
-#pragma unroll 1
-            for (int h = 0; h < G; ++h) {
-              *handed(h, lrow - 64) = joined(h);
-            }
-            __syncwarp();
-            if (lane == 0) mbar_arrive(bar_xch);
-          } else {
-            if (!wait_warp(bar_xch, xch_cnt & 1, wc, ATTN_DEVERR_WAIT_TIMEOUT_SITE(kSiteXchg))) break;
-          }
-          ++xch_cnt;
-        }
-        if (kTPS == 1 || lrow < 64) {
-#pragma unroll 1
-          for (int h = 0; h < G; ++h) {
-            float v = joined(h);
-            if constexpr (kTPS == 2) v += *handed(h, lrow);
-            if (whole) {
-              int head;
-              const long long at = (static_cast<long long>(out_row(h, head)) * p.Hq + head) * DA + lrow;
-              p.o[at] = p.fp16 ? __half_as_ushort(__float2half_rn(v)) : __bfloat16_as_ushort(__float2bfloat16_rn(v));
-            } else {
-              p.part_o[(static_cast<size_t>(slot) * N + gcol + h) * DA + lrow] = v;
-            }
-          }
-        }
-        if (sw == 0 && lane < G) {
-          const float mx = factors[lane].x, lh = factors[lane].y;
-          if (whole) {
-            int head;
-            const long long row = out_row(lane, head);
-            p.lse[static_cast<long long>(head) * p.total + row] =
-                (lh != 0.0f) ? mx * 0.69314718055994531f + __logf(lh) : -INFINITY;
-          } else {
-            p.part_ml[slot * N + gcol + lane] = make_float2(mx, lh);
-          }
-        }
+        fence_proxy_async_smem();
         tc_fence_before();
         __syncwarp();
-        if (lane == 0) mbar_arrive(b_o_free);   // u^T may be overwritten by the next unit
-        ++units_done;
-        // the unit's pieces lie on the ranges p / range ... (p + T - 1) / range
-        if (!whole && w.t0 == 0 && tid == 32 * kWarpSoft1)
-          p.rec[blockIdx.x] = make_int4(w.b, w.hc * p.abreast + place,
-                                        static_cast<int>((w.p + w.T - 1) / line.range) - line.range_id + 1, u.cols);
+        if (lane == 0) mbar_arrive(b_p_full + 8 * sb);
+        ++step;
       }
+      if (!ok) break;
+      if (lane == 0) mbar_arrive(b_q_empty + 8 * qs);   // (what it read of the slot: the columns' factors and masks)
+      // the piece's exp-sums over all its keys, then u^T R / l (rolled over the
+      // columns: this code runs once per unit)
+#pragma unroll
+      for (int c = 0; c < NC; ++c) {
+        float v[CH];
+#pragma unroll
+        for (int i = 0; i < CH; ++i) v[i] = l[c * CH + i];
+        put_folded(c, fold_columns<CH>(v, lane, [](float a, float b) { return a + b; }));
+      }
+      if (!meet()) break;
+      const float4* got = red + ((red_cnt - 1) & 1) * (GT + 1);
+      auto sum_of = [&](int h) {
+        const float4 v = got[h];
+        return (v.x + v.y) + (v.z + v.w);
+      };
+      float* fin_m = reinterpret_cast<float*>(smem + C::kOffFin);
+      float* fin_l = fin_m + GT;
+      float* fin_r = fin_l + GT;
+      if (TG == 2 && grp == 1) {
+        // hands its maxima and sums over (of no step: -inf and 0), once the first group
+        // has read those of the unit before
+        if (units_done > 0 &&
+            !wait_warp(b_o_free, (units_done - 1) & 1, wc, ATTN_DEVERR_WAIT_TIMEOUT_SITE(kSiteODone)))
+          break;
+        if (sw == 0) {
+          if (lane < GT) {
+            fin_m[lane] = m[lane];
+            fin_l[lane] = sum_of(lane);
+          }
+          if (lane == 0) *fin_r = R;
+          __syncwarp();
+          if (lane == 0) mbar_arrive(b_fin);
+        }
+        ++units_done;
+        continue;
+      }
+      // The second group's sums first: it has handed over all of its steps then, and seen
+      // the phase of its barrier before each, so that the waits for both groups' last
+      // products below cannot take an earlier phase for theirs
+      if (TG == 2 && !wait_warp(b_fin, units_done & 1, wc, ATTN_DEVERR_WAIT_TIMEOUT_SITE(kSiteMerge))) break;
+      if (!pv_wait(step - 1)) break;
+      if (TG == 2 && step - step0 >= 2 && !pv_wait(step - 2)) break;
+      tc_fence_after();
+      const bool whole = w.t0 == 0 && w.t1 == w.T;
+      const int slot = 2 * blockIdx.x + (w.t0 == 0 ? 1 : 0);
+      // A column's maximum and sum, and the factors of the groups' u^T over the sum
+      // (0: it has none); a lane per column, left in shared memory for the warp
+      float4* factors = reinterpret_cast<float4*>(smem + C::kOffFactor) + (4 * grp + sw) * GT;
+      if (lane < GT) {
+        float lh = sum_of(lane), mx = m[lane];
+        float w0 = lh != 0.0f ? R : 0.0f, w1 = 0.0f;
+        if constexpr (TG == 2) {
+          const float m1 = fin_m[lane], l1 = fin_l[lane];
+          if (l1 != 0.0f) {
+            const float top = lh != 0.0f ? fmaxf(mx, m1) : m1;
+            const float a = lh != 0.0f ? ex2_approx(mx - top) : 0.0f, b = ex2_approx(m1 - top);
+            w0 *= a;
+            w1 = b * *fin_r;
+            lh = (lh != 0.0f ? lh * a : 0.0f) + l1 * b;
+            mx = top;
+          }
+        }
+        const float inv = lh != 0.0f ? 1.0f / lh : 0.0f;   // 0: saw no key; a NaN stays one
+        factors[lane] = make_float4(mx, lh * kPDrop, w0 * inv, w1 * inv);
+      }
+      __syncwarp();
+      auto joined = [&](int h) {
+        const float4 f = factors[h];
+        float a[1], b[1];
+        tld_start<1>(t_u + h, a);
+        if constexpr (TG == 2) tld_start<1>(t_u + C::kRows + h, b);
+        else b[0] = 0.0f;
+        tld_wait<1>(a, b);
+        return (f.z != 0.0f ? a[0] * f.z : 0.0f) + (f.w != 0.0f ? b[0] * f.w : 0.0f);
+      };
+      // u = u_a + u_b at head dimension 64: lanes 64-127 hand u_b over in the rows of
+      // this group's columns in the first P^T buffer, idle now that every P.V that read
+      // it has completed; this group writes them next after its next meeting
+      auto handed = [&](int h, int i) {
+        return reinterpret_cast<float*>(smem + C::kOffP + (i >> 5) * C::kPChunk + (gcol + h) * 128 + (i & 31) * 4);
+      };
+      if constexpr (kTPS == 2) {
+        if (lrow >= 64) {
+#pragma unroll 1
+          for (int h = 0; h < G; ++h) {
+            *handed(h, lrow - 64) = joined(h);
+          }
+          __syncwarp();
+          if (lane == 0) mbar_arrive(bar_xch);
+        } else {
+          if (!wait_warp(bar_xch, xch_cnt & 1, wc, ATTN_DEVERR_WAIT_TIMEOUT_SITE(kSiteXchg))) break;
+        }
+        ++xch_cnt;
+      }
+      if (kTPS == 1 || lrow < 64) {
+#pragma unroll 1
+        for (int h = 0; h < G; ++h) {
+          float v = joined(h);
+          if constexpr (kTPS == 2) v += *handed(h, lrow);
+          if (whole) {
+            int head;
+            const long long at = (static_cast<long long>(out_row(h, head)) * p.Hq + head) * DA + lrow;
+            p.o[at] = p.fp16 ? __half_as_ushort(__float2half_rn(v)) : __bfloat16_as_ushort(__float2bfloat16_rn(v));
+          } else {
+            p.part_o[(static_cast<size_t>(slot) * N + gcol + h) * DA + lrow] = v;
+          }
+        }
+      }
+      if (sw == 0 && lane < G) {
+        const float mx = factors[lane].x, lh = factors[lane].y;
+        if (whole) {
+          int head;
+          const long long row = out_row(lane, head);
+          p.lse[static_cast<long long>(head) * p.total + row] =
+              (lh != 0.0f) ? mx * 0.69314718055994531f + __logf(lh) : -INFINITY;
+        } else {
+          p.part_ml[slot * N + gcol + lane] = make_float2(mx, lh);
+        }
+      }
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(b_o_free);   // u^T may be overwritten by the next unit
+      ++units_done;
+      // the unit's pieces lie on the ranges p / range ... (p + T - 1) / range
+      if (!whole && w.t0 == 0 && tid == 32 * kWarpSoft1)
+        p.rec[blockIdx.x] = make_int4(w.b, w.hc * p.abreast + place,
+                                      static_cast<int>((w.p + w.T - 1) / line.range) - line.range_id + 1, u.cols);
     }
   }
   tc_fence_before();

@@ -400,8 +400,9 @@ __device__ __forceinline__ void produce(const Params& p, Walk w, int place, cons
 }
 
 // Waits until the P.V of this CTA's step i (over all units) has completed: phase i >> 1
-// of pv_done(i & 1).  The next phase, step i + 2's, does not complete before the caller
-// has handed over that step's operand, so the parity tells them apart.
+// of pv_done(i & 1).  Parity tells that phase from its neighbours alone, so step i - 2's
+// has to have been seen to complete (by this warp, or by one that it has waited for), and
+// step i + 2's must not until the caller goes on.
 __device__ __forceinline__ bool wait_pv(uint32_t b_pv_done, uint32_t i, const WaitCtl& wc) {
   return wait_warp(b_pv_done + 8 * (i & 1), (i >> 1) & 1, wc, ATTN_DEVERR_WAIT_TIMEOUT_SITE(kSitePvDone));
 }

@@ -74,37 +74,6 @@ __device__ __forceinline__ float2 turned(unsigned long long turns, long long pos
   return make_float2(c, sn);
 }
 
-// The 16 features of two words.
-template <bool BF16>
-__device__ __forceinline__ void widen(const uint4& a, const uint4& b, float (&x)[16]) {
-  const uint32_t u[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
-#pragma unroll
-  for (int i = 0; i < 8; ++i) {
-    const float2 f = unpack<BF16>(u[i]);
-    x[2 * i] = f.x;
-    x[2 * i + 1] = f.y;
-  }
-}
-template <bool BF16>
-__device__ __forceinline__ void narrow(const float (&x)[16], uint4& a, uint4& b) {
-  a = make_uint4(pack<BF16>(x[0], x[1]), pack<BF16>(x[2], x[3]), pack<BF16>(x[4], x[5]), pack<BF16>(x[6], x[7]));
-  b = make_uint4(pack<BF16>(x[8], x[9]), pack<BF16>(x[10], x[11]), pack<BF16>(x[12], x[13]), pack<BF16>(x[14], x[15]));
-}
-
-// Turns the item's 8 pairs by cs (sign -1: back).  GPT-NeoX: pair i is (x[i],
-// x[8 + i]); GPT-J: (x[2i], x[2i + 1]).
-template <bool GPTJ>
-__device__ __forceinline__ void turn(float (&x)[16], const float2 (&cs)[8], float sign) {
-#pragma unroll
-  for (int i = 0; i < 8; ++i) {
-    float& a = x[GPTJ ? 2 * i : i];
-    float& b = x[GPTJ ? 2 * i + 1 : 8 + i];
-    const float c = cs[i].x, s = cs[i].y * sign, u = a;
-    a = u * c - b * s;
-    b = u * s + b * c;
-  }
-}
-
 // The same, an eighth of a turn from a quarter at the most going through fp32: sine and
 // cosine are off by 2^-25 from the argument instead of 2^-23, as much as by their own
 // rounding (keys that are rounded to 8 bits next keep what the angle gives them).

@@ -71,6 +71,8 @@ def _arguments(q, k, q_weight, k_weight, freqs, positions, axes, eps, amplitude,
     rows = 1
     for n in lead:
         rows *= n
+    if rows >= 1 << 31:
+        raise ValueError("q has 2^31 tokens or more")
     w32, weights = 0, []
     for name, w, x in (("q_weight", q_weight, q), ("k_weight", k_weight, k)):
         if w is None:
