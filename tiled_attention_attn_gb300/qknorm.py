@@ -111,8 +111,7 @@ def _arguments(q, k, q_weight, k_weight, freqs, positions, axes, eps, amplitude,
     sq, sk = _strides(q, "q"), _strides(k, "k") if k is not None else (0, 0)
     args = [*sq, *sk, rows, Hq, Hk, d, q_weight.data_ptr() if q_weight is not None else None,
             k_weight.data_ptr() if k_weight is not None else None, w32, float(eps), rot,
-            f.data_ptr() if f is not None else None, ctypes.cast(table, ctypes.c_void_p) if table is not None else None,
-            n_axes, float(amplitude), int(bool(interleaved)), pos.data_ptr() if pos is not None else None,
+            f.data_ptr() if f is not None else None, table, n_axes, float(amplitude), int(bool(interleaved)), pos.data_ptr() if pos is not None else None,
             int(q.dtype == torch.float16)]
     return args, (f, table)
 
