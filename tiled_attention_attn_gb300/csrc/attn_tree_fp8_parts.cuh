@@ -541,6 +541,13 @@ __device__ __forceinline__ void convert_queries(const Params& p, const Walk& w, 
     }
     return v;
   };
+  // the masks, a lane each, on their way first (a warp has 32 rows at the most)
+  const int my = c0 + lane * dc;
+  unsigned long long my_mask = 0;
+  if (my < u.cols) {
+    const int row = place_of(my);
+    my_mask = p.mask ? static_cast<unsigned long long>(__ldg(p.mask + row)) : (2ull << (row - w.row0)) - 1;
+  }
   uint2 next[F], after[F];
 #pragma unroll
   for (int f = 0; f < F; ++f) next[f] = load(c0 + f * dc);
@@ -577,11 +584,7 @@ __device__ __forceinline__ void convert_queries(const Params& p, const Walk& w, 
       const float up = __uint_as_float(static_cast<uint32_t>(max(127 + k, 1)) << 23);
       const float down = __uint_as_float(static_cast<uint32_t>(min(127 - k, 254)) << 23);
       const int at = c + f * dc;
-      if (lane == 0 && at < u.cols) {
-        const int row = place_of(at);
-        col[at] = fmaxf(p.scale_log2 * down, 0x1p-126f);   // (positive: -inf stays -inf)
-        mask[at] = p.mask ? static_cast<unsigned long long>(__ldg(p.mask + row)) : (2ull << (row - w.row0)) - 1;
-      }
+      if (lane == 0 && at < u.cols) col[at] = fmaxf(p.scale_log2 * down, 0x1p-126f);   // (positive: -inf stays -inf)
 #pragma unroll
       for (int e = 0; e < 4; ++e) x[f][e] = top[f] < 0x7f800000u ? x[f][e] * up : __uint_as_float(0x7fffffffu);
     }
@@ -599,6 +602,7 @@ __device__ __forceinline__ void convert_queries(const Params& p, const Walk& w, 
       }
     }
   }
+  if (my < u.cols) mask[my] = my_mask;
 }
 
 // Joins the pieces of the unit that block x's CTA began, for columns y, y + gridDim.y, ...
