@@ -515,7 +515,7 @@ __device__ __forceinline__ void widen_and_scales(const Params& p, Walk w, int pl
   asm volatile("cp.async.wait_all;" ::: "memory");
 }
 
-// The rows of q that are columns c0, c0 + dc, ... of the unit, as e4m3 pieces (three of
+// The rows of q that are columns c0, c0 + dc, ... of the unit, as e4m3 pieces (two or three of
 // `piece` bytes, rows of DA bytes, swizzled), their factors (scale, log2 e and the power
 // of two, in one) and masks.  A warp takes F rows at a time, the next 2 F on their
 // way, in a loop: it runs once per unit, so fetching its code counts.  (Rows past u.cols
@@ -590,7 +590,7 @@ __device__ __forceinline__ void convert_queries(const Params& p, const Walk& w, 
     }
     uint8_t* to = dst;
 #pragma unroll 1
-    for (int s = 0; s < 3; ++s, to += piece) {
+    for (int s = p.fp16 ? 3 : 2; s > 0; --s, to += piece) {
 #pragma unroll
       for (int f = 0; f < F; ++f) {
         const int at = c + f * dc;

@@ -5,16 +5,19 @@
 // so that a softmax thread owns a row and needs no other thread for its maximum and
 // sum.  (With the columns on N, as in attn_tree_fp8_kernel.cuh, their maxima over the
 // keys are exchanges between threads: eight trees of 64 tokens, 32 heads on 8 of 128,
-// over 16,384 keys took 579 us; 162 us here.)
+// over 16,384 keys took 579 us; 155 us here.)
 //
 // Two groups of four softmax warps take 64 of a step's 128 keys each, with maxima, sums
 // and an accumulator of their own, joined at the unit's end, while S of the next step and
 // P V of the last run.  P overwrites the S that it comes from.  (Taking whole steps in
 // turns, a group waited for the P V and the S that have to follow its P: 220 us against
 // 199 then; with more registers for the softmax warps, so that they hold their 64 values
-// of S, 173; with the scales five steps ahead 162.)  Bound by a step's chain, S to
-// softmax to P V, whose parts overlap over two steps only: the tensor pipe is 31 % busy
-// (its floor for the 64 tokens is 51 us), the schedulers issue in 45 % of their cycles.
+// of S, 173; with the scales five steps ahead 162; with the masks read ahead 158.)  S and
+// P V are issued by a warp each, so that neither waits in the other's queue (155; one
+// warp 158).  Bound by shared memory: a step of 128 keys moves 512 wavefronts of K and Q
+// and 256 of V to the tensor core, 256 from TMA, 384 to widen V and about 870 of the
+// scales (each as 16-byte broadcasts to 32 rows), 2,280 of a step's 2,650 cycles; the
+// tensor pipe is 31 % busy (its floor for the 64 tokens is 51 us).
 // The rest is as in attn_tree_fp8_kernel.cuh: V widened to
 // fp16 by four warps, weights in fp16 times their value's scale over R, R a power of
 // two above the scales so far.
@@ -84,6 +87,7 @@ __global__ void __launch_bounds__(kThreads, 1) tree_rows_kernel(const __grid_con
                          : in(b_p_full, 2) || in(b_q_full, 1) ? 8       // the softmax warps, which convert the queries too
                          : in(b_q_empty, 1)                   ? 1 + 8   // the MMA, the softmax warps
                          : in(b_c_full, kRing)                ? 128     // the copying threads
+                         : in(b_drain, 1)                     ? 2       // the two that issue MMAs
                                                               : 1;
     mbar_init(bar, arrivals);
     fence_mbar_init();
@@ -116,52 +120,30 @@ __global__ void __launch_bounds__(kThreads, 1) tree_rows_kernel(const __grid_con
       widen_and_scales<DA, 1, N, kStages>(p, w, place, smem, C::kOffV, C::kOffW, C::kOffScale, b_v_full, b_v_empty, b_w_full,
                                           b_pv_done, b_c_full, wc);
     } else if (warp == kWarpMMA) {
-      // ------------------------------------------------------------------ MMA issuer
+      // ------------------------------------------------------------------ S's issuer
       if (lane == 0) {
         constexpr uint32_t kIdescS = idesc_e4m3(128, 128);
-        constexpr uint32_t kIdescO = idesc_f16_f32acc(128, DA, false, true);   // B = V read MN-major
         const int pieces = p.fp16 ? 3 : 2;
         const uint64_t dq0 = sdesc_rows<DA>(sbase + C::kOffQ);
         const uint64_t dk0 = sdesc_rows<DA>(sbase + C::kOffK);
-        const uint64_t dv0 = sdesc_sw128(sbase + C::kOffW, T::kWideChunk, 1024);
-        uint32_t k_cnt = 0, pv_cnt = 0, units_done = 0;
+        uint32_t k_cnt = 0, units_done = 0;
         bool ok = true;
         for (bool more = next_unit<KS>(p, w, true); more && ok; more = next_unit<KS>(p, w, false)) {
           const Unit u = unit_of<N>(p, w, place);
           if (w.t1 <= w.t0 || u.cols <= 0) continue;
           if (!wait(b_q_full, units_done & 1, wc, ATTN_DEVERR_WAIT_TIMEOUT_SITE(kSiteQFull))) break;
           tc_fence_after();
-          // u += P V of the next step in line, each group's keys into its accumulator.
-          // Before a unit's first products, which overwrite them, the previous unit's
-          // epilogue must have read both
-          bool first = true;
-          auto do_pv = [&]() -> bool {
-            const int b = pv_cnt & 1;
-            if (!wait(b_w_full + 8 * b, (pv_cnt >> 1) & 1, wc, ATTN_DEVERR_WAIT_TIMEOUT_SITE(kSiteVFull))) return false;
-            if (!wait(b_p_full + 8 * b, (pv_cnt >> 1) & 1, wc, ATTN_DEVERR_WAIT_TIMEOUT_SITE(kSitePFull))) return false;
-            ++pv_cnt;
-            if (first && units_done > 0 &&
-                !wait(b_o_free, (units_done - 1) & 1, wc, ATTN_DEVERR_WAIT_TIMEOUT_SITE(kSiteODone)))
-              return false;
-            tc_fence_after();
-#pragma unroll
-            for (int kk = 0; kk < kKeys / 16; ++kk)
-              umma_ts(tmem + C::kColU + (kk >> 2) * DA, tmem + b * 128 + (kk >> 2) * 64 + (kk & 3) * 8,
-                      dv0 + ((b * T::kWide + kk * 2048) >> 4), kIdescO, (first && (kk & 3) == 0) ? 0u : 1u);
-            first = false;
-            umma_commit(b_pv_done + 8 * b);
-            return true;
-          };
           for (int t = w.t0; t < w.t1; ++t) {
             const int st = k_cnt % kStages, sb = k_cnt & 1;
-            if (!wait(b_k_full + 8 * st, (k_cnt / kStages) & 1, wc, ATTN_DEVERR_WAIT_TIMEOUT_SITE(kSiteKFull))) {
+            // into buffer sb, once the P.V that reads the P there has completed
+            if ((k_cnt >= 2 && !wait(b_pv_done + 8 * sb, ((k_cnt >> 1) - 1) & 1, wc,
+                                     ATTN_DEVERR_WAIT_TIMEOUT_SITE(kSitePvDone))) ||
+                !wait(b_k_full + 8 * st, (k_cnt / kStages) & 1, wc, ATTN_DEVERR_WAIT_TIMEOUT_SITE(kSiteKFull))) {
               ok = false;
               break;
             }
             ++k_cnt;
             tc_fence_after();
-            // S into buffer sb, after the P.V that reads the P there (issued before, and
-            // MMAs run in the order of their issue)
             for (int s = 0; s < pieces; ++s) {
 #pragma unroll
               for (int kk = 0; kk < DA / 32; ++kk)
@@ -170,15 +152,44 @@ __global__ void __launch_bounds__(kThreads, 1) tree_rows_kernel(const __grid_con
             }
             umma_commit(b_s_full + 8 * sb);
             umma_commit(b_k_empty + 8 * st);
-            if (t > w.t0 && !do_pv()) {
+          }
+          if (!ok) break;
+          umma_commit(b_q_empty);
+          ++units_done;
+        }
+        umma_commit(b_drain);
+        mbar_wait(b_drain, 0, wc, ATTN_DEVERR_WAIT_TIMEOUT_SITE(kSiteDrain), false);
+      }
+    } else if (warp == kWarpQ) {
+      // ------------------------------------------------------------------ P V's issuer
+      if (lane == 0) {
+        constexpr uint32_t kIdescO = idesc_f16_f32acc(128, DA, false, true);   // B = V read MN-major
+        const uint64_t dv0 = sdesc_sw128(sbase + C::kOffW, T::kWideChunk, 1024);
+        uint32_t pv_cnt = 0, units_done = 0;
+        bool ok = true;
+        for (bool more = next_unit<KS>(p, w, true); more && ok; more = next_unit<KS>(p, w, false)) {
+          const Unit u = unit_of<N>(p, w, place);
+          if (w.t1 <= w.t0 || u.cols <= 0) continue;
+          // u += P V, each group's keys into its accumulator.  Before a unit's first
+          // products, which overwrite them, the previous unit's epilogue must have read both
+          for (int t = w.t0; t < w.t1; ++t, ++pv_cnt) {
+            const int b = pv_cnt & 1;
+            const bool first = t == w.t0;
+            if (!wait(b_w_full + 8 * b, (pv_cnt >> 1) & 1, wc, ATTN_DEVERR_WAIT_TIMEOUT_SITE(kSiteVFull)) ||
+                !wait(b_p_full + 8 * b, (pv_cnt >> 1) & 1, wc, ATTN_DEVERR_WAIT_TIMEOUT_SITE(kSitePFull)) ||
+                (first && units_done > 0 &&
+                 !wait(b_o_free, (units_done - 1) & 1, wc, ATTN_DEVERR_WAIT_TIMEOUT_SITE(kSiteODone)))) {
               ok = false;
               break;
             }
+            tc_fence_after();
+#pragma unroll
+            for (int kk = 0; kk < kKeys / 16; ++kk)
+              umma_ts(tmem + C::kColU + (kk >> 2) * DA, tmem + b * 128 + (kk >> 2) * 64 + (kk & 3) * 8,
+                      dv0 + ((b * T::kWide + kk * 2048) >> 4), kIdescO, (first && (kk & 3) == 0) ? 0u : 1u);
+            umma_commit(b_pv_done + 8 * b);
           }
           if (!ok) break;
-          // the unit's last step
-          if (!do_pv()) break;
-          umma_commit(b_q_empty);
           ++units_done;
         }
         umma_commit(b_drain);
