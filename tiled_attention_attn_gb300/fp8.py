@@ -17,6 +17,7 @@ from __future__ import annotations
 
 import ctypes
 import math
+import struct
 from typing import Optional, Tuple
 
 import torch
@@ -38,7 +39,7 @@ class _PagedKV8(ctypes.Structure):
 def declare(L) -> None:
     """Argument types of the entry points."""
     vp, i, f, ll = ctypes.c_void_p, ctypes.c_int, ctypes.c_float, ctypes.c_longlong
-    kv = ctypes.POINTER(_PagedKV8)
+    kv = vp   # (a _PagedKV8 by reference, or its bytes)
     L.attn_cache_append_fp8.argtypes = [vp, vp, vp, vp, ll, ll, ll, i, i, i, kv, vp, i, vp, f, i, vp, i, vp]
     L.attn_cache_read_fp8.argtypes = [vp, vp, i, i, kv, vp, vp, i, vp]
     L.attn_tree_fp8.argtypes = [vp, vp, vp, i, i, i, i, kv, vp, vp, f, i, vp, ll, vp]
@@ -48,8 +49,12 @@ def declare(L) -> None:
         getattr(L, n).restype = i
 
 
+# The structure's bytes (quicker than its constructor: the small calls are the host's).
+_pack = struct.Struct("6P6q6i").pack
+
+
 def _cache(k_pages: torch.Tensor, v_pages: torch.Tensor, k_scales: torch.Tensor, v_scales: torch.Tensor,
-           page_table: torch.Tensor, seqlens_k: torch.Tensor) -> _PagedKV8:
+           page_table: torch.Tensor, seqlens_k: torch.Tensor) -> bytes:
     dev, shape, strides = k_pages.device, k_pages.shape, k_pages.stride()
     if k_pages.dtype != torch.float8_e4m3fn or v_pages.dtype != torch.float8_e4m3fn:
         raise TypeError("k_pages and v_pages must be float8_e4m3fn")
@@ -73,9 +78,9 @@ def _cache(k_pages: torch.Tensor, v_pages: torch.Tensor, k_scales: torch.Tensor,
     # strides of an axis of one entry address nothing: any valid value serves
     sp, sh = sp if n > 1 else max(16, d), sh if hkv > 1 else max(16, d)
     cp, ch = cp if n > 1 else 1, ch if hkv > 1 else 1
-    return _PagedKV8(k_pages.data_ptr(), v_pages.data_ptr(), k_scales.data_ptr(), v_scales.data_ptr(),
-                     page_table.data_ptr(), seqlens_k.data_ptr(), sp, st, sh, cp, ct, ch,
-                     page_table.stride(0) if B > 1 else max_pages, max_pages, n, P, hkv, d)
+    return _pack(k_pages.data_ptr(), v_pages.data_ptr(), k_scales.data_ptr(), v_scales.data_ptr(),
+                 page_table.data_ptr(), seqlens_k.data_ptr(), sp, st, sh, cp, ct, ch,
+                 page_table.stride(0) if B > 1 else max_pages, max_pages, n, P, hkv, d)
 
 
 @_placed
@@ -94,7 +99,7 @@ def cache_append_fp8(k: torch.Tensor, v: torch.Tensor, k_pages: torch.Tensor, v_
     c = _cache(k_pages, v_pages, k_scales, v_scales, page_table, seqlens_k)
     dev, B = k_pages.device, page_table.shape[0]
     _check_int(cu_seqlens, "cu_seqlens", dev, (B + 1,))
-    hkv, d = c.num_kv_heads, c.head_dim
+    hkv, d = k_pages.shape[2:]
     if k.dtype not in _HALF:
         raise TypeError("k and v must be bfloat16 or float16")
     total = k.shape[0] if k.dim() == 3 else -1
@@ -125,7 +130,7 @@ def cache_append_fp8(k: torch.Tensor, v: torch.Tensor, k_pages: torch.Tensor, v_
     rc = _attn.lib().attn_cache_append_fp8(
         q.data_ptr() if q is not None else None, k.data_ptr() or None, v.data_ptr() or None,
         q_out.data_ptr() if q is not None else None, *strides, B, q.shape[1] if q is not None else 0, total,
-        ctypes.byref(c), cu_seqlens.data_ptr(), rot, f.data_ptr() if f is not None else None, float(amplitude),
+        c, cu_seqlens.data_ptr(), rot, f.data_ptr() if f is not None else None, float(amplitude),
         int(bool(interleaved)), positions.data_ptr() if positions is not None else None, int(k.dtype == torch.float16),
         s) if total else 0
     _check_rc(rc, "attn_cache_append_fp8")
@@ -153,7 +158,7 @@ def cache_read_fp8(k_pages: torch.Tensor, v_pages: torch.Tensor, k_scales: torch
     if total < 0:
         raise ValueError("total must not be negative")
     s = _stream(dev)
-    shape = (int(total), c.num_kv_heads, c.head_dim)
+    shape = (int(total), *k_pages.shape[2:])
     outs = []
     for name, t in (("k_out", k_out), ("v_out", v_out)):
         if t is None:
@@ -161,7 +166,7 @@ def cache_read_fp8(k_pages: torch.Tensor, v_pages: torch.Tensor, k_scales: torch
         elif t.shape != shape or t.dtype != dtype or t.device != dev or not t.is_contiguous():
             raise ValueError(f"{name} must be a contiguous {dtype} tensor of shape {shape}")
         outs.append(t)
-    rc = _attn.lib().attn_cache_read_fp8(outs[0].data_ptr(), outs[1].data_ptr(), B, int(total), ctypes.byref(c),
+    rc = _attn.lib().attn_cache_read_fp8(outs[0].data_ptr(), outs[1].data_ptr(), B, int(total), c,
                                          cu_seqlens.data_ptr(), starts.data_ptr() if starts is not None else None,
                                          int(dtype == torch.float16), s) if total else 0
     _check_rc(rc, "attn_cache_read_fp8")
@@ -173,10 +178,10 @@ _ws_bytes: dict = {}
 
 def _attend(q, cache, cu_seqlens, tree_mask, max_tokens, scale, out, lse):
     c = _cache(*cache)
-    dev, B = cache[0].device, cache[4].shape[0]
+    dev, B, d = cache[0].device, cache[4].shape[0], cache[0].shape[3]
     if q.dtype not in _HALF:
         raise TypeError("q must be bfloat16 or float16")
-    if q.device != dev or not q.is_contiguous() or q.dim() != 3 or q.shape[2] != c.head_dim:
+    if q.device != dev or not q.is_contiguous() or q.dim() != 3 or q.shape[2] != d:
         raise ValueError("q is a contiguous CUDA tensor (tokens, Hq, d) on the cache's device")
     T = q.shape[0]
     if cu_seqlens is not None:
@@ -189,20 +194,20 @@ def _attend(q, cache, cu_seqlens, tree_mask, max_tokens, scale, out, lse):
     if not 1 <= max_tokens <= 64:
         raise ValueError("max_tokens is between 1 and 64")
     if scale is None:
-        scale = 1.0 / math.sqrt(c.head_dim)
+        scale = 1.0 / math.sqrt(d)
     s = _stream(dev)
     out, lse = _outputs(q, out, lse)
     if T == 0:
         return out, lse
-    n = _ws_bytes.get((dev.index, c.head_dim))
+    n = _ws_bytes.get((dev.index, d))
     if n is None:
-        n = _attn.lib().attn_fp8_workspace_bytes(c.head_dim)
+        n = _attn.lib().attn_fp8_workspace_bytes(d)
         if n < 0:
             raise _attn.AttnError(int(n), "attn_fp8_workspace_bytes")
-        _ws_bytes[(dev.index, c.head_dim)] = n
+        _ws_bytes[(dev.index, d)] = n
     ws = _scratch(dev, s, n)
     rc = _attn.lib().attn_tree_fp8(q.data_ptr(), out.data_ptr(), lse.data_ptr(), B, q.shape[1], T, int(max_tokens),
-                                   ctypes.byref(c), cu_seqlens.data_ptr() if cu_seqlens is not None else None,
+                                   c, cu_seqlens.data_ptr() if cu_seqlens is not None else None,
                                    tree_mask.data_ptr() if tree_mask is not None else None, float(scale),
                                    int(q.dtype == torch.float16), ws.data_ptr(), ws.numel(), s)
     _check_rc(rc, "attn_tree_fp8")

@@ -32,13 +32,15 @@ def declare(L) -> None:
 
 
 @functools.lru_cache(maxsize=64)
-def _axis_array(axes: Tuple[int, ...]):
-    return (ctypes.c_int * len(axes))(*axes)
+def _axis_table(axes: Tuple[int, ...], n_axes: int, pairs: int):
+    if len(axes) != pairs or not all(0 <= a < n_axes for a in axes):
+        raise ValueError(f"axes names one of the {n_axes} axes for each of the {pairs} pairs")
+    return (ctypes.c_int * pairs)(*axes)
 
 
-def _strides(x: torch.Tensor, name: str) -> Tuple[int, int]:
+def _strides(x: torch.Tensor, shape, rows: int, name: str) -> Tuple[int, int]:
     """(token, head) strides of x, (rows, H, d) or (B, L, H, d)."""
-    shape, st = x.shape, x.stride()
+    st = x.stride()
     H, d = shape[-2:]
     if d > 1 and st[-1] != 1:
         raise ValueError(f"the features of {name} must be contiguous")
@@ -50,43 +52,48 @@ def _strides(x: torch.Tensor, name: str) -> Tuple[int, int]:
         token = st[1] if L > 1 else st[0]
     head = st[-2] if H > 1 else d
     # strides of an axis of one entry address nothing: any valid value serves
-    return token if x.numel() > H * d else H * max(head, d), head
+    return token if rows > 1 else H * max(head, d), head
+
+
+def _weight(name: str, w: Optional[torch.Tensor], dtype, dev, d: int) -> Optional[int]:
+    if w is None:
+        return None
+    if w.dtype != dtype and w.dtype != torch.float32:
+        raise TypeError(f"{name} must be float32 or of the tensors' dtype")
+    if w.device != dev or w.shape != (d,) or not w.is_contiguous():
+        raise ValueError(f"{name} must be a contiguous tensor of {d} entries on {dev}")
+    return w.data_ptr()
 
 
 def _arguments(q, k, q_weight, k_weight, freqs, positions, axes, eps, amplitude, interleaved):
     """The arguments that both directions share, as the library takes them from
     the strides on, and what has to stay alive until the call."""
-    if q.dtype not in _HALF or (k is not None and k.dtype != q.dtype):
+    dtype, dev, shape = q.dtype, q.device, q.shape
+    if dtype not in _HALF or (k is not None and k.dtype != dtype):
         raise TypeError("q and k must share one 16-bit dtype")
-    if not q.is_cuda or q.dim() not in (3, 4):
+    if not q.is_cuda or len(shape) not in (3, 4):
         raise ValueError("q is a CUDA tensor (tokens, Hq, d) or (B, L, Hq, d)")
-    dev, lead, (Hq, d) = q.device, q.shape[:-2], q.shape[-2:]
+    lead, (Hq, d) = shape[:-2], shape[-2:]
     if Hq == 0 or d == 0:
         raise ValueError("q has no heads or no features")
-    Hk = 0
-    if k is not None:
-        if k.device != dev or k.dim() != q.dim() or k.shape[:-2] != lead or k.shape[-1] != d or k.shape[-2] == 0:
-            raise ValueError("k is shaped like q but for its heads, on the same device")
-        Hk = k.shape[-2]
-    rows = 1
-    for n in lead:
-        rows *= n
+    rows = lead.numel()
     if rows >= 1 << 31:
         raise ValueError("q has 2^31 tokens or more")
-    w32, weights = 0, []
-    for name, w, x in (("q_weight", q_weight, q), ("k_weight", k_weight, k)):
-        if w is None:
-            continue
-        if x is None:
-            raise ValueError(f"{name} without its heads")
-        if w.dtype not in (q.dtype, torch.float32):
-            raise TypeError(f"{name} must be float32 or of the tensors' dtype")
-        if w.device != dev or w.shape != (d,) or not w.is_contiguous():
-            raise ValueError(f"{name} must be a contiguous tensor of {d} entries on {dev}")
-        w32 = int(w.dtype == torch.float32)
-        weights.append(w.dtype)
-    if len(set(weights)) > 1:
+    sq, sk, Hk = _strides(q, shape, rows, "q"), (0, 0), 0
+    if k is not None:
+        kshape = k.shape
+        if k.device != dev or len(kshape) != len(shape) or kshape[:-2] != lead or kshape[-1] != d or kshape[-2] == 0:
+            raise ValueError("k is shaped like q but for its heads, on the same device")
+        Hk = kshape[-2]
+        sk = _strides(k, kshape, rows, "k")
+    wq = _weight("q_weight", q_weight, dtype, dev, d)
+    if k_weight is not None and k is None:
+        raise ValueError("k_weight without its heads")
+    wk = _weight("k_weight", k_weight, dtype, dev, d)
+    if wq is not None and wk is not None and q_weight.dtype != k_weight.dtype:
         raise TypeError("q_weight and k_weight must share one dtype")
+    w = q_weight if q_weight is not None else k_weight
+    w32 = int(w is not None and w.dtype == torch.float32)
     f, rot, n_axes, table, pos = None, 0, 1, None, None
     if freqs is None:
         if positions is not None or axes is not None:
@@ -95,24 +102,19 @@ def _arguments(q, k, q_weight, k_weight, freqs, positions, axes, eps, amplitude,
         f, rot = _freqs(freqs, d)
         if positions is None:
             raise ValueError("freqs without positions")
+        pshape = positions.shape
         if positions.dtype != torch.int32 or positions.device != dev or not positions.is_contiguous() or \
-                positions.shape[-len(lead):] != lead or positions.dim() not in (len(lead), len(lead) + 1):
+                (pshape != lead and pshape[1:] != lead):
             raise ValueError("positions must be a contiguous int32 tensor of q's leading shape, or (axes, ...) of it")
-        pos = positions
-        if positions.dim() > len(lead):
-            n_axes = positions.shape[0]
+        pos = positions.data_ptr()
+        if len(pshape) > len(lead):
+            n_axes = pshape[0]
         if axes is not None:
-            axes = tuple(int(a) for a in axes)
-            if len(axes) != rot // 2 or not all(0 <= a < n_axes for a in axes):
-                raise ValueError(f"axes names one of the {n_axes} axes for each of the {rot // 2} pairs")
-            table = _axis_array(axes)
+            table = _axis_table(tuple(map(int, axes)), n_axes, rot // 2)
         elif n_axes != 1:
             raise ValueError("positions of several axes need axes")
-    sq, sk = _strides(q, "q"), _strides(k, "k") if k is not None else (0, 0)
-    args = [*sq, *sk, rows, Hq, Hk, d, q_weight.data_ptr() if q_weight is not None else None,
-            k_weight.data_ptr() if k_weight is not None else None, w32, float(eps), rot,
-            f.data_ptr() if f is not None else None, table, n_axes, float(amplitude), int(bool(interleaved)), pos.data_ptr() if pos is not None else None,
-            int(q.dtype == torch.float16)]
+    args = (*sq, *sk, rows, Hq, Hk, d, wq, wk, w32, float(eps), rot, f.data_ptr() if f is not None else None, table, n_axes,
+            float(amplitude), int(bool(interleaved)), pos, int(dtype == torch.float16))
     return args, (f, table)
 
 
@@ -122,7 +124,7 @@ def _output(x, out, name):
             raise ValueError(f"{name} without k")
         return None
     if out is None:
-        return torch.empty(x.shape, dtype=x.dtype, device=x.device)
+        return torch.empty_like(x, memory_format=torch.contiguous_format)
     if out.shape != x.shape or out.dtype != x.dtype or out.device != x.device or not out.is_contiguous():
         raise ValueError(f"{name} must be a contiguous tensor of its input's shape and dtype")
     return out
