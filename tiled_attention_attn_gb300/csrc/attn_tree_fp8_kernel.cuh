@@ -191,10 +191,10 @@ __global__ void __launch_bounds__(kThreads, 1) tree_kernel(const __grid_constant
       if (lane == 0) {
         const uint32_t idesc_s = idesc_e4m3(kKeys, N * (p.fp16 ? 3 : 2));
         constexpr uint32_t kIdescO = idesc_f16_f32acc(128, C::kRows, false, false) | (1u << 15);   // A = V read MN-major
-        const uint64_t dq0 = sdesc_rows<DA>(sbase + C::kOffQ);
-        const uint64_t dk0 = sdesc_rows<DA>(sbase + C::kOffK);
-        const uint64_t dv0 = sdesc_sw128(sbase + C::kOffW, kWideChunk, 1024);
-        const uint64_t dp0 = sdesc_sw128(sbase + C::kOffP, 16, 1024);
+        const uint32_t dq0 = desc_low(sbase + C::kOffQ, 16);
+        const uint32_t dk0 = desc_low(sbase + C::kOffK, 16);
+        const uint32_t dv0 = desc_low(sbase + C::kOffW, kWideChunk);
+        const uint32_t dp0 = desc_low(sbase + C::kOffP, 16);
         const uint32_t t_u = tmem + C::kColU;   // u^T columns
         uint32_t q_cnt = 0, k_cnt = 0, pv_cnt = 0, units_done = 0;
         bool ok = true;
@@ -220,9 +220,9 @@ __global__ void __launch_bounds__(kThreads, 1) tree_kernel(const __grid_constant
             tc_fence_after();
 #pragma unroll
             for (int kk = 0; kk < kKeys / 16; ++kk) {
-              const uint64_t a = dv0 + ((b * kWide + kk * 2048) >> 4);
-              const uint64_t x = dp0 + ((b * C::kP + (kk >> 2) * C::kPChunk + (kk & 3) * 32) >> 4);
-              umma_ss(t_u + (TG == 2 ? b * C::kRows : 0), a, x, kIdescO, (first && kk == 0) ? 0u : 1u);
+              const uint32_t a = dv0 + ((b * kWide + kk * 2048) >> 4);
+              const uint32_t x = dp0 + ((b * C::kP + (kk >> 2) * C::kPChunk + (kk & 3) * 32) >> 4);
+              mma_f16(t_u + (TG == 2 ? b * C::kRows : 0), a, x, kIdescO, (first && kk == 0) ? 0u : 1u);
             }
             umma_commit(b_pv_done + 8 * b);
             return true;
@@ -238,9 +238,9 @@ __global__ void __launch_bounds__(kThreads, 1) tree_kernel(const __grid_constant
             for (int x = 0; x < nt; ++x) {
 #pragma unroll
               for (int kk = 0; kk < DA / 32; ++kk) {
-                const uint64_t a = dk0 + ((st * kRaw + x * (kKeys * DA) + kk * 32) >> 4);
-                const uint64_t b = dq0 + ((qs * C::kQ + kk * 32) >> 4);
-                umma_ss_f8(tmem + (sb * kTPS + x) * C::kSCols, a, b, idesc_s, kk > 0 ? 1u : 0u);
+                const uint32_t a = dk0 + ((st * kRaw + x * (kKeys * DA) + kk * 32) >> 4);
+                const uint32_t b = dq0 + ((qs * C::kQ + kk * 32) >> 4);
+                mma_f8<kHighRows<DA>>(tmem + (sb * kTPS + x) * C::kSCols, a, b, idesc_s, kk > 0 ? 1u : 0u);
               }
             }
             umma_commit(b_s_full + 8 * sb);

@@ -129,22 +129,42 @@ __device__ __forceinline__ uint32_t swizzled(int row, int at) {
   return static_cast<uint32_t>(row * ROW + ((((at >> 4) ^ x) << 4) | (at & 15)));
 }
 
-// Shared-memory matrix descriptor of a K-major tile of e4m3 rows of ROW bytes: as
-// sdesc_sw128, with the swizzle mode of the row's width (2: 128 bytes, 4: 64).
-template <int ROW>
-__device__ __forceinline__ uint64_t sdesc_rows(uint32_t saddr) {
-  const uint64_t d = sdesc_sw128(saddr, 16, 8 * ROW);
-  return ROW == 128 ? d : (d & ~(7ull << 61)) | (4ull << 61);
+// The halves of a shared-memory matrix descriptor (sdesc_sw128): the lower has the
+// address and the leading byte offset, the upper is a constant, the stride byte offset
+// and the swizzle mode (2: 128 bytes, 4: 64).
+__device__ __forceinline__ uint32_t desc_low(uint32_t saddr, uint32_t lbo_bytes) {
+  return (saddr & 0x3FFFFu) >> 4 | lbo_bytes >> 4 << 16;
 }
+constexpr uint32_t desc_high(uint32_t sbo_bytes, uint32_t mode) { return sbo_bytes >> 4 | 1u << 14 | mode << 29; }
+constexpr uint32_t kHigh = desc_high(1024, 2);   // rows of 128 bytes
+template <int ROW>
+constexpr uint32_t kHighRows = ROW == 128 ? kHigh : desc_high(8 * ROW, 4);   // K-major e4m3 rows of ROW bytes
 
-// D[tmem] (+)= A[smem] * B[smem]^T, 8-bit operands, fp32 accumulation.
-__device__ __forceinline__ void umma_ss_f8(uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc, uint32_t idesc,
-                                           uint32_t accumulate) {
+// The MMAs by the descriptors' lower halves.  D[tmem] (+)= A[smem] * B[smem]^T, 8-bit
+// operands; the same, 16-bit; A in tensor memory, 16-bit.  fp32 accumulation.
+template <uint32_t H>
+__device__ __forceinline__ void mma_f8(uint32_t d_tmem, uint32_t a, uint32_t b, uint32_t idesc, uint32_t accumulate) {
   asm volatile(
-      "{\n\t.reg .pred p;\n\t"
-      "setp.ne.b32 p, %4, 0;\n\t"
-      "tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], %1, %2, %3, p;\n\t}"
-      :: "r"(d_tmem), "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(accumulate)
+      "{\n\t.reg .pred p;\n\t.reg .b64 x, y;\n\t"
+      "setp.ne.b32 p, %4, 0;\n\tmov.b64 x, {%1, %5};\n\tmov.b64 y, {%2, %5};\n\t"
+      "tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], x, y, %3, p;\n\t}"
+      :: "r"(d_tmem), "r"(a), "r"(b), "r"(idesc), "r"(accumulate), "n"(H)
+      : "memory");
+}
+__device__ __forceinline__ void mma_f16(uint32_t d_tmem, uint32_t a, uint32_t b, uint32_t idesc, uint32_t accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t.reg .b64 x, y;\n\t"
+      "setp.ne.b32 p, %4, 0;\n\tmov.b64 x, {%1, %5};\n\tmov.b64 y, {%2, %5};\n\t"
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], x, y, %3, p;\n\t}"
+      :: "r"(d_tmem), "r"(a), "r"(b), "r"(idesc), "r"(accumulate), "n"(kHigh)
+      : "memory");
+}
+__device__ __forceinline__ void mma_f16_ts(uint32_t d_tmem, uint32_t a_tmem, uint32_t b, uint32_t idesc, uint32_t accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t.reg .b64 y;\n\t"
+      "setp.ne.b32 p, %4, 0;\n\tmov.b64 y, {%2, %5};\n\t"
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], y, %3, p;\n\t}"
+      :: "r"(d_tmem), "r"(a_tmem), "r"(b), "r"(idesc), "r"(accumulate), "n"(kHigh)
       : "memory");
 }
 // kind::f8f6f4, e4m3 operands, both K-major.

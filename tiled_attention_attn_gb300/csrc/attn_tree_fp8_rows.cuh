@@ -124,8 +124,8 @@ __global__ void __launch_bounds__(kThreads, 1) tree_rows_kernel(const __grid_con
       if (lane == 0) {
         constexpr uint32_t kIdescS = idesc_e4m3(128, 128);
         const int pieces = p.fp16 ? 3 : 2;
-        const uint64_t dq0 = sdesc_rows<DA>(sbase + C::kOffQ);
-        const uint64_t dk0 = sdesc_rows<DA>(sbase + C::kOffK);
+        const uint32_t dq0 = desc_low(sbase + C::kOffQ, 16);
+        const uint32_t dk0 = desc_low(sbase + C::kOffK, 16);
         uint32_t k_cnt = 0, units_done = 0;
         bool ok = true;
         for (bool more = next_unit<KS>(p, w, true); more && ok; more = next_unit<KS>(p, w, false)) {
@@ -147,7 +147,7 @@ __global__ void __launch_bounds__(kThreads, 1) tree_rows_kernel(const __grid_con
             for (int s = 0; s < pieces; ++s) {
 #pragma unroll
               for (int kk = 0; kk < DA / 32; ++kk)
-                umma_ss_f8(tmem + sb * 128, dq0 + ((s * C::kQPiece + kk * 32) >> 4), dk0 + ((st * T::kRaw + kk * 32) >> 4),
+                mma_f8<kHighRows<DA>>(tmem + sb * 128, dq0 + ((s * C::kQPiece + kk * 32) >> 4), dk0 + ((st * T::kRaw + kk * 32) >> 4),
                            kIdescS, (s > 0 || kk > 0) ? 1u : 0u);
             }
             umma_commit(b_s_full + 8 * sb);
@@ -164,7 +164,7 @@ __global__ void __launch_bounds__(kThreads, 1) tree_rows_kernel(const __grid_con
       // ------------------------------------------------------------------ P V's issuer
       if (lane == 0) {
         constexpr uint32_t kIdescO = idesc_f16_f32acc(128, DA, false, true);   // B = V read MN-major
-        const uint64_t dv0 = sdesc_sw128(sbase + C::kOffW, T::kWideChunk, 1024);
+        const uint32_t dv0 = desc_low(sbase + C::kOffW, T::kWideChunk);
         uint32_t pv_cnt = 0, units_done = 0;
         bool ok = true;
         for (bool more = next_unit<KS>(p, w, true); more && ok; more = next_unit<KS>(p, w, false)) {
@@ -185,7 +185,7 @@ __global__ void __launch_bounds__(kThreads, 1) tree_rows_kernel(const __grid_con
             tc_fence_after();
 #pragma unroll
             for (int kk = 0; kk < kKeys / 16; ++kk)
-              umma_ts(tmem + C::kColU + (kk >> 2) * DA, tmem + b * 128 + (kk >> 2) * 64 + (kk & 3) * 8,
+              mma_f16_ts(tmem + C::kColU + (kk >> 2) * DA, tmem + b * 128 + (kk >> 2) * 64 + (kk & 3) * 8,
                       dv0 + ((b * T::kWide + kk * 2048) >> 4), kIdescO, (first && (kk & 3) == 0) ? 0u : 1u);
             umma_commit(b_pv_done + 8 * b);
           }
