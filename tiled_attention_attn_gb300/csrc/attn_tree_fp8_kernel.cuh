@@ -105,7 +105,7 @@ __global__ void __launch_bounds__(kThreads, 1) tree_kernel(const __grid_constant
   extern __shared__ __align__(1024) uint8_t smem_raw[];
   // (by an offset, not through an integer: the accesses stay ones of shared memory)
   uint8_t* smem = smem_raw + ((1024 - (smem_u32(smem_raw) & 1023)) & 1023);
-  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int tid = threadIdx.x, warp = uniform(tid >> 5), lane = tid & 31;
   const uint32_t sbase = smem_u32(smem);
   uint32_t bar_at = sbase + C::kOffBar;
   auto take = [&](int n) { const uint32_t a = bar_at; bar_at += 8 * n; return a; };
@@ -160,6 +160,7 @@ __global__ void __launch_bounds__(kThreads, 1) tree_kernel(const __grid_constant
 
   if (!softmax) {
     regs_dec<kRegsFew>();
+    auto any = [](bool x) { return __any_sync(0xffffffffu, x) != 0; };   // (uniform to the compiler too)
     if (warp == kWarpK) {
       produce<DA, kTPS, N, kStages>(p, w, place, &p.tm_k, sbase + C::kOffK, b_k_full, b_k_empty, wc);
     } else if (warp == kWarpV) {
@@ -188,77 +189,89 @@ __global__ void __launch_bounds__(kThreads, 1) tree_kernel(const __grid_constant
       }
     } else if (warp == kWarpMMA) {
       // ------------------------------------------------------------------ MMA issuer
-      if (lane == 0) {
-        const uint32_t idesc_s = idesc_e4m3(kKeys, N * (p.fp16 ? 3 : 2));
-        constexpr uint32_t kIdescO = idesc_f16_f32acc(128, C::kRows, false, false) | (1u << 15);   // A = V read MN-major
-        const uint32_t dq0 = desc_low(sbase + C::kOffQ, 16);
-        const uint32_t dk0 = desc_low(sbase + C::kOffK, 16);
-        const uint32_t dv0 = desc_low(sbase + C::kOffW, kWideChunk);
-        const uint32_t dp0 = desc_low(sbase + C::kOffP, 16);
-        const uint32_t t_u = tmem + C::kColU;   // u^T columns
-        uint32_t q_cnt = 0, k_cnt = 0, pv_cnt = 0, units_done = 0;
-        bool ok = true;
-        for (bool more = next_unit<KS>(p, w, true); more && ok; more = next_unit<KS>(p, w, false)) {
-          const Unit u = unit_of<N>(p, w, place);
-          if (w.t1 <= w.t0 || u.cols <= 0) continue;
-          const int qs = q_cnt % kSlots;
-          if (!wait(b_q_full + 8 * qs, (q_cnt / kSlots) & 1, wc, ATTN_DEVERR_WAIT_TIMEOUT_SITE(kSiteQFull))) break;
-          ++q_cnt;
+      const uint32_t idesc_s = idesc_e4m3(kKeys, N * (p.fp16 ? 3 : 2));
+      constexpr uint32_t kIdescO = idesc_f16_f32acc(128, C::kRows, false, false) | (1u << 15);   // A = V read MN-major
+      const uint32_t dq0 = desc_low(sbase + C::kOffQ, 16);
+      const uint32_t dk0 = desc_low(sbase + C::kOffK, 16);
+      const uint32_t dv0 = desc_low(sbase + C::kOffW, kWideChunk);
+      const uint32_t dp0 = desc_low(sbase + C::kOffP, 16);
+      const uint32_t t_u = tmem + C::kColU;   // u^T columns
+      uint32_t q_cnt = 0, k_cnt = 0, pv_cnt = 0, units_done = 0;
+      bool ok = true;
+      for (bool more = any(next_unit<KS>(p, w, true)); more && ok; more = any(next_unit<KS>(p, w, false))) {
+        const Unit u = unit_of<N>(p, w, place);
+        if (w.t1 <= w.t0 || u.cols <= 0) continue;
+        const int qs = q_cnt % kSlots;
+        if (!wait_warp(b_q_full + 8 * qs, (q_cnt / kSlots) & 1, wc, ATTN_DEVERR_WAIT_TIMEOUT_SITE(kSiteQFull))) break;
+        ++q_cnt;
+        tc_fence_after();
+        // u^T += V^T P^T of the next step in line.  Before a unit's first products,
+        // which overwrite u^T, the previous unit's epilogue must have read it
+        int pv_unit = 0;
+        auto do_pv = [&]() -> bool {
+          const bool first = pv_unit++ < TG;
+          const int b = pv_cnt & 1;
+          if (!wait_warp(b_w_full + 8 * b, (pv_cnt >> 1) & 1, wc, ATTN_DEVERR_WAIT_TIMEOUT_SITE(kSiteVFull))) return false;
+          if (!wait_warp(b_p_full + 8 * b, (pv_cnt >> 1) & 1, wc, ATTN_DEVERR_WAIT_TIMEOUT_SITE(kSitePFull))) return false;
+          ++pv_cnt;
+          if (pv_unit == 1 && units_done > 0 &&
+              !wait_warp(b_o_free, (units_done - 1) & 1, wc, ATTN_DEVERR_WAIT_TIMEOUT_SITE(kSiteODone)))
+            return false;
           tc_fence_after();
-          // u^T += V^T P^T of the next step in line.  Before a unit's first products,
-          // which overwrite u^T, the previous unit's epilogue must have read it
-          int pv_unit = 0;
-          auto do_pv = [&]() -> bool {
-            const bool first = pv_unit++ < TG;
-            const int b = pv_cnt & 1;
-            if (!wait(b_w_full + 8 * b, (pv_cnt >> 1) & 1, wc, ATTN_DEVERR_WAIT_TIMEOUT_SITE(kSiteVFull))) return false;
-            if (!wait(b_p_full + 8 * b, (pv_cnt >> 1) & 1, wc, ATTN_DEVERR_WAIT_TIMEOUT_SITE(kSitePFull))) return false;
-            ++pv_cnt;
-            if (pv_unit == 1 && units_done > 0 &&
-                !wait(b_o_free, (units_done - 1) & 1, wc, ATTN_DEVERR_WAIT_TIMEOUT_SITE(kSiteODone)))
-              return false;
-            tc_fence_after();
+          const uint32_t tu = uniform(t_u + (TG == 2 ? b * C::kRows : 0)), a0 = uniform(dv0 + (b * kWide >> 4));
+          const uint32_t b0 = uniform(dp0 + (b * C::kP >> 4)), done = uniform(b_pv_done + 8 * b);
+          const uint32_t more_of_it = uniform(first ? 0u : 1u);
+          if (elect_one()) {
 #pragma unroll
-            for (int kk = 0; kk < kKeys / 16; ++kk) {
-              const uint32_t a = dv0 + ((b * kWide + kk * 2048) >> 4);
-              const uint32_t x = dp0 + ((b * C::kP + (kk >> 2) * C::kPChunk + (kk & 3) * 32) >> 4);
-              mma_f16(t_u + (TG == 2 ? b * C::kRows : 0), a, x, kIdescO, (first && kk == 0) ? 0u : 1u);
-            }
-            umma_commit(b_pv_done + 8 * b);
-            return true;
-          };
-          // S^T of a step's tiles into its buffer, whose last contents were consumed:
-          // this thread has waited for that step's P
-          auto issue_s = [&](int t) -> bool {
-            const int st = k_cnt % kStages, sb = k_cnt & 1;
-            const int nt = kTPS == 1 ? 1 : (w.n - t * KS > kKeys ? 2 : 1);
-            if (!wait(b_k_full + 8 * st, (k_cnt / kStages) & 1, wc, ATTN_DEVERR_WAIT_TIMEOUT_SITE(kSiteKFull))) return false;
-            ++k_cnt;
-            tc_fence_after();
-            for (int x = 0; x < nt; ++x) {
-#pragma unroll
-              for (int kk = 0; kk < DA / 32; ++kk) {
-                const uint32_t a = dk0 + ((st * kRaw + x * (kKeys * DA) + kk * 32) >> 4);
-                const uint32_t b = dq0 + ((qs * C::kQ + kk * 32) >> 4);
-                mma_f8<kHighRows<DA>>(tmem + (sb * kTPS + x) * C::kSCols, a, b, idesc_s, kk > 0 ? 1u : 0u);
-              }
-            }
-            umma_commit(b_s_full + 8 * sb);
-            umma_commit(b_k_empty + 8 * st);
-            return true;
-          };
-          // S^T of a step goes before P.V of the one before it
-          for (int t = w.t0; t <= w.t1 && ok; ++t) {
-            if (t < w.t1) ok = issue_s(t);
-            if (ok && t > w.t0) ok = do_pv();
+            for (int kk = 0; kk < kKeys / 16; ++kk)
+              mma_f16(tu, a0 + (kk * 2048 >> 4), b0 + (((kk >> 2) * C::kPChunk + (kk & 3) * 32) >> 4), kIdescO,
+                      kk == 0 ? more_of_it : 1u);
+            umma_commit(done);
           }
-          if (!ok) break;
-          umma_commit(b_q_empty + 8 * qs);
-          ++units_done;
+          __syncwarp();
+          return true;
+        };
+        // S^T of a step's tiles into its buffer, whose last contents were consumed:
+        // this warp has waited for that step's P
+        auto issue_s = [&](int t) -> bool {
+          const int st = k_cnt % kStages, sb = k_cnt & 1;
+          const int nt = kTPS == 1 ? 1 : (w.n - t * KS > kKeys ? 2 : 1);
+          if (!wait_warp(b_k_full + 8 * st, (k_cnt / kStages) & 1, wc, ATTN_DEVERR_WAIT_TIMEOUT_SITE(kSiteKFull))) return false;
+          ++k_cnt;
+          tc_fence_after();
+          const uint32_t ts = uniform(tmem + sb * kTPS * C::kSCols), a0 = uniform(dk0 + (st * kRaw >> 4));
+          const uint32_t b0 = uniform(dq0 + (qs * C::kQ >> 4));
+          const uint32_t full = uniform(b_s_full + 8 * sb), empty = uniform(b_k_empty + 8 * st);
+          if (elect_one()) {
+#pragma unroll
+            for (int x = 0; x < kTPS; ++x) {
+              if (x >= nt) break;
+#pragma unroll
+              for (int kk = 0; kk < DA / 32; ++kk)
+                mma_f8<kHighRows<DA>>(ts + x * C::kSCols, a0 + ((x * (kKeys * DA) + kk * 32) >> 4), b0 + 2 * kk, idesc_s,
+                                      kk > 0 ? 1u : 0u);
+            }
+            umma_commit(full);
+            umma_commit(empty);
+          }
+          __syncwarp();
+          return true;
+        };
+        // S^T of a step goes before P.V of the one before it
+        for (int t = w.t0; t <= w.t1 && ok; ++t) {
+          if (t < w.t1) ok = issue_s(t);
+          if (ok && t > w.t0) ok = do_pv();
         }
+        if (!ok) break;
+        if (elect_one()) umma_commit(b_q_empty + 8 * qs);
+        __syncwarp();
+        ++units_done;
+      }
+      if (elect_one()) {
         umma_commit(b_drain);
         mbar_wait(b_drain, 0, wc, ATTN_DEVERR_WAIT_TIMEOUT_SITE(kSiteDrain), false);
       }
+      __syncwarp();
     }
   } else {
     regs_inc<kRegsMany>();

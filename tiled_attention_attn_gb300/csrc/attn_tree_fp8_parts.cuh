@@ -167,6 +167,15 @@ __device__ __forceinline__ void mma_f16_ts(uint32_t d_tmem, uint32_t a_tmem, uin
       :: "r"(d_tmem), "r"(a_tmem), "r"(b), "r"(idesc), "r"(accumulate), "n"(kHigh)
       : "memory");
 }
+// What lane 0 has, uniform over the warp to the compiler too: the MMAs take their operands
+// from uniform registers, and moving each of them there from a thread's is what an issuing
+// thread spends most of its time on.  The warps that issue MMAs run with all their lanes.
+__device__ __forceinline__ uint32_t uniform(uint32_t x) { return __shfl_sync(0xffffffffu, x, 0); }
+__device__ __forceinline__ bool elect_one() {
+  uint32_t on;
+  asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(on));
+  return on != 0;
+}
 // kind::f8f6f4, e4m3 operands, both K-major.
 __host__ __device__ constexpr uint32_t idesc_e4m3(int M, int N) {
   return (1u << 4) | (static_cast<uint32_t>(N >> 3) << 17) | (static_cast<uint32_t>(M >> 4) << 24);

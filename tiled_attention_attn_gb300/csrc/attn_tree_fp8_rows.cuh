@@ -60,7 +60,7 @@ __global__ void __launch_bounds__(kThreads, 1) tree_rows_kernel(const __grid_con
   extern __shared__ __align__(1024) uint8_t smem_raw[];
   // (by an offset, not through an integer: the accesses stay ones of shared memory)
   uint8_t* smem = smem_raw + ((1024 - (smem_u32(smem_raw) & 1023)) & 1023);
-  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int tid = threadIdx.x, warp = uniform(tid >> 5), lane = tid & 31;
   const uint32_t sbase = smem_u32(smem);
   uint32_t bar_at = sbase + C::kOffBar;
   auto take = [&](int n) { const uint32_t a = bar_at; bar_at += 8 * n; return a; };
@@ -112,6 +112,7 @@ __global__ void __launch_bounds__(kThreads, 1) tree_rows_kernel(const __grid_con
 
   if (!softmax) {
     regs_dec<kRegsFew>();
+    auto any = [](bool x) { return __any_sync(0xffffffffu, x) != 0; };   // (uniform to the compiler too)
     if (warp == kWarpK) {
       produce<DA, 1, N, kStages>(p, w, place, &p.tm_k, sbase + C::kOffK, b_k_full, b_k_empty, wc);
     } else if (warp == kWarpV) {
@@ -121,80 +122,95 @@ __global__ void __launch_bounds__(kThreads, 1) tree_rows_kernel(const __grid_con
                                           b_pv_done, b_c_full, wc);
     } else if (warp == kWarpMMA) {
       // ------------------------------------------------------------------ S's issuer
-      if (lane == 0) {
-        constexpr uint32_t kIdescS = idesc_e4m3(128, 128);
-        const int pieces = p.fp16 ? 3 : 2;
-        const uint32_t dq0 = desc_low(sbase + C::kOffQ, 16);
-        const uint32_t dk0 = desc_low(sbase + C::kOffK, 16);
-        uint32_t k_cnt = 0, units_done = 0;
-        bool ok = true;
-        for (bool more = next_unit<KS>(p, w, true); more && ok; more = next_unit<KS>(p, w, false)) {
-          const Unit u = unit_of<N>(p, w, place);
-          if (w.t1 <= w.t0 || u.cols <= 0) continue;
-          if (!wait(b_q_full, units_done & 1, wc, ATTN_DEVERR_WAIT_TIMEOUT_SITE(kSiteQFull))) break;
+      constexpr uint32_t kIdescS = idesc_e4m3(128, 128);
+      const uint32_t dq0 = desc_low(sbase + C::kOffQ, 16);
+      const uint32_t dk0 = desc_low(sbase + C::kOffK, 16);
+      uint32_t k_cnt = 0, units_done = 0;
+      bool ok = true;
+      for (bool more = any(next_unit<KS>(p, w, true)); more && ok; more = any(next_unit<KS>(p, w, false))) {
+        const Unit u = unit_of<N>(p, w, place);
+        if (w.t1 <= w.t0 || u.cols <= 0) continue;
+        if (!wait_warp(b_q_full, units_done & 1, wc, ATTN_DEVERR_WAIT_TIMEOUT_SITE(kSiteQFull))) break;
+        tc_fence_after();
+        for (int t = w.t0; t < w.t1; ++t) {
+          const int st = k_cnt % kStages, sb = k_cnt & 1;
+          // into buffer sb, once the P.V that reads the P there has completed
+          if ((k_cnt >= 2 && !wait_warp(b_pv_done + 8 * sb, ((k_cnt >> 1) - 1) & 1, wc,
+                                   ATTN_DEVERR_WAIT_TIMEOUT_SITE(kSitePvDone))) ||
+              !wait_warp(b_k_full + 8 * st, (k_cnt / kStages) & 1, wc, ATTN_DEVERR_WAIT_TIMEOUT_SITE(kSiteKFull))) {
+            ok = false;
+            break;
+          }
+          ++k_cnt;
           tc_fence_after();
-          for (int t = w.t0; t < w.t1; ++t) {
-            const int st = k_cnt % kStages, sb = k_cnt & 1;
-            // into buffer sb, once the P.V that reads the P there has completed
-            if ((k_cnt >= 2 && !wait(b_pv_done + 8 * sb, ((k_cnt >> 1) - 1) & 1, wc,
-                                     ATTN_DEVERR_WAIT_TIMEOUT_SITE(kSitePvDone))) ||
-                !wait(b_k_full + 8 * st, (k_cnt / kStages) & 1, wc, ATTN_DEVERR_WAIT_TIMEOUT_SITE(kSiteKFull))) {
-              ok = false;
-              break;
-            }
-            ++k_cnt;
-            tc_fence_after();
-            for (int s = 0; s < pieces; ++s) {
+          const uint32_t tm = uniform(tmem + sb * 128), a0 = uniform(dq0), b0 = uniform(dk0 + (st * T::kRaw >> 4));
+          const uint32_t full = uniform(b_s_full + 8 * sb), empty = uniform(b_k_empty + 8 * st);
+          if (elect_one()) {
+#pragma unroll
+            for (int s = 0; s < 3; ++s) {
+              if (s == 2 && !p.fp16) break;
 #pragma unroll
               for (int kk = 0; kk < DA / 32; ++kk)
-                mma_f8<kHighRows<DA>>(tmem + sb * 128, dq0 + ((s * C::kQPiece + kk * 32) >> 4), dk0 + ((st * T::kRaw + kk * 32) >> 4),
-                           kIdescS, (s > 0 || kk > 0) ? 1u : 0u);
+                mma_f8<kHighRows<DA>>(tm, a0 + ((s * C::kQPiece + kk * 32) >> 4), b0 + 2 * kk, kIdescS,
+                                      (s > 0 || kk > 0) ? 1u : 0u);
             }
-            umma_commit(b_s_full + 8 * sb);
-            umma_commit(b_k_empty + 8 * st);
+            umma_commit(full);
+            umma_commit(empty);
           }
-          if (!ok) break;
-          umma_commit(b_q_empty);
-          ++units_done;
+          __syncwarp();
         }
+        if (!ok) break;
+        if (elect_one()) umma_commit(b_q_empty);
+        __syncwarp();
+        ++units_done;
+      }
+      if (elect_one()) {
         umma_commit(b_drain);
         mbar_wait(b_drain, 0, wc, ATTN_DEVERR_WAIT_TIMEOUT_SITE(kSiteDrain), false);
       }
+      __syncwarp();
     } else if (warp == kWarpQ) {
       // ------------------------------------------------------------------ P V's issuer
-      if (lane == 0) {
-        constexpr uint32_t kIdescO = idesc_f16_f32acc(128, DA, false, true);   // B = V read MN-major
-        const uint32_t dv0 = desc_low(sbase + C::kOffW, T::kWideChunk);
-        uint32_t pv_cnt = 0, units_done = 0;
-        bool ok = true;
-        for (bool more = next_unit<KS>(p, w, true); more && ok; more = next_unit<KS>(p, w, false)) {
-          const Unit u = unit_of<N>(p, w, place);
-          if (w.t1 <= w.t0 || u.cols <= 0) continue;
-          // u += P V, each group's keys into its accumulator.  Before a unit's first
-          // products, which overwrite them, the previous unit's epilogue must have read both
-          for (int t = w.t0; t < w.t1; ++t, ++pv_cnt) {
-            const int b = pv_cnt & 1;
-            const bool first = t == w.t0;
-            if (!wait(b_w_full + 8 * b, (pv_cnt >> 1) & 1, wc, ATTN_DEVERR_WAIT_TIMEOUT_SITE(kSiteVFull)) ||
-                !wait(b_p_full + 8 * b, (pv_cnt >> 1) & 1, wc, ATTN_DEVERR_WAIT_TIMEOUT_SITE(kSitePFull)) ||
-                (first && units_done > 0 &&
-                 !wait(b_o_free, (units_done - 1) & 1, wc, ATTN_DEVERR_WAIT_TIMEOUT_SITE(kSiteODone)))) {
-              ok = false;
-              break;
-            }
-            tc_fence_after();
+      constexpr uint32_t kIdescO = idesc_f16_f32acc(128, DA, false, true);   // B = V read MN-major
+      const uint32_t dv0 = desc_low(sbase + C::kOffW, T::kWideChunk);
+      uint32_t pv_cnt = 0, units_done = 0;
+      bool ok = true;
+      for (bool more = any(next_unit<KS>(p, w, true)); more && ok; more = any(next_unit<KS>(p, w, false))) {
+        const Unit u = unit_of<N>(p, w, place);
+        if (w.t1 <= w.t0 || u.cols <= 0) continue;
+        // u += P V, each group's keys into its accumulator.  Before a unit's first
+        // products, which overwrite them, the previous unit's epilogue must have read both
+        for (int t = w.t0; t < w.t1; ++t, ++pv_cnt) {
+          const int b = pv_cnt & 1;
+          const bool first = t == w.t0;
+          if (!wait_warp(b_w_full + 8 * b, (pv_cnt >> 1) & 1, wc, ATTN_DEVERR_WAIT_TIMEOUT_SITE(kSiteVFull)) ||
+              !wait_warp(b_p_full + 8 * b, (pv_cnt >> 1) & 1, wc, ATTN_DEVERR_WAIT_TIMEOUT_SITE(kSitePFull)) ||
+              (first && units_done > 0 &&
+               !wait_warp(b_o_free, (units_done - 1) & 1, wc, ATTN_DEVERR_WAIT_TIMEOUT_SITE(kSiteODone)))) {
+            ok = false;
+            break;
+          }
+          tc_fence_after();
+          const uint32_t tm = uniform(tmem), ta = uniform(tmem + b * 128), b0 = uniform(dv0 + (b * T::kWide >> 4));
+          const uint32_t done = uniform(b_pv_done + 8 * b);
+          const uint32_t more_of_it = uniform(first ? 0u : 1u);
+          if (elect_one()) {
 #pragma unroll
             for (int kk = 0; kk < kKeys / 16; ++kk)
-              mma_f16_ts(tmem + C::kColU + (kk >> 2) * DA, tmem + b * 128 + (kk >> 2) * 64 + (kk & 3) * 8,
-                      dv0 + ((b * T::kWide + kk * 2048) >> 4), kIdescO, (first && (kk & 3) == 0) ? 0u : 1u);
-            umma_commit(b_pv_done + 8 * b);
+              mma_f16_ts(tm + C::kColU + (kk >> 2) * DA, ta + (kk >> 2) * 64 + (kk & 3) * 8, b0 + (kk * 2048 >> 4), kIdescO,
+                         (kk & 3) == 0 ? more_of_it : 1u);
+            umma_commit(done);
           }
-          if (!ok) break;
-          ++units_done;
+          __syncwarp();
         }
+        if (!ok) break;
+        ++units_done;
+      }
+      if (elect_one()) {
         umma_commit(b_drain);
         mbar_wait(b_drain, 0, wc, ATTN_DEVERR_WAIT_TIMEOUT_SITE(kSiteDrain), false);
       }
+      __syncwarp();
     }
   } else {
     regs_inc<kRegsMany>();
