@@ -133,7 +133,7 @@ __global__ void __launch_bounds__(kThreads, 1) tree_kernel(const __grid_constant
     const int arrivals = in(b_v_empty, kStages) || in(b_w_full, 2) || in(b_red, 2) ? 4   // the warps that widen; a group
                          : in(b_q_empty, 2)                          ? 1 + 8     // the MMA, the softmax warps
                          : in(b_p_full, 2) || in(b_o_free, 1)        ? 4 * SG    // the softmax warps of a step; those that read u^T
-                         : in(b_c_full, kRing)                       ? 128       // the copying threads
+                         : in(b_c_full, kRing)                       ? 64        // the copying threads
                          : in(b_xch, 2)                              ? 2
                                                                      : 1;
     mbar_init(bar, arrivals);
@@ -162,12 +162,13 @@ __global__ void __launch_bounds__(kThreads, 1) tree_kernel(const __grid_constant
     regs_dec<kRegsFew>();
     auto any = [](bool x) { return __any_sync(0xffffffffu, x) != 0; };   // (uniform to the compiler too)
     if (warp == kWarpK) {
-      produce<DA, kTPS, N, kStages>(p, w, place, &p.tm_k, sbase + C::kOffK, b_k_full, b_k_empty, wc);
+      produce<DA, kTPS, N, kStages>(p, w, place, &p.tm_k, sbase + C::kOffK, b_k_full, b_k_empty, p.c.ks,
+                                   sbase + C::kOffScale, b_c_full, wc);
     } else if (warp == kWarpV) {
-      produce<DA, kTPS, N, kStages>(p, w, place, &p.tm_v, sbase + C::kOffV, b_v_full, b_v_empty, wc);
+      produce<DA, kTPS, N, kStages>(p, w, place, &p.tm_v, sbase + C::kOffV, b_v_full, b_v_empty, p.c.vs,
+                                   sbase + C::kOffScale + KS * 4, b_c_full, wc);
     } else if (warp >= kWarpWiden && warp < kWarpWiden + 4) {
-      widen_and_scales<DA, kTPS, N, kStages>(p, w, place, smem, C::kOffV, C::kOffW, C::kOffScale, b_v_full, b_v_empty,
-                                             b_w_full, b_pv_done, b_c_full, wc);
+      widen<DA, kTPS, N, kStages>(p, w, place, smem, C::kOffV, C::kOffW, b_v_full, b_v_empty, b_w_full, b_pv_done, wc);
     } else if (warp == kWarpQ) {
       // ------------------------------------------------------------------ queries
       uint32_t cnt = 0;

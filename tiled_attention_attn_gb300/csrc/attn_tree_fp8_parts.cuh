@@ -1,6 +1,6 @@
 // What the two kernels of the attention over caches of 8-bit floating point share
 // (attn_tree_fp8_kernel.cuh, attn_tree_fp8_rows.cuh): the walk over the work, the
-// producers of K and V, the warps that widen V and bring the scales, the queries'
+// producers of K, V and their scales, the warps that widen V, the queries'
 // e4m3 pieces, and the join of a cut unit's pieces.
 #pragma once
 #include <cuda_bf16.h>
@@ -380,12 +380,18 @@ __device__ __forceinline__ Walk enter_line(const Params& p, const Line& line, in
 }
 
 // A warp that loads K, or V, of every step: stages of kRaw bytes from `stages` on, a
-// box per page and tile.
+// box per page and tile; and the keys' or the values' scales, KS floats a step at
+// `to_scales` + 2 KS (step % kRing), by 4-byte asynchronous copies.  (The scales' ring
+// needs no barrier for its empty stages: a stage of K or V is empty kStages steps later,
+// once S, or the widening, of that step is through, which P of the step two before it
+// goes ahead of; and kStages + 2 < kRing.)
 template <int DA, int TPS, int N, int kStages>
 __device__ __forceinline__ void produce(const Params& p, Walk w, int place, const CUtensorMap* map, uint32_t stages,
-                                        uint32_t b_full, uint32_t b_empty, const WaitCtl& wc) {
+                                        uint32_t b_full, uint32_t b_empty, const float* scales, uint32_t to_scales,
+                                        uint32_t b_c_full, const WaitCtl& wc) {
   using T = Tiles<DA, TPS>;
-  constexpr int KS = T::KS;
+  constexpr int KS = T::KS, L = KS / 32;   // scales per lane: of keys 32 i + lane
+  static_assert(kStages + 2 < kRing, "the scales' ring");
   const int lane = threadIdx.x & 31;
   uint32_t cnt = 0;
   const int box = min(1 << p.c.t.page_log2, kKeys);   // tokens per box
@@ -400,7 +406,13 @@ __device__ __forceinline__ void produce(const Params& p, Walk w, int place, cons
   for (bool more = next_unit<KS>(p, w, true); more && ok; more = next_unit<KS>(p, w, false)) {
     const Unit u = unit_of<N>(p, w, place);
     if (w.t1 <= w.t0 || u.cols <= 0) continue;
-    int entry = box_entry(w.t0);
+    const float* head = scales + u.g * p.c.c_head;
+    int entry = box_entry(w.t0), of_key[L];
+    auto key_entries = [&](int t) {
+#pragma unroll
+      for (int i = 0; i < L; ++i) of_key[i] = entry_of(p, w, t * KS + 32 * i + lane);
+    };
+    key_entries(w.t0);
     for (int t = w.t0; t < w.t1; ++t) {
       const int st = cnt % kStages;
       const int next = t + 1 < w.t1 ? box_entry(t + 1) : -1;
@@ -415,10 +427,20 @@ __device__ __forceinline__ void produce(const Params& p, Walk w, int place, cons
       if (page >= 0)
         tma_load_4d(dst0 + st * T::kRaw, map, b_full + 8 * st, 0, u.g, (t * KS + key_off) & ((1 << p.c.t.page_log2) - 1),
                     page);
+      const uint32_t ring = cnt % kRing, dst = to_scales + ring * (2 * KS * 4) + lane * 4;
+#pragma unroll
+      for (int i = 0; i < L; ++i) {
+        const int key = t * KS + 32 * i + lane;
+        if (key < w.n && static_cast<unsigned>(of_key[i]) < static_cast<unsigned>(p.c.t.num_pages))   // (a box has reported other pages)
+          copy4(dst + 32 * i * 4, head + of_key[i] * p.c.c_page + (key & ((1 << p.c.t.page_log2) - 1)) * p.c.c_token);
+      }
+      copies_arrive(b_c_full + 8 * ring);
+      if (t + 1 < w.t1) key_entries(t + 1);
       entry = next;
       ++cnt;
     }
   }
+  asm volatile("cp.async.wait_all;" ::: "memory");
   if (lane == 0 && *wc.abort_flag) {
     // let the loads already issued land before the CTA exits
     for (int s = 0; s < kStages; ++s) {
@@ -436,13 +458,11 @@ __device__ __forceinline__ bool wait_pv(uint32_t b_pv_done, uint32_t i, const Wa
   return wait_warp(b_pv_done + 8 * (i & 1), (i >> 1) & 1, wc, ATTN_DEVERR_WAIT_TIMEOUT_SITE(kSitePvDone));
 }
 
-// Four warps that widen V of every step to fp16 (two buffers at off_wide) and bring the
-// scales ([kRing][k, v][KS] floats at off_scale).
+// Four warps that widen V of every step to fp16 (two buffers at off_wide).
 template <int DA, int TPS, int N, int kStages>
-__device__ __forceinline__ void widen_and_scales(const Params& p, Walk w, int place, uint8_t* smem, int off_raw,
-                                                 int off_wide, int off_scale, uint32_t b_v_full, uint32_t b_v_empty,
-                                                 uint32_t b_w_full, uint32_t b_pv_done, uint32_t b_c_full,
-                                                 const WaitCtl& wc) {
+__device__ __forceinline__ void widen(const Params& p, Walk w, int place, uint8_t* smem, int off_raw, int off_wide,
+                                      uint32_t b_v_full, uint32_t b_v_empty, uint32_t b_w_full, uint32_t b_pv_done,
+                                      const WaitCtl& wc) {
   using T = Tiles<DA, TPS>;
   constexpr int KS = T::KS, kItems = KS * DA / 16 / 128;   // of 16 features, per thread
   const int me = threadIdx.x - 32 * kWarpWiden, lane = threadIdx.x & 31;
@@ -454,51 +474,6 @@ __device__ __forceinline__ void widen_and_scales(const Params& p, Walk w, int pl
   const int c = DA == 128 ? 4 * ((me >> 3) & 1) + (me & 3) : me & 3;
   const uint32_t from = DA == 128 ? swizzled<128>(row, 16 * c) : row * 64 + 16 * c;
   const uint32_t to = (DA == 128 ? (c >> 2) * T::kWideChunk : 0) + row * 128 + ((2 * (c & 3) ^ (row & 7)) << 4);   // (the second word: bit 4 flipped)
-  // The scales are copied kAhead steps ahead, over the units' ends: a walk of their own,
-  // whose table entries are read a step before that.  Key 128 i + me of the step.  Their
-  // ring needs no barrier for its empty stages: what the stage of step i + kAhead held was
-  // of a step up to i - 2, whose P.V has completed when this is reached.
-  constexpr int kAhead = kRing - 3;
-  const uint32_t sbase = smem_u32(smem);
-  Walk wa = w;
-  Unit ua = {};
-  int ta = 0, entry[TPS];
-  bool on = true;
-  uint32_t copied = 0;
-  auto settle = [&](bool first) {
-    do {
-      on = next_unit<KS>(p, wa, first);
-      first = false;
-      if (!on) return;
-      ua = unit_of<N>(p, wa, place);
-    } while (wa.t1 <= wa.t0 || ua.cols <= 0);
-    ta = wa.t0;
-  };
-  auto entries = [&]() {
-#pragma unroll
-    for (int i = 0; i < TPS; ++i) entry[i] = on ? entry_of(p, wa, ta * KS + kKeys * i + me) : -1;
-  };
-  auto copy_scales = [&]() {
-    if (!on) return;
-    const uint32_t dst = sbase + off_scale + (copied % kRing) * (2 * KS * 4) + me * 4;
-#pragma unroll
-    for (int i = 0; i < TPS; ++i) {
-      const int key = ta * KS + kKeys * i + me, page = page_of(p, wa, entry[i], key);
-      if (page < 0 || page == p.c.t.num_pages) continue;
-      const int slot = key & ((1 << p.c.t.page_log2) - 1);
-      const long long at = page * p.c.c_page + slot * p.c.c_token + ua.g * p.c.c_head;
-      copy4(dst + kKeys * i * 4, p.c.ks + at);
-      copy4(dst + (KS + kKeys * i) * 4, p.c.vs + at);
-    }
-    copies_arrive(b_c_full + 8 * (copied % kRing));
-    ++copied;
-    if (++ta == wa.t1) settle(false);
-    entries();
-  };
-  settle(true);
-  entries();
-#pragma unroll 1
-  for (int i = 0; i < kAhead; ++i) copy_scales();
   uint32_t step = 0;
   bool ok = true;
   for (bool more = next_unit<KS>(p, w, true); more && ok; more = next_unit<KS>(p, w, false)) {
@@ -537,11 +512,9 @@ __device__ __forceinline__ void widen_and_scales(const Params& p, Walk w, int pl
         mbar_arrive(b_v_empty + 8 * st);
         mbar_arrive(b_w_full + 8 * (step & 1));
       }
-      copy_scales();
       ++step;
     }
   }
-  asm volatile("cp.async.wait_all;" ::: "memory");
 }
 
 // The rows of q that are columns c0, c0 + dc, ... of the unit, as e4m3 pieces (two or three of

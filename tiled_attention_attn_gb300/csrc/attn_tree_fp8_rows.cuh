@@ -86,7 +86,7 @@ __global__ void __launch_bounds__(kThreads, 1) tree_rows_kernel(const __grid_con
     const int arrivals = in(b_v_empty, kStages) || in(b_w_full, 2) || in(b_o_free, 1) || in(b_fin, 1) ? 4   // the warps that widen; a group
                          : in(b_p_full, 2) || in(b_q_full, 1) ? 8       // the softmax warps, which convert the queries too
                          : in(b_q_empty, 1)                   ? 1 + 8   // the MMA, the softmax warps
-                         : in(b_c_full, kRing)                ? 128     // the copying threads
+                         : in(b_c_full, kRing)                ? 64      // the copying threads
                          : in(b_drain, 1)                     ? 2       // the two that issue MMAs
                                                               : 1;
     mbar_init(bar, arrivals);
@@ -114,12 +114,13 @@ __global__ void __launch_bounds__(kThreads, 1) tree_rows_kernel(const __grid_con
     regs_dec<kRegsFew>();
     auto any = [](bool x) { return __any_sync(0xffffffffu, x) != 0; };   // (uniform to the compiler too)
     if (warp == kWarpK) {
-      produce<DA, 1, N, kStages>(p, w, place, &p.tm_k, sbase + C::kOffK, b_k_full, b_k_empty, wc);
+      produce<DA, 1, N, kStages>(p, w, place, &p.tm_k, sbase + C::kOffK, b_k_full, b_k_empty, p.c.ks,
+                                sbase + C::kOffScale, b_c_full, wc);
     } else if (warp == kWarpV) {
-      produce<DA, 1, N, kStages>(p, w, place, &p.tm_v, sbase + C::kOffV, b_v_full, b_v_empty, wc);
+      produce<DA, 1, N, kStages>(p, w, place, &p.tm_v, sbase + C::kOffV, b_v_full, b_v_empty, p.c.vs,
+                                sbase + C::kOffScale + KS * 4, b_c_full, wc);
     } else if (warp >= kWarpWiden && warp < kWarpWiden + 4) {
-      widen_and_scales<DA, 1, N, kStages>(p, w, place, smem, C::kOffV, C::kOffW, C::kOffScale, b_v_full, b_v_empty, b_w_full,
-                                          b_pv_done, b_c_full, wc);
+      widen<DA, 1, N, kStages>(p, w, place, smem, C::kOffV, C::kOffW, b_v_full, b_v_empty, b_w_full, b_pv_done, wc);
     } else if (warp == kWarpMMA) {
       // ------------------------------------------------------------------ S's issuer
       constexpr uint32_t kIdescS = idesc_e4m3(128, 128);
