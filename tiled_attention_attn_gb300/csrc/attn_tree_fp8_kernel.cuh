@@ -25,20 +25,22 @@
 //
 // Bound by HBM: per key and head d bytes of K and of V, and 8 of scales.  TMA
 // stages of 16 KB of K and 16 of V (three or four), per page one box per tile; the
-// warps that widen V bring the scales with 4-byte asynchronous copies, five steps
-// ahead.  The queries' pieces are further columns of S^T, whose parts the softmax
-// adds: at these widths the number of products counts, not their columns (a product per
-// piece, and all softmax warps on one step: 120 us for 32 caches of ~3,550 keys, 32
-// heads on 8 of 128).  Measured (device time, merge included): those caches
-// 60.7 us, of which the 236 MB take 35 at the copy rate; one of 131,072 keys 62.5 of
-// 41; the line itself runs at 5.1 to 5.9 TB/s, what is left is 7 us to the first S
-// (prologue, the walk, the queries' conversion), the epilogue and 3 to 4.5 of the merge.
+// warps that load them bring the scales too, with 4-byte asynchronous copies.  The
+// queries' pieces are further columns of S^T, whose parts the softmax adds: at these
+// widths the number of products counts, not their columns (a product per piece, and all
+// softmax warps on one step: 120 us for 32 caches of ~3,550 keys, 32 heads on 8 of
+// 128).  So does what it takes to issue one: with the operands in one thread's registers
+// about 85 cycles each, whatever their size, and 61 us for those caches; uniform over the
+// warp (see uniform()) 55.  Measured (device time, merge included): those caches 55.6 us,
+// of which the 236 MB take 35 at the copy rate; one of 131,072 keys 55.3 of 41, its line
+// of steps at 6.6 TB/s.  What is left is the start (4 us to the first S: prologue, the
+// walk, the queries' conversion), the epilogue and 3 to 4 of the merge.
 //
 // Work is cut as in the 16-bit decode kernel: the steps of all (sequence, unit) on
 // one line, equal ranges per CTA, pieces of a cut unit joined by tree_merge_kernel.
 // A unit has up to 32 columns; more are the rows of attn_tree_fp8_rows.cuh (48
 // columns as two units here, each reading the keys, took 83 us where that kernel
-// took 53).
+// took 53, then).
 //
 // Slots past a sequence's last key may hold anything: their scores are dropped by
 // index, their V is zeroed as it is widened.

@@ -18,8 +18,9 @@
 namespace attn {
 namespace tree {
 
-// Warps: K's TMA, the MMA, V's TMA and the queries; four of softmax; four that widen V;
-// four more of softmax.
+// Warps: the loads of K, the MMAs, the loads of V, and the queries (in the kernel with
+// rows the MMAs of S, and those of P V); four of softmax; four that widen V; four more of
+// softmax.
 constexpr int kWarpK = 0, kWarpMMA = 1, kWarpV = 2, kWarpQ = 3, kWarpSoft1 = 4, kWarpWiden = 8, kWarpSoft2 = 12;
 constexpr int kThreads = 512;
 // Registers: of the launch's 4 x 128 a thread per warpgroup, the softmax warps take what

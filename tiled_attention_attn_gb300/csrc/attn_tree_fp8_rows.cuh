@@ -5,19 +5,18 @@
 // so that a softmax thread owns a row and needs no other thread for its maximum and
 // sum.  (With the columns on N, as in attn_tree_fp8_kernel.cuh, their maxima over the
 // keys are exchanges between threads: eight trees of 64 tokens, 32 heads on 8 of 128,
-// over 16,384 keys took 579 us; 155 us here.)
+// over 16,384 keys took 579 us; 138 us here.)
 //
 // Two groups of four softmax warps take 64 of a step's 128 keys each, with maxima, sums
 // and an accumulator of their own, joined at the unit's end, while S of the next step and
 // P V of the last run.  P overwrites the S that it comes from.  (Taking whole steps in
 // turns, a group waited for the P V and the S that have to follow its P: 220 us against
 // 199 then; with more registers for the softmax warps, so that they hold their 64 values
-// of S, 173; with the scales five steps ahead 162; with the masks read ahead 158.)  S and
-// P V are issued by a warp each, so that neither waits in the other's queue (155; one
-// warp 158).  Bound by shared memory: a step of 128 keys moves 512 wavefronts of K and Q
-// and 256 of V to the tensor core, 256 from TMA, 384 to widen V and about 870 of the
-// scales (each as 16-byte broadcasts to 32 rows), 2,280 of a step's 2,650 cycles; the
-// tensor pipe is 31 % busy (its floor for the 64 tokens is 51 us).
+// of S, 173; with the scales further ahead 162, the masks read ahead 158.)  S and P V are
+// issued by a warp each, so that neither waits in the other's queue (155), from uniform
+// operands (143); with the scales copied by the loading warps 138.  Bound by the softmax
+// warps: a step takes 2,200 cycles, of which a group is at work for 1,500 to 2,100; the
+// tensor pipe is 37 % busy (its floor for the 64 tokens is 51 us).
 // The rest is as in attn_tree_fp8_kernel.cuh: V widened to
 // fp16 by four warps, weights in fp16 times their value's scale over R, R a power of
 // two above the scales so far.
