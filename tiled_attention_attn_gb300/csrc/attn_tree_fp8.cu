@@ -84,9 +84,10 @@ int attn_tree_fp8(const void* q, void* o, float* lse, int B, int Hq, int total, 
   p.total = total;
   p.max_tokens = cu_seqlens_or_null ? max_tokens : 1;
   p.group = Hq / p.c.t.hkv;
-  // Up to 32 columns (token, head) of a key/value head are a unit of the kernel that has
+  // Up to 8 columns (token, head) of a key/value head are a unit of the kernel that has
   // them as columns; more are rows, 128 to a unit, and the units of a head each read the
-  // keys.
+  // keys.  (8 sequences of 1,000 to 16,384 keys, 8 heads of 128: 8 columns 44.5 us against
+  // 60 as rows, 16 columns 63 against 60.6; 16 sequences of 4 heads, 32 columns 60 against 36.)
   const long long cols = static_cast<long long>(p.max_tokens) * p.group;
   if (cols > (1 << 20)) return ATTN_EINVAL;
   const bool rows = cols > tree::kMostCols;

@@ -10,7 +10,7 @@ namespace attn {
 namespace tree {
 
 constexpr int kKeys = 128;     // keys per tile
-constexpr int kMostCols = 32;      // columns (token, head) of a unit of attn_tree_fp8_kernel.cuh
+constexpr int kMostCols = 8;       // columns (token, head) of a unit of attn_tree_fp8_kernel.cuh
 constexpr int kRowsPerUnit = 128;  // and of attn_tree_fp8_rows.cuh, which has them as rows
 constexpr int kMinSteps = 4;   // pieces of a cut unit are at least about this long
 

@@ -38,9 +38,7 @@
 //
 // Work is cut as in the 16-bit decode kernel: the steps of all (sequence, unit) on
 // one line, equal ranges per CTA, pieces of a cut unit joined by tree_merge_kernel.
-// A unit has up to 32 columns; more are the rows of attn_tree_fp8_rows.cuh (48
-// columns as two units here, each reading the keys, took 83 us where that kernel
-// took 53, then).
+// A unit has up to 8 columns; more are the rows of attn_tree_fp8_rows.cuh.
 //
 // Slots past a sequence's last key may hold anything: their scores are dropped by
 // index, their V is zeroed as it is widened.
@@ -57,20 +55,19 @@ constexpr int kRaw = kKeys * 128;       // a stage of K, or of V, in bytes
 constexpr int kWide = 2 * kRaw;         // a step's V in fp16: two chunks of 128-byte rows
 constexpr int kWideChunk = kRaw;
 
-// Two groups of four softmax warps, GT columns each: of 32 columns (SG = 2) each takes
-// half; up to 16 columns (SG = 1, TG = 2) they take turns, step by step, with maxima,
+// GT columns.  Two groups of four softmax warps take turns, step by step, with maxima,
 // sums and accumulators of their own that are joined at the unit's end (one group's
 // chain of waits is longer than a step takes to arrive).  Two buffers of S^T, so that a
 // group meets every phase of its buffer's barriers: with three it would see every
 // second, which parity cannot tell from the one before.
-template <int GT_, int SG_, int DA>
+template <int GT_, int DA>
 struct Cfg {
-  static constexpr int GT = GT_, SG = SG_, TG = 3 - SG;
-  static constexpr int N = GT * SG < 16 ? 16 : GT * SG;
+  static constexpr int GT = GT_, N = 16;
+  static_assert(GT <= kMostCols, "columns");
   static constexpr int kTPS = 128 / DA;            // tiles per step
   static constexpr int KS = kKeys * kTPS;          // keys per step
   static constexpr int kRows = kTPS * N;           // rows of P^T (the P.V's N)
-  static constexpr int kStages = N == 16 && DA == 128 ? 4 : 3;
+  static constexpr int kStages = DA == 128 ? 4 : 3;
   static constexpr int kQSlots = 2;
   static constexpr int kSCols = 3 * N;   // columns of S^T per tile: the queries' pieces as further columns
   static constexpr int kQPiece = N * DA;
@@ -90,20 +87,20 @@ struct Cfg {
   static constexpr int kOffFin = kOffMax + 8 * GT * 4;   // the second group's (m, l) and R
   static constexpr int kOffFactor = (kOffFin + (2 * GT + 1) * 4 + 15) / 16 * 16;   // [softmax warp][GT][4] floats
   static constexpr int kOffBar = kOffFactor + 8 * GT * 16;
-  static constexpr int kNBars = 4 * kStages + 12 + kRing + 7;
+  static constexpr int kNBars = 4 * kStages + 12 + kRing + 6;
   static constexpr int kOffMisc = kOffBar + (kNBars * 8 + 15) / 16 * 16;
   static constexpr int kSmem = kOffMisc + 512 + 1024;
   // S^T: two buffers of kTPS tiles, then u^T (kRows columns) of each group with its own
   static constexpr int kColU = 2 * kTPS * kSCols;
-  static constexpr int kUsedCols = kColU + TG * kRows;
+  static constexpr int kUsedCols = kColU + 2 * kRows;
   static constexpr uint32_t kTmemCols = kUsedCols <= 128 ? 128 : kUsedCols <= 256 ? 256 : 512;
   static_assert(kSmem <= 227 * 1024 && kUsedCols <= 512, "shared and tensor memory");
 };
 
-template <int GT, int SG, int DA>
+template <int GT, int DA>
 __global__ void __launch_bounds__(kThreads, 1) tree_kernel(const __grid_constant__ Params p) {
-  using C = Cfg<GT, SG, DA>;
-  constexpr int N = C::N, kTPS = C::kTPS, KS = C::KS, TG = C::TG, kStages = C::kStages, kSlots = C::kQSlots;
+  using C = Cfg<GT, DA>;
+  constexpr int N = C::N, kTPS = C::kTPS, KS = C::KS, kStages = C::kStages, kSlots = C::kQSlots;
   extern __shared__ __align__(1024) uint8_t smem_raw[];
   // (by an offset, not through an integer: the accesses stay ones of shared memory)
   uint8_t* smem = smem_raw + ((1024 - (smem_u32(smem_raw) & 1023)) & 1023);
@@ -115,7 +112,7 @@ __global__ void __launch_bounds__(kThreads, 1) tree_kernel(const __grid_constant
   const uint32_t b_q_full = take(2), b_q_empty = take(2), b_s_full = take(2), b_p_full = take(2), b_w_full = take(2);
   const uint32_t b_pv_done = take(2);   // the P.V that read P^T and V buffer i has completed (one phase per use)
   const uint32_t b_c_full = take(kRing);
-  const uint32_t b_o_free = take(1), b_drain = take(1), b_red = take(2), b_xch = take(2), b_fin = take(1);
+  const uint32_t b_o_free = take(1), b_drain = take(1), b_red = take(2), b_xch = take(1), b_fin = take(1);
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + C::kOffMisc);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + C::kOffMisc + 4);
   volatile int* start_b = reinterpret_cast<volatile int*>(smem + C::kOffMisc + 8);
@@ -134,9 +131,9 @@ __global__ void __launch_bounds__(kThreads, 1) tree_kernel(const __grid_constant
     auto in = [&](uint32_t first, int n) { return bar >= first && bar < first + 8 * n; };
     const int arrivals = in(b_v_empty, kStages) || in(b_w_full, 2) || in(b_red, 2) ? 4   // the warps that widen; a group
                          : in(b_q_empty, 2)                          ? 1 + 8     // the MMA, the softmax warps
-                         : in(b_p_full, 2) || in(b_o_free, 1)        ? 4 * SG    // the softmax warps of a step; those that read u^T
+                         : in(b_p_full, 2) || in(b_o_free, 1)        ? 4         // the softmax warps of a step; those that read u^T
                          : in(b_c_full, kRing)                       ? 64        // the copying threads
-                         : in(b_xch, 2)                              ? 2
+                         : in(b_xch, 1)                              ? 2
                                                                      : 1;
     mbar_init(bar, arrivals);
     fence_mbar_init();
@@ -212,7 +209,7 @@ __global__ void __launch_bounds__(kThreads, 1) tree_kernel(const __grid_constant
         // which overwrite u^T, the previous unit's epilogue must have read it
         int pv_unit = 0;
         auto do_pv = [&]() -> bool {
-          const bool first = pv_unit++ < TG;
+          const bool first = pv_unit++ < 2;
           const int b = pv_cnt & 1;
           if (!wait_warp(b_w_full + 8 * b, (pv_cnt >> 1) & 1, wc, ATTN_DEVERR_WAIT_TIMEOUT_SITE(kSiteVFull))) return false;
           if (!wait_warp(b_p_full + 8 * b, (pv_cnt >> 1) & 1, wc, ATTN_DEVERR_WAIT_TIMEOUT_SITE(kSitePFull))) return false;
@@ -221,7 +218,7 @@ __global__ void __launch_bounds__(kThreads, 1) tree_kernel(const __grid_constant
               !wait_warp(b_o_free, (units_done - 1) & 1, wc, ATTN_DEVERR_WAIT_TIMEOUT_SITE(kSiteODone)))
             return false;
           tc_fence_after();
-          const uint32_t tu = uniform(t_u + (TG == 2 ? b * C::kRows : 0)), a0 = uniform(dv0 + (b * kWide >> 4));
+          const uint32_t tu = uniform(t_u + b * C::kRows), a0 = uniform(dv0 + (b * kWide >> 4));
           const uint32_t b0 = uniform(dp0 + (b * C::kP >> 4)), done = uniform(b_pv_done + 8 * b);
           const uint32_t more_of_it = uniform(first ? 0u : 1u);
           if (elect_one()) {
@@ -286,22 +283,20 @@ __global__ void __launch_bounds__(kThreads, 1) tree_kernel(const __grid_constant
     const int sw = warp - (grp ? kWarpSoft2 : kWarpSoft1);  // softmax warp 0..3 of its group
     const int quarter = warp & 3;                  // TMEM lane quarter this warp may address
     const int lrow = quarter * 32 + lane;          // TMEM lane: key of the tile (S^T), d (u^T)
-    constexpr int CH = GT < 16 ? GT : 16, NC = GT / CH;   // columns at a time
-    constexpr int LD = CH < 4 ? 4 : CH;            // as they are read
-    const int gcol = SG == 2 ? grp * GT : 0;       // first column of the group
+    constexpr int LD = GT < 4 ? 4 : GT;            // columns as they are read
     const uint32_t t_lane = tmem + (static_cast<uint32_t>(quarter * 32) << 16);
     // u^T columns this thread's lane holds: at DA = 64 lanes 64-127 keep u_b
-    const uint32_t t_u = t_lane + C::kColU + ((kTPS == 2 && lrow >= 64) ? N : 0) + gcol + (TG == 2 ? grp * C::kRows : 0);
+    const uint32_t t_u = t_lane + C::kColU + ((kTPS == 2 && lrow >= 64) ? N : 0) + grp * C::kRows;
     float4* red = reinterpret_cast<float4*>(smem + C::kOffRed) + grp * 2 * (GT + 1);   // [parity][GT + 1], a float per warp
-    const uint32_t bar_red = b_red + 8 * grp, bar_xch = b_xch + 8 * grp;
+    const uint32_t bar_red = b_red + 8 * grp;
     uint32_t q_cnt = 0, red_cnt = 0, xch_cnt = 0, units_done = 0;
     float* m = reinterpret_cast<float*>(smem + C::kOffMax) + (4 * grp + sw) * GT;   // this warp's copy of the maxima
     // A warp hands GT + 1 values over to the group: column h by put(h, v) of one
     // lane, then meet(); then red[par * (GT + 1) + h] has the four warps'
     auto put = [&](int h, float v) { reinterpret_cast<float*>(red + (red_cnt & 1) * (GT + 1))[4 * h + sw] = v; };
-    constexpr int kOwn = CH == 16 ? 1 : CH == 8 ? 2 : CH == 4 ? 3 : CH == 2 ? 4 : 5;   // log2 of the lanes per column of fold_columns
-    auto put_folded = [&](int c, float v) {
-      if ((lane & ((1 << kOwn) - 1)) == 0) put(c * CH + (lane >> kOwn), v);
+    constexpr int kOwn = GT == 8 ? 2 : GT == 4 ? 3 : GT == 2 ? 4 : 5;   // log2 of the lanes per column of fold_columns
+    auto put_folded = [&](float v) {
+      if ((lane & ((1 << kOwn) - 1)) == 0) put(lane >> kOwn, v);
     };
     auto meet = [&]() -> bool {
       __syncwarp();
@@ -330,23 +325,23 @@ __global__ void __launch_bounds__(kThreads, 1) tree_kernel(const __grid_constant
       for (int i = 0; i < LD; ++i) x[i] *= scale;
       if (!all) {
 #pragma unroll
-        for (int i = 0; i < CH; ++i)
+        for (int i = 0; i < GT; ++i)
           if (!((bits >> i) & 1)) x[i] = -INFINITY;
       }
     };
     for (bool more = next_unit<KS>(p, w, true); more && ok; more = next_unit<KS>(p, w, false)) {
       const Unit u = unit_of<N>(p, w, place);
       if (u.cols <= 0) continue;
-      const int G = min(GT, u.cols - gcol);   // this group's columns (may be none)
-      // row of q and head of this group's column h
+      const int G = min(GT, u.cols);   // columns
+      // row of q and head of column h
       auto out_row = [&](int h, int& head) {
-        const int cc = u.col0 + gcol + h, token = token_of(p, cc);
+        const int cc = u.col0 + h, token = token_of(p, cc);
         head = u.g * p.group + cc - token * p.group;
         return w.row0 + token;
       };
       if (w.T == 0) {
         // a sequence without keys: O = 0, lse = -inf
-        for (int h = 0; h < G && (SG == 2 || grp == 0); ++h) {
+        for (int h = 0; h < G && grp == 0; ++h) {
           int head;
           const long long row = out_row(h, head);
           if (lrow < DA) p.o[(row * p.Hq + head) * DA + lrow] = 0;
@@ -358,8 +353,8 @@ __global__ void __launch_bounds__(kThreads, 1) tree_kernel(const __grid_constant
       const int qs = q_cnt % kSlots;
       if (!wait_warp(b_q_full + 8 * qs, (q_cnt / kSlots) & 1, wc, ATTN_DEVERR_WAIT_TIMEOUT_SITE(kSiteQFull))) break;
       ++q_cnt;
-      const float* col = reinterpret_cast<const float*>(smem + C::kOffCol) + qs * N + gcol;
-      const unsigned long long* mask = reinterpret_cast<const unsigned long long*>(smem + C::kOffMask) + qs * N + gcol;
+      const float* col = reinterpret_cast<const float*>(smem + C::kOffCol) + qs * N;
+      const unsigned long long* mask = reinterpret_cast<const unsigned long long*>(smem + C::kOffMask) + qs * N;
       float l[GT], R = 0.0f, inv_r = 0.0f;
 #pragma unroll
       for (int h = 0; h < GT; ++h) l[h] = 0.0f;
@@ -368,7 +363,7 @@ __global__ void __launch_bounds__(kThreads, 1) tree_kernel(const __grid_constant
       const uint32_t step0 = step;   // of the unit
       int first_t = -1;              // this group's first step
       for (int t = w.t0; t < w.t1; ++t) {
-        if (TG == 2 && static_cast<int>(step & 1) != grp) {   // the other group's
+        if (static_cast<int>(step & 1) != grp) {   // the other group's
           ++step;
           continue;
         }
@@ -404,21 +399,20 @@ __global__ void __launch_bounds__(kThreads, 1) tree_kernel(const __grid_constant
           break;
         }
         tc_fence_after();
-        const uint32_t t_s = t_lane + sb * kTPS * C::kSCols + gcol;
-        float s[kTPS][LD];   // (the last columns', where there are more)
+        const uint32_t t_s = t_lane + sb * kTPS * C::kSCols;
+        float s[kTPS][LD];
         bool all = vis[0] == 0xffffffffu;   // every column sees every key of this warp
         if constexpr (kTPS == 2) all = all && vis[1] == 0xffffffffu;
         all = __all_sync(0xffffffffu, all);
-#pragma unroll
-        for (int c = 0; c < NC; ++c) {
-          float x[CH];
+        {
+          float x[GT];
 #pragma unroll
           for (int y = 0; y < kTPS; ++y) {
-            scores(t_s + y * C::kSCols + c * 16, ks[y], all, vis[y] >> (c * CH), s[y]);
+            scores(t_s + y * C::kSCols, ks[y], all, vis[y], s[y]);
 #pragma unroll
-            for (int i = 0; i < CH; ++i) x[i] = y == 0 ? s[y][i] : fmaxf(x[i], s[y][i]);
+            for (int i = 0; i < GT; ++i) x[i] = y == 0 ? s[y][i] : fmaxf(x[i], s[y][i]);
           }
-          put_folded(c, fold_columns<CH>(x, lane, [](float a, float b) { return fmaxf(a, b); }));
+          put_folded(fold_columns<GT>(x, lane, [](float a, float b) { return fmaxf(a, b); }));
         }
         // (scales are not negative, so their bits are in order)
         const uint32_t v_top = __reduce_max_sync(0xffffffffu, v_max);
@@ -454,75 +448,64 @@ __global__ void __launch_bounds__(kThreads, 1) tree_kernel(const __grid_constant
           }
         }
         // where P^T of this thread's key lies: row r at (pbuf ^ (r & 7) << 4) + 128 r
-        const uint32_t pbuf = sbase + C::kOffP + sb * C::kP + (lrow >> 6) * C::kPChunk + gcol * 128 +
+        const uint32_t pbuf = sbase + C::kOffP + sb * C::kP + (lrow >> 6) * C::kPChunk +
                               ((lrow & 63) >> 3 << 4) + 2 * (lrow & 7);
+        // running max (scaled units): rescale only when it grows by more than 2^8
+        // (loads first, and no branches among them: a load behind a condition would
+        // wait for the one before)
+        float mt[GT], old[GT], cs[GT];
 #pragma unroll
-        for (int c = 0; c < NC; ++c) {
-          if constexpr (NC > 1) {
+        for (int i = 0; i < GT; ++i) {
+          mt[i] = top4(got[i]);
+          cs[i] = col[i];
+          old[i] = m[i];
+        }
+        bool any = rr != 1.0f;
 #pragma unroll
-            for (int y = 0; y < kTPS; ++y) {
-              scores(t_s + y * C::kSCols + c * 16, ks[y], all, vis[y] >> (c * CH), s[y]);
-            }
+        for (int i = 0; i < GT; ++i) {
+          mt[i] *= cs[i];   // (-inf where no column sees a key)
+          // grows past old + 8, or past -inf at all
+          const bool grows = mt[i] > fmaxf(old[i] + 8.0f, -3.0e38f);
+          mt[i] = grows ? mt[i] : old[i];
+          any |= grows;
+        }
+        // m and R are the same in every thread, so the decision is too; the vote
+        // keeps the warp-collective TMEM accesses below uniform regardless.
+        any = __any_sync(0xffffffffu, any);
+        if (any) {
+          float r[16];
+#pragma unroll
+          for (int i = 0; i < 16; ++i) r[i] = rr;
+#pragma unroll
+          for (int i = 0; i < GT; ++i) {
+            const float q = old[i] == mt[i] ? 1.0f : ex2_approx(old[i] - mt[i]);   // (from -inf: 0)
+            l[i] *= q;
+            r[i] *= q;
           }
-          // running max (scaled units): rescale only when it grows by more than 2^8
-          // (loads first, and no branches among them: a load behind a condition would
-          // wait for the one before)
-          float mt[CH], old[CH], cs[CH];
+          __syncwarp();
 #pragma unroll
-          for (int i = 0; i < CH; ++i) {
-            mt[i] = top4(got[c * CH + i]);
-            cs[i] = col[c * CH + i];
-            old[i] = m[c * CH + i];
+          for (int i = 0; i < GT; ++i)
+            if (lane == i) m[i] = mt[i];
+          __syncwarp();
+          // u^T rescale (rare): this group's last P.V has completed
+          if (t > first_t) {
+            tc_fence_after();
+            float o[16];
+            tld<16>(t_u, o);
+#pragma unroll
+            for (int i = 0; i < GT; ++i) o[i] *= r[i];
+            tst16(t_u, o);
+            tmem_wait_st();
           }
-          bool any = rr != 1.0f;
+        }
 #pragma unroll
-          for (int i = 0; i < CH; ++i) {
-            mt[i] *= cs[i];   // (-inf where no column sees a key)
-            // grows past old + 8, or past -inf at all
-            const bool grows = mt[i] > fmaxf(old[i] + 8.0f, -3.0e38f);
-            mt[i] = grows ? mt[i] : old[i];
-            any |= grows;
-          }
-          // m and R are the same in every thread, so the decision is too; the vote
-          // keeps the warp-collective TMEM accesses below uniform regardless.
-          any = __any_sync(0xffffffffu, any);
-          if (any) {
-            float r[16];
+        for (int i = 0; i < GT; ++i) {
+          const float mh = fmaxf(mt[i], -3.0e38f) - kPLift;   // (finite)
 #pragma unroll
-            for (int i = 0; i < 16; ++i) r[i] = rr;
-#pragma unroll
-            for (int i = 0; i < CH; ++i) {
-              const float q = old[i] == mt[i] ? 1.0f : ex2_approx(old[i] - mt[i]);   // (from -inf: 0)
-              l[c * CH + i] *= q;
-              r[i] *= q;
-            }
-            __syncwarp();
-#pragma unroll
-            for (int i = 0; i < CH; ++i)
-              if (lane == i) m[c * CH + i] = mt[i];
-            __syncwarp();
-            // u^T rescale (rare): needs this group's last P.V complete
-            if (t > first_t) {
-              if (TG == 1 && !pv_wait(step - 1)) { ok = false; break; }
-              tc_fence_after();
-              float o[16];
-              tld<16>(t_u + c * 16, o);
-#pragma unroll
-              for (int i = 0; i < CH; ++i) o[i] *= r[i];
-              tst16(t_u + c * 16, o);
-              tmem_wait_st();
-            }
-          }
-#pragma unroll
-          for (int i = 0; i < CH; ++i) {
-            const int h = c * CH + i;
-            const float mh = fmaxf(mt[i], -3.0e38f) - kPLift;   // (finite)
-#pragma unroll
-            for (int y = 0; y < kTPS; ++y) {
-              const float e = ex2_approx(fmaf(s[y][i], cs[i], -mh));
-              l[h] += e;
-              store_half((pbuf ^ ((h & 7) << 4)) + (y * N + h) * 128, e * f[y]);
-            }
+          for (int y = 0; y < kTPS; ++y) {
+            const float e = ex2_approx(fmaf(s[y][i], cs[i], -mh));
+            l[i] += e;
+            store_half((pbuf ^ ((i & 7) << 4)) + (y * N + i) * 128, e * f[y]);
           }
         }
         if (strange) {
@@ -536,7 +519,6 @@ __global__ void __launch_bounds__(kThreads, 1) tree_kernel(const __grid_constant
               store_half((pbuf ^ ((h & 7) << 4)) + (y * N + h) * 128, __uint_as_float(0x7fffffffu));
           }
         }
-        if (!ok) break;
         fence_proxy_async_smem();
         tc_fence_before();
         __syncwarp();
@@ -547,13 +529,7 @@ __global__ void __launch_bounds__(kThreads, 1) tree_kernel(const __grid_constant
       if (lane == 0) mbar_arrive(b_q_empty + 8 * qs);   // (what it read of the slot: the columns' factors and masks)
       // the piece's exp-sums over all its keys, then u^T R / l (rolled over the
       // columns: this code runs once per unit)
-#pragma unroll
-      for (int c = 0; c < NC; ++c) {
-        float v[CH];
-#pragma unroll
-        for (int i = 0; i < CH; ++i) v[i] = l[c * CH + i];
-        put_folded(c, fold_columns<CH>(v, lane, [](float a, float b) { return a + b; }));
-      }
+      put_folded(fold_columns<GT>(l, lane, [](float a, float b) { return a + b; }));
       if (!meet()) break;
       const float4* got = red + ((red_cnt - 1) & 1) * (GT + 1);
       auto sum_of = [&](int h) {
@@ -563,7 +539,7 @@ __global__ void __launch_bounds__(kThreads, 1) tree_kernel(const __grid_constant
       float* fin_m = reinterpret_cast<float*>(smem + C::kOffFin);
       float* fin_l = fin_m + GT;
       float* fin_r = fin_l + GT;
-      if (TG == 2 && grp == 1) {
+      if (grp == 1) {
         // hands its maxima and sums over (of no step: -inf and 0), once the first group
         // has read those of the unit before
         if (units_done > 0 &&
@@ -584,9 +560,9 @@ __global__ void __launch_bounds__(kThreads, 1) tree_kernel(const __grid_constant
       // The second group's sums first: it has handed over all of its steps then, and seen
       // the phase of its barrier before each, so that the waits for both groups' last
       // products below cannot take an earlier phase for theirs
-      if (TG == 2 && !wait_warp(b_fin, units_done & 1, wc, ATTN_DEVERR_WAIT_TIMEOUT_SITE(kSiteMerge))) break;
+      if (!wait_warp(b_fin, units_done & 1, wc, ATTN_DEVERR_WAIT_TIMEOUT_SITE(kSiteMerge))) break;
       if (!pv_wait(step - 1)) break;
-      if (TG == 2 && step - step0 >= 2 && !pv_wait(step - 2)) break;
+      if (step - step0 >= 2 && !pv_wait(step - 2)) break;
       tc_fence_after();
       const bool whole = w.t0 == 0 && w.t1 == w.T;
       const int slot = 2 * blockIdx.x + (w.t0 == 0 ? 1 : 0);
@@ -596,16 +572,14 @@ __global__ void __launch_bounds__(kThreads, 1) tree_kernel(const __grid_constant
       if (lane < GT) {
         float lh = sum_of(lane), mx = m[lane];
         float w0 = lh != 0.0f ? R : 0.0f, w1 = 0.0f;
-        if constexpr (TG == 2) {
-          const float m1 = fin_m[lane], l1 = fin_l[lane];
-          if (l1 != 0.0f) {
-            const float top = lh != 0.0f ? fmaxf(mx, m1) : m1;
-            const float a = lh != 0.0f ? ex2_approx(mx - top) : 0.0f, b = ex2_approx(m1 - top);
-            w0 *= a;
-            w1 = b * *fin_r;
-            lh = (lh != 0.0f ? lh * a : 0.0f) + l1 * b;
-            mx = top;
-          }
+        const float m1 = fin_m[lane], l1 = fin_l[lane];
+        if (l1 != 0.0f) {
+          const float top = lh != 0.0f ? fmaxf(mx, m1) : m1;
+          const float a = lh != 0.0f ? ex2_approx(mx - top) : 0.0f, b = ex2_approx(m1 - top);
+          w0 *= a;
+          w1 = b * *fin_r;
+          lh = (lh != 0.0f ? lh * a : 0.0f) + l1 * b;
+          mx = top;
         }
         const float inv = lh != 0.0f ? 1.0f / lh : 0.0f;   // 0: saw no key; a NaN stays one
         factors[lane] = make_float4(mx, lh * kPDrop, w0 * inv, w1 * inv);
@@ -615,16 +589,15 @@ __global__ void __launch_bounds__(kThreads, 1) tree_kernel(const __grid_constant
         const float4 f = factors[h];
         float a[1], b[1];
         tld_start<1>(t_u + h, a);
-        if constexpr (TG == 2) tld_start<1>(t_u + C::kRows + h, b);
-        else b[0] = 0.0f;
+        tld_start<1>(t_u + C::kRows + h, b);
         tld_wait<1>(a, b);
         return (f.z != 0.0f ? a[0] * f.z : 0.0f) + (f.w != 0.0f ? b[0] * f.w : 0.0f);
       };
-      // u = u_a + u_b at head dimension 64: lanes 64-127 hand u_b over in the rows of
-      // this group's columns in the first P^T buffer, idle now that every P.V that read
+      // u = u_a + u_b at head dimension 64: lanes 64-127 hand u_b over in the
+      // first P^T buffer, idle now that every P.V that read
       // it has completed; this group writes them next after its next meeting
       auto handed = [&](int h, int i) {
-        return reinterpret_cast<float*>(smem + C::kOffP + (i >> 5) * C::kPChunk + (gcol + h) * 128 + (i & 31) * 4);
+        return reinterpret_cast<float*>(smem + C::kOffP + (i >> 5) * C::kPChunk + h * 128 + (i & 31) * 4);
       };
       if constexpr (kTPS == 2) {
         if (lrow >= 64) {
@@ -633,9 +606,9 @@ __global__ void __launch_bounds__(kThreads, 1) tree_kernel(const __grid_constant
             *handed(h, lrow - 64) = joined(h);
           }
           __syncwarp();
-          if (lane == 0) mbar_arrive(bar_xch);
+          if (lane == 0) mbar_arrive(b_xch);
         } else {
-          if (!wait_warp(bar_xch, xch_cnt & 1, wc, ATTN_DEVERR_WAIT_TIMEOUT_SITE(kSiteXchg))) break;
+          if (!wait_warp(b_xch, xch_cnt & 1, wc, ATTN_DEVERR_WAIT_TIMEOUT_SITE(kSiteXchg))) break;
         }
         ++xch_cnt;
       }
@@ -649,7 +622,7 @@ __global__ void __launch_bounds__(kThreads, 1) tree_kernel(const __grid_constant
             const long long at = (static_cast<long long>(out_row(h, head)) * p.Hq + head) * DA + lrow;
             p.o[at] = p.fp16 ? __half_as_ushort(__float2half_rn(v)) : __bfloat16_as_ushort(__float2bfloat16_rn(v));
           } else {
-            p.part_o[(static_cast<size_t>(slot) * N + gcol + h) * DA + lrow] = v;
+            p.part_o[(static_cast<size_t>(slot) * N + h) * DA + lrow] = v;
           }
         }
       }
@@ -661,7 +634,7 @@ __global__ void __launch_bounds__(kThreads, 1) tree_kernel(const __grid_constant
           p.lse[static_cast<long long>(head) * p.total + row] =
               (lh != 0.0f) ? mx * 0.69314718055994531f + __logf(lh) : -INFINITY;
         } else {
-          p.part_ml[slot * N + gcol + lane] = make_float2(mx, lh);
+          p.part_ml[slot * N + lane] = make_float2(mx, lh);
         }
       }
       tc_fence_before();
@@ -683,21 +656,19 @@ __global__ void __launch_bounds__(kThreads, 1) tree_kernel(const __grid_constant
   }
 }
 
-template <int GT, int SG, int DA>
+template <int GT, int DA>
 cudaError_t launch(const Params& p, int cols, int grid, cudaStream_t stream) {
-  using C = Cfg<GT, SG, DA>;
+  using C = Cfg<GT, DA>;
   static bool done[64] = {};   // per instantiation
-  return launch_with_merge<C::N, DA>(tree_kernel<GT, SG, DA>, C::kSmem, done, p, cols, grid, stream);
+  return launch_with_merge<C::N, DA>(tree_kernel<GT, DA>, C::kSmem, done, p, cols, grid, stream);
 }
 
 template <int DA>
 cudaError_t pick(const Params& p, int cols, int grid, cudaStream_t stream) {
-  if (cols <= 1) return launch<1, 1, DA>(p, cols, grid, stream);
-  if (cols <= 2) return launch<2, 1, DA>(p, cols, grid, stream);
-  if (cols <= 4) return launch<4, 1, DA>(p, cols, grid, stream);
-  if (cols <= 8) return launch<8, 1, DA>(p, cols, grid, stream);
-  if (cols <= 16) return launch<16, 1, DA>(p, cols, grid, stream);
-  return launch<16, 2, DA>(p, cols, grid, stream);
+  if (cols <= 1) return launch<1, DA>(p, cols, grid, stream);
+  if (cols <= 2) return launch<2, DA>(p, cols, grid, stream);
+  if (cols <= 4) return launch<4, DA>(p, cols, grid, stream);
+  return launch<8, DA>(p, cols, grid, stream);
 }
 
 }  // namespace tree

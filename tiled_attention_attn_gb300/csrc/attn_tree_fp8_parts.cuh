@@ -262,7 +262,7 @@ __device__ __forceinline__ void store_half(uint32_t at, float x) {
   asm volatile("st.shared.b16 [%0], %1;" :: "r"(at), "h"(__half_as_ushort(__float2half_rn(x))) : "memory");
 }
 
-// Combines n columns (a power of two, at most 32) over the warp's lanes: each
+// Combines n columns (a power of two, at most 8 here) over the warp's lanes: each
 // exchange halves the columns that a lane holds, n - 1 shuffles and the rest of five
 // instead of 5 n.  Returns the result of column lane >> (5 - log2 n).
 template <int n, typename Op>
