@@ -599,7 +599,7 @@ long long attn_qk_norm_workspace_bytes(int d);
  *   the others as in attn_paged_kv, with its rules for what the host does not
  *   read: key counts, offsets and pages out of range, slots past the last key.
  * What a query does not see never reaches its outputs, NaN rows included, as long
- * as v holds no NaN itself (attn_cache_append_fp8 writes none).
+ * as v holds no NaN itself (attn_cache_append_fp8 writes none); nor does its size.
  */
 typedef struct attn_paged_kv8 {
   void *k;
@@ -646,8 +646,11 @@ int attn_cache_read_fp8(void *k, void *v, int B, int total, const attn_paged_kv8
  * i] set (device int64 (total); its ancestors and itself, as a rule); null: the
  * chain t <= i.
  *     o = softmax(scale q . K) V over what it sees,  lse (Hq, total) fp32;
- * a token that sees nothing gives o = 0 and lse = -inf, one that sees a NaN score
- * NaN; rows outside every sequence are left as they are.  Hq a multiple of
+ * a token that sees nothing gives o = 0 and lse = -inf, one that sees a NaN score or
+ * value NaN.  Of a row of q, features are held to 2^-17 of its largest; of a weight
+ * times its value's scale, 22 bits where max_tokens Hq / num_kv_heads <= 8 and 11 bits
+ * otherwise, to 2^-30 of the row's largest (scales below 2^-70 count as 2^-70 there).
+ * Rows outside every sequence are left as they are.  Hq a multiple of
  * num_kv_heads, scale finite and not negative.  workspace: 256-byte aligned,
  * attn_fp8_workspace_bytes(d) bytes.  The same call gives the same bits.
  */

@@ -24,7 +24,7 @@ struct Params {
   const int* cu;       // or null: one token per sequence
   const long long* mask;   // or null: chains
   int4* rec;           // per CTA: the unit whose first piece it ran (sequence, unit, pieces, columns)
-  float2* part_ml;     // (m, l) [2 CTAs][columns]
+  float2* part_ml;     // (log2 of the weights' sum, 1; or -inf, 0: no key) [2 CTAs][columns]
   float* part_o;       // O of a piece [2 CTAs][columns][d]
   int* err;
   unsigned long long timeout_ns;

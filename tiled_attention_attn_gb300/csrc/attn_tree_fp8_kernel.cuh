@@ -5,7 +5,7 @@
 // the columns of transposed products, as in the 16-bit decode kernel:
 //   S^T = K Q^T    (M = 128 keys, N columns, K = d)
 //   u^T += V^T P^T (M = d, N columns, K = 128 keys)
-// with the online softmax's running maximum m, sum l and accumulator u per column;
+// with the online softmax's running reference m, sum l and accumulator u per column;
 // m may lag by up to 2^8, which cancels in u / l.
 //
 // K stays in e4m3 from HBM to the tensor core (kind::f8f6f4): what has 16 bits is
@@ -17,11 +17,12 @@
 //
 // V is widened to fp16, which holds e4m3 exactly, by four warps between the TMA's
 // stage and the second product: P in e4m3 would lose the light keys of a long
-// cache.  A value's scale goes into its weight: P' = p vs / R in fp16, R a power of
-// two at least the largest scale so far, so P' <= p; u is rescaled where R grows, as
-// where m grows.  l sums p itself.  P' is held times 2^7 as in the 16-bit kernel
-// (kPLift).  The rounding of P' to fp16, 2^-11 of it, is the only one below fp32
-// before O's own.
+// cache.  A value's scale goes into its weight, P' = p vs 2^-m, and m follows the
+// largest p vs of what the column sees (see kHeldUp): a reference for the scales of all
+// keys would let a large value row that a column does not see, or sees without weight,
+// take the bits of its other weights.  P' is a sum of two fp16 values, the second 2^11
+// times what the first leaves, in columns of P^T that the product has anyway: off by
+// 2^-22 of itself.
 //
 // Bound by HBM: per key and head d bytes of K and of V, and 8 of scales.  TMA
 // stages of 16 KB of K and 16 of V (three or four), per page one box per tile; the
@@ -31,8 +32,8 @@
 // softmax warps on one step: 120 us for 32 caches of ~3,550 keys, 32 heads on 8 of
 // 128).  So does what it takes to issue one: with the operands in one thread's registers
 // about 85 cycles each, whatever their size, and 61 us for those caches; uniform over the
-// warp (see uniform()) 55.  Measured (device time, merge included): those caches 55.6 us,
-// of which the 236 MB take 35 at the copy rate; one of 131,072 keys 55.3 of 41, its line
+// warp (see uniform()) 55.  Measured (device time, merge included): those caches 56.5 us,
+// of which the 236 MB take 35 at the copy rate; one of 131,072 keys 55.2 of 41, its line
 // of steps at 6.6 TB/s.  What is left is the start (4 us to the first S: prologue, the
 // walk, the queries' conversion), the epilogue and 3 to 4 of the merge.
 //
@@ -55,7 +56,7 @@ constexpr int kRaw = kKeys * 128;       // a stage of K, or of V, in bytes
 constexpr int kWide = 2 * kRaw;         // a step's V in fp16: two chunks of 128-byte rows
 constexpr int kWideChunk = kRaw;
 
-// GT columns.  Two groups of four softmax warps take turns, step by step, with maxima,
+// GT columns.  Two groups of four softmax warps take turns, step by step, with references,
 // sums and accumulators of their own that are joined at the unit's end (one group's
 // chain of waits is longer than a step takes to arrive).  Two buffers of S^T, so that a
 // group meets every phase of its buffer's barriers: with three it would see every
@@ -82,10 +83,10 @@ struct Cfg {
   static constexpr int kOffScale = kOffQ + kQSlots * kQ;   // [kRing][k, v][KS] floats
   static constexpr int kOffMask = kOffScale + kRing * 2 * KS * 4;   // [slot][N] 64-bit words
   static constexpr int kOffCol = kOffMask + kQSlots * N * 8;        // [slot][N] floats
-  static constexpr int kOffRed = kOffCol + kQSlots * N * 4;         // [group][parity][GT + 1][4] floats
-  static constexpr int kOffMax = kOffRed + 2 * 2 * (GT + 1) * 16;  // running maxima, [softmax warp][GT] floats
-  static constexpr int kOffFin = kOffMax + 8 * GT * 4;   // the second group's (m, l) and R
-  static constexpr int kOffFactor = (kOffFin + (2 * GT + 1) * 4 + 15) / 16 * 16;   // [softmax warp][GT][4] floats
+  static constexpr int kOffRed = kOffCol + kQSlots * N * 4;         // [group][parity][GT][4] floats
+  static constexpr int kOffMax = kOffRed + 2 * 2 * GT * 16;  // references, [softmax warp][GT] floats
+  static constexpr int kOffFin = kOffMax + 8 * GT * 4;   // the second group's (m, l)
+  static constexpr int kOffFactor = (kOffFin + 2 * GT * 4 + 15) / 16 * 16;   // [softmax warp][GT][4] floats
   static constexpr int kOffBar = kOffFactor + 8 * GT * 16;
   static constexpr int kNBars = 4 * kStages + 12 + kRing + 6;
   static constexpr int kOffMisc = kOffBar + (kNBars * 8 + 15) / 16 * 16;
@@ -287,13 +288,13 @@ __global__ void __launch_bounds__(kThreads, 1) tree_kernel(const __grid_constant
     const uint32_t t_lane = tmem + (static_cast<uint32_t>(quarter * 32) << 16);
     // u^T columns this thread's lane holds: at DA = 64 lanes 64-127 keep u_b
     const uint32_t t_u = t_lane + C::kColU + ((kTPS == 2 && lrow >= 64) ? N : 0) + grp * C::kRows;
-    float4* red = reinterpret_cast<float4*>(smem + C::kOffRed) + grp * 2 * (GT + 1);   // [parity][GT + 1], a float per warp
+    float4* red = reinterpret_cast<float4*>(smem + C::kOffRed) + grp * 2 * GT;   // [parity][GT], a float per warp
     const uint32_t bar_red = b_red + 8 * grp;
     uint32_t q_cnt = 0, red_cnt = 0, xch_cnt = 0, units_done = 0;
-    float* m = reinterpret_cast<float*>(smem + C::kOffMax) + (4 * grp + sw) * GT;   // this warp's copy of the maxima
-    // A warp hands GT + 1 values over to the group: column h by put(h, v) of one
-    // lane, then meet(); then red[par * (GT + 1) + h] has the four warps'
-    auto put = [&](int h, float v) { reinterpret_cast<float*>(red + (red_cnt & 1) * (GT + 1))[4 * h + sw] = v; };
+    float* m = reinterpret_cast<float*>(smem + C::kOffMax) + (4 * grp + sw) * GT;   // this warp's copy of the references
+    // A warp hands GT values over to the group: column h by put(h, v) of one
+    // lane, then meet(); then red[par * GT + h] has the four warps'
+    auto put = [&](int h, float v) { reinterpret_cast<float*>(red + (red_cnt & 1) * GT)[4 * h + sw] = v; };
     constexpr int kOwn = GT == 8 ? 2 : GT == 4 ? 3 : GT == 2 ? 4 : 5;   // log2 of the lanes per column of fold_columns
     auto put_folded = [&](float v) {
       if ((lane & ((1 << kOwn) - 1)) == 0) put(lane >> kOwn, v);
@@ -355,7 +356,7 @@ __global__ void __launch_bounds__(kThreads, 1) tree_kernel(const __grid_constant
       ++q_cnt;
       const float* col = reinterpret_cast<const float*>(smem + C::kOffCol) + qs * N;
       const unsigned long long* mask = reinterpret_cast<const unsigned long long*>(smem + C::kOffMask) + qs * N;
-      float l[GT], R = 0.0f, inv_r = 0.0f;
+      float l[GT];
 #pragma unroll
       for (int h = 0; h < GT; ++h) l[h] = 0.0f;
       if (lane < GT) m[lane] = -INFINITY;
@@ -376,16 +377,16 @@ __global__ void __launch_bounds__(kThreads, 1) tree_kernel(const __grid_constant
         // this thread's key in each tile of the step: its scales, and the columns that see it
         const float* scales = reinterpret_cast<const float*>(smem + C::kOffScale) + ring * 2 * KS;
         float ks[kTPS], vs[kTPS];
-        uint32_t v_max = 0;   // bits
+        float cs[GT], lv[kTPS];   // the columns' factors; log2 of the values' scales
         uint32_t vis[kTPS];
 #pragma unroll
         for (int y = 0; y < kTPS; ++y) {
           const int key = t * KS + y * kKeys + lrow, at = key - w.ctx;   // at: place among the new tokens
           ks[y] = scales[y * kKeys + lrow];
           vs[y] = scales[KS + y * kKeys + lrow];
+          lv[y] = scale_log2(vs[y]);
           vis[y] = key < w.n ? 0xffffffffu : 0u;
           if (key < w.n) {
-            if (vs[y] > 0.0f) v_max = max(v_max, __float_as_uint(vs[y]));   // (not a NaN)
             if (at >= 0) {
               uint32_t bits = 0;
 #pragma unroll 1
@@ -394,6 +395,8 @@ __global__ void __launch_bounds__(kThreads, 1) tree_kernel(const __grid_constant
             }
           }
         }
+#pragma unroll
+        for (int i = 0; i < GT; ++i) cs[i] = col[i];
         if (!wait_warp(b_s_full + 8 * sb, (step >> 1) & 1, wc, ATTN_DEVERR_WAIT_TIMEOUT_SITE(kSiteSFull))) {
           ok = false;
           break;
@@ -410,39 +413,26 @@ __global__ void __launch_bounds__(kThreads, 1) tree_kernel(const __grid_constant
           for (int y = 0; y < kTPS; ++y) {
             scores(t_s + y * C::kSCols, ks[y], all, vis[y], s[y]);
 #pragma unroll
-            for (int i = 0; i < GT; ++i) x[i] = y == 0 ? s[y][i] : fmaxf(x[i], s[y][i]);
+            for (int i = 0; i < GT; ++i) {
+              const float z = fmaf(s[y][i], cs[i], lv[y]);
+              x[i] = y == 0 ? z : fmaxf(x[i], z);
+            }
           }
           put_folded(fold_columns<GT>(x, lane, [](float a, float b) { return fmaxf(a, b); }));
         }
-        // (scales are not negative, so their bits are in order)
-        const uint32_t v_top = __reduce_max_sync(0xffffffffu, v_max);
-        if (lane == 0) put(GT, __uint_as_float(v_top));
         if (!meet()) { ok = false; break; }
-        const float4* got = red + ((red_cnt - 1) & 1) * (GT + 1);
+        const float4* got = red + ((red_cnt - 1) & 1) * GT;
         auto top4 = [](const float4& v) { return fmaxf(fmaxf(v.x, v.y), fmaxf(v.z, v.w)); };
-        // the values' reference: the power of two above the largest scale so far
-        float rr = 1.0f;
-        {
-          const float top = top4(got[GT]);
-          if (top >= R && top > 0.0f) {
-            const float next = __uint_as_float(min((__float_as_uint(top) >> 23) + 1, 253u) << 23);
-            rr = R * __uint_as_float((254u - (__float_as_uint(next) >> 23)) << 23);
-            R = next;
-            inv_r = __uint_as_float((254u - (__float_as_uint(next) >> 23)) << 23);
-          }
-        }
         // P^T of these keys into buffer sb, once the P.V that read it two
         // steps back has completed
         if (step >= 2 && !pv_wait(step - 2)) { ok = false; break; }
+        // (no weight of a slot past the last key; a scale that is no number is dealt with below)
         float f[kTPS];
-#pragma unroll
-        for (int y = 0; y < kTPS; ++y) f[y] = vs[y] * inv_r;
-        // (no weight of a slot past the last key; a NaN among the scales is dealt with below)
         bool strange = false;
 #pragma unroll
         for (int y = 0; y < kTPS; ++y) {
-          if (vis[y] == 0) f[y] = 0.0f;
-          if (!(f[y] <= 4.0f)) {
+          f[y] = vis[y] == 0 ? 0.0f : vs[y] * kScaleDown;
+          if (!(f[y] <= kMostScale)) {
             strange = true;
             f[y] = 0.0f;
           }
@@ -450,37 +440,36 @@ __global__ void __launch_bounds__(kThreads, 1) tree_kernel(const __grid_constant
         // where P^T of this thread's key lies: row r at (pbuf ^ (r & 7) << 4) + 128 r
         const uint32_t pbuf = sbase + C::kOffP + sb * C::kP + (lrow >> 6) * C::kPChunk +
                               ((lrow & 63) >> 3 << 4) + 2 * (lrow & 7);
-        // running max (scaled units): rescale only when it grows by more than 2^8
+        // the references: rescale only when one grows by more than 2^8
         // (loads first, and no branches among them: a load behind a condition would
         // wait for the one before)
-        float mt[GT], old[GT], cs[GT];
+        float mt[GT], old[GT];
 #pragma unroll
         for (int i = 0; i < GT; ++i) {
-          mt[i] = top4(got[i]);
-          cs[i] = col[i];
+          mt[i] = top4(got[i]);   // (-inf where no column sees a key)
           old[i] = m[i];
         }
-        bool any = rr != 1.0f;
+        bool any = false;
 #pragma unroll
         for (int i = 0; i < GT; ++i) {
-          mt[i] *= cs[i];   // (-inf where no column sees a key)
           // grows past old + 8, or past -inf at all
           const bool grows = mt[i] > fmaxf(old[i] + 8.0f, -3.0e38f);
           mt[i] = grows ? mt[i] : old[i];
           any |= grows;
         }
-        // m and R are the same in every thread, so the decision is too; the vote
+        // m is the same in every thread, so the decision is too; the vote
         // keeps the warp-collective TMEM accesses below uniform regardless.
         any = __any_sync(0xffffffffu, any);
         if (any) {
           float r[16];
 #pragma unroll
-          for (int i = 0; i < 16; ++i) r[i] = rr;
+          for (int i = 0; i < 16; ++i) r[i] = 1.0f;
 #pragma unroll
           for (int i = 0; i < GT; ++i) {
-            const float q = old[i] == mt[i] ? 1.0f : ex2_approx(old[i] - mt[i]);   // (from -inf: 0)
-            l[i] *= q;
-            r[i] *= q;
+            // (from -inf: 0; by halves, since l has the range for 2^-189, from rows of zeros to the largest scale)
+            const float h = old[i] == mt[i] ? 1.0f : ex2_approx(0.5f * (old[i] - mt[i]));
+            l[i] = l[i] * h * h;
+            r[i] = r[8 + i] = h * h;
           }
           __syncwarp();
 #pragma unroll
@@ -493,19 +482,39 @@ __global__ void __launch_bounds__(kThreads, 1) tree_kernel(const __grid_constant
             float o[16];
             tld<16>(t_u, o);
 #pragma unroll
-            for (int i = 0; i < GT; ++i) o[i] *= r[i];
+            for (int i = 0; i < 16; ++i) o[i] *= r[i];
             tst16(t_u, o);
             tmem_wait_st();
           }
         }
+        // P^T, and 2^11 times its rest as columns 8 on, whose products cost nothing more
+        auto weight = [&](int i, int y) {
+          const float e = ex2_approx(fmaf(s[y][i], cs[i], (kHeldUp + kMiddle) - fmaxf(mt[i], -3.0e38f)));
+          l[i] += e;
+          return e * f[y];
+        };
+        auto store = [&](int i, int y, uint32_t high, uint32_t rest) {
+          const uint32_t at = (pbuf ^ ((i & 7) << 4)) + (y * N + i) * 128;
+          store16(at, high);
+          store16(at + 8 * 128, rest);
+        };
+        if constexpr (kTPS == 2 || GT == 1) {
 #pragma unroll
-        for (int i = 0; i < GT; ++i) {
-          const float mh = fmaxf(mt[i], -3.0e38f) - kPLift;   // (finite)
+          for (int i = 0; i < GT; ++i) {
+            uint32_t high, rest;
+            const float a = weight(i, 0);
+            split2(make_float2(a, kTPS == 2 ? weight(i, kTPS - 1) : 0.0f), high, rest);
+            store(i, 0, high, rest);
+            if constexpr (kTPS == 2) store(i, 1, high >> 16, rest >> 16);
+          }
+        } else {
 #pragma unroll
-          for (int y = 0; y < kTPS; ++y) {
-            const float e = ex2_approx(fmaf(s[y][i], cs[i], -mh));
-            l[i] += e;
-            store_half((pbuf ^ ((i & 7) << 4)) + (y * N + i) * 128, e * f[y]);
+          for (int i = 0; i < GT; i += 2) {
+            uint32_t high, rest;
+            const float a = weight(i, 0);
+            split2(make_float2(a, weight(i + 1, 0)), high, rest);
+            store(i, 0, high, rest);
+            store(i + 1, 0, high >> 16, rest >> 16);
           }
         }
         if (strange) {
@@ -515,8 +524,7 @@ __global__ void __launch_bounds__(kThreads, 1) tree_kernel(const __grid_constant
             const int y = i / GT, h = i - y * GT;
             const float v = y == 0 ? vs[0] : vs[kTPS - 1];
             const uint32_t seen = y == 0 ? vis[0] : vis[kTPS - 1];
-            if (!(v * inv_r <= 4.0f) && ((seen >> h) & 1))
-              store_half((pbuf ^ ((h & 7) << 4)) + (y * N + h) * 128, __uint_as_float(0x7fffffffu));
+            if (!(v <= kMostScale) && ((seen >> h) & 1)) store16((pbuf ^ ((h & 7) << 4)) + (y * N + h) * 128, kNan2);
           }
         }
         fence_proxy_async_smem();
@@ -527,20 +535,19 @@ __global__ void __launch_bounds__(kThreads, 1) tree_kernel(const __grid_constant
       }
       if (!ok) break;
       if (lane == 0) mbar_arrive(b_q_empty + 8 * qs);   // (what it read of the slot: the columns' factors and masks)
-      // the piece's exp-sums over all its keys, then u^T R / l (rolled over the
+      // the piece's exp-sums over all its keys, then u^T / l (rolled over the
       // columns: this code runs once per unit)
       put_folded(fold_columns<GT>(l, lane, [](float a, float b) { return a + b; }));
       if (!meet()) break;
-      const float4* got = red + ((red_cnt - 1) & 1) * (GT + 1);
+      const float4* got = red + ((red_cnt - 1) & 1) * GT;
       auto sum_of = [&](int h) {
         const float4 v = got[h];
         return (v.x + v.y) + (v.z + v.w);
       };
       float* fin_m = reinterpret_cast<float*>(smem + C::kOffFin);
       float* fin_l = fin_m + GT;
-      float* fin_r = fin_l + GT;
       if (grp == 1) {
-        // hands its maxima and sums over (of no step: -inf and 0), once the first group
+        // hands its references and sums over (of no step: -inf and 0), once the first group
         // has read those of the unit before
         if (units_done > 0 &&
             !wait_warp(b_o_free, (units_done - 1) & 1, wc, ATTN_DEVERR_WAIT_TIMEOUT_SITE(kSiteODone)))
@@ -550,7 +557,6 @@ __global__ void __launch_bounds__(kThreads, 1) tree_kernel(const __grid_constant
             fin_m[lane] = m[lane];
             fin_l[lane] = sum_of(lane);
           }
-          if (lane == 0) *fin_r = R;
           __syncwarp();
           if (lane == 0) mbar_arrive(b_fin);
         }
@@ -566,32 +572,25 @@ __global__ void __launch_bounds__(kThreads, 1) tree_kernel(const __grid_constant
       tc_fence_after();
       const bool whole = w.t0 == 0 && w.t1 == w.T;
       const int slot = 2 * blockIdx.x + (w.t0 == 0 ? 1 : 0);
-      // A column's maximum and sum, and the factors of the groups' u^T over the sum
-      // (0: it has none); a lane per column, left in shared memory for the warp
+      // log2 of a column's sum, and the factors of the groups' u^T (join); a lane per
+      // column, left in shared memory for the warp
       float4* factors = reinterpret_cast<float4*>(smem + C::kOffFactor) + (4 * grp + sw) * GT;
       if (lane < GT) {
-        float lh = sum_of(lane), mx = m[lane];
-        float w0 = lh != 0.0f ? R : 0.0f, w1 = 0.0f;
-        const float m1 = fin_m[lane], l1 = fin_l[lane];
-        if (l1 != 0.0f) {
-          const float top = lh != 0.0f ? fmaxf(mx, m1) : m1;
-          const float a = lh != 0.0f ? ex2_approx(mx - top) : 0.0f, b = ex2_approx(m1 - top);
-          w0 *= a;
-          w1 = b * *fin_r;
-          lh = (lh != 0.0f ? lh * a : 0.0f) + l1 * b;
-          mx = top;
-        }
-        const float inv = lh != 0.0f ? 1.0f / lh : 0.0f;   // 0: saw no key; a NaN stays one
-        factors[lane] = make_float4(mx, lh * kPDrop, w0 * inv, w1 * inv);
+        const Joined r = join(m[lane], sum_of(lane), fin_m[lane], fin_l[lane]);
+        factors[lane] = make_float4(r.sum, r.some ? 1.0f : 0.0f, r.f0, r.f1);
       }
       __syncwarp();
       auto joined = [&](int h) {
         const float4 f = factors[h];
-        float a[1], b[1];
+        float a[1], b[1], ar[1], br[1];   // of P^T, and of its rest
         tld_start<1>(t_u + h, a);
+        tld_start<1>(t_u + h + 8, ar);
         tld_start<1>(t_u + C::kRows + h, b);
+        tld_start<1>(t_u + C::kRows + h + 8, br);
         tld_wait<1>(a, b);
-        return (f.z != 0.0f ? a[0] * f.z : 0.0f) + (f.w != 0.0f ? b[0] * f.w : 0.0f);
+        tie<1>(ar);
+        tie<1>(br);
+        return (f.z < 0.0f ? 0.0f : fmaf(ar[0], 0x1p-11f, a[0]) * f.z) + (f.w < 0.0f ? 0.0f : fmaf(br[0], 0x1p-11f, b[0]) * f.w);
       };
       // u = u_a + u_b at head dimension 64: lanes 64-127 hand u_b over in the
       // first P^T buffer, idle now that every P.V that read
@@ -627,14 +626,13 @@ __global__ void __launch_bounds__(kThreads, 1) tree_kernel(const __grid_constant
         }
       }
       if (sw == 0 && lane < G) {
-        const float mx = factors[lane].x, lh = factors[lane].y;
+        const float4 r = factors[lane];
         if (whole) {
           int head;
           const long long row = out_row(lane, head);
-          p.lse[static_cast<long long>(head) * p.total + row] =
-              (lh != 0.0f) ? mx * 0.69314718055994531f + __logf(lh) : -INFINITY;
+          p.lse[static_cast<long long>(head) * p.total + row] = r.x * 0.69314718055994531f;
         } else {
-          p.part_ml[slot * N + lane] = make_float2(mx, lh);
+          p.part_ml[slot * N + lane] = make_float2(r.x, r.y);
         }
       }
       tc_fence_before();

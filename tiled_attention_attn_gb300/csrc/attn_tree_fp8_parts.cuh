@@ -28,8 +28,19 @@ constexpr int kThreads = 512;
 constexpr int kRegsFew = 88, kRegsMany = 168;
 static_assert(2 * (kRegsFew + kRegsMany) <= 512, "the launch's registers");
 constexpr int kRing = 8;                // stages of scales
-constexpr float kPLift = 7.0f;          // log2 of the factor of P'
-constexpr float kPDrop = 0x1p-7f;
+// A key that a row (a query's column) sees weighs p = 2^s, s its score in powers of two, and
+// its value row's scale is vs.  The row's reference m is the running maximum of s + log2 vs
+// over what it sees (it may lag by 8), so that P' = p vs 2^-m is measured by what reaches the
+// row's output: neither a key that it does not see nor one without weight counts there,
+// however large its value row.  P' is held times 2^kHeldUp in fp16, which has 2^8 to spare
+// above (the lag) and keeps P' to 2^-32 below.  Scales count in m as 2^-70 at the least
+// (rows of zeros have 2^-126).  l sums p itself in fp32, relative to m: times 2^(kHeldUp +
+// kMiddle), and P' takes 2^-kMiddle with the scale, which puts scales from 2^-70 to 2^119
+// (the largest there is) around the middle of fp32's range.
+constexpr float kHeldUp = 7.0f, kMiddle = 15.0f;
+constexpr float kScaleDown = 0x1p-15f, kScaleUp = 0x1p15f;
+constexpr float kLeastInRef = 0x1p-70f;
+constexpr float kMostScale = 3.402823466e38f;   // (larger: none, or no number)
 
 // The CTA's walk over units: (b, hc) in order, unit at position p of the line
 // of steps with T steps and one more for its fixed cost.
@@ -258,8 +269,34 @@ __device__ __forceinline__ void tst16(uint32_t taddr, const float (&x)[16]) {
   tmem_st_32x32b_x16(taddr, r);
 }
 
-__device__ __forceinline__ void store_half(uint32_t at, float x) {
-  asm volatile("st.shared.b16 [%0], %1;" :: "r"(at), "h"(__half_as_ushort(__float2half_rn(x))) : "memory");
+__device__ __forceinline__ void store16(uint32_t at, uint32_t x) {
+  asm volatile("st.shared.b16 [%0], %1;" :: "r"(at), "h"(static_cast<unsigned short>(x)) : "memory");
+}
+constexpr uint32_t kNan2 = 0x7fff7fffu;   // two fp16 NaN
+
+// log2 of a value's scale, as the rows' references count it (none, where it is no number).
+__device__ __forceinline__ float scale_log2(float vs) {
+  return vs <= kMostScale ? __log2f(fmaxf(vs, kLeastInRef)) : -70.0f;
+}
+
+// What joins two parts (m, l) of a row: log2 of the sum of its weights (-inf: none), and the
+// factors that bring each part's u to O (negative: it saw no key, and its u is nothing).
+// By the logarithms of the sums, which do not depend on the parts' references.
+struct Joined {
+  float sum, f0, f1;
+  bool some;
+};
+__device__ __forceinline__ Joined join(float m0, float l0, float m1, float l1) {
+  const bool has0 = l0 != 0.0f, has1 = l1 != 0.0f;   // (a NaN is something, and stays)
+  const float a = m0 + __log2f(l0), b = m1 + __log2f(l1);
+  const float top = !has1 ? a : has0 ? fmaxf(a, b) : b;
+  const float w0 = has0 ? ex2_approx(a - top) : 0.0f, w1 = has1 ? ex2_approx(b - top) : 0.0f, w = w0 + w1;
+  Joined r;
+  r.some = has0 || has1;
+  r.sum = r.some ? top + __log2f(w) - (kHeldUp + kMiddle) : -INFINITY;
+  r.f0 = has0 ? w0 / (l0 * w) * kScaleUp : -1.0f;
+  r.f1 = has1 ? w1 / (l1 * w) * kScaleUp : -1.0f;
+  return r;
 }
 
 // Combines n columns (a power of two, at most 8 here) over the warp's lanes: each
@@ -287,6 +324,13 @@ __device__ __forceinline__ uint32_t widen2(uint32_t x) {
   uint32_t h;
   asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(h) : "h"(static_cast<unsigned short>(x)));
   return h;
+}
+// x as two fp16 pairs: the nearest, and 2^11 times the rest.
+__device__ __forceinline__ void split2(float2 x, uint32_t& high, uint32_t& rest) {
+  high = pack2<false>(x.x, x.y);
+  const float2 h = __half22float2(*reinterpret_cast<const __half2*>(&high));
+  const float2 r = fmul2(fadd2(x, make_float2(-h.x, -h.y)), make_float2(2048.0f, 2048.0f));
+  rest = pack2<false>(r.x, r.y);
 }
 // Two floats as the nearest e4m3 pair, which is taken off them.
 __device__ __forceinline__ uint32_t take2(float& a, float& b) {

@@ -5,9 +5,9 @@
 // so that a softmax thread owns a row and needs no other thread for its maximum and
 // sum.  (With the columns on N, as in attn_tree_fp8_kernel.cuh, their maxima over the
 // keys are exchanges between threads: eight trees of 64 tokens, 32 heads on 8 of 128,
-// over 16,384 keys took 579 us; 138 us here.)
+// over 16,384 keys took 579 us; 143 us here.)
 //
-// Two groups of four softmax warps take 64 of a step's 128 keys each, with maxima, sums
+// Two groups of four softmax warps take 64 of a step's 128 keys each, with references, sums
 // and an accumulator of their own, joined at the unit's end, while S of the next step and
 // P V of the last run.  P overwrites the S that it comes from.  (Taking whole steps in
 // turns, a group waited for the P V and the S that have to follow its P: 220 us against
@@ -17,9 +17,13 @@
 // operands (143); with the scales copied by the loading warps 138.  Bound by the softmax
 // warps: a step takes 2,200 cycles, of which a group is at work for 1,500 to 2,100; the
 // tensor pipe is 37 % busy (its floor for the 64 tokens is 51 us).
-// The rest is as in attn_tree_fp8_kernel.cuh: V widened to
-// fp16 by four warps, weights in fp16 times their value's scale over R, R a power of
-// two above the scales so far.
+// The rest is as in attn_tree_fp8_kernel.cuh, but that P' is one fp16 value, off by 2^-11 of
+// itself: a second one would double the products of P V, and V and P as bf16 values, which
+// need no reference, took 180 us (its widening 14, the two values 9).  The references
+// by p vs instead of p and a common one of the scales: 138 to 143 us.  (A step looks
+// for the largest p vs with an addition per key.  A cheaper bound that is exact where the
+// scales are much the same, with a branch for where they are not, took 153 us, the branch
+// taken or not.)
 #pragma once
 #include "attn_tree_fp8_parts.cuh"
 
@@ -36,11 +40,11 @@ struct RowsCfg {
   static constexpr int kOffW = kOffV + kStages * T::kRaw;
   static constexpr int kOffQ = kOffW + 2 * T::kWide;
   static constexpr int kOffScale = kOffQ + 3 * kQPiece;          // [kRing][k, v][128] floats
-  static constexpr int kOffF = kOffScale + kRing * 2 * 128 * 4;  // [softmax warp][64] floats: vs / R
-  static constexpr int kOffMask = kOffF + 8 * 64 * 4;           // [128] 64-bit words
+  static constexpr int kOffF = kOffScale + kRing * 2 * 128 * 4;  // [softmax warp][2][64] floats: vs 2^-kMiddle, log2 vs
+  static constexpr int kOffMask = kOffF + 8 * 2 * 64 * 4;           // [128] 64-bit words
   static constexpr int kOffCol = kOffMask + 128 * 8;             // [128] floats
-  static constexpr int kOffFin = kOffCol + 128 * 4;              // the second group's (m, l) per row, then R
-  static constexpr int kOffBar = kOffFin + 128 * 8 + 16;
+  static constexpr int kOffFin = kOffCol + 128 * 4;              // the second group's (m, l) per row
+  static constexpr int kOffBar = kOffFin + 128 * 8;
   static constexpr int kNBars = 4 * kStages + 10 + kRing + 3;
   static constexpr int kOffMisc = kOffBar + (kNBars * 8 + 15) / 16 * 16;
   static constexpr int kSmem = kOffMisc + 512 + 1024;
@@ -221,9 +225,8 @@ __global__ void __launch_bounds__(kThreads, 1) tree_rows_kernel(const __grid_con
     const int row = quarter * 32 + lane;           // of the unit
     const uint32_t t_lane = tmem + (static_cast<uint32_t>(quarter * 32) << 16);
     const uint32_t t_u = t_lane + C::kColU;
-    float* factor = reinterpret_cast<float*>(smem + C::kOffF) + sw * 64;   // this warp's copy of vs / R
+    float* factor = reinterpret_cast<float*>(smem + C::kOffF) + sw * 128;   // this warp's, of the values' scales
     float2* fin = reinterpret_cast<float2*>(smem + C::kOffFin);
-    float* fin_r = reinterpret_cast<float*>(smem + C::kOffFin + 128 * 8);
     uint32_t step = 0, units_done = 0;
     bool ok = true;
     for (bool more = next_unit<KS>(p, w, true); more && ok; more = next_unit<KS>(p, w, false)) {
@@ -256,11 +259,41 @@ __global__ void __launch_bounds__(kThreads, 1) tree_rows_kernel(const __grid_con
       if (lane == 0) mbar_arrive(b_q_empty);
       // warps without a row leave their part of P as it is: rows of their own alone
       const bool idle = quarter * 32 >= u.cols;
-      float m = -INFINITY, l = 0.0f, R = 0.0f, inv_r = 0.0f;
+      float m = -INFINITY, l = 0.0f;
+      // which of the 32 keys from `key` on this row sees
+      auto seen = [&](int key) {
+        const int at = key - w.ctx;   // the first among the new tokens
+        const uint32_t tree = at >= 64 ? 0u : at >= 0 ? static_cast<uint32_t>(mask >> at)
+                              : at > -32 ? static_cast<uint32_t>(mask) << -at : 0u;
+        return (low_bits(-at) | tree) & low_bits(w.n - key);
+      };
       for (int t = w.t0; t < w.t1; ++t) {
         const int sb = step & 1, ring = step % kRing;
-        if (!wait_warp(b_c_full + 8 * ring, (step / kRing) & 1, wc, ATTN_DEVERR_WAIT_TIMEOUT_SITE(kSiteSFree)) ||
-            !wait_warp(b_s_full + 8 * sb, (step >> 1) & 1, wc, ATTN_DEVERR_WAIT_TIMEOUT_SITE(kSiteSFull))) {
+        if (!wait_warp(b_c_full + 8 * ring, (step / kRing) & 1, wc, ATTN_DEVERR_WAIT_TIMEOUT_SITE(kSiteSFree))) {
+          ok = false;
+          break;
+        }
+        const uint32_t t_s = t_lane + sb * 128 + grp * 64;   // this group's keys
+        const float* ks = reinterpret_cast<const float*>(smem + C::kOffScale) + ring * 2 * 128 + grp * 64;
+        const int k0 = t * KS + grp * 64;
+        // the values' scales: two keys per lane, for the warp
+        uint32_t strange = 0;   // bit i: the lane's key i has no number for a scale
+        {
+          const float2 v2 = reinterpret_cast<const float2*>(ks + 128)[lane];
+          float v[2] = {v2.x, v2.y};
+#pragma unroll
+          for (int i = 0; i < 2; ++i) {
+            v[i] = k0 + 2 * lane + i < w.n ? v[i] : 0.0f;
+            if (!(v[i] <= kMostScale)) {
+              strange |= 1u << i;
+              v[i] = 0.0f;
+            }
+          }
+          reinterpret_cast<float2*>(factor)[lane] = make_float2(v[0] * kScaleDown, v[1] * kScaleDown);
+          reinterpret_cast<float2*>(factor)[32 + lane] = make_float2(scale_log2(v[0]), scale_log2(v[1]));
+          __syncwarp();
+        }
+        if (!wait_warp(b_s_full + 8 * sb, (step >> 1) & 1, wc, ATTN_DEVERR_WAIT_TIMEOUT_SITE(kSiteSFull))) {
           ok = false;
           break;
         }
@@ -272,50 +305,12 @@ __global__ void __launch_bounds__(kThreads, 1) tree_rows_kernel(const __grid_con
           ++step;
           continue;
         }
-        const uint32_t t_s = t_lane + sb * 128 + grp * 64;   // this group's keys
-        const float* ks = reinterpret_cast<const float*>(smem + C::kOffScale) + ring * 2 * 128 + grp * 64;
-        const int k0 = t * KS + grp * 64;
-        // the values' reference and factors: two keys per lane, for the warp
-        float rr = 1.0f;
-        uint32_t strange = 0;   // bit i: the lane's key i has no number for a scale
-        {
-          const float2 v2 = reinterpret_cast<const float2*>(ks + 128)[lane];
-          float v[2] = {v2.x, v2.y};
-          uint32_t top = 0;
-#pragma unroll
-          for (int i = 0; i < 2; ++i) {
-            v[i] = k0 + 2 * lane + i < w.n ? v[i] : 0.0f;
-            top = v[i] > 0.0f ? max(top, __float_as_uint(v[i])) : top;
-          }
-          top = __reduce_max_sync(0xffffffffu, top);
-          if (top >= __float_as_uint(R) && top > 0) {
-            const uint32_t e = min((top >> 23) + 1, 253u);
-            inv_r = __uint_as_float((254u - e) << 23);
-            rr = R * inv_r;
-            R = __uint_as_float(e << 23);
-          }
-#pragma unroll
-          for (int i = 0; i < 2; ++i) {
-            v[i] *= inv_r;
-            if (!(v[i] <= 4.0f)) {
-              strange |= 1u << i;
-              v[i] = 0.0f;
-            }
-          }
-          reinterpret_cast<float2*>(factor)[lane] = make_float2(v[0], v[1]);
-          __syncwarp();
-        }
         // which keys this row sees: all, but in the tiles that hold new tokens or the end
         const bool all = k0 + 64 <= min(w.ctx, w.n);
         uint32_t vis[2] = {0xffffffffu, 0xffffffffu};
         if (!all) {
 #pragma unroll
-          for (int i = 0; i < 2; ++i) {
-            const int at = 32 * i + k0 - w.ctx;   // the word's first key among the new tokens
-            const uint32_t tree = at >= 64 ? 0u : at >= 0 ? static_cast<uint32_t>(mask >> at)
-                                  : at > -32 ? static_cast<uint32_t>(mask) << -at : 0u;
-            vis[i] = (low_bits(-at) | tree) & low_bits(w.n - k0 - 32 * i);
-          }
+          for (int i = 0; i < 2; ++i) vis[i] = seen(k0 + 32 * i);
         }
         // S of the 64 keys, times the keys' scales, -inf where this row does not see the key
         float s[64];
@@ -336,24 +331,31 @@ __global__ void __launch_bounds__(kThreads, 1) tree_rows_kernel(const __grid_con
           for (int i = 0; i < 64; ++i)
             if (!((vis[i >> 5] >> (i & 31)) & 1)) s[i] = -INFINITY;
         }
-        float top = fmaxf(s[0], s[1]);
+        // the largest s + log2 vs
+        float mt = -INFINITY;
         {
-          float a = fmaxf(s[2], s[3]), b = fmaxf(s[4], s[5]), c = fmaxf(s[6], s[7]);
+          float a = mt, b = mt, c = mt;
 #pragma unroll
-          for (int i = 8; i < 64; i += 8) {
-            top = fmax3(top, s[i], s[i + 1]);
-            a = fmax3(a, s[i + 2], s[i + 3]);
-            b = fmax3(b, s[i + 4], s[i + 5]);
-            c = fmax3(c, s[i + 6], s[i + 7]);
+          for (int i = 0; i < 64; i += 8) {
+            const float4 u4 = reinterpret_cast<const float4*>(factor)[16 + i / 4], v4 = reinterpret_cast<const float4*>(factor)[17 + i / 4];
+            const float2 cs2 = make_float2(cs, cs);
+            const float2 x0 = ffma2(make_float2(s[i], s[i + 1]), cs2, make_float2(u4.x, u4.y));
+            const float2 x1 = ffma2(make_float2(s[i + 2], s[i + 3]), cs2, make_float2(u4.z, u4.w));
+            const float2 x2 = ffma2(make_float2(s[i + 4], s[i + 5]), cs2, make_float2(v4.x, v4.y));
+            const float2 x3 = ffma2(make_float2(s[i + 6], s[i + 7]), cs2, make_float2(v4.z, v4.w));
+            mt = fmax3(mt, x0.x, x0.y);
+            a = fmax3(a, x1.x, x1.y);
+            b = fmax3(b, x2.x, x2.y);
+            c = fmax3(c, x3.x, x3.y);
           }
-          top = fmaxf(fmax3(top, a, b), c);
+          mt = fmaxf(fmax3(mt, a, b), c);
         }
-        // running max (scaled units): rescale only when it grows by more than 2^8, or past -inf at all
-        const float mt = top * cs;
+        // the reference: rescale only when it grows by more than 2^8, or past -inf at all
         const bool grows = mt > fmaxf(m + 8.0f, -3.0e38f);
-        if (__any_sync(0xffffffffu, grows || rr != 1.0f)) {
-          const float q = grows ? ex2_approx(m - mt) : 1.0f, f = q * rr;   // (from -inf: 0)
-          l *= q;
+        if (__any_sync(0xffffffffu, grows)) {
+          // (from -inf: 0; by halves, since l has the range for 2^-189, from rows of zeros to the largest scale)
+          const float h = grows ? ex2_approx(0.5f * (m - mt)) : 1.0f, q = h * h;
+          l = l * h * h;
           m = grows ? mt : m;
           if (t > w.t0) {
             if (!wait_pv(b_pv_done, step - 1, wc)) { ok = false; break; }
@@ -364,12 +366,12 @@ __global__ void __launch_bounds__(kThreads, 1) tree_rows_kernel(const __grid_con
               tmem_ld_32x32b_x32(t_u + grp * DA + c, o);
               tmem_wait_ld(o);
 #pragma unroll
-              for (int i = 0; i < 32; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * f);
+              for (int i = 0; i < 32; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * q);
               tmem_st_32x32b_x32(t_u + grp * DA + c, o);
             }
           }
         }
-        const float mh = fmaxf(m, -3.0e38f) - kPLift;   // (finite)
+        const float mh = fmaxf(m, -3.0e38f) - (kHeldUp + kMiddle);   // (finite)
         const float2 cs2 = make_float2(cs, cs), mh2 = make_float2(-mh, -mh);
         float2 la = make_float2(0.0f, 0.0f), lb = la;
 #pragma unroll
@@ -407,7 +409,7 @@ __global__ void __launch_bounds__(kThreads, 1) tree_rows_kernel(const __grid_con
           tmem_wait_st();
           asm volatile("tcgen05.ld.sync.aligned.32x32b.x1.b32 {%0}, [%1];\n\ttcgen05.wait::ld.sync.aligned;"
                        : "=r"(one[0]) : "r"(t_s) : "memory");
-          if (hit) one[0] = 0x7fff7fffu;
+          if (hit) one[0] = kNan2;
           asm volatile("tcgen05.st.sync.aligned.32x32b.x1.b32 [%0], {%1};" :: "r"(t_s), "r"(one[0]) : "memory");
         }
         tmem_wait_st();
@@ -424,7 +426,6 @@ __global__ void __launch_bounds__(kThreads, 1) tree_rows_kernel(const __grid_con
             !wait_warp(b_o_free, (units_done - 1) & 1, wc, ATTN_DEVERR_WAIT_TIMEOUT_SITE(kSiteODone)))
           break;
         fin[row] = make_float2(m, l);
-        if (sw == 4 && lane == 0) *fin_r = R;   // (the same in every warp that has rows, and the first has)
         __syncwarp();
         if (lane == 0) mbar_arrive(b_fin);
         ++units_done;
@@ -435,18 +436,7 @@ __global__ void __launch_bounds__(kThreads, 1) tree_rows_kernel(const __grid_con
       tc_fence_after();
       if (!idle) {
         const float2 other = fin[row];
-        float w0 = l != 0.0f ? R : 0.0f, w1 = 0.0f;
-        if (other.y != 0.0f) {
-          const float mx = l != 0.0f ? fmaxf(m, other.x) : other.x;
-          const float a = l != 0.0f ? ex2_approx(m - mx) : 0.0f, b = ex2_approx(other.x - mx);
-          w0 *= a;
-          w1 = b * *fin_r;
-          l = (l != 0.0f ? l * a : 0.0f) + other.y * b;
-          m = mx;
-        }
-        const float inv = l != 0.0f ? 1.0f / l : 0.0f;   // 0: saw no key; a NaN stays one
-        w0 *= inv;
-        w1 *= inv;
+        const Joined f = join(m, l, other.x, other.y);
         const bool whole = w.t0 == 0 && w.t1 == w.T;
         const int slot = 2 * blockIdx.x + (w.t0 == 0 ? 1 : 0);
         float* part = p.part_o + (static_cast<size_t>(slot) * N + row) * DA;
@@ -457,7 +447,7 @@ __global__ void __launch_bounds__(kThreads, 1) tree_rows_kernel(const __grid_con
           tld_start<16>(t_u + DA + c, b);
           tld_wait<16>(a, b);
 #pragma unroll
-          for (int i = 0; i < 16; ++i) a[i] = (w0 != 0.0f ? a[i] * w0 : 0.0f) + (w1 != 0.0f ? b[i] * w1 : 0.0f);
+          for (int i = 0; i < 16; ++i) a[i] = (f.f0 < 0.0f ? 0.0f : a[i] * f.f0) + (f.f1 < 0.0f ? 0.0f : b[i] * f.f1);
           if (mine && whole) {
             uint32_t v[8];
 #pragma unroll
@@ -472,12 +462,8 @@ __global__ void __launch_bounds__(kThreads, 1) tree_rows_kernel(const __grid_con
           }
         }
         if (mine) {
-          l *= kPDrop;
-          if (whole)
-            p.lse[static_cast<long long>(head) * p.total + q_row] =
-                (l != 0.0f) ? m * 0.69314718055994531f + __logf(l) : -INFINITY;
-          else
-            p.part_ml[slot * N + row] = make_float2(m, l);
+          if (whole) p.lse[static_cast<long long>(head) * p.total + q_row] = f.sum * 0.69314718055994531f;
+          else p.part_ml[slot * N + row] = make_float2(f.sum, f.some ? 1.0f : 0.0f);
         }
         // the unit's pieces lie on the ranges p / range ... (p + T - 1) / range
         if (!whole && w.t0 == 0 && row == 0)
