@@ -647,7 +647,7 @@ int attn_cache_read_fp8(void *k, void *v, int B, int total, const attn_paged_kv8
  * chain t <= i.
  *     o = softmax(scale q . K) V over what it sees,  lse (Hq, total) fp32;
  * a token that sees nothing gives o = 0 and lse = -inf, one that sees a NaN score or
- * value NaN.  Of a row of q, features are held to 2^-17 of its largest; of a weight
+ * value NaN.  Of a row of q, features are held to 2^-21 of its largest; of a weight
  * times its value's scale, 22 bits where max_tokens Hq / num_kv_heads <= 8 and 11 bits
  * otherwise, to 2^-30 of the row's largest (scales below 2^-70 count as 2^-70 there).
  * Rows outside every sequence are left as they are.  Hq a multiple of

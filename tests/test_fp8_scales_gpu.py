@@ -220,3 +220,41 @@ def test_value_rows_without_a_number(form, n, bad):
     o, lse = attn.attn_tree_fp8(q, *c.args(), cu_of([T]), tree_mask=masks, max_tokens=T)
     ok()
     assert bool(o.isnan().all()) and bool(torch.isfinite(lse).all())
+
+
+@pytest.mark.parametrize("dtype", [BF, HF])
+@pytest.mark.parametrize("octaves", [0, 8, 13])
+@pytest.mark.parametrize("form", [(64, 2, 1), (128, 8, 1), (64, 4, 4), (64, 32, 1), (128, 8, 9), (64, 16, 12)], ids=str)
+def test_queries_with_one_large_feature(form, octaves, dtype):
+    """Keys that are zero where the queries are large: the scores are made of the other
+    features, which are all of one sign, so that what each loses adds up.  In the unit in
+    which the largest is 2^8, a feature is 2^-5 or more here: in bf16 exact, as two values of
+    4 or 3 bits.  In fp16 as e4m3, e4m3 and e5m2, what is left below e4m3's smallest step, at
+    most 2^-10, keeps three bits: off by 2^-14, 2^-22 of the largest."""
+    d, hq, T = form
+    n, scale = 400, 1 / math.sqrt(d)
+    c = Cache8([n], 2, d, 16, 6)
+    g = torch.Generator().manual_seed(4)
+    q = (1 + torch.rand(T, hq, d, generator=g)).to(dtype)
+    q[..., 0] = 2.0 ** octaves
+    k = (torch.rand(n, 2, 1, generator=g) * 8 / (1.5 * d * scale)).expand(-1, -1, d).clone()
+    k[..., 0] = 0.0
+    page, slot = c.places(0)
+    k8, ks = ref.quantise(k.cuda())
+    c.k.view(torch.uint8)[page, slot], c.ks[page, slot] = k8.view(torch.uint8), ks
+    q = q.cuda()
+    o, lse = attn.attn_tree_fp8(q, *c.args(), cu_of([T]), max_tokens=T)
+    ok()
+    (k, ks), (v, vs) = c.rows(0, "k"), c.rows(0, "v")
+    small = q.clone()
+    small[..., 0] = 0.0      # what the scores are made of
+    want, rl, a, _ = ref.attention(small, k, ks, v, vs, None, scale)
+    kk = k * ks[..., None]
+    ds = 2.0 ** -18 + score_error(small, kk, scale)
+    if dtype == HF:
+        ds += 2.0 ** -22 * 2.0 ** max(octaves, 1) * float(kk.abs().double().sum(-1).max()) * scale
+    bar = half_step(dtype) * want.abs() * 1.01 + (2.0 ** (-22 if T * hq <= 16 else -11) + 2 * ds) * 1.01 * a
+    bar = bar + (2.0 ** -25 if dtype == HF else 1e-30)
+    err = (o.double() - want).abs()
+    assert bool((err <= bar).all()), float((err / bar).max())
+    assert bool(((lse.double() - rl).abs() <= ds + 2.0 ** -20 + rl.abs() * 2.0 ** -22).all())

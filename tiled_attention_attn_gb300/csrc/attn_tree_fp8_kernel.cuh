@@ -11,8 +11,8 @@
 // K stays in e4m3 from HBM to the tensor core (kind::f8f6f4): what has 16 bits is
 // the query, and it is small.  A query row, times the power of two that brings its
 // largest value into (224, 448], is held as a sum of e4m3 values, two for bf16 and
-// three for fp16 (4 significant bits each, so 8 and 11 exactly; down to 2^-10,
-// which is 2^-17.8 of the largest), and S^T sums the products in fp32.  The key's
+// three for fp16 (4 significant bits each, so 8 and 11 exactly; see convert_queries for
+// the small features), and S^T sums the products in fp32.  The key's
 // scale and the row's power of two are applied to S.
 //
 // V is widened to fp16, which holds e4m3 exactly, by four warps between the TMA's
@@ -182,7 +182,7 @@ __global__ void __launch_bounds__(kThreads, 1) tree_kernel(const __grid_constant
         unsigned long long* mask = reinterpret_cast<unsigned long long*>(smem + C::kOffMask) + slot * N;
         if (!wait_warp(b_q_empty + 8 * slot, ((cnt / kSlots) & 1) ^ 1, wc,
                             ATTN_DEVERR_WAIT_TIMEOUT_SITE(kSiteQEmpty))) break;
-        convert_queries<DA, 1>(p, w, u, 0, 1, dst, C::kQPiece, col, mask);
+        convert_queries<DA, 1, true>(p, w, u, 0, 1, dst, C::kQPiece, col, mask);
         fence_proxy_async_smem();
         __syncwarp();
         if (lane == 0) mbar_arrive(b_q_full + 8 * slot);
@@ -315,11 +315,11 @@ __global__ void __launch_bounds__(kThreads, 1) tree_kernel(const __grid_constant
         tld_start<LD>(at + N, y);
         tld_wait<LD>(x, y);
 #pragma unroll
-        for (int i = 0; i < LD; ++i) x[i] += y[i];
+        for (int i = 0; i < LD; ++i) x[i] = fmaf(y[i], kPieceDown, x[i]);
         if (p.fp16) {
           tld<LD>(at + 2 * N, y);
 #pragma unroll
-          for (int i = 0; i < LD; ++i) x[i] += y[i];
+          for (int i = 0; i < LD; ++i) x[i] = fmaf(y[i], kPieceDown * kPieceDown, x[i]);
         }
       }
 #pragma unroll

@@ -40,6 +40,7 @@ constexpr int kRing = 8;                // stages of scales
 constexpr float kHeldUp = 7.0f, kMiddle = 15.0f;
 constexpr float kScaleDown = 0x1p-15f, kScaleUp = 0x1p15f;
 constexpr float kLeastInRef = 0x1p-70f;
+constexpr float kPieceUp = 0x1p4f, kPieceDown = 0x1p-4f;   // of the queries' pieces (convert_queries)
 constexpr float kMostScale = 3.402823466e38f;   // (larger: none, or no number)
 
 // The CTA's walk over units: (b, hc) in order, unit at position p of the line
@@ -188,9 +189,9 @@ __device__ __forceinline__ bool elect_one() {
   asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(on));
   return on != 0;
 }
-// kind::f8f6f4, e4m3 operands, both K-major.
-__host__ __device__ constexpr uint32_t idesc_e4m3(int M, int N) {
-  return (1u << 4) | (static_cast<uint32_t>(N >> 3) << 17) | (static_cast<uint32_t>(M >> 4) << 24);
+// kind::f8f6f4, A of e4m3 or e5m2 and B of e4m3, both K-major.
+__host__ __device__ constexpr uint32_t idesc_e4m3(int M, int N, bool a_e5m2 = false) {
+  return (1u << 4) | ((a_e5m2 ? 1u : 0u) << 7) | (static_cast<uint32_t>(N >> 3) << 17) | (static_cast<uint32_t>(M >> 4) << 24);
 }
 
 // 4-byte asynchronous copy to shared memory, and the arrival of this thread's
@@ -562,12 +563,18 @@ __device__ __forceinline__ void widen(const Params& p, Walk w, int place, uint8_
   }
 }
 
-// The rows of q that are columns c0, c0 + dc, ... of the unit, as e4m3 pieces (two or three of
+// The rows of q that are columns c0, c0 + dc, ... of the unit, as 8-bit pieces (two or three of
 // `piece` bytes, rows of DA bytes, swizzled), their factors (scale, log2 e and the power
-// of two, in one) and masks.  A warp takes F rows at a time, the next 2 F on their
+// of two, in one) and masks.  A row, its largest value in (224, 448], is the sum of its
+// pieces, each the nearest to what the one before leaves, which is half its step.  STEPPED:
+// e4m3 pieces, each kPieceUp times the scale of the one before (what is left reaches 2^8 then,
+// of 448).  Otherwise their products are summed as they are: e4m3 pieces, the last e5m2,
+// whose three bits are what is left of 8 (after one) or 11 (after two) and which reaches
+// down to 2^-16.  A feature is off by 2^-14, 2^-21.8 of the row's largest, at the most, and
+// by nothing from 2^-6 on.  A warp takes F rows at a time, the next 2 F on their
 // way, in a loop: it runs once per unit, so fetching its code counts.  (Rows past u.cols
 // hold anything: nothing reads their results.)
-template <int DA, int F>
+template <int DA, int F, bool STEPPED>
 __device__ __forceinline__ void convert_queries(const Params& p, const Walk& w, const Unit& u, int c0, int dc, uint8_t* dst,
                                                 int piece, float* col, unsigned long long* mask) {
   constexpr int E = DA / 32;      // features per lane
@@ -637,14 +644,31 @@ __device__ __forceinline__ void convert_queries(const Params& p, const Walk& w, 
     }
     uint8_t* to = dst;
 #pragma unroll 1
-    for (int s = p.fp16 ? 3 : 2; s > 0; --s, to += piece) {
+    for (int s = (p.fp16 ? 3 : 2) - (STEPPED ? 0 : 1); s > 0; --s, to += piece) {
 #pragma unroll
       for (int f = 0; f < F; ++f) {
         const int at = c + f * dc;
-        const uint32_t a = take2(x[f][0], x[f][1]);
+        uint32_t a = take2(x[f][0], x[f][1]), b = 0;
+        if constexpr (E == 4) b = take2(x[f][2], x[f][3]);
+        if constexpr (STEPPED) {
+#pragma unroll
+          for (int e = 0; e < E; ++e) x[f][e] *= kPieceUp;
+        }
         uint8_t* y = to + swizzled<DA>(at, E * lane);
         if (F > 1 && at >= u.cols) continue;
-        if constexpr (E == 4) *reinterpret_cast<uint32_t*>(y) = a | take2(x[f][2], x[f][3]) << 16;
+        if constexpr (E == 4) *reinterpret_cast<uint32_t*>(y) = a | b << 16;
+        else *reinterpret_cast<uint16_t*>(y) = static_cast<uint16_t>(a);
+      }
+    }
+    if constexpr (!STEPPED) {
+#pragma unroll
+      for (int f = 0; f < F; ++f) {
+        const int at = c + f * dc;
+        const uint32_t a = __nv_cvt_float2_to_fp8x2(make_float2(x[f][0], x[f][1]), __NV_SATFINITE, __NV_E5M2);
+        const uint32_t b = E == 4 ? __nv_cvt_float2_to_fp8x2(make_float2(x[f][2], x[f][3]), __NV_SATFINITE, __NV_E5M2) : 0;
+        uint8_t* y = to + swizzled<DA>(at, E * lane);
+        if (F > 1 && at >= u.cols) continue;
+        if constexpr (E == 4) *reinterpret_cast<uint32_t*>(y) = a | b << 16;
         else *reinterpret_cast<uint16_t*>(y) = static_cast<uint16_t>(a);
       }
     }

@@ -1,11 +1,11 @@
 // The attention over caches of 8-bit floating point for trees with many columns
 // (token, head) per key/value head: they are the rows of the products,
-//   S = Q K^T   (M = 128 rows, N = 128 keys, K = d; e4m3, Q's pieces one after another)
+//   S = Q K^T   (M = 128 rows, N = 128 keys, K = d; 8 bits, Q's pieces one after another)
 //   u += P V    (M = 128 rows, N = d, K = 128 keys; P in tensor memory)
 // so that a softmax thread owns a row and needs no other thread for its maximum and
 // sum.  (With the columns on N, as in attn_tree_fp8_kernel.cuh, their maxima over the
 // keys are exchanges between threads: eight trees of 64 tokens, 32 heads on 8 of 128,
-// over 16,384 keys took 579 us; 143 us here.)
+// over 16,384 keys took 579 us; 141 us here.)
 //
 // Two groups of four softmax warps take 64 of a step's 128 keys each, with references, sums
 // and an accumulator of their own, joined at the unit's end, while S of the next step and
@@ -20,7 +20,7 @@
 // The rest is as in attn_tree_fp8_kernel.cuh, but that P' is one fp16 value, off by 2^-11 of
 // itself: a second one would double the products of P V, and V and P as bf16 values, which
 // need no reference, took 180 us (its widening 14, the two values 9).  The references
-// by p vs instead of p and a common one of the scales: 138 to 143 us.  (A step looks
+// by p vs instead of p and a common one of the scales cost 5 of 143 us.  (A step looks
 // for the largest p vs with an addition per key.  A cheaper bound that is exact where the
 // scales are much the same, with a branch for where they are not, took 153 us, the branch
 // taken or not.)
@@ -126,7 +126,8 @@ __global__ void __launch_bounds__(kThreads, 1) tree_rows_kernel(const __grid_con
       widen<DA, 1, N, kStages>(p, w, place, smem, C::kOffV, C::kOffW, b_v_full, b_v_empty, b_w_full, b_pv_done, wc);
     } else if (warp == kWarpMMA) {
       // ------------------------------------------------------------------ S's issuer
-      constexpr uint32_t kIdescS = idesc_e4m3(128, 128);
+      constexpr uint32_t kIdescS = idesc_e4m3(128, 128), kIdescLast = idesc_e4m3(128, 128, true);
+      const uint32_t idesc_1 = uniform(p.fp16 ? kIdescS : kIdescLast);   // (the last piece is e5m2)
       const uint32_t dq0 = desc_low(sbase + C::kOffQ, 16);
       const uint32_t dk0 = desc_low(sbase + C::kOffK, 16);
       uint32_t k_cnt = 0, units_done = 0;
@@ -155,7 +156,7 @@ __global__ void __launch_bounds__(kThreads, 1) tree_rows_kernel(const __grid_con
               if (s == 2 && !p.fp16) break;
 #pragma unroll
               for (int kk = 0; kk < DA / 32; ++kk)
-                mma_f8<kHighRows<DA>>(tm, a0 + ((s * C::kQPiece + kk * 32) >> 4), b0 + 2 * kk, kIdescS,
+                mma_f8<kHighRows<DA>>(tm, a0 + ((s * C::kQPiece + kk * 32) >> 4), b0 + 2 * kk, s == 0 ? kIdescS : s == 1 ? idesc_1 : kIdescLast,
                                       (s > 0 || kk > 0) ? 1u : 0u);
             }
             umma_commit(full);
@@ -247,7 +248,7 @@ __global__ void __launch_bounds__(kThreads, 1) tree_rows_kernel(const __grid_con
       if (w.t1 <= w.t0) continue;
       // the queries, by all eight warps, once the unit before is done with the last
       if (!wait_warp(b_q_empty, (units_done & 1) ^ 1, wc, ATTN_DEVERR_WAIT_TIMEOUT_SITE(kSiteQEmpty))) break;
-      convert_queries<DA, 4>(p, w, u, sw, 8, smem + C::kOffQ, C::kQPiece, reinterpret_cast<float*>(smem + C::kOffCol),
+      convert_queries<DA, 4, false>(p, w, u, sw, 8, smem + C::kOffQ, C::kQPiece, reinterpret_cast<float*>(smem + C::kOffCol),
                           reinterpret_cast<unsigned long long*>(smem + C::kOffMask));
       fence_proxy_async_smem();
       __syncwarp();
@@ -361,13 +362,12 @@ __global__ void __launch_bounds__(kThreads, 1) tree_rows_kernel(const __grid_con
             if (!wait_pv(b_pv_done, step - 1, wc)) { ok = false; break; }
             tc_fence_after();
 #pragma unroll 1
-            for (int c = 0; c < DA; c += 32) {
-              uint32_t o[32];
-              tmem_ld_32x32b_x32(t_u + grp * DA + c, o);
-              tmem_wait_ld(o);
+            for (int c = 0; c < DA; c += 16) {   // (by 32: 146 us against 141, the code being longer)
+              float o[16];
+              tld<16>(t_u + grp * DA + c, o);
 #pragma unroll
-              for (int i = 0; i < 32; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * q);
-              tmem_st_32x32b_x32(t_u + grp * DA + c, o);
+              for (int i = 0; i < 16; ++i) o[i] *= q;
+              tst16(t_u + grp * DA + c, o);
             }
           }
         }
