@@ -20,9 +20,9 @@
 // worked on, the token's place is looked up behind them.
 //
 // Measured: 8,000 new tokens of eight sequences, 32 + 2 x 8 heads of 128, 37.7 us (4.8
-// TB/s; a copy of as many bytes 26.7), bound by instructions (52 % of the schedulers'
-// cycles issue) and the scattered rows; 84,500 keys of 8 heads read back 85.5 us (6.1
-// TB/s; 77).
+// TB/s; a copy of as many bytes 26.7): neither HBM (47 % of its nominal rate under the
+// profiler) nor issue (52 % of the schedulers' cycles) is full, 16 warps per SM with a step
+// of loads each on its way; 84,500 keys of 8 heads read back 85 us (6.2 TB/s; 77).
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 #include <cuda_fp8.h>
@@ -346,7 +346,7 @@ int device(DeviceInfo& info) {
 // Warps per row, and blocks: a warp per row once the rows fill the GPU's warps, below
 // that a row's heads are shared by up to 8.  (Runs of 8 rows per warp, their places
 // looked up at once, were slower: warps side by side then read places far apart.  Reading
-// 84,500 rows of 8 heads of 128 back 95 us against 83.)
+// 84,500 rows of 8 heads of 128 back 95 us against the 83 of that time.)
 int shape(int rows, int heads, int lg, int per_sm, int sms, int& parts) {
   const long long slots = static_cast<long long>(per_sm) * kWarps * sms;
   const int per = 32 >> lg;

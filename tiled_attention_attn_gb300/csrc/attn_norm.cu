@@ -25,9 +25,10 @@
 // blocks by a second launch (sum_weights_kernel).  The same sizes give the same bits.
 //
 // Measured: 8,192 tokens of 32 + 8 heads of 128 over three axes 34.3 us (4.9 TB/s; a
-// copy of as many bytes 24.8), the gradients of 16,384 101 us (5.0 TB/s; 74); both issue
-// in a bit over half of the schedulers' cycles at two blocks per SM, which the registers
-// allow.
+// copy of as many bytes 24.8), the gradients of 16,384 101 us (5.0 TB/s; 74).  Neither
+// HBM (45 and 60 % of its nominal rate under the profiler) nor issue (52 and 55 % of the
+// schedulers' cycles) is full: what is left is the latency of the loads, of which the 16
+// warps that an SM has at these registers (two blocks) keep one step each on its way.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 #include <cuda_runtime.h>
@@ -480,7 +481,7 @@ template <bool BWD>
 void run(const Params& p, bool bf16, bool gptj, int grid, cudaStream_t stream) {
   size_t smem = (static_cast<size_t>(kWarps) * p.rot + 2 * p.d) * sizeof(float);
   if (BWD) smem += std::max(static_cast<size_t>(kWarps) * 2 * p.d, static_cast<size_t>(kThreads) * 32) * sizeof(float);
-  if (smem > 48 * 1024) smem_allowed<BWD>(bf16, gptj);   // (d = 512)
+  if (smem > 48 * 1024) smem_allowed<BWD>(bf16, gptj);   // (backward, from 8 rot + 2 d > 4,096 on: d = rot from 416)
   if (bf16) gptj ? norm_kernel<true, true, BWD><<<grid, kThreads, smem, stream>>>(p)
                  : norm_kernel<true, false, BWD><<<grid, kThreads, smem, stream>>>(p);
   else gptj ? norm_kernel<false, true, BWD><<<grid, kThreads, smem, stream>>>(p)

@@ -14,9 +14,9 @@
 // 199 then; with more registers for the softmax warps, so that they hold their 64 values
 // of S, 173; with the scales further ahead 162, the masks read ahead 158.)  S and P V are
 // issued by a warp each, so that neither waits in the other's queue (155), from uniform
-// operands (143); with the scales copied by the loading warps 138.  Bound by the softmax
-// warps: a step takes 2,200 cycles, of which a group is at work for 1,500 to 2,100; the
-// tensor pipe is 37 % busy (its floor for the 64 tokens is 51 us).
+// operands (143); with the scales copied by the loading warps 138.  Bound by the
+// chains of the softmax warps (at work for 1,500 to 2,100 of a step's 2,200 cycles when that
+// took 138 us); the tensor pipe is 35 % busy (its floor for the 64 tokens is 51 us).
 // The rest is as in attn_tree_fp8_kernel.cuh, but that P' is one fp16 value, off by 2^-11 of
 // itself: a second one would double the products of P V, and V and P as bf16 values, which
 // need no reference, took 180 us (its widening 14, the two values 9).  The references
@@ -362,7 +362,7 @@ __global__ void __launch_bounds__(kThreads, 1) tree_rows_kernel(const __grid_con
             if (!wait_pv(b_pv_done, step - 1, wc)) { ok = false; break; }
             tc_fence_after();
 #pragma unroll 1
-            for (int c = 0; c < DA; c += 16) {   // (by 32: 146 us against 141, the code being longer)
+            for (int c = 0; c < DA; c += 16) {   // (by 32: 146 us against 141)
               float o[16];
               tld<16>(t_u + grp * DA + c, o);
 #pragma unroll

@@ -228,7 +228,8 @@ def qk_norm_rotary_func(q: torch.Tensor, k: Optional[torch.Tensor] = None, q_wei
                         amplitude: float = 1.0, interleaved: bool = False):
     """``qk_norm_rotary`` with gradients for q, k and the weights, on the current
     stream (frequencies and positions are constants: changing them in place before
-    the backward is an error).  A backward that is captured into a CUDA graph needs,
+    the backward is an error).  The gradients have none of their own: asking for one
+    is an error.  A backward that is captured into a CUDA graph needs,
     as with any operator of torch, that no eager graph of the same leaves is alive."""
     axes = tuple(int(a) for a in axes) if axes is not None else None
     return _QkNormRotaryFunction.apply(q, k, q_weight, k_weight, freqs, positions, axes, float(eps), float(amplitude),
