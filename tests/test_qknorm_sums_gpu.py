@@ -1,5 +1,5 @@
 """The weights' gradients of the head norms over many tokens: every row of every head is in
-the sums, whichever warp, round of tokens or part of a token's heads it falls to."""
+the sums, whichever warp, turn of tokens or part of a token's heads it falls to."""
 
 import math
 
