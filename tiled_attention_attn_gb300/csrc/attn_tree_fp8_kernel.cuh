@@ -32,8 +32,8 @@
 // softmax warps on one step: 120 us for 32 caches of ~3,550 keys, 32 heads on 8 of
 // 128).  So does what it takes to issue one: with the operands in one thread's registers
 // about 85 cycles each, whatever their size, and 61 us for those caches; uniform over the
-// warp (see uniform()) 55.  Measured (device time, merge included): those caches 56.5 us,
-// of which the 236 MB take 35 at the copy rate; one of 131,072 keys 55.2 of 41, its line
+// warp (see uniform()) 55.  Measured (device time, merge included): those caches 56.1 us,
+// of which the 236 MB take 35 at the copy rate; one of 131,072 keys 55.3 of 41, its line
 // of steps at 6.6 TB/s.  What is left is the start (4 us to the first S: prologue, the
 // walk, the queries' conversion), the epilogue and 3 to 4 of the merge.
 //
